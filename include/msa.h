@@ -148,6 +148,64 @@ MSA_API msa_status_t msa_qk_norm_rope_bwd(const void* x, const void* dy, void* d
                                           size_t workspace_bytes, msa_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Prologue for any rotary layout: the norm and the rotation of
+ * msa_qk_norm_rope with the head dim (64, 128 or 256, e.g. the narrow-block
+ * layers'), the rotated part, the pairing and the frequencies as arguments.
+ * Frequencies scaled for contexts beyond the trained length come from
+ * msa_rope_init (host only; a rope may also be filled in by hand):
+ *   PLAIN   f_i = base^(-2 i / dim), i < dim / 2
+ *   LINEAR  f_i / factor                       (positions interpolated)
+ *   NTK     base * factor^(dim / (dim - 2)) in place of base
+ *   YARN    by parts ("YaRN: Efficient Context Window Extension of Large
+ *           Language Models", Peng et al. 2023, 3.2 and 3.3): with t_i = orig_len
+ *           f_i / (2 pi) turns over the trained length and k = clamp((t_i -
+ *           beta_slow) / (beta_fast - beta_slow), 0, 1): f_i k + f_i / factor (1 - k);
+ *           gain 0.1 ln(factor) + 1
+ * gain multiplies the rotated channels; 0 in msa_rope_init takes the scaling's
+ * own (1 except for YARN).  dim: a multiple of 16, 16 .. 256, at most the head
+ * dim.  Layout HALF pairs channels (i, i + dim/2), INTERLEAVED (2i, 2i + 1).
+ */
+enum { MSA_ROPE_HALF = 0, MSA_ROPE_INTERLEAVED = 1 };
+enum { MSA_ROPE_PLAIN = 0, MSA_ROPE_LINEAR = 1, MSA_ROPE_NTK = 2, MSA_ROPE_YARN = 3 };
+
+typedef struct {
+  int32_t dim;        /* rotated channels */
+  int32_t layout;     /* MSA_ROPE_HALF or MSA_ROPE_INTERLEAVED */
+  float gain;         /* factor of the rotated channels */
+  float reserved;
+  double freqs[128];  /* angle per position of pair i < dim / 2, in radians */
+} msa_rope_t;
+
+MSA_API msa_status_t msa_rope_init(msa_rope_t* rope, int dim, double base, int layout,
+                                   int scaling, double factor, double orig_len,
+                                   double beta_fast, double beta_slow, double gain);
+
+/* x bf16 [T, H, D] -> y bf16 [T, H, D] (y may be x).  w bf16 [D], or NULL for
+ * the rotation alone (z = x).  The position of token t is positions[t] (int32
+ * [T], any value) or, with positions NULL, its place in cu_seqlens' sequence.
+ * `rope` is read on the host during the call.  1 <= H <= 256.
+ */
+MSA_API msa_status_t msa_qk_norm_rope_ex(const void* x, void* y, int T, int H, int D,
+                                         const void* w, const int32_t* positions,
+                                         const int32_t* cu_seqlens, int S,
+                                         const msa_rope_t* rope, float eps,
+                                         msa_stream_t stream);
+
+/* Its gradients, as msa_qk_norm_rope_bwd: dx bf16 [T, H, D] (may be dy) and dw
+ * fp32 [D] (overwritten; fixed summation order).  With w NULL only dx = the
+ * gradient turned back is formed; x, dw and the workspace may then be NULL.
+ */
+MSA_API size_t msa_qk_norm_rope_bwd_ex_workspace_size(int T, int H, int D);
+
+MSA_API msa_status_t msa_qk_norm_rope_bwd_ex(const void* x, const void* dy, void* dx, float* dw,
+                                             int T, int H, int D, const void* w,
+                                             const int32_t* positions,
+                                             const int32_t* cu_seqlens, int S,
+                                             const msa_rope_t* rope, float eps,
+                                             void* workspace, size_t workspace_bytes,
+                                             msa_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Index select ("MiniMax-M3.1-Flash", 1 "Model Introduction"; "#4581",
  * "Kernel tuning").  q_idx, k_idx: post-prologue bf16 [T, Hi, 128].
  * For token t at position p and index head h the own block is p / 128; every
@@ -343,6 +401,161 @@ MSA_API msa_status_t msa_decode_append(const void* q, const void* q_idx, const v
                                        int B, int Hq, int Hkv, int num_pages, int max_pages,
                                        int rope_dim, float rope_base, float eps, void* q_out,
                                        void* q_idx_out, msa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged cache held in 4 bits.  A page of one head (a "slab") is 9216 bytes:
+ * 128 tokens x 64 bytes of e2m1 codes (low nibble = even channel), then 128
+ * tokens x 8 bytes of e4m3 scales, one for 16 consecutive channels.  A cache is
+ * uint8 [num_pages, Hkv, 9216]; pages, block tables and positions are those of
+ * msa_decode_step, so a cache takes 72 bytes per (token, head) instead of 256.
+ * Per 16 channels with values x (bf16) and the cache's gain g:
+ *   scale = e4m3(min(max|x| / g / 6, 448)),  code = e2m1(x / g / scale)
+ * both rounded to nearest even (magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6, larger
+ * ones saturate; scale 0 gives codes 0).  A code stands for code * scale * g,
+ * exact in bf16.  Sixteen channels that hold an infinity or NaN get the scale
+ * NaN, so they read back as NaN.  Gains (one per cache, finite, > 0, a power
+ * of two from 2^-64 to 2^64) place values far from 1 in e4m3's range [2^-9, 448].
+ *
+ * msa_cache4_store writes a pack: token t of sequence s (cu_seqlens) goes to
+ * position start[s] + t - cu_seqlens[s] of block table row s (start int32 [S],
+ * NULL = 0); k, v, k_idx bf16 [T, Hkv, 128].  msa_cache4_load is its inverse:
+ * the held values of those positions as bf16 [T, Hkv, 128].  Either may leave
+ * out tensors: a NULL tensor with its cache NULL is skipped (one at least is
+ * needed).  Tokens outside [0, max_pages * 128) or on pages outside
+ * [0, num_pages) set MSA_STATUS_BOUNDS; they are not stored, and load as zeros.
+ * Rows of the pack outside [cu_seqlens[0], cu_seqlens[S]) are left alone.
+ */
+MSA_API msa_status_t msa_cache4_store(const void* k, const void* v, const void* k_idx,
+                                      void* k_cache, void* v_cache, void* kidx_cache,
+                                      const int32_t* block_table, const int32_t* cu_seqlens,
+                                      const int32_t* start, int S, int T, int Hkv,
+                                      int num_pages, int max_pages, float k_gain, float v_gain,
+                                      float kidx_gain, msa_stream_t stream);
+
+MSA_API msa_status_t msa_cache4_load(const void* k_cache, const void* v_cache,
+                                     const void* kidx_cache, const int32_t* block_table,
+                                     const int32_t* cu_seqlens, const int32_t* start, int S,
+                                     int T, int Hkv, int num_pages, int max_pages, float k_gain,
+                                     float v_gain, float kidx_gain, void* k, void* v,
+                                     void* k_idx, msa_stream_t stream);
+
+/* msa_decode_append into a 4-bit cache, with the rotation of `rope` (dim <=
+ * 128): q_out and q_idx_out as there, and k, k_idx (normed, rotated, rounded to
+ * bf16) and v held in 4 bits at position cache_lens[b] - 1.  Hq is any multiple
+ * of Hkv up to 256 heads.  A row with cache_lens[b] = 0 is padding: nothing of
+ * it is read or written.  Other lengths outside [1, 128 max_pages] and pages
+ * outside [0, num_pages) set MSA_STATUS_BOUNDS and leave the row untouched.
+ */
+MSA_API msa_status_t msa_decode4_append(const void* q, const void* q_idx, const void* k,
+                                        const void* v, const void* k_idx, const void* w_q,
+                                        const void* w_qi, const void* w_k, const void* w_ki,
+                                        void* k_cache, void* v_cache, void* kidx_cache,
+                                        const int32_t* block_table, const int32_t* cache_lens,
+                                        int B, int Hq, int Hkv, int num_pages, int max_pages,
+                                        const msa_rope_t* rope, float k_gain, float v_gain,
+                                        float kidx_gain, float eps, void* q_out,
+                                        void* q_idx_out, msa_stream_t stream);
+
+/* msa_decode_step_ex over 4-bit caches.  Selection and attention are those of
+ * the held values: blocks are scored by their largest index logit (the own
+ * block and the first n_init blocks are kept without a score, and sequences of
+ * at most 16 blocks keep all), equal scores go to the lower block.  Hq = G Hkv
+ * with 1 <= G <= 16.  A row with cache_lens[b] = 0 gets o = 0 and sel = -1;
+ * lengths outside [0, 128 max_pages] set MSA_STATUS_BOUNDS and are treated
+ * so too.  A page outside [0, num_pages) sets MSA_STATUS_BOUNDS; its block scores
+ * -infinity and, if it is selected all the same, has no keys.  Slots of the
+ * own page behind the sequence's end may hold anything.  kidx_gain scales all
+ * scores of a call alike and is not needed.
+ */
+MSA_API size_t msa_decode4_step_workspace_size(int B, int Hq, int Hkv, int max_pages);
+
+MSA_API msa_status_t msa_decode4_step(const void* q, const void* q_idx, const void* k_cache,
+                                      const void* v_cache, const void* kidx_cache,
+                                      const int32_t* block_table, const int32_t* cache_lens,
+                                      int B, int Hq, int Hkv, int num_pages, int max_pages,
+                                      float scale, float k_gain, float v_gain, int n_init,
+                                      void* o, int32_t* sel_out, void* workspace,
+                                      size_t workspace_bytes, msa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Pages of a paged cache: block_table int32 [B, max_pages], cache_lens int32
+ * [B] and ref_count int32 [num_pages] (rows that hold the page; 0 = free) on the
+ * device are changed in place, with no host synchronisation, and what is
+ * chosen depends on their contents alone (the same calls give the same tables).
+ * Row b holds ceil(cache_lens[b] / 128) pages; entries behind those are not
+ * read.  `caches` is a HOST array of n_caches (0 .. 8) device pointers, page p of
+ * cache c at caches[c] + p * page_bytes[c] (host array, multiples of 16): any
+ * format, 16 or 4 bits.  Contents that contradict each other (rows or pages out
+ * of range, a reference count below what the tables hold) set
+ * MSA_STATUS_BOUNDS and are skipped.  Calls on one set of tables are ordered by
+ * the caller (one stream, or events).
+ *
+ * fork: row dst[i] (empty before: length 0) becomes the first keep[i] tokens
+ * (keep NULL = all) of row src[i]; the pages are shared.  Sources are read as
+ * they were before the call.  forked[i] (int32 [n], output) is the length given, -1
+ * where the pair is refused (dst not empty or equal to src, a row out of range,
+ * or an earlier pair with the same dst); keep outside [0, length] is clamped and
+ * sets MSA_STATUS_BOUNDS.
+ */
+MSA_API msa_status_t msa_pages_fork(const int32_t* src, const int32_t* dst, const int32_t* keep,
+                                    int n, int32_t* block_table, int32_t* cache_lens,
+                                    int32_t* ref_count, int B, int num_pages, int max_pages,
+                                    int32_t* forked, msa_stream_t stream);
+
+/* free: row rows[i] keeps its first keep[i] tokens (keep NULL = none): the
+ * pages behind lose one reference, their table entries become -1 and the length
+ * becomes keep[i] (a keep above the length changes nothing).  dropped[i] (int32
+ * [n], output) is the number of tokens dropped, -1 where refused (a row out of range,
+ * keep < 0, or a row that an earlier entry already shortens).
+ */
+MSA_API msa_status_t msa_pages_free(const int32_t* rows, const int32_t* keep, int n,
+                                    int32_t* block_table, int32_t* cache_lens,
+                                    int32_t* ref_count, int B, int num_pages, int max_pages,
+                                    int32_t* dropped, msa_stream_t stream);
+
+/* extend: row b grows by add[b] >= 0 tokens (int32 [B]), so that they can be
+ * appended: it gets the pages it lacks, and if its last page is partly filled
+ * and shared, a copy of that page for itself first (copy on write, the page's
+ * bytes of every cache).  Free pages go out in ascending order, to the rows in order,
+ * the copy before the new pages.  done[b] (int32 [B], output) is 1 where the row
+ * has grown; 0 where it is left as it was: what rows 0 .. b want together is more than
+ * the pages that were free before the call, or the row would exceed max_pages,
+ * or add[b] < 0 (which sets MSA_STATUS_BOUNDS); rows of the last two kinds want
+ * nothing.  Rows with add[b] = 0 are done.  A page that loses its last row here (all
+ * its sharers copied it) is free after the call.
+ */
+MSA_API size_t msa_pages_extend_workspace_size(int B, int num_pages);
+
+MSA_API msa_status_t msa_pages_extend(const int32_t* add, int32_t* block_table,
+                                      int32_t* cache_lens, int32_t* ref_count, int B,
+                                      int num_pages, int max_pages, void* const* caches,
+                                      const int64_t* page_bytes, int n_caches, int32_t* done,
+                                      void* workspace, size_t workspace_bytes,
+                                      msa_stream_t stream);
+
+/* compact: the pages in use (ref_count > 0) move to the front of the pool: of
+ * n of them, those at n and behind go, in ascending order, to the free places
+ * below n, in ascending order; tables and reference counts follow.  page_map int32
+ * [num_pages] (output): the new place of each page, -1 for free ones; n_live
+ * int32 [1] (output): n.  Bytes of the places that become free are left as they were.
+ */
+MSA_API size_t msa_pages_compact_workspace_size(int num_pages);
+
+MSA_API msa_status_t msa_pages_compact(int32_t* block_table, const int32_t* cache_lens,
+                                       int32_t* ref_count, int B, int num_pages, int max_pages,
+                                       void* const* caches, const int64_t* page_bytes,
+                                       int n_caches, int32_t* page_map, int32_t* n_live,
+                                       void* workspace, size_t workspace_bytes,
+                                       msa_stream_t stream);
+
+/* copy: the bytes of page src[i] become those of page dst[i], i < n, in every
+ * cache (a page must not be a dst twice, nor both a dst and another pair's src;
+ * src[i] = dst[i] does nothing).  Pairs with a page out of range set
+ * MSA_STATUS_BOUNDS and are skipped.
+ */
+MSA_API msa_status_t msa_pages_copy(const int32_t* src, const int32_t* dst, int n, int num_pages,
+                                    void* const* caches, const int64_t* page_bytes, int n_caches,
+                                    msa_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * msa_decode_step_static: the decode step above for callers that cannot

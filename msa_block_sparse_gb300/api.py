@@ -20,6 +20,7 @@ D = 128
 TOPK = 16
 
 _c_int, _c_float, _c_size, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
+_c_double = ctypes.c_double
 
 # name -> (restype, argtypes); mirrors include/msa.h
 _SIGNATURES = {
@@ -71,6 +72,28 @@ _SIGNATURES = {
     "msa_decode_step_ex": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int,
                                     _c_int, _c_int, _c_float, _c_int, _vp, _vp, _vp, _c_size,
                                     _vp]),
+    "msa_rope_init": (_c_int, [_vp, _c_int, _c_double, _c_int, _c_int] + [_c_double] * 5),
+    "msa_qk_norm_rope_ex": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_int, _vp,
+                                     _c_float, _vp]),
+    "msa_qk_norm_rope_bwd_ex_workspace_size": (_c_size, [_c_int] * 3),
+    "msa_qk_norm_rope_bwd_ex": (_c_int, [_vp] * 4 + [_c_int] * 3 + [_vp] * 3 + [_c_int, _vp,
+                                                                             _c_float, _vp,
+                                                                             _c_size, _vp]),
+    "msa_cache4_store": (_c_int, [_vp] * 9 + [_c_int] * 5 + [_c_float] * 3 + [_vp]),
+    "msa_cache4_load": (_c_int, [_vp] * 6 + [_c_int] * 5 + [_c_float] * 3 + [_vp] * 4),
+    "msa_decode4_append": (_c_int, [_vp] * 14 + [_c_int] * 5 + [_vp] + [_c_float] * 4 + [_vp] * 3),
+    "msa_decode4_step_workspace_size": (_c_size, [_c_int] * 4),
+    "msa_decode4_step": (_c_int, [_vp] * 7 + [_c_int] * 5 + [_c_float] * 3 + [_c_int, _vp, _vp, _vp,
+                                                                          _c_size, _vp]),
+    "msa_pages_fork": (_c_int, [_vp] * 3 + [_c_int] + [_vp] * 3 + [_c_int] * 3 + [_vp, _vp]),
+    "msa_pages_free": (_c_int, [_vp] * 2 + [_c_int] + [_vp] * 3 + [_c_int] * 3 + [_vp, _vp]),
+    "msa_pages_extend_workspace_size": (_c_size, [_c_int] * 2),
+    "msa_pages_extend": (_c_int, [_vp] * 4 + [_c_int] * 3 + [_vp, _vp, _c_int, _vp, _vp, _c_size,
+                                                          _vp]),
+    "msa_pages_compact_workspace_size": (_c_size, [_c_int]),
+    "msa_pages_compact": (_c_int, [_vp] * 3 + [_c_int] * 3 + [_vp, _vp, _c_int, _vp, _vp, _vp,
+                                                           _c_size, _vp]),
+    "msa_pages_copy": (_c_int, [_vp, _vp, _c_int, _c_int, _vp, _vp, _c_int, _vp]),
     "msa_decode_step_static": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int,
                                         _c_int, _c_int, _c_int, _c_float, _vp, _vp, _vp]),
 }
@@ -464,8 +487,385 @@ def msa_qsa_attn_bwd(q, k, v, o, dout, lse, sel, cu_seqlens, max_seqlen: int,
     return dq, dk, dv
 
 
+# ------------------------------------------------------------------ prologue, any rotary layout
+
+class Rope(ctypes.Structure):
+    """A rotation (msa_rope_t): `dim` rotated channels, `layout` (0 half, 1
+    interleaved), `gain` of the rotated channels and the angle per position of each
+    pair.  Made by msa_rope; may be kept and used by any number of calls."""
+    _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("gain", _c_float),
+                ("reserved", _c_float), ("freqs", _c_double * 128)]
+
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def msa_rope(dim: int = 64, base: float = 1.0e7, layout: str = "half", scaling: str = "none",
+             factor: float = 1.0, orig_len: float = 32768.0, beta_fast: float = 32.0,
+             beta_slow: float = 1.0, gain: Optional[float] = None) -> Rope:
+    """The rotation of the first `dim` channels (msa_rope_init, host only): layout
+    "half" or "interleaved", scaling "none", "linear", "ntk" or "yarn" by `factor` (yarn
+    also takes the trained length and its two turn counts); gain None = the scaling's own."""
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}, got {scaling!r}")
+    if gain is not None and not gain > 0:
+        raise ValueError("gain must be > 0")
+    r = Rope()
+    _check(lib().msa_rope_init(ctypes.byref(r), dim, base, _LAYOUTS[layout], _SCALINGS[scaling],
+                               factor, orig_len, beta_fast, beta_slow,
+                               0.0 if gain is None else gain))
+    return r
+
+
+def _on_current_device(*tensors):
+    """The calls run on the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _rope_positions(cu_seqlens, positions, T):
+    if (cu_seqlens is None) == (positions is None):
+        raise ValueError("give either cu_seqlens or positions")
+    if positions is not None:
+        _req(positions, "positions", torch.int32, (T,))
+        return 1
+    _req(cu_seqlens, "cu_seqlens", torch.int32)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must have shape (S + 1,)")
+    return cu_seqlens.numel() - 1
+
+
+def _is_rope(rope):
+    if not isinstance(rope, Rope):
+        raise ValueError("rope must come from msa_rope")
+
+
+def msa_qk_norm_rope_ex(x, w, rope: Rope, cu_seqlens: Optional[torch.Tensor] = None,
+                        positions: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None, eps: float = 1.0e-6):
+    """x bf16 [T, H, D] (D 64, 128 or 256) -> out: gemma RMSNorm with weight w (bf16
+    [D]; None: no norm), then the rotation `rope` at positions (int32 [T]) or at the
+    tokens' places in cu_seqlens' sequences.  Pass out=x for in place."""
+    if x.dim() != 3:
+        raise ValueError("x must have shape (T, H, D)")
+    T, H, Dh = x.shape
+    _req(x, "x", torch.bfloat16)
+    _is_rope(rope)
+    if w is not None:
+        _req(w, "w", torch.bfloat16, (Dh,))
+    S = _rope_positions(cu_seqlens, positions, T)
+    out = torch.empty_like(x) if out is None else out
+    _req(out, "out", torch.bfloat16, (T, H, Dh))
+    _on_current_device(x, w, cu_seqlens, positions, out)
+    _check(lib().msa_qk_norm_rope_ex(_ptr(x), _ptr(out), T, H, Dh, _ptr(w), _ptr(positions),
+                                     _ptr(cu_seqlens), S, ctypes.byref(rope), eps, _stream(x)))
+    return out
+
+
+def msa_qk_norm_rope_bwd_ex(x, dy, w, rope: Rope, cu_seqlens: Optional[torch.Tensor] = None,
+                            positions: Optional[torch.Tensor] = None,
+                            dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                            eps: float = 1.0e-6, workspace: Optional[torch.Tensor] = None):
+    """Gradients of msa_qk_norm_rope_ex: (dx bf16 [T, H, D], dw fp32 [D]) from its input
+    x and dy (pass dx=dy to overwrite dy); with w None (dx, None), and x may be None."""
+    if dy.dim() != 3:
+        raise ValueError("dy must have shape (T, H, D)")
+    T, H, Dh = dy.shape
+    _req(dy, "dy", torch.bfloat16)
+    _is_rope(rope)
+    dx = torch.empty_like(dy) if dx is None else dx
+    _req(dx, "dx", torch.bfloat16, (T, H, Dh))
+    S = _rope_positions(cu_seqlens, positions, T)
+    ws = None
+    if w is not None:
+        _req(w, "w", torch.bfloat16, (Dh,))
+        _req(x, "x", torch.bfloat16, (T, H, Dh))
+        dw = torch.empty(Dh, dtype=torch.float32, device=dy.device) if dw is None else dw
+        _req(dw, "dw", torch.float32, (Dh,))
+        ws = _workspace(lib().msa_qk_norm_rope_bwd_ex_workspace_size(T, H, Dh), dy.device, workspace)
+    elif dw is not None:
+        raise ValueError("dw needs w")
+    _on_current_device(x, dy, w, cu_seqlens, positions, dx, dw, ws)
+    _check(lib().msa_qk_norm_rope_bwd_ex(_ptr(x), _ptr(dy), _ptr(dx), _ptr(dw), T, H, Dh, _ptr(w),
+                                         _ptr(positions), _ptr(cu_seqlens), S, ctypes.byref(rope),
+                                         eps, _ptr(ws), 0 if ws is None else _nbytes(ws),
+                                         _stream(dy)))
+    return dx, dw
+
+
+# ------------------------------------------------------------------ 4-bit paged cache
+
+SLAB4 = 9216     # bytes of a page of one head: 128 x 64 of codes, 128 x 8 of scales
+
+
+def _nbytes(t):
+    return t.numel() * t.element_size()
+
+
+def _caches4(named, block_table, rows):
+    """Checks 4-bit caches (name, tensor) and the table; (Hkv, num_pages, max_pages)."""
+    first = next(c for _, c in named if c is not None)
+    if not isinstance(first, torch.Tensor) or first.dim() != 3:
+        raise ValueError("a 4-bit cache must have shape (num_pages, Hkv, 9216)")
+    P, Hkv = first.shape[0], first.shape[1]
+    for n, c in named:
+        if c is not None:
+            _req(c, n, torch.uint8, (P, Hkv, SLAB4))
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must have shape (rows, max_pages)")
+    _req(block_table, "block_table", torch.int32, (rows, block_table.shape[1]))
+    return Hkv, P, block_table.shape[1]
+
+
+def _cache4_pack(kvi, caches, block_table, cu_seqlens, T, start):
+    _req(cu_seqlens, "cu_seqlens", torch.int32)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must have shape (S + 1,)")
+    S = cu_seqlens.numel() - 1
+    names = ("k", "v", "k_idx")
+    for n, x, c in zip(names, kvi, caches):
+        if (x is None) != (c is None):
+            raise ValueError(f"{n} and its cache must be given together")
+    if all(c is None for c in caches):
+        raise ValueError("no cache given")
+    Hkv, P, maxp = _caches4([(n + "_cache", c) for n, c in zip(names, caches)], block_table, S)
+    for n, x in zip(names, kvi):
+        if x is not None:
+            _req(x, n, torch.bfloat16, (T, Hkv, D))
+    if start is not None:
+        _req(start, "start", torch.int32, (S,))
+    _on_current_device(*kvi, *caches, block_table, cu_seqlens, start)
+    return S, Hkv, P, maxp
+
+
+def msa_cache4_store(k, v, k_idx, k_cache, v_cache, kidx_cache, block_table, cu_seqlens,
+                     start: Optional[torch.Tensor] = None, gains=(1.0, 1.0, 1.0)) -> None:
+    """Writes a pack (k, v, k_idx bf16 [T, Hkv, 128], post-prologue) into 4-bit caches
+    (uint8 [num_pages, Hkv, 9216]): token i of sequence s at position start[s] + i of
+    row s of block_table.  k, v or k_idx may be None together with its cache.  gains:
+    of k, v and k_idx, powers of two; the same ones have to be given when reading."""
+    kvi = (k, v, k_idx)
+    have = [x for x in kvi if x is not None]
+    if not have:
+        raise ValueError("no tensor given")
+    T = have[0].shape[0]
+    S, Hkv, P, maxp = _cache4_pack(kvi, (k_cache, v_cache, kidx_cache), block_table, cu_seqlens, T,
+                                   start)
+    _check(lib().msa_cache4_store(_ptr(k), _ptr(v), _ptr(k_idx), _ptr(k_cache), _ptr(v_cache),
+                                  _ptr(kidx_cache), _ptr(block_table), _ptr(cu_seqlens),
+                                  _ptr(start), S, T, Hkv, P, maxp, *gains, _stream(block_table)))
+
+
+def msa_cache4_load(k_cache, v_cache, kidx_cache, block_table, cu_seqlens, T: int,
+                    start: Optional[torch.Tensor] = None, gains=(1.0, 1.0, 1.0), k=None, v=None,
+                    k_idx=None):
+    """The held values of a pack's positions, as bf16 [T, Hkv, 128] each: the inverse of
+    msa_cache4_store.  A cache that is None is left out (its result is None)."""
+    caches = (k_cache, v_cache, kidx_cache)
+    outs = []
+    for n, c, x in zip(("k", "v", "k_idx"), caches, (k, v, k_idx)):
+        if c is None and x is not None:
+            raise ValueError(f"{n} needs its cache")
+        if c is not None and x is None:
+            x = torch.empty((T, c.shape[1], D), dtype=torch.bfloat16, device=c.device)
+        outs.append(x)
+    S, Hkv, P, maxp = _cache4_pack(outs, caches, block_table, cu_seqlens, T, start)
+    _check(lib().msa_cache4_load(_ptr(k_cache), _ptr(v_cache), _ptr(kidx_cache), _ptr(block_table),
+                                 _ptr(cu_seqlens), _ptr(start), S, T, Hkv, P, maxp, *gains,
+                                 _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]), _stream(block_table)))
+    return tuple(outs)
+
+
+def msa_decode4_append(q, q_idx, k, v, k_idx, w_q, w_qi, w_k, w_ki, k_cache, v_cache, kidx_cache,
+                       block_table, cache_lens, rope: Rope, gains=(1.0, 1.0, 1.0), q_out=None,
+                       q_idx_out=None, eps: float = 1.0e-6):
+    """msa_decode_append into 4-bit caches: the prologue (norm, rotation `rope`) of one
+    new token per sequence at position cache_lens - 1, its k, index-k and v held in 4
+    bits; returns (q_out, q_idx_out).  Rows of length 0 are padding and left alone."""
+    B, Hq = q.shape[0], q.shape[1]
+    Hkv, P, maxp = _caches4((("k_cache", k_cache), ("v_cache", v_cache),
+                             ("kidx_cache", kidx_cache)), block_table, B)
+    _is_rope(rope)
+    _req(q, "q", torch.bfloat16, (B, Hq, D))
+    for n, t in (("q_idx", q_idx), ("k", k), ("v", v), ("k_idx", k_idx)):
+        _req(t, n, torch.bfloat16, (B, Hkv, D))
+    for n, w in (("w_q", w_q), ("w_qi", w_qi), ("w_k", w_k), ("w_ki", w_ki)):
+        _req(w, n, torch.bfloat16, (D,))
+    _req(cache_lens, "cache_lens", torch.int32, (B,))
+    q_out = torch.empty_like(q) if q_out is None else q_out
+    q_idx_out = torch.empty_like(q_idx) if q_idx_out is None else q_idx_out
+    _req(q_out, "q_out", torch.bfloat16, (B, Hq, D))
+    _req(q_idx_out, "q_idx_out", torch.bfloat16, (B, Hkv, D))
+    _on_current_device(q, q_idx, k, v, k_idx, w_q, w_qi, w_k, w_ki, k_cache, v_cache, kidx_cache,
+                       block_table, cache_lens, q_out, q_idx_out)
+    kg, vg, ig = gains
+    _check(lib().msa_decode4_append(_ptr(q), _ptr(q_idx), _ptr(k), _ptr(v), _ptr(k_idx), _ptr(w_q),
+                                    _ptr(w_qi), _ptr(w_k), _ptr(w_ki), _ptr(k_cache),
+                                    _ptr(v_cache), _ptr(kidx_cache), _ptr(block_table),
+                                    _ptr(cache_lens), B, Hq, Hkv, P, maxp, ctypes.byref(rope), kg,
+                                    vg, ig, eps, _ptr(q_out), _ptr(q_idx_out), _stream(q)))
+    return q_out, q_idx_out
+
+
+def msa_decode4_step(q, q_idx, k_cache, v_cache, kidx_cache, block_table, cache_lens,
+                     scale: Optional[float] = None, gains=(1.0, 1.0, 1.0),
+                     out: Optional[torch.Tensor] = None, sel_out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, n_init: int = 0):
+    """msa_decode_step over 4-bit caches: (o bf16 [B, Hq, 128], sel int32 [B, Hkv, 16]),
+    Hq = 1 .. 16 heads per KV head.  Rows of length 0 get o = 0, sel = -1."""
+    B, Hq = q.shape[0], q.shape[1]
+    Hkv, P, maxp = _caches4((("k_cache", k_cache), ("v_cache", v_cache),
+                             ("kidx_cache", kidx_cache)), block_table, B)
+    _req(q, "q", torch.bfloat16, (B, Hq, D))
+    _req(q_idx, "q_idx", torch.bfloat16, (B, Hkv, D))
+    _req(cache_lens, "cache_lens", torch.int32, (B,))
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    out = torch.empty_like(q) if out is None else out
+    if sel_out is None:
+        sel_out = torch.empty((B, Hkv, TOPK), dtype=torch.int32, device=q.device)
+    _req(out, "out", torch.bfloat16, (B, Hq, D))
+    _req(sel_out, "sel_out", torch.int32, (B, Hkv, TOPK))
+    ws = _workspace(lib().msa_decode4_step_workspace_size(B, Hq, Hkv, maxp), q.device, workspace)
+    _on_current_device(q, q_idx, k_cache, v_cache, kidx_cache, block_table, cache_lens, out, sel_out,
+                       ws)
+    _check(lib().msa_decode4_step(_ptr(q), _ptr(q_idx), _ptr(k_cache), _ptr(v_cache),
+                                  _ptr(kidx_cache), _ptr(block_table), _ptr(cache_lens), B, Hq, Hkv,
+                                  P, maxp, scale, gains[0], gains[1], n_init, _ptr(out),
+                                  _ptr(sel_out), _ptr(ws), _nbytes(ws), _stream(q)))
+    return out, sel_out
+
+
+# ------------------------------------------------------------------ pages of a cache
+
+def _tables(block_table, cache_lens, ref_count):
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must have shape (B, max_pages)")
+    B, maxp = block_table.shape
+    _req(block_table, "block_table", torch.int32)
+    _req(cache_lens, "cache_lens", torch.int32, (B,))
+    _req(ref_count, "ref_count", torch.int32)
+    if ref_count.dim() != 1:
+        raise ValueError("ref_count must have shape (num_pages,)")
+    return B, ref_count.numel(), maxp
+
+
+def _page_args(caches, P):
+    """Host arrays of the caches' addresses and bytes per page."""
+    for i, c in enumerate(caches):
+        if not isinstance(c, torch.Tensor) or not c.is_cuda or not c.is_contiguous():
+            raise ValueError(f"cache {i} must be a contiguous CUDA tensor")
+        if c.dim() < 1 or c.shape[0] != P:
+            raise ValueError(f"cache {i} must have {P} pages in its first dimension")
+    n = len(caches)
+    ptrs = (_vp * max(n, 1))(*[c.data_ptr() for c in caches])
+    sizes = (ctypes.c_int64 * max(n, 1))(*[_nbytes(c) // P for c in caches])
+    return ptrs, sizes, n
+
+
+def _row_list(t, name, n=None):
+    _req(t, name, torch.int32, None if n is None else (n,))
+    if t.dim() != 1 or t.numel() < 1:
+        raise ValueError(f"{name} must have shape (n,) with n >= 1")
+    return t.numel()
+
+
+def msa_pages_fork(src, dst, block_table, cache_lens, ref_count,
+                   keep: Optional[torch.Tensor] = None, forked: Optional[torch.Tensor] = None):
+    """Row dst[i] (empty) shares the pages of the first keep[i] tokens (None: all) of
+    row src[i]; tables, lengths and reference counts change in place.  Returns forked
+    int32 [n]: the length given, -1 where the pair was refused."""
+    B, P, maxp = _tables(block_table, cache_lens, ref_count)
+    n = _row_list(src, "src")
+    _row_list(dst, "dst", n)
+    if keep is not None:
+        _row_list(keep, "keep", n)
+    forked = torch.empty(n, dtype=torch.int32, device=src.device) if forked is None else forked
+    _row_list(forked, "forked", n)
+    _on_current_device(src, dst, keep, block_table, cache_lens, ref_count, forked)
+    _check(lib().msa_pages_fork(_ptr(src), _ptr(dst), _ptr(keep), n, _ptr(block_table),
+                                _ptr(cache_lens), _ptr(ref_count), B, P, maxp, _ptr(forked),
+                                _stream(src)))
+    return forked
+
+
+def msa_pages_free(rows, block_table, cache_lens, ref_count, keep: Optional[torch.Tensor] = None,
+                   dropped: Optional[torch.Tensor] = None):
+    """Row rows[i] keeps its first keep[i] tokens (None: none); pages that no row
+    holds any more are free.  Returns dropped int32 [n]: tokens dropped, -1 where refused."""
+    B, P, maxp = _tables(block_table, cache_lens, ref_count)
+    n = _row_list(rows, "rows")
+    if keep is not None:
+        _row_list(keep, "keep", n)
+    dropped = torch.empty(n, dtype=torch.int32, device=rows.device) if dropped is None else dropped
+    _row_list(dropped, "dropped", n)
+    _on_current_device(rows, keep, block_table, cache_lens, ref_count, dropped)
+    _check(lib().msa_pages_free(_ptr(rows), _ptr(keep), n, _ptr(block_table), _ptr(cache_lens),
+                                _ptr(ref_count), B, P, maxp, _ptr(dropped), _stream(rows)))
+    return dropped
+
+
+def msa_pages_extend(add, block_table, cache_lens, ref_count, caches,
+                     done: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None):
+    """Row b grows by add[b] tokens: new pages from the free ones, and an own copy of a
+    shared, partly filled last page in every tensor of `caches` (first dimension =
+    pages, any format).  Returns done int32 [B]: 1 where the row has grown, 0 where the
+    pool or the table is too small for it."""
+    B, P, maxp = _tables(block_table, cache_lens, ref_count)
+    _req(add, "add", torch.int32, (B,))
+    ptrs, sizes, n = _page_args(caches, P)
+    done = torch.empty(B, dtype=torch.int32, device=add.device) if done is None else done
+    _req(done, "done", torch.int32, (B,))
+    ws = _workspace(lib().msa_pages_extend_workspace_size(B, P), add.device, workspace)
+    _on_current_device(add, block_table, cache_lens, ref_count, done, ws, *caches)
+    _check(lib().msa_pages_extend(_ptr(add), _ptr(block_table), _ptr(cache_lens), _ptr(ref_count), B,
+                                  P, maxp, ptrs, sizes, n, _ptr(done), _ptr(ws), _nbytes(ws),
+                                  _stream(add)))
+    return done
+
+
+def msa_pages_compact(block_table, cache_lens, ref_count, caches,
+                      page_map: Optional[torch.Tensor] = None,
+                      n_live: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None):
+    """Moves the pages in use to the front of the pool, in every tensor of `caches`;
+    tables and counts follow.  Returns (page_map int32 [num_pages], -1 for free pages,
+    n_live int32 [1])."""
+    B, P, maxp = _tables(block_table, cache_lens, ref_count)
+    ptrs, sizes, n = _page_args(caches, P)
+    dev = block_table.device
+    page_map = torch.empty(P, dtype=torch.int32, device=dev) if page_map is None else page_map
+    n_live = torch.empty(1, dtype=torch.int32, device=dev) if n_live is None else n_live
+    _req(page_map, "page_map", torch.int32, (P,))
+    _req(n_live, "n_live", torch.int32, (1,))
+    ws = _workspace(lib().msa_pages_compact_workspace_size(P), dev, workspace)
+    _on_current_device(block_table, cache_lens, ref_count, page_map, n_live, ws, *caches)
+    _check(lib().msa_pages_compact(_ptr(block_table), _ptr(cache_lens), _ptr(ref_count), B, P, maxp,
+                                   ptrs, sizes, n, _ptr(page_map), _ptr(n_live), _ptr(ws),
+                                   _nbytes(ws), _stream(block_table)))
+    return page_map, n_live
+
+
+def msa_pages_copy(src, dst, caches) -> None:
+    """Page src[i] -> page dst[i] in every tensor of `caches` (first dimension = pages)."""
+    n = _row_list(src, "src")
+    _row_list(dst, "dst", n)
+    if not caches:
+        raise ValueError("no cache given")
+    P = caches[0].shape[0]
+    ptrs, sizes, nc = _page_args(caches, P)
+    _on_current_device(src, dst, *caches)
+    _check(lib().msa_pages_copy(_ptr(src), _ptr(dst), n, P, ptrs, sizes, nc, _stream(src)))
+
+
 def workspace_bytes(call: str, *args) -> int:
     """Workspace size of `call` ('qk_norm_rope_bwd', 'index_select', 'sparse_attn_fwd',
-    'sparse_attn_bwd', 'qsa_attn_fwd', 'qsa_attn_bwd', 'decode_step') for the given sizes,
-    as the C ABI reports it."""
+    'sparse_attn_bwd', 'qsa_attn_fwd', 'qsa_attn_bwd', 'decode_step', 'qk_norm_rope_bwd_ex',
+    'decode4_step', 'pages_extend', 'pages_compact') for the given sizes, as the C ABI
+    reports it."""
     return int(getattr(lib(), f"msa_{call}_workspace_size")(*args))

@@ -389,18 +389,6 @@ static msa_status_t check_pack(const int32_t* cu, int S, int T, int max_seqlen) 
   return MSA_OK;
 }
 
-#define MSA_REQUIRE_PTR(p)                                                            \
-  do {                                                                                \
-    if (!(p) || !aligned16(p))                                                        \
-      return fail(MSA_ERR_INVALID_ARG, "%s is null or not 16-byte aligned", #p);      \
-  } while (0)
-
-#define MSA_TRY(expr)                 \
-  do {                                \
-    msa_status_t _s = (expr);         \
-    if (_s != MSA_OK) return _s;      \
-  } while (0)
-
 extern "C" {
 
 int msa_abi_version(void) { return MSA_ABI_VERSION; }

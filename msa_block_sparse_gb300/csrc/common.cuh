@@ -119,3 +119,16 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace msa
+
+// Argument checks of the C entry points.
+#define MSA_REQUIRE_PTR(p)                                                            \
+  do {                                                                                \
+    if (!(p) || !aligned16(p))                                                        \
+      return fail(MSA_ERR_INVALID_ARG, "%s is null or not 16-byte aligned", #p);      \
+  } while (0)
+
+#define MSA_TRY(expr)                 \
+  do {                                \
+    msa_status_t _s = (expr);         \
+    if (_s != MSA_OK) return _s;      \
+  } while (0)

@@ -35,6 +35,25 @@ msa_status_t launch_prologue_bwd(const __nv_bfloat16* x, const __nv_bfloat16* dy
                                  const int32_t* cu, int S, int T, float rope_base, float eps,
                                  float* dw_part, cudaStream_t stream);
 
+// ---------------------------------------------------------------- prologue, any rotary layout
+struct RopeExJob {
+  const __nv_bfloat16* x;        // [T, H, D] input
+  const __nv_bfloat16* dy;       // backward: [T, H, D] upstream gradient
+  __nv_bfloat16* y;              // forward: output (may equal x); backward: dx (may equal dy)
+  const __nv_bfloat16* w;        // [D], null: no norm
+  const int32_t* positions;      // [T], null: position within the sequences of cu
+  const int32_t* cu;             // [S + 1]
+  int T, H, D, S;
+  float eps;
+};
+msa_status_t check_rope_arg(const msa_rope_t* rope, int D);
+// Angle per position as the 64-bit fixed-point fraction of a turn (mod 1).
+unsigned long long rope_turn(double freq);
+msa_status_t launch_rope_ex(const RopeExJob& j, const msa_rope_t& rope, cudaStream_t stream);
+size_t rope_ex_bwd_workspace_floats(int T, int H, int D);
+msa_status_t launch_rope_ex_bwd(const RopeExJob& j, const msa_rope_t& rope, float* dw,
+                                float* dw_part, cudaStream_t stream);
+
 // ---------------------------------------------------------------- index select
 // Work units (query tile, index head, chunk of earlier key blocks): at most
 // tiles x Hi + kSelUnitsBeyondTiles of them (the plan sizes the chunks so).
@@ -135,6 +154,10 @@ msa_status_t launch_decode(const void* q, const void* q_idx, const void* k_cache
                            int Hkv, int num_pages, int max_pages, float scale, int n_init,
                            void* o, int32_t* sel_out, const DecodeWorkspace& ws,
                            cudaStream_t stream);
+
+// ---------------------------------------------------------------- 4-bit cache
+msa_status_t check_gains(float k_gain, float v_gain, float kidx_gain);
+msa_status_t check_cache_sizes(int Hkv, int num_pages, int max_pages);
 
 // ---------------------------------------------------------------- narrow blocks
 // 4-token key blocks, head dim 256, 12 query heads per KV head.

@@ -1,0 +1,575 @@
+// Prologue for any rotary layout: per-head Gemma RMSNorm (optional) and the
+// rotation of the first R channels, in one pass, with its backward.
+//   z = x rsqrt(mean(x^2) + eps) (1 + w)      (z = x without weights)
+//   y = z with its pairs (a, b) turned: a' = gain (a cos - b sin),
+//       b' = gain (b cos + a sin), angle = position * f_i;
+//       pair i = channels (i, i + R/2) ("half") or (2i, 2i + 1) ("interleaved")
+//   dz = the pairs of dy turned back (times gain), g = dz (1 + w), xh = x r:
+//   dx = r (g - xh mean(g xh)),  dw = sum over tokens and heads of dz xh
+// Bound by memory: 4 bytes per value forward, 6 backward.
+//
+// Work: the [T * H, D] rows are cut into runs of consecutive rows, one run per
+// CTA (grid-stride in the backward).  A row belongs to D / 8 threads with 8
+// consecutive channels each, so a row is one 16-byte access per thread; "half"
+// pairs sit D-independent R / 16 lanes apart and meet by shuffling the four
+// packed words of x, "interleaved" pairs sit in one thread.  The angles of the
+// run's tokens are computed once per CTA into shared memory.
+//
+// Angles: the host turns each frequency into the 64-bit fixed-point fraction of
+// a turn F_i = f_i / (2 pi) * 2^64, so position * F_i mod 2^64 is the angle in
+// turns without a large fp32 argument (positions up to 2^31 keep their angle to
+// 2^-33 of a turn; F_i itself comes from a double).
+#include <cmath>
+#include "kernels.cuh"
+
+namespace msa {
+
+namespace {
+
+constexpr int kRxThreads = 128;
+constexpr int kRxMaxAngles = 2048;   // (token, pair) entries of a CTA's table: 16 KB
+constexpr int kRxMaxH = 256;
+constexpr int kRxMaxPairs = 128;
+
+struct RxTurns {
+  unsigned long long f[kRxMaxPairs];
+};
+
+struct RxArgs {
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* dy;        // backward: upstream gradient
+  __nv_bfloat16* y;               // forward: y, backward: dx
+  const __nv_bfloat16* w;         // null: no norm
+  const int32_t* positions;       // null: position within cu's sequence
+  const int32_t* cu;
+  float* dw_part;                 // backward: [gridDim.x, D]
+  long long rows;                 // T * H
+  int T, H, S, R, layout, run;    // run: rows per CTA
+  uint32_t inv;                   // ceil(2^20 / H): i / H == (i * inv) >> 20 for i < 4096
+  float eps, gain;
+};
+
+__device__ __forceinline__ float2 bf2(uint32_t u) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
+}
+
+// cos and sin (times gain) of the tokens t0 .. t0 + ntok - 1 of the run:
+// table[tok * R + i] = cos, [tok * R + R / 2 + i] = sin of pair i
+__device__ __forceinline__ void rx_angles(const RxArgs& a, const RxTurns& turns, int t0, int ntok,
+                                          float* table) {
+  const int half = a.R >> 1;
+  for (int k = threadIdx.x; k < ntok * half; k += blockDim.x) {
+    const int tok = k / half, i = k - tok * half;
+    const int t = t0 + tok;
+    long long pos;
+    if (a.positions) {
+      pos = __ldg(a.positions + t);
+    } else {
+      int lo = 0, hi = a.S;                  // largest s with cu[s] <= t
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid;
+      }
+      pos = t - __ldg(a.cu + lo);
+    }
+    const long long ang = static_cast<long long>(static_cast<unsigned long long>(pos) * turns.f[i]);
+    float s, c;
+    sincospif(static_cast<float>(ang) * 1.0842021724855044e-19f, &s, &c);   // * 2^-63
+    table[tok * a.R + i] = c * a.gain;
+    table[tok * a.R + half + i] = s * a.gain;
+  }
+}
+
+// The thread's 8 channels turned by the token's angles; sgn = 1 turns forward,
+// -1 back.  v: own values, p: the partner channels' values ("half" only).
+__device__ __forceinline__ void rx_turn(float (&v)[8], const float (&p)[8], const float* tab, int c,
+                                        int R, int layout, float sgn) {
+  const int half = R >> 1;
+  if (layout == MSA_ROPE_HALF) {
+    const int i0 = 8 * c >= half ? 8 * c - half : 8 * c;
+    const float sg = 8 * c >= half ? sgn : -sgn;
+    float cs[8], sn[8];
+    *reinterpret_cast<float4*>(cs) = *reinterpret_cast<const float4*>(tab + i0);
+    *reinterpret_cast<float4*>(cs + 4) = *reinterpret_cast<const float4*>(tab + i0 + 4);
+    *reinterpret_cast<float4*>(sn) = *reinterpret_cast<const float4*>(tab + half + i0);
+    *reinterpret_cast<float4*>(sn + 4) = *reinterpret_cast<const float4*>(tab + half + i0 + 4);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], cs[e], sg * p[e] * sn[e]);
+  } else {
+    float cs[4], sn[4];
+    *reinterpret_cast<float4*>(cs) = *reinterpret_cast<const float4*>(tab + 4 * c);
+    *reinterpret_cast<float4*>(sn) = *reinterpret_cast<const float4*>(tab + half + 4 * c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x1 = v[2 * e], x2 = v[2 * e + 1];
+      v[2 * e] = fmaf(x1, cs[e], -sgn * x2 * sn[e]);
+      v[2 * e + 1] = fmaf(x2, cs[e], sgn * x1 * sn[e]);
+    }
+  }
+}
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
+  const float2 a = bf2(u.x), b = bf2(u.y), c = bf2(u.z), d = bf2(u.w);
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+  v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  uint4 u;
+  u.x = pack_bf16x2(v[0], v[1]);
+  u.y = pack_bf16x2(v[2], v[3]);
+  u.z = pack_bf16x2(v[4], v[5]);
+  u.w = pack_bf16x2(v[6], v[7]);
+  return u;
+}
+
+__device__ __forceinline__ uint4 shfl4(const uint4& u, int src) {
+  uint4 r;
+  r.x = __shfl_sync(0xffffffffu, u.x, src);
+  r.y = __shfl_sync(0xffffffffu, u.y, src);
+  r.z = __shfl_sync(0xffffffffu, u.z, src);
+  r.w = __shfl_sync(0xffffffffu, u.w, src);
+  return r;
+}
+
+}  // namespace
+
+template <int D, bool kNorm>
+__global__ void __launch_bounds__(kRxThreads) rope_ex_kernel(const RxArgs a, const RxTurns turns) {
+  pdl_enter();
+  constexpr int kLpr = D / 8, kSlots = kRxThreads / kLpr;
+  __shared__ __align__(16) float table[2 * kRxMaxAngles];
+  const long long r0 = static_cast<long long>(blockIdx.x) * a.run;
+  const int n = static_cast<int>(a.rows - r0 < a.run ? a.rows - r0 : a.run);
+  const int t0 = static_cast<int>(r0 / a.H);
+  const int h0 = static_cast<int>(r0 - static_cast<long long>(t0) * a.H);
+  const int ntok = (h0 + n + a.H - 1) / a.H;
+  const int lane = threadIdx.x & 31;
+  const int c = threadIdx.x & (kLpr - 1), slot = threadIdx.x / kLpr;
+  const bool rot = 8 * c < a.R;
+  // lane of the partner channels ("half" layout; itself elsewhere)
+  const int hop = a.R >> 4;
+  const int pc = (a.layout == MSA_ROPE_HALF && rot) ? (c < hop ? c + hop : c - hop) : c;
+  const int psrc = (lane & ~(kLpr - 1)) | pc;
+  float w1[8], wp[8];
+  if (kNorm) {
+    unpack8(*reinterpret_cast<const uint4*>(a.w + 8 * c), w1);
+    unpack8(*reinterpret_cast<const uint4*>(a.w + 8 * pc), wp);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w1[e] += 1.f, wp[e] += 1.f;
+  }
+  rx_angles(a, turns, t0, ntok, table);
+  __syncthreads();
+  constexpr int kDeep = 4;                       // rows in flight per thread
+  const __nv_bfloat16* xb = a.x + r0 * D + 8 * c;
+  __nv_bfloat16* yb = a.y + r0 * D + 8 * c;
+  // the loop bounds are uniform over the CTA: every lane reaches the shuffles
+  for (int base = 0; base < n; base += kDeep * kSlots) {
+    uint4 raw[kDeep];
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+      const int i = base + k * kSlots + slot;
+      raw[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < n) raw[k] = __ldcs(reinterpret_cast<const uint4*>(xb + static_cast<size_t>(i) * D));
+    }
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+      const int i = base + k * kSlots + slot;
+      if (base + k * kSlots >= n) break;
+      float v[8], p[8];
+      unpack8(raw[k], v);
+      if (a.layout == MSA_ROPE_HALF) unpack8(shfl4(raw[k], psrc), p);
+      if (kNorm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+#pragma unroll
+        for (int m = kLpr / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+        const float rinv = rsqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[e] *= rinv * w1[e];
+          if (a.layout == MSA_ROPE_HALF) p[e] *= rinv * wp[e];
+        }
+      }
+      if (i < n) {
+        const int tok = static_cast<int>((static_cast<uint32_t>(h0 + i) * a.inv) >> 20);
+        if (rot) rx_turn(v, p, table + tok * a.R, c, a.R, a.layout, 1.f);
+        *reinterpret_cast<uint4*>(yb + static_cast<size_t>(i) * D) = pack8(v);
+      }
+    }
+  }
+}
+
+template <int D, bool kNorm>
+__global__ void __launch_bounds__(kRxThreads) rope_ex_bwd_kernel(const RxArgs a,
+                                                                  const RxTurns turns) {
+  pdl_enter();
+  constexpr int kLpr = D / 8, kSlots = kRxThreads / kLpr;
+  __shared__ __align__(16) float table[2 * kRxMaxAngles];
+  const int lane = threadIdx.x & 31;
+  const int c = threadIdx.x & (kLpr - 1), slot = threadIdx.x / kLpr;
+  const bool rot = 8 * c < a.R;
+  const int hop = a.R >> 4;
+  const int pc = (a.layout == MSA_ROPE_HALF && rot) ? (c < hop ? c + hop : c - hop) : c;
+  const int psrc = (lane & ~(kLpr - 1)) | pc;
+  float w1[8], aw[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) aw[e] = 0.f;
+  if (kNorm) {
+    unpack8(*reinterpret_cast<const uint4*>(a.w + 8 * c), w1);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w1[e] += 1.f;
+  }
+  constexpr int kDeep = 2;
+  for (long long r0 = static_cast<long long>(blockIdx.x) * a.run; r0 < a.rows;
+       r0 += static_cast<long long>(gridDim.x) * a.run) {
+    const int n = static_cast<int>(a.rows - r0 < a.run ? a.rows - r0 : a.run);
+    const int t0 = static_cast<int>(r0 / a.H);
+    const int h0 = static_cast<int>(r0 - static_cast<long long>(t0) * a.H);
+    const int ntok = (h0 + n + a.H - 1) / a.H;
+    __syncthreads();                              // the previous run's angles are consumed
+    rx_angles(a, turns, t0, ntok, table);
+    __syncthreads();
+    const size_t off = static_cast<size_t>(r0) * D + 8 * c;
+    for (int base = 0; base < n; base += kDeep * kSlots) {
+      uint4 rg[kDeep], rx[kDeep];
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const int i = base + k * kSlots + slot;
+        rg[k] = rx[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < n) {
+          rg[k] = __ldcs(reinterpret_cast<const uint4*>(a.dy + off + static_cast<size_t>(i) * D));
+          if (kNorm) rx[k] = __ldcs(reinterpret_cast<const uint4*>(a.x + off + static_cast<size_t>(i) * D));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const int i = base + k * kSlots + slot;
+        if (base + k * kSlots >= n) break;
+        float dz[8], p[8];
+        unpack8(rg[k], dz);
+        if (a.layout == MSA_ROPE_HALF) unpack8(shfl4(rg[k], psrc), p);
+        const int ii = i < n ? i : n - 1;
+        const int tok = static_cast<int>((static_cast<uint32_t>(h0 + ii) * a.inv) >> 20);
+        if (rot) rx_turn(dz, p, table + tok * a.R, c, a.R, a.layout, -1.f);
+        if (kNorm) {
+          float xv[8], ss = 0.f, dot = 0.f;
+          unpack8(rx[k], xv);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            ss = fmaf(xv[e], xv[e], ss);
+            dot = fmaf(dz[e] * w1[e], xv[e], dot);
+          }
+#pragma unroll
+          for (int m = kLpr / 2; m >= 1; m >>= 1) {
+            ss += __shfl_xor_sync(0xffffffffu, ss, m);
+            dot += __shfl_xor_sync(0xffffffffu, dot, m);
+          }
+          const float rinv = rsqrtf(ss * (1.f / D) + a.eps);
+          const float mean = dot * rinv * (1.f / D);   // mean(g xh)
+          if (i < n) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float xh = xv[e] * rinv;
+              aw[e] = fmaf(dz[e], xh, aw[e]);
+              dz[e] = rinv * (dz[e] * w1[e] - xh * mean);
+            }
+          }
+        }
+        if (i < n) *reinterpret_cast<uint4*>(a.y + off + static_cast<size_t>(i) * D) = pack8(dz);
+      }
+    }
+  }
+  if (kNorm) {
+    // the CTA's row slots, added in slot order -> one partial row
+    __syncthreads();
+    float* red = table;                            // [kSlots][D]: 4 KB
+#pragma unroll
+    for (int e = 0; e < 8; ++e) red[slot * D + 8 * c + e] = aw[e];
+    __syncthreads();
+    for (int ch = threadIdx.x; ch < D; ch += kRxThreads) {
+      float acc = 0.f;
+      for (int sl = 0; sl < kSlots; ++sl) acc += red[sl * D + ch];
+      a.dw_part[static_cast<size_t>(blockIdx.x) * D + ch] = acc;
+    }
+  }
+}
+
+// dw[ch] = the partial rows in a fixed order: thread (k, ch) adds rows k,
+// k + 128, ..., then a pairwise tree over k.
+constexpr int kRxSumCh = 8, kRxSumWays = 128;
+__global__ void __launch_bounds__(kRxSumCh * kRxSumWays)
+    rope_ex_dw_kernel(const float* __restrict__ part, int nparts, int D, float* __restrict__ dw) {
+  pdl_enter();
+  __shared__ float red[kRxSumWays][kRxSumCh];
+  const int cl = threadIdx.x % kRxSumCh, k = threadIdx.x / kRxSumCh;
+  const int ch = blockIdx.x * kRxSumCh + cl;
+  float acc = 0.f;
+  for (int p = k; p < nparts; p += kRxSumWays) acc += part[static_cast<size_t>(p) * D + ch];
+  red[k][cl] = acc;
+  __syncthreads();
+#pragma unroll
+  for (int s = kRxSumWays / 2; s >= 1; s >>= 1) {
+    if (k < s) red[k][cl] += red[k + s][cl];
+    __syncthreads();
+  }
+  if (k == 0) dw[ch] = red[0][cl];
+}
+
+// ---------------------------------------------------------------- host
+
+// Rows per CTA: `target` rows, fewer when the run's tokens would not fit the
+// angle table.  A run of n rows touches at most (n + 2 H - 2) / H tokens.
+static int rx_run(int H, int R, int target) {
+  const int cap_tok = kRxMaxAngles / (R / 2);            // >= 16
+  const long long cap = static_cast<long long>(cap_tok - 1) * H;
+  return static_cast<int>(cap < target ? cap : target);
+}
+
+constexpr int kRxFwdRun = 128, kRxBwdRun = 128, kRxBwdCtas = 1216;   // 8 per SM
+
+static int rx_bwd_ctas(long long rows, int run) {
+  const long long n = (rows + run - 1) / run;
+  return static_cast<int>(n < kRxBwdCtas ? n : kRxBwdCtas);
+}
+
+size_t rope_ex_bwd_workspace_floats(int T, int H, int D) {
+  (void)T;
+  (void)H;
+  return static_cast<size_t>(kRxBwdCtas) * D;
+}
+
+unsigned long long rope_turn(double freq) {
+  const double turn = freq / 6.283185307179586476925286766559;
+  const double frac = turn - std::floor(turn);
+  return frac >= 1.0 ? 0 : static_cast<unsigned long long>(frac * 18446744073709551616.0);
+}
+
+static RxTurns rx_turns(const msa_rope_t& rope) {
+  RxTurns t;
+  for (int i = 0; i < kRxMaxPairs; ++i)
+    t.f[i] = i < rope.dim / 2 ? rope_turn(rope.freqs[i]) : 0;
+  return t;
+}
+
+static RxArgs rx_args(const RopeExJob& j, const msa_rope_t& rope) {
+  RxArgs a{};
+  a.x = j.x;
+  a.dy = j.dy;
+  a.y = j.y;
+  a.w = j.w;
+  a.positions = j.positions;
+  a.cu = j.cu;
+  a.rows = static_cast<long long>(j.T) * j.H;
+  a.T = j.T;
+  a.H = j.H;
+  a.S = j.S;
+  a.R = rope.dim;
+  a.layout = rope.layout;
+  a.inv = ((1u << 20) + j.H - 1) / j.H;
+  a.eps = j.eps;
+  a.gain = rope.gain;
+  return a;
+}
+
+template <int D>
+static msa_status_t rx_forward(const RopeExJob& j, const msa_rope_t& rope, cudaStream_t stream) {
+  RxArgs a = rx_args(j, rope);
+  a.run = rx_run(j.H, rope.dim, kRxFwdRun);
+  const RxTurns turns = rx_turns(rope);
+  const unsigned grid = static_cast<unsigned>((a.rows + a.run - 1) / a.run);
+  TraceScope trace_("rope_ex_kernel", stream);
+  launch_pdl(j.w ? rope_ex_kernel<D, true> : rope_ex_kernel<D, false>, grid, kRxThreads, 0, stream,
+             a, turns);
+  return check_launch("rope_ex_kernel");
+}
+
+template <int D>
+static msa_status_t rx_backward(const RopeExJob& j, const msa_rope_t& rope, float* dw,
+                                float* dw_part, cudaStream_t stream) {
+  RxArgs a = rx_args(j, rope);
+  a.run = rx_run(j.H, rope.dim, kRxBwdRun);
+  a.dw_part = dw_part;
+  const RxTurns turns = rx_turns(rope);
+  const int ctas = rx_bwd_ctas(a.rows, a.run);
+  {
+    TraceScope trace_("rope_ex_bwd_kernel", stream);
+    launch_pdl(j.w ? rope_ex_bwd_kernel<D, true> : rope_ex_bwd_kernel<D, false>, ctas, kRxThreads,
+               0, stream, a, turns);
+  }
+  msa_status_t e = check_launch("rope_ex_bwd_kernel");
+  if (e != MSA_OK || !j.w) return e;
+  {
+    TraceScope trace_("rope_ex_dw_kernel", stream);
+    launch_pdl(rope_ex_dw_kernel, D / kRxSumCh, kRxSumCh * kRxSumWays, 0, stream, dw_part, ctas, D,
+               dw);
+  }
+  return check_launch("rope_ex_dw_kernel");
+}
+
+msa_status_t launch_rope_ex(const RopeExJob& j, const msa_rope_t& rope, cudaStream_t stream) {
+  if (j.D == 64) return rx_forward<64>(j, rope, stream);
+  if (j.D == 128) return rx_forward<128>(j, rope, stream);
+  return rx_forward<256>(j, rope, stream);
+}
+
+msa_status_t launch_rope_ex_bwd(const RopeExJob& j, const msa_rope_t& rope, float* dw,
+                                float* dw_part, cudaStream_t stream) {
+  if (j.D == 64) return rx_backward<64>(j, rope, dw, dw_part, stream);
+  if (j.D == 128) return rx_backward<128>(j, rope, dw, dw_part, stream);
+  return rx_backward<256>(j, rope, dw, dw_part, stream);
+}
+
+// ====================================================================== C ABI
+
+msa_status_t check_rope_arg(const msa_rope_t* rope, int D) {
+  if (!rope) return fail(MSA_ERR_INVALID_ARG, "rope is null");
+  if (rope->dim < 16 || rope->dim % 16 != 0 || rope->dim > 2 * kRxMaxPairs)
+    return fail(MSA_ERR_UNSUPPORTED, "rope dim %d is not a multiple of 16 in [16, %d]", rope->dim,
+                2 * kRxMaxPairs);
+  if (rope->dim > D)
+    return fail(MSA_ERR_INVALID_ARG, "rope dim %d above the head dim %d", rope->dim, D);
+  if (rope->layout != MSA_ROPE_HALF && rope->layout != MSA_ROPE_INTERLEAVED)
+    return fail(MSA_ERR_INVALID_ARG, "rope layout %d unknown", rope->layout);
+  if (!(rope->gain > 0.0f) || !std::isfinite(rope->gain))
+    return fail(MSA_ERR_INVALID_ARG, "rope gain must be finite and > 0");
+  for (int i = 0; i < rope->dim / 2; ++i)
+    if (!std::isfinite(rope->freqs[i]))
+      return fail(MSA_ERR_INVALID_ARG, "rope frequency %d is not finite", i);
+  return MSA_OK;
+}
+
+static msa_status_t check_rope_ex(const void* x, const void* w, const int32_t* positions,
+                                  const int32_t* cu, int S, int T, int H, int D, float eps,
+                                  const msa_rope_t* rope) {
+  (void)x;
+  if (w && !aligned16(w)) return fail(MSA_ERR_INVALID_ARG, "w is not 16-byte aligned");
+  if (T < 1 || H < 1) return fail(MSA_ERR_INVALID_ARG, "T and H must be >= 1 (got %d, %d)", T, H);
+  if (H > kRxMaxH)
+    return fail(MSA_ERR_UNSUPPORTED, "at most %d heads per tensor (got %d)", kRxMaxH, H);
+  if (D != 64 && D != 128 && D != 256)
+    return fail(MSA_ERR_UNSUPPORTED, "head dim must be 64, 128 or 256 (got %d)", D);
+  if (positions) {
+    if (!aligned16(positions)) return fail(MSA_ERR_INVALID_ARG, "positions is not 16-byte aligned");
+  } else {
+    if (!cu || !aligned16(cu))
+      return fail(MSA_ERR_INVALID_ARG, "neither positions nor (16-byte aligned) cu_seqlens given");
+    if (S < 1) return fail(MSA_ERR_INVALID_ARG, "S must be >= 1 (got %d)", S);
+  }
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(MSA_ERR_INVALID_ARG, "eps must be >= 0");
+  return check_rope_arg(rope, D);
+}
+
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" {
+
+msa_status_t msa_rope_init(msa_rope_t* rope, int dim, double base, int layout, int scaling,
+                           double factor, double orig_len, double beta_fast, double beta_slow,
+                           double gain) {
+  if (!rope) return fail(MSA_ERR_INVALID_ARG, "rope is null");
+  if (dim < 16 || dim % 16 != 0 || dim > 2 * kRxMaxPairs)
+    return fail(MSA_ERR_UNSUPPORTED, "rope dim %d is not a multiple of 16 in [16, %d]", dim,
+                2 * kRxMaxPairs);
+  if (layout != MSA_ROPE_HALF && layout != MSA_ROPE_INTERLEAVED)
+    return fail(MSA_ERR_INVALID_ARG, "rope layout %d unknown", layout);
+  if (scaling < MSA_ROPE_PLAIN || scaling > MSA_ROPE_YARN)
+    return fail(MSA_ERR_INVALID_ARG, "rope scaling %d unknown", scaling);
+  if (!(base > 1.0) || !std::isfinite(base))
+    return fail(MSA_ERR_INVALID_ARG, "rope base must be finite and > 1");
+  if (scaling != MSA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return fail(MSA_ERR_INVALID_ARG, "rope factor must be finite and >= 1");
+  if (scaling == MSA_ROPE_YARN) {
+    if (!(orig_len >= 1.0) || !std::isfinite(orig_len))
+      return fail(MSA_ERR_INVALID_ARG, "orig_len must be finite and >= 1");
+    if (!(beta_fast > beta_slow) || !(beta_slow >= 0.0) || !std::isfinite(beta_fast))
+      return fail(MSA_ERR_INVALID_ARG, "beta_fast > beta_slow >= 0 is needed");
+  }
+  if (!std::isfinite(gain) || gain < 0.0)
+    return fail(MSA_ERR_INVALID_ARG, "gain must be finite and >= 0 (0: the scaling's own)");
+  const double two_pi = 6.283185307179586476925286766559;
+  const double b = scaling == MSA_ROPE_NTK
+                       ? base * std::pow(factor, static_cast<double>(dim) / (dim - 2)) : base;
+  if (!std::isfinite(b)) return fail(MSA_ERR_INVALID_ARG, "rope base overflows");
+  rope->dim = dim;
+  rope->layout = layout;
+  rope->reserved = 0.0f;
+  for (int i = 0; i < kRxMaxPairs; ++i) {
+    rope->freqs[i] = 0.0;
+    if (i >= dim / 2) continue;
+    double f = std::pow(b, -2.0 * i / dim);
+    if (scaling == MSA_ROPE_LINEAR) f /= factor;
+    if (scaling == MSA_ROPE_YARN) {
+      // pairs with more than beta_fast turns over the trained length keep their
+      // angle, those below beta_slow are stretched, a linear ramp between
+      double keep = (orig_len * f / two_pi - beta_slow) / (beta_fast - beta_slow);
+      keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+      f = f / factor * (1.0 - keep) + f * keep;
+    }
+    rope->freqs[i] = f;
+  }
+  const double own = scaling == MSA_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  rope->gain = static_cast<float>(gain > 0.0 ? gain : own);
+  return MSA_OK;
+}
+
+msa_status_t msa_qk_norm_rope_ex(const void* x, void* y, int T, int H, int D, const void* w,
+                                 const int32_t* positions, const int32_t* cu_seqlens, int S,
+                                 const msa_rope_t* rope, float eps, msa_stream_t stream) {
+  MSA_REQUIRE_PTR(x);
+  MSA_REQUIRE_PTR(y);
+  MSA_TRY(check_rope_ex(x, w, positions, cu_seqlens, S, T, H, D, eps, rope));
+  RopeExJob j{};
+  j.x = static_cast<const __nv_bfloat16*>(x);
+  j.y = static_cast<__nv_bfloat16*>(y);
+  j.w = static_cast<const __nv_bfloat16*>(w);
+  j.positions = positions;
+  j.cu = cu_seqlens;
+  j.T = T;
+  j.H = H;
+  j.D = D;
+  j.S = S;
+  j.eps = eps;
+  return launch_rope_ex(j, *rope, static_cast<cudaStream_t>(stream));
+}
+
+size_t msa_qk_norm_rope_bwd_ex_workspace_size(int T, int H, int D) {
+  if (T < 1 || H < 1 || D < 1) return 0;
+  return rope_ex_bwd_workspace_floats(T, H, D) * sizeof(float);
+}
+
+msa_status_t msa_qk_norm_rope_bwd_ex(const void* x, const void* dy, void* dx, float* dw, int T,
+                                     int H, int D, const void* w, const int32_t* positions,
+                                     const int32_t* cu_seqlens, int S, const msa_rope_t* rope,
+                                     float eps, void* workspace, size_t workspace_bytes,
+                                     msa_stream_t stream) {
+  MSA_REQUIRE_PTR(dy);
+  MSA_REQUIRE_PTR(dx);
+  if (w) {
+    MSA_REQUIRE_PTR(x);
+    MSA_REQUIRE_PTR(dw);
+    MSA_REQUIRE_PTR(workspace);
+  }
+  MSA_TRY(check_rope_ex(x, w, positions, cu_seqlens, S, T, H, D, eps, rope));
+  if (w && workspace_bytes < msa_qk_norm_rope_bwd_ex_workspace_size(T, H, D))
+    return fail(MSA_ERR_INVALID_ARG, "workspace too small");
+  RopeExJob j{};
+  j.x = static_cast<const __nv_bfloat16*>(x);
+  j.dy = static_cast<const __nv_bfloat16*>(dy);
+  j.y = static_cast<__nv_bfloat16*>(dx);
+  j.w = static_cast<const __nv_bfloat16*>(w);
+  j.positions = positions;
+  j.cu = cu_seqlens;
+  j.T = T;
+  j.H = H;
+  j.D = D;
+  j.S = S;
+  j.eps = eps;
+  return launch_rope_ex_bwd(j, *rope, dw, static_cast<float*>(workspace),
+                            static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
