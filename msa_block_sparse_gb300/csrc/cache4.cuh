@@ -38,8 +38,8 @@ __device__ __forceinline__ uint32_t code_pair(float a, float b, float s, float r
   a = fminf(fmaxf(a, -1e30f), 1e30f);
   b = fminf(fmaxf(b, -1e30f), 1e30f);
   float qa = a * rs, qb = b * rs;
-  qa = fmaf(fmaf(-qa, s, a), rs, qa);
-  qb = fmaf(fmaf(-qb, s, b), rs, qb);
+  qa = copysignf(fmaf(fmaf(-qa, s, a), rs, qa), a);   // -0 keeps its sign
+  qb = copysignf(fmaf(fmaf(-qb, s, b), rs, qb), b);
   return __nv_cvt_float2_to_fp4x2(make_float2(qa, qb), __NV_E2M1, cudaRoundNearest);
 }
 
