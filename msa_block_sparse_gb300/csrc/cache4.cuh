@@ -71,12 +71,18 @@ __device__ __forceinline__ uint2 quantise16(const uint32_t (&x)[8], float inv_ga
   return make_uint2(w[0], w[1]);
 }
 
-// 8 codes (one word, channel order) as four packed fp16 pairs, exact
+// 8 codes (one word, channel order) as four packed fp16 pairs, exact.  The
+// bytes are unpacked in the conversion's own block: taken out by shifts and masks
+// they cost two more instructions each, and this unpacking bounds the score kernel.
 __device__ __forceinline__ void codes_half2(uint32_t w, __half2 (&h)[4]) {
+  uint32_t r[4];
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = __half2(__nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>((w >> (8 * i)) & 0xFFu),
-                                              __NV_E2M1));
+  for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<__half2*>(&r[i]);
 }
 
 }  // namespace msa

@@ -79,93 +79,198 @@ __device__ __forceinline__ float2 scales_f2(uint32_t two) {
 
 // ---------------------------------------------------------------- scores
 
-constexpr int kScPages = 8;     // pages of one sequence per CTA
-constexpr int kScWarps = 8;
+constexpr int kScWarps = 12;
+constexpr int kScStages = 2;
+constexpr int kScMaxB = 1024;   // rows whose unit counts are summed in shared memory
 
-// grid (ceil(max_pages / 8), B): a warp takes (page, head) units.
-__global__ void __launch_bounds__(32 * kScWarps) decode4_score_kernel(
+struct Score4Smem {
+  alignas(128) uint8_t slab[kScWarps][kScStages][kSlab];
+  uint64_t full[kScWarps][kScStages];
+  int start[kScMaxB + 1];       // first unit of each sequence of the pass
+  int warp_sums[kScWarps];
+};
+static_assert(sizeof(Score4Smem) <= 232448, "score shared memory above the 227 KB limit");
+
+// Persistent CTAs, one per SM.  The units (sequence, head, block to score) are
+// counted from the lengths by every CTA and cut into equal runs, one per warp of the
+// grid; a warp streams its slabs through its own two buffers with bulk copies and
+// shares nothing with the others.  Rows beyond 1024 are taken in further passes.
+__global__ void __launch_bounds__(32 * kScWarps, 1) decode4_score_kernel(
     const __nv_bfloat16* __restrict__ q_idx, const uint8_t* __restrict__ kidx,
-    const int32_t* __restrict__ table, const int32_t* __restrict__ lens, int Hkv, int num_pages,
-    int max_pages, int n_init, float* __restrict__ scores, uint32_t* status) {
+    const int32_t* __restrict__ table, const int32_t* __restrict__ lens, int B, int Hkv,
+    int num_pages, int max_pages, int n_init, float* __restrict__ scores, uint32_t* status) {
   pdl_enter();
-  const int b = blockIdx.y;
-  const int L = d4_len(lens[b], max_pages, status);
-  const int own = (L + kBlock - 1) / kBlock - 1;
-  if (own < kTopK) return;                         // every block is kept
-  const int c0 = max(blockIdx.x * kScPages, n_init), c1 = min(own, (blockIdx.x + 1) * kScPages);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, c = lane & 3;
-  const int units = (c1 - c0) * Hkv;
-  int have_h = -1;
-  uint32_t bq[2][4][2];                            // B operand of the k-steps
-  for (int u = warp; u < units; u += kScWarps) {
-    // pages of one head after another, so that a warp keeps its q operand
-    const int h = u / (c1 - c0), blk = c0 + u % (c1 - c0);
-    const int pg = table[static_cast<size_t>(b) * max_pages + blk];
-    float* out = scores + (static_cast<size_t>(b) * Hkv + h) * max_pages + blk;
-    if (pg < 0 || pg >= num_pages) {
-      atomicOr(status, kStatusBounds);
-      if (lane == 0) *out = -INFINITY;
-      continue;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Score4Smem& sm = *reinterpret_cast<Score4Smem*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int gw = blockIdx.x * kScWarps + warp, nw = gridDim.x * kScWarps;
+  if (lane == 0) {
+    for (int i = 0; i < kScStages; ++i) mbar_init(&sm.full[warp][i], 1);
+    fence_mbar_init();
+  }
+  uint32_t nload = 0, nuse = 0;                    // slabs asked for and used by this warp
+  bool dead = false;                               // a wait ran out
+  for (int b0 = 0; b0 < B; b0 += kScMaxB) {
+    const int nb = min(kScMaxB, B - b0);
+    // ---- start[i] = units of the sequences before i; none where all blocks are kept
+    auto units_of = [&](int b) {
+      const int L = d4_len(lens[b], max_pages, status);
+      const int own = (L + kBlock - 1) / kBlock - 1;
+      return own >= kTopK ? (own - n_init) * Hkv : 0;
+    };
+    __syncthreads();
+    int carry = 0;
+    for (int i0 = 0; i0 < nb; i0 += 32 * kScWarps) {
+      const int i = i0 + tid;
+      const int v = i < nb ? units_of(b0 + i) : 0;
+      int x = v;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+      }
+      if (lane == 31) sm.warp_sums[warp] = x;
+      __syncthreads();
+      int before = carry, total = carry;
+#pragma unroll
+      for (int w = 0; w < kScWarps; ++w) {
+        if (w < warp) before += sm.warp_sums[w];
+        total += sm.warp_sums[w];
+      }
+      if (i < nb) sm.start[i] = before + x - v;
+      carry = total;
+      __syncthreads();
     }
-    if (h != have_h) {
-      have_h = h;
-      // lane l looks at channels 4l .. 4l + 3 for the row's largest magnitude
-      const __nv_bfloat16* qr = q_idx + (static_cast<size_t>(b) * Hkv + h) * kD;
-      const uint2 mine = *reinterpret_cast<const uint2*>(qr + 4 * lane);
-      uint32_t m = __vmaxu2(mine.x & 0x7FFF7FFFu, mine.y & 0x7FFF7FFFu);
-      m = max(m & 0xFFFFu, m >> 16);
-      m = __reduce_max_sync(0xffffffffu, m);
-      const float f = exp2i(row_shift(m));
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint2 w = *reinterpret_cast<const uint2*>(qr + 32 * c + 16 * hf + 4 * t);
-          const bool col = g == 2 * c + hf;        // this thread's column is the block's
-          bq[hf][t][0] = col ? bf2_to_h2(w.x, f) : 0u;
-          bq[hf][t][1] = col ? bf2_to_h2(w.y, f) : 0u;
+    if (tid == 0) sm.start[nb] = carry;
+    __syncthreads();
+    const int total = carry;
+    // ---- this warp's run of units
+    const int u0 = static_cast<int>(static_cast<long long>(total) * gw / nw);
+    const int u1 = static_cast<int>(static_cast<long long>(total) * (gw + 1) / nw);
+    if (u0 >= u1 || dead) continue;
+    // lane l keeps (row, head, block, page) of unit base + l
+    int my_bh = 0, my_blk = 0, my_pg = -1;
+    auto look_up = [&](int base) {
+      const int u = base + lane;
+      my_pg = -1;
+      if (u < u1) {
+        int lo = 0, hi = nb;                       // largest i with start[i] <= u
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (sm.start[mid] <= u) lo = mid; else hi = mid;
         }
-    }
-    const uint8_t* slab = kidx + (static_cast<size_t>(pg) * Hkv + h) * kSlab;
-    float best = -INFINITY;
-#pragma unroll 2
-    for (int r0 = 0; r0 < kBlock; r0 += 16) {
-      const uint4 ka = __ldcs(reinterpret_cast<const uint4*>(slab + slab_code(r0 + g)) + c);
-      const uint4 kb = __ldcs(reinterpret_cast<const uint4*>(slab + slab_code(r0 + g + 8)) + c);
-      const uint32_t sa = __ldcs(reinterpret_cast<const uint16_t*>(slab + slab_scale(r0 + g)) + c);
-      const uint32_t sb = __ldcs(reinterpret_cast<const uint16_t*>(slab + slab_scale(r0 + g + 8)) + c);
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {                // 8 channels: two k-steps
-        __half2 ha[4], hb[4];
-        codes_half2(wa[w], ha);
-        codes_half2(wb[w], hb);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int t = (2 * w + k) & 3, hf = w >> 1;
-          mma_f16_16816(acc, h2u(ha[2 * k]), h2u(hb[2 * k]), h2u(ha[2 * k + 1]), h2u(hb[2 * k + 1]),
-                        bq[hf][t][0], bq[hf][t][1]);
+        const int b = b0 + lo, r = u - sm.start[lo];
+        const int per = (sm.start[lo + 1] - sm.start[lo]) / Hkv;   // blocks of one head
+        const int h = r / per;
+        my_bh = b * Hkv + h;
+        my_blk = n_init + r - h * per;
+        my_pg = table[static_cast<size_t>(b) * max_pages + my_blk];
+        if (my_pg < 0 || my_pg >= num_pages) {
+          atomicOr(status, kStatusBounds);
+          scores[static_cast<size_t>(my_bh) * max_pages + my_blk] = -INFINITY;
+          my_pg = -1;
         }
       }
-      const float2 fa = scales_f2(sa), fb = scales_f2(sb);
-      float za = fmaf(acc[0], fa.x, acc[1] * fa.y), zb = fmaf(acc[2], fb.x, acc[3] * fb.y);
-      za += __shfl_xor_sync(0xffffffffu, za, 1);
-      zb += __shfl_xor_sync(0xffffffffu, zb, 1);
-      za += __shfl_xor_sync(0xffffffffu, za, 2);
-      zb += __shfl_xor_sync(0xffffffffu, zb, 2);
-      best = fmaxf(best, fmaxf(za, zb));
-    }
+    };
+    int have_bh = -1;
+    uint32_t bq[2][4][2];                          // B operand of the k-steps
+    bool ok = true;
+    for (int base = u0; base < u1 && ok; base += 32) {
+      look_up(base);
+      // units of this group that have a page, in order
+      uint32_t todo = __ballot_sync(0xffffffffu, my_pg >= 0), ask = todo;
+      auto load = [&]() {
+        if (!ask) return;
+        const int j = __ffs(ask) - 1;
+        ask &= ask - 1u;
+        const int pg = __shfl_sync(0xffffffffu, my_pg, j), bh = __shfl_sync(0xffffffffu, my_bh, j);
+        if (lane == 0) {
+          const int st = nload % kScStages;
+          mbar_arrive_expect_tx(&sm.full[warp][st], kSlab);
+          bulk_load(sm.slab[warp][st], kidx + (static_cast<size_t>(pg) * Hkv + bh % Hkv) * kSlab, kSlab,
+                    &sm.full[warp][st]);
+        }
+        ++nload;
+      };
+      for (int i = 0; i < kScStages; ++i) load();
+      while (todo) {
+        const int j = __ffs(todo) - 1;
+        todo &= todo - 1u;
+        const int bh = __shfl_sync(0xffffffffu, my_bh, j), blk = __shfl_sync(0xffffffffu, my_blk, j);
+        if (bh != have_bh) {
+          have_bh = bh;
+          // lane l looks at channels 4l .. 4l + 3 for the row's largest magnitude
+          const __nv_bfloat16* qr = q_idx + static_cast<size_t>(bh) * kD;
+          const uint2 mine = *reinterpret_cast<const uint2*>(qr + 4 * lane);
+          uint32_t m = __vmaxu2(mine.x & 0x7FFF7FFFu, mine.y & 0x7FFF7FFFu);
+          m = max(m & 0xFFFFu, m >> 16);
+          m = __reduce_max_sync(0xffffffffu, m);
+          const float f = exp2i(row_shift(m));
 #pragma unroll
-    for (int m = 4; m <= 16; m <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, m));
-    if (lane == 0) *out = best;
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const uint2 w = *reinterpret_cast<const uint2*>(qr + 32 * c + 16 * hf + 4 * t);
+              const bool col = g == 2 * c + hf;    // this thread's column is the block's
+              bq[hf][t][0] = col ? bf2_to_h2(w.x, f) : 0u;
+              bq[hf][t][1] = col ? bf2_to_h2(w.y, f) : 0u;
+            }
+        }
+        const int st = nuse % kScStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[warp][st], (nuse / kScStages) & 1, status, 81))) {
+          ok = false;
+          break;
+        }
+        ++nuse;
+        const uint8_t* slab = sm.slab[warp][st];
+        float best = -INFINITY;
+#pragma unroll 2
+        for (int r0 = 0; r0 < kBlock; r0 += 16) {
+          const uint4 ka = *(reinterpret_cast<const uint4*>(slab + slab_code(r0 + g)) + c);
+          const uint4 kb = *(reinterpret_cast<const uint4*>(slab + slab_code(r0 + g + 8)) + c);
+          const uint32_t sa = *(reinterpret_cast<const uint16_t*>(slab + slab_scale(r0 + g)) + c);
+          const uint32_t sb = *(reinterpret_cast<const uint16_t*>(slab + slab_scale(r0 + g + 8)) + c);
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {            // 8 channels: two k-steps
+            __half2 ha[4], hb[4];
+            codes_half2(wa[w], ha);
+            codes_half2(wb[w], hb);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int t = (2 * w + k) & 3, hf = w >> 1;
+              mma_f16_16816(acc, h2u(ha[2 * k]), h2u(hb[2 * k]), h2u(ha[2 * k + 1]),
+                            h2u(hb[2 * k + 1]), bq[hf][t][0], bq[hf][t][1]);
+            }
+          }
+          const float2 fa = scales_f2(sa), fb = scales_f2(sb);
+          float za = fmaf(acc[0], fa.x, acc[1] * fa.y), zb = fmaf(acc[2], fb.x, acc[3] * fb.y);
+          za += __shfl_xor_sync(0xffffffffu, za, 1);
+          zb += __shfl_xor_sync(0xffffffffu, zb, 1);
+          za += __shfl_xor_sync(0xffffffffu, za, 2);
+          zb += __shfl_xor_sync(0xffffffffu, zb, 2);
+          best = fmaxf(best, fmaxf(za, zb));
+        }
+        __syncwarp();                              // every lane has read the buffer
+        load();
+#pragma unroll
+        for (int m = 4; m <= 16; m <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, m));
+        if (lane == 0) scores[static_cast<size_t>(bh) * max_pages + blk] = best;
+      }
+    }
+    if (!ok) {                                     // slabs still on their way: wait (bounded), leave
+      for (; nuse < nload; ++nuse)
+        (void)mbar_wait(&sm.full[warp][nuse % kScStages], (nuse / kScStages) & 1, status, 82);
+      dead = true;
+    }
   }
 }
 
 // ---------------------------------------------------------------- attention
 
 constexpr int kAtWarps = kD4Threads / 32;
+constexpr int kCand = kTopK;        // candidates per warp: 15 and one empty
 
 template <int NS>
 struct Attend4Smem {
@@ -176,7 +281,7 @@ struct Attend4Smem {
   float ml[kAtWarps][16][2];
   float cta_ml[16][2];
   union {
-    alignas(16) float key[kMaxSeqlen / kBlock];    // scores
+    alignas(16) uint2 cand[kAtWarps * kCand];      // selection: (key, block)
     uint32_t qh[16 * kD / 2];                      // q rows, packed fp16
   };
   float qfac[16];                                  // per row: what undoes q's power of two
@@ -242,27 +347,54 @@ __global__ void __launch_bounds__(kD4Threads) decode4_attend_kernel(
   if (tid < kMaxSeqlen / kBlock / 32) sm.bits[tid] = 0u;
   if (tid < kTopK) sm.list[tid] = -1;
   if (own >= kTopK) {
+    // Block 128 r + 32 w + l is lane l's r-th of warp w.  Each warp takes out its
+    // 15 best in turn (ties: lowest id), then the 60 candidates are ranked.
     const float* sc = scores + static_cast<size_t>(bh) * max_pages;
-    const int own4 = (own + 3) & ~3;
-    for (int i = tid; i < own4; i += kD4Threads)
-      sm.key[i] = i < own ? (i < n_init ? INFINITY : sc[i]) : -INFINITY;
-    __syncthreads();
-    // a block is kept when fewer than 15 rank before it: a higher score, or an
-    // equal one and a lower id (the padding behind own never does)
-    for (int i = tid; i < own; i += kD4Threads) {
-      const float ki = sm.key[i];
-      int n0 = 0, n1 = 0, n2 = 0, n3 = 0;
-#pragma unroll 4
-      for (int j = 0; j < own4; j += 4) {
-        const float4 k4 = *reinterpret_cast<const float4*>(&sm.key[j]);
-        n0 += (k4.x > ki || (k4.x == ki && j < i)) ? 1 : 0;
-        n1 += (k4.y > ki || (k4.y == ki && j + 1 < i)) ? 1 : 0;
-        n2 += (k4.z > ki || (k4.z == ki && j + 2 < i)) ? 1 : 0;
-        n3 += (k4.w > ki || (k4.w == ki && j + 3 < i)) ? 1 : 0;
+    constexpr int kPer = kMaxSeqlen / kBlock / kD4Threads;
+    uint32_t key[kPer];                            // ordered as the scores are; 0: none
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+      const int i = kD4Threads * r + tid;
+      key[r] = 0u;
+      if (i < own) {
+        // + 0: a score of -0 equals one of 0
+        const uint32_t u = i < n_init ? 0u : __float_as_uint(sc[i] + 0.f);
+        key[r] = i < n_init ? 0xFFFFFFFFu : (u & 0x80000000u ? ~u : u | 0x80000000u);
       }
-      if (n0 + n1 + n2 + n3 < kTopK - 1) atomicOr(&sm.bits[i >> 5], 1u << (i & 31));
     }
-    if (tid == 0) atomicOr(&sm.bits[own >> 5], 1u << (own & 31));
+    __syncthreads();                               // bits and list are set up
+#pragma unroll 1
+    for (int n = 0; n < kTopK - 1; ++n) {
+      uint32_t top = key[0];
+      int at = 0;
+#pragma unroll
+      for (int r = 1; r < kPer; ++r)
+        if (key[r] > top) top = key[r], at = r;
+      const uint32_t best = __reduce_max_sync(0xffffffffu, top);
+      const uint32_t id = static_cast<uint32_t>(kD4Threads * at + tid);
+      const uint32_t win = __reduce_min_sync(0xffffffffu, top == best ? id : 0xFFFFFFFFu);
+      if (lane == 0) sm.cand[warp * kCand + n] = make_uint2(best, win);
+      if (best == 0u) {                            // the warp has no more blocks
+        for (int k = n + 1 + lane; k < kTopK - 1; k += 32) sm.cand[warp * kCand + k] = make_uint2(0u, 0u);
+        break;
+      }
+#pragma unroll
+      for (int r = 0; r < kPer; ++r)
+        if (id == win && r == at) key[r] = 0u;
+    }
+    if (lane == 0) sm.cand[warp * kCand + kCand - 1] = make_uint2(0u, 0u);
+    __syncthreads();
+    if (tid < kAtWarps * kCand) {
+      const uint2 me = sm.cand[tid];
+      int before = 0;
+#pragma unroll 16
+      for (int j = 0; j < kAtWarps * kCand; ++j) {
+        const uint2 x = sm.cand[j];
+        before += (x.x > me.x || (x.x == me.x && x.y < me.y)) ? 1 : 0;
+      }
+      if (me.x != 0u && before < kTopK - 1) atomicOr(&sm.bits[me.y >> 5], 1u << (me.y & 31));
+    }
+    if (tid == kD4Threads - 1) atomicOr(&sm.bits[own >> 5], 1u << (own & 31));
     __syncthreads();
     if (warp == 0) {                               // set bits in ascending order
       uint32_t m = sm.bits[lane];
@@ -630,11 +762,11 @@ msa_status_t msa_decode4_step(const void* q, const void* q_idx, const void* k_ca
   MSA_TRY(status_word(&sw));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (max_pages > kTopK) {
+    MSA_TRY(ensure_smem(decode4_score_kernel, sizeof(Score4Smem), "decode4_score_kernel"));
     TraceScope trace_("decode4_score_kernel", st);
-    dim3 grid((max_pages + kScPages - 1) / kScPages, B);
-    launch_pdl(decode4_score_kernel, grid, 32 * kScWarps, 0, st,
+    launch_pdl(decode4_score_kernel, device_sm_count(), 32 * kScWarps, sizeof(Score4Smem), st,
                static_cast<const __nv_bfloat16*>(q_idx), static_cast<const uint8_t*>(kidx_cache),
-               block_table, cache_lens, Hkv, num_pages, max_pages, n_init, w.scores, sw);
+               block_table, cache_lens, B, Hkv, num_pages, max_pages, n_init, w.scores, sw);
     MSA_TRY(check_launch("decode4_score_kernel"));
   }
   return launch_attend4<4>(q, k_cache, v_cache, block_table, cache_lens, w.scores, B, G, Hkv,
