@@ -32,7 +32,6 @@ namespace msa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kD4Threads = 128;
 
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -80,22 +79,29 @@ __device__ __forceinline__ float2 scales_f2(uint32_t two) {
 // ---------------------------------------------------------------- scores
 
 constexpr int kScWarps = 12;
+constexpr int kScThreads = 32 * kScWarps;
 constexpr int kScStages = 2;
-constexpr int kScMaxB = 1024;   // rows whose unit counts are summed in shared memory
+constexpr int kScUnroll = 4;    // tiles of 16 keys whose products overlap
+constexpr int kScMaxB = 1024;   // rows whose unit counts are summed at a time
 
 struct Score4Smem {
   alignas(128) uint8_t slab[kScWarps][kScStages][kSlab];
   uint64_t full[kScWarps][kScStages];
-  int start[kScMaxB + 1];       // first unit of each sequence of the pass
+  int start[kScMaxB + 1];       // first unit of each row
+  int bh[kScThreads];           // units of the pass: row * Hkv + head,
+  int blk[kScThreads];          // block,
+  int page[kScThreads];         // page (-1: none)
+  int at[kScWarps][kScStages];  // unit of each buffer
   int warp_sums[kScWarps];
+  int claim;                    // next unit of the pass
 };
 static_assert(sizeof(Score4Smem) <= 232448, "score shared memory above the 227 KB limit");
 
-// Persistent CTAs, one per SM.  The units (sequence, head, block to score) are
-// counted from the lengths by every CTA and cut into equal runs, one per warp of the
-// grid; a warp streams its slabs through its own two buffers with bulk copies and
-// shares nothing with the others.  Rows beyond 1024 are taken in further passes.
-__global__ void __launch_bounds__(32 * kScWarps, 1) decode4_score_kernel(
+// Persistent CTAs, one per SM, each with an equal run of the units (row, head,
+// block to score), counted from the lengths by every CTA for itself.  A CTA looks up
+// 384 units at a time, one per thread; then its warps claim units and stream their
+// slabs, each through its own two buffers with bulk copies.
+__global__ void __launch_bounds__(kScThreads, 1) decode4_score_kernel(
     const __nv_bfloat16* __restrict__ q_idx, const uint8_t* __restrict__ kidx,
     const int32_t* __restrict__ table, const int32_t* __restrict__ lens, int B, int Hkv,
     int num_pages, int max_pages, int n_init, float* __restrict__ scores, uint32_t* status) {
@@ -103,7 +109,6 @@ __global__ void __launch_bounds__(32 * kScWarps, 1) decode4_score_kernel(
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Score4Smem& sm = *reinterpret_cast<Score4Smem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int gw = blockIdx.x * kScWarps + warp, nw = gridDim.x * kScWarps;
   if (lane == 0) {
     for (int i = 0; i < kScStages; ++i) mbar_init(&sm.full[warp][i], 1);
     fence_mbar_init();
@@ -112,17 +117,16 @@ __global__ void __launch_bounds__(32 * kScWarps, 1) decode4_score_kernel(
   bool dead = false;                               // a wait ran out
   for (int b0 = 0; b0 < B; b0 += kScMaxB) {
     const int nb = min(kScMaxB, B - b0);
-    // ---- start[i] = units of the sequences before i; none where all blocks are kept
-    auto units_of = [&](int b) {
-      const int L = d4_len(lens[b], max_pages, status);
-      const int own = (L + kBlock - 1) / kBlock - 1;
-      return own >= kTopK ? (own - n_init) * Hkv : 0;
-    };
+    // ---- start[i] = units of the rows before i; none where all blocks are kept
     __syncthreads();
-    int carry = 0;
-    for (int i0 = 0; i0 < nb; i0 += 32 * kScWarps) {
+    int total = 0;
+    for (int i0 = 0; i0 < nb; i0 += kScThreads) {
       const int i = i0 + tid;
-      const int v = i < nb ? units_of(b0 + i) : 0;
+      int v = 0;
+      if (i < nb) {
+        const int own = (d4_len(lens[b0 + i], max_pages, status) + kBlock - 1) / kBlock - 1;
+        v = own >= kTopK ? (own - n_init) * Hkv : 0;
+      }
       int x = v;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -131,72 +135,75 @@ __global__ void __launch_bounds__(32 * kScWarps, 1) decode4_score_kernel(
       }
       if (lane == 31) sm.warp_sums[warp] = x;
       __syncthreads();
-      int before = carry, total = carry;
+      int before = total;
 #pragma unroll
       for (int w = 0; w < kScWarps; ++w) {
         if (w < warp) before += sm.warp_sums[w];
         total += sm.warp_sums[w];
       }
       if (i < nb) sm.start[i] = before + x - v;
-      carry = total;
       __syncthreads();
     }
-    if (tid == 0) sm.start[nb] = carry;
+    if (tid == 0) sm.start[nb] = total;
     __syncthreads();
-    const int total = carry;
-    // ---- this warp's run of units
-    const int u0 = static_cast<int>(static_cast<long long>(total) * gw / nw);
-    const int u1 = static_cast<int>(static_cast<long long>(total) * (gw + 1) / nw);
-    if (u0 >= u1 || dead) continue;
-    // lane l keeps (row, head, block, page) of unit base + l
-    int my_bh = 0, my_blk = 0, my_pg = -1;
-    auto look_up = [&](int base) {
-      const int u = base + lane;
-      my_pg = -1;
-      if (u < u1) {
+    const int u0 = static_cast<int>(static_cast<long long>(total) * blockIdx.x / gridDim.x);
+    const int u1 = static_cast<int>(static_cast<long long>(total) * (blockIdx.x + 1) / gridDim.x);
+    for (int base = u0; base < u1; base += kScThreads) {
+      const int n = min(kScThreads, u1 - base);
+      __syncthreads();                             // the previous pass is done
+      if (tid < n) {
+        const int u = base + tid;
         int lo = 0, hi = nb;                       // largest i with start[i] <= u
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
           if (sm.start[mid] <= u) lo = mid; else hi = mid;
         }
-        const int b = b0 + lo, r = u - sm.start[lo];
+        const int r = u - sm.start[lo];
         const int per = (sm.start[lo + 1] - sm.start[lo]) / Hkv;   // blocks of one head
-        const int h = r / per;
-        my_bh = b * Hkv + h;
-        my_blk = n_init + r - h * per;
-        my_pg = table[static_cast<size_t>(b) * max_pages + my_blk];
-        if (my_pg < 0 || my_pg >= num_pages) {
+        const int h = r / per, bh = (b0 + lo) * Hkv + h, blk = n_init + r - h * per;
+        int pg = table[static_cast<size_t>(b0 + lo) * max_pages + blk];
+        if (pg < 0 || pg >= num_pages) {
           atomicOr(status, kStatusBounds);
-          scores[static_cast<size_t>(my_bh) * max_pages + my_blk] = -INFINITY;
-          my_pg = -1;
+          scores[static_cast<size_t>(bh) * max_pages + blk] = -INFINITY;
+          pg = -1;
         }
+        sm.bh[tid] = bh;
+        sm.blk[tid] = blk;
+        sm.page[tid] = pg;
       }
-    };
-    int have_bh = -1;
-    uint32_t bq[2][4][2];                          // B operand of the k-steps
-    bool ok = true;
-    for (int base = u0; base < u1 && ok; base += 32) {
-      look_up(base);
-      // units of this group that have a page, in order
-      uint32_t todo = __ballot_sync(0xffffffffu, my_pg >= 0), ask = todo;
-      auto load = [&]() {
-        if (!ask) return;
-        const int j = __ffs(ask) - 1;
-        ask &= ask - 1u;
-        const int pg = __shfl_sync(0xffffffffu, my_pg, j), bh = __shfl_sync(0xffffffffu, my_bh, j);
+      if (tid == 0) sm.claim = 0;
+      __syncthreads();
+      if (dead) continue;
+      auto load = [&]() {                          // claim a unit and ask for its slab
+        int i = n;
         if (lane == 0) {
-          const int st = nload % kScStages;
-          mbar_arrive_expect_tx(&sm.full[warp][st], kSlab);
-          bulk_load(sm.slab[warp][st], kidx + (static_cast<size_t>(pg) * Hkv + bh % Hkv) * kSlab, kSlab,
-                    &sm.full[warp][st]);
+          do {
+            i = atomicAdd(&sm.claim, 1);
+          } while (i < n && sm.page[i] < 0);
+          if (i < n) {
+            const int st = nload % kScStages;
+            sm.at[warp][st] = i;
+            mbar_arrive_expect_tx(&sm.full[warp][st], kSlab);
+            bulk_load(sm.slab[warp][st],
+                      kidx + (static_cast<size_t>(sm.page[i]) * Hkv + sm.bh[i] % Hkv) * kSlab, kSlab,
+                      &sm.full[warp][st]);
+          }
         }
-        ++nload;
+        nload += __shfl_sync(0xffffffffu, i, 0) < n ? 1u : 0u;
       };
+      int have_bh = -1;
+      uint32_t bq[2][4][2];                        // B operand of the k-steps
       for (int i = 0; i < kScStages; ++i) load();
-      while (todo) {
-        const int j = __ffs(todo) - 1;
-        todo &= todo - 1u;
-        const int bh = __shfl_sync(0xffffffffu, my_bh, j), blk = __shfl_sync(0xffffffffu, my_blk, j);
+      while (nuse < nload) {
+        const int st = nuse % kScStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[warp][st], (nuse / kScStages) & 1, status, 81))) {
+          for (++nuse; nuse < nload; ++nuse)       // wait (bounded) for what is on its way
+            (void)mbar_wait(&sm.full[warp][nuse % kScStages], (nuse / kScStages) & 1, status, 82);
+          dead = true;
+          break;
+        }
+        ++nuse;
+        const int unit = sm.at[warp][st], bh = sm.bh[unit];
         if (bh != have_bh) {
           have_bh = bh;
           // lane l looks at channels 4l .. 4l + 3 for the row's largest magnitude
@@ -216,15 +223,9 @@ __global__ void __launch_bounds__(32 * kScWarps, 1) decode4_score_kernel(
               bq[hf][t][1] = col ? bf2_to_h2(w.y, f) : 0u;
             }
         }
-        const int st = nuse % kScStages;
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[warp][st], (nuse / kScStages) & 1, status, 81))) {
-          ok = false;
-          break;
-        }
-        ++nuse;
         const uint8_t* slab = sm.slab[warp][st];
         float best = -INFINITY;
-#pragma unroll 2
+#pragma unroll kScUnroll
         for (int r0 = 0; r0 < kBlock; r0 += 16) {
           const uint4 ka = *(reinterpret_cast<const uint4*>(slab + slab_code(r0 + g)) + c);
           const uint4 kb = *(reinterpret_cast<const uint4*>(slab + slab_code(r0 + g + 8)) + c);
@@ -252,6 +253,7 @@ __global__ void __launch_bounds__(32 * kScWarps, 1) decode4_score_kernel(
           zb += __shfl_xor_sync(0xffffffffu, zb, 2);
           best = fmaxf(best, fmaxf(za, zb));
         }
+        const int blk = sm.blk[unit];
         __syncwarp();                              // every lane has read the buffer
         load();
 #pragma unroll
@@ -259,37 +261,48 @@ __global__ void __launch_bounds__(32 * kScWarps, 1) decode4_score_kernel(
         if (lane == 0) scores[static_cast<size_t>(bh) * max_pages + blk] = best;
       }
     }
-    if (!ok) {                                     // slabs still on their way: wait (bounded), leave
-      for (; nuse < nload; ++nuse)
-        (void)mbar_wait(&sm.full[warp][nuse % kScStages], (nuse / kScStages) & 1, status, 82);
-      dead = true;
-    }
   }
 }
 
 // ---------------------------------------------------------------- attention
 
-constexpr int kAtWarps = kD4Threads / 32;
-constexpr int kCand = kTopK;        // candidates per warp: 15 and one empty
+constexpr int kAtWarps = 4;
+constexpr int kAtThreads = 32 * kAtWarps;
+constexpr int kKeysPerWarp = kBlock / kAtWarps;
+constexpr float kAtRescale = 8.0f;  // log2 of the largest weight before a rescale (fp16: below 2^16)
 
 template <int NS>
 struct Attend4Smem {
   static constexpr int kBlocks = kTopK / NS;       // blocks per CTA
-  alignas(16) uint8_t k[kBlocks][kSlab];
-  alignas(16) uint8_t v[kBlocks][kSlab];
-  alignas(16) float o[kAtWarps][16][kD];           // per warp, then [0] = the CTA's sum
+  union {
+    struct {
+      alignas(16) uint8_t k[kBlocks][kSlab];
+      alignas(16) uint8_t v[kBlocks][kSlab];
+    } s;
+    alignas(16) float o[kAtWarps][16][kD];         // per warp once the slabs are used, then [0]
+                                                   // = the CTA's sum
+  };
   float ml[kAtWarps][16][2];
   float cta_ml[16][2];
-  union {
-    alignas(16) uint2 cand[kAtWarps * kCand];      // selection: (key, block)
-    uint32_t qh[16 * kD / 2];                      // q rows, packed fp16
-  };
-  float qfac[16];                                  // per row: what undoes q's power of two
-  uint32_t bits[kMaxSeqlen / kBlock / 32];         // kept blocks
-  int list[kTopK];
+  unsigned long long gmax[32];                     // selection: best key of each group of threads
+  int list[kTopK];                                 // selected blocks, -1 behind
   int page[kBlocks];
+  int ncand;
   uint64_t full[kBlocks];
 };
+
+// Float4 `chunk` (channel / 4) of row r in a [16][128] array of sums: permuted so
+// that the accumulator fragments' stores and the rows' loads meet no bank twice.
+__device__ __forceinline__ int o_at(int r, int chunk) {
+  return r * kD + 4 * (chunk ^ (chunk >> 3) ^ ((r & 1) << 2));
+}
+
+// Orders (score, block): a higher score first, then the lower block; 0 = none.
+__device__ __forceinline__ unsigned long long rank_key(float score, int block) {
+  const uint32_t u = __float_as_uint(score + 0.f);         // -0 equals 0
+  const uint32_t k = u & 0x80000000u ? ~u : u | 0x80000000u;
+  return static_cast<unsigned long long>(k) << 32 | static_cast<uint32_t>(0x7FFFFFFF - block);
+}
 
 __device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
   uint32_t r;
@@ -311,6 +324,11 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // grid (NS, B * Hkv) in clusters of NS CTAs; CTA `split` attends to the selected
 // blocks split, split + NS, ...  Each warp takes 32 keys of every block.
@@ -323,12 +341,12 @@ __device__ __forceinline__ void cluster_sync() {
 // g of n-tile i is channel 16 g + i.  Keys behind the sequence's end have P = 0 and
 // scale 0, whatever their slots hold.
 template <int NS>
-__global__ void __launch_bounds__(kD4Threads) decode4_attend_kernel(
+__global__ void __launch_bounds__(kAtThreads, 3) decode4_attend_kernel(
     const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ kc,
     const uint8_t* __restrict__ vc, const int32_t* __restrict__ table,
     const int32_t* __restrict__ lens, const float* __restrict__ scores, int G, int Hkv,
-    int num_pages, int max_pages, int n_init, float sl2, float v_gain,
-    __nv_bfloat16* __restrict__ o, int32_t* __restrict__ sel_out, uint32_t* status) {
+    int num_pages, int max_pages, int n_init, float sl2, float v_gain, __nv_bfloat16* __restrict__ o,
+    int32_t* __restrict__ sel_out, uint32_t* status) {
   pdl_enter();
   extern __shared__ __align__(128) uint8_t smem_raw[];
   using Smem = Attend4Smem<NS>;
@@ -336,135 +354,141 @@ __global__ void __launch_bounds__(kD4Threads) decode4_attend_kernel(
   constexpr int kBlocks = Smem::kBlocks;
   const int split = blockIdx.x, bh = blockIdx.y, b = bh / Hkv, h = bh % Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int L = d4_len(lens[b], max_pages, status);
-  const int nblk = (L + kBlock - 1) / kBlock;
-  const int own = nblk - 1;
-  if (tid == 0) {
-    for (int i = 0; i < kBlocks; ++i) mbar_init(&sm.full[i], 1);
-    fence_mbar_init();
-  }
-  // ---- selection (every CTA of the cluster for itself)
-  if (tid < kMaxSeqlen / kBlock / 32) sm.bits[tid] = 0u;
-  if (tid < kTopK) sm.list[tid] = -1;
-  if (own >= kTopK) {
-    // Block 128 r + 32 w + l is lane l's r-th of warp w.  Each warp takes out its
-    // 15 best in turn (ties: lowest id), then the 60 candidates are ranked.
-    const float* sc = scores + static_cast<size_t>(bh) * max_pages;
-    constexpr int kPer = kMaxSeqlen / kBlock / kD4Threads;
-    uint32_t key[kPer];                            // ordered as the scores are; 0: none
+  // ---- everything that depends on no other load is asked for at once
+  const int len = lens[b];
+  const float* sc = scores + static_cast<size_t>(bh) * max_pages;
+  constexpr int kPer = kMaxSeqlen / kBlock / kAtThreads;
+  float score[kPer];                               // blocks tid + 128 r (behind the own block: anything)
+  if (max_pages > kTopK) {
 #pragma unroll
     for (int r = 0; r < kPer; ++r) {
-      const int i = kD4Threads * r + tid;
-      key[r] = 0u;
-      if (i < own) {
-        // + 0: a score of -0 equals one of 0
-        const uint32_t u = i < n_init ? 0u : __float_as_uint(sc[i] + 0.f);
-        key[r] = i < n_init ? 0xFFFFFFFFu : (u & 0x80000000u ? ~u : u | 0x80000000u);
-      }
-    }
-    __syncthreads();                               // bits and list are set up
-#pragma unroll 1
-    for (int n = 0; n < kTopK - 1; ++n) {
-      uint32_t top = key[0];
-      int at = 0;
-#pragma unroll
-      for (int r = 1; r < kPer; ++r)
-        if (key[r] > top) top = key[r], at = r;
-      const uint32_t best = __reduce_max_sync(0xffffffffu, top);
-      const uint32_t id = static_cast<uint32_t>(kD4Threads * at + tid);
-      const uint32_t win = __reduce_min_sync(0xffffffffu, top == best ? id : 0xFFFFFFFFu);
-      if (lane == 0) sm.cand[warp * kCand + n] = make_uint2(best, win);
-      if (best == 0u) {                            // the warp has no more blocks
-        for (int k = n + 1 + lane; k < kTopK - 1; k += 32) sm.cand[warp * kCand + k] = make_uint2(0u, 0u);
-        break;
-      }
-#pragma unroll
-      for (int r = 0; r < kPer; ++r)
-        if (id == win && r == at) key[r] = 0u;
-    }
-    if (lane == 0) sm.cand[warp * kCand + kCand - 1] = make_uint2(0u, 0u);
-    __syncthreads();
-    if (tid < kAtWarps * kCand) {
-      const uint2 me = sm.cand[tid];
-      int before = 0;
-#pragma unroll 16
-      for (int j = 0; j < kAtWarps * kCand; ++j) {
-        const uint2 x = sm.cand[j];
-        before += (x.x > me.x || (x.x == me.x && x.y < me.y)) ? 1 : 0;
-      }
-      if (me.x != 0u && before < kTopK - 1) atomicOr(&sm.bits[me.y >> 5], 1u << (me.y & 31));
-    }
-    if (tid == kD4Threads - 1) atomicOr(&sm.bits[own >> 5], 1u << (own & 31));
-    __syncthreads();
-    if (warp == 0) {                               // set bits in ascending order
-      uint32_t m = sm.bits[lane];
-      int at = __popc(m);
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, at, d);
-        if (lane >= d) at += x;
-      }
-      at -= __popc(m);
-      while (m && at < kTopK) {
-        sm.list[at++] = 32 * lane + __ffs(m) - 1;
-        m &= m - 1u;
-      }
-    }
-  } else {
-    __syncthreads();
-    if (tid < nblk) sm.list[tid] = tid;            // every block
-  }
-  __syncthreads();
-  if (split == 0 && tid < kTopK && sel_out)
-    sel_out[static_cast<size_t>(bh) * kTopK + tid] = sm.list[tid];
-  // ---- this CTA's blocks: all K and V slabs on their way at once
-  if (tid < kBlocks) {
-    const int blk = sm.list[split + NS * tid];
-    int pg = -1;
-    if (blk >= 0) {
-      pg = table[static_cast<size_t>(b) * max_pages + blk];
-      if (pg < 0 || pg >= num_pages) {
-        atomicOr(status, kStatusBounds);
-        pg = -1;
-      }
-    }
-    sm.page[tid] = pg;
-    if (pg >= 0) {
-      const size_t off = (static_cast<size_t>(pg) * Hkv + h) * kSlab;
-      mbar_arrive_expect_tx(&sm.full[tid], 2 * kSlab);
-      bulk_load(sm.k[tid], kc + off, kSlab, &sm.full[tid]);
-      bulk_load(sm.v[tid], vc + off, kSlab, &sm.full[tid]);
+      const int i = kAtThreads * r + tid;
+      score[r] = i < max_pages ? sc[i] : 0.f;
     }
   }
-  // ---- q rows as fp16 with a power of two per row; warp w rows 4w .. 4w + 3
+  // q as the A operand of the 8 k-steps: rows g and g + 8 in fp16, each with a power
+  // of two; thread c of a row has channels 32 c .. 32 c + 31
+  uint32_t qa[8][4];
+  float f0, f1;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 4 * warp + i;
-    uint2 x = make_uint2(0u, 0u);
-    if (r < G)
-      x = *reinterpret_cast<const uint2*>(
-          q + (static_cast<size_t>(b) * G * Hkv + static_cast<size_t>(h) * G + r) * kD + 4 * lane);
-    uint32_t m = __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu);
+  for (int half = 0; half < 2; ++half) {
+    const int r = g + 8 * half;
+    uint4 x[4];
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < G)
+        x[i] = *(reinterpret_cast<const uint4*>(
+                     q + (static_cast<size_t>(b) * G * Hkv + static_cast<size_t>(h) * G + r) * kD +
+                     32 * c) + i);
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
+                               __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
+    }
     m = max(m & 0xFFFFu, m >> 16);
-    m = __reduce_max_sync(0xffffffffu, m);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const int e = row_shift(m);
     const float f = exp2i(e);
-    sm.qh[r * (kD / 2) + 2 * lane] = bf2_to_h2(x.x, f);
-    sm.qh[r * (kD / 2) + 2 * lane + 1] = bf2_to_h2(x.y, f);
-    if (lane == 0) sm.qfac[r] = exp2i(-e);
-  }
-  __syncthreads();
-  uint32_t qa[8][4];                               // A operand of the 8 k-steps
+    (half ? f1 : f0) = sl2 * exp2i(-e);
 #pragma unroll
-  for (int t = 0; t < 8; ++t) {
-    const uint2 r0 = *reinterpret_cast<const uint2*>(&sm.qh[g * (kD / 2) + 16 * c + 2 * t]);
-    const uint2 r1 = *reinterpret_cast<const uint2*>(&sm.qh[(g + 8) * (kD / 2) + 16 * c + 2 * t]);
-    qa[t][0] = r0.x;
-    qa[t][1] = r1.x;
-    qa[t][2] = r0.y;
-    qa[t][3] = r1.y;
+    for (int i = 0; i < 4; ++i) {
+      qa[2 * i][half] = bf2_to_h2(x[i].x, f);
+      qa[2 * i][2 + half] = bf2_to_h2(x[i].y, f);
+      qa[2 * i + 1][half] = bf2_to_h2(x[i].z, f);
+      qa[2 * i + 1][2 + half] = bf2_to_h2(x[i].w, f);
+    }
   }
-  const float f0 = sl2 * sm.qfac[g], f1 = sl2 * sm.qfac[g + 8];
+  const int L = d4_len(len, max_pages, status);
+  const int nblk = (L + kBlock - 1) / kBlock;
+  const int own = nblk - 1;
+  if (tid < kBlocks) {
+    mbar_init(&sm.full[tid], 1);
+    fence_mbar_init();
+  }
+  if (tid == 0) sm.ncand = 0;
+  if (own >= kTopK) {
+    // ---- the 15 best earlier blocks.  The threads form 32 groups of 4; the 15th of
+    // the groups' best keys bounds the 15th best key from below, so that few keys
+    // (about 20; at most 15 groups' keys) are left to be ranked among each other.
+    unsigned long long* cand = reinterpret_cast<unsigned long long*>(sm.o);   // [<= 15 * 4 * kPer]
+    unsigned long long key[kPer], top = 0ull;
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+      const int i = kAtThreads * r + tid;
+      key[r] = 0ull;
+      if (i < own)
+        key[r] = i < n_init ? (0xFFFFFFFFull << 32 | static_cast<uint32_t>(0x7FFFFFFF - i))
+                            : rank_key(score[r], i);
+      top = key[r] > top ? key[r] : top;
+    }
+#pragma unroll
+    for (int m = 8; m <= 16; m <<= 1) {            // lanes l, l + 8, l + 16, l + 24
+      const unsigned long long x = __shfl_xor_sync(0xffffffffu, top, m);
+      top = x > top ? x : top;
+    }
+    if (lane < 8) sm.gmax[8 * warp + lane] = top;
+    __syncthreads();
+    const unsigned long long mine = sm.gmax[lane];
+    int before = 0;
+#pragma unroll 8
+    for (int j = 0; j < 32; ++j) before += sm.gmax[j] > mine ? 1 : 0;
+    // fewer than 15 groups with keys: every key is a candidate
+    const uint32_t at15 = __ballot_sync(0xffffffffu, mine != 0ull && before == kTopK - 2);
+    const unsigned long long bar =
+        at15 ? __shfl_sync(0xffffffffu, mine, __ffs(at15) - 1) : 1ull;
+#pragma unroll
+    for (int r = 0; r < kPer; ++r)
+      if (key[r] >= bar) cand[atomicAdd(&sm.ncand, 1)] = key[r];
+    __syncthreads();
+    if (warp == 0) {
+      const int nc = sm.ncand;
+      for (int t = lane; t < nc; t += 32) {
+        const unsigned long long me = cand[t];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < nc; ++j) rank += cand[j] > me ? 1 : 0;
+        if (rank < kTopK - 1) sm.list[rank] = 0x7FFFFFFF - static_cast<int>(static_cast<uint32_t>(me));
+      }
+      if (lane == 31) sm.list[kTopK - 1] = own;
+    }
+  } else if (tid < kTopK) {
+    sm.list[tid] = tid < nblk ? tid : -1;          // every block
+  }
+  __syncwarp();
+  // ---- warp 0: this CTA's blocks, all K and V slabs on their way at once
+  if (warp == 0) {
+    if (lane < kBlocks) {
+      const int blk = sm.list[split + NS * lane];
+      int pg = -1;
+      if (blk >= 0) {
+        pg = table[static_cast<size_t>(b) * max_pages + blk];
+        if (pg < 0 || pg >= num_pages) {
+          atomicOr(status, kStatusBounds);
+          pg = -1;
+        }
+      }
+      sm.page[lane] = pg;
+      if (pg >= 0) {
+        const size_t off = (static_cast<size_t>(pg) * Hkv + h) * kSlab;
+        fence_proxy_async_smem();                  // the slabs lie over the candidates
+        mbar_arrive_expect_tx(&sm.full[lane], 2 * kSlab);
+        bulk_load(sm.s.k[lane], kc + off, kSlab, &sm.full[lane]);
+        bulk_load(sm.s.v[lane], vc + off, kSlab, &sm.full[lane]);
+      }
+    }
+    if (split == 0 && lane < kTopK && sel_out) {   // ascending, -1 last
+      const uint32_t me = static_cast<uint32_t>(sm.list[lane]);
+      int at = 0;
+#pragma unroll
+      for (int j = 0; j < kTopK; ++j) {
+        const uint32_t x = static_cast<uint32_t>(sm.list[j]);
+        at += x < me || (x == me && j < lane) ? 1 : 0;
+      }
+      sel_out[static_cast<size_t>(bh) * kTopK + at] = static_cast<int>(me);
+    }
+  }
+  __syncthreads();                                 // blocks and pages are known to every warp
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
   float acc[16][4];
 #pragma unroll
@@ -473,27 +497,35 @@ __global__ void __launch_bounds__(kD4Threads) decode4_attend_kernel(
 #pragma unroll 1
   for (int i = 0; i < kBlocks; ++i) {
     if (sm.page[i] < 0) continue;                  // uniform over the CTA
-    const int blk = sm.list[split + NS * i];
-    const int nvalid = blk == own ? L - own * kBlock : kBlock;
-    const int kw = 32 * warp;                      // this warp's first key
-    if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[i], 0, status, 80))) break;
+    const int nvalid = sm.list[split + NS * i] == own ? L - own * kBlock : kBlock;
+    const int kw = kKeysPerWarp * warp;            // this warp's first key
+    if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[i], 0, status, 80))) {
+      for (int j = i + 1; j < kBlocks; ++j)        // wait (bounded) for what is on its way, leave
+        if (sm.page[j] >= 0) (void)mbar_wait(&sm.full[j], 0, status, 83);
+      break;
+    }
     if (kw >= nvalid) continue;                    // uniform over the warp
-    // ---- S
+    // ---- S: four n-tiles side by side, so that four chains of products overlap
     float s[4][4];
+    uint4 w4[4];
+    __half2 ksc[4];
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
       const int key = kw + 8 * nt + (g >> 1) + 4 * (g & 1);
-      const uint4 w4 = *(reinterpret_cast<const uint4*>(sm.k[i] + slab_code(key)) + c);
-      const uint32_t sc = *(reinterpret_cast<const uint16_t*>(sm.k[i] + slab_scale(key)) + c);
-      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-      const __half2 sh = __half2(
-          __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(sc), __NV_E4M3));
+      w4[nt] = *(reinterpret_cast<const uint4*>(sm.s.k[i] + slab_code(key)) + c);
+      const uint32_t two = *(reinterpret_cast<const uint16_t*>(sm.s.k[i] + slab_scale(key)) + c);
+      ksc[nt] = __half2(
+          __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3));
+      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {                // 8 channels: two k-steps
+    for (int j = 0; j < 4; ++j) {                  // 8 channels: two k-steps
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        const uint32_t w = j == 0 ? w4[nt].x : (j == 1 ? w4[nt].y : (j == 2 ? w4[nt].z : w4[nt].w));
         __half2 hh[4];
-        codes_half2(w[j], hh);
-        const __half2 s2 = j < 2 ? __low2half2(sh) : __high2half2(sh);
+        codes_half2(w, hh);
+        const __half2 s2 = j < 2 ? __low2half2(ksc[nt]) : __high2half2(ksc[nt]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int t = 2 * j + k;
@@ -505,42 +537,52 @@ __global__ void __launch_bounds__(kD4Threads) decode4_attend_kernel(
     // ---- mask and running softmax of this warp's keys
     float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
+    for (int nt = 0; nt < 4; ++nt) {
+      if (nvalid < kBlock) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const bool ok = kw + 8 * nt + c + 4 * e < nvalid;
-        s[nt][e] = ok ? s[nt][e] * f0 : -INFINITY;
-        s[nt][2 + e] = ok ? s[nt][2 + e] * f1 : -INFINITY;
-        mx0 = fmaxf(mx0, s[nt][e]);
-        mx1 = fmaxf(mx1, s[nt][2 + e]);
+        for (int e = 0; e < 2; ++e) {
+          const bool ok = kw + 8 * nt + c + 4 * e < nvalid;
+          s[nt][e] = ok ? s[nt][e] : -INFINITY;
+          s[nt][2 + e] = ok ? s[nt][2 + e] : -INFINITY;
+        }
       }
+      mx0 = fmaxf(mx0, fmaxf(s[nt][0], s[nt][1]));
+      mx1 = fmaxf(mx1, fmaxf(s[nt][2], s[nt][3]));
+    }
 #pragma unroll
     for (int m = 1; m <= 2; m <<= 1) {
       mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, m));
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, m));
     }
-    const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-    const float a0 = mn0 == -INFINITY ? 1.f : exp2f(m0 - mn0);
-    const float a1 = mn1 == -INFINITY ? 1.f : exp2f(m1 - mn1);
-    const float e0 = mn0 == -INFINITY ? 0.f : mn0, e1 = mn1 == -INFINITY ? 0.f : mn1;
-    m0 = mn0;
-    m1 = mn1;
-    l0 *= a0;
-    l1 *= a1;
+    // the maximum moves only when it grows by more than 2^8: weights stay below
+    // 2^8, which fp16 holds as well as those below 1
+    mx0 *= f0;
+    mx1 *= f1;
+    const bool up0 = mx0 > m0 + kAtRescale || m0 == -INFINITY;
+    const bool up1 = mx1 > m1 + kAtRescale || m1 == -INFINITY;
+    if (__any_sync(0xffffffffu, up0 || up1)) {
+      const float n0 = up0 ? mx0 : m0, n1 = up1 ? mx1 : m1;
+      const float a0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), a1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
+      m0 = n0;
+      m1 = n1;
+      l0 *= a0;
+      l1 *= a1;
 #pragma unroll
-    for (int nt = 0; nt < 16; ++nt) {
-      acc[nt][0] *= a0;
-      acc[nt][1] *= a0;
-      acc[nt][2] *= a1;
-      acc[nt][3] *= a1;
+      for (int nt = 0; nt < 16; ++nt) {
+        acc[nt][0] *= a0;
+        acc[nt][1] *= a0;
+        acc[nt][2] *= a1;
+        acc[nt][3] *= a1;
+      }
     }
-    // P in fp16 (11 significant bits; the row's largest is 1): the row sum takes
-    // the rounded values, so rounding does not change the weights' total
+    const float e0 = m0 == -INFINITY ? 0.f : -m0, e1 = m1 == -INFINITY ? 0.f : -m1;
+    // P in fp16 (11 significant bits); the row sum takes the rounded values, so
+    // rounding does not change the weights' total
     uint32_t pa[2][4];
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-      const __half2 p0 = __floats2half2_rn(exp2f(s[nt][0] - e0), exp2f(s[nt][1] - e0));
-      const __half2 p1 = __floats2half2_rn(exp2f(s[nt][2] - e1), exp2f(s[nt][3] - e1));
+      const __half2 p0 = __floats2half2_rn(ex2(fmaf(s[nt][0], f0, e0)), ex2(fmaf(s[nt][1], f0, e0)));
+      const __half2 p1 = __floats2half2_rn(ex2(fmaf(s[nt][2], f1, e1)), ex2(fmaf(s[nt][3], f1, e1)));
       const float2 r0 = __half22float2(p0), r1 = __half22float2(p1);
       l0 += r0.x + r0.y;
       l1 += r1.x + r1.y;
@@ -550,33 +592,42 @@ __global__ void __launch_bounds__(kD4Threads) decode4_attend_kernel(
     // ---- O += P V
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      __half2 vv[4][8];                            // keys c, c + 4, c + 8, c + 12: channels 16 g ..
+      // keys c + 4 r, r = 0 .. 3, channels 16 g ..; each conversion takes a byte with
+      // one channel's codes of two keys, the pair that the B operand wants
+      uint2 w[4];
+      uint32_t sb[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int key = kw + 16 * kk + c + 4 * r;
-        const uint2 w = *reinterpret_cast<const uint2*>(sm.v[i] + slab_code(key) + 8 * g);
-        const uint32_t sb = key < nvalid ? sm.v[i][slab_scale(key) + g] : 0u;
-        const __half2 s2 = __half2half2(__half(__nv_cvt_fp8_to_halfraw(
-            static_cast<__nv_fp8_storage_t>(sb), __NV_E4M3)));
-        __half2 t4[4];
-        codes_half2(w.x, t4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) vv[r][j] = __hmul2(t4[j], s2);
-        codes_half2(w.y, t4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) vv[r][4 + j] = __hmul2(t4[j], s2);
+        w[r] = *reinterpret_cast<const uint2*>(sm.s.v[i] + slab_code(key) + 8 * g);
+        sb[r] = key < nvalid ? sm.s.v[i][slab_scale(key) + g] : 0u;
       }
+      __half2 s2[2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {                // channels 16 g + 2j and + 2j + 1
-        const uint32_t lo0 = __byte_perm(h2u(vv[0][j]), h2u(vv[1][j]), 0x5410);
-        const uint32_t lo1 = __byte_perm(h2u(vv[2][j]), h2u(vv[3][j]), 0x5410);
-        const uint32_t hi0 = __byte_perm(h2u(vv[0][j]), h2u(vv[1][j]), 0x7632);
-        const uint32_t hi1 = __byte_perm(h2u(vv[2][j]), h2u(vv[3][j]), 0x7632);
-        mma_f16_16816(acc[2 * j], pa[kk][0], pa[kk][1], pa[kk][2], pa[kk][3], lo0, lo1);
-        mma_f16_16816(acc[2 * j + 1], pa[kk][0], pa[kk][1], pa[kk][2], pa[kk][3], hi0, hi1);
+      for (int r = 0; r < 2; ++r)
+        s2[r] = __half2(__nv_cvt_fp8x2_to_halfraw2(
+            static_cast<__nv_fp8x2_storage_t>(sb[2 * r] | sb[2 * r + 1] << 8), __NV_E4M3));
+#pragma unroll
+      for (int q8 = 0; q8 < 2; ++q8) {             // 8 channels
+        __half2 ev[2][4], od[2][4];                // even and odd channels, keys r = 0, 1 and 2, 3
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t x = q8 ? w[2 * r].y : w[2 * r].x, y = q8 ? w[2 * r + 1].y : w[2 * r + 1].x;
+          codes_half2((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[r]);
+          codes_half2(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[r]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {              // channels 16 g + 8 q8 + 2 j and + 1
+          const int nt = 8 * q8 + 2 * j;
+          mma_f16_16816(acc[nt], pa[kk][0], pa[kk][1], pa[kk][2], pa[kk][3],
+                        h2u(__hmul2(ev[0][j], s2[0])), h2u(__hmul2(ev[1][j], s2[1])));
+          mma_f16_16816(acc[nt + 1], pa[kk][0], pa[kk][1], pa[kk][2], pa[kk][3],
+                        h2u(__hmul2(od[0][j], s2[0])), h2u(__hmul2(od[1][j], s2[1])));
+        }
       }
     }
   }
+  __syncthreads();                                 // the slabs make room for the warps' sums
   l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
   l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
   l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
@@ -585,12 +636,11 @@ __global__ void __launch_bounds__(kD4Threads) decode4_attend_kernel(
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     // columns 2c, 2c + 1 of n-tile i: channels 32 c + i and 32 c + 16 + i
-    float* r0 = &sm.o[warp][g][32 * c + 4 * j];
-    float* r1 = &sm.o[warp][g + 8][32 * c + 4 * j];
-    *reinterpret_cast<float4*>(r0) = make_float4(acc[4 * j][0], acc[4 * j + 1][0], acc[4 * j + 2][0], acc[4 * j + 3][0]);
-    *reinterpret_cast<float4*>(r0 + 16) = make_float4(acc[4 * j][1], acc[4 * j + 1][1], acc[4 * j + 2][1], acc[4 * j + 3][1]);
-    *reinterpret_cast<float4*>(r1) = make_float4(acc[4 * j][2], acc[4 * j + 1][2], acc[4 * j + 2][2], acc[4 * j + 3][2]);
-    *reinterpret_cast<float4*>(r1 + 16) = make_float4(acc[4 * j][3], acc[4 * j + 1][3], acc[4 * j + 2][3], acc[4 * j + 3][3]);
+    float* ow = &sm.o[warp][0][0];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<float4*>(ow + o_at(g + 8 * (e >> 1), 8 * c + 4 * (e & 1) + j)) =
+          make_float4(acc[4 * j][e], acc[4 * j + 1][e], acc[4 * j + 2][e], acc[4 * j + 3][e]);
   }
   if (c == 0) {
     sm.ml[warp][g][0] = m0;
@@ -600,27 +650,28 @@ __global__ void __launch_bounds__(kD4Threads) decode4_attend_kernel(
   }
   __syncthreads();
   {
-    const int r = tid >> 3, d0 = (tid & 7) * 16;   // 16 rows x 8 threads
+    const int r = tid >> 3;                        // 16 rows x 8 threads, float4s tid % 8 + 8 j
     float mm = -INFINITY, f[kAtWarps], l = 0.f;
 #pragma unroll
     for (int w = 0; w < kAtWarps; ++w) mm = fmaxf(mm, sm.ml[w][r][0]);
 #pragma unroll
     for (int w = 0; w < kAtWarps; ++w) {
-      f[w] = sm.ml[w][r][0] == -INFINITY ? 0.f : exp2f(sm.ml[w][r][0] - mm);
+      f[w] = sm.ml[w][r][0] == -INFINITY ? 0.f : ex2(sm.ml[w][r][0] - mm);
       l += f[w] * sm.ml[w][r][1];
     }
 #pragma unroll
-    for (int d = 0; d < 16; d += 4) {
+    for (int j = 0; j < 4; ++j) {
+      const int at = o_at(r, (tid & 7) + 8 * j);
       float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kAtWarps; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][r][d0 + d]);
+        const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][0][0] + at);
         t.x = fmaf(f[w], x.x, t.x);
         t.y = fmaf(f[w], x.y, t.y);
         t.z = fmaf(f[w], x.z, t.z);
         t.w = fmaf(f[w], x.w, t.w);
       }
-      *reinterpret_cast<float4*>(&sm.o[0][r][d0 + d]) = t;
+      *reinterpret_cast<float4*>(&sm.o[0][0][0] + at) = t;
     }
     if ((tid & 7) == 0) {
       sm.cta_ml[r][0] = mm;
@@ -629,29 +680,29 @@ __global__ void __launch_bounds__(kD4Threads) decode4_attend_kernel(
   }
   cluster_sync();
   {
-    // CTA `split` finishes rows split * 16 / NS ..: 8 threads per row and 16
-    // channels each (2 rows or more), 64 threads per row otherwise unused
+    // CTA `split` finishes rows split * 16 / NS .., a warp each
     constexpr int kRows = 16 / NS;
-    const int r = split * kRows + (tid >> 5), d0 = (tid & 31) * 4;
-    if ((tid >> 5) < kRows && r < G) {
-      const uint32_t mla = smem_u32(&sm.cta_ml[r][0]), oa = smem_u32(&sm.o[0][r][d0]);
+    const int r = split * kRows + warp, d0 = lane * 4;
+    if (warp < kRows && r < G) {
+      const uint32_t mla = smem_u32(&sm.cta_ml[r][0]), oa = smem_u32(&sm.o[0][0][0] + o_at(r, lane));
       float2 ml[NS];
+      float4 x[NS];
       float mm = -INFINITY, l = 0.f;
 #pragma unroll
       for (int p = 0; p < NS; ++p) {
         ml[p] = ld_cluster2(cluster_map(mla, p));
+        x[p] = ld_cluster4(cluster_map(oa, p));
         mm = fmaxf(mm, ml[p].x);
       }
       float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int p = 0; p < NS; ++p) {
-        const float f = ml[p].x == -INFINITY ? 0.f : exp2f(ml[p].x - mm);
-        const float4 x = ld_cluster4(cluster_map(oa, p));
+        const float f = ml[p].x == -INFINITY ? 0.f : ex2(ml[p].x - mm);
         l = fmaf(f, ml[p].y, l);
-        t.x = fmaf(f, x.x, t.x);
-        t.y = fmaf(f, x.y, t.y);
-        t.z = fmaf(f, x.z, t.z);
-        t.w = fmaf(f, x.w, t.w);
+        t.x = fmaf(f, x[p].x, t.x);
+        t.y = fmaf(f, x[p].y, t.y);
+        t.z = fmaf(f, x[p].z, t.z);
+        t.w = fmaf(f, x[p].w, t.w);
       }
       const float inv = l > 0.f ? v_gain / l : 0.f;
       uint2 out;
@@ -681,14 +732,14 @@ Decode4Workspace carve_decode4_workspace(WsCursor& ws, int B, int Hkv, int max_p
 template <int NS>
 msa_status_t launch_attend4(const void* q, const void* kc, const void* vc, const int32_t* table,
                             const int32_t* lens, const float* scores, int B, int G, int Hkv,
-                            int num_pages, int max_pages, int n_init, float sl2, float v_gain,
-                            void* o, int32_t* sel_out, uint32_t* sw, cudaStream_t stream) {
+                            int num_pages, int max_pages, int n_init, float sl2, float v_gain, void* o,
+                            int32_t* sel_out, uint32_t* sw, cudaStream_t stream) {
   const size_t smem = sizeof(Attend4Smem<NS>);
   MSA_TRY(ensure_smem(decode4_attend_kernel<NS>, smem, "decode4_attend_kernel"));
   TraceScope trace_("decode4_attend_kernel", stream);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(NS, static_cast<unsigned>(B) * Hkv);
-  cfg.blockDim = kD4Threads;
+  cfg.blockDim = kAtThreads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -763,15 +814,17 @@ msa_status_t msa_decode4_step(const void* q, const void* q_idx, const void* k_ca
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (max_pages > kTopK) {
     MSA_TRY(ensure_smem(decode4_score_kernel, sizeof(Score4Smem), "decode4_score_kernel"));
-    TraceScope trace_("decode4_score_kernel", st);
-    launch_pdl(decode4_score_kernel, device_sm_count(), 32 * kScWarps, sizeof(Score4Smem), st,
-               static_cast<const __nv_bfloat16*>(q_idx), static_cast<const uint8_t*>(kidx_cache),
-               block_table, cache_lens, B, Hkv, num_pages, max_pages, n_init, w.scores, sw);
+    {
+      TraceScope trace_("decode4_score_kernel", st);
+      launch_pdl(decode4_score_kernel, device_sm_count(), kScThreads, sizeof(Score4Smem), st,
+                 static_cast<const __nv_bfloat16*>(q_idx), static_cast<const uint8_t*>(kidx_cache),
+                 block_table, cache_lens, B, Hkv, num_pages, max_pages, n_init, w.scores, sw);
+    }
     MSA_TRY(check_launch("decode4_score_kernel"));
   }
   return launch_attend4<4>(q, k_cache, v_cache, block_table, cache_lens, w.scores, B, G, Hkv,
-                           num_pages, max_pages, n_init, scale * k_gain * kLog2e, v_gain, o,
-                           sel_out, sw, st);
+                           num_pages, max_pages, n_init, scale * k_gain * kLog2e, v_gain, o, sel_out,
+                           sw, st);
 }
 
 }  // extern "C"
