@@ -24,6 +24,7 @@
 // elsewhere: the product's 8 columns are the 8 scale blocks' partial sums, so the
 // scales are applied to fp32 sums, 2 per thread and key, and nothing is rounded
 // before that.
+#include <atomic>
 #include <cmath>
 #include "cache4.cuh"
 
@@ -729,6 +730,19 @@ Decode4Workspace carve_decode4_workspace(WsCursor& ws, int B, int Hkv, int max_p
   return w;
 }
 
+// Clusters of 16 are beyond the portable size: allowed once per device.
+msa_status_t allow_large_cluster(const void* kernel) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return fail(MSA_ERR_CUDA, "cudaGetDevice failed");
+  if (dev < 0 || dev >= 64 || !done[dev].load()) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return fail(MSA_ERR_CUDA, "decode4_attend_kernel: %s", cudaGetErrorString(e));
+    if (dev >= 0 && dev < 64) done[dev].store(true);
+  }
+  return MSA_OK;
+}
+
 template <int NS>
 msa_status_t launch_attend4(const void* q, const void* kc, const void* vc, const int32_t* table,
                             const int32_t* lens, const float* scores, int B, int G, int Hkv,
@@ -742,6 +756,7 @@ msa_status_t launch_attend4(const void* q, const void* kc, const void* vc, const
   cfg.blockDim = kAtThreads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
+  if (NS > 8) MSA_TRY(allow_large_cluster(reinterpret_cast<const void*>(decode4_attend_kernel<NS>)));
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -822,9 +837,16 @@ msa_status_t msa_decode4_step(const void* q, const void* q_idx, const void* k_ca
     }
     MSA_TRY(check_launch("decode4_score_kernel"));
   }
-  return launch_attend4<4>(q, k_cache, v_cache, block_table, cache_lens, w.scores, B, G, Hkv,
-                           num_pages, max_pages, n_init, scale * k_gain * kLog2e, v_gain, o, sel_out,
-                           sw, st);
+  // CTAs per row: as many as still run side by side, 3 per SM (the kernel's
+  // shared memory and registers); more CTAs shorten a row's chain of blocks, fewer repeat
+  // its selection less often.  Attention of 4 rows: 7.0 us with 4, 5.0 with 16; of
+  // 20 rows with up to 1024 blocks: 16.1 with 4, 14.3 with 16; of 66 rows 16.3 with 4, 20.4
+  // with 8; of 256 rows 43 with 4, 70 with 8.
+  const long long rows = static_cast<long long>(B) * Hkv, room = 3LL * device_sm_count();
+  auto attend = rows * 16 <= room ? launch_attend4<16>
+                                  : (rows * 8 <= room ? launch_attend4<8> : launch_attend4<4>);
+  return attend(q, k_cache, v_cache, block_table, cache_lens, w.scores, B, G, Hkv, num_pages,
+                max_pages, n_init, scale * k_gain * kLog2e, v_gain, o, sel_out, sw, st);
 }
 
 }  // extern "C"
