@@ -788,17 +788,23 @@ def _tables(block_table, cache_lens, ref_count):
                  _arg(ref_count, "ref_count", _I32, (P,), dev)), (B, P, maxp)
 
 
+_PTRS = [_vp * max(n, 1) for n in range(9)]             # made once: an array type costs
+_SIZES = [ctypes.c_int64 * max(n, 1) for n in range(9)]  # more than a call
+
+
 def _page_args(caches, P, dev):
     """Host arrays of the caches' addresses and bytes per page."""
     n = len(caches)
-    ptrs, sizes = (_vp * max(n, 1))(), (ctypes.c_int64 * max(n, 1))()
+    if n > 8:
+        raise ValueError(f"at most 8 caches, got {n}")
+    ptrs, sizes = _PTRS[n](), _SIZES[n]()
     for i, c in enumerate(caches):
         if not isinstance(c, torch.Tensor) or c.get_device() != dev or not c.is_contiguous():
             raise ValueError(f"cache {i} must be a contiguous tensor on cuda:{dev}")
         if c.dim() < 1 or c.shape[0] != P:
             raise ValueError(f"cache {i} must have {P} pages in its first dimension")
         ptrs[i] = c.data_ptr()
-        sizes[i] = c.numel() // max(P, 1) * c.element_size()
+        sizes[i] = c.nbytes // max(P, 1)
     return ptrs, sizes, n
 
 

@@ -2,11 +2,12 @@
 // token of a decode step (append).  Moves of 256 bytes of bf16 against 72 bytes
 // of pages per (token, head): bound by memory for a pack, by latency for a step.
 //
-// Store and load: one thread per 16 channels (32 bytes of bf16, 8 bytes of
-// codes, one scale byte), so that a scale needs no exchange between threads.
-// The 8 threads of a row sit side by side and a warp takes 4 consecutive tokens
-// of one head: its codes are 256 consecutive bytes of the slab and its scales
-// one 32-byte sector.
+// Store and load: one thread per 16 channels (32 bytes of bf16, 8 bytes of codes,
+// one scale byte), so that a scale needs no exchange between threads.  The 8 threads of
+// a row sit side by side and a warp takes 4 consecutive tokens of one head: its
+// codes are 256 consecutive bytes of the slab and its scales one 32-byte sector.  A CTA
+// finds the places of its 32 tokens once and then takes them through its share of
+// the (tensor, head) pairs, the next pair's loads in flight.
 #include <cmath>
 #include "cache4.cuh"
 
@@ -22,15 +23,15 @@ struct Cache4Args {
   __nv_bfloat16* y[3];           // load: outputs
   uint8_t* cache[3];             // [num_pages, H, 9216]
   const uint8_t* rcache[3];
-  float gain[3];                 // store: 1 / gain
+  float gain[3], inv_gain[3];
   const int32_t* table;
   const int32_t* cu;
   const int32_t* start;
   int n, S, T, H, num_pages, max_pages;
 };
 
-// Slab of token t's position (page * H + h still to come): page and slot, or
-// page -1 (out of range) / -2 (not a token of the pack).
+// Page and slot of token t's position; page -1: out of range, -2: not a token of
+// the pack.
 __device__ __forceinline__ int2 c4_place(const Cache4Args& a, int t, uint32_t* status) {
   if (t >= a.T || t < __ldg(a.cu) || t >= __ldg(a.cu + a.S)) return make_int2(-2, 0);
   int lo = 0, hi = a.S;                            // largest s with cu[s] <= t
@@ -50,26 +51,42 @@ __device__ __forceinline__ int2 c4_place(const Cache4Args& a, int t, uint32_t* s
   return make_int2(page, static_cast<int>(pos % kBlock));
 }
 
+struct C4Words {
+  uint4 a, b;
+};
+
 }  // namespace
 
-// grid (token groups, H, tensors)
+// grid (token groups, shares of the n * H pairs)
 __global__ void __launch_bounds__(kC4Threads) cache4_store_kernel(const Cache4Args a,
                                                                   uint32_t* status) {
   pdl_enter();
   const int c = threadIdx.x & 7;                   // 16 channels
   const int t = blockIdx.x * kC4Tokens + (threadIdx.x >> 3);
-  const int h = blockIdx.y, n = blockIdx.z;
   const int2 at = c4_place(a, t, status);
   if (at.x < 0) return;
-  const uint4* src = reinterpret_cast<const uint4*>(
-      a.x[n] + (static_cast<size_t>(t) * a.H + h) * kD + 16 * c);
-  const uint4 u0 = __ldcs(src), u1 = __ldcs(src + 1);
-  const uint32_t x[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-  uint32_t sb;
-  const uint2 codes = quantise16(x, a.gain[n], &sb);
-  uint8_t* slab = a.cache[n] + (static_cast<size_t>(at.x) * a.H + h) * kSlab;
-  *reinterpret_cast<uint2*>(slab + slab_code(at.y) + 8 * c) = codes;
-  slab[slab_scale(at.y) + c] = static_cast<uint8_t>(sb);
+  const int jobs = a.n * a.H;
+  auto fetch = [&](int j) {
+    const int n = j / a.H, h = j - n * a.H;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        a.x[n] + (static_cast<size_t>(t) * a.H + h) * kD + 16 * c);
+    return C4Words{__ldcs(src), __ldcs(src + 1)};
+  };
+  int j = blockIdx.y;
+  if (j >= jobs) return;
+  C4Words u = fetch(j);
+  while (j < jobs) {
+    const int next = j + gridDim.y;
+    const uint32_t x[8] = {u.a.x, u.a.y, u.a.z, u.a.w, u.b.x, u.b.y, u.b.z, u.b.w};
+    if (next < jobs) u = fetch(next);
+    const int n = j / a.H, h = j - n * a.H;
+    uint32_t sb;
+    const uint2 codes = quantise16(x, a.gain[n], a.inv_gain[n], &sb);
+    uint8_t* slab = a.cache[n] + (static_cast<size_t>(at.x) * a.H + h) * kSlab;
+    *reinterpret_cast<uint2*>(slab + slab_code(at.y) + 8 * c) = codes;
+    slab[slab_scale(at.y) + c] = static_cast<uint8_t>(sb);
+    j = next;
+  }
 }
 
 __global__ void __launch_bounds__(kC4Threads) cache4_load_kernel(const Cache4Args a,
@@ -77,30 +94,53 @@ __global__ void __launch_bounds__(kC4Threads) cache4_load_kernel(const Cache4Arg
   pdl_enter();
   const int c = threadIdx.x & 7;
   const int t = blockIdx.x * kC4Tokens + (threadIdx.x >> 3);
-  const int h = blockIdx.y, n = blockIdx.z;
   const int2 at = c4_place(a, t, status);
   if (at.x == -2) return;
-  uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-  if (at.x >= 0) {
+  const int jobs = a.n * a.H;
+  uint2 w = make_uint2(0u, 0u);
+  uint32_t sb = 0u;
+  auto fetch = [&](int j) {
+    if (at.x < 0) return;
+    const int n = j / a.H, h = j - n * a.H;
     const uint8_t* slab = a.rcache[n] + (static_cast<size_t>(at.x) * a.H + h) * kSlab;
-    const uint2 w = __ldcs(reinterpret_cast<const uint2*>(slab + slab_code(at.y) + 8 * c));
-    const __half2 s2 = __half2half2(__float2half(scale_value(__ldcs(slab + slab_scale(at.y) + c))));
-    __half2 h4[4];
+    w = __ldcs(reinterpret_cast<const uint2*>(slab + slab_code(at.y) + 8 * c));
+    sb = __ldcs(slab + slab_scale(at.y) + c);
+  };
+  int j = blockIdx.y;
+  if (j >= jobs) return;
+  fetch(j);
+  while (j < jobs) {
+    const int next = j + gridDim.y;
+    const int n = j / a.H, h = j - n * a.H;
+    const uint2 cw = w;
+    const float s = scale_value(sb) * a.gain[n];
+    if (next < jobs) fetch(next);
+    // code * scale * gain has at most 6 significant bits: exact in fp32 and in bf16
+    const float2 s2 = make_float2(s, s);
+    uint32_t o[8];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      codes_half2(half ? w.y : w.x, h4);
+      __half2 h4[4];
+      codes_half2(half ? cw.y : cw.x, h4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        // code * scale has at most 6 significant bits and lies in [2^-10, 2688]:
-        // exact in fp16; the gain is a power of two: exact in bf16
-        const float2 f = __half22float2(__hmul2(h4[i], s2));
-        o[4 * half + i] = pack_bf16x2(f.x * a.gain[n], f.y * a.gain[n]);
+        const float2 f = __fmul2_rn(__half22float2(h4[i]), s2);
+        o[4 * half + i] = pack_bf16x2(f.x, f.y);
       }
     }
+    uint4* dst = reinterpret_cast<uint4*>(a.y[n] + (static_cast<size_t>(t) * a.H + h) * kD + 16 * c);
+    __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
+    __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
+    j = next;
   }
-  uint4* dst = reinterpret_cast<uint4*>(a.y[n] + (static_cast<size_t>(t) * a.H + h) * kD + 16 * c);
-  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// CTAs: one per token group while that fills the GPU twice over; the (tensor,
+// head) pairs are split among several per group when there are few groups.
+static dim3 c4_grid(int T, int jobs) {
+  const int groups = (T + kC4Tokens - 1) / kC4Tokens;
+  const int want = (8 * device_sm_count() + groups - 1) / groups;
+  return dim3(groups, want < jobs ? want : jobs);
 }
 
 // ---------------------------------------------------------------- append
@@ -118,11 +158,11 @@ struct Append4Args {
   const __nv_bfloat16* w[4];
   __nv_bfloat16* out[2];          // q_out, q_idx_out
   uint8_t* cache[3];              // k, index k, v
-  float inv_gain[3];
+  float gain[3], inv_gain[3];
   const int32_t* table;
   const int32_t* lens;
   int Hq, H, num_pages, max_pages, R, layout;
-  float eps, gain;
+  float eps, rope_gain;
 };
 
 struct Append4Turns {
@@ -168,8 +208,8 @@ __global__ void __launch_bounds__(32 * kApWarps) decode4_append_kernel(const App
         static_cast<long long>(static_cast<unsigned long long>(p) * turns.f[threadIdx.x]);
     float s, c;
     sincospif(static_cast<float>(ang) * 1.0842021724855044e-19f, &s, &c);   // * 2^-63
-    cs[threadIdx.x] = c * a.gain;
-    sn[threadIdx.x] = s * a.gain;
+    cs[threadIdx.x] = c * a.rope_gain;
+    sn[threadIdx.x] = s * a.rope_gain;
   }
   __syncthreads();
   if (r >= rows) return;                            // whole warps
@@ -214,20 +254,13 @@ __global__ void __launch_bounds__(32 * kApWarps) decode4_append_kernel(const App
   m = max(m & 0xFFFFu, m >> 16);
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  uint32_t sb = 0x7Fu, code = 0u;
-  if (m < 0x7F80u) {
-    const float ig = a.inv_gain[n];
-    sb = scale_byte(__uint_as_float(m << 16) * ig);
-    if (sb != 0u) {
-      const float s = scale_value(sb), rs = __frcp_rn(s);
-      const float2 f0 = word_f2(o[0]), f1 = word_f2(o[1]);
-      code = code_pair(f0.x * ig, f0.y * ig, s, rs) | code_pair(f1.x * ig, f1.y * ig, s, rs) << 8;
-    }
-  }
+  const Scale16 sc = scale16(m, a.gain[n], a.inv_gain[n]);
+  uint32_t code = 0u;
+  if (sc.s != 0.f) code = code_word(sc, o[0]) | code_word(sc, o[1]) << 8;
   uint8_t* slab = a.cache[n] + (static_cast<size_t>(page) * a.H + h) * kSlab;
   const int slot = p % kBlock;
   *reinterpret_cast<uint16_t*>(slab + slab_code(slot) + 2 * lane) = static_cast<uint16_t>(code);
-  if ((lane & 3) == 0) slab[slab_scale(slot) + (lane >> 2)] = static_cast<uint8_t>(sb);
+  if ((lane & 3) == 0) slab[slab_scale(slot) + (lane >> 2)] = static_cast<uint8_t>(sc.byte);
 }
 
 // ====================================================================== C ABI
@@ -310,15 +343,15 @@ msa_status_t msa_cache4_store(const void* k, const void* v, const void* k_idx, v
   for (int i = 0; i < a.n; ++i) {
     a.x[i] = static_cast<const __nv_bfloat16*>(x[which[i]]);
     a.cache[i] = static_cast<uint8_t*>(const_cast<void*>(c[which[i]]));
-    a.gain[i] = 1.0f / g[which[i]];
+    a.gain[i] = g[which[i]];
+    a.inv_gain[i] = 1.0f / g[which[i]];
   }
   uint32_t* sw = nullptr;
   MSA_TRY(status_word(&sw));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   {
     TraceScope trace_("cache4_store_kernel", st);
-    dim3 grid((T + kC4Tokens - 1) / kC4Tokens, Hkv, a.n);
-    launch_pdl(cache4_store_kernel, grid, kC4Threads, 0, st, a, sw);
+    launch_pdl(cache4_store_kernel, c4_grid(T, a.n * Hkv), kC4Threads, 0, st, a, sw);
   }
   return check_launch("cache4_store_kernel");
 }
@@ -345,8 +378,7 @@ msa_status_t msa_cache4_load(const void* k_cache, const void* v_cache, const voi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   {
     TraceScope trace_("cache4_load_kernel", st);
-    dim3 grid((T + kC4Tokens - 1) / kC4Tokens, Hkv, a.n);
-    launch_pdl(cache4_load_kernel, grid, kC4Threads, 0, st, a, sw);
+    launch_pdl(cache4_load_kernel, c4_grid(T, a.n * Hkv), kC4Threads, 0, st, a, sw);
   }
   return check_launch("cache4_load_kernel");
 }
@@ -394,9 +426,11 @@ msa_status_t msa_decode4_append(const void* q, const void* q_idx, const void* k,
   a.cache[0] = static_cast<uint8_t*>(k_cache);
   a.cache[1] = static_cast<uint8_t*>(kidx_cache);
   a.cache[2] = static_cast<uint8_t*>(v_cache);
-  a.inv_gain[0] = 1.0f / k_gain;
-  a.inv_gain[1] = 1.0f / kidx_gain;
-  a.inv_gain[2] = 1.0f / v_gain;
+  const float gains[3] = {k_gain, kidx_gain, v_gain};
+  for (int i = 0; i < 3; ++i) {
+    a.gain[i] = gains[i];
+    a.inv_gain[i] = 1.0f / gains[i];
+  }
   a.table = block_table;
   a.lens = cache_lens;
   a.Hq = Hq;
@@ -406,7 +440,7 @@ msa_status_t msa_decode4_append(const void* q, const void* q_idx, const void* k,
   a.R = rope->dim;
   a.layout = rope->layout;
   a.eps = eps;
-  a.gain = rope->gain;
+  a.rope_gain = rope->gain;
   Append4Turns turns;
   for (int i = 0; i < kD / 2; ++i) turns.f[i] = i < rope->dim / 2 ? rope_turn(rope->freqs[i]) : 0;
   uint32_t* sw = nullptr;

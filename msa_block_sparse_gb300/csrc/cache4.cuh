@@ -29,46 +29,71 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3)));
 }
 
-// e2m1 codes of two values divided by a scale s > 0 (rs = 1 / s rounded); low
-// nibble = a.  The quotient is formed as x rs and corrected once by its exact
-// residual: a quotient on the border of two codes has few bits, so the
-// corrected value hits it exactly and the tie goes to the even code, as in the
-// definition.  Magnitudes are bounded first so that no step overflows.
-__device__ __forceinline__ uint32_t code_pair(float a, float b, float s, float rs) {
-  a = fminf(fmaxf(a, -1e30f), 1e30f);
-  b = fminf(fmaxf(b, -1e30f), 1e30f);
-  float qa = a * rs, qb = b * rs;
-  qa = copysignf(fmaf(fmaf(-qa, s, a), rs, qa), a);   // -0 keeps its sign
-  qb = copysignf(fmaf(fmaf(-qb, s, b), rs, qb), b);
-  return __nv_cvt_float2_to_fp4x2(make_float2(qa, qb), __NV_E2M1, cudaRoundNearest);
-}
-
 __device__ __forceinline__ float2 word_f2(uint32_t u) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
 }
 
+// e2m1 codes of the pair x divided by a scale s > 0 (ns = -s; nr = -1 / s, rounded);
+// low nibble = x.x.  The quotient is formed as x / s rounded twice at most and corrected
+// once by its exact residual q s - x: a quotient on the border of two codes has few
+// bits, so the corrected value hits it exactly and the tie goes to the even code, as
+// in the definition.  -0 stays -0.
+__device__ __forceinline__ uint32_t code_pair(float2 x, float s, float rs) {
+  const float2 q = __fmul2_rn(x, make_float2(rs, rs));
+  const float2 e = __ffma2_rn(q, make_float2(s, s), make_float2(-x.x, -x.y));
+  return __nv_cvt_float2_to_fp4x2(__ffma2_rn(e, make_float2(-rs, -rs), q), __NV_E2M1,
+                                  cudaRoundNearest);
+}
+
+// Scale of 16 channels from their largest magnitude m (bf16 bits): the byte, and
+// in *s what the values are divided by (scale times gain; 0: all codes are 0).
+// Values that could overflow the quotient's residual (only past 2^100 times the
+// largest held value) are to be cut to +-*cut first.
+struct Scale16 {
+  uint32_t byte;
+  float s, rs, cut;      // cut: 0 = no need
+};
+
+__device__ __forceinline__ Scale16 scale16(uint32_t m, float gain, float inv_gain) {
+  Scale16 r;
+  r.cut = 0.f;
+  if (m >= 0x7F80u) {                              // an infinity or NaN
+    r.byte = 0x7Fu;
+    r.s = r.rs = 0.f;
+    return r;
+  }
+  const float amax = __uint_as_float(m << 16);
+  r.byte = scale_byte(amax * inv_gain);
+  r.s = scale_value(r.byte) * gain;
+  r.rs = r.byte ? __frcp_rn(r.s) : 0.f;
+  if (amax * 0x1p-30f > r.s && r.byte) r.cut = 8.f * r.s;   // saturated: any cut above 6 scales
+  return r;
+}
+
+__device__ __forceinline__ uint32_t code_word(const Scale16& sc, uint32_t x) {
+  float2 f = word_f2(x);
+  if (sc.cut != 0.f) {
+    f.x = fminf(fmaxf(f.x, -sc.cut), sc.cut);
+    f.y = fminf(fmaxf(f.y, -sc.cut), sc.cut);
+  }
+  return code_pair(f, sc.s, sc.rs);
+}
+
 // Codes (8 bytes) and scale byte of 16 bf16 channels (8 packed words).
-__device__ __forceinline__ uint2 quantise16(const uint32_t (&x)[8], float inv_gain,
+__device__ __forceinline__ uint2 quantise16(const uint32_t (&x)[8], float gain, float inv_gain,
                                             uint32_t* scale) {
   uint32_t m = 0;                                  // largest magnitude as bf16 bits
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = __vmaxu2(m, x[i] & 0x7FFF7FFFu);
   m = max(m & 0xFFFFu, m >> 16);
-  if (m >= 0x7F80u) {                              // an infinity or NaN
-    *scale = 0x7Fu;
-    return make_uint2(0u, 0u);
-  }
-  const uint32_t sb = scale_byte(__uint_as_float(m << 16) * inv_gain);
-  *scale = sb;
-  if (sb == 0u) return make_uint2(0u, 0u);
-  const float s = scale_value(sb), rs = __frcp_rn(s);
-  uint32_t w[2] = {0u, 0u};
+  const Scale16 sc = scale16(m, gain, inv_gain);
+  *scale = sc.byte;
+  if (sc.s == 0.f) return make_uint2(0u, 0u);
+  uint32_t c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = word_f2(x[i]);
-    w[i >> 2] |= code_pair(f.x * inv_gain, f.y * inv_gain, s, rs) << (8 * (i & 3));
-  }
-  return make_uint2(w[0], w[1]);
+  for (int i = 0; i < 8; ++i) c[i] = code_word(sc, x[i]);
+  return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
 }
 
 // 8 codes (one word, channel order) as four packed fp16 pairs, exact.  The

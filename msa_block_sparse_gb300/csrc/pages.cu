@@ -60,15 +60,43 @@ __device__ __forceinline__ bool row_ok(int len, int max_pages) {
 
 // ---------------------------------------------------------------- fork, free
 //
-// Two launches each.  The first (one CTA) settles which pairs hold and the new
-// lengths; a row named twice is claimed by the lowest index with atomicMin on its
-// length (claims are negative, lengths are not).  The second (one CTA per pair) moves
-// table entries and reference counts.
+// One CTA settles which pairs hold and the new lengths; a row named twice is
+// claimed by the lowest index with atomicMin on its length (claims are negative, lengths
+// are not).  Then table entries and reference counts are moved: by the same CTA, a
+// warp per pair, when there are few entries (one launch less: 2 us), by a second
+// launch with a CTA per pair otherwise.
+constexpr long long kPgOneLaunch = 16384;   // entries at most
+
+// Row `to` takes the first entries of row `from`, as many as `len` tokens need.
+__device__ __forceinline__ void fork_row(const int32_t* from, int32_t* to, int len, int32_t* ref,
+                                         int num_pages, int tid, int nthreads, uint32_t* status) {
+  for (int j = tid; j < blocks_of(len); j += nthreads) {
+    const int pg = from[j];
+    to[j] = pg;
+    if (pg < 0 || pg >= num_pages) atomicOr(status, kStatusBounds);
+    else atomicAdd(&ref[pg], 1);
+  }
+}
+
+// Entries of the tokens keep .. keep + drop - 1 leave the row.
+__device__ __forceinline__ void free_row(int32_t* row, int keep, int drop, int32_t* ref,
+                                         int num_pages, int tid, int nthreads, uint32_t* status) {
+  for (int j = blocks_of(keep) + tid; j < blocks_of(keep + drop); j += nthreads) {
+    const int pg = row[j];
+    row[j] = -1;
+    if (pg < 0 || pg >= num_pages) {
+      atomicOr(status, kStatusBounds);
+    } else if (atomicSub(&ref[pg], 1) <= 0) {      // held more often than counted
+      atomicAdd(&ref[pg], 1);
+      atomicOr(status, kStatusBounds);
+    }
+  }
+}
 
 __global__ void __launch_bounds__(kPgThreads) pages_fork_claim_kernel(
     const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
     const int32_t* __restrict__ keep, int n, int32_t* lens, int B, int max_pages,
-    int32_t* __restrict__ forked, uint32_t* status) {
+    int32_t* forked, bool all, int32_t* table, int32_t* ref, int num_pages, uint32_t* status) {
   pdl_enter();
   // 1. what every pair would get, from the lengths before the call
   for (int i = threadIdx.x; i < n; i += kPgThreads) {
@@ -102,6 +130,12 @@ __global__ void __launch_bounds__(kPgThreads) pages_fork_claim_kernel(
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kPgThreads)
     if (forked[i] >= 0) lens[dst[i]] = forked[i];
+  if (!all) return;
+  for (int i = threadIdx.x >> 5; i < n; i += kPgThreads / 32)
+    if (forked[i] > 0)
+      fork_row(table + static_cast<size_t>(src[i]) * max_pages,
+               table + static_cast<size_t>(dst[i]) * max_pages, forked[i], ref, num_pages,
+               threadIdx.x & 31, 32, status);
 }
 
 __global__ void __launch_bounds__(128) pages_fork_kernel(const int32_t* __restrict__ src,
@@ -112,21 +146,17 @@ __global__ void __launch_bounds__(128) pages_fork_kernel(const int32_t* __restri
                                                          uint32_t* status) {
   pdl_enter();
   const int len = forked[blockIdx.x];
-  if (len <= 0) return;
-  const int32_t* from = table + static_cast<size_t>(src[blockIdx.x]) * max_pages;
-  int32_t* to = table + static_cast<size_t>(dst[blockIdx.x]) * max_pages;
-  for (int j = threadIdx.x; j < blocks_of(len); j += blockDim.x) {
-    const int pg = from[j];
-    to[j] = pg;
-    if (pg < 0 || pg >= num_pages) atomicOr(status, kStatusBounds);
-    else atomicAdd(&ref[pg], 1);
-  }
+  if (len > 0)
+    fork_row(table + static_cast<size_t>(src[blockIdx.x]) * max_pages,
+             table + static_cast<size_t>(dst[blockIdx.x]) * max_pages, len, ref, num_pages,
+             threadIdx.x, blockDim.x, status);
 }
 
 // An entry that drops nothing claims nothing (the length stays as it is).
 __global__ void __launch_bounds__(kPgThreads) pages_free_claim_kernel(
     const int32_t* __restrict__ rows, const int32_t* __restrict__ keep, int n, int32_t* lens,
-    int B, int max_pages, int32_t* __restrict__ dropped, uint32_t* status) {
+    int B, int max_pages, int32_t* dropped, bool all, int32_t* table, int32_t* ref, int num_pages,
+    uint32_t* status) {
   pdl_enter();
   for (int i = threadIdx.x; i < n; i += kPgThreads) {
     const int r = rows[i], k = keep ? keep[i] : 0;
@@ -144,6 +174,11 @@ __global__ void __launch_bounds__(kPgThreads) pages_free_claim_kernel(
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kPgThreads)
     if (dropped[i] > 0) lens[rows[i]] = keep ? keep[i] : 0;
+  if (!all) return;
+  for (int i = threadIdx.x >> 5; i < n; i += kPgThreads / 32)
+    if (dropped[i] > 0)
+      free_row(table + static_cast<size_t>(rows[i]) * max_pages, keep ? keep[i] : 0, dropped[i], ref,
+               num_pages, threadIdx.x & 31, 32, status);
 }
 
 __global__ void __launch_bounds__(128) pages_free_kernel(const int32_t* __restrict__ rows,
@@ -154,19 +189,9 @@ __global__ void __launch_bounds__(128) pages_free_kernel(const int32_t* __restri
                                                          uint32_t* status) {
   pdl_enter();
   const int drop = dropped[blockIdx.x];
-  if (drop <= 0) return;
-  const int k = keep ? keep[blockIdx.x] : 0;
-  int32_t* row = table + static_cast<size_t>(rows[blockIdx.x]) * max_pages;
-  for (int j = blocks_of(k) + threadIdx.x; j < blocks_of(k + drop); j += blockDim.x) {
-    const int pg = row[j];
-    row[j] = -1;
-    if (pg < 0 || pg >= num_pages) {
-      atomicOr(status, kStatusBounds);
-    } else if (atomicSub(&ref[pg], 1) <= 0) {      // held more often than counted
-      atomicAdd(&ref[pg], 1);
-      atomicOr(status, kStatusBounds);
-    }
-  }
+  if (drop > 0)
+    free_row(table + static_cast<size_t>(rows[blockIdx.x]) * max_pages, keep ? keep[blockIdx.x] : 0,
+             drop, ref, num_pages, threadIdx.x, blockDim.x, status);
 }
 
 // ---------------------------------------------------------------- extend
@@ -304,7 +329,7 @@ __global__ void __launch_bounds__(kPgThreads) pages_compact_kernel(
 
 // ---------------------------------------------------------------- copies
 //
-// Items are (pair, chunk of a page's caches), dealt round-robin over a
+// Items are (pair, chunk of a page's caches), cut into equal runs over a
 // persistent grid.  Thread 0 of a CTA keeps kPgAhead loads and as many stores of
 // 16 KB in flight through a ring in shared memory.  The other threads
 // meanwhile rewrite block tables by page_map (compact).
@@ -346,45 +371,56 @@ __global__ void __launch_bounds__(128) pages_copy_kernel(
   if (per_page == 0) return;
   const int pairs = n_dev ? *n_dev : n;
   const long long items = static_cast<long long>(pairs) * per_page;
+  // this CTA's run of items; the next pair's pages are read a page ahead
+  const long long i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
+  if (i0 >= i1) return;
   for (int i = 0; i < kPgStages; ++i) mbar_init(&sm.full[i], 1);
   fence_mbar_init();
   fence_proxy_async_smem();
-  // item -> source, destination, bytes (0: skipped)
-  auto locate = [&](long long it, const uint8_t** s, uint8_t** d) -> uint32_t {
-    const int pair = static_cast<int>(it / per_page);
-    int ch = static_cast<int>(it - static_cast<long long>(pair) * per_page);
-    const int ps = src[pair], pd = dst[pair];
+  int pair = static_cast<int>(i0 / per_page);
+  int ch = static_cast<int>(i0 - static_cast<long long>(pair) * per_page), c = 0;
+  long long left = i1 - i0;
+  int ps = src[pair], pd = dst[pair], ps_next = -1, pd_next = -1;
+  bool skip = false;
+  auto enter = [&]() {                             // a pair begins: check it, read the next one
+    skip = ps == pd;
     if (ps < 0 || ps >= num_pages || pd < 0 || pd >= num_pages) {
       atomicOr(status, kStatusBounds);
-      return 0;
+      skip = true;
     }
-    if (ps == pd) return 0;
-    int c = 0;
-    while (ch >= pc.chunks[c + 1]) ++c;
-    const long long off = static_cast<long long>(ch - pc.chunks[c]) * kPgChunk;
-    const long long left = pc.bytes[c] - off;
-    *s = pc.base[c] + ps * pc.bytes[c] + off;
-    *d = pc.base[c] + pd * pc.bytes[c] + off;
-    return static_cast<uint32_t>(left < kPgChunk ? left : kPgChunk);
+    if (pair + 1 < pairs) {
+      ps_next = src[pair + 1];
+      pd_next = dst[pair + 1];
+    }
   };
+  enter();
   uint8_t* to[kPgStages];
   uint32_t bytes[kPgStages];
-  long long next = blockIdx.x;                     // next item to load
   uint32_t nl = 0;                                 // loads issued
-  auto load = [&]() {                              // skips items without bytes
-    for (; next < items; next += gridDim.x) {
-      const uint8_t* s;
-      uint8_t* d;
-      const uint32_t sz = locate(next, &s, &d);
-      if (sz == 0) continue;
-      const int st = nl % kPgStages;
-      to[st] = d;
-      bytes[st] = sz;
-      mbar_arrive_expect_tx(&sm.full[st], sz);
-      bulk_load(sm.buf[st], s, sz, &sm.full[st]);
-      ++nl;
-      next += gridDim.x;
-      return;
+  auto load = [&]() {
+    bool issued = false;
+    while (left > 0 && !issued) {
+      if (!skip) {
+        while (ch >= pc.chunks[c + 1]) ++c;
+        const long long off = static_cast<long long>(ch - pc.chunks[c]) * kPgChunk;
+        const long long rest = pc.bytes[c] - off;
+        const uint32_t sz = static_cast<uint32_t>(rest < kPgChunk ? rest : kPgChunk);
+        const int st = nl % kPgStages;
+        to[st] = pc.base[c] + pd * pc.bytes[c] + off;
+        bytes[st] = sz;
+        mbar_arrive_expect_tx(&sm.full[st], sz);
+        bulk_load(sm.buf[st], pc.base[c] + ps * pc.bytes[c] + off, sz, &sm.full[st]);
+        ++nl;
+        issued = true;
+      }
+      --left;
+      if (++ch == per_page) {
+        ch = c = 0;
+        ++pair;
+        ps = ps_next;
+        pd = pd_next;
+        if (left > 0) enter();
+      }
     }
   };
   for (int i = 0; i < kPgAhead; ++i) load();
@@ -510,12 +546,14 @@ msa_status_t msa_pages_fork(const int32_t* src, const int32_t* dst, const int32_
   uint32_t* sw = nullptr;
   MSA_TRY(status_word(&sw));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool all = static_cast<long long>(n) * max_pages <= kPgOneLaunch;
   {
     TraceScope trace_("pages_fork_claim_kernel", st);
     launch_pdl(pages_fork_claim_kernel, 1, kPgThreads, 0, st, src, dst, keep, n, cache_lens, B,
-               max_pages, forked, sw);
+               max_pages, forked, all, block_table, ref_count, num_pages, sw);
   }
   MSA_TRY(check_launch("pages_fork_claim_kernel"));
+  if (all) return MSA_OK;
   {
     TraceScope trace_("pages_fork_kernel", st);
     launch_pdl(pages_fork_kernel, n, 128, 0, st, src, dst, forked, block_table, ref_count,
@@ -535,12 +573,14 @@ msa_status_t msa_pages_free(const int32_t* rows, const int32_t* keep, int n, int
   uint32_t* sw = nullptr;
   MSA_TRY(status_word(&sw));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool all = static_cast<long long>(n) * max_pages <= kPgOneLaunch;
   {
     TraceScope trace_("pages_free_claim_kernel", st);
     launch_pdl(pages_free_claim_kernel, 1, kPgThreads, 0, st, rows, keep, n, cache_lens, B,
-               max_pages, dropped, sw);
+               max_pages, dropped, all, block_table, ref_count, num_pages, sw);
   }
   MSA_TRY(check_launch("pages_free_claim_kernel"));
+  if (all) return MSA_OK;
   {
     TraceScope trace_("pages_free_kernel", st);
     launch_pdl(pages_free_kernel, n, 128, 0, st, rows, keep, dropped, block_table, ref_count,

@@ -10,10 +10,10 @@
 //
 // Work: the [T * H, D] rows are cut into runs of consecutive rows, one run per
 // CTA (grid-stride in the backward).  A row belongs to D / 8 threads with 8
-// consecutive channels each, so a row is one 16-byte access per thread; "half"
-// pairs sit D-independent R / 16 lanes apart and meet by shuffling the four
-// packed words of x, "interleaved" pairs sit in one thread.  The angles of the
-// run's tokens are computed once per CTA into shared memory.
+// channels each, chosen so that the two halves of every pair sit in one thread: two
+// pieces of 4 channels R / 2 apart in the rotated part of the "half" layout, 8
+// consecutive channels elsewhere.  The angles of the run's tokens are computed once per
+// CTA into shared memory.
 //
 // Angles: the host turns each frequency into the 64-bit fixed-point fraction of
 // a turn F_i = f_i / (2 pi) * 2^64, so position * F_i mod 2^64 is the angle in
@@ -44,7 +44,7 @@ struct RxArgs {
   const int32_t* cu;
   float* dw_part;                 // backward: [gridDim.x, D]
   long long rows;                 // T * H
-  int T, H, S, R, layout, run;    // run: rows per CTA
+  int T, H, S, R, run;            // run: rows per CTA
   uint32_t inv;                   // ceil(2^20 / H): i / H == (i * inv) >> 20 for i < 4096
   float eps, gain;
 };
@@ -80,62 +80,107 @@ __device__ __forceinline__ void rx_angles(const RxArgs& a, const RxTurns& turns,
   }
 }
 
-// The thread's 8 channels turned by the token's angles; sgn = 1 turns forward,
-// -1 back.  v: own values, p: the partner channels' values ("half" only).
-__device__ __forceinline__ void rx_turn(float (&v)[8], const float (&p)[8], const float* tab, int c,
-                                        int R, int layout, float sgn) {
-  const int half = R >> 1;
-  if (layout == MSA_ROPE_HALF) {
-    const int i0 = 8 * c >= half ? 8 * c - half : 8 * c;
-    const float sg = 8 * c >= half ? sgn : -sgn;
-    float cs[8], sn[8];
-    *reinterpret_cast<float4*>(cs) = *reinterpret_cast<const float4*>(tab + i0);
-    *reinterpret_cast<float4*>(cs + 4) = *reinterpret_cast<const float4*>(tab + i0 + 4);
-    *reinterpret_cast<float4*>(sn) = *reinterpret_cast<const float4*>(tab + half + i0);
-    *reinterpret_cast<float4*>(sn + 4) = *reinterpret_cast<const float4*>(tab + half + i0 + 4);
+// The 8 channels of a thread: pieces [off0, off0 + 4) and [off1, off1 + 4).  In
+// the rotated part of the "half" layout the pieces are partners (off1 = off0 + R/2);
+// elsewhere they are 8 consecutive channels.
+struct RxLane {
+  int off0, off1, pair;   // pair: first frequency
+  bool rot;
+};
+
+template <bool kHalf>
+__device__ __forceinline__ RxLane rx_lane(int c, int R) {
+  RxLane l;
+  l.rot = 8 * c < R;
+  l.off0 = kHalf && l.rot ? 4 * c : 8 * c;
+  l.off1 = kHalf && l.rot ? 4 * c + (R >> 1) : 8 * c + 4;
+  l.pair = 4 * c;
+  return l;
+}
+
+struct RxRow {
+  uint2 a, b;
+};
+
+__device__ __forceinline__ RxRow rx_load(const __nv_bfloat16* row, const RxLane& l) {
+  RxRow r;
+  r.a = __ldcs(reinterpret_cast<const uint2*>(row + l.off0));
+  r.b = __ldcs(reinterpret_cast<const uint2*>(row + l.off1));
+  return r;
+}
+
+__device__ __forceinline__ void rx_store(__nv_bfloat16* row, const RxLane& l, const float2 (&v)[4]) {
+  *reinterpret_cast<uint2*>(row + l.off0) = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
+  *reinterpret_cast<uint2*>(row + l.off1) = make_uint2(pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+}
+
+__device__ __forceinline__ void rx_unpack(const RxRow& r, float2 (&v)[4]) {
+  v[0] = bf2(r.a.x);
+  v[1] = bf2(r.a.y);
+  v[2] = bf2(r.b.x);
+  v[3] = bf2(r.b.y);
+}
+
+// Turns 8 channels: v[p] = v[p] * c[p] + partner * s[p].  The partner of pair p is
+// v[p ^ 2] ("half") or v[p] with its halves swapped ("interleaved"); signs and any
+// factors are in the coefficients.
+template <bool kHalf>
+__device__ __forceinline__ void rx_turn(float2 (&v)[4], const float2 (&c)[4], const float2 (&s)[4]) {
+  float2 o[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], cs[e], sg * p[e] * sn[e]);
+  for (int p = 0; p < 4; ++p) {
+    const float2 q = kHalf ? v[p ^ 2] : make_float2(v[p].y, v[p].x);
+    o[p] = __ffma2_rn(v[p], c[p], __fmul2_rn(q, s[p]));
+  }
+#pragma unroll
+  for (int p = 0; p < 4; ++p) v[p] = o[p];
+}
+
+// Coefficients of one token: cos and +-sin (dir = 1 forward, -1 back), each times
+// the factor w of the value it multiplies (w = 1 + weight, or all ones).
+template <bool kHalf>
+__device__ __forceinline__ void rx_coefficients(const float* tab, int half, const RxLane& l,
+                                                const float2 (&w)[4], float dir, float2 (&c)[4],
+                                                float2 (&s)[4]) {
+  if (!l.rot) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      c[p] = w[p];
+      s[p] = make_float2(0.f, 0.f);
+    }
+    return;
+  }
+  const float4 cv = *reinterpret_cast<const float4*>(tab + l.pair);
+  const float4 sv = *reinterpret_cast<const float4*>(tab + half + l.pair);
+  if (kHalf) {
+    const float2 c2[2] = {make_float2(cv.x, cv.y), make_float2(cv.z, cv.w)};
+    const float2 s2[2] = {make_float2(dir * sv.x, dir * sv.y), make_float2(dir * sv.z, dir * sv.w)};
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      c[p] = __fmul2_rn(w[p], c2[p & 1]);
+      const float2 t = __fmul2_rn(w[p ^ 2], s2[p & 1]);
+      s[p] = p < 2 ? make_float2(-t.x, -t.y) : t;
+    }
   } else {
-    float cs[4], sn[4];
-    *reinterpret_cast<float4*>(cs) = *reinterpret_cast<const float4*>(tab + 4 * c);
-    *reinterpret_cast<float4*>(sn) = *reinterpret_cast<const float4*>(tab + half + 4 * c);
+    const float ce[4] = {cv.x, cv.y, cv.z, cv.w};
+    const float se[4] = {dir * sv.x, dir * sv.y, dir * sv.z, dir * sv.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x1 = v[2 * e], x2 = v[2 * e + 1];
-      v[2 * e] = fmaf(x1, cs[e], -sgn * x2 * sn[e]);
-      v[2 * e + 1] = fmaf(x2, cs[e], sgn * x1 * sn[e]);
+    for (int p = 0; p < 4; ++p) {
+      c[p] = make_float2(w[p].x * ce[p], w[p].y * ce[p]);
+      s[p] = make_float2(-w[p].y * se[p], w[p].x * se[p]);
     }
   }
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
-  const float2 a = bf2(u.x), b = bf2(u.y), c = bf2(u.z), d = bf2(u.w);
-  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-  v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  uint4 u;
-  u.x = pack_bf16x2(v[0], v[1]);
-  u.y = pack_bf16x2(v[2], v[3]);
-  u.z = pack_bf16x2(v[4], v[5]);
-  u.w = pack_bf16x2(v[6], v[7]);
-  return u;
-}
-
-__device__ __forceinline__ uint4 shfl4(const uint4& u, int src) {
-  uint4 r;
-  r.x = __shfl_sync(0xffffffffu, u.x, src);
-  r.y = __shfl_sync(0xffffffffu, u.y, src);
-  r.z = __shfl_sync(0xffffffffu, u.z, src);
-  r.w = __shfl_sync(0xffffffffu, u.w, src);
-  return r;
-}
-
 }  // namespace
 
-template <int D, bool kNorm>
-__global__ void __launch_bounds__(kRxThreads) rope_ex_kernel(const RxArgs a, const RxTurns turns) {
+// Rows of a thread come one after another, kSlots apart; three rows' loads are in
+// flight while a fourth is normed, turned and stored.  The coefficients (1 + w) cos
+// and (1 + w) sin stay in registers while the token stays the same.  Arithmetic runs on
+// packed pairs of fp32: the kernel would be bound by instruction issue otherwise
+// (162 instructions per warp and row took 112 us for 16,384 tokens x 64 heads).
+template <int D, bool kNorm, bool kHalf>
+__global__ void __launch_bounds__(kRxThreads, 7) rope_ex_kernel(const RxArgs a, const RxTurns turns) {
   pdl_enter();
   constexpr int kLpr = D / 8, kSlots = kRxThreads / kLpr;
   __shared__ __align__(16) float table[2 * kRxMaxAngles];
@@ -144,140 +189,161 @@ __global__ void __launch_bounds__(kRxThreads) rope_ex_kernel(const RxArgs a, con
   const int t0 = static_cast<int>(r0 / a.H);
   const int h0 = static_cast<int>(r0 - static_cast<long long>(t0) * a.H);
   const int ntok = (h0 + n + a.H - 1) / a.H;
-  const int lane = threadIdx.x & 31;
   const int c = threadIdx.x & (kLpr - 1), slot = threadIdx.x / kLpr;
-  const bool rot = 8 * c < a.R;
-  // lane of the partner channels ("half" layout; itself elsewhere)
-  const int hop = a.R >> 4;
-  const int pc = (a.layout == MSA_ROPE_HALF && rot) ? (c < hop ? c + hop : c - hop) : c;
-  const int psrc = (lane & ~(kLpr - 1)) | pc;
-  float w1[8], wp[8];
-  if (kNorm) {
-    unpack8(*reinterpret_cast<const uint4*>(a.w + 8 * c), w1);
-    unpack8(*reinterpret_cast<const uint4*>(a.w + 8 * pc), wp);
+  const RxLane l = rx_lane<kHalf>(c, a.R);
+  const __nv_bfloat16* xb = a.x + r0 * D;
+  __nv_bfloat16* yb = a.y + r0 * D;
+  constexpr int kDeep = 4;
+  RxRow raw[kDeep];
+  auto fetch = [&](int i, RxRow& r) {
+    r.a = r.b = make_uint2(0u, 0u);
+    if (i < n) r = rx_load(xb + static_cast<size_t>(i) * D, l);
+  };
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w1[e] += 1.f, wp[e] += 1.f;
+  for (int k = 0; k < kDeep - 1; ++k) fetch(k * kSlots + slot, raw[k]);
+  float2 w1[4];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) w1[p] = make_float2(1.f, 1.f);
+  if (kNorm) {
+    float2 wv[4];
+    RxRow wr;
+    wr.a = *reinterpret_cast<const uint2*>(a.w + l.off0);
+    wr.b = *reinterpret_cast<const uint2*>(a.w + l.off1);
+    rx_unpack(wr, wv);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) w1[p] = __fadd2_rn(wv[p], w1[p]);
   }
   rx_angles(a, turns, t0, ntok, table);
   __syncthreads();
-  constexpr int kDeep = 4;                       // rows in flight per thread
-  const __nv_bfloat16* xb = a.x + r0 * D + 8 * c;
-  __nv_bfloat16* yb = a.y + r0 * D + 8 * c;
+  int have = -1;
+  float2 cc[4], ss[4];
   // the loop bounds are uniform over the CTA: every lane reaches the shuffles
   for (int base = 0; base < n; base += kDeep * kSlots) {
-    uint4 raw[kDeep];
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
-      const int i = base + k * kSlots + slot;
-      raw[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < n) raw[k] = __ldcs(reinterpret_cast<const uint4*>(xb + static_cast<size_t>(i) * D));
-    }
-#pragma unroll
-    for (int k = 0; k < kDeep; ++k) {
-      const int i = base + k * kSlots + slot;
       if (base + k * kSlots >= n) break;
-      float v[8], p[8];
-      unpack8(raw[k], v);
-      if (a.layout == MSA_ROPE_HALF) unpack8(shfl4(raw[k], psrc), p);
+      const int i = base + k * kSlots + slot;
+      fetch(i + (kDeep - 1) * kSlots, raw[(k + kDeep - 1) % kDeep]);
+      float2 v[4];
+      rx_unpack(raw[k], v);
+      float2 rr = make_float2(1.f, 1.f);
       if (kNorm) {
-        float ss = 0.f;
+        float2 q = __fmul2_rn(v[0], v[0]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+        for (int p = 1; p < 4; ++p) q = __ffma2_rn(v[p], v[p], q);
+        float sum = q.x + q.y;
 #pragma unroll
-        for (int m = kLpr / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-        const float rinv = rsqrtf(ss * (1.f / D) + a.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[e] *= rinv * w1[e];
-          if (a.layout == MSA_ROPE_HALF) p[e] *= rinv * wp[e];
-        }
+        for (int m = kLpr / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        rr.x = rr.y = rsqrtf(sum * (1.f / D) + a.eps);
       }
       if (i < n) {
         const int tok = static_cast<int>((static_cast<uint32_t>(h0 + i) * a.inv) >> 20);
-        if (rot) rx_turn(v, p, table + tok * a.R, c, a.R, a.layout, 1.f);
-        *reinterpret_cast<uint4*>(yb + static_cast<size_t>(i) * D) = pack8(v);
+        if (tok != have) {
+          have = tok;
+          rx_coefficients<kHalf>(table + tok * a.R, a.R >> 1, l, w1, 1.f, cc, ss);
+        }
+        rx_turn<kHalf>(v, cc, ss);
+        if (kNorm) {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) v[p] = __fmul2_rn(v[p], rr);
+        }
+        rx_store(yb + static_cast<size_t>(i) * D, l, v);
       }
     }
   }
 }
 
-template <int D, bool kNorm>
-__global__ void __launch_bounds__(kRxThreads) rope_ex_bwd_kernel(const RxArgs a,
-                                                                  const RxTurns turns) {
+template <int D, bool kNorm, bool kHalf>
+__global__ void __launch_bounds__(kRxThreads, 5) rope_ex_bwd_kernel(const RxArgs a,
+                                                                    const RxTurns turns) {
   pdl_enter();
   constexpr int kLpr = D / 8, kSlots = kRxThreads / kLpr;
   __shared__ __align__(16) float table[2 * kRxMaxAngles];
-  const int lane = threadIdx.x & 31;
   const int c = threadIdx.x & (kLpr - 1), slot = threadIdx.x / kLpr;
-  const bool rot = 8 * c < a.R;
-  const int hop = a.R >> 4;
-  const int pc = (a.layout == MSA_ROPE_HALF && rot) ? (c < hop ? c + hop : c - hop) : c;
-  const int psrc = (lane & ~(kLpr - 1)) | pc;
-  float w1[8], aw[8];
+  const RxLane l = rx_lane<kHalf>(c, a.R);
+  float2 one[4], w1[4], aw[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) aw[e] = 0.f;
-  if (kNorm) {
-    unpack8(*reinterpret_cast<const uint4*>(a.w + 8 * c), w1);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w1[e] += 1.f;
+  for (int p = 0; p < 4; ++p) {
+    one[p] = make_float2(1.f, 1.f);
+    aw[p] = make_float2(0.f, 0.f);
   }
-  constexpr int kDeep = 2;
+  if (kNorm) {
+    RxRow wr;
+    wr.a = *reinterpret_cast<const uint2*>(a.w + l.off0);
+    wr.b = *reinterpret_cast<const uint2*>(a.w + l.off1);
+    rx_unpack(wr, w1);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) w1[p] = __fadd2_rn(w1[p], one[p]);
+  }
+  constexpr int kDeep = 3;
   for (long long r0 = static_cast<long long>(blockIdx.x) * a.run; r0 < a.rows;
        r0 += static_cast<long long>(gridDim.x) * a.run) {
     const int n = static_cast<int>(a.rows - r0 < a.run ? a.rows - r0 : a.run);
     const int t0 = static_cast<int>(r0 / a.H);
     const int h0 = static_cast<int>(r0 - static_cast<long long>(t0) * a.H);
     const int ntok = (h0 + n + a.H - 1) / a.H;
+    const __nv_bfloat16* gb = a.dy + r0 * D;
+    const __nv_bfloat16* xb = kNorm ? a.x + r0 * D : nullptr;
+    __nv_bfloat16* ob = a.y + r0 * D;
+    RxRow rg[kDeep], rx[kDeep];
+    auto fetch = [&](int i, RxRow& g, RxRow& x) {
+      g.a = g.b = x.a = x.b = make_uint2(0u, 0u);
+      if (i < n) {
+        g = rx_load(gb + static_cast<size_t>(i) * D, l);
+        if (kNorm) x = rx_load(xb + static_cast<size_t>(i) * D, l);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < kDeep - 1; ++k) fetch(k * kSlots + slot, rg[k], rx[k]);
     __syncthreads();                              // the previous run's angles are consumed
     rx_angles(a, turns, t0, ntok, table);
     __syncthreads();
-    const size_t off = static_cast<size_t>(r0) * D + 8 * c;
+    int have = -1;
+    float2 cc[4], ss[4];
     for (int base = 0; base < n; base += kDeep * kSlots) {
-      uint4 rg[kDeep], rx[kDeep];
 #pragma unroll
       for (int k = 0; k < kDeep; ++k) {
-        const int i = base + k * kSlots + slot;
-        rg[k] = rx[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (i < n) {
-          rg[k] = __ldcs(reinterpret_cast<const uint4*>(a.dy + off + static_cast<size_t>(i) * D));
-          if (kNorm) rx[k] = __ldcs(reinterpret_cast<const uint4*>(a.x + off + static_cast<size_t>(i) * D));
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kDeep; ++k) {
-        const int i = base + k * kSlots + slot;
         if (base + k * kSlots >= n) break;
-        float dz[8], p[8];
-        unpack8(rg[k], dz);
-        if (a.layout == MSA_ROPE_HALF) unpack8(shfl4(rg[k], psrc), p);
+        const int i = base + k * kSlots + slot;
+        fetch(i + (kDeep - 1) * kSlots, rg[(k + kDeep - 1) % kDeep], rx[(k + kDeep - 1) % kDeep]);
+        float2 dz[4];
+        rx_unpack(rg[k], dz);
         const int ii = i < n ? i : n - 1;
         const int tok = static_cast<int>((static_cast<uint32_t>(h0 + ii) * a.inv) >> 20);
-        if (rot) rx_turn(dz, p, table + tok * a.R, c, a.R, a.layout, -1.f);
+        if (tok != have) {
+          have = tok;
+          rx_coefficients<kHalf>(table + tok * a.R, a.R >> 1, l, one, -1.f, cc, ss);
+        }
+        rx_turn<kHalf>(dz, cc, ss);
         if (kNorm) {
-          float xv[8], ss = 0.f, dot = 0.f;
-          unpack8(rx[k], xv);
+          // r = rsqrt(mean(x^2) + eps), dot = sum(g x):
+          // dx = r g - x (r^3 dot / D), dw += dz x r
+          float2 xv[4], g[4];
+          rx_unpack(rx[k], xv);
+          float2 q = make_float2(0.f, 0.f), d = q;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            ss = fmaf(xv[e], xv[e], ss);
-            dot = fmaf(dz[e] * w1[e], xv[e], dot);
+          for (int p = 0; p < 4; ++p) {
+            g[p] = __fmul2_rn(dz[p], w1[p]);
+            q = __ffma2_rn(xv[p], xv[p], q);
+            d = __ffma2_rn(g[p], xv[p], d);
           }
+          float2 sums = make_float2(q.x + q.y, d.x + d.y);
 #pragma unroll
-          for (int m = kLpr / 2; m >= 1; m >>= 1) {
-            ss += __shfl_xor_sync(0xffffffffu, ss, m);
-            dot += __shfl_xor_sync(0xffffffffu, dot, m);
-          }
-          const float rinv = rsqrtf(ss * (1.f / D) + a.eps);
-          const float mean = dot * rinv * (1.f / D);   // mean(g xh)
+          for (int m = kLpr / 2; m >= 1; m >>= 1)
+            sums = __fadd2_rn(sums, make_float2(__shfl_xor_sync(0xffffffffu, sums.x, m),
+                                                __shfl_xor_sync(0xffffffffu, sums.y, m)));
+          const float r = rsqrtf(sums.x * (1.f / D) + a.eps);
+          const float k2 = -(r * r) * (r * (sums.y * (1.f / D)));
+          const float2 rr = make_float2(r, r), kk = make_float2(k2, k2);
           if (i < n) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float xh = xv[e] * rinv;
-              aw[e] = fmaf(dz[e], xh, aw[e]);
-              dz[e] = rinv * (dz[e] * w1[e] - xh * mean);
+            for (int p = 0; p < 4; ++p) {
+              aw[p] = __ffma2_rn(__fmul2_rn(dz[p], rr), xv[p], aw[p]);
+              dz[p] = __ffma2_rn(xv[p], kk, __fmul2_rn(g[p], rr));
             }
           }
         }
-        if (i < n) *reinterpret_cast<uint4*>(a.y + off + static_cast<size_t>(i) * D) = pack8(dz);
+        if (i < n) rx_store(ob + static_cast<size_t>(i) * D, l, dz);
       }
     }
   }
@@ -286,7 +352,10 @@ __global__ void __launch_bounds__(kRxThreads) rope_ex_bwd_kernel(const RxArgs a,
     __syncthreads();
     float* red = table;                            // [kSlots][D]: 4 KB
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[slot * D + 8 * c + e] = aw[e];
+    for (int p = 0; p < 4; ++p) {
+      const int ch = (p < 2 ? l.off0 : l.off1) + 2 * (p & 1);
+      *reinterpret_cast<float2*>(red + slot * D + ch) = aw[p];
+    }
     __syncthreads();
     for (int ch = threadIdx.x; ch < D; ch += kRxThreads) {
       float acc = 0.f;
@@ -297,16 +366,25 @@ __global__ void __launch_bounds__(kRxThreads) rope_ex_bwd_kernel(const RxArgs a,
 }
 
 // dw[ch] = the partial rows in a fixed order: thread (k, ch) adds rows k,
-// k + 128, ..., then a pairwise tree over k.
+// k + 128, ... (all its loads in flight), then a pairwise tree over k.
 constexpr int kRxSumCh = 8, kRxSumWays = 128;
+constexpr int kRxBwdCtas = 760;                    // 5 per SM, all resident
+constexpr int kRxSumRows = (kRxBwdCtas + kRxSumWays - 1) / kRxSumWays;
 __global__ void __launch_bounds__(kRxSumCh * kRxSumWays)
     rope_ex_dw_kernel(const float* __restrict__ part, int nparts, int D, float* __restrict__ dw) {
   pdl_enter();
   __shared__ float red[kRxSumWays][kRxSumCh];
   const int cl = threadIdx.x % kRxSumCh, k = threadIdx.x / kRxSumCh;
   const int ch = blockIdx.x * kRxSumCh + cl;
+  float v[kRxSumRows];
+#pragma unroll
+  for (int j = 0; j < kRxSumRows; ++j) {
+    const int p = k + j * kRxSumWays;
+    v[j] = p < nparts ? part[static_cast<size_t>(p) * D + ch] : 0.f;
+  }
   float acc = 0.f;
-  for (int p = k; p < nparts; p += kRxSumWays) acc += part[static_cast<size_t>(p) * D + ch];
+#pragma unroll
+  for (int j = 0; j < kRxSumRows; ++j) acc += v[j];
   red[k][cl] = acc;
   __syncthreads();
 #pragma unroll
@@ -327,7 +405,7 @@ static int rx_run(int H, int R, int target) {
   return static_cast<int>(cap < target ? cap : target);
 }
 
-constexpr int kRxFwdRun = 128, kRxBwdRun = 128, kRxBwdCtas = 1216;   // 8 per SM
+constexpr int kRxFwdRun = 128, kRxBwdRun = 128;
 
 static int rx_bwd_ctas(long long rows, int run) {
   const long long n = (rows + run - 1) / run;
@@ -366,7 +444,6 @@ static RxArgs rx_args(const RopeExJob& j, const msa_rope_t& rope) {
   a.H = j.H;
   a.S = j.S;
   a.R = rope.dim;
-  a.layout = rope.layout;
   a.inv = ((1u << 20) + j.H - 1) / j.H;
   a.eps = j.eps;
   a.gain = rope.gain;
@@ -380,8 +457,10 @@ static msa_status_t rx_forward(const RopeExJob& j, const msa_rope_t& rope, cudaS
   const RxTurns turns = rx_turns(rope);
   const unsigned grid = static_cast<unsigned>((a.rows + a.run - 1) / a.run);
   TraceScope trace_("rope_ex_kernel", stream);
-  launch_pdl(j.w ? rope_ex_kernel<D, true> : rope_ex_kernel<D, false>, grid, kRxThreads, 0, stream,
-             a, turns);
+  const bool half = rope.layout == MSA_ROPE_HALF;
+  launch_pdl(j.w ? (half ? rope_ex_kernel<D, true, true> : rope_ex_kernel<D, true, false>)
+                 : (half ? rope_ex_kernel<D, false, true> : rope_ex_kernel<D, false, false>),
+             grid, kRxThreads, 0, stream, a, turns);
   return check_launch("rope_ex_kernel");
 }
 
@@ -395,8 +474,10 @@ static msa_status_t rx_backward(const RopeExJob& j, const msa_rope_t& rope, floa
   const int ctas = rx_bwd_ctas(a.rows, a.run);
   {
     TraceScope trace_("rope_ex_bwd_kernel", stream);
-    launch_pdl(j.w ? rope_ex_bwd_kernel<D, true> : rope_ex_bwd_kernel<D, false>, ctas, kRxThreads,
-               0, stream, a, turns);
+    const bool half = rope.layout == MSA_ROPE_HALF;
+    launch_pdl(j.w ? (half ? rope_ex_bwd_kernel<D, true, true> : rope_ex_bwd_kernel<D, true, false>)
+                   : (half ? rope_ex_bwd_kernel<D, false, true> : rope_ex_bwd_kernel<D, false, false>),
+               ctas, kRxThreads, 0, stream, a, turns);
   }
   msa_status_t e = check_launch("rope_ex_bwd_kernel");
   if (e != MSA_OK || !j.w) return e;
