@@ -31,16 +31,34 @@ struct Cache4Args {
 };
 
 // Page and slot of token t's position; page -1: out of range, -2: not a token of
-// the pack.
+// the pack.  Every lane of the warp calls it (8 lanes per token, tokens ascending).
+// Up to 32 sequences are searched by one load and a vote per token, more by bisection.
 __device__ __forceinline__ int2 c4_place(const Cache4Args& a, int t, uint32_t* status) {
-  if (t >= a.T || t < __ldg(a.cu) || t >= __ldg(a.cu + a.S)) return make_int2(-2, 0);
-  int lo = 0, hi = a.S;                            // largest s with cu[s] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid;
+  int lo = 0, first, from = 0;
+  const int begin = __ldg(a.cu), end = __ldg(a.cu + a.S);
+  if (a.S <= 32) {
+    const int lane = threadIdx.x & 31;
+    const int cu = lane < a.S ? __ldg(a.cu + lane) : 0;
+    const int st = a.start && lane < a.S ? __ldg(a.start + lane) : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {                  // largest s with cu[s] <= the warp's k-th token
+      const int tk = __shfl_sync(0xffffffffu, t, 8 * k);
+      const uint32_t at = __ballot_sync(0xffffffffu, lane < a.S && cu <= tk);
+      if (lane >> 3 == k) lo = at ? 31 - __clz(at) : 0;
+    }
+    first = __shfl_sync(0xffffffffu, cu, lo);
+    from = __shfl_sync(0xffffffffu, st, lo);
+  } else {
+    int hi = a.S;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid;
+    }
+    first = __ldg(a.cu + lo);
+    if (a.start) from = __ldg(a.start + lo);
   }
-  const long long pos = static_cast<long long>(t - __ldg(a.cu + lo)) +
-                        (a.start ? __ldg(a.start + lo) : 0);
+  if (t >= a.T || t < begin || t >= end) return make_int2(-2, 0);
+  const long long pos = static_cast<long long>(t - first) + from;
   int page = -1;
   if (pos >= 0 && pos < static_cast<long long>(a.max_pages) * kBlock)
     page = __ldg(a.table + static_cast<size_t>(lo) * a.max_pages + pos / kBlock);
@@ -49,6 +67,12 @@ __device__ __forceinline__ int2 c4_place(const Cache4Args& a, int t, uint32_t* s
     return make_int2(-1, 0);
   }
   return make_int2(page, static_cast<int>(pos % kBlock));
+}
+
+// Tensor and head of a (tensor, head) pair
+__device__ __forceinline__ int2 c4_job(int j, int H) {
+  const int n = j >= 2 * H ? 2 : (j >= H ? 1 : 0);
+  return make_int2(n, j - n * H);
 }
 
 struct C4Words {
@@ -66,10 +90,11 @@ __global__ void __launch_bounds__(kC4Threads) cache4_store_kernel(const Cache4Ar
   const int2 at = c4_place(a, t, status);
   if (at.x < 0) return;
   const int jobs = a.n * a.H;
+  const size_t row = static_cast<size_t>(t) * a.H, page = static_cast<size_t>(at.x) * a.H;
   auto fetch = [&](int j) {
-    const int n = j / a.H, h = j - n * a.H;
-    const uint4* src = reinterpret_cast<const uint4*>(
-        a.x[n] + (static_cast<size_t>(t) * a.H + h) * kD + 16 * c);
+    const int2 nh = c4_job(j, a.H);
+    const uint4* src =
+        reinterpret_cast<const uint4*>(a.x[nh.x] + (row + static_cast<size_t>(nh.y)) * kD + 16 * c);
     return C4Words{__ldcs(src), __ldcs(src + 1)};
   };
   int j = blockIdx.y;
@@ -77,12 +102,12 @@ __global__ void __launch_bounds__(kC4Threads) cache4_store_kernel(const Cache4Ar
   C4Words u = fetch(j);
   while (j < jobs) {
     const int next = j + gridDim.y;
-    const uint32_t x[8] = {u.a.x, u.a.y, u.a.z, u.a.w, u.b.x, u.b.y, u.b.z, u.b.w};
+    uint32_t x[8] = {u.a.x, u.a.y, u.a.z, u.a.w, u.b.x, u.b.y, u.b.z, u.b.w};
     if (next < jobs) u = fetch(next);
-    const int n = j / a.H, h = j - n * a.H;
+    const int2 nh = c4_job(j, a.H);
     uint32_t sb;
-    const uint2 codes = quantise16(x, a.gain[n], a.inv_gain[n], &sb);
-    uint8_t* slab = a.cache[n] + (static_cast<size_t>(at.x) * a.H + h) * kSlab;
+    const uint2 codes = quantise16(x, a.gain[nh.x], a.inv_gain[nh.x], &sb);
+    uint8_t* slab = a.cache[nh.x] + (page + static_cast<size_t>(nh.y)) * kSlab;
     *reinterpret_cast<uint2*>(slab + slab_code(at.y) + 8 * c) = codes;
     slab[slab_scale(at.y) + c] = static_cast<uint8_t>(sb);
     j = next;
@@ -97,12 +122,13 @@ __global__ void __launch_bounds__(kC4Threads) cache4_load_kernel(const Cache4Arg
   const int2 at = c4_place(a, t, status);
   if (at.x == -2) return;
   const int jobs = a.n * a.H;
+  const size_t row = static_cast<size_t>(t) * a.H, page = static_cast<size_t>(max(at.x, 0)) * a.H;
   uint2 w = make_uint2(0u, 0u);
   uint32_t sb = 0u;
   auto fetch = [&](int j) {
     if (at.x < 0) return;
-    const int n = j / a.H, h = j - n * a.H;
-    const uint8_t* slab = a.rcache[n] + (static_cast<size_t>(at.x) * a.H + h) * kSlab;
+    const int2 nh = c4_job(j, a.H);
+    const uint8_t* slab = a.rcache[nh.x] + (page + static_cast<size_t>(nh.y)) * kSlab;
     w = __ldcs(reinterpret_cast<const uint2*>(slab + slab_code(at.y) + 8 * c));
     sb = __ldcs(slab + slab_scale(at.y) + c);
   };
@@ -111,9 +137,9 @@ __global__ void __launch_bounds__(kC4Threads) cache4_load_kernel(const Cache4Arg
   fetch(j);
   while (j < jobs) {
     const int next = j + gridDim.y;
-    const int n = j / a.H, h = j - n * a.H;
+    const int2 nh = c4_job(j, a.H);
     const uint2 cw = w;
-    const float s = scale_value(sb) * a.gain[n];
+    const float s = scale_value(sb) * a.gain[nh.x];
     if (next < jobs) fetch(next);
     // code * scale * gain has at most 6 significant bits: exact in fp32 and in bf16
     const float2 s2 = make_float2(s, s);
@@ -128,7 +154,7 @@ __global__ void __launch_bounds__(kC4Threads) cache4_load_kernel(const Cache4Arg
         o[4 * half + i] = pack_bf16x2(f.x, f.y);
       }
     }
-    uint4* dst = reinterpret_cast<uint4*>(a.y[n] + (static_cast<size_t>(t) * a.H + h) * kD + 16 * c);
+    uint4* dst = reinterpret_cast<uint4*>(a.y[nh.x] + (row + static_cast<size_t>(nh.y)) * kD + 16 * c);
     __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
     __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
     j = next;
@@ -256,6 +282,10 @@ __global__ void __launch_bounds__(32 * kApWarps) decode4_append_kernel(const App
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   const Scale16 sc = scale16(m, a.gain[n], a.inv_gain[n]);
   uint32_t code = 0u;
+  if (sc.cut != 0.f) {
+    o[0] = cut_word(sc, o[0]);
+    o[1] = cut_word(sc, o[1]);
+  }
   if (sc.s != 0.f) code = code_word(sc, o[0]) | code_word(sc, o[1]) << 8;
   uint8_t* slab = a.cache[n] + (static_cast<size_t>(page) * a.H + h) * kSlab;
   const int slot = p % kBlock;

@@ -70,17 +70,18 @@ __device__ __forceinline__ Scale16 scale16(uint32_t m, float gain, float inv_gai
   return r;
 }
 
+// x (packed bf16) cut to +-sc.cut
+__device__ __forceinline__ uint32_t cut_word(const Scale16& sc, uint32_t x) {
+  const float2 f = word_f2(x);
+  return pack_bf16x2(fminf(fmaxf(f.x, -sc.cut), sc.cut), fminf(fmaxf(f.y, -sc.cut), sc.cut));
+}
+
 __device__ __forceinline__ uint32_t code_word(const Scale16& sc, uint32_t x) {
-  float2 f = word_f2(x);
-  if (sc.cut != 0.f) {
-    f.x = fminf(fmaxf(f.x, -sc.cut), sc.cut);
-    f.y = fminf(fmaxf(f.y, -sc.cut), sc.cut);
-  }
-  return code_pair(f, sc.s, sc.rs);
+  return code_pair(word_f2(x), sc.s, sc.rs);
 }
 
 // Codes (8 bytes) and scale byte of 16 bf16 channels (8 packed words).
-__device__ __forceinline__ uint2 quantise16(const uint32_t (&x)[8], float gain, float inv_gain,
+__device__ __forceinline__ uint2 quantise16(uint32_t (&x)[8], float gain, float inv_gain,
                                             uint32_t* scale) {
   uint32_t m = 0;                                  // largest magnitude as bf16 bits
 #pragma unroll
@@ -88,10 +89,14 @@ __device__ __forceinline__ uint2 quantise16(const uint32_t (&x)[8], float gain, 
   m = max(m & 0xFFFFu, m >> 16);
   const Scale16 sc = scale16(m, gain, inv_gain);
   *scale = sc.byte;
-  if (sc.s == 0.f) return make_uint2(0u, 0u);
+  if (sc.cut != 0.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = cut_word(sc, x[i]);
+  }
   uint32_t c[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) c[i] = code_word(sc, x[i]);
+  if (sc.s == 0.f) return make_uint2(0u, 0u);
   return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
                     __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
 }

@@ -46,6 +46,7 @@ struct RxArgs {
   long long rows;                 // T * H
   int T, H, S, R, run;            // run: rows per CTA
   uint32_t inv;                   // ceil(2^20 / H): i / H == (i * inv) >> 20 for i < 4096
+  uint32_t inv_half;              // ceil(2^20 / (R / 2)), for k < 2048
   float eps, gain;
 };
 
@@ -54,25 +55,33 @@ __device__ __forceinline__ float2 bf2(uint32_t u) {
 }
 
 // cos and sin (times gain) of the tokens t0 .. t0 + ntok - 1 of the run:
-// table[tok * R + i] = cos, [tok * R + R / 2 + i] = sin of pair i
+// table[tok * R + i] = cos, [tok * R + R / 2 + i] = sin of pair i.  Every thread of the
+// CTA takes part; the table may be read after the next barrier.
 __device__ __forceinline__ void rx_angles(const RxArgs& a, const RxTurns& turns, int t0, int ntok,
-                                          float* table) {
+                                          unsigned long long* freq, int* pos, float* table) {
   const int half = a.R >> 1;
-  for (int k = threadIdx.x; k < ntok * half; k += blockDim.x) {
-    const int tok = k / half, i = k - tok * half;
+  // frequencies by way of shared memory: lanes that index the parameters apart are
+  // served one at a time
+  for (int i = threadIdx.x; i < half; i += blockDim.x) freq[i] = turns.f[i];
+  for (int tok = threadIdx.x; tok < ntok; tok += blockDim.x) {
     const int t = t0 + tok;
-    long long pos;
     if (a.positions) {
-      pos = __ldg(a.positions + t);
+      pos[tok] = __ldg(a.positions + t);
     } else {
       int lo = 0, hi = a.S;                  // largest s with cu[s] <= t
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid;
       }
-      pos = t - __ldg(a.cu + lo);
+      pos[tok] = t - __ldg(a.cu + lo);
     }
-    const long long ang = static_cast<long long>(static_cast<unsigned long long>(pos) * turns.f[i]);
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < ntok * half; k += blockDim.x) {
+    const int tok = static_cast<int>((static_cast<uint32_t>(k) * a.inv_half) >> 20);
+    const int i = k - tok * half;
+    const long long ang = static_cast<long long>(
+        static_cast<unsigned long long>(static_cast<long long>(pos[tok])) * freq[i]);
     float s, c;
     sincospif(static_cast<float>(ang) * 1.0842021724855044e-19f, &s, &c);   // * 2^-63
     table[tok * a.R + i] = c * a.gain;
@@ -102,74 +111,98 @@ struct RxRow {
   uint2 a, b;
 };
 
+template <bool kHalf>
 __device__ __forceinline__ RxRow rx_load(const __nv_bfloat16* row, const RxLane& l) {
   RxRow r;
-  r.a = __ldcs(reinterpret_cast<const uint2*>(row + l.off0));
-  r.b = __ldcs(reinterpret_cast<const uint2*>(row + l.off1));
+  if (kHalf) {
+    r.a = __ldcs(reinterpret_cast<const uint2*>(row + l.off0));
+    r.b = __ldcs(reinterpret_cast<const uint2*>(row + l.off1));
+  } else {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(row + l.off0));
+    r.a = make_uint2(u.x, u.y);
+    r.b = make_uint2(u.z, u.w);
+  }
   return r;
 }
 
-__device__ __forceinline__ void rx_store(__nv_bfloat16* row, const RxLane& l, const float2 (&v)[4]) {
-  *reinterpret_cast<uint2*>(row + l.off0) = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
-  *reinterpret_cast<uint2*>(row + l.off1) = make_uint2(pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
-}
-
-__device__ __forceinline__ void rx_unpack(const RxRow& r, float2 (&v)[4]) {
-  v[0] = bf2(r.a.x);
-  v[1] = bf2(r.a.y);
-  v[2] = bf2(r.b.x);
-  v[3] = bf2(r.b.y);
-}
-
-// Turns 8 channels: v[p] = v[p] * c[p] + partner * s[p].  The partner of pair p is
-// v[p ^ 2] ("half") or v[p] with its halves swapped ("interleaved"); signs and any
-// factors are in the coefficients.
+// The 8 channels as four packed values: v[0], v[1] the first channels of the thread's
+// pairs 0, 1 and 2, 3, v[2], v[3] their second channels, for either layout.
 template <bool kHalf>
+__device__ __forceinline__ void rx_unpack(const RxRow& r, float2 (&v)[4]) {
+  const float2 a = bf2(r.a.x), b = bf2(r.a.y), c = bf2(r.b.x), d = bf2(r.b.y);
+  if (kHalf) {
+    v[0] = a;
+    v[1] = b;
+    v[2] = c;
+    v[3] = d;
+  } else {
+    v[0] = make_float2(a.x, b.x);
+    v[1] = make_float2(c.x, d.x);
+    v[2] = make_float2(a.y, b.y);
+    v[3] = make_float2(c.y, d.y);
+  }
+}
+
+template <bool kHalf>
+__device__ __forceinline__ void rx_store(__nv_bfloat16* row, const RxLane& l, const float2 (&v)[4]) {
+  if (kHalf) {
+    *reinterpret_cast<uint2*>(row + l.off0) = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
+    *reinterpret_cast<uint2*>(row + l.off1) = make_uint2(pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+  } else {
+    *reinterpret_cast<uint4*>(row + l.off0) =
+        make_uint4(pack_bf16x2(v[0].x, v[2].x), pack_bf16x2(v[0].y, v[2].y),
+                   pack_bf16x2(v[1].x, v[3].x), pack_bf16x2(v[1].y, v[3].y));
+  }
+}
+
+// Turns the 8 channels: v[p] = v[p] * c[p] + v[p ^ 2] * s[p]; signs and any factors
+// are in the coefficients.
 __device__ __forceinline__ void rx_turn(float2 (&v)[4], const float2 (&c)[4], const float2 (&s)[4]) {
   float2 o[4];
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const float2 q = kHalf ? v[p ^ 2] : make_float2(v[p].y, v[p].x);
-    o[p] = __ffma2_rn(v[p], c[p], __fmul2_rn(q, s[p]));
-  }
+  for (int p = 0; p < 4; ++p) o[p] = __ffma2_rn(v[p], c[p], __fmul2_rn(v[p ^ 2], s[p]));
 #pragma unroll
   for (int p = 0; p < 4; ++p) v[p] = o[p];
 }
 
 // Coefficients of one token: cos and +-sin (dir = 1 forward, -1 back), each times
 // the factor w of the value it multiplies (w = 1 + weight, or all ones).
-template <bool kHalf>
 __device__ __forceinline__ void rx_coefficients(const float* tab, int half, const RxLane& l,
                                                 const float2 (&w)[4], float dir, float2 (&c)[4],
                                                 float2 (&s)[4]) {
-  if (!l.rot) {
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      c[p] = w[p];
-      s[p] = make_float2(0.f, 0.f);
-    }
-    return;
+  float4 cv = make_float4(1.f, 1.f, 1.f, 1.f), sv = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (l.rot) {
+    cv = *reinterpret_cast<const float4*>(tab + l.pair);
+    sv = *reinterpret_cast<const float4*>(tab + half + l.pair);
   }
-  const float4 cv = *reinterpret_cast<const float4*>(tab + l.pair);
-  const float4 sv = *reinterpret_cast<const float4*>(tab + half + l.pair);
-  if (kHalf) {
-    const float2 c2[2] = {make_float2(cv.x, cv.y), make_float2(cv.z, cv.w)};
-    const float2 s2[2] = {make_float2(dir * sv.x, dir * sv.y), make_float2(dir * sv.z, dir * sv.w)};
+  const float2 c2[2] = {make_float2(cv.x, cv.y), make_float2(cv.z, cv.w)};
+  const float2 s2[2] = {make_float2(dir * sv.x, dir * sv.y), make_float2(dir * sv.z, dir * sv.w)};
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      c[p] = __fmul2_rn(w[p], c2[p & 1]);
-      const float2 t = __fmul2_rn(w[p ^ 2], s2[p & 1]);
-      s[p] = p < 2 ? make_float2(-t.x, -t.y) : t;
-    }
-  } else {
-    const float ce[4] = {cv.x, cv.y, cv.z, cv.w};
-    const float se[4] = {dir * sv.x, dir * sv.y, dir * sv.z, dir * sv.w};
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      c[p] = make_float2(w[p].x * ce[p], w[p].y * ce[p]);
-      s[p] = make_float2(-w[p].y * se[p], w[p].x * se[p]);
-    }
+  for (int p = 0; p < 4; ++p) {
+    c[p] = __fmul2_rn(w[p], c2[p & 1]);
+    const float2 t = __fmul2_rn(w[p ^ 2], s2[p & 1]);
+    s[p] = p < 2 ? make_float2(-t.x, -t.y) : t;
   }
+}
+
+// Sums of four values over the D / 8 lanes of a row, in every lane: two exchanges
+// halve what a lane carries, so that the four cost 10 shuffles and not 20 (32 lanes).
+template <int kLpr>
+__device__ __forceinline__ void rx_sum4(float& a, float& b, float& c, float& d) {
+  const int lane = threadIdx.x & 31;
+  const bool hi = lane & (kLpr / 2), odd = lane & (kLpr / 4);
+  float x = hi ? c : a, y = hi ? d : b;            // what this lane keeps
+  x += __shfl_xor_sync(0xffffffffu, hi ? a : c, kLpr / 2);
+  y += __shfl_xor_sync(0xffffffffu, hi ? b : d, kLpr / 2);
+  float z = odd ? y : x;
+  z += __shfl_xor_sync(0xffffffffu, odd ? x : y, kLpr / 4);
+#pragma unroll
+  for (int m = kLpr / 8; m >= 1; m >>= 1) z += __shfl_xor_sync(0xffffffffu, z, m);
+  const int base = lane & ~(kLpr - 1);
+  a = __shfl_sync(0xffffffffu, z, base);
+  b = __shfl_sync(0xffffffffu, z, base + kLpr / 4);
+  c = __shfl_sync(0xffffffffu, z, base + kLpr / 2);
+  d = __shfl_sync(0xffffffffu, z, base + 3 * kLpr / 4);
 }
 
 }  // namespace
@@ -180,10 +213,12 @@ __device__ __forceinline__ void rx_coefficients(const float* tab, int half, cons
 // packed pairs of fp32: the kernel would be bound by instruction issue otherwise
 // (162 instructions per warp and row took 112 us for 16,384 tokens x 64 heads).
 template <int D, bool kNorm, bool kHalf>
-__global__ void __launch_bounds__(kRxThreads, 7) rope_ex_kernel(const RxArgs a, const RxTurns turns) {
+__global__ void __launch_bounds__(kRxThreads, 8) rope_ex_kernel(const RxArgs a, const RxTurns turns) {
   pdl_enter();
   constexpr int kLpr = D / 8, kSlots = kRxThreads / kLpr;
   __shared__ __align__(16) float table[2 * kRxMaxAngles];
+  __shared__ int pos[kRxMaxAngles / 8];
+  __shared__ unsigned long long freq[kRxMaxPairs];
   const long long r0 = static_cast<long long>(blockIdx.x) * a.run;
   const int n = static_cast<int>(a.rows - r0 < a.run ? a.rows - r0 : a.run);
   const int t0 = static_cast<int>(r0 / a.H);
@@ -197,7 +232,7 @@ __global__ void __launch_bounds__(kRxThreads, 7) rope_ex_kernel(const RxArgs a, 
   RxRow raw[kDeep];
   auto fetch = [&](int i, RxRow& r) {
     r.a = r.b = make_uint2(0u, 0u);
-    if (i < n) r = rx_load(xb + static_cast<size_t>(i) * D, l);
+    if (i < n) r = rx_load<kHalf>(xb + static_cast<size_t>(i) * D, l);
   };
 #pragma unroll
   for (int k = 0; k < kDeep - 1; ++k) fetch(k * kSlots + slot, raw[k]);
@@ -209,11 +244,11 @@ __global__ void __launch_bounds__(kRxThreads, 7) rope_ex_kernel(const RxArgs a, 
     RxRow wr;
     wr.a = *reinterpret_cast<const uint2*>(a.w + l.off0);
     wr.b = *reinterpret_cast<const uint2*>(a.w + l.off1);
-    rx_unpack(wr, wv);
+    rx_unpack<kHalf>(wr, wv);
 #pragma unroll
     for (int p = 0; p < 4; ++p) w1[p] = __fadd2_rn(wv[p], w1[p]);
   }
-  rx_angles(a, turns, t0, ntok, table);
+  rx_angles(a, turns, t0, ntok, freq, pos, table);
   __syncthreads();
   int have = -1;
   float2 cc[4], ss[4];
@@ -225,7 +260,7 @@ __global__ void __launch_bounds__(kRxThreads, 7) rope_ex_kernel(const RxArgs a, 
       const int i = base + k * kSlots + slot;
       fetch(i + (kDeep - 1) * kSlots, raw[(k + kDeep - 1) % kDeep]);
       float2 v[4];
-      rx_unpack(raw[k], v);
+      rx_unpack<kHalf>(raw[k], v);
       float2 rr = make_float2(1.f, 1.f);
       if (kNorm) {
         float2 q = __fmul2_rn(v[0], v[0]);
@@ -240,25 +275,29 @@ __global__ void __launch_bounds__(kRxThreads, 7) rope_ex_kernel(const RxArgs a, 
         const int tok = static_cast<int>((static_cast<uint32_t>(h0 + i) * a.inv) >> 20);
         if (tok != have) {
           have = tok;
-          rx_coefficients<kHalf>(table + tok * a.R, a.R >> 1, l, w1, 1.f, cc, ss);
+          rx_coefficients(table + tok * a.R, a.R >> 1, l, w1, 1.f, cc, ss);
         }
-        rx_turn<kHalf>(v, cc, ss);
+        rx_turn(v, cc, ss);
         if (kNorm) {
 #pragma unroll
           for (int p = 0; p < 4; ++p) v[p] = __fmul2_rn(v[p], rr);
         }
-        rx_store(yb + static_cast<size_t>(i) * D, l, v);
+        rx_store<kHalf>(yb + static_cast<size_t>(i) * D, l, v);
       }
     }
   }
 }
 
+// Two rows at a time, the next two rows' loads in flight: their reductions share
+// shuffles and their chains overlap.
 template <int D, bool kNorm, bool kHalf>
-__global__ void __launch_bounds__(kRxThreads, 5) rope_ex_bwd_kernel(const RxArgs a,
+__global__ void __launch_bounds__(kRxThreads, 4) rope_ex_bwd_kernel(const RxArgs a,
                                                                     const RxTurns turns) {
   pdl_enter();
   constexpr int kLpr = D / 8, kSlots = kRxThreads / kLpr;
   __shared__ __align__(16) float table[2 * kRxMaxAngles];
+  __shared__ int pos[kRxMaxAngles / 8];
+  __shared__ unsigned long long freq[kRxMaxPairs];
   const int c = threadIdx.x & (kLpr - 1), slot = threadIdx.x / kLpr;
   const RxLane l = rx_lane<kHalf>(c, a.R);
   float2 one[4], w1[4], aw[4];
@@ -271,11 +310,10 @@ __global__ void __launch_bounds__(kRxThreads, 5) rope_ex_bwd_kernel(const RxArgs
     RxRow wr;
     wr.a = *reinterpret_cast<const uint2*>(a.w + l.off0);
     wr.b = *reinterpret_cast<const uint2*>(a.w + l.off1);
-    rx_unpack(wr, w1);
+    rx_unpack<kHalf>(wr, w1);
 #pragma unroll
     for (int p = 0; p < 4; ++p) w1[p] = __fadd2_rn(w1[p], one[p]);
   }
-  constexpr int kDeep = 3;
   for (long long r0 = static_cast<long long>(blockIdx.x) * a.run; r0 < a.rows;
        r0 += static_cast<long long>(gridDim.x) * a.run) {
     const int n = static_cast<int>(a.rows - r0 < a.run ? a.rows - r0 : a.run);
@@ -285,76 +323,86 @@ __global__ void __launch_bounds__(kRxThreads, 5) rope_ex_bwd_kernel(const RxArgs
     const __nv_bfloat16* gb = a.dy + r0 * D;
     const __nv_bfloat16* xb = kNorm ? a.x + r0 * D : nullptr;
     __nv_bfloat16* ob = a.y + r0 * D;
-    RxRow rg[kDeep], rx[kDeep];
-    auto fetch = [&](int i, RxRow& g, RxRow& x) {
-      g.a = g.b = x.a = x.b = make_uint2(0u, 0u);
-      if (i < n) {
-        g = rx_load(gb + static_cast<size_t>(i) * D, l);
-        if (kNorm) x = rx_load(xb + static_cast<size_t>(i) * D, l);
+    struct Pair {
+      RxRow g[2], x[2];
+    };
+    auto fetch = [&](int i, Pair& q) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int ik = i + k * kSlots;
+        q.g[k].a = q.g[k].b = q.x[k].a = q.x[k].b = make_uint2(0u, 0u);
+        if (ik < n) {
+          q.g[k] = rx_load<kHalf>(gb + static_cast<size_t>(ik) * D, l);
+          if (kNorm) q.x[k] = rx_load<kHalf>(xb + static_cast<size_t>(ik) * D, l);
+        }
       }
     };
-#pragma unroll
-    for (int k = 0; k < kDeep - 1; ++k) fetch(k * kSlots + slot, rg[k], rx[k]);
+    Pair now, next;
+    fetch(slot, now);
     __syncthreads();                              // the previous run's angles are consumed
-    rx_angles(a, turns, t0, ntok, table);
+    rx_angles(a, turns, t0, ntok, freq, pos, table);
     __syncthreads();
     int have = -1;
     float2 cc[4], ss[4];
-    for (int base = 0; base < n; base += kDeep * kSlots) {
+    for (int base = 0; base < n; base += 2 * kSlots) {   // uniform over the CTA
+      const int i = base + slot;
+      fetch(i + 2 * kSlots, next);
+      float2 dz[2][4], xv[2][4], g[2][4];
+      float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-      for (int k = 0; k < kDeep; ++k) {
-        if (base + k * kSlots >= n) break;
-        const int i = base + k * kSlots + slot;
-        fetch(i + (kDeep - 1) * kSlots, rg[(k + kDeep - 1) % kDeep], rx[(k + kDeep - 1) % kDeep]);
-        float2 dz[4];
-        rx_unpack(rg[k], dz);
-        const int ii = i < n ? i : n - 1;
-        const int tok = static_cast<int>((static_cast<uint32_t>(h0 + ii) * a.inv) >> 20);
+      for (int k = 0; k < 2; ++k) {
+        rx_unpack<kHalf>(now.g[k], dz[k]);
+        const int ik = i + k * kSlots < n ? i + k * kSlots : n - 1;
+        const int tok = static_cast<int>((static_cast<uint32_t>(h0 + ik) * a.inv) >> 20);
         if (tok != have) {
           have = tok;
-          rx_coefficients<kHalf>(table + tok * a.R, a.R >> 1, l, one, -1.f, cc, ss);
+          rx_coefficients(table + tok * a.R, a.R >> 1, l, one, -1.f, cc, ss);
         }
-        rx_turn<kHalf>(dz, cc, ss);
+        rx_turn(dz[k], cc, ss);
         if (kNorm) {
-          // r = rsqrt(mean(x^2) + eps), dot = sum(g x):
-          // dx = r g - x (r^3 dot / D), dw += dz x r
-          float2 xv[4], g[4];
-          rx_unpack(rx[k], xv);
+          rx_unpack<kHalf>(now.x[k], xv[k]);
           float2 q = make_float2(0.f, 0.f), d = q;
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
-            g[p] = __fmul2_rn(dz[p], w1[p]);
-            q = __ffma2_rn(xv[p], xv[p], q);
-            d = __ffma2_rn(g[p], xv[p], d);
+            g[k][p] = __fmul2_rn(dz[k][p], w1[p]);
+            q = __ffma2_rn(xv[k][p], xv[k][p], q);
+            d = __ffma2_rn(g[k][p], xv[k][p], d);
           }
-          float2 sums = make_float2(q.x + q.y, d.x + d.y);
+          sum[k][0] = q.x + q.y;
+          sum[k][1] = d.x + d.y;
+        }
+      }
+      if (kNorm) rx_sum4<kLpr>(sum[0][0], sum[0][1], sum[1][0], sum[1][1]);
 #pragma unroll
-          for (int m = kLpr / 2; m >= 1; m >>= 1)
-            sums = __fadd2_rn(sums, make_float2(__shfl_xor_sync(0xffffffffu, sums.x, m),
-                                                __shfl_xor_sync(0xffffffffu, sums.y, m)));
-          const float r = rsqrtf(sums.x * (1.f / D) + a.eps);
-          const float k2 = -(r * r) * (r * (sums.y * (1.f / D)));
+      for (int k = 0; k < 2; ++k) {
+        if (i + k * kSlots >= n) break;
+        if (kNorm) {
+          // r = rsqrt(mean(x^2) + eps), dot = sum(g x):
+          // dx = r g - x (r^3 dot / D), dw += dz x r
+          const float r = rsqrtf(sum[k][0] * (1.f / D) + a.eps);
+          const float k2 = -(r * r) * (r * (sum[k][1] * (1.f / D)));
           const float2 rr = make_float2(r, r), kk = make_float2(k2, k2);
-          if (i < n) {
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              aw[p] = __ffma2_rn(__fmul2_rn(dz[p], rr), xv[p], aw[p]);
-              dz[p] = __ffma2_rn(xv[p], kk, __fmul2_rn(g[p], rr));
-            }
+          for (int p = 0; p < 4; ++p) {
+            aw[p] = __ffma2_rn(__fmul2_rn(dz[k][p], rr), xv[k][p], aw[p]);
+            dz[k][p] = __ffma2_rn(xv[k][p], kk, __fmul2_rn(g[k][p], rr));
           }
         }
-        if (i < n) rx_store(ob + static_cast<size_t>(i) * D, l, dz);
+        rx_store<kHalf>(ob + static_cast<size_t>(i + k * kSlots) * D, l, dz[k]);
       }
+      now = next;
     }
   }
   if (kNorm) {
     // the CTA's row slots, added in slot order -> one partial row
     __syncthreads();
     float* red = table;                            // [kSlots][D]: 4 KB
+    const float av[8] = {aw[0].x, aw[0].y, aw[1].x, aw[1].y, aw[2].x, aw[2].y, aw[3].x, aw[3].y};
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int ch = (p < 2 ? l.off0 : l.off1) + 2 * (p & 1);
-      *reinterpret_cast<float2*>(red + slot * D + ch) = aw[p];
+    for (int e = 0; e < 8; ++e) {
+      // channel of the thread's e-th value (rx_unpack)
+      const int ch = kHalf ? (e < 4 ? l.off0 + e : l.off1 + e - 4) : l.off0 + 2 * (e & 3) + (e >> 2);
+      red[slot * D + ch] = av[e];
     }
     __syncthreads();
     for (int ch = threadIdx.x; ch < D; ch += kRxThreads) {
@@ -368,7 +416,7 @@ __global__ void __launch_bounds__(kRxThreads, 5) rope_ex_bwd_kernel(const RxArgs
 // dw[ch] = the partial rows in a fixed order: thread (k, ch) adds rows k,
 // k + 128, ... (all its loads in flight), then a pairwise tree over k.
 constexpr int kRxSumCh = 8, kRxSumWays = 128;
-constexpr int kRxBwdCtas = 760;                    // 5 per SM, all resident
+constexpr int kRxBwdCtas = 608;                    // 4 per SM, all resident
 constexpr int kRxSumRows = (kRxBwdCtas + kRxSumWays - 1) / kRxSumWays;
 __global__ void __launch_bounds__(kRxSumCh * kRxSumWays)
     rope_ex_dw_kernel(const float* __restrict__ part, int nparts, int D, float* __restrict__ dw) {
@@ -397,15 +445,37 @@ __global__ void __launch_bounds__(kRxSumCh * kRxSumWays)
 
 // ---------------------------------------------------------------- host
 
-// Rows per CTA: `target` rows, fewer when the run's tokens would not fit the
-// angle table.  A run of n rows touches at most (n + 2 H - 2) / H tokens.
-static int rx_run(int H, int R, int target) {
+// Rows per run: about `target`, whole tokens where they fit (a token cut in two has
+// its angles computed twice), fewer when the run's tokens would not fit the angle
+// table.  A run of n rows touches at most (n + 2 H - 2) / H tokens.
+static int rx_run(int H, int R, long long target) {
   const int cap_tok = kRxMaxAngles / (R / 2);            // >= 16
   const long long cap = static_cast<long long>(cap_tok - 1) * H;
-  return static_cast<int>(cap < target ? cap : target);
+  if (target > cap) target = cap;
+  if (target > 512) target = 512;
+  return static_cast<int>(target > H ? target / H * H : target);
 }
 
-constexpr int kRxFwdRun = 128, kRxBwdRun = 128;
+constexpr int kRxRun = 128;         // backward
+constexpr int kRxFwdRun = 64;       // forward, when there are rows enough
+
+// Forward: 64 rows per CTA (128 cost small calls 1.4 us and gain nothing), fewer
+// when that would leave SMs without a CTA, 16 at least.
+static int rx_fwd_run(long long rows, int H, int R) {
+  long long run = rows / (2 * device_sm_count());
+  run = run < 16 ? 16 : (run > kRxFwdRun ? kRxFwdRun : run);
+  return rx_run(H, R, run);
+}
+
+// Backward: the resident CTAs share the rows evenly, each in runs of at most 128
+// rows or so.
+static int rx_bwd_run(long long rows, int H, int R) {
+  const long long share = (rows + kRxBwdCtas - 1) / kRxBwdCtas;
+  const long long parts = (share + kRxRun - 1) / kRxRun;
+  long long run = (share + parts - 1) / parts;
+  if (run > H) run = (run + H - 1) / H * H;              // whole tokens, rounded up
+  return rx_run(H, R, run);
+}
 
 static int rx_bwd_ctas(long long rows, int run) {
   const long long n = (rows + run - 1) / run;
@@ -445,6 +515,7 @@ static RxArgs rx_args(const RopeExJob& j, const msa_rope_t& rope) {
   a.S = j.S;
   a.R = rope.dim;
   a.inv = ((1u << 20) + j.H - 1) / j.H;
+  a.inv_half = ((1u << 20) + rope.dim / 2 - 1) / (rope.dim / 2);
   a.eps = j.eps;
   a.gain = rope.gain;
   return a;
@@ -453,7 +524,7 @@ static RxArgs rx_args(const RopeExJob& j, const msa_rope_t& rope) {
 template <int D>
 static msa_status_t rx_forward(const RopeExJob& j, const msa_rope_t& rope, cudaStream_t stream) {
   RxArgs a = rx_args(j, rope);
-  a.run = rx_run(j.H, rope.dim, kRxFwdRun);
+  a.run = rx_fwd_run(a.rows, j.H, rope.dim);
   const RxTurns turns = rx_turns(rope);
   const unsigned grid = static_cast<unsigned>((a.rows + a.run - 1) / a.run);
   TraceScope trace_("rope_ex_kernel", stream);
@@ -468,7 +539,7 @@ template <int D>
 static msa_status_t rx_backward(const RopeExJob& j, const msa_rope_t& rope, float* dw,
                                 float* dw_part, cudaStream_t stream) {
   RxArgs a = rx_args(j, rope);
-  a.run = rx_run(j.H, rope.dim, kRxBwdRun);
+  a.run = rx_bwd_run(a.rows, j.H, rope.dim);
   a.dw_part = dw_part;
   const RxTurns turns = rx_turns(rope);
   const int ctas = rx_bwd_ctas(a.rows, a.run);
