@@ -272,24 +272,39 @@ constexpr int kAtThreads = 32 * kAtWarps;
 constexpr int kKeysPerWarp = kBlock / kAtWarps;
 constexpr float kAtRescale = 8.0f;  // log2 of the largest weight before a rescale (fp16: below 2^16)
 
-template <int NS>
+// A warp's 32 keys of a block, as they lie in the slabs
+struct Attend4Keys {
+  alignas(16) uint8_t k[kKeysPerWarp * kCodeBytes];
+  alignas(16) uint8_t ks[kKeysPerWarp * kScaleBytes];
+  alignas(16) uint8_t v[kKeysPerWarp * kCodeBytes];
+  alignas(16) uint8_t vs[kKeysPerWarp * kScaleBytes];
+};
+
+// kWhole: the CTA's slabs all at once, asked for by warp 0 as soon as it knows the
+// blocks; three CTAs fit an SM.  Otherwise each warp streams its keys through two
+// buffers of its own; four CTAs fit.
+template <int NS, bool kWhole_>
 struct Attend4Smem {
   static constexpr int kBlocks = kTopK / NS;       // blocks per CTA
+  static constexpr bool kWhole = kWhole_;
+  static constexpr int kStages = 2;
   union {
     struct {
-      alignas(16) uint8_t k[kBlocks][kSlab];
-      alignas(16) uint8_t v[kBlocks][kSlab];
-    } s;
-    alignas(16) float o[kAtWarps][16][kD];         // per warp once the slabs are used, then [0]
+      alignas(16) uint8_t k[kWhole ? kBlocks : 1][kSlab];
+      alignas(16) uint8_t v[kWhole ? kBlocks : 1][kSlab];
+    } whole;
+    Attend4Keys s[kWhole ? 1 : kAtWarps][kStages];
+    alignas(16) float o[kAtWarps][16][kD];         // per warp once the keys are used, then [0]
                                                    // = the CTA's sum
   };
+  alignas(16) uint4 qa[8][32];                     // A operand of the 8 k-steps, per lane
   float ml[kAtWarps][16][2];
   float cta_ml[16][2];
   unsigned long long gmax[32];                     // selection: best key of each group of threads
   int list[kTopK];                                 // selected blocks, -1 behind
   int page[kBlocks];
   int ncand;
-  uint64_t full[kBlocks];
+  uint64_t full[kAtWarps][kStages];                // whole slabs: the first kBlocks of them
 };
 
 // Float4 `chunk` (channel / 4) of row r in a [16][128] array of sums: permuted so
@@ -341,8 +356,8 @@ __device__ __forceinline__ float ex2(float x) {
 // O = P V: thread (g, c) reads 8 bytes of codes = scale block g of a key, column
 // g of n-tile i is channel 16 g + i.  Keys behind the sequence's end have P = 0 and
 // scale 0, whatever their slots hold.
-template <int NS>
-__global__ void __launch_bounds__(kAtThreads, 3) decode4_attend_kernel(
+template <int NS, bool kWhole>
+__global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_kernel(
     const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ kc,
     const uint8_t* __restrict__ vc, const int32_t* __restrict__ table,
     const int32_t* __restrict__ lens, const float* __restrict__ scores, int G, int Hkv,
@@ -350,7 +365,7 @@ __global__ void __launch_bounds__(kAtThreads, 3) decode4_attend_kernel(
     int32_t* __restrict__ sel_out, uint32_t* status) {
   pdl_enter();
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  using Smem = Attend4Smem<NS>;
+  using Smem = Attend4Smem<NS, kWhole>;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   constexpr int kBlocks = Smem::kBlocks;
   const int split = blockIdx.x, bh = blockIdx.y, b = bh / Hkv, h = bh % Hkv;
@@ -369,8 +384,9 @@ __global__ void __launch_bounds__(kAtThreads, 3) decode4_attend_kernel(
   }
   // q as the A operand of the 8 k-steps: rows g and g + 8 in fp16, each with a power
   // of two; thread c of a row has channels 32 c .. 32 c + 31
-  uint32_t qa[8][4];
   float f0, f1;
+  {
+  uint32_t qa[8][4];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int r = g + 8 * half;
@@ -400,11 +416,16 @@ __global__ void __launch_bounds__(kAtThreads, 3) decode4_attend_kernel(
       qa[2 * i + 1][2 + half] = bf2_to_h2(x[i].w, f);
     }
   }
+  // every warp has all of it; each stores two k-steps
+#pragma unroll
+  for (int t = 0; t < 8; ++t)
+    if (t >> 1 == warp) sm.qa[t][lane] = make_uint4(qa[t][0], qa[t][1], qa[t][2], qa[t][3]);
+  }
   const int L = d4_len(len, max_pages, status);
   const int nblk = (L + kBlock - 1) / kBlock;
   const int own = nblk - 1;
-  if (tid < kBlocks) {
-    mbar_init(&sm.full[tid], 1);
+  if (lane == 0) {
+    for (int i = 0; i < Smem::kStages; ++i) mbar_init(&sm.full[warp][i], 1);
     fence_mbar_init();
   }
   if (tid == 0) sm.ncand = 0;
@@ -457,7 +478,7 @@ __global__ void __launch_bounds__(kAtThreads, 3) decode4_attend_kernel(
     sm.list[tid] = tid < nblk ? tid : -1;          // every block
   }
   __syncwarp();
-  // ---- warp 0: this CTA's blocks, all K and V slabs on their way at once
+  // ---- warp 0: this CTA's blocks
   if (warp == 0) {
     if (lane < kBlocks) {
       const int blk = sm.list[split + NS * lane];
@@ -470,12 +491,12 @@ __global__ void __launch_bounds__(kAtThreads, 3) decode4_attend_kernel(
         }
       }
       sm.page[lane] = pg;
-      if (pg >= 0) {
+      if (kWhole && pg >= 0) {
         const size_t off = (static_cast<size_t>(pg) * Hkv + h) * kSlab;
         fence_proxy_async_smem();                  // the slabs lie over the candidates
-        mbar_arrive_expect_tx(&sm.full[lane], 2 * kSlab);
-        bulk_load(sm.s.k[lane], kc + off, kSlab, &sm.full[lane]);
-        bulk_load(sm.s.v[lane], vc + off, kSlab, &sm.full[lane]);
+        mbar_arrive_expect_tx(&sm.full[0][0] + lane, 2 * kSlab);
+        bulk_load(sm.whole.k[lane], kc + off, kSlab, &sm.full[0][0] + lane);
+        bulk_load(sm.whole.v[lane], vc + off, kSlab, &sm.full[0][0] + lane);
       }
     }
     if (split == 0 && lane < kTopK && sel_out) {   // ascending, -1 last
@@ -489,38 +510,82 @@ __global__ void __launch_bounds__(kAtThreads, 3) decode4_attend_kernel(
       sel_out[static_cast<size_t>(bh) * kTopK + at] = static_cast<int>(me);
     }
   }
-  __syncthreads();                                 // blocks and pages are known to every warp
+  __syncthreads();                                 // blocks, pages and q are known to every warp
+  // ---- each warp takes its 32 keys of the CTA's blocks
+  const int kw = kKeysPerWarp * warp;              // this warp's first key
+  int my_page = -1, my_keys = 0;                   // lane i: block i's page and its valid keys of mine
+  if (lane < kBlocks) {
+    my_page = sm.page[lane];
+    const int n = (sm.list[split + NS * lane] == own ? L - own * kBlock : kBlock) - kw;
+    my_keys = my_page < 0 ? 0 : max(0, min(n, kKeysPerWarp));
+  }
+  uint32_t todo = __ballot_sync(0xffffffffu, my_keys > 0), ask = todo;
+  const size_t head = static_cast<size_t>(h) * kSlab, row = static_cast<size_t>(Hkv) * kSlab;
+  uint32_t nload = 0, nuse = 0;
+  bool dead = false;                               // a wait ran out
+  auto load = [&]() {                              // the next block's keys, K and V
+    if (kWhole || ask == 0u) return;
+    const int pg = __shfl_sync(0xffffffffu, my_page, __ffs(ask) - 1);
+    if (lane == 0) {
+      const int st = nload % Smem::kStages;
+      Attend4Keys& d = sm.s[warp][st];
+      const size_t off = pg * row + head;
+      mbar_arrive_expect_tx(&sm.full[warp][st], sizeof(Attend4Keys));
+      bulk_load(d.k, kc + off + slab_code(kw), sizeof(d.k), &sm.full[warp][st]);
+      bulk_load(d.ks, kc + off + slab_scale(kw), sizeof(d.ks), &sm.full[warp][st]);
+      bulk_load(d.v, vc + off + slab_code(kw), sizeof(d.v), &sm.full[warp][st]);
+      bulk_load(d.vs, vc + off + slab_scale(kw), sizeof(d.vs), &sm.full[warp][st]);
+    }
+    ++nload;
+    ask &= ask - 1u;
+  };
+  if (lane == 0) fence_proxy_async_smem();         // the buffers lie over the candidates
+  for (int i = 0; i < Smem::kStages; ++i) load();
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
   float acc[16][4];
 #pragma unroll
   for (int nt = 0; nt < 16; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
 
 #pragma unroll 1
-  for (int i = 0; i < kBlocks; ++i) {
-    if (sm.page[i] < 0) continue;                  // uniform over the CTA
-    const int nvalid = sm.list[split + NS * i] == own ? L - own * kBlock : kBlock;
-    const int kw = kKeysPerWarp * warp;            // this warp's first key
-    if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[i], 0, status, 80))) {
-      for (int j = i + 1; j < kBlocks; ++j)        // wait (bounded) for what is on its way, leave
-        if (sm.page[j] >= 0) (void)mbar_wait(&sm.full[j], 0, status, 83);
+  for (; todo; todo &= todo - 1u) {                // uniform over the warp
+    const int i = __ffs(todo) - 1;
+    const int nvalid = __shfl_sync(0xffffffffu, my_keys, i);
+    const int st = nuse % Smem::kStages;
+    uint64_t* full = kWhole ? &sm.full[0][0] + i : &sm.full[warp][st];
+    if (!__all_sync(0xffffffffu, mbar_wait(full, kWhole ? 0 : (nuse / Smem::kStages) & 1, status, 80))) {
+      dead = true;
       break;
     }
-    if (kw >= nvalid) continue;                    // uniform over the warp
+    ++nuse;
+    const uint8_t *dk, *dks, *dv, *dvs;            // this warp's keys
+    if (kWhole) {
+      dk = sm.whole.k[i] + slab_code(kw);
+      dks = sm.whole.k[i] + slab_scale(kw);
+      dv = sm.whole.v[i] + slab_code(kw);
+      dvs = sm.whole.v[i] + slab_scale(kw);
+    } else {
+      const Attend4Keys& d = sm.s[warp][st];
+      dk = d.k;
+      dks = d.ks;
+      dv = d.v;
+      dvs = d.vs;
+    }
     // ---- S: four n-tiles side by side, so that four chains of products overlap
     float s[4][4];
     uint4 w4[4];
     __half2 ksc[4];
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-      const int key = kw + 8 * nt + (g >> 1) + 4 * (g & 1);
-      w4[nt] = *(reinterpret_cast<const uint4*>(sm.s.k[i] + slab_code(key)) + c);
-      const uint32_t two = *(reinterpret_cast<const uint16_t*>(sm.s.k[i] + slab_scale(key)) + c);
+      const int key = 8 * nt + (g >> 1) + 4 * (g & 1);
+      w4[nt] = *(reinterpret_cast<const uint4*>(dk + kCodeBytes * key) + c);
+      const uint32_t two = *(reinterpret_cast<const uint16_t*>(dks + kScaleBytes * key) + c);
       ksc[nt] = __half2(
           __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3));
       s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {                  // 8 channels: two k-steps
+      const uint4 qa[2] = {sm.qa[2 * j][lane], sm.qa[2 * j + 1][lane]};
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt) {
         const uint32_t w = j == 0 ? w4[nt].x : (j == 1 ? w4[nt].y : (j == 2 ? w4[nt].z : w4[nt].w));
@@ -528,21 +593,19 @@ __global__ void __launch_bounds__(kAtThreads, 3) decode4_attend_kernel(
         codes_half2(w, hh);
         const __half2 s2 = j < 2 ? __low2half2(ksc[nt]) : __high2half2(ksc[nt]);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int t = 2 * j + k;
-          mma_f16_16816(s[nt], qa[t][0], qa[t][1], qa[t][2], qa[t][3],
+        for (int k = 0; k < 2; ++k)
+          mma_f16_16816(s[nt], qa[k].x, qa[k].y, qa[k].z, qa[k].w,
                         h2u(__hmul2(hh[2 * k], s2)), h2u(__hmul2(hh[2 * k + 1], s2)));
-        }
       }
     }
     // ---- mask and running softmax of this warp's keys
     float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-      if (nvalid < kBlock) {
+      if (nvalid < kKeysPerWarp) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const bool ok = kw + 8 * nt + c + 4 * e < nvalid;
+          const bool ok = 8 * nt + c + 4 * e < nvalid;
           s[nt][e] = ok ? s[nt][e] : -INFINITY;
           s[nt][2 + e] = ok ? s[nt][2 + e] : -INFINITY;
         }
@@ -599,9 +662,9 @@ __global__ void __launch_bounds__(kAtThreads, 3) decode4_attend_kernel(
       uint32_t sb[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int key = kw + 16 * kk + c + 4 * r;
-        w[r] = *reinterpret_cast<const uint2*>(sm.s.v[i] + slab_code(key) + 8 * g);
-        sb[r] = key < nvalid ? sm.s.v[i][slab_scale(key) + g] : 0u;
+        const int key = 16 * kk + c + 4 * r;
+        w[r] = *reinterpret_cast<const uint2*>(dv + kCodeBytes * key + 8 * g);
+        sb[r] = key < nvalid ? dvs[kScaleBytes * key + g] : 0u;
       }
       __half2 s2[2];
 #pragma unroll
@@ -627,8 +690,20 @@ __global__ void __launch_bounds__(kAtThreads, 3) decode4_attend_kernel(
         }
       }
     }
+    __syncwarp();                                  // every lane has read the buffer
+    load();
   }
-  __syncthreads();                                 // the slabs make room for the warps' sums
+  // Wait (bounded) for whatever is still on its way: after a wait that ran out, and
+  // for whole slabs in which this warp had no valid keys.
+  if (kWhole) {
+    if (warp == 0)
+      for (int i = 0; i < kBlocks; ++i)
+        if (sm.page[i] >= 0) (void)mbar_wait(&sm.full[0][0] + i, 0, status, 83);
+  } else if (dead) {
+    for (++nuse; nuse < nload; ++nuse)
+      (void)mbar_wait(&sm.full[warp][nuse % Smem::kStages], (nuse / Smem::kStages) & 1, status, 83);
+  }
+  __syncthreads();                                 // the keys make room for the warps' sums
   l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
   l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
   l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
@@ -743,20 +818,20 @@ msa_status_t allow_large_cluster(const void* kernel) {
   return MSA_OK;
 }
 
-template <int NS>
+template <int NS, bool kWhole>
 msa_status_t launch_attend4(const void* q, const void* kc, const void* vc, const int32_t* table,
                             const int32_t* lens, const float* scores, int B, int G, int Hkv,
                             int num_pages, int max_pages, int n_init, float sl2, float v_gain, void* o,
                             int32_t* sel_out, uint32_t* sw, cudaStream_t stream) {
-  const size_t smem = sizeof(Attend4Smem<NS>);
-  MSA_TRY(ensure_smem(decode4_attend_kernel<NS>, smem, "decode4_attend_kernel"));
+  const size_t smem = sizeof(Attend4Smem<NS, kWhole>);
+  MSA_TRY(ensure_smem(decode4_attend_kernel<NS, kWhole>, smem, "decode4_attend_kernel"));
   TraceScope trace_("decode4_attend_kernel", stream);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(NS, static_cast<unsigned>(B) * Hkv);
   cfg.blockDim = kAtThreads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  if (NS > 8) MSA_TRY(allow_large_cluster(reinterpret_cast<const void*>(decode4_attend_kernel<NS>)));
+  if (NS > 8) MSA_TRY(allow_large_cluster(reinterpret_cast<const void*>(decode4_attend_kernel<NS, kWhole>)));
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -766,7 +841,7 @@ msa_status_t launch_attend4(const void* q, const void* kc, const void* vc, const
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaLaunchKernelEx(&cfg, decode4_attend_kernel<NS>, static_cast<const __nv_bfloat16*>(q),
+  cudaLaunchKernelEx(&cfg, decode4_attend_kernel<NS, kWhole>, static_cast<const __nv_bfloat16*>(q),
                      static_cast<const uint8_t*>(kc), static_cast<const uint8_t*>(vc), table, lens,
                      scores, G, Hkv, num_pages, max_pages, n_init, sl2, v_gain,
                      static_cast<__nv_bfloat16*>(o), sel_out, sw);
@@ -837,14 +912,16 @@ msa_status_t msa_decode4_step(const void* q, const void* q_idx, const void* k_ca
     }
     MSA_TRY(check_launch("decode4_score_kernel"));
   }
-  // CTAs per row: as many as still run side by side, 3 per SM (the kernel's
-  // shared memory and registers); more CTAs shorten a row's chain of blocks, fewer repeat
-  // its selection less often.  Attention of 4 rows: 7.0 us with 4, 5.0 with 16; of
-  // 20 rows with up to 1024 blocks: 16.1 with 4, 14.3 with 16; of 66 rows 16.3 with 4, 20.4
-  // with 8; of 256 rows 43 with 4, 70 with 8.
-  const long long rows = static_cast<long long>(B) * Hkv, room = 3LL * device_sm_count();
-  auto attend = rows * 16 <= room ? launch_attend4<16>
-                                  : (rows * 8 <= room ? launch_attend4<8> : launch_attend4<4>);
+  // CTAs per row: 16, 8 or 4, as many as still run side by side with their slabs
+  // whole (3 per SM, 2 with 4 blocks each); more CTAs shorten a row's chain of blocks.
+  // Beyond that the rows' work counts, not its latency: 4 CTAs that stream, 4 per SM.
+  // The whole step, 4 short rows: 7.5 us with 4 CTAs, 5.4 with 16; 20 rows of 60k -
+  // 131k tokens 44.4 and 37.3; 66 rows 19.8 with 4 whole, 25.0 streaming, 23.6 with 8;
+  // 256 rows 103.6 with 4 whole, 97.8 streaming, 112 with 8.
+  const long long rows = static_cast<long long>(B) * Hkv, sms = device_sm_count();
+  auto attend = rows * 16 <= 3 * sms ? launch_attend4<16, true>
+                : rows * 8 <= 3 * sms ? launch_attend4<8, true>
+                : rows * 4 <= 2 * sms ? launch_attend4<4, true> : launch_attend4<4, false>;
   return attend(q, k_cache, v_cache, block_table, cache_lens, w.scores, B, G, Hkv, num_pages,
                 max_pages, n_init, scale * k_gain * kLog2e, v_gain, o, sel_out, sw, st);
 }
