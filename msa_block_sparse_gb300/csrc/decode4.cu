@@ -385,7 +385,6 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
   // q as the A operand of the 8 k-steps: rows g and g + 8 in fp16, each with a power
   // of two; thread c of a row has channels 32 c .. 32 c + 31
   float f0, f1;
-  {
   uint32_t qa[8][4];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -420,12 +419,12 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
 #pragma unroll
   for (int t = 0; t < 8; ++t)
     if (t >> 1 == warp) sm.qa[t][lane] = make_uint4(qa[t][0], qa[t][1], qa[t][2], qa[t][3]);
-  }
   const int L = d4_len(len, max_pages, status);
   const int nblk = (L + kBlock - 1) / kBlock;
   const int own = nblk - 1;
-  if (lane == 0) {
-    for (int i = 0; i < Smem::kStages; ++i) mbar_init(&sm.full[warp][i], 1);
+  // by the lanes of warp 0 that use them before the next barrier of the CTA
+  if (tid < kAtWarps * Smem::kStages) {
+    mbar_init(&sm.full[0][0] + tid, 1);
     fence_mbar_init();
   }
   if (tid == 0) sm.ncand = 0;

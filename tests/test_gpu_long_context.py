@@ -416,6 +416,9 @@ def check_decode(m, lens, G, H, seed=0, n_init=0, gains=(1.0, 1.0), max_pages=No
     ((2600, 100), 16, 1, dict(scale=2.0)),
     ((256, 512, 640, 300, 2048), 3, 1, {}),
     ((512,), 16, 1, {}),
+    ((300, 2100, 0, 17, 2048, 640) * 4, 3, 3, {}),        # 72 rows, most of them short
+    ((129, 5000, 1) * 13, 1, 1, {}),                      # 39 rows
+    ((129, 2500, 1) * 27, 2, 1, dict(n_init=2)),          # 81 rows
     ((0, 0), 16, 2, {}),
 ], ids=str)
 def test_decode4(m, lens, G, H, kw):
