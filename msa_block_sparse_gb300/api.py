@@ -1,8 +1,9 @@
-"""Python binding of libmsa.so (ctypes).  Argument marshalling only: every step
-of the computation runs in the library's CUDA kernels.  Function names match
-the C ABI in include/msa.h; tensors are torch CUDA tensors in the layouts that
-header states, outputs and workspaces are allocated here with torch when the
-caller does not pass them, and the work is enqueued on the current stream.
+"""Python binding of libmsa.so (ctypes, and csrc/binding.cpp for the calls of a
+decode loop).  Argument marshalling only: every step of the computation runs in the
+library's CUDA kernels.  Function names match the C ABI in include/msa.h; tensors
+are torch CUDA tensors in the layouts that header states, outputs and workspaces are
+allocated with torch when the caller does not pass them, and the work is enqueued
+on the current stream.
 """
 from __future__ import annotations
 
@@ -520,72 +521,28 @@ def msa_rope(dim: int = 64, base: float = 1.0e7, layout: str = "half", scaling: 
     return r
 
 
-# The newer calls check an argument and take its address in one step: a decode step
-# spends more time in its binding than on the GPU otherwise.
-
-def _dev(t, name: str) -> int:
-    """The current device, which has to be the one that CUDA tensor `t` is on."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    dev = torch.cuda.current_device()
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    return dev
+_binding = None
 
 
-def _arg(t, name: str, dtype, shape, dev: int) -> int:
-    """Address of a contiguous tensor of this type, shape and device, or ValueError."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _req(t, name, dtype, shape)
-    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+def _native():
+    """The native part of the binding (csrc/binding.cpp): argument checks, outputs and
+    the C call in one step.  Raises if it has not been built (there is no fallback)."""
+    global _binding
+    if _binding is None:
+        lib()
+        try:
+            from . import _msa_torch
+        except ImportError as e:
+            raise RuntimeError("the native binding is missing or does not load: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        _binding = _msa_torch
+    return _binding
 
 
-def _opt(t, name: str, dtype, shape, dev: int):
-    return None if t is None else _arg(t, name, dtype, shape, dev)
-
-
-def _scratch(size: int, ws: Optional[torch.Tensor], dev: int):
-    """(address, bytes, tensor) of a workspace of `size` bytes; the tensor keeps it alive."""
-    if ws is None:
-        ws = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
-    elif not isinstance(ws, torch.Tensor) or not ws.is_contiguous() or ws.get_device() != dev:
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
-    n = ws.numel() * ws.element_size()
-    if n < size:
-        raise ValueError(f"workspace needs {size} bytes")
-    return ws.data_ptr(), n, ws
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-_BF, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
-
-
-def _rope_positions(cu_seqlens, positions, T, dev):
-    """(positions, cu_seqlens, S) as the C call takes them."""
-    if (cu_seqlens is None) == (positions is None):
-        raise ValueError("give either cu_seqlens or positions")
-    if positions is not None:
-        return _arg(positions, "positions", _I32, (T,), dev), None, 1
-    cu, S = _cu(cu_seqlens, dev)
-    return None, cu, S
-
-
-def _cu(cu_seqlens, dev):
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-        raise ValueError("cu_seqlens must be a tensor of shape (S + 1,)")
-    n = cu_seqlens.numel()
-    return _arg(cu_seqlens, "cu_seqlens", _I32, (n,), dev), n - 1
-
-
-def _rope_ref(rope):
+def _rope_at(rope) -> int:
     if not isinstance(rope, Rope):
         raise ValueError("rope must come from msa_rope")
-    return ctypes.byref(rope)
+    return ctypes.addressof(rope)
 
 
 def msa_qk_norm_rope_ex(x, w, rope: Rope, cu_seqlens: Optional[torch.Tensor] = None,
@@ -594,19 +551,7 @@ def msa_qk_norm_rope_ex(x, w, rope: Rope, cu_seqlens: Optional[torch.Tensor] = N
     """x bf16 [T, H, D] (D 64, 128 or 256) -> out: gemma RMSNorm with weight w (bf16
     [D]; None: no norm), then the rotation `rope` at positions (int32 [T]) or at the
     tokens' places in cu_seqlens' sequences.  Pass out=x for in place."""
-    dev = _dev(x, "x")
-    shape = x.shape
-    if len(shape) != 3:
-        raise ValueError("x must have shape (T, H, D)")
-    T, H, Dh = shape
-    xp = _arg(x, "x", _BF, shape, dev)
-    wp = _opt(w, "w", _BF, (Dh,), dev)
-    pos, cu, S = _rope_positions(cu_seqlens, positions, T, dev)
-    if out is None:
-        out = torch.empty_like(x)
-    _check(lib().msa_qk_norm_rope_ex(xp, _arg(out, "out", _BF, shape, dev), T, H, Dh, wp, pos, cu, S,
-                                     _rope_ref(rope), eps, _raw_stream(dev)))
-    return out
+    return _native().qk_norm_rope_ex(x, w, _rope_at(rope), cu_seqlens, positions, out, eps)
 
 
 def msa_qk_norm_rope_bwd_ex(x, dy, w, rope: Rope, cu_seqlens: Optional[torch.Tensor] = None,
@@ -615,65 +560,14 @@ def msa_qk_norm_rope_bwd_ex(x, dy, w, rope: Rope, cu_seqlens: Optional[torch.Ten
                             eps: float = 1.0e-6, workspace: Optional[torch.Tensor] = None):
     """Gradients of msa_qk_norm_rope_ex: (dx bf16 [T, H, D], dw fp32 [D]) from its input
     x and dy (pass dx=dy to overwrite dy); with w None (dx, None), and x may be None."""
-    dev = _dev(dy, "dy")
-    shape = dy.shape
-    if len(shape) != 3:
-        raise ValueError("dy must have shape (T, H, D)")
-    T, H, Dh = shape
-    dyp = _arg(dy, "dy", _BF, shape, dev)
-    pos, cu, S = _rope_positions(cu_seqlens, positions, T, dev)
-    if dx is None:
-        dx = torch.empty_like(dy)
-    dxp = _arg(dx, "dx", _BF, shape, dev)
-    xp = wp = dwp = wsp = None
-    nbytes = 0
-    if w is not None:
-        wp = _arg(w, "w", _BF, (Dh,), dev)
-        xp = _arg(x, "x", _BF, shape, dev)
-        if dw is None:
-            dw = torch.empty(Dh, dtype=torch.float32, device=dev)
-        dwp = _arg(dw, "dw", torch.float32, (Dh,), dev)
-        wsp, nbytes, workspace = _scratch(lib().msa_qk_norm_rope_bwd_ex_workspace_size(T, H, Dh),
-                                          workspace, dev)
-    elif dw is not None:
-        raise ValueError("dw needs w")
-    _check(lib().msa_qk_norm_rope_bwd_ex(xp, dyp, dxp, dwp, T, H, Dh, wp, pos, cu, S,
-                                         _rope_ref(rope), eps, wsp, nbytes, _raw_stream(dev)))
-    return dx, dw
+    return _native().qk_norm_rope_bwd_ex(x, dy, w, _rope_at(rope), cu_seqlens, positions, dx, dw, eps,
+                                         workspace)
 
 
 # ------------------------------------------------------------------ 4-bit paged cache
 
 SLAB4 = 9216     # bytes of a page of one head: 128 x 64 of codes, 128 x 8 of scales
-
-
-def _table4(first, block_table, rows):
-    """Shape of the caches (that of `first`) and pages per row of the block table."""
-    if not isinstance(first, torch.Tensor) or first.dim() != 3:
-        raise ValueError("a 4-bit cache must have shape (num_pages, Hkv, 9216)")
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2 \
-            or block_table.shape[0] != rows:
-        raise ValueError(f"block_table must have shape ({rows}, max_pages)")
-    P, Hkv, _ = first.shape
-    return (P, Hkv, SLAB4), block_table.shape[1]
-
-
-def _pack4(kvi, caches, block_table, cu_seqlens, T, start):
-    """The common arguments of store and load: (tensors, caches, table, cu, start, sizes)."""
-    names = ("k", "v", "k_idx")
-    for n, x, c in zip(names, kvi, caches):
-        if (x is None) != (c is None):
-            raise ValueError(f"{n} and its cache must be given together")
-    first = next((c for c in caches if c is not None), None)
-    if first is None:
-        raise ValueError("no cache given")
-    dev = _dev(first, "the cache")
-    cu, S = _cu(cu_seqlens, dev)
-    shape, maxp = _table4(first, block_table, S)
-    xp = [_opt(x, n, _BF, (T, shape[1], D), dev) for n, x in zip(names, kvi)]
-    cp = [_opt(c, n + "_cache", _U8, shape, dev) for n, c in zip(names, caches)]
-    return (dev, xp, cp, _arg(block_table, "block_table", _I32, (S, maxp), dev), cu,
-            _opt(start, "start", _I32, (S,), dev), (S, T, shape[1], shape[0], maxp))
+_SCALE = 1.0 / math.sqrt(D)
 
 
 def msa_cache4_store(k, v, k_idx, k_cache, v_cache, kidx_cache, block_table, cu_seqlens,
@@ -682,13 +576,8 @@ def msa_cache4_store(k, v, k_idx, k_cache, v_cache, kidx_cache, block_table, cu_
     (uint8 [num_pages, Hkv, 9216]): token i of sequence s at position start[s] + i of
     row s of block_table.  k, v or k_idx may be None together with its cache.  gains:
     of k, v and k_idx, powers of two; the same ones have to be given when reading."""
-    kvi = (k, v, k_idx)
-    have = next((x for x in kvi if x is not None), None)
-    if not isinstance(have, torch.Tensor) or have.dim() != 3:
-        raise ValueError("k, v or k_idx must be given, with shape (T, Hkv, 128)")
-    dev, xp, cp, table, cu, st, sizes = _pack4(kvi, (k_cache, v_cache, kidx_cache), block_table,
-                                               cu_seqlens, have.shape[0], start)
-    _check(lib().msa_cache4_store(*xp, *cp, table, cu, st, *sizes, *gains, _raw_stream(dev)))
+    _native().cache4_store(k, v, k_idx, k_cache, v_cache, kidx_cache, block_table, cu_seqlens, start,
+                           *gains)
 
 
 def msa_cache4_load(k_cache, v_cache, kidx_cache, block_table, cu_seqlens, T: int,
@@ -696,19 +585,8 @@ def msa_cache4_load(k_cache, v_cache, kidx_cache, block_table, cu_seqlens, T: in
                     k_idx=None):
     """The held values of a pack's positions, as bf16 [T, Hkv, 128] each: the inverse of
     msa_cache4_store.  A cache that is None is left out (its result is None)."""
-    caches = (k_cache, v_cache, kidx_cache)
-    outs = []
-    for n, c, x in zip(("k", "v", "k_idx"), caches, (k, v, k_idx)):
-        if c is None and x is not None:
-            raise ValueError(f"{n} needs its cache")
-        if c is not None and x is None:
-            if not isinstance(c, torch.Tensor) or c.dim() != 3:
-                raise ValueError("a 4-bit cache must have shape (num_pages, Hkv, 9216)")
-            x = torch.empty((T, c.shape[1], D), dtype=_BF, device=c.device)
-        outs.append(x)
-    dev, xp, cp, table, cu, st, sizes = _pack4(outs, caches, block_table, cu_seqlens, T, start)
-    _check(lib().msa_cache4_load(*cp, table, cu, st, *sizes, *gains, *xp, _raw_stream(dev)))
-    return tuple(outs)
+    return _native().cache4_load(k_cache, v_cache, kidx_cache, block_table, cu_seqlens, T, start, *gains,
+                                 k, v, k_idx)
 
 
 def msa_decode4_append(q, q_idx, k, v, k_idx, w_q, w_qi, w_k, w_ki, k_cache, v_cache, kidx_cache,
@@ -717,28 +595,9 @@ def msa_decode4_append(q, q_idx, k, v, k_idx, w_q, w_qi, w_k, w_ki, k_cache, v_c
     """msa_decode_append into 4-bit caches: the prologue (norm, rotation `rope`) of one
     new token per sequence at position cache_lens - 1, its k, index-k and v held in 4
     bits; returns (q_out, q_idx_out).  Rows of length 0 are padding and left alone."""
-    dev = _dev(q, "q")
-    B, Hq = q.shape[0], q.shape[1]
-    cs, maxp = _table4(k_cache, block_table, B)
-    P, Hkv, _ = cs
-    qs, ks, ws = (B, Hq, D), (B, Hkv, D), (D,)
-    if q_out is None:
-        q_out = torch.empty_like(q)
-    if q_idx_out is None:
-        q_idx_out = torch.empty_like(q_idx)
-    kg, vg, ig = gains
-    _check(lib().msa_decode4_append(
-        _arg(q, "q", _BF, qs, dev), _arg(q_idx, "q_idx", _BF, ks, dev), _arg(k, "k", _BF, ks, dev),
-        _arg(v, "v", _BF, ks, dev), _arg(k_idx, "k_idx", _BF, ks, dev),
-        _arg(w_q, "w_q", _BF, ws, dev), _arg(w_qi, "w_qi", _BF, ws, dev),
-        _arg(w_k, "w_k", _BF, ws, dev), _arg(w_ki, "w_ki", _BF, ws, dev),
-        _arg(k_cache, "k_cache", _U8, cs, dev), _arg(v_cache, "v_cache", _U8, cs, dev),
-        _arg(kidx_cache, "kidx_cache", _U8, cs, dev),
-        _arg(block_table, "block_table", _I32, (B, maxp), dev),
-        _arg(cache_lens, "cache_lens", _I32, (B,), dev), B, Hq, Hkv, P, maxp, _rope_ref(rope), kg, vg,
-        ig, eps, _arg(q_out, "q_out", _BF, qs, dev), _arg(q_idx_out, "q_idx_out", _BF, ks, dev),
-        _raw_stream(dev)))
-    return q_out, q_idx_out
+    return _native().decode4_append(q, q_idx, k, v, k_idx, w_q, w_qi, w_k, w_ki, k_cache, v_cache,
+                                    kidx_cache, block_table, cache_lens, _rope_at(rope), *gains, q_out,
+                                    q_idx_out, eps)
 
 
 def msa_decode4_step(q, q_idx, k_cache, v_cache, kidx_cache, block_table, cache_lens,
@@ -747,99 +606,26 @@ def msa_decode4_step(q, q_idx, k_cache, v_cache, kidx_cache, block_table, cache_
                      workspace: Optional[torch.Tensor] = None, n_init: int = 0):
     """msa_decode_step over 4-bit caches: (o bf16 [B, Hq, 128], sel int32 [B, Hkv, 16]),
     Hq = 1 .. 16 heads per KV head.  Rows of length 0 get o = 0, sel = -1."""
-    dev = _dev(q, "q")
-    B, Hq = q.shape[0], q.shape[1]
-    cs, maxp = _table4(k_cache, block_table, B)
-    P, Hkv, _ = cs
-    qs = (B, Hq, D)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    if out is None:
-        out = torch.empty_like(q)
-    if sel_out is None:
-        sel_out = torch.empty((B, Hkv, TOPK), dtype=_I32, device=dev)
-    l = lib()
-    wsp, nbytes, workspace = _scratch(l.msa_decode4_step_workspace_size(B, Hq, Hkv, maxp), workspace,
-                                      dev)
-    _check(l.msa_decode4_step(
-        _arg(q, "q", _BF, qs, dev), _arg(q_idx, "q_idx", _BF, (B, Hkv, D), dev),
-        _arg(k_cache, "k_cache", _U8, cs, dev), _arg(v_cache, "v_cache", _U8, cs, dev),
-        _arg(kidx_cache, "kidx_cache", _U8, cs, dev),
-        _arg(block_table, "block_table", _I32, (B, maxp), dev),
-        _arg(cache_lens, "cache_lens", _I32, (B,), dev), B, Hq, Hkv, P, maxp, scale, gains[0],
-        gains[1], n_init, _arg(out, "out", _BF, qs, dev),
-        _arg(sel_out, "sel_out", _I32, (B, Hkv, TOPK), dev), wsp, nbytes, _raw_stream(dev)))
-    return out, sel_out
+    return _native().decode4_step(q, q_idx, k_cache, v_cache, kidx_cache, block_table, cache_lens,
+                                  _SCALE if scale is None else scale, gains[0], gains[1], out, sel_out,
+                                  workspace, n_init)
 
 
 # ------------------------------------------------------------------ pages of a cache
-
-def _tables(block_table, cache_lens, ref_count):
-    """(device, addresses, (B, num_pages, max_pages)) of a set of tables."""
-    dev = _dev(block_table, "block_table")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must have shape (B, max_pages)")
-    if not isinstance(ref_count, torch.Tensor) or ref_count.dim() != 1:
-        raise ValueError("ref_count must be a tensor of shape (num_pages,)")
-    B, maxp = block_table.shape
-    P = ref_count.numel()
-    return dev, (_arg(block_table, "block_table", _I32, (B, maxp), dev),
-                 _arg(cache_lens, "cache_lens", _I32, (B,), dev),
-                 _arg(ref_count, "ref_count", _I32, (P,), dev)), (B, P, maxp)
-
-
-_PTRS = [_vp * max(n, 1) for n in range(9)]             # made once: an array type costs
-_SIZES = [ctypes.c_int64 * max(n, 1) for n in range(9)]  # more than a call
-
-
-def _page_args(caches, P, dev):
-    """Host arrays of the caches' addresses and bytes per page."""
-    n = len(caches)
-    if n > 8:
-        raise ValueError(f"at most 8 caches, got {n}")
-    ptrs, sizes = _PTRS[n](), _SIZES[n]()
-    for i, c in enumerate(caches):
-        if not isinstance(c, torch.Tensor) or c.get_device() != dev or not c.is_contiguous():
-            raise ValueError(f"cache {i} must be a contiguous tensor on cuda:{dev}")
-        if c.dim() < 1 or c.shape[0] != P:
-            raise ValueError(f"cache {i} must have {P} pages in its first dimension")
-        ptrs[i] = c.data_ptr()
-        sizes[i] = c.nbytes // max(P, 1)
-    return ptrs, sizes, n
-
-
-def _rows(t, name, dev):
-    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.numel() < 1:
-        raise ValueError(f"{name} must be a tensor of shape (n,) with n >= 1")
-    return _arg(t, name, _I32, (t.numel(),), dev), t.numel()
-
 
 def msa_pages_fork(src, dst, block_table, cache_lens, ref_count,
                    keep: Optional[torch.Tensor] = None, forked: Optional[torch.Tensor] = None):
     """Row dst[i] (empty) shares the pages of the first keep[i] tokens (None: all) of
     row src[i]; tables, lengths and reference counts change in place.  Returns forked
     int32 [n]: the length given, -1 where the pair was refused."""
-    dev, tables, sizes = _tables(block_table, cache_lens, ref_count)
-    sp, n = _rows(src, "src", dev)
-    if forked is None:
-        forked = torch.empty(n, dtype=_I32, device=dev)
-    _check(lib().msa_pages_fork(sp, _arg(dst, "dst", _I32, (n,), dev),
-                                _opt(keep, "keep", _I32, (n,), dev), n, *tables, *sizes,
-                                _arg(forked, "forked", _I32, (n,), dev), _raw_stream(dev)))
-    return forked
+    return _native().pages_fork(src, dst, block_table, cache_lens, ref_count, keep, forked)
 
 
 def msa_pages_free(rows, block_table, cache_lens, ref_count, keep: Optional[torch.Tensor] = None,
                    dropped: Optional[torch.Tensor] = None):
     """Row rows[i] keeps its first keep[i] tokens (None: none); pages that no row
     holds any more are free.  Returns dropped int32 [n]: tokens dropped, -1 where refused."""
-    dev, tables, sizes = _tables(block_table, cache_lens, ref_count)
-    rp, n = _rows(rows, "rows", dev)
-    if dropped is None:
-        dropped = torch.empty(n, dtype=_I32, device=dev)
-    _check(lib().msa_pages_free(rp, _opt(keep, "keep", _I32, (n,), dev), n, *tables, *sizes,
-                                _arg(dropped, "dropped", _I32, (n,), dev), _raw_stream(dev)))
-    return dropped
+    return _native().pages_free(rows, block_table, cache_lens, ref_count, keep, dropped)
 
 
 def msa_pages_extend(add, block_table, cache_lens, ref_count, caches,
@@ -849,16 +635,7 @@ def msa_pages_extend(add, block_table, cache_lens, ref_count, caches,
     shared, partly filled last page in every tensor of `caches` (first dimension =
     pages, any format).  Returns done int32 [B]: 1 where the row has grown, 0 where the
     pool or the table is too small for it."""
-    dev, tables, sizes = _tables(block_table, cache_lens, ref_count)
-    B, P, _ = sizes
-    if done is None:
-        done = torch.empty(B, dtype=_I32, device=dev)
-    l = lib()
-    wsp, nbytes, workspace = _scratch(l.msa_pages_extend_workspace_size(B, P), workspace, dev)
-    _check(l.msa_pages_extend(_arg(add, "add", _I32, (B,), dev), *tables, *sizes,
-                              *_page_args(caches, P, dev), _arg(done, "done", _I32, (B,), dev), wsp,
-                              nbytes, _raw_stream(dev)))
-    return done
+    return _native().pages_extend(add, block_table, cache_lens, ref_count, caches, done, workspace)
 
 
 def msa_pages_compact(block_table, cache_lens, ref_count, caches,
@@ -868,32 +645,12 @@ def msa_pages_compact(block_table, cache_lens, ref_count, caches,
     """Moves the pages in use to the front of the pool, in every tensor of `caches`;
     tables and counts follow.  Returns (page_map int32 [num_pages], -1 for free pages,
     n_live int32 [1])."""
-    dev, tables, sizes = _tables(block_table, cache_lens, ref_count)
-    P = sizes[1]
-    if page_map is None:
-        page_map = torch.empty(P, dtype=_I32, device=dev)
-    if n_live is None:
-        n_live = torch.empty(1, dtype=_I32, device=dev)
-    l = lib()
-    wsp, nbytes, workspace = _scratch(l.msa_pages_compact_workspace_size(P), workspace, dev)
-    _check(l.msa_pages_compact(*tables, *sizes, *_page_args(caches, P, dev),
-                               _arg(page_map, "page_map", _I32, (P,), dev),
-                               _arg(n_live, "n_live", _I32, (1,), dev), wsp, nbytes,
-                               _raw_stream(dev)))
-    return page_map, n_live
+    return _native().pages_compact(block_table, cache_lens, ref_count, caches, page_map, n_live, workspace)
 
 
 def msa_pages_copy(src, dst, caches) -> None:
     """Page src[i] -> page dst[i] in every tensor of `caches` (first dimension = pages)."""
-    if not caches:
-        raise ValueError("no cache given")
-    dev = _dev(caches[0], "cache 0")
-    if caches[0].dim() < 1:
-        raise ValueError("cache 0 must have pages in its first dimension")
-    P = caches[0].shape[0]
-    sp, n = _rows(src, "src", dev)
-    _check(lib().msa_pages_copy(sp, _arg(dst, "dst", _I32, (n,), dev), n, P,
-                                *_page_args(caches, P, dev), _raw_stream(dev)))
+    _native().pages_copy(src, dst, caches)
 
 
 def workspace_bytes(call: str, *args) -> int:
