@@ -27,7 +27,8 @@
  *     the device that is current when the call is made.
  *   - bf16 means IEEE bfloat16 (2 bytes); compute is fp32 inside the kernels.
  *   - D (head dim) is 128, the key block is 128 tokens, top-k is 16, the
- *     rotated part is the first 64 channels: the library rejects other values.
+ *     rotated part is the first 64 channels: the library rejects other values,
+ *     except where a call states its own.
  *   - Packed (THD) inputs: token t of the pack belongs to sequence s with
  *     cu_seqlens[s] <= t < cu_seqlens[s+1]; its position is t - cu_seqlens[s].
  *     Key block b of sequence s covers positions [128 b, 128 b + 128); the last
@@ -424,6 +425,9 @@ MSA_API msa_status_t msa_decode_append(const void* q, const void* q_idx, const v
  * needed).  Tokens outside [0, max_pages * 128) or on pages outside
  * [0, num_pages) set MSA_STATUS_BOUNDS; they are not stored, and load as zeros.
  * Rows of the pack outside [cu_seqlens[0], cu_seqlens[S]) are left alone.
+ * Store and append write where the table says: a page that rows share has to
+ * be made the row's own first (msa_pages_extend), and no position may be written twice
+ * in one call.
  */
 MSA_API msa_status_t msa_cache4_store(const void* k, const void* v, const void* k_idx,
                                       void* k_cache, void* v_cache, void* kidx_cache,

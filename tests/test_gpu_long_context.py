@@ -270,6 +270,58 @@ def test_store_and_load_out_of_range(m):
     assert np.array_equal(f64(y), L.held(*L.quantise(f64(x)[100:200])))
 
 
+def test_store_and_load_many_sequences(m):
+    """More than 32 sequences (found by bisection), empty ones among them."""
+    rng = np.random.default_rng(3)
+    lens = rng.integers(0, 9, 70)
+    lens[[0, 5, 69]] = 0
+    first = rng.integers(0, 300, 70)
+    T, cu = int(lens.sum()), np.concatenate([[0], np.cumsum(lens)])
+    table, P = layout_of(rng, first + lens)
+    x = spread(rng, T, 2, 128)
+    cache = torch.zeros(P, 2, 9216, dtype=torch.uint8, device=DEV)
+    m.msa_cache4_store(None, bf16(x), None, None, cache, None, i32(table), i32(cu), start=i32(first))
+    got = m.msa_cache4_load(None, cache, None, i32(table), i32(cu), T, start=i32(first))[1]
+    want = L.held(*L.quantise(x))
+    assert np.array_equal(f64(got), want)
+    raw = L.slab_values(cache.cpu().numpy())
+    for s in range(70):
+        for i in range(lens[s]):
+            p, o = divmod(first[s] + i, 128)
+            assert np.array_equal(raw[table[s, p], :, o], want[cu[s] + i])
+    m.msa_check_status()
+
+
+def test_cache_beyond_4_gb(m):
+    """Slabs whose offset in the cache passes 32 bits: store, load, decode and copies."""
+    rng = np.random.default_rng(4)
+    P, H, n = 120000, 4, 2300
+    assert P * H * 9216 > 1 << 32
+    nb = -(-n // 128)
+    cache = torch.zeros(P, H, 9216, dtype=torch.uint8, device=DEV)
+    pages = P - 1 - rng.permutation(2 * nb)
+    table = pages[None, :nb].astype(np.int32)
+    x = f64(bf16(rng.standard_normal((n, H, 128))))
+    # one cache stands for all three: v and the index keys equal the keys
+    m.msa_cache4_store(bf16(x), None, None, cache, None, None, i32(table), i32([0, n]))
+    got = m.msa_cache4_load(cache, None, None, i32(table), i32([0, n]), n)[0]
+    assert np.array_equal(f64(got), L.held(*L.quantise(x)))
+    q, qi = (f64(bf16(rng.standard_normal((1, h, 128)))) for h in (4 * H, H))
+    o, sel = m.msa_decode4_step(bf16(q), bf16(qi), cache, cache, cache, i32(table), i32([n]))
+    slabs = cache[torch.tensor(pages[:nb].copy(), device=DEV)].cpu().numpy()
+    local = np.arange(nb)[None]
+    for h in range(H):
+        want, gap = L.select(L.decode_scores(qi, slabs, local, 0, h, n))
+        assert gap < 1e-5 or sel[0, h].tolist() == want
+        ref = L.attend(q[0, 4 * h:4 * h + 4], slabs, slabs, local, 0, h, n, want, SCALE)
+        within(f64(o)[0, 4 * h:4 * h + 4], ref, 2.0 ** -8 * np.abs(ref) + 2.0 ** -9 * 6, f"o[{h}]")
+    m.msa_pages_copy(i32(pages[:nb]), i32(pages[nb:]), [cache])
+    m.msa_pages_copy(i32(pages[:1]), i32([0]), [cache])
+    t = torch.tensor(pages.copy(), device=DEV)
+    assert torch.equal(cache[t[:nb]], cache[t[nb:]]) and torch.equal(cache[0], cache[t[0]])
+    m.msa_check_status()
+
+
 @pytest.mark.parametrize("G,H,R,layout,scaling", [
     (16, 4, 64, "half", "yarn"), (1, 1, 128, "interleaved", "none"), (3, 5, 16, "half", "ntk"),
     (12, 2, 96, "interleaved", "linear"),
@@ -423,6 +475,46 @@ def check_decode(m, lens, G, H, seed=0, n_init=0, gains=(1.0, 1.0), max_pages=No
 ], ids=str)
 def test_decode4(m, lens, G, H, kw):
     check_decode(m, lens, G, H, seed=len(lens), **kw)
+
+
+def test_decode4_many_rows(m):
+    """More rows than the score kernel counts at a time; some checked, all compared with the
+    same rows alone."""
+    rng = np.random.default_rng(5)
+    lens = rng.integers(0, 300, 1300)
+    some = [0, 7, 500, 1023, 1024, 1025, 1299]
+    lens[some] = [2200, 0, 2600, 2177, 3000, 130, 2049]
+    q, qi, slabs, table = decode_case(rng, lens, 1, 1)
+    o, sel = run_decode(m, q, qi, slabs, table, lens)
+    m.msa_check_status()
+    for b in some:
+        if lens[b] == 0:
+            assert (o[b] == 0).all() and (sel[b] == -1).all()
+            continue
+        want, gap = L.select(L.decode_scores(qi, slabs[2], table, b, 0, lens[b]))
+        assert gap < 1e-5 or [x for x in sel[b, 0] if x >= 0] == want
+        ref = L.attend(q[b], slabs[0], slabs[1], table, b, 0, lens[b], want, SCALE)
+        within(o[b], ref, 2.0 ** -8 * np.abs(ref) + 2.0 ** -9 * 6, f"o[{b}]")
+    pick = rng.permutation(1300)[:40]
+    o2, sel2 = run_decode(m, q[pick], qi[pick], slabs, table[pick], lens[pick])
+    assert np.array_equal(sel2, sel[pick])
+    # other splits of a row's blocks over CTAs: other orders of the sums
+    assert np.abs(o2 - o[pick]).max() <= 2.0 ** -7 * np.abs(o).max()
+
+
+def test_decode4_beside_the_16_bit_step(m):
+    """The same values held in 16 bits: msa_decode_step gives the same blocks and, within the
+    two calls' roundings, the same output."""
+    rng = np.random.default_rng(6)
+    lens = (5000, 2049, 300, 4000)
+    q, qi, slabs, table = decode_case(rng, lens, 16, 2, garbage=False)
+    o, sel = run_decode(m, q, qi, slabs, table, lens)
+    wide = [bf16(L.slab_values(s)) for s in slabs]
+    ow, selw = m.msa_decode_step(bf16(q), bf16(qi), *wide, i32(table), i32(lens))
+    m.msa_check_status()
+    assert np.array_equal(selw.cpu().numpy(), sel)
+    # its weights are rounded to bf16: 2^-8 each, independent
+    assert np.linalg.norm(f64(ow) - o) <= 2.0 ** -7 * np.linalg.norm(o)
 
 
 def test_decode4_longest(m):
