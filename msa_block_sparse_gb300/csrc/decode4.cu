@@ -273,6 +273,8 @@ __global__ void __launch_bounds__(kScThreads, 1) decode4_score_kernel(
 constexpr int kAtWarps = 4;
 constexpr int kAtThreads = 32 * kAtWarps;
 constexpr int kKeysPerWarp = kBlock / kAtWarps;
+constexpr int kAtPer = kMaxSeqlen / kBlock / kAtThreads;   // scores per thread
+constexpr int kMaxDevices = 64;
 constexpr float kAtRescale = 8.0f;  // log2 of the largest weight before a rescale (fp16: below 2^16)
 
 // A warp's 32 keys of a block, as they lie in the slabs
@@ -284,8 +286,8 @@ struct Attend4Keys {
 };
 
 // kWhole: the CTA's slabs all at once, asked for by warp 0 as soon as it knows the
-// blocks; three CTAs fit an SM.  Otherwise each warp streams its keys through two
-// buffers of its own; four CTAs fit.
+// blocks; two (4 blocks) or three CTAs fit an SM.  Otherwise each warp streams its keys
+// through two buffers of its own; four CTAs fit.
 template <int NS, bool kWhole_>
 struct Attend4Smem {
   static constexpr int kBlocks = kTopK / NS;       // blocks per CTA
@@ -297,17 +299,21 @@ struct Attend4Smem {
       alignas(16) uint8_t v[kWhole ? kBlocks : 1][kSlab];
     } whole;
     Attend4Keys s[kWhole ? 1 : kAtWarps][kStages];
-    alignas(16) float o[kAtWarps][16][kD];         // per warp once the keys are used, then [0]
-                                                   // = the CTA's sum
+    alignas(16) float o[kAtWarps][16][kD];         // per warp, once the keys are used
   };
+  // sums (and maximum, weight) of this CTA's rows of the result, by sender: stored here
+  // by the cluster's CTAs, which may be ahead of this one
+  alignas(16) float part[NS][16 / NS][kD];
+  alignas(16) float part_ml[NS][16 / NS][2];
+  unsigned long long cand[4 * (kTopK - 1) * kAtPer];   // selection: keys left to be ranked
   alignas(16) uint4 qa[8][32];                     // A operand of the 8 k-steps, per lane
   float ml[kAtWarps][16][2];
-  float cta_ml[16][2];
   unsigned long long gmax[32];                     // selection: best key of each group of threads
   int list[kTopK];                                 // selected blocks, -1 behind
   int page[kBlocks];
   int ncand;
   uint64_t full[kAtWarps][kStages];                // whole slabs: the first kBlocks of them
+  uint64_t joined;                                 // part, part_ml are complete
 };
 
 // Float4 `chunk` (channel / 4) of row r in a [16][128] array of sums: permuted so
@@ -328,19 +334,22 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-  return v;
+// Stores into a CTA of the cluster; `bar`, in the same CTA, counts the bytes.
+__device__ __forceinline__ void st_async4(uint32_t a, const float4& v, uint32_t bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
+      "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+      : "memory");
 }
-__device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void st_async2(uint32_t a, float x, float y, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(a),
+               "f"(x), "f"(y), "r"(bar)
+               : "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {  // publishes barriers (after fence_mbar_init), no data
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -351,8 +360,17 @@ __device__ __forceinline__ float ex2(float x) {
 
 // grid (NS, B * Hkv) in clusters of NS CTAs; CTA `split` attends to the selected
 // blocks split, split + NS, ...  Each warp takes 32 keys of every block.  Bound by
-// instruction issue and latency: 256 rows, 75 MB, 38 us at 1.9 instructions per cycle and
-// SM (a fifth of the time is the selection, a sixth the merge); 4 rows 5.4 us.
+// instruction issue and latency: 256 rows, 75 MB, 33 us with cold caches and 25 us
+// behind the scores, 2.0 instructions per cycle and SM (a fifth of the time is the
+// selection, a tenth the joining of the sums); 4 rows 3.8 us.  Slabs shared by the CTA's
+// warps instead of a stream for each (8 times fewer copies) took 1.5 us more.
+//
+// The CTAs' sums are joined by asynchronous stores into the CTA that finishes a row,
+// counted by its barrier; two cluster barriers around loads from the others took 1.2 us
+// more (4 rows: 5.0 us), since their release waits for all earlier stores.
+//
+// Lengths, q and everything else but the scores were complete before the scores' kernel
+// passed its own wait, so they are read while that kernel's last CTAs run.
 //
 // S = Q K^T: rows are heads; n-tile column g is key (g >> 1) + 4 (g & 1) of 8, so
 // that the accumulator's column pair (2c, 2c + 1) is keys (c, c + 4), which is how
@@ -368,79 +386,83 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
     const int32_t* __restrict__ lens, const float* __restrict__ scores, int G, int Hkv,
     int num_pages, int max_pages, int n_init, float sl2, float v_gain, __nv_bfloat16* __restrict__ o,
     int32_t* __restrict__ sel_out, uint32_t* status) {
-  pdl_enter();
+  if (max_pages <= kTopK) pdl_wait();              // no scores' kernel stands in between
   extern __shared__ __align__(128) uint8_t smem_raw[];
   using Smem = Attend4Smem<NS, kWhole>;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
-  constexpr int kBlocks = Smem::kBlocks;
+  constexpr int kBlocks = Smem::kBlocks, kRows = 16 / NS;
   const int split = blockIdx.x, bh = blockIdx.y, b = bh / Hkv, h = bh % Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   // ---- everything that depends on no other load is asked for at once
+  const int my_rows = max(0, min(G - split * kRows, kRows));   // of the result, to finish here
   const int len = lens[b];
+  // q as the A operand of the 8 k-steps: rows g and g + 8 in fp16, each with a power
+  // of two; thread c of a row has channels 32 c .. 32 c + 31.  Each warp makes and
+  // stores two k-steps.
+  float f0, f1;
+  {
+    uint4 a0, a1;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = g + 8 * half;
+      uint4 x[4];
+      uint32_t m = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < G)
+          x[i] = *(reinterpret_cast<const uint4*>(
+                       q + (static_cast<size_t>(b) * G * Hkv + static_cast<size_t>(h) * G + r) * kD +
+                       32 * c) + i);
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
+                                 __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
+      }
+      m = max(m & 0xFFFFu, m >> 16);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int e = row_shift(m);
+      const float f = exp2i(e);
+      (half ? f1 : f0) = sl2 * exp2i(-e);
+      const uint4 mine = warp == 0 ? x[0] : (warp == 1 ? x[1] : (warp == 2 ? x[2] : x[3]));
+      (half ? a0.y : a0.x) = bf2_to_h2(mine.x, f);
+      (half ? a0.w : a0.z) = bf2_to_h2(mine.y, f);
+      (half ? a1.y : a1.x) = bf2_to_h2(mine.z, f);
+      (half ? a1.w : a1.z) = bf2_to_h2(mine.w, f);
+    }
+    sm.qa[2 * warp][lane] = a0;
+    sm.qa[2 * warp + 1][lane] = a1;
+  }
+  if (max_pages > kTopK) pdl_wait();
+  pdl_launch();
   const float* sc = scores + static_cast<size_t>(bh) * max_pages;
-  constexpr int kPer = kMaxSeqlen / kBlock / kAtThreads;
-  float score[kPer];                               // blocks tid + 128 r (behind the own block: anything)
+  float score[kAtPer];                             // blocks tid + 128 r (behind the own block: anything)
   if (max_pages > kTopK) {
 #pragma unroll
-    for (int r = 0; r < kPer; ++r) {
+    for (int r = 0; r < kAtPer; ++r) {
       const int i = kAtThreads * r + tid;
-      score[r] = i < max_pages ? sc[i] : 0.f;
+      score[r] = i < max_pages ? __ldcg(sc + i) : 0.f;   // not to be moved before the wait
     }
   }
-  // q as the A operand of the 8 k-steps: rows g and g + 8 in fp16, each with a power
-  // of two; thread c of a row has channels 32 c .. 32 c + 31
-  float f0, f1;
-  uint32_t qa[8][4];
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int r = g + 8 * half;
-    uint4 x[4];
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < G)
-        x[i] = *(reinterpret_cast<const uint4*>(
-                     q + (static_cast<size_t>(b) * G * Hkv + static_cast<size_t>(h) * G + r) * kD +
-                     32 * c) + i);
-      m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
-                               __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
-    }
-    m = max(m & 0xFFFFu, m >> 16);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const int e = row_shift(m);
-    const float f = exp2i(e);
-    (half ? f1 : f0) = sl2 * exp2i(-e);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      qa[2 * i][half] = bf2_to_h2(x[i].x, f);
-      qa[2 * i][2 + half] = bf2_to_h2(x[i].y, f);
-      qa[2 * i + 1][half] = bf2_to_h2(x[i].z, f);
-      qa[2 * i + 1][2 + half] = bf2_to_h2(x[i].w, f);
-    }
-  }
-  // every warp has all of it; each stores two k-steps
-#pragma unroll
-  for (int t = 0; t < 8; ++t)
-    if (t >> 1 == warp) sm.qa[t][lane] = make_uint4(qa[t][0], qa[t][1], qa[t][2], qa[t][3]);
   const int L = d4_len(len, max_pages, status);
   const int nblk = (L + kBlock - 1) / kBlock;
   const int own = nblk - 1;
   // by the lanes of warp 0 that use them before the next barrier of the CTA
   if (tid < kAtWarps * Smem::kStages) {
     mbar_init(&sm.full[0][0] + tid, 1);
+    if (tid == 0) mbar_init(&sm.joined, 1);
     fence_mbar_init();
+    if (tid == 0 && my_rows > 0)
+      mbar_arrive_expect_tx(&sm.joined, NS * my_rows * (kD + 2) * sizeof(float));
   }
+  cluster_arrive();
   if (tid == 0) sm.ncand = 0;
   if (own >= kTopK) {
     // ---- the 15 best earlier blocks.  The threads form 32 groups of 4; the 15th of
     // the groups' best keys bounds the 15th best key from below, so that few keys
     // (about 20; at most 15 groups' keys) are left to be ranked among each other.
-    unsigned long long* cand = reinterpret_cast<unsigned long long*>(sm.o);   // [<= 15 * 4 * kPer]
-    unsigned long long key[kPer], top = 0ull;
+    unsigned long long key[kAtPer], top = 0ull;
 #pragma unroll
-    for (int r = 0; r < kPer; ++r) {
+    for (int r = 0; r < kAtPer; ++r) {
       const int i = kAtThreads * r + tid;
       key[r] = 0ull;
       if (i < own)
@@ -464,16 +486,16 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
     const unsigned long long bar =
         at15 ? __shfl_sync(0xffffffffu, mine, __ffs(at15) - 1) : 1ull;
 #pragma unroll
-    for (int r = 0; r < kPer; ++r)
-      if (key[r] >= bar) cand[atomicAdd(&sm.ncand, 1)] = key[r];
+    for (int r = 0; r < kAtPer; ++r)
+      if (key[r] >= bar) sm.cand[atomicAdd(&sm.ncand, 1)] = key[r];
     __syncthreads();
     if (warp == 0) {
       const int nc = sm.ncand;
       for (int t = lane; t < nc; t += 32) {
-        const unsigned long long me = cand[t];
+        const unsigned long long me = sm.cand[t];
         int rank = 0;
 #pragma unroll 4
-        for (int j = 0; j < nc; ++j) rank += cand[j] > me ? 1 : 0;
+        for (int j = 0; j < nc; ++j) rank += sm.cand[j] > me ? 1 : 0;
         if (rank < kTopK - 1) sm.list[rank] = 0x7FFFFFFF - static_cast<int>(static_cast<uint32_t>(me));
       }
       if (lane == 31) sm.list[kTopK - 1] = own;
@@ -497,7 +519,6 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
       sm.page[lane] = pg;
       if (kWhole && pg >= 0) {
         const size_t off = (static_cast<size_t>(pg) * Hkv + h) * kSlab;
-        fence_proxy_async_smem();                  // the slabs lie over the candidates
         mbar_arrive_expect_tx(&sm.full[0][0] + lane, 2 * kSlab);
         bulk_load(sm.whole.k[lane], kc + off, kSlab, &sm.full[0][0] + lane);
         bulk_load(sm.whole.v[lane], vc + off, kSlab, &sm.full[0][0] + lane);
@@ -543,7 +564,6 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
     ++nload;
     ask &= ask - 1u;
   };
-  if (lane == 0) fence_proxy_async_smem();         // the buffers lie over the candidates
   for (int i = 0; i < Smem::kStages; ++i) load();
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
   float acc[16][4];
@@ -729,6 +749,7 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
     sm.ml[warp][g + 8][1] = l1;
   }
   __syncthreads();
+  cluster_wait();                                  // every CTA's barrier is initialised
   {
     const int r = tid >> 3;                        // 16 rows x 8 threads, float4s tid % 8 + 8 j
     float mm = -INFINITY, f[kAtWarps], l = 0.f;
@@ -739,6 +760,9 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
       f[w] = sm.ml[w][r][0] == -INFINITY ? 0.f : ex2(sm.ml[w][r][0] - mm);
       l += f[w] * sm.ml[w][r][1];
     }
+    // to the CTA that finishes the row
+    const uint32_t to = r / kRows, bar = cluster_map(smem_u32(&sm.joined), to);
+    const uint32_t row_at = cluster_map(smem_u32(sm.part[split][r % kRows]), to);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int at = o_at(r, (tid & 7) + 8 * j);
@@ -751,48 +775,40 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
         t.z = fmaf(f[w], x.z, t.z);
         t.w = fmaf(f[w], x.w, t.w);
       }
-      *reinterpret_cast<float4*>(&sm.o[0][0][0] + at) = t;
+      if (r < G) st_async4(row_at + 16 * ((tid & 7) + 8 * j), t, bar);
     }
-    if ((tid & 7) == 0) {
-      sm.cta_ml[r][0] = mm;
-      sm.cta_ml[r][1] = l;
-    }
+    if ((tid & 7) == 0 && r < G) st_async2(cluster_map(smem_u32(sm.part_ml[split][r % kRows]), to), mm, l, bar);
   }
-  cluster_sync();
-  {
-    // CTA `split` finishes rows split * 16 / NS .., a warp each
-    constexpr int kRows = 16 / NS;
-    const int r = split * kRows + warp, d0 = lane * 4;
-    if (warp < kRows && r < G) {
-      const uint32_t mla = smem_u32(&sm.cta_ml[r][0]), oa = smem_u32(&sm.o[0][0][0] + o_at(r, lane));
-      float2 ml[NS];
-      float4 x[NS];
-      float mm = -INFINITY, l = 0.f;
+  // ---- this CTA's rows of the result, a warp each.  Every CTA stores its sums, also
+  // after waits that ran out, a few limits later at most: none leaves while it is
+  // stored to.
+  if (warp >= my_rows) return;
+  bool here = false;
+  for (int t = 0; t < 8 && !here; ++t) here = mbar_wait<true>(&sm.joined, 0, status, 84);
+  for (int w = warp; w < my_rows; w += kAtWarps) {
+    const int r = split * kRows + w;
+    float mm = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int p = 0; p < NS; ++p) {
-        ml[p] = ld_cluster2(cluster_map(mla, p));
-        x[p] = ld_cluster4(cluster_map(oa, p));
-        mm = fmaxf(mm, ml[p].x);
-      }
-      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = 0; p < NS; ++p) mm = fmaxf(mm, sm.part_ml[p][w][0]);
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int p = 0; p < NS; ++p) {
-        const float f = ml[p].x == -INFINITY ? 0.f : ex2(ml[p].x - mm);
-        l = fmaf(f, ml[p].y, l);
-        t.x = fmaf(f, x[p].x, t.x);
-        t.y = fmaf(f, x[p].y, t.y);
-        t.z = fmaf(f, x[p].z, t.z);
-        t.w = fmaf(f, x[p].w, t.w);
-      }
-      const float inv = l > 0.f ? v_gain / l : 0.f;
-      uint2 out;
-      out.x = pack_bf16x2(t.x * inv, t.y * inv);
-      out.y = pack_bf16x2(t.z * inv, t.w * inv);
-      *reinterpret_cast<uint2*>(
-          o + (static_cast<size_t>(b) * G * Hkv + static_cast<size_t>(h) * G + r) * kD + d0) = out;
+    for (int p = 0; p < NS; ++p) {
+      const float2 ml = *reinterpret_cast<const float2*>(sm.part_ml[p][w]);
+      const float4 x = *reinterpret_cast<const float4*>(&sm.part[p][w][4 * lane]);
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mm);
+      l = fmaf(f, ml.y, l);
+      t.x = fmaf(f, x.x, t.x);
+      t.y = fmaf(f, x.y, t.y);
+      t.z = fmaf(f, x.z, t.z);
+      t.w = fmaf(f, x.w, t.w);
     }
+    const float inv = l > 0.f ? v_gain / l : 0.f;
+    uint2 out;
+    out.x = pack_bf16x2(t.x * inv, t.y * inv);
+    out.y = pack_bf16x2(t.z * inv, t.w * inv);
+    *reinterpret_cast<uint2*>(o + (static_cast<size_t>(b) * G * Hkv + static_cast<size_t>(h) * G + r) * kD +
+                              4 * lane) = out;
   }
-  cluster_sync();                                  // no CTA leaves while it is read
 }
 
 // ---------------------------------------------------------------- host
@@ -809,48 +825,77 @@ Decode4Workspace carve_decode4_workspace(WsCursor& ws, int B, int Hkv, int max_p
   return w;
 }
 
-// Clusters of 16 are beyond the portable size: allowed once per device.
-msa_status_t allow_large_cluster(const void* kernel) {
-  static std::atomic<bool> done[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return fail(MSA_ERR_CUDA, "cudaGetDevice failed");
-  if (dev < 0 || dev >= 64 || !done[dev].load()) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return fail(MSA_ERR_CUDA, "decode4_attend_kernel: %s", cudaGetErrorString(e));
-    if (dev >= 0 && dev < 64) done[dev].store(true);
-  }
-  return MSA_OK;
-}
-
 template <int NS, bool kWhole>
-msa_status_t launch_attend4(const void* q, const void* kc, const void* vc, const int32_t* table,
-                            const int32_t* lens, const float* scores, int B, int G, int Hkv,
-                            int num_pages, int max_pages, int n_init, float sl2, float v_gain, void* o,
-                            int32_t* sel_out, uint32_t* sw, cudaStream_t stream) {
-  const size_t smem = sizeof(Attend4Smem<NS, kWhole>);
-  MSA_TRY(ensure_smem(decode4_attend_kernel<NS, kWhole>, smem, "decode4_attend_kernel"));
-  TraceScope trace_("decode4_attend_kernel", stream);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(NS, static_cast<unsigned>(B) * Hkv);
-  cfg.blockDim = kAtThreads;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  if (NS > 8) MSA_TRY(allow_large_cluster(reinterpret_cast<const void*>(decode4_attend_kernel<NS, kWhole>)));
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = NS;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  cudaLaunchKernelEx(&cfg, decode4_attend_kernel<NS, kWhole>, static_cast<const __nv_bfloat16*>(q),
-                     static_cast<const uint8_t*>(kc), static_cast<const uint8_t*>(vc), table, lens,
-                     scores, G, Hkv, num_pages, max_pages, n_init, sl2, v_gain,
-                     static_cast<__nv_bfloat16*>(o), sel_out, sw);
-  return check_launch("decode4_attend_kernel");
-}
+struct Attend4 {
+  static constexpr size_t kSmem = sizeof(Attend4Smem<NS, kWhole>);
+
+  // Launch attributes; the kernel's own, where they are not the default ones
+  static msa_status_t prepare(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], int rows) {
+    MSA_TRY(ensure_smem(decode4_attend_kernel<NS, kWhole>, kSmem, "decode4_attend_kernel"));
+    if (NS > 8) {                                  // beyond the portable size of a cluster
+      static std::atomic<bool> done[kMaxDevices];
+      int dev = 0;
+      if (cudaGetDevice(&dev) != cudaSuccess) return fail(MSA_ERR_CUDA, "cudaGetDevice failed");
+      const bool known = dev >= 0 && dev < kMaxDevices;
+      if (!known || !done[dev].load()) {
+        const cudaError_t e = cudaFuncSetAttribute(decode4_attend_kernel<NS, kWhole>,
+                                                   cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return fail(MSA_ERR_CUDA, "decode4_attend_kernel: %s", cudaGetErrorString(e));
+        if (known) done[dev].store(true);
+      }
+    }
+    cfg->gridDim = dim3(NS, static_cast<unsigned>(rows));
+    cfg->blockDim = kAtThreads;
+    cfg->dynamicSmemBytes = kSmem;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = NS;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg->attrs = attr;
+    cfg->numAttrs = 1;
+    return MSA_OK;
+  }
+
+  // Whether all the rows' clusters run side by side on the current device
+  static bool fits(long long rows) {
+    static std::atomic<int> most[kMaxDevices];     // clusters + 1, 0: not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    int n = most[dev].load();
+    if (n == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[2];
+      int c = 0;
+      if (prepare(&cfg, attr, 1) != MSA_OK ||
+          cudaOccupancyMaxActiveClusters(&c, decode4_attend_kernel<NS, kWhole>, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        c = 0;
+      }
+      n = c + 1;
+      most[dev].store(n);
+    }
+    return rows < n;
+  }
+
+  static msa_status_t launch(const void* q, const void* kc, const void* vc, const int32_t* table,
+                             const int32_t* lens, const float* scores, int B, int G, int Hkv,
+                             int num_pages, int max_pages, int n_init, float sl2, float v_gain, void* o,
+                             int32_t* sel_out, uint32_t* sw, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    MSA_TRY(prepare(&cfg, attr, B * Hkv));
+    cfg.stream = stream;
+    cfg.numAttrs = 2;
+    TraceScope trace_("decode4_attend_kernel", stream);
+    cudaLaunchKernelEx(&cfg, decode4_attend_kernel<NS, kWhole>, static_cast<const __nv_bfloat16*>(q),
+                       static_cast<const uint8_t*>(kc), static_cast<const uint8_t*>(vc), table, lens,
+                       scores, G, Hkv, num_pages, max_pages, n_init, sl2, v_gain,
+                       static_cast<__nv_bfloat16*>(o), sel_out, sw);
+    return check_launch("decode4_attend_kernel");
+  }
+};
 
 }  // namespace
 
@@ -916,16 +961,19 @@ msa_status_t msa_decode4_step(const void* q, const void* q_idx, const void* k_ca
     }
     MSA_TRY(check_launch("decode4_score_kernel"));
   }
-  // CTAs per row: 16, 8 or 4, as many as still run side by side with their slabs
-  // whole (3 per SM, 2 with 4 blocks each); more CTAs shorten a row's chain of blocks.
-  // Beyond that the rows' work counts, not its latency: 4 CTAs that stream, 4 per SM.
-  // The whole step, 4 short rows: 7.5 us with 4 CTAs, 5.4 with 16; 20 rows of 60k -
-  // 131k tokens 44.4 and 37.3; 66 rows 19.8 with 4 whole, 25.0 streaming, 23.6 with 8;
-  // 256 rows 103.6 with 4 whole, 97.8 streaming, 112 with 8.
-  const long long rows = static_cast<long long>(B) * Hkv, sms = device_sm_count();
-  auto attend = rows * 16 <= 3 * sms ? launch_attend4<16, true>
-                : rows * 8 <= 3 * sms ? launch_attend4<8, true>
-                : rows * 4 <= 2 * sms ? launch_attend4<4, true> : launch_attend4<4, false>;
+  // CTAs per row: as many as run side by side with all rows' (more of them shorten a
+  // row's chain of blocks, a second wave costs more than that gains), with their slabs
+  // whole while that fits too.  The whole step, rows of 4k - 8k tokens, 16 / 8 / 4 whole /
+  // 4 / 2 / 1 CTAs: 20 rows 12.6 / 13.9 / 14.8 / 20.6 / 30.4 / 50.2 us, 40 rows 20.3 / 15.1 /
+  // 15.9 / 21.8 / 31.6 / 51.3, 68 rows 36.6 / 26.7 / 19.7 / 24.7 / 34.1 / 53.4, 128 rows 64.9 /
+  // 43.7 / 37.9 / 32.5 / 41.5 / 61.3, 304 rows 139 / 87 / 79 / 66 / 56 / 74; 1 CTA per row is
+  // within 5 % of 2 from 480 rows on.
+  const long long rows = static_cast<long long>(B) * Hkv;
+  auto attend = Attend4<16, true>::fits(rows)  ? Attend4<16, true>::launch
+                : Attend4<8, true>::fits(rows) ? Attend4<8, true>::launch
+                : Attend4<4, true>::fits(rows) ? Attend4<4, true>::launch
+                : Attend4<4, false>::fits(rows) ? Attend4<4, false>::launch
+                                                : Attend4<2, false>::launch;
   return attend(q, k_cache, v_cache, block_table, cache_lens, w.scores, B, G, Hkv, num_pages,
                 max_pages, n_init, scale * k_gain * kLog2e, v_gain, o, sel_out, sw, st);
 }
