@@ -1,7 +1,7 @@
 // Writing and reading the 4-bit paged cache: a pack (store, load) and the new
 // token of a decode step (append).  Moves of 256 bytes of bf16 against 72 bytes
 // of pages per (token, head): bound by memory for a pack, by latency for a step.
-// Measured: 18,245 tokens x 4 heads x 3 tensors (60 MB each way) stored and loaded in
+// Measured: 15,190 tokens x 4 heads x 3 tensors (60 MB each way) stored and loaded in
 // 26.4 us together, 4.5 TB/s; 64 new tokens appended and read back in 6.0 us.
 //
 // Store and load: one thread per 16 channels (32 bytes of bf16, 8 bytes of codes,
