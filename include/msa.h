@@ -183,7 +183,8 @@ MSA_API msa_status_t msa_rope_init(msa_rope_t* rope, int dim, double base, int l
 
 /* x bf16 [T, H, D] -> y bf16 [T, H, D] (y may be x).  w bf16 [D], or NULL for
  * the rotation alone (z = x).  The position of token t is positions[t] (int32
- * [T], any value) or, with positions NULL, its place in cu_seqlens' sequence.
+ * [T], any value) or, with positions NULL, its place in cu_seqlens' sequence;
+ * tokens outside [cu_seqlens[0], cu_seqlens[S]) are then left alone.
  * `rope` is read on the host during the call.  1 <= H <= 256.
  */
 MSA_API msa_status_t msa_qk_norm_rope_ex(const void* x, void* y, int T, int H, int D,
@@ -195,6 +196,7 @@ MSA_API msa_status_t msa_qk_norm_rope_ex(const void* x, void* y, int T, int H, i
 /* Its gradients, as msa_qk_norm_rope_bwd: dx bf16 [T, H, D] (may be dy) and dw
  * fp32 [D] (overwritten; fixed summation order).  With w NULL only dx = the
  * gradient turned back is formed; x, dw and the workspace may then be NULL.
+ * Tokens outside the sequences add nothing to dw and have no dx written.
  */
 MSA_API size_t msa_qk_norm_rope_bwd_ex_workspace_size(int T, int H, int D);
 

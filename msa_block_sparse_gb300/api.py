@@ -550,7 +550,8 @@ def msa_qk_norm_rope_ex(x, w, rope: Rope, cu_seqlens: Optional[torch.Tensor] = N
                         out: Optional[torch.Tensor] = None, eps: float = 1.0e-6):
     """x bf16 [T, H, D] (D 64, 128 or 256) -> out: gemma RMSNorm with weight w (bf16
     [D]; None: no norm), then the rotation `rope` at positions (int32 [T]) or at the
-    tokens' places in cu_seqlens' sequences.  Pass out=x for in place."""
+    tokens' places in cu_seqlens' sequences (tokens outside those are left alone).  Pass
+    out=x for in place."""
     return _native().qk_norm_rope_ex(x, w, _rope_at(rope), cu_seqlens, positions, out, eps)
 
 
@@ -570,6 +571,12 @@ SLAB4 = 9216     # bytes of a page of one head: 128 x 64 of codes, 128 x 8 of sc
 _SCALE = 1.0 / math.sqrt(D)
 
 
+def _gains(gains):
+    if len(gains) != 3:
+        raise ValueError("gains must be those of k, v and k_idx")
+    return gains
+
+
 def msa_cache4_store(k, v, k_idx, k_cache, v_cache, kidx_cache, block_table, cu_seqlens,
                      start: Optional[torch.Tensor] = None, gains=(1.0, 1.0, 1.0)) -> None:
     """Writes a pack (k, v, k_idx bf16 [T, Hkv, 128], post-prologue) into 4-bit caches
@@ -577,7 +584,7 @@ def msa_cache4_store(k, v, k_idx, k_cache, v_cache, kidx_cache, block_table, cu_
     row s of block_table.  k, v or k_idx may be None together with its cache.  gains:
     of k, v and k_idx, powers of two; the same ones have to be given when reading."""
     _native().cache4_store(k, v, k_idx, k_cache, v_cache, kidx_cache, block_table, cu_seqlens, start,
-                           *gains)
+                           *_gains(gains))
 
 
 def msa_cache4_load(k_cache, v_cache, kidx_cache, block_table, cu_seqlens, T: int,
@@ -585,7 +592,8 @@ def msa_cache4_load(k_cache, v_cache, kidx_cache, block_table, cu_seqlens, T: in
                     k_idx=None):
     """The held values of a pack's positions, as bf16 [T, Hkv, 128] each: the inverse of
     msa_cache4_store.  A cache that is None is left out (its result is None)."""
-    return _native().cache4_load(k_cache, v_cache, kidx_cache, block_table, cu_seqlens, T, start, *gains,
+    return _native().cache4_load(k_cache, v_cache, kidx_cache, block_table, cu_seqlens, T, start,
+                                 *_gains(gains),
                                  k, v, k_idx)
 
 
@@ -596,8 +604,8 @@ def msa_decode4_append(q, q_idx, k, v, k_idx, w_q, w_qi, w_k, w_ki, k_cache, v_c
     new token per sequence at position cache_lens - 1, its k, index-k and v held in 4
     bits; returns (q_out, q_idx_out).  Rows of length 0 are padding and left alone."""
     return _native().decode4_append(q, q_idx, k, v, k_idx, w_q, w_qi, w_k, w_ki, k_cache, v_cache,
-                                    kidx_cache, block_table, cache_lens, _rope_at(rope), *gains, q_out,
-                                    q_idx_out, eps)
+                                    kidx_cache, block_table, cache_lens, _rope_at(rope), *_gains(gains),
+                                    q_out, q_idx_out, eps)
 
 
 def msa_decode4_step(q, q_idx, k_cache, v_cache, kidx_cache, block_table, cache_lens,
@@ -606,8 +614,9 @@ def msa_decode4_step(q, q_idx, k_cache, v_cache, kidx_cache, block_table, cache_
                      workspace: Optional[torch.Tensor] = None, n_init: int = 0):
     """msa_decode_step over 4-bit caches: (o bf16 [B, Hq, 128], sel int32 [B, Hkv, 16]),
     Hq = 1 .. 16 heads per KV head.  Rows of length 0 get o = 0, sel = -1."""
+    k_gain, v_gain, _ = _gains(gains)
     return _native().decode4_step(q, q_idx, k_cache, v_cache, kidx_cache, block_table, cache_lens,
-                                  _SCALE if scale is None else scale, gains[0], gains[1], out, sel_out,
+                                  _SCALE if scale is None else scale, k_gain, v_gain, out, sel_out,
                                   workspace, n_init)
 
 

@@ -513,6 +513,12 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   } catch (const PyErrSet&) {
   } catch (const ValueErr& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (const c10::OutOfMemoryError& e) {
+    PyObject* mod = PyImport_ImportModule("torch");
+    PyObject* cls = mod ? PyObject_GetAttrString(mod, "OutOfMemoryError") : nullptr;
+    if (cls) PyErr_SetString(cls, e.what());
+    Py_XDECREF(cls);
+    Py_XDECREF(mod);
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   }

@@ -7,7 +7,7 @@
 //   dz = the pairs of dy turned back (times gain), g = dz (1 + w), xh = x r:
 //   dx = r (g - xh mean(g xh)),  dw = sum over tokens and heads of dz xh
 // Bound by memory: 4 bytes per value forward, 6 backward.  Measured: 16,384 tokens x 64
-// heads x 128 (537 MB) forward 88 us, 6.1 TB/s; gradients of 16,384 x 12 x 256 (302
+// heads x 128 (537 MB) forward 90 us, 6.0 TB/s; gradients of 16,384 x 12 x 256 (302
 // MB) 59 us, 5.1 TB/s, of which 53 the main kernel; 32 tokens x 64 heads 2.8 us.
 //
 // Work: the [T * H, D] rows are cut into runs of consecutive rows, one run per
@@ -57,10 +57,11 @@ __device__ __forceinline__ float2 bf2(uint32_t u) {
 }
 
 // cos and sin (times gain) of the tokens t0 .. t0 + ntok - 1 of the run:
-// table[tok * R + i] = cos, [tok * R + R / 2 + i] = sin of pair i.  Every thread of the
-// CTA takes part; the table may be read after the next barrier.
+// table[tok * R + i] = cos, [tok * R + R / 2 + i] = sin of pair i.  live[tok]: the token
+// is one of cu's sequences (or has a position given).  Every thread of the CTA takes
+// part; both may be read after the next barrier.
 __device__ __forceinline__ void rx_angles(const RxArgs& a, const RxTurns& turns, int t0, int ntok,
-                                          unsigned long long* freq, int* pos, float* table) {
+                                          unsigned long long* freq, int* pos, bool* live, float* table) {
   const int half = a.R >> 1;
   // frequencies by way of shared memory: lanes that index the parameters apart are
   // served one at a time
@@ -69,13 +70,16 @@ __device__ __forceinline__ void rx_angles(const RxArgs& a, const RxTurns& turns,
     const int t = t0 + tok;
     if (a.positions) {
       pos[tok] = __ldg(a.positions + t);
+      live[tok] = true;
     } else {
       int lo = 0, hi = a.S;                  // largest s with cu[s] <= t
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid;
       }
-      pos[tok] = t - __ldg(a.cu + lo);
+      const int first = __ldg(a.cu + lo), end = __ldg(a.cu + lo + 1);
+      pos[tok] = t - first;
+      live[tok] = t >= first && t < end;
     }
   }
   __syncthreads();
@@ -220,6 +224,7 @@ __global__ void __launch_bounds__(kRxThreads, 8) rope_ex_kernel(const RxArgs a, 
   constexpr int kLpr = D / 8, kSlots = kRxThreads / kLpr;
   __shared__ __align__(16) float table[2 * kRxMaxAngles];
   __shared__ int pos[kRxMaxAngles / 8];
+  __shared__ bool live[kRxMaxAngles / 8];
   __shared__ unsigned long long freq[kRxMaxPairs];
   const long long r0 = static_cast<long long>(blockIdx.x) * a.run;
   const int n = static_cast<int>(a.rows - r0 < a.run ? a.rows - r0 : a.run);
@@ -250,7 +255,7 @@ __global__ void __launch_bounds__(kRxThreads, 8) rope_ex_kernel(const RxArgs a, 
 #pragma unroll
     for (int p = 0; p < 4; ++p) w1[p] = __fadd2_rn(wv[p], w1[p]);
   }
-  rx_angles(a, turns, t0, ntok, freq, pos, table);
+  rx_angles(a, turns, t0, ntok, freq, pos, live, table);
   __syncthreads();
   int have = -1;
   float2 cc[4], ss[4];
@@ -284,7 +289,7 @@ __global__ void __launch_bounds__(kRxThreads, 8) rope_ex_kernel(const RxArgs a, 
 #pragma unroll
           for (int p = 0; p < 4; ++p) v[p] = __fmul2_rn(v[p], rr);
         }
-        rx_store<kHalf>(yb + static_cast<size_t>(i) * D, l, v);
+        if (live[tok]) rx_store<kHalf>(yb + static_cast<size_t>(i) * D, l, v);
       }
     }
   }
@@ -299,6 +304,7 @@ __global__ void __launch_bounds__(kRxThreads, 4) rope_ex_bwd_kernel(const RxArgs
   constexpr int kLpr = D / 8, kSlots = kRxThreads / kLpr;
   __shared__ __align__(16) float table[2 * kRxMaxAngles];
   __shared__ int pos[kRxMaxAngles / 8];
+  __shared__ bool live[kRxMaxAngles / 8];
   __shared__ unsigned long long freq[kRxMaxPairs];
   const int c = threadIdx.x & (kLpr - 1), slot = threadIdx.x / kLpr;
   const RxLane l = rx_lane<kHalf>(c, a.R);
@@ -342,15 +348,17 @@ __global__ void __launch_bounds__(kRxThreads, 4) rope_ex_bwd_kernel(const RxArgs
     Pair now, next;
     fetch(slot, now);
     __syncthreads();                              // the previous run's angles are consumed
-    rx_angles(a, turns, t0, ntok, freq, pos, table);
+    rx_angles(a, turns, t0, ntok, freq, pos, live, table);
     __syncthreads();
     int have = -1;
+    bool on = false;
     float2 cc[4], ss[4];
     for (int base = 0; base < n; base += 2 * kSlots) {   // uniform over the CTA
       const int i = base + slot;
       fetch(i + 2 * kSlots, next);
       float2 dz[2][4], xv[2][4], g[2][4];
       float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+      bool put[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         rx_unpack<kHalf>(now.g[k], dz[k]);
@@ -358,8 +366,10 @@ __global__ void __launch_bounds__(kRxThreads, 4) rope_ex_bwd_kernel(const RxArgs
         const int tok = static_cast<int>((static_cast<uint32_t>(h0 + ik) * a.inv) >> 20);
         if (tok != have) {
           have = tok;
+          on = live[tok];
           rx_coefficients(table + tok * a.R, a.R >> 1, l, one, -1.f, cc, ss);
         }
+        put[k] = on;
         rx_turn(dz[k], cc, ss);
         if (kNorm) {
           rx_unpack<kHalf>(now.x[k], xv[k]);
@@ -378,6 +388,7 @@ __global__ void __launch_bounds__(kRxThreads, 4) rope_ex_bwd_kernel(const RxArgs
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (i + k * kSlots >= n) break;
+        if (!put[k]) continue;
         if (kNorm) {
           // r = rsqrt(mean(x^2) + eps), dot = sum(g x):
           // dx = r g - x (r^3 dot / D), dw += dz x r

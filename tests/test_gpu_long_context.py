@@ -120,6 +120,39 @@ def test_prologue_ex(m, case):
     m.msa_check_status()
 
 
+@pytest.mark.parametrize("T,H,D,first,last", [(90, 3, 128, 7, 61), (40, 64, 64, 0, 1), (300, 5, 256, 128, 300),
+                                              (12, 2, 128, 5, 5), (5000, 2, 64, 1, 4999)])
+def test_prologue_ex_leaves_tokens_outside_the_sequences(m, T, H, D, first, last):
+    rng = np.random.default_rng(T)
+    x, dy = f64(bf16(rng.standard_normal((T, H, D)))), f64(bf16(rng.standard_normal((T, H, D))))
+    w = bf16(0.1 * rng.standard_normal(D))
+    cu = i32([first, (first + last) // 2, last])
+    inside = slice(first, last)
+    rope = m.msa_rope(32, 1e6)
+    xt, dyt = bf16(x), bf16(dy)
+    for t in (xt, dyt):                                  # what lies outside is not looked at
+        t[:first] = float("nan")
+        t[last:] = float("nan")
+    y, dx = torch.full_like(xt, 7.0), torch.full_like(xt, 7.0)
+    m.msa_qk_norm_rope_ex(xt, w, rope, cu_seqlens=cu, out=y)
+    _, dw = m.msa_qk_norm_rope_bwd_ex(xt, dyt, w, rope, cu_seqlens=cu, dx=dx)
+    pos = i32(np.concatenate([np.arange((first + last) // 2 - first), np.arange(last - (first + last) // 2)]))
+    if last > first:
+        xi, di = xt[inside].contiguous(), dyt[inside].contiguous()
+        assert torch.equal(y[inside], m.msa_qk_norm_rope_ex(xi, w, rope, positions=pos))
+        ref, dwi = m.msa_qk_norm_rope_bwd_ex(xi, di, w, rope, positions=pos)
+        assert torch.equal(dx[inside], ref)
+        # the same terms in another order: 2^-24 of their magnitudes per addition, 2^10 of them
+        r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-6)
+        terms = (2 * np.abs(dy).max() * np.abs(x * r))[inside].sum((0, 1))
+        within(f64(dw), f64(dwi), 2.0 ** -14 * terms, "dw")
+    else:
+        assert (dw == 0).all()
+    for t in (y, dx):
+        assert (t[:first] == 7.0).all() and (t[last:] == 7.0).all()
+    m.msa_check_status()
+
+
 def test_prologue_ex_is_the_fixed_prologue(m):
     """At the fixed layout it computes what msa_qk_norm_rope does (one bf16 step at most)."""
     rng = np.random.default_rng(5)
