@@ -79,10 +79,10 @@ __device__ __forceinline__ float2 scales_f2(uint32_t two) {
 
 // ---------------------------------------------------------------- scores
 
-constexpr int kScWarps = 12;
+constexpr int kScWarps = 9;
 constexpr int kScThreads = 32 * kScWarps;
 constexpr int kScStages = 2;
-constexpr int kScUnroll = 4;    // tiles of 16 keys whose products overlap
+constexpr int kScUnroll = 8;    // tiles of 16 keys whose products overlap
 constexpr int kScMaxB = 1024;   // rows whose unit counts are summed at a time
 
 struct Score4Smem {
@@ -100,10 +100,11 @@ static_assert(sizeof(Score4Smem) <= 232448, "score shared memory above the 227 K
 
 // Persistent CTAs, one per SM, each with an equal run of the units (row, head,
 // block to score), counted from the lengths by every CTA for itself.  A CTA looks up
-// 384 units at a time, one per thread; then its warps claim units and stream their
+// 288 units at a time, one per thread; then its warps claim units and stream their
 // slabs, each through its own two buffers with bulk copies.  Bound by memory: 64 rows of
-// 8k - 32k tokens x 4 heads, 379 MB, 66 us, 5.7 TB/s (the first slab is there after
-// 3 to 7 us, the median SM is done at 56).  Loads straight to registers took 91 us,
+// 8k - 32k tokens x 4 heads, 379 MB, 64 us, 5.9 TB/s.  166 KB in flight per SM: 12 warps
+// (221 KB) took 67 us and left no room for a CTA of the attention to start beside them (the
+// whole step 91.2 us, with 9 warps 88.1), 6 warps 76.  Loads straight to registers took 91 us,
 // claims across SMs from a counter in global memory 69.
 __global__ void __launch_bounds__(kScThreads, 1) decode4_score_kernel(
     const __nv_bfloat16* __restrict__ q_idx, const uint8_t* __restrict__ kidx,
