@@ -19,10 +19,21 @@ __device__ __forceinline__ int slab_code(int slot) { return slot * kCodeBytes; }
 __device__ __forceinline__ int slab_scale(int slot) { return kSlabCodes + slot * kScaleBytes; }
 
 // Scale byte of 16 channels from their largest magnitude (after the gain).
-// Both roundings are the format's: /6 in fp32 (correctly rounded), then e4m3
-// to nearest even with saturation.
+// Both roundings are the format's: /6 in fp32, then e4m3 to nearest even with
+// saturation.  The quotient is a times the rounded 1/6, corrected by its exact
+// residual a - 6 q, which rounds it correctly (Markstein 1990) unless it underflows, far
+// below the smallest scale; what is cut off saturates all the same.
 __device__ __forceinline__ uint32_t scale_byte(float amax) {
-  return __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.0f), __NV_SATFINITE, __NV_E4M3);
+  constexpr float kSixth = 1.0f / 6.0f;
+  const float a = fminf(amax, 0x1p100f), q = a * kSixth;
+  return __nv_cvt_float_to_fp8(fmaf(fmaf(-6.0f, q, a), kSixth, q), __NV_SATFINITE, __NV_E4M3);
+}
+
+// 1 / x to 2^-22 or so, for normal x
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ float scale_value(uint32_t byte) {
@@ -33,11 +44,11 @@ __device__ __forceinline__ float2 word_f2(uint32_t u) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
 }
 
-// e2m1 codes of the pair x divided by a scale s > 0 (ns = -s; nr = -1 / s, rounded);
-// low nibble = x.x.  The quotient is formed as x / s rounded twice at most and corrected
-// once by its exact residual q s - x: a quotient on the border of two codes has few
-// bits, so the corrected value hits it exactly and the tie goes to the even code, as
-// in the definition.  -0 stays -0.
+// e2m1 codes of the pair x divided by a scale s > 0 (rs near 1 / s); low nibble = x.x.
+// The quotient x rs, good to 2^-21, is corrected once by its exact residual q s - x and is
+// then off by 2^-40 before its last rounding: a quotient on the border of two codes has
+// few bits, so the corrected value hits it exactly and the tie goes to the even code, as
+// in the definition; any other is 2^-12 or more away (8 bits over 4).  -0 stays -0.
 __device__ __forceinline__ uint32_t code_pair(float2 x, float s, float rs) {
   const float2 q = __fmul2_rn(x, make_float2(rs, rs));
   const float2 e = __ffma2_rn(q, make_float2(s, s), make_float2(-x.x, -x.y));
@@ -65,7 +76,7 @@ __device__ __forceinline__ Scale16 scale16(uint32_t m, float gain, float inv_gai
   const float amax = __uint_as_float(m << 16);
   r.byte = scale_byte(amax * inv_gain);
   r.s = scale_value(r.byte) * gain;
-  r.rs = r.byte ? __frcp_rn(r.s) : 0.f;
+  r.rs = r.byte ? rcp(r.s) : 0.f;
   if (amax * 0x1p-30f > r.s && r.byte) r.cut = 8.f * r.s;   // saturated: any cut above 6 scales
   return r;
 }
