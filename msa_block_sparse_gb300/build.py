@@ -77,7 +77,7 @@ def _link_binding(obj: str):
     tmp = BINDING + ".tmp"
     _run([shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", PKG, "-lmsa",
           "-Wl,-rpath,$ORIGIN", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10",
-          "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"], "link of the binding")
+          "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"], "link of the binding")
     os.replace(tmp, BINDING)
 
 

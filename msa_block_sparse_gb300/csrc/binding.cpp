@@ -7,8 +7,7 @@
 // No computation happens here.  A wrong argument raises ValueError, a refusal of the
 // library raises MSAError, as everywhere in the package.
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -64,8 +63,9 @@ struct Call {
     throw ValueErr(s.str());
   }
   void* stream() const { return c10::cuda::getCurrentCUDAStream(dev).stream(); }
-  at::TensorOptions options(at::ScalarType t) const {
-    return at::TensorOptions().dtype(t).device(at::Device(at::kCUDA, dev));
+  // straight from the allocator: a fifth of a call's host time less than by at::empty
+  Tensor fresh(at::ScalarType type, at::IntArrayRef shape) const {
+    return Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, dev), std::nullopt));
   }
   // Address of a contiguous tensor of this type, shape and device
   void* arg(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape) const {
@@ -89,7 +89,7 @@ struct Call {
   }
   // The given output, or a new one
   Tensor out(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape) const {
-    if (none(o)) return at::empty(shape, options(type));
+    if (none(o)) return fresh(type, shape);
     const Tensor& t = tensor(o, name);
     arg(t, name, type, shape);
     return t;
@@ -102,7 +102,7 @@ struct Workspace {
   Workspace(const Call& c, PyObject* o, size_t size) {
     if (none(o)) {
       bytes = size < 256 ? 256 : size;
-      t = at::empty({static_cast<int64_t>(bytes)}, c.options(at::kByte));
+      t = c.fresh(at::kByte, {static_cast<int64_t>(bytes)});
       return;
     }
     t = tensor(o, "workspace");

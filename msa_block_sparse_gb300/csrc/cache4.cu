@@ -17,7 +17,7 @@ namespace msa {
 
 namespace {
 
-constexpr int kC4Threads = 256;
+constexpr int kC4Threads = 128;
 constexpr int kC4Tokens = kC4Threads / 8;   // tokens of one head that a CTA takes together
 
 struct Cache4Args {
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kC4Threads) cache4_load_kernel(const Cache4Arg
 // head) pairs are split among several per group when there are few groups.
 static dim3 c4_grid(int T, int jobs) {
   const int groups = (T + kC4Tokens - 1) / kC4Tokens;
-  const int want = (8 * device_sm_count() + groups - 1) / groups;
+  const int want = (20 * device_sm_count() + groups - 1) / groups;
   return dim3(groups, want < jobs ? want : jobs);
 }
 
