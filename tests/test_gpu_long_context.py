@@ -19,6 +19,9 @@ largest relative rounding of bf16.
     |o error| <= (2^-10 + 2^-10) max|v| + 2^-8 |o|.
 """
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -841,6 +844,40 @@ def test_prefill_fork_decode_together(m):
     a = m.msa_cache4_load(*caches, table[:1].contiguous(), i32([0, 1000]), 1000)
     c = m.msa_cache4_load(*caches, table[4:5].contiguous(), i32([0, 1000]), 1000)
     assert all(torch.equal(x, y) for x, y in zip(a, c))
+
+
+CAPTURE_FIRST = """
+import torch, sys
+import msa_block_sparse_gb300 as m
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+bf = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+rope, B = m.msa_rope(64, 1e7), int(sys.argv[1])
+caches = [torch.zeros(B * 20, 1, 9216, dtype=torch.uint8, device="cuda") for _ in range(3)]
+table, lens, ref = i32([[-1] * 20] * B), i32([0] * B), i32([0] * (B * 20))
+add, one, rows = i32([2300] * B), i32([1] * B), i32(list(range(B)))
+w, x = bf(4, 128), [bf(B, h, 128) for h in (16, 1, 1, 1, 1)]
+g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+torch.cuda.synchronize()
+with torch.cuda.graph(g, stream=st):
+    m.msa_pages_extend(add, table, lens, ref, caches)
+    m.msa_pages_extend(one, table, lens, ref, caches)
+    q, qi = m.msa_decode4_append(*x, *w, *caches, table, lens, rope)
+    o, sel = m.msa_decode4_step(q, qi, *caches, table, lens)
+    m.msa_pages_free(rows, table, lens, ref)
+for _ in range(2):
+    g.replay()
+torch.cuda.synchronize()
+m.msa_check_status()
+assert lens.tolist() == [0] * B and not ref.any() and bool(torch.isfinite(o.float()).all())
+assert bool((sel[:, 0, -1] == 17).all())
+"""
+
+
+@pytest.mark.parametrize("B", [2, 30, 60, 100, 200])     # each choice of CTAs per row
+def test_first_calls_of_a_process_are_captured(m, B):
+    r = subprocess.run([sys.executable, "-c", CAPTURE_FIRST, str(B)], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_captured_steps_and_streams(m):

@@ -319,3 +319,14 @@ def test_binding_refuses_cpu_tensors():
         api.msa_pages_fork(i[:1], i[:1], table, i, torch.zeros(8, dtype=torch.int32))
     with pytest.raises(ValueError):
         api.msa_pages_copy(i, i, [slab])
+
+
+def test_gains_are_three():
+    with pytest.raises(ValueError, match="gains"):
+        api.msa_cache4_store(None, None, None, None, None, None, None, None, gains=(1.0, 1.0))
+    with pytest.raises(ValueError, match="gains"):
+        api.msa_cache4_load(None, None, None, None, None, 1, gains=(1.0,))
+    with pytest.raises(ValueError, match="gains"):
+        api.msa_decode4_append(*[None] * 14, api.msa_rope(64), gains=(1.0, 1.0))
+    with pytest.raises(ValueError, match="gains"):
+        api.msa_decode4_step(*[None] * 7, gains=(1.0, 1.0, 1.0, 1.0))
