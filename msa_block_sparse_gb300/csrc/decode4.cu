@@ -486,9 +486,19 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
     const uint32_t at15 = __ballot_sync(0xffffffffu, mine != 0ull && before == kTopK - 2);
     const unsigned long long bar =
         at15 ? __shfl_sync(0xffffffffu, mine, __ffs(at15) - 1) : 1ull;
+    int cnt = 0, at[kAtPer];                       // places among the warp's candidates
+#pragma unroll
+    for (int r = 0; r < kAtPer; ++r) {
+      const uint32_t in = __ballot_sync(0xffffffffu, key[r] >= bar);
+      at[r] = cnt + __popc(in & ((1u << lane) - 1u));
+      cnt += __popc(in);
+    }
+    int from = 0;
+    if (lane == 0 && cnt > 0) from = atomicAdd(&sm.ncand, cnt);
+    from = __shfl_sync(0xffffffffu, from, 0);
 #pragma unroll
     for (int r = 0; r < kAtPer; ++r)
-      if (key[r] >= bar) sm.cand[atomicAdd(&sm.ncand, 1)] = key[r];
+      if (key[r] >= bar) sm.cand[from + at[r]] = key[r];
     __syncthreads();
     if (warp == 0) {
       const int nc = sm.ncand;
