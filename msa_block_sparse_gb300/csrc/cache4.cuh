@@ -44,16 +44,23 @@ __device__ __forceinline__ float2 word_f2(uint32_t u) {
   return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
 }
 
-// e2m1 codes of the pair x divided by a scale s > 0 (rs near 1 / s); low nibble = x.x.
-// The quotient x rs, good to 2^-21, is corrected once by its exact residual q s - x and is
-// then off by 2^-40 before its last rounding: a quotient on the border of two codes has
-// few bits, so the corrected value hits it exactly and the tie goes to the even code, as
-// in the definition; any other is 2^-12 or more away (8 bits over 4).  -0 stays -0.
-__device__ __forceinline__ uint32_t code_pair(float2 x, float s, float rs) {
-  const float2 q = __fmul2_rn(x, make_float2(rs, rs));
-  const float2 e = __ffma2_rn(q, make_float2(s, s), make_float2(-x.x, -x.y));
-  return __nv_cvt_float2_to_fp4x2(__ffma2_rn(e, make_float2(-rs, -rs), q), __NV_E2M1,
-                                  cudaRoundNearest);
+// e2m1 codes of the pair x divided by a scale s > 0, from nx = -x and nrs near -1 / s;
+// low nibble = x.x.  The quotient q = nx nrs, good to 2^-21, is corrected once by its exact
+// residual q s - x and is then off by 2^-40 before its last rounding: a quotient on the
+// border of two codes has few bits, so the corrected value hits it exactly and the tie
+// goes to the even code, as in the definition; any other is 2^-12 or more away (8 bits over
+// 4).  -0 stays -0.
+__device__ __forceinline__ uint32_t code_pair(float2 nx, float s, float nrs) {
+  const float2 r2 = make_float2(nrs, nrs);
+  const float2 q = __fmul2_rn(nx, r2);
+  const float2 e = __ffma2_rn(q, make_float2(s, s), nx);
+  return __nv_cvt_float2_to_fp4x2(__ffma2_rn(e, r2, q), __NV_E2M1, cudaRoundNearest);
+}
+
+// The negatives of two packed bf16: an integer addition flips a float's sign bit
+__device__ __forceinline__ float2 neg_word_f2(uint32_t u) {
+  return make_float2(__uint_as_float(u * 0x10000u + 0x80000000u),
+                     __uint_as_float((u & 0xFFFF0000u) ^ 0x80000000u));
 }
 
 // Scale of 16 channels from their largest magnitude m (bf16 bits): the byte, and
@@ -62,7 +69,7 @@ __device__ __forceinline__ uint32_t code_pair(float2 x, float s, float rs) {
 // largest held value) are to be cut to +-*cut first.
 struct Scale16 {
   uint32_t byte;
-  float s, rs, cut;      // cut: 0 = no need
+  float s, nrs, cut;     // nrs: near -1 / s; cut: 0 = no need
 };
 
 __device__ __forceinline__ Scale16 scale16(uint32_t m, float gain, float inv_gain) {
@@ -70,13 +77,13 @@ __device__ __forceinline__ Scale16 scale16(uint32_t m, float gain, float inv_gai
   r.cut = 0.f;
   if (m >= 0x7F80u) {                              // an infinity or NaN
     r.byte = 0x7Fu;
-    r.s = r.rs = 0.f;
+    r.s = r.nrs = 0.f;
     return r;
   }
   const float amax = __uint_as_float(m << 16);
   r.byte = scale_byte(amax * inv_gain);
   r.s = scale_value(r.byte) * gain;
-  r.rs = r.byte ? rcp(r.s) : 0.f;
+  r.nrs = r.byte ? -rcp(r.s) : 0.f;
   if (amax * 0x1p-30f > r.s && r.byte) r.cut = 8.f * r.s;   // saturated: any cut above 6 scales
   return r;
 }
@@ -88,7 +95,7 @@ __device__ __forceinline__ uint32_t cut_word(const Scale16& sc, uint32_t x) {
 }
 
 __device__ __forceinline__ uint32_t code_word(const Scale16& sc, uint32_t x) {
-  return code_pair(word_f2(x), sc.s, sc.rs);
+  return code_pair(neg_word_f2(x), sc.s, sc.nrs);
 }
 
 // Codes (8 bytes) and scale byte of 16 bf16 channels (8 packed words).
