@@ -508,6 +508,10 @@ def check_decode(m, lens, G, H, seed=0, n_init=0, gains=(1.0, 1.0), max_pages=No
     ((129, 5000, 1) * 13, 1, 1, {}),                      # 39 rows
     ((129, 2500, 1) * 27, 2, 1, dict(n_init=2)),          # 81 rows
     ((0, 0), 16, 2, {}),
+    ((2100, 90) * 20, 15, 1, {}),                         # 40, 60, 100 and 160 rows of many heads
+    ((700, 2300) * 15, 16, 2, {}),
+    ((2200, 40) * 25, 16, 2, {}),
+    ((100, 2100) * 40, 16, 2, dict(n_init=1)),
 ], ids=str)
 def test_decode4(m, lens, G, H, kw):
     check_decode(m, lens, G, H, seed=len(lens), **kw)
