@@ -8,7 +8,7 @@
 //   dx = r (g - xh mean(g xh)),  dw = sum over tokens and heads of dz xh
 // Bound by memory: 4 bytes per value forward, 6 backward.  Measured: 16,384 tokens x 64
 // heads x 128 (537 MB) forward 88 us, 6.1 TB/s; gradients of 16,384 x 12 x 256 (302
-// MB) 59 us, 5.1 TB/s, of which 53 the main kernel; 32 tokens x 64 heads 2.8 us.
+// MB) 57 us, 5.3 TB/s; 32 tokens x 64 heads 2.8 us.
 //
 // Work: the [T * H, D] rows are cut into runs of consecutive rows, one run per
 // CTA (grid-stride in the backward).  A row belongs to D / 8 threads with 8
@@ -125,6 +125,21 @@ __device__ __forceinline__ RxRow rx_load(const __nv_bfloat16* row, const RxLane&
     r.b = __ldcs(reinterpret_cast<const uint2*>(row + l.off1));
   } else {
     const uint4 u = __ldcs(reinterpret_cast<const uint4*>(row + l.off0));
+    r.a = make_uint2(u.x, u.y);
+    r.b = make_uint2(u.z, u.w);
+  }
+  return r;
+}
+
+// The same from shared memory
+template <bool kHalf>
+__device__ __forceinline__ RxRow rx_read(const __nv_bfloat16* row, const RxLane& l) {
+  RxRow r;
+  if (kHalf) {
+    r.a = *reinterpret_cast<const uint2*>(row + l.off0);
+    r.b = *reinterpret_cast<const uint2*>(row + l.off1);
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(row + l.off0);
     r.a = make_uint2(u.x, u.y);
     r.b = make_uint2(u.z, u.w);
   }
@@ -295,19 +310,74 @@ __global__ void __launch_bounds__(kRxThreads, 8) rope_ex_kernel(const RxArgs a, 
   }
 }
 
-// Two rows at a time, the next two rows' loads in flight: their reductions share
-// shuffles and their chains overlap.
+// Two rows of a thread at a time: their reductions share shuffles and their chains
+// overlap.  Rows come through a ring of bulk copies per warp (a stage holds the
+// warp's next 1 KB of dy and of x) that runs ahead across runs.  16,384 x 12 x 256, with
+// the sum of dw behind it: 57.2 us (1, 3, 4 stages: 62.2, 58.0, 59.0; loads to registers a
+// pair of rows ahead 59.5; 5 CTAs per SM 64.5).
+constexpr int kRxStages = 2;
+
+struct RxBwdSmem {
+  alignas(128) uint8_t ring[kRxThreads / 32][kRxStages][2][1024];
+  alignas(16) float table[2 * kRxMaxAngles];
+  unsigned long long freq[kRxMaxPairs];
+  uint64_t full[kRxThreads / 32][kRxStages];
+  int pos[kRxMaxAngles / 8];
+  bool live[kRxMaxAngles / 8];
+};
+
 template <int D, bool kNorm, bool kHalf>
 __global__ void __launch_bounds__(kRxThreads, 4) rope_ex_bwd_kernel(const RxArgs a,
-                                                                    const RxTurns turns) {
+                                                                    const RxTurns turns,
+                                                                    uint32_t* status) {
   pdl_enter();
   constexpr int kLpr = D / 8, kSlots = kRxThreads / kLpr;
-  __shared__ __align__(16) float table[2 * kRxMaxAngles];
-  __shared__ int pos[kRxMaxAngles / 8];
-  __shared__ bool live[kRxMaxAngles / 8];
-  __shared__ unsigned long long freq[kRxMaxPairs];
+  constexpr int kPass = 32 / kLpr;                 // rows of a warp side by side
+  constexpr int kWarpRows = 2 * kPass, kCtaRows = 2 * kSlots;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  RxBwdSmem& sm = *reinterpret_cast<RxBwdSmem*>(smem_raw);
+  float* table = sm.table;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = threadIdx.x & (kLpr - 1), slot = threadIdx.x / kLpr;
   const RxLane l = rx_lane<kHalf>(c, a.R);
+  if (lane == 0) {
+    for (int i = 0; i < kRxStages; ++i) mbar_init(&sm.full[warp][i], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  const long long stride = static_cast<long long>(gridDim.x) * a.run;
+  auto rows_of = [&](long long r0) {
+    return static_cast<int>(a.rows - r0 < a.run ? a.rows - r0 : a.run);
+  };
+  // ---- loads: the warp's part of chunk after chunk, run after run
+  long long load_r0 = static_cast<long long>(blockIdx.x) * a.run;
+  int load_base = 0;
+  uint32_t nload = 0, nuse = 0;
+  bool dead = false;                               // a wait ran out
+  auto load = [&]() {
+    if (load_r0 >= a.rows) return;
+    const int n = rows_of(load_r0);
+    if (lane == 0) {
+      const int st = nload % kRxStages, i = load_base + warp * kWarpRows;
+      const int rows = n - i < kWarpRows ? n - i : kWarpRows;
+      if (rows > 0) {
+        const uint32_t bytes = rows * D * sizeof(__nv_bfloat16);
+        const size_t at = static_cast<size_t>(load_r0 + i) * D;
+        mbar_arrive_expect_tx(&sm.full[warp][st], kNorm ? 2 * bytes : bytes);
+        bulk_load(sm.ring[warp][st][0], a.dy + at, bytes, &sm.full[warp][st]);
+        if (kNorm) bulk_load(sm.ring[warp][st][1], a.x + at, bytes, &sm.full[warp][st]);
+      } else {
+        mbar_arrive(&sm.full[warp][st]);           // no rows of this chunk are the warp's
+      }
+    }
+    ++nload;
+    load_base += kCtaRows;
+    if (load_base >= n) {
+      load_base = 0;
+      load_r0 += stride;
+    }
+  };
+  for (int i = 0; i < kRxStages; ++i) load();
   float2 one[4], w1[4], aw[4];
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
@@ -322,57 +392,56 @@ __global__ void __launch_bounds__(kRxThreads, 4) rope_ex_bwd_kernel(const RxArgs
 #pragma unroll
     for (int p = 0; p < 4; ++p) w1[p] = __fadd2_rn(w1[p], one[p]);
   }
-  for (long long r0 = static_cast<long long>(blockIdx.x) * a.run; r0 < a.rows;
-       r0 += static_cast<long long>(gridDim.x) * a.run) {
-    const int n = static_cast<int>(a.rows - r0 < a.run ? a.rows - r0 : a.run);
+  for (long long r0 = static_cast<long long>(blockIdx.x) * a.run; r0 < a.rows; r0 += stride) {
+    const int n = rows_of(r0);
     const int t0 = static_cast<int>(r0 / a.H);
     const int h0 = static_cast<int>(r0 - static_cast<long long>(t0) * a.H);
     const int ntok = (h0 + n + a.H - 1) / a.H;
-    const __nv_bfloat16* gb = a.dy + r0 * D;
-    const __nv_bfloat16* xb = kNorm ? a.x + r0 * D : nullptr;
     __nv_bfloat16* ob = a.y + r0 * D;
-    struct Pair {
-      RxRow g[2], x[2];
-    };
-    auto fetch = [&](int i, Pair& q) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int ik = i + k * kSlots;
-        q.g[k].a = q.g[k].b = q.x[k].a = q.x[k].b = make_uint2(0u, 0u);
-        if (ik < n) {
-          q.g[k] = rx_load<kHalf>(gb + static_cast<size_t>(ik) * D, l);
-          if (kNorm) q.x[k] = rx_load<kHalf>(xb + static_cast<size_t>(ik) * D, l);
-        }
-      }
-    };
-    Pair now, next;
-    fetch(slot, now);
     __syncthreads();                              // the previous run's angles are consumed
-    rx_angles(a, turns, t0, ntok, freq, pos, live, table);
+    rx_angles(a, turns, t0, ntok, sm.freq, sm.pos, sm.live, table);
     __syncthreads();
     int have = -1;
     bool on = false;
     float2 cc[4], ss[4];
-    for (int base = 0; base < n; base += 2 * kSlots) {   // uniform over the CTA
-      const int i = base + slot;
-      fetch(i + 2 * kSlots, next);
+    for (int base = 0; base < n; base += kCtaRows) {   // uniform over the CTA
+      const int st = nuse % kRxStages;
+      if (!dead && !__all_sync(0xffffffffu, mbar_wait(&sm.full[warp][st], (nuse / kRxStages) & 1, status, 70))) {
+        for (uint32_t k = nuse + 1; k < nload; ++k)    // wait (bounded) for what is on its way
+          (void)mbar_wait(&sm.full[warp][k % kRxStages], (k / kRxStages) & 1, status, 71);
+        dead = true;
+      }
+      if (dead) continue;
+      ++nuse;
+      // rows i and i + kPass; behind the run's end the ring holds old rows, which are
+      // read but not used
+      const int i = base + warp * kWarpRows + lane / kLpr;
+      RxRow raw[2][2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int x = 0; x < (kNorm ? 2 : 1); ++x)
+          raw[k][x] = rx_read<kHalf>(reinterpret_cast<const __nv_bfloat16*>(sm.ring[warp][st][x]) +
+                                         (lane / kLpr + k * kPass) * D, l);
+      __syncwarp();
+      load();
       float2 dz[2][4], xv[2][4], g[2][4];
       float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
       bool put[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        rx_unpack<kHalf>(now.g[k], dz[k]);
-        const int ik = i + k * kSlots < n ? i + k * kSlots : n - 1;
+        rx_unpack<kHalf>(raw[k][0], dz[k]);
+        const int ik = i + k * kPass < n ? i + k * kPass : n - 1;
         const int tok = static_cast<int>((static_cast<uint32_t>(h0 + ik) * a.inv) >> 20);
         if (tok != have) {
           have = tok;
-          on = live[tok];
+          on = sm.live[tok];
           rx_coefficients(table + tok * a.R, a.R >> 1, l, one, -1.f, cc, ss);
         }
-        put[k] = on;
+        put[k] = on && i + k * kPass < n;
         rx_turn(dz[k], cc, ss);
         if (kNorm) {
-          rx_unpack<kHalf>(now.x[k], xv[k]);
+          rx_unpack<kHalf>(raw[k][1], xv[k]);
           float2 q = make_float2(0.f, 0.f), d = q;
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
@@ -387,7 +456,6 @@ __global__ void __launch_bounds__(kRxThreads, 4) rope_ex_bwd_kernel(const RxArgs
       if (kNorm) rx_sum4<kLpr>(sum[0][0], sum[0][1], sum[1][0], sum[1][1]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        if (i + k * kSlots >= n) break;
         if (!put[k]) continue;
         if (kNorm) {
           // r = rsqrt(mean(x^2) + eps), dot = sum(g x):
@@ -401,9 +469,8 @@ __global__ void __launch_bounds__(kRxThreads, 4) rope_ex_bwd_kernel(const RxArgs
             dz[k][p] = __ffma2_rn(xv[k][p], kk, __fmul2_rn(g[k][p], rr));
           }
         }
-        rx_store<kHalf>(ob + static_cast<size_t>(i + k * kSlots) * D, l, dz[k]);
+        rx_store<kHalf>(ob + static_cast<size_t>(i + k * kPass) * D, l, dz[k]);
       }
-      now = next;
     }
   }
   if (kNorm) {
@@ -556,12 +623,15 @@ static msa_status_t rx_backward(const RopeExJob& j, const msa_rope_t& rope, floa
   a.dw_part = dw_part;
   const RxTurns turns = rx_turns(rope);
   const int ctas = rx_bwd_ctas(a.rows, a.run);
+  uint32_t* sw = nullptr;
+  MSA_TRY(status_word(&sw));
   {
     TraceScope trace_("rope_ex_bwd_kernel", stream);
     const bool half = rope.layout == MSA_ROPE_HALF;
-    launch_pdl(j.w ? (half ? rope_ex_bwd_kernel<D, true, true> : rope_ex_bwd_kernel<D, true, false>)
-                   : (half ? rope_ex_bwd_kernel<D, false, true> : rope_ex_bwd_kernel<D, false, false>),
-               ctas, kRxThreads, 0, stream, a, turns);
+    auto kernel = j.w ? (half ? rope_ex_bwd_kernel<D, true, true> : rope_ex_bwd_kernel<D, true, false>)
+                      : (half ? rope_ex_bwd_kernel<D, false, true> : rope_ex_bwd_kernel<D, false, false>);
+    MSA_TRY(ensure_smem(kernel, sizeof(RxBwdSmem), "rope_ex_bwd_kernel"));
+    launch_pdl(kernel, ctas, kRxThreads, sizeof(RxBwdSmem), stream, a, turns, sw);
   }
   msa_status_t e = check_launch("rope_ex_bwd_kernel");
   if (e != MSA_OK || !j.w) return e;
