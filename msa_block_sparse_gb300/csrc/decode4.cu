@@ -201,13 +201,8 @@ __global__ void __launch_bounds__(kScThreads, 1) decode4_score_kernel(
       for (int i = 0; i < kScStages; ++i) load();
       while (nuse < nload) {
         const int st = nuse % kScStages;
-        if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[warp][st], (nuse / kScStages) & 1, status, 81))) {
-          for (++nuse; nuse < nload; ++nuse)       // wait (bounded) for what is on its way
-            (void)mbar_wait(&sm.full[warp][nuse % kScStages], (nuse / kScStages) & 1, status, 82);
-          dead = true;
-          break;
-        }
-        ++nuse;
+        __syncwarp();                              // lane 0's entry of the unit
+        // the row's q, while the slab is on its way
         const int unit = sm.at[warp][st], bh = sm.bh[unit];
         if (bh != have_bh) {
           have_bh = bh;
@@ -228,6 +223,13 @@ __global__ void __launch_bounds__(kScThreads, 1) decode4_score_kernel(
               bq[hf][t][1] = col ? bf2_to_h2(w.y, f) : 0u;
             }
         }
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.full[warp][st], (nuse / kScStages) & 1, status, 81))) {
+          for (++nuse; nuse < nload; ++nuse)       // wait (bounded) for what is on its way
+            (void)mbar_wait(&sm.full[warp][nuse % kScStages], (nuse / kScStages) & 1, status, 82);
+          dead = true;
+          break;
+        }
+        ++nuse;
         const uint8_t* slab = sm.slab[warp][st];
         float best = -INFINITY;
 #pragma unroll kScUnroll
