@@ -470,7 +470,8 @@ MSA_API msa_status_t msa_decode4_append(const void* q, const void* q_idx, const 
  * lengths outside [0, 128 max_pages] set MSA_STATUS_BOUNDS and are treated
  * so too.  A page outside [0, num_pages) sets MSA_STATUS_BOUNDS; its block scores
  * -infinity and, if it is selected all the same, has no keys.  Slots of the
- * own page behind the sequence's end may hold anything.  kidx_gain scales all
+ * own page behind the sequence's end may hold anything.  scale > 0 and its product
+ * with k_gain have to be finite.  kidx_gain scales all
  * scores of a call alike and is not needed.
  */
 MSA_API size_t msa_decode4_step_workspace_size(int B, int Hq, int Hkv, int max_pages);

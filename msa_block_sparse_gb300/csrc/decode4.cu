@@ -955,6 +955,8 @@ msa_status_t msa_decode4_step(const void* q, const void* q_idx, const void* k_ca
   if (!(scale > 0.0f) || !std::isfinite(scale))
     return fail(MSA_ERR_INVALID_ARG, "scale must be finite and > 0");
   MSA_TRY(check_gains(k_gain, v_gain, 1.0f));
+  if (!std::isfinite(scale * k_gain * kLog2e))
+    return fail(MSA_ERR_INVALID_ARG, "scale * k_gain overflows");
   if (n_init < 0 || n_init > kTopK - 1)
     return fail(MSA_ERR_INVALID_ARG, "n_init %d outside [0, %d]", n_init, kTopK - 1);
   if (workspace_bytes < msa_decode4_step_workspace_size(B, Hq, Hkv, max_pages))

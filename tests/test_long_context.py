@@ -330,3 +330,10 @@ def test_gains_are_three():
         api.msa_decode4_append(*[None] * 14, api.msa_rope(64), gains=(1.0, 1.0))
     with pytest.raises(ValueError, match="gains"):
         api.msa_decode4_step(*[None] * 7, gains=(1.0, 1.0, 1.0, 1.0))
+
+
+def test_decode_scale_times_gain_must_be_finite(lib):
+    n = lib.msa_decode4_step_workspace_size(1, 16, 1, 4)
+    args = [FAKE] * 7 + [1, 16, 1, 8, 4]
+    assert lib.msa_decode4_step(*args, 1e30, 2.0 ** 64, 1.0, 0, FAKE, None, FAKE, n, None) == 1
+    assert b"overflows" in lib.msa_last_error()
