@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(kPgThreads) pages_extend_kernel(
     if (lane == 0) done[b] = ok ? 1 : 0;
     if (!ok) continue;
     const int L = lens[b];
+    __syncwarp();                                  // every lane has the old length before it is replaced
     int32_t* row = table + static_cast<size_t>(b) * max_pages;
     for (int j = lane; j < need; j += 32) {
       const int pg = free_list[pl.x + j];
