@@ -32,7 +32,7 @@ namespace msa {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLog2e = 1.4426950408889634;
 
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -387,8 +387,8 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
     const __nv_bfloat16* __restrict__ q, const uint8_t* __restrict__ kc,
     const uint8_t* __restrict__ vc, const int32_t* __restrict__ table,
     const int32_t* __restrict__ lens, const float* __restrict__ scores, int G, int Hkv,
-    int num_pages, int max_pages, int n_init, float sl2, float v_gain, __nv_bfloat16* __restrict__ o,
-    int32_t* __restrict__ sel_out, uint32_t* status) {
+    int num_pages, int max_pages, int n_init, float sl2, int sl2_exp, float v_gain,
+    __nv_bfloat16* __restrict__ o, int32_t* __restrict__ sel_out, uint32_t* status) {
   if (max_pages <= kTopK) pdl_wait();              // no scores' kernel stands in between
   extern __shared__ __align__(128) uint8_t smem_raw[];
   using Smem = Attend4Smem<NS, kWhole>;
@@ -401,7 +401,10 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
   const int len = lens[b];
   // q as the A operand of the 8 k-steps: rows g and g + 8 in fp16, each with a power
   // of two; thread c of a row has channels 32 c .. 32 c + 31.  Each warp makes and
-  // stores two k-steps.
+  // stores two k-steps.  f0, f1: factor of the rows' sums, scale * k_gain * log2(e) over
+  // that power (sl2 in [1, 2] times 2^sl2_exp).  It stays a normal, finite fp32: where it would
+  // fall below, the sums (below 2^35) times 2^-126 are 0 for the softmax as well, and a
+  // masked key's -inf stays -inf, which 0 would turn into a NaN.
   float f0, f1;
   {
     uint4 a0, a1;
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const int e = row_shift(m);
       const float f = exp2i(e);
-      (half ? f1 : f0) = sl2 * exp2i(-e);
+      (half ? f1 : f0) = sl2 * exp2i(max(-126, min(126, sl2_exp - e)));
       const uint4 mine = warp == 0 ? x[0] : (warp == 1 ? x[1] : (warp == 2 ? x[2] : x[3]));
       (half ? a0.y : a0.x) = bf2_to_h2(mine.x, f);
       (half ? a0.w : a0.z) = bf2_to_h2(mine.y, f);
@@ -894,8 +897,10 @@ struct Attend4 {
 
   static msa_status_t launch(const void* q, const void* kc, const void* vc, const int32_t* table,
                              const int32_t* lens, const float* scores, int B, int G, int Hkv,
-                             int num_pages, int max_pages, int n_init, float sl2, float v_gain, void* o,
-                             int32_t* sel_out, uint32_t* sw, cudaStream_t stream) {
+                             int num_pages, int max_pages, int n_init, double logit_scale, float v_gain,
+                             void* o, int32_t* sel_out, uint32_t* sw, cudaStream_t stream) {
+    int e = 0;
+    const float sl2 = static_cast<float>(2.0 * std::frexp(logit_scale, &e));
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     MSA_TRY(prepare(&cfg, attr, B * Hkv));
@@ -904,7 +909,7 @@ struct Attend4 {
     TraceScope trace_("decode4_attend_kernel", stream);
     cudaLaunchKernelEx(&cfg, decode4_attend_kernel<NS, kWhole>, static_cast<const __nv_bfloat16*>(q),
                        static_cast<const uint8_t*>(kc), static_cast<const uint8_t*>(vc), table, lens,
-                       scores, G, Hkv, num_pages, max_pages, n_init, sl2, v_gain,
+                       scores, G, Hkv, num_pages, max_pages, n_init, sl2, e - 1, v_gain,
                        static_cast<__nv_bfloat16*>(o), sel_out, sw);
     return check_launch("decode4_attend_kernel");
   }
@@ -955,7 +960,7 @@ msa_status_t msa_decode4_step(const void* q, const void* q_idx, const void* k_ca
   if (!(scale > 0.0f) || !std::isfinite(scale))
     return fail(MSA_ERR_INVALID_ARG, "scale must be finite and > 0");
   MSA_TRY(check_gains(k_gain, v_gain, 1.0f));
-  if (!std::isfinite(scale * k_gain * kLog2e))
+  if (!std::isfinite(static_cast<float>(static_cast<double>(scale) * k_gain * kLog2e)))
     return fail(MSA_ERR_INVALID_ARG, "scale * k_gain overflows");
   if (n_init < 0 || n_init > kTopK - 1)
     return fail(MSA_ERR_INVALID_ARG, "n_init %d outside [0, %d]", n_init, kTopK - 1);
@@ -990,7 +995,7 @@ msa_status_t msa_decode4_step(const void* q, const void* q_idx, const void* k_ca
                 : Attend4<4, false>::fits(rows) ? Attend4<4, false>::launch
                                                 : Attend4<2, false>::launch;
   return attend(q, k_cache, v_cache, block_table, cache_lens, w.scores, B, G, Hkv, num_pages,
-                max_pages, n_init, scale * k_gain * kLog2e, v_gain, o, sel_out, sw, st);
+                max_pages, n_init, static_cast<double>(scale) * k_gain * kLog2e, v_gain, o, sel_out, sw, st);
 }
 
 }  // extern "C"

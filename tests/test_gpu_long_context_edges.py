@@ -4,6 +4,7 @@ Helpers, definitions and tolerances are those of test_gpu_long_context.py."""
 import numpy as np
 import pytest
 
+from oracle import long_oracle as L
 from tests import test_gpu_long_context as base
 
 pytestmark = pytest.mark.gpu
@@ -27,3 +28,78 @@ def test_extend_by_more_pages_than_lanes(m, B, maxp, seed):
     g.extend([128 * maxp - n for n in g.o.lens])
     assert (g.o.lens == 128 * maxp).all()
     g.check("all filled")
+
+
+# ------------------------------------------------------------------ comparisons that fail on NaN
+
+def strict(got, want, tol, what):
+    ok = np.abs(got - want) <= tol
+    assert ok.all(), f"{what}: {(~ok).sum()} of {ok.size} off, {np.isnan(got).sum()} NaN"
+
+
+def cases_of(test):
+    """The parameters that a test of the other file runs with."""
+    return [mark.args[1] for mark in test.pytestmark if mark.name == "parametrize"][0]
+
+
+@pytest.fixture
+def nan_fails(monkeypatch):
+    """The other file's comparisons are of the form `error > tolerance`, which no NaN meets."""
+    monkeypatch.setattr(base, "within", strict)
+
+
+@pytest.mark.parametrize("case", base.PRO, ids=str)
+def test_prologue_ex_without_nan(m, nan_fails, case):
+    base.test_prologue_ex(m, case)
+
+
+@pytest.mark.parametrize("case", cases_of(base.test_prologue_ex_leaves_tokens_outside_the_sequences), ids=str)
+def test_tokens_outside_without_nan(m, nan_fails, case):
+    base.test_prologue_ex_leaves_tokens_outside_the_sequences(m, *case)
+
+
+@pytest.mark.parametrize("case", cases_of(base.test_append), ids=str)
+def test_append_without_nan(m, nan_fails, case):
+    base.test_append(m, *case)
+
+
+@pytest.mark.parametrize("test", [base.test_decode4_extreme_queries, base.test_decode4_bad_pages_and_lengths,
+                                  base.test_decode4_many_rows, base.test_cache_beyond_4_gb,
+                                  base.test_prefill_fork_decode_together], ids=lambda f: f.__name__)
+def test_decode4_without_nan(m, nan_fails, test):
+    test(m)
+    m.msa_check_status()
+
+
+# ------------------------------------------------------------------ decode: logits near 0 and far from it
+
+def check_attention(m, lens, q, qi, slabs, table, scale, gains, ref_of=None):
+    o, sel = base.run_decode(m, q, qi, slabs, table, lens, scale=scale, gains=(*gains, 1.0))
+    m.msa_check_status()
+    assert np.isfinite(o).all()
+    G = q.shape[1] // qi.shape[1]
+    for b, n in enumerate(lens):
+        for h in range(qi.shape[1]):
+            picked = [x for x in sel[b, h] if x >= 0]
+            want, gap = L.select(L.decode_scores(qi, slabs[2], table, b, h, n))
+            assert gap < 1e-5 or picked == want
+            rows = slice(h * G, (h + 1) * G)
+            ref = L.attend(q[b, rows], slabs[0], slabs[1], table, b, h, n, picked, scale, *gains)
+            vmax = np.nanmax(np.abs(L.slab_values(slabs[1][table[b, picked], h], gains[1])))
+            strict(o[b, rows], ref, 2.0 ** -8 * np.abs(ref) + 2.0 ** -9 * vmax, f"o[{b},{h}]")
+
+
+@pytest.mark.parametrize("G,H", [(16, 1), (3, 2)])
+@pytest.mark.parametrize("scale,k_gain", [
+    (base.SCALE, 1.0), (base.SCALE, 2.0 ** -28), (base.SCALE, 2.0 ** -64), (1e-30, 1.0), (1e-38, 1.0),
+    (1e-38, 2.0 ** -64), (1e18, 2.0 ** -64), (1e-30, 2.0 ** 64)])
+def test_decode4_small_logits(m, scale, k_gain, G, H):
+    """Zero, tiny and ordinary heads at every accepted scale of the logits, in rows whose own block
+    is partly filled: masked keys have no weight however flat the softmax is."""
+    rng = np.random.default_rng(20)
+    lens = (2500, 68, 1, 300, 129, 4000)
+    q, qi, slabs, table = base.decode_case(rng, lens, G, H, gains=(k_gain, 1.0))
+    q[:, 0] = 0.0
+    q[:3, 1] = base.f64(base.bf16(q[:3, 1] * 1e-30))
+    q[1:, 2] = base.f64(base.bf16(q[1:, 2] * 2.0 ** -126))     # down to subnormal values
+    check_attention(m, lens, q, qi, slabs, table, scale, (k_gain, 1.0))
