@@ -402,9 +402,10 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
   // q as the A operand of the 8 k-steps: rows g and g + 8 in fp16, each with a power
   // of two; thread c of a row has channels 32 c .. 32 c + 31.  Each warp makes and
   // stores two k-steps.  f0, f1: factor of the rows' sums, scale * k_gain * log2(e) over
-  // that power (sl2 in [1, 2] times 2^sl2_exp).  It stays a normal, finite fp32: where it would
-  // fall below, the sums (below 2^35) times 2^-126 are 0 for the softmax as well, and a
-  // masked key's -inf stays -inf, which 0 would turn into a NaN.
+  // that power (sl2 in [1, 2] times 2^sl2_exp).  It is kept in [2^-126, 2^91]: the sums lie
+  // below 2^34 and are multiples of 2^-34, so that 2^-126 makes all of them 0 for the
+  // softmax, 2^91 tells any two of them apart and no product overflows.  With 0 a masked
+  // key's -inf would become a NaN.
   float f0, f1;
   {
     uint4 a0, a1;
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const int e = row_shift(m);
       const float f = exp2i(e);
-      (half ? f1 : f0) = sl2 * exp2i(max(-126, min(126, sl2_exp - e)));
+      (half ? f1 : f0) = sl2 * exp2i(max(-126, min(90, sl2_exp - e)));
       const uint4 mine = warp == 0 ? x[0] : (warp == 1 ? x[1] : (warp == 2 ? x[2] : x[3]));
       (half ? a0.y : a0.x) = bf2_to_h2(mine.x, f);
       (half ? a0.w : a0.z) = bf2_to_h2(mine.y, f);
@@ -660,13 +661,11 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
     }
     // the maximum moves only when it grows by more than 2^8: weights stay below
     // 2^8, which fp16 holds as well as those below 1
-    mx0 *= f0;
-    mx1 *= f1;
-    const bool up0 = mx0 > m0 + kAtRescale || m0 == -INFINITY;
-    const bool up1 = mx1 > m1 + kAtRescale || m1 == -INFINITY;
+    const bool up0 = (mx0 - m0) * f0 > kAtRescale || m0 == -INFINITY;
+    const bool up1 = (mx1 - m1) * f1 > kAtRescale || m1 == -INFINITY;
     if (__any_sync(0xffffffffu, up0 || up1)) {
       const float n0 = up0 ? mx0 : m0, n1 = up1 ? mx1 : m1;
-      const float a0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), a1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
+      const float a0 = m0 == -INFINITY ? 0.f : ex2((m0 - n0) * f0), a1 = m1 == -INFINITY ? 0.f : ex2((m1 - n1) * f1);
       m0 = n0;
       m1 = n1;
       l0 *= a0;
@@ -681,12 +680,17 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
     }
     const float e0 = m0 == -INFINITY ? 0.f : -m0, e1 = m1 == -INFINITY ? 0.f : -m1;
     // P in fp16 (11 significant bits); the row sum takes the rounded values, so
-    // rounding does not change the weights' total
+    // rounding does not change the weights' total.  Exponents are (s - m) f, of which the
+    // maximum's own is exactly 0: fma(s, f, -(m f)) is off by half a unit of m f, which passes 16
+    // from logits of 2^29 on.
+    auto weights = [](float x, float y, float e, float f) {
+      const float2 z = __fmul2_rn(__fadd2_rn(make_float2(x, y), make_float2(e, e)), make_float2(f, f));
+      return __floats2half2_rn(ex2(z.x), ex2(z.y));
+    };
     uint32_t pa[2][4];
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-      const __half2 p0 = __floats2half2_rn(ex2(fmaf(s[nt][0], f0, e0)), ex2(fmaf(s[nt][1], f0, e0)));
-      const __half2 p1 = __floats2half2_rn(ex2(fmaf(s[nt][2], f1, e1)), ex2(fmaf(s[nt][3], f1, e1)));
+      const __half2 p0 = weights(s[nt][0], s[nt][1], e0, f0), p1 = weights(s[nt][2], s[nt][3], e1, f1);
       const float2 r0 = __half22float2(p0), r1 = __half22float2(p1);
       l0 += r0.x + r0.y;
       l1 += r1.x + r1.y;
@@ -759,9 +763,9 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
           make_float4(acc[4 * j][e], acc[4 * j + 1][e], acc[4 * j + 2][e], acc[4 * j + 3][e]);
   }
   if (c == 0) {
-    sm.ml[warp][g][0] = m0;
+    sm.ml[warp][g][0] = m0 * f0;                   // finite, or -inf without keys
     sm.ml[warp][g][1] = l0;
-    sm.ml[warp][g + 8][0] = m1;
+    sm.ml[warp][g + 8][0] = m1 * f1;
     sm.ml[warp][g + 8][1] = l1;
   }
   __syncthreads();

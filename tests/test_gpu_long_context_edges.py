@@ -103,3 +103,50 @@ def test_decode4_small_logits(m, scale, k_gain, G, H):
     q[:3, 1] = base.f64(base.bf16(q[:3, 1] * 1e-30))
     q[1:, 2] = base.f64(base.bf16(q[1:, 2] * 2.0 ** -126))     # down to subnormal values
     check_attention(m, lens, q, qi, slabs, table, scale, (k_gain, 1.0))
+
+
+@pytest.mark.parametrize("up,k_gain", [(20, 1.0), (24, 1.0), (31, 1.0), (40, 1.0), (120, 1.0), (60, 2.0 ** 64),
+                                       (120, 2.0 ** 64)])
+def test_decode4_large_logits(m, up, k_gain):
+    """Heads whose logits reach 2^20 to 2^184: the softmax is finite, and all on the largest one."""
+    rng = np.random.default_rng(21)
+    lens = (2500, 68, 300, 4000)
+    q, qi, slabs, table = base.decode_case(rng, lens, 16, 1, gains=(k_gain, 1.0))
+    # the two largest logits of a head lie far enough apart for the sums of 128 products that
+    # decide between them (2^-18 of the products' magnitudes, far above fp32's rounding of them)
+    for b, n in enumerate(lens):
+        sel, _ = L.select(L.decode_scores(qi, slabs[2], table, b, 0, n))
+        K = np.concatenate([L.slab_values(slabs[0][table[b, c], 0])[:min(128, n - 128 * c)] for c in sel])
+        z = q[b] @ K.T
+        top = np.sort(z, -1)
+        assert ((top[:, -1] - top[:, -2]) > 2.0 ** -18 * (np.abs(q[b]) @ np.abs(K).T).max(-1)).all()
+        assert ((top[:, -1] - top[:, -2]) * base.SCALE * 2.0 ** up > 200).all()
+    q = q * 2.0 ** up
+    check_attention(m, lens, q, qi, slabs, table, base.SCALE, (k_gain, 1.0))
+
+
+def test_decode4_heads_do_not_mix(m):
+    """A head whose query is not finite leaves the row's other heads as they are."""
+    rng = np.random.default_rng(22)
+    lens = (2500, 70)
+    q, qi, slabs, table = base.decode_case(rng, lens, 16, 1)
+    o, sel = base.run_decode(m, q, qi, slabs, table, lens)
+    bad = q.copy()
+    bad[0, 3, 5], bad[1, 9, 100] = np.nan, np.inf
+    ob, selb = base.run_decode(m, bad, qi, slabs, table, lens)
+    m.msa_check_status()
+    keep = np.ones((2, 16), bool)
+    keep[0, 3] = keep[1, 9] = False
+    assert np.array_equal(sel, selb) and np.array_equal(o[keep], ob[keep]) and np.isfinite(o).all()
+    assert not np.isfinite(ob[0, 3]).any()
+
+
+def test_decode4_repeats_itself(m):
+    """The same call gives the same bits."""
+    rng = np.random.default_rng(23)
+    for lens in ((2500, 70), (3000, 2200, 129) * 30):
+        args = base.decode_case(rng, lens, 16, 1)
+        first = base.run_decode(m, *args, lens)
+        for _ in range(5):
+            o, sel = base.run_decode(m, *args, lens)
+            assert np.array_equal(o, first[0]) and np.array_equal(sel, first[1])
