@@ -461,6 +461,7 @@ __global__ void __launch_bounds__(kAtThreads, kWhole ? 3 : 4) decode4_attend_ker
     if (tid == 0 && my_rows > 0)
       mbar_arrive_expect_tx(&sm.joined, NS * my_rows * (kD + 2) * sizeof(float));
   }
+  __syncwarp();                                    // the barrier wants whole warps
   cluster_arrive();
   if (tid == 0) sm.ncand = 0;
   if (own >= kTopK) {
