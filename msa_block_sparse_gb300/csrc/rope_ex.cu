@@ -6,9 +6,10 @@
 //       pair i = channels (i, i + R/2) ("half") or (2i, 2i + 1) ("interleaved")
 //   dz = the pairs of dy turned back (times gain), g = dz (1 + w), xh = x r:
 //   dx = r (g - xh mean(g xh)),  dw = sum over tokens and heads of dz xh
-// Bound by memory: 4 bytes per value forward, 6 backward.  Measured: 16,384 tokens x 64
-// heads x 128 (537 MB) forward 88 us, 6.1 TB/s; gradients of 16,384 x 12 x 256 (302
-// MB) 57 us, 5.3 TB/s; 32 tokens x 64 heads 2.8 us.
+// Bound by memory: 4 bytes per value forward, 6 backward (4 without weights).  Measured:
+// 16,384 tokens x 64 heads x 128 (537 MB) forward 89 us, 6.0 TB/s; gradients of 16,384 x
+// 12 x 256 (302 MB) 57 us, 5.3 TB/s; 32 tokens x 64 heads 2.8 us; the first without weights
+// (64 channels rotated) 90 us forward and 92 us back.
 //
 // Work: the [T * H, D] rows are cut into runs of consecutive rows, one run per
 // CTA (grid-stride in the backward).  A row belongs to D / 8 threads with 8
@@ -165,23 +166,38 @@ __device__ __forceinline__ void rx_unpack(const RxRow& r, float2 (&v)[4]) {
 }
 
 template <bool kHalf>
-__device__ __forceinline__ void rx_store(__nv_bfloat16* row, const RxLane& l, const float2 (&v)[4]) {
+__device__ __forceinline__ RxRow rx_pack(const float2 (&v)[4]) {
+  RxRow r;
   if (kHalf) {
-    *reinterpret_cast<uint2*>(row + l.off0) = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
-    *reinterpret_cast<uint2*>(row + l.off1) = make_uint2(pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+    r.a = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
+    r.b = make_uint2(pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
   } else {
-    *reinterpret_cast<uint4*>(row + l.off0) =
-        make_uint4(pack_bf16x2(v[0].x, v[2].x), pack_bf16x2(v[0].y, v[2].y),
-                   pack_bf16x2(v[1].x, v[3].x), pack_bf16x2(v[1].y, v[3].y));
+    r.a = make_uint2(pack_bf16x2(v[0].x, v[2].x), pack_bf16x2(v[0].y, v[2].y));
+    r.b = make_uint2(pack_bf16x2(v[1].x, v[3].x), pack_bf16x2(v[1].y, v[3].y));
+  }
+  return r;
+}
+
+template <bool kHalf>
+__device__ __forceinline__ void rx_store(__nv_bfloat16* row, const RxLane& l, const RxRow& r) {
+  if (kHalf) {
+    *reinterpret_cast<uint2*>(row + l.off0) = r.a;
+    *reinterpret_cast<uint2*>(row + l.off1) = r.b;
+  } else {
+    *reinterpret_cast<uint4*>(row + l.off0) = make_uint4(r.a.x, r.a.y, r.b.x, r.b.y);
   }
 }
 
 // Turns the 8 channels: v[p] = v[p] * c[p] + v[p ^ 2] * s[p]; signs and any factors
-// are in the coefficients.
-__device__ __forceinline__ void rx_turn(float2 (&v)[4], const float2 (&c)[4], const float2 (&s)[4]) {
+// are in the coefficients.  Channels that are not rotated (`rot` false) take no part of
+// another one: their sines of 0 would make a NaN of an infinity there.
+__device__ __forceinline__ void rx_turn(float2 (&v)[4], const float2 (&c)[4], const float2 (&s)[4], bool rot) {
   float2 o[4];
 #pragma unroll
-  for (int p = 0; p < 4; ++p) o[p] = __ffma2_rn(v[p], c[p], __fmul2_rn(v[p ^ 2], s[p]));
+  for (int p = 0; p < 4; ++p) {
+    const float2 t = __fmul2_rn(v[p ^ 2], s[p]);
+    o[p] = __ffma2_rn(v[p], c[p], make_float2(rot ? t.x : 0.f, rot ? t.y : 0.f));
+  }
 #pragma unroll
   for (int p = 0; p < 4; ++p) v[p] = o[p];
 }
@@ -300,12 +316,13 @@ __global__ void __launch_bounds__(kRxThreads, 8) rope_ex_kernel(const RxArgs a, 
         have = tok;
         rx_coefficients(table + tok * a.R, a.R >> 1, l, w1, 1.f, cc, ss);
       }
-      rx_turn(v, cc, ss);
+      rx_turn(v, cc, ss, !kNorm || l.rot);
       if (kNorm) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) v[p] = __fmul2_rn(v[p], rr);
       }
-      rx_store<kHalf>(yb + static_cast<size_t>(i) * D, l, v);
+      // without the norm, what is not rotated keeps its bits
+      rx_store<kHalf>(yb + static_cast<size_t>(i) * D, l, kNorm || l.rot ? rx_pack<kHalf>(v) : raw[k]);
     }
   }
 }
@@ -439,7 +456,12 @@ __global__ void __launch_bounds__(kRxThreads, 4) rope_ex_bwd_kernel(const RxArgs
           rx_coefficients(table + tok * a.R, a.R >> 1, l, one, -1.f, cc, ss);
         }
         put[k] = on && i + k * kPass < n;
-        rx_turn(dz[k], cc, ss);
+        if (!kNorm || l.rot) {                     // a branch: selects took 59.0 us for 57.2
+          rx_turn(dz[k], cc, ss, true);
+        } else {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) dz[k][p] = __fmul2_rn(dz[k][p], cc[p]);
+        }
         if (kNorm) {
           rx_unpack<kHalf>(raw[k][1], xv[k]);
           float2 q = make_float2(0.f, 0.f), d = q;
@@ -469,7 +491,8 @@ __global__ void __launch_bounds__(kRxThreads, 4) rope_ex_bwd_kernel(const RxArgs
             dz[k][p] = __ffma2_rn(xv[k][p], kk, __fmul2_rn(g[k][p], rr));
           }
         }
-        rx_store<kHalf>(ob + static_cast<size_t>(i + k * kPass) * D, l, dz[k]);
+        rx_store<kHalf>(ob + static_cast<size_t>(i + k * kPass) * D, l,
+                        kNorm || l.rot ? rx_pack<kHalf>(dz[k]) : raw[k][0]);
       }
     }
   }

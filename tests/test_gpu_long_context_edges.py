@@ -1,8 +1,11 @@
 """Long-context operators on the GPU where their arithmetic or their order of steps could
 go wrong: values that are not finite or far from 1, rows that grow by many pages.
 Helpers, definitions and tolerances are those of test_gpu_long_context.py."""
+import math
+
 import numpy as np
 import pytest
+import torch
 
 from oracle import long_oracle as L
 from tests import test_gpu_long_context as base
@@ -150,3 +153,77 @@ def test_decode4_repeats_itself(m):
         for _ in range(5):
             o, sel = base.run_decode(m, *args, lens)
             assert np.array_equal(o, first[0]) and np.array_equal(sel, first[1])
+
+
+# ------------------------------------------------------------------ rotation: channels that are not rotated
+
+ROT = [(9, 3, 128, 64, "half"), (33, 2, 128, 32, "interleaved"), (5, 7, 256, 224, "half"), (40, 5, 64, 16, "half"),
+       (12, 4, 256, 16, "interleaved"), (6, 1, 128, 112, "interleaved")]
+
+
+def spoil(x, R, rng):
+    """A copy with an infinity, a NaN, a -0 and a huge value in channels behind the rotated ones of
+    different rows, and where they are."""
+    bad = x.clone()
+    T, H, D = x.shape
+    at = []
+    for i, v in enumerate((math.inf, -math.inf, math.nan, -0.0, 3e38)):
+        t, h, c = i % T, int(rng.integers(H)), int(rng.integers(R, D))
+        bad[t, h, c] = v
+        at.append((t, h, c))
+    return bad, at
+
+
+@pytest.mark.parametrize("T,H,D,R,layout", ROT)
+def test_rotation_alone_passes_other_channels_through(m, T, H, D, R, layout):
+    rng = np.random.default_rng(30)
+    x = base.bf16(rng.standard_normal((T, H, D)))
+    rope = m.msa_rope(R, 1e6, layout=layout, scaling="yarn", factor=4.0)
+    pos = base.i32(rng.integers(0, 100000, T))
+    bad, _ = spoil(x, R, rng)
+
+    def turn(a, back, out=None):
+        if back:
+            return m.msa_qk_norm_rope_bwd_ex(None, a, None, rope, positions=pos, dx=out)[0]
+        return m.msa_qk_norm_rope_ex(a, None, rope, positions=pos, out=out)
+
+    bits = lambda t: t.view(torch.int16)    # noqa: E731
+    for back in (False, True):
+        clean, got = turn(x, back), turn(bad, back)
+        assert torch.equal(bits(got[..., :R]), bits(clean[..., :R]))
+        assert torch.equal(bits(got[..., R:]), bits(bad[..., R:])) and torch.equal(bits(clean[..., R:]), bits(x[..., R:]))
+        own = bad.clone()
+        assert torch.equal(bits(turn(own, back, out=own)), bits(got))
+    m.msa_check_status()
+
+
+@pytest.mark.parametrize("T,H,D,R,layout", ROT)
+def test_norm_and_rotation_keep_channels_apart(m, T, H, D, R, layout):
+    rng = np.random.default_rng(31)
+    x, dy, w = (base.bf16(rng.standard_normal(s)) for s in ((T, H, D), (T, H, D), (D,)))
+    rope = m.msa_rope(R, 1e6, layout=layout)
+    pos = base.i32(rng.integers(0, 100000, T))
+    t, h, c = T - 1, H - 1, D - 3
+    bad = x.clone()
+    bad[t, h, c] = math.inf
+    y, clean = (m.msa_qk_norm_rope_ex(a, w, rope, positions=pos) for a in (bad, x))
+    # r = 0: every other channel of the row is 0, its own is 0 * inf
+    assert torch.isnan(y[t, h, c]) and (y[t, h, :c] == 0).all() and (y[t, h, c + 1:] == 0).all()
+    y[t, h] = clean[t, h]
+    assert torch.equal(y, clean)
+    # an infinite weight of a channel that is not rotated
+    wide = w.clone()
+    wide[c] = math.inf
+    y = m.msa_qk_norm_rope_ex(x, wide, rope, positions=pos)
+    assert torch.isinf(y[..., c]).all()
+    y[..., c] = clean[..., c]
+    assert torch.equal(y, clean)
+    # backward: dw of the other channels does not see it
+    bad = dy.clone()
+    bad[t, h, c] = math.inf
+    (dx, dw), (cdx, cdw) = (m.msa_qk_norm_rope_bwd_ex(x, a, w, rope, positions=pos) for a in (bad, dy))
+    rest = torch.arange(D, device=base.DEV) != c
+    assert torch.equal(dw[rest], cdw[rest]) and not torch.isfinite(dw[c])
+    dx[t, h] = cdx[t, h]
+    assert torch.equal(dx, cdx)
+    m.msa_check_status()
