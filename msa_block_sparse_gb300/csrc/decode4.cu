@@ -110,6 +110,8 @@ __global__ void __launch_bounds__(kScThreads, 1) decode4_score_kernel(
     const __nv_bfloat16* __restrict__ q_idx, const uint8_t* __restrict__ kidx,
     const int32_t* __restrict__ table, const int32_t* __restrict__ lens, int B, int Hkv,
     int num_pages, int max_pages, int n_init, float* __restrict__ scores, uint32_t* status) {
+  // the wait has to stay ahead of the trigger, and no launch may come between this kernel and
+  // decode4_attend_kernel, which reads q and the lengths before it waits for this one
   pdl_enter();
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Score4Smem& sm = *reinterpret_cast<Score4Smem*>(smem_raw);
