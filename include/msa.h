@@ -184,7 +184,9 @@ MSA_API msa_status_t msa_rope_init(msa_rope_t* rope, int dim, double base, int l
 /* x bf16 [T, H, D] -> y bf16 [T, H, D] (y may be x).  w bf16 [D], or NULL for
  * the rotation alone (z = x).  The position of token t is positions[t] (int32
  * [T], any value) or, with positions NULL, its place in cu_seqlens' sequence;
- * tokens outside [cu_seqlens[0], cu_seqlens[S]) are then left alone.
+ * tokens outside [cu_seqlens[0], cu_seqlens[S]) are then left alone.  Channels
+ * behind the rotated part take nothing from other channels, whatever those hold, and
+ * with w NULL they keep their bits (so does their dx).
  * `rope` is read on the host during the call.  1 <= H <= 256.
  */
 MSA_API msa_status_t msa_qk_norm_rope_ex(const void* x, void* y, int T, int H, int D,

@@ -7,7 +7,9 @@
 // memory with bulk copies (global -> shared -> global), no registers involved.
 // Measured: 890 of 4,096 pages of 98 KB moved in 31 us (175 MB read and written, 5.6
 // TB/s; chunks of 8 or 32 KB, deeper rings and two CTAs per SM all within 3 %), the
-// tables' part of a free and a compaction 8 us.
+// tables' part of a free and a compaction 8 us.  The one CTA walks all reference counts:
+// growing 96 rows by a token takes 4.3 us with 4,096 pages, 22 with 100,000 and 183 with a
+// million, a compaction of the tables 5.3, 114 and 1,092 us.
 #include "kernels.cuh"
 
 namespace msa {
