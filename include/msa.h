@@ -408,6 +408,85 @@ MSA_API msa_status_t msa_decode_append(const void* q, const void* q_idx, const v
                                        void* q_idx_out, msa_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Append to a 16-bit paged cache: msa_decode_append for any number of new
+ * tokens per row and any rotation.  A pack of T tokens, those of row s at cu_seqlens[s] ..
+ * cu_seqlens[s + 1] - 1, is the end of the row: cache_lens[s] counts them, so that
+ * token t is at position cache_lens[s] - cu_seqlens[s + 1] + t (a prompt, a chunk of
+ * one, drafted tokens; one token per row in a decode step).  q bf16 [T, Hq, 128], k and v
+ * bf16 [T, Hkv, 128]; optionally (all four or none) index q and k bf16 [T, Hkv, 128] with
+ * kidx_cache and q_idx_out.  Then, with the prologue of msa_qk_norm_rope_ex at the token's
+ * position (each weight bf16 [128], or NULL: no norm):
+ *   q_out, q_idx_out = prologue(q, w_q), prologue(q_idx, w_qi)   (may be q / q_idx)
+ *   k_cache[page, h, p % 128]    = prologue(k, w_k)[h]
+ *   kidx_cache[page, h, p % 128] = prologue(k_idx, w_ki)[h]
+ *   v_cache[page, h, p % 128]    = v[h]             with page = block_table[s, p / 128]
+ * Caches as in msa_decode_step; Hq is any multiple of Hkv up to 256.  Tokens outside
+ * [cu_seqlens[0], cu_seqlens[S]) and those of rows with cache_lens[s] = 0 (padding) are
+ * left alone.  Positions outside [0, 128 max_pages) and pages outside [0, num_pages) set
+ * MSA_STATUS_BOUNDS and leave the token's outputs untouched.  A page that rows share has
+ * to be made the row's own first (msa_pages_extend).
+ */
+MSA_API msa_status_t msa_cache_append(const void* q, const void* k, const void* v,
+                                      const void* q_idx, const void* k_idx, const void* w_q,
+                                      const void* w_k, const void* w_qi, const void* w_ki,
+                                      void* k_cache, void* v_cache, void* kidx_cache,
+                                      const int32_t* block_table, const int32_t* cu_seqlens,
+                                      const int32_t* cache_lens, int S, int T, int Hq, int Hkv,
+                                      int num_pages, int max_pages, const msa_rope_t* rope,
+                                      float eps, void* q_out, void* q_idx_out,
+                                      msa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Full attention of one new token per row over the 16-bit paged cache (the
+ * model's layers without an indexer), computed once where rows share pages.
+ *   o[b, i]   = softmax(scale * q[b, i] k_j) v_j over the row's cache_lens[b] tokens
+ *   lse[b, i] = log sum_j exp(scale * q[b, i] k_j)         fp32 [B, Hq] (may be NULL)
+ * q, o bf16 [B, Hq, 128], Hq = G Hkv with 1 <= G <= 128; caches, block_table and
+ * cache_lens as in msa_decode_step (the new token included).  The result is that of every
+ * row by itself, whatever the tables hold.  Where neighbouring rows (those of length 0
+ * not counted) begin with the same pages, as rows that were forked or reordered do, the
+ * full pages that they have in common are read once for all of them, at up to 6
+ * levels (a system prompt, behind it a prompt of each user, behind that its samples); so
+ * put rows that share next to each other.  This is found out on the device in each call.
+ * A row with cache_lens[b] = 0 gets o = 0 and lse = -infinity; lengths outside
+ * [0, 128 max_pages] set MSA_STATUS_BOUNDS and are treated so too.  A page outside
+ * [0, num_pages) sets MSA_STATUS_BOUNDS and has no keys.  Slots of a row's last page behind
+ * its end may hold anything.  B <= 2048; scale from 2^-64 to 2^64.
+ */
+MSA_API size_t msa_decode_shared_workspace_size(int B, int Hq, int Hkv, int max_pages);
+
+MSA_API msa_status_t msa_decode_shared(const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* block_table, const int32_t* cache_lens,
+                                       int B, int Hq, int Hkv, int num_pages, int max_pages,
+                                       float scale, void* o, float* lse, void* workspace,
+                                       size_t workspace_bytes, msa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Beam search's selection.  Row n W + w is beam w of prompt n; logits of row r at
+ * logits + r * row_stride (elements; row_stride >= V, any alignment of the type),
+ * scores fp32 [N W] the beams' log probabilities.  Of the continuations
+ *   score(w, v) = scores[w] + logits[w, v] - log sum_u exp(logits[w, u])
+ * of a prompt the K best, best first: scores_out fp32 [N, K], parents int32 [N, K] (the row
+ * n W + w), tokens int32 [N, K].  Scores are compared before they are rounded to fp32,
+ * as 64-bit values over a log-sum-exp of fp32 exponentials; equal ones go to the lower
+ * w V + v.  A beam with finished[r] != 0 (uint8 [N W], NULL: none) goes on by
+ * pad_token alone, with its score unchanged; its logits are not read.  A NaN among
+ * the logits counts as -infinity, +infinity as the largest finite value; a beam whose
+ * score is -infinity or NaN is dead.  Continuations of probability zero are never chosen:
+ * where fewer than K are left, the last places get score -infinity, parent -1, token -1
+ * (msa_pages_reorder empties such rows).  W, K <= 64, K <= W V, V <= 2^24, N W <= 65535.
+ */
+enum { MSA_F32 = 0, MSA_BF16 = 1 };
+
+MSA_API size_t msa_beam_select_workspace_size(int N, int W, int V, int K);
+
+MSA_API msa_status_t msa_beam_select(const void* logits, int dtype, int64_t row_stride,
+                                     const float* scores, const uint8_t* finished, int N, int W,
+                                     int V, int K, int pad_token, float* scores_out,
+                                     int32_t* parents, int32_t* tokens, void* workspace,
+                                     size_t workspace_bytes, msa_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Paged cache held in 4 bits.  A page of one head (a "slab") is 9216 bytes:
  * 128 tokens x 64 bytes of e2m1 codes (low nibble = even channel), then 128
  * tokens x 8 bytes of e4m3 scales, one for 16 consecutive channels.  A cache is
@@ -554,6 +633,23 @@ MSA_API msa_status_t msa_pages_compact(int32_t* block_table, const int32_t* cach
                                        int32_t* ref_count, int B, int num_pages, int max_pages,
                                        void* const* caches, const int64_t* page_bytes,
                                        int n_caches, int32_t* page_map, int32_t* n_live,
+                                       void* workspace, size_t workspace_bytes,
+                                       msa_stream_t stream);
+
+/* reorder: row r becomes what row parents[r] (int32 [B]) was before the call: its table
+ * entries, its length and, from now on, its pages, which rows with the same parent share
+ * (a partly filled last page too: msa_pages_extend gives each its own copy before it is
+ * written).  parents[r] = r keeps the row, -1 empties it; rows that are nobody's
+ * parent lose their pages, and entries that a row no longer needs become -1.  kept[r]
+ * (int32 [B], output) is the row's length after the call, -1 where it is refused and left
+ * as it was: a parent outside [-1, B), or one whose length is out of range (both set
+ * MSA_STATUS_BOUNDS).
+ */
+MSA_API size_t msa_pages_reorder_workspace_size(int B, int max_pages);
+
+MSA_API msa_status_t msa_pages_reorder(const int32_t* parents, int32_t* block_table,
+                                       int32_t* cache_lens, int32_t* ref_count, int B,
+                                       int num_pages, int max_pages, int32_t* kept,
                                        void* workspace, size_t workspace_bytes,
                                        msa_stream_t stream);
 

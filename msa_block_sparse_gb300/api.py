@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libmsa.so")
 
 D = 128
 TOPK = 16
+_SCALE = 1.0 / math.sqrt(D)
 
 _c_int, _c_float, _c_size, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
 _c_double = ctypes.c_double
@@ -94,6 +95,14 @@ _SIGNATURES = {
     "msa_pages_compact_workspace_size": (_c_size, [_c_int]),
     "msa_pages_compact": (_c_int, [_vp] * 3 + [_c_int] * 3 + [_vp, _vp, _c_int, _vp, _vp, _vp,
                                                            _c_size, _vp]),
+    "msa_pages_reorder_workspace_size": (_c_size, [_c_int] * 2),
+    "msa_pages_reorder": (_c_int, [_vp] * 4 + [_c_int] * 3 + [_vp, _vp, _c_size, _vp]),
+    "msa_cache_append": (_c_int, [_vp] * 15 + [_c_int] * 6 + [_vp, _c_float, _vp, _vp, _vp]),
+    "msa_decode_shared_workspace_size": (_c_size, [_c_int] * 4),
+    "msa_decode_shared": (_c_int, [_vp] * 5 + [_c_int] * 5 + [_c_float, _vp, _vp, _vp, _c_size, _vp]),
+    "msa_beam_select_workspace_size": (_c_size, [_c_int] * 4),
+    "msa_beam_select": (_c_int, [_vp, _c_int, ctypes.c_int64, _vp, _vp] + [_c_int] * 5 + [_vp] * 4 +
+                        [_c_size, _vp]),
     "msa_pages_copy": (_c_int, [_vp, _vp, _c_int, _c_int, _vp, _vp, _c_int, _vp]),
     "msa_decode_step_static": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int,
                                         _c_int, _c_int, _c_int, _c_float, _vp, _vp, _vp]),
@@ -565,10 +574,58 @@ def msa_qk_norm_rope_bwd_ex(x, dy, w, rope: Rope, cu_seqlens: Optional[torch.Ten
                                          workspace)
 
 
+# ------------------------------------------------------------------ 16-bit paged cache
+
+def msa_cache_append(q, k, v, k_cache, v_cache, block_table, cu_seqlens, cache_lens, rope: Rope,
+                     w_q: Optional[torch.Tensor] = None, w_k: Optional[torch.Tensor] = None,
+                     q_idx: Optional[torch.Tensor] = None, k_idx: Optional[torch.Tensor] = None,
+                     kidx_cache: Optional[torch.Tensor] = None,
+                     w_qi: Optional[torch.Tensor] = None, w_ki: Optional[torch.Tensor] = None,
+                     q_out: Optional[torch.Tensor] = None,
+                     q_idx_out: Optional[torch.Tensor] = None, eps: float = 1.0e-6):
+    """The prologue (norm with w_* bf16 [128], None: none; rotation `rope`) of a pack of
+    new tokens (q bf16 [T, Hq, 128], k, v bf16 [T, Hkv, 128]), the keys and values
+    written into the caches bf16 [num_pages, Hkv, 128, 128]: the tokens of sequence s
+    of cu_seqlens are the last ones of row s, whose cache_lens[s] counts them.  q_idx,
+    k_idx (bf16 [T, Hkv, 128]) and kidx_cache go together.  Returns (q_out, q_idx_out or
+    None); pass q / q_idx to update them in place.  Rows of length 0 are left alone."""
+    return _native().cache_append(q, k, v, k_cache, v_cache, block_table, cu_seqlens, cache_lens,
+                                  _rope_at(rope), w_q, w_k, q_idx, k_idx, kidx_cache, w_qi, w_ki, q_out,
+                                  q_idx_out, eps)
+
+
+def msa_decode_shared(q, k_cache, v_cache, block_table, cache_lens, scale: Optional[float] = None,
+                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None):
+    """Full attention of one new token per row (q bf16 [B, Hq, 128]) over all cached
+    tokens of the row: (o bf16 [B, Hq, 128], lse fp32 [B, Hq]).  Full pages with which
+    neighbouring rows begin alike are read once for all of them.  Rows of length 0 get o = 0,
+    lse = -inf."""
+    return _native().decode_shared(q, k_cache, v_cache, block_table, cache_lens,
+                                   _SCALE if scale is None else scale, out, lse, workspace)
+
+
+# ------------------------------------------------------------------ beams
+
+def msa_beam_select(logits, scores, beams: int, n_out: Optional[int] = None,
+                    finished: Optional[torch.Tensor] = None, pad_token: int = 0,
+                    scores_out: Optional[torch.Tensor] = None,
+                    parents: Optional[torch.Tensor] = None,
+                    tokens: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None):
+    """The n_out (default: beams) best continuations of each prompt by scores[r] +
+    log softmax(logits[r]): logits fp32 or bf16 [N * beams, V] (rows of any stride), scores
+    fp32 [N * beams].  Returns (scores fp32, parents int32, tokens int32), each [N, n_out],
+    best first, equal scores by the lower beam and token; parents are rows of logits.
+    finished (bool or uint8 [N * beams]): such a beam goes on by pad_token alone, its score
+    unchanged.  Where fewer continuations are possible: -inf, -1, -1."""
+    return _native().beam_select(logits, scores, beams, beams if n_out is None else n_out, finished,
+                                 pad_token, scores_out, parents, tokens, workspace)
+
+
 # ------------------------------------------------------------------ 4-bit paged cache
 
 SLAB4 = 9216     # bytes of a page of one head: 128 x 64 of codes, 128 x 8 of scales
-_SCALE = 1.0 / math.sqrt(D)
 
 
 def _gains(gains):
@@ -657,6 +714,15 @@ def msa_pages_compact(block_table, cache_lens, ref_count, caches,
     return _native().pages_compact(block_table, cache_lens, ref_count, caches, page_map, n_live, workspace)
 
 
+def msa_pages_reorder(parents, block_table, cache_lens, ref_count,
+                      kept: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None):
+    """Row r becomes what row parents[r] (int32 [B]; -1: empty) was: table entries, length
+    and shared pages; reference counts follow.  Returns kept int32 [B]: the row's
+    length, -1 where refused."""
+    return _native().pages_reorder(parents, block_table, cache_lens, ref_count, kept, workspace)
+
+
 def msa_pages_copy(src, dst, caches) -> None:
     """Page src[i] -> page dst[i] in every tensor of `caches` (first dimension = pages)."""
     _native().pages_copy(src, dst, caches)
@@ -665,6 +731,7 @@ def msa_pages_copy(src, dst, caches) -> None:
 def workspace_bytes(call: str, *args) -> int:
     """Workspace size of `call` ('qk_norm_rope_bwd', 'index_select', 'sparse_attn_fwd',
     'sparse_attn_bwd', 'qsa_attn_fwd', 'qsa_attn_bwd', 'decode_step', 'qk_norm_rope_bwd_ex',
-    'decode4_step', 'pages_extend', 'pages_compact') for the given sizes, as the C ABI
+    'decode4_step', 'pages_extend', 'pages_compact', 'pages_reorder', 'decode_shared',
+    'beam_select') for the given sizes, as the C ABI
     reports it."""
     return int(getattr(lib(), f"msa_{call}_workspace_size")(*args))

@@ -1,0 +1,644 @@
+// Beam search's selection: of all W * V continuations of a prompt's W beams the K with the
+// best score s_w + log softmax(x_w)_v.
+//
+// Bound by memory: the logits are read once (the only large input).
+//
+//   beam_scan_kernel   CTA = a slice of one beam's vocabulary.  Every thread keeps the
+//                      running maximum and sum of exponentials of its values (sums joined
+//                      in 64 bits); the slice's K best values are kept beside
+//                      them.  Within a beam the order of the scores is that of the values,
+//                      so that nothing else of the slice can be chosen.
+//   beam_merge_kernel  CTA = a prompt.  Log-sum-exp of its beams from the slices, scores of
+//                      the slices' candidates in 64 bits, the best K in order.
+//
+// K best of n values without sorting: the values are dealt into groups, and the K-th
+// largest of the groups' maxima is a bound that at least K values reach; of values in no
+// particular order about 1.4 K do.  These few are ranked by counting.  Keys are unique
+// (value, then the lower index), so that at most the K best groups hold anything above
+// the bound, whatever the values are.
+#include <cfloat>
+#include "kernels.cuh"
+
+namespace msa {
+
+namespace {
+
+constexpr int kBmThreads = 256;
+constexpr int kBmMaxK = 64;
+constexpr int kBmMaxW = 64;
+constexpr int kBmValues = 32;                          // of a thread and tile
+constexpr int kBmTile = kBmThreads * kBmValues;
+constexpr int kBmCap = kBmMaxK * kBmValues + kBmThreads;   // keys of the buffer
+constexpr int kBmCandidates = 16384;                   // of a prompt, at most
+constexpr int kBmMergeThreads = 512;
+constexpr float kBmLog2e = 1.4426950408889634f;
+
+// Order of floats as order of unsigned integers (0: below -infinity, used for "nothing")
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+__device__ __forceinline__ unsigned long long ordered(double x) {
+  const unsigned long long u = static_cast<unsigned long long>(__double_as_longlong(x));
+  return u >> 63 ? ~u : u | (1ull << 63);
+}
+
+// A value and its place in the vocabulary: larger is better, no two are equal
+__device__ __forceinline__ unsigned long long key_of(float x, uint32_t idx) {
+  return (static_cast<unsigned long long>(ordered(x)) << 32) | (0xFFFFFFFFu - idx);
+}
+
+struct BeamScan {
+  double top;    // maximum
+  double sum;    // of e^(x - top)
+};
+
+template <typename T>
+struct Vec;      // 16 bytes of logits
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ void unpack(const uint4& u, float* x) {
+    x[0] = __uint_as_float(u.x);
+    x[1] = __uint_as_float(u.y);
+    x[2] = __uint_as_float(u.z);
+    x[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 part(const float* p, int lo, int hi) {
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = i >= lo && i < hi ? p[i] : -INFINITY;
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                      __float_as_uint(x[3]));
+  }
+  static __device__ __forceinline__ uint4 nothing() {
+    return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void unpack(const uint4& u, float* x) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 part(const __nv_bfloat16* p, int lo, int hi) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = 2 * i >= lo && 2 * i < hi ? __bfloat16_as_ushort(p[2 * i]) : 0xFF80u;
+      const uint32_t b =
+          2 * i + 1 >= lo && 2 * i + 1 < hi ? __bfloat16_as_ushort(p[2 * i + 1]) : 0xFF80u;
+      w[i] = a | b << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  static __device__ __forceinline__ uint4 nothing() {
+    return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+  }
+};
+
+__device__ __forceinline__ float bm_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// NaN counts as -infinity, +infinity as the largest finite value
+__device__ __forceinline__ float plain(float x) {
+  return x != x ? -INFINITY : fminf(x, FLT_MAX);
+}
+
+struct ScanSmem {
+  unsigned long long key[kBmCap];
+  unsigned long long best[kBmMaxK];
+  alignas(16) float group[128];
+  alignas(16) unsigned long long gkey[kBmThreads];
+  double sum[kBmThreads / 32];
+  float top[kBmThreads / 32];
+  float bound;
+  unsigned long long bound_key;
+  int count;
+};
+
+// The K best of the sm.count keys in sm.key, in order, into sm.best; count <= kBmCap.
+// All threads; sm.count becomes what is kept.  Ranks by counting; more than kBmThreads keys
+// (rare) are first cut by the bound of their groups.
+__device__ __forceinline__ void bm_rank(ScanSmem& sm, int K) {
+  __syncthreads();
+  int n = sm.count;
+  const int tid = threadIdx.x;
+  while (n > kBmThreads) {
+    // groups: the keys i, i + 256, ... of a thread
+    unsigned long long mine[(kBmCap + kBmThreads - 1) / kBmThreads], top = 0;
+#pragma unroll
+    for (int k = 0; k < (kBmCap + kBmThreads - 1) / kBmThreads; ++k) {
+      const int i = tid + k * kBmThreads;
+      mine[k] = i < n ? sm.key[i] : 0;
+      top = mine[k] > top ? mine[k] : top;
+    }
+    sm.gkey[tid] = top;
+    __syncthreads();
+    int above = 0;
+    for (int i = 0; i < kBmThreads; ++i) above += sm.gkey[i] > top;
+    if (above == K - 1) sm.bound_key = top;      // n > 256 >= K: there is a K-th group
+    if (tid == 0) sm.count = 0;
+    __syncthreads();
+    const unsigned long long bound = sm.bound_key;
+#pragma unroll
+    for (int k = 0; k < (kBmCap + kBmThreads - 1) / kBmThreads; ++k)
+      if (mine[k] >= bound) sm.key[atomicAdd(&sm.count, 1)] = mine[k];
+    __syncthreads();
+    n = sm.count;
+  }
+  if (tid < n) {
+    const unsigned long long mine = sm.key[tid];
+    int above = 0;
+    for (int i = 0; i < n; ++i) above += sm.key[i] > mine;
+    if (above < K) sm.best[above] = mine;
+  }
+  __syncthreads();
+  n = min(n, K);
+  if (tid < n) sm.key[tid] = sm.best[tid];
+  if (tid == 0) sm.count = n;
+  __syncthreads();
+}
+
+}  // namespace
+
+// e^(x - top) as a power of two; the factor's rounding (1.3e-8 of the exponent) is far below
+// the exponential's own
+__device__ __forceinline__ float bm_exp(float x, float top) { return bm_ex2((x - top) * kBmLog2e); }
+
+// grid (slices, rows)
+template <typename T>
+__global__ void __launch_bounds__(kBmThreads) beam_scan_kernel(
+    const T* __restrict__ logits, long long ld, int V, int K, const uint8_t* __restrict__ finished,
+    BeamScan* __restrict__ stats, unsigned long long* __restrict__ keys) {
+  pdl_enter();
+  using L = Vec<T>;
+  constexpr int kVecs = kBmValues / L::kN;
+  __shared__ ScanSmem sm;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slices = gridDim.x, row = blockIdx.y;
+  if (finished && finished[row]) return;                 // goes on by the pad token alone
+  const T* x = logits + static_cast<long long>(row) * ld;
+  // vectors of 16 aligned bytes; the row begins `skew` values into the first one
+  const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+  const T* xa = x - skew;
+  const int nvec = (skew + V + L::kN - 1) / L::kN;
+  const int v0 = static_cast<int>(static_cast<long long>(nvec) * blockIdx.x / slices);
+  const int v1 = static_cast<int>(static_cast<long long>(nvec) * (blockIdx.x + 1) / slices);
+  auto load = [&](int v) -> uint4 {
+    if (v >= v1) return L::nothing();
+    const int lo = v * L::kN;
+    if (lo >= skew && lo + L::kN <= skew + V)
+      return __ldcs(reinterpret_cast<const uint4*>(xa + lo));
+    return L::part(xa + lo, skew - lo, skew + V - lo);
+  };
+  float top = -INFINITY, bound = -INFINITY;
+  double sum = 0.0;
+  if (tid == 0) sm.count = 0;
+  uint4 raw[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) raw[u] = load(v0 + u * kBmThreads + tid);
+  for (int vt = v0; vt < v1; vt += kVecs * kBmThreads) {
+    float val[kBmValues];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) L::unpack(raw[u], val + u * L::kN);
+    if (vt + kVecs * kBmThreads < v1) {
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) raw[u] = load(vt + (kVecs + u) * kBmThreads + tid);
+    }
+    auto place = [&](int i) -> uint32_t {
+      return static_cast<uint32_t>((vt + (i / L::kN) * kBmThreads + tid) * L::kN + i % L::kN - skew);
+    };
+    // ---- maximum and sum of exponentials of this thread's values
+    float best = -INFINITY, part = 0.f;
+    auto scan = [&]() {
+      best = val[0];
+#pragma unroll
+      for (int i = 1; i < kBmValues; ++i) best = fmaxf(best, val[i]);
+      const float ref = best > -INFINITY ? -best : 0.f;
+      float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                       make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int i = 0; i < kBmValues; i += 2) {
+        const float2 y = __fmul2_rn(__fadd2_rn(make_float2(val[i], val[i + 1]), make_float2(ref, ref)),
+                                    make_float2(kBmLog2e, kBmLog2e));
+        acc[(i >> 1) & 3] = __fadd2_rn(acc[(i >> 1) & 3], make_float2(bm_ex2(y.x), bm_ex2(y.y)));
+      }
+      const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+      part = a.x + a.y;
+    };
+    scan();
+    if (!(part < INFINITY)) {                            // a NaN or +infinity among them
+#pragma unroll
+      for (int i = 0; i < kBmValues; ++i) val[i] = plain(val[i]);
+      scan();
+    }
+    if (best > top) {
+      sum = sum * bm_exp(top, best) + part;
+      top = best;
+    } else if (best > -INFINITY) {
+      sum += static_cast<double>(part) * bm_exp(best, top);
+    }
+    // ---- candidates: what reaches the bound goes into the buffer
+    int kept = 0;                                        // keys of earlier tiles
+    float least = bound;
+    const bool first = vt == v0;
+    if (first) {
+      // bound: the K-th largest of the maxima of 64 or 128 groups of threads
+      const int groups = K <= 32 ? 64 : 128, per = kBmThreads / groups;
+      float g = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
+      if (per == 4) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+      if (tid % per == 0) sm.group[tid / per] = g;
+      __syncthreads();
+      // the threads of a group compare its maximum with a share of the others each
+      int above = 0, level = 0;
+      const int share = groups / per, from = tid % per * share;
+      for (int i = from; i < from + share; i += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(&sm.group[i]);
+        above += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g);
+        level += (o.x >= g) + (o.y >= g) + (o.z >= g) + (o.w >= g);
+      }
+      above += __shfl_xor_sync(0xffffffffu, above, 1);
+      level += __shfl_xor_sync(0xffffffffu, level, 1);
+      if (per == 4) {
+        above += __shfl_xor_sync(0xffffffffu, above, 2);
+        level += __shfl_xor_sync(0xffffffffu, level, 2);
+      }
+      if (above < K && level >= K) sm.bound = g;         // one value, whoever writes it
+      __syncthreads();
+      bound = least = sm.bound;
+    } else {
+      kept = sm.count;                                   // at most kBmThreads
+      __syncthreads();
+    }
+    // later tiles lose ties: K values at least as large stand before them
+    if (first ? best >= least : best > least) {
+#pragma unroll
+      for (int i = 0; i < kBmValues; ++i)
+        if ((first ? val[i] >= least : val[i] > least) && val[i] > -INFINITY) {
+          const int at = atomicAdd(&sm.count, 1);
+          if (at < kBmCap) sm.key[at] = key_of(val[i], place(i));
+        }
+    }
+    __syncthreads();
+    if (sm.count > kBmCap) {
+      // far more than K (equal or ascending values): the threads are the groups, their best
+      // keys, no two alike, give the bound, and at most K threads hold anything above it
+      unsigned long long mine = 0;
+#pragma unroll
+      for (int i = 0; i < kBmValues; ++i) {
+        const unsigned long long k = val[i] > -INFINITY ? key_of(val[i], place(i)) : 0;
+        mine = k > mine ? k : mine;
+      }
+      sm.gkey[tid] = mine;
+      if (tid == 0) sm.bound_key = 1;                    // fewer than K threads hold anything
+      __syncthreads();
+      int above = 0;
+      for (int i = 0; i < kBmThreads; ++i) above += sm.gkey[i] > mine;
+      if (above == K - 1 && mine > 0) sm.bound_key = mine;
+      if (tid == 0) sm.count = kept;
+      __syncthreads();
+      const unsigned long long bk = sm.bound_key;
+#pragma unroll
+      for (int i = 0; i < kBmValues; ++i) {
+        const unsigned long long k = val[i] > -INFINITY ? key_of(val[i], place(i)) : 0;
+        if (k >= bk) sm.key[atomicAdd(&sm.count, 1)] = k;
+      }
+      __syncthreads();
+    }
+    if (sm.count > kBmThreads) {
+      bm_rank(sm, K);
+      if (sm.count == K) bound = unordered(static_cast<uint32_t>(sm.key[K - 1] >> 32));
+    }
+  }
+  bm_rank(sm, K);
+  unsigned long long* out = keys + (static_cast<size_t>(row) * slices + blockIdx.x) * K;
+  if (tid < K) out[tid] = tid < sm.count ? sm.key[tid] : 0;
+  // ---- maximum and sum of the slice
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) {
+    const float o = __shfl_xor_sync(0xffffffffu, top, m);
+    const double os = __shfl_xor_sync(0xffffffffu, sum, m);
+    const float t = fmaxf(top, o);
+    if (t > -INFINITY) sum = sum * bm_exp(top, t) + os * bm_exp(o, t);
+    top = t;
+  }
+  if (lane == 0) {
+    sm.top[warp] = top;
+    sm.sum[warp] = sum;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    for (int i = 1; i < kBmThreads / 32; ++i) {
+      const float o = sm.top[i], t = fmaxf(top, o);
+      if (t > -INFINITY) sum = sum * bm_exp(top, t) + sm.sum[i] * bm_exp(o, t);
+      top = t;
+    }
+    stats[static_cast<size_t>(row) * slices + blockIdx.x] = {top, sum};
+  }
+}
+
+// ---------------------------------------------------------------- merge
+
+namespace {
+
+constexpr int kBmGroups = 128;
+constexpr int kBmPer = kBmMergeThreads / kBmGroups;
+constexpr int kBmMine = kBmCandidates / kBmMergeThreads;            // candidates of a thread
+constexpr int kBmSurvivors = kBmMaxK * kBmPer * kBmMine;            // at most after the first cut
+
+// A candidate: score (ordered; 0: none) and ~(place among the prompt's W * V): larger wins
+struct Cand {
+  unsigned long long s;
+  uint32_t at;
+};
+__device__ __forceinline__ bool beats(unsigned long long s, uint32_t at, unsigned long long t, uint32_t bt) {
+  return s > t || (s == t && at > bt);
+}
+
+struct MergeSmem {
+  unsigned long long s[kBmSurvivors];
+  uint32_t at[kBmSurvivors];
+  unsigned long long gs[kBmGroups];
+  uint32_t gat[kBmGroups];
+  double lse[kBmMaxW], score[kBmMaxW];
+  unsigned long long bound_s;
+  uint32_t bound_at;
+  int count;
+};
+
+// Bound that at least K candidates reach, from the best candidate of every thread.  At most
+// the K best groups (of 4 threads) hold anything at or above it.
+__device__ __forceinline__ void bm_bound(MergeSmem& sm, Cand top, int K) {
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int m = 1; m < kBmPer; m <<= 1) {
+    const unsigned long long s = __shfl_xor_sync(0xffffffffu, top.s, m);
+    const uint32_t at = __shfl_xor_sync(0xffffffffu, top.at, m);
+    if (beats(s, at, top.s, top.at)) top = {s, at};
+  }
+  if (tid % kBmPer == 0) {
+    sm.gs[tid / kBmPer] = top.s;
+    sm.gat[tid / kBmPer] = top.at;
+  }
+  if (tid == 0) {
+    sm.bound_s = 1;                     // fewer than K groups hold anything
+    sm.bound_at = 0;
+    sm.count = 0;
+  }
+  __syncthreads();
+  int above = 0;
+  const int share = kBmGroups / kBmPer, from = tid % kBmPer * share;
+  for (int i = from; i < from + share; ++i) above += beats(sm.gs[i], sm.gat[i], top.s, top.at);
+#pragma unroll
+  for (int m = 1; m < kBmPer; m <<= 1) above += __shfl_xor_sync(0xffffffffu, above, m);
+  if (above == K - 1 && top.s > 0 && tid % kBmPer == 0) {
+    sm.bound_s = top.s;
+    sm.bound_at = top.at;
+  }
+  __syncthreads();
+}
+
+}  // namespace
+
+// grid (prompts)
+__global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
+    const BeamScan* __restrict__ stats, const unsigned long long* __restrict__ keys,
+    const float* __restrict__ scores, const uint8_t* __restrict__ finished, int W, int V, int K,
+    int slices, int pad_token, float* __restrict__ scores_out, int32_t* __restrict__ parents,
+    int32_t* __restrict__ tokens) {
+  pdl_enter();
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  MergeSmem& sm = *reinterpret_cast<MergeSmem*>(smem_raw);
+  const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // ---- log-sum-exp of every beam, a warp each; NaN as score: the beam is dead
+  for (int w = warp; w < W; w += kBmMergeThreads / 32) {
+    const int row = n * W + w;
+    const float s = scores[row];
+    const bool live = s > -INFINITY;
+    const bool ended = finished && finished[row];
+    double top = -INFINITY, sum = 0.0;
+    if (live && !ended) {
+      for (int i = lane; i < slices; i += 32) {
+        const BeamScan b = stats[static_cast<size_t>(row) * slices + i];
+        const double t = fmax(top, b.top);
+        if (t > -INFINITY) sum = sum * exp(top - t) + b.sum * exp(b.top - t);
+        top = t;
+      }
+#pragma unroll
+      for (int m = 16; m >= 1; m >>= 1) {
+        const double o = __shfl_xor_sync(0xffffffffu, top, m), os = __shfl_xor_sync(0xffffffffu, sum, m);
+        const double t = fmax(top, o);
+        if (t > -INFINITY) sum = sum * exp(top - t) + os * exp(o - t);
+        top = t;
+      }
+    }
+    if (lane == 0) {
+      sm.score[w] = live ? static_cast<double>(s) : -INFINITY;
+      sm.lse[w] = ended ? 0.0 : top + log(sum);        // all masked: -infinity + -infinity
+    }
+  }
+  __syncthreads();
+  // ---- candidate i = (beam, slice, rank)
+  const int per_row = slices * K, total = W * per_row;
+  auto get = [&](int i) -> Cand {
+    const int w = i / per_row, row = n * W + w;
+    const double s = sm.score[w];
+    if (!(s > -INFINITY)) return {0, 0};
+    if (finished && finished[row]) {
+      if (i - w * per_row != 0) return {0, 0};
+      return {ordered(s), ~(static_cast<uint32_t>(w) * V + pad_token)};
+    }
+    const unsigned long long key = keys[static_cast<size_t>(n) * total + i];
+    if (key == 0) return {0, 0};
+    const uint32_t v = 0xFFFFFFFFu - static_cast<uint32_t>(key);
+    const double x = unordered(static_cast<uint32_t>(key >> 32));
+    return {ordered(s + (x - sm.lse[w])), ~(static_cast<uint32_t>(w) * V + v)};
+  };
+  Cand top = {0, 0};
+  for (int i = tid; i < total; i += kBmMergeThreads) {
+    const Cand c = get(i);
+    if (beats(c.s, c.at, top.s, top.at)) top = c;
+  }
+  bm_bound(sm, top, K);
+  {
+    const unsigned long long bs = sm.bound_s;
+    const uint32_t ba = sm.bound_at;
+    if (!beats(bs, ba, top.s, top.at))
+      for (int i = tid; i < total; i += kBmMergeThreads) {
+        const Cand c = get(i);
+        if (!beats(bs, ba, c.s, c.at)) {
+          const int at = atomicAdd(&sm.count, 1);
+          sm.s[at] = c.s;
+          sm.at[at] = c.at;
+        }
+      }
+  }
+  __syncthreads();
+  int left = sm.count;
+  __syncthreads();
+  while (left > kBmMergeThreads) {                     // rare: the best ones lie in few threads
+    Cand mine[kBmSurvivors / kBmMergeThreads];
+    top = {0, 0};
+#pragma unroll
+    for (int k = 0; k < kBmSurvivors / kBmMergeThreads; ++k) {
+      const int i = tid + k * kBmMergeThreads;
+      mine[k] = i < left ? Cand{sm.s[i], sm.at[i]} : Cand{0, 0};
+      if (beats(mine[k].s, mine[k].at, top.s, top.at)) top = mine[k];
+    }
+    bm_bound(sm, top, K);                              // its first barrier: all have read theirs
+    const unsigned long long bs = sm.bound_s;
+    const uint32_t ba = sm.bound_at;
+#pragma unroll
+    for (int k = 0; k < kBmSurvivors / kBmMergeThreads; ++k)
+      if (!beats(bs, ba, mine[k].s, mine[k].at)) {
+        const int at = atomicAdd(&sm.count, 1);
+        sm.s[at] = mine[k].s;
+        sm.at[at] = mine[k].at;
+      }
+    __syncthreads();
+    left = sm.count;
+    __syncthreads();                                   // read before the next round clears it
+  }
+  // ---- in order
+  float* so = scores_out + static_cast<size_t>(n) * K;
+  int32_t *po = parents + static_cast<size_t>(n) * K, *to = tokens + static_cast<size_t>(n) * K;
+  if (tid < left) {
+    const unsigned long long s = sm.s[tid];
+    const uint32_t at = sm.at[tid];
+    int above = 0;
+    for (int i = 0; i < left; ++i) above += beats(sm.s[i], sm.at[i], s, at);
+    if (above < K) {
+      const uint32_t flat = ~at;
+      const unsigned long long u = s >> 63 ? s & ~(1ull << 63) : ~s;
+      so[above] = static_cast<float>(__longlong_as_double(static_cast<long long>(u)));
+      po[above] = n * W + static_cast<int>(flat / V);
+      to[above] = static_cast<int>(flat % V);
+    }
+  }
+  if (tid >= left && tid < K) {                        // fewer continuations than places
+    so[tid] = -INFINITY;
+    po[tid] = -1;
+    to[tid] = -1;
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+namespace {
+
+struct BeamWorkspace {
+  BeamScan* stats;
+  unsigned long long* keys;
+};
+
+// Slices of a row: enough CTAs for the GPU, tiles of a row shared evenly; no slice under
+// 1024 values, and a prompt's candidates within what the merge takes.
+int beam_slices(long long rows, int W, int V, int K) {
+  const int fill = 8 * device_sm_count();
+  const int tiles = (V + kBmTile - 1) / kBmTile;
+  long long want = (fill + rows - 1) / rows;
+  if (want >= tiles) {
+    const int small = V / 1024 < 1 ? 1 : V / 1024;
+    want = want < small ? want : small;
+    if (want < tiles) want = tiles;
+  }
+  const int most = kBmCandidates / (W * K);
+  if (want > most) want = most;
+  return static_cast<int>(want < 1 ? 1 : want);
+}
+
+BeamWorkspace carve_beam_workspace(WsCursor& ws, long long rows, int slices, int K) {
+  BeamWorkspace w;
+  w.stats = ws.take<BeamScan>(static_cast<size_t>(rows) * slices);
+  w.keys = ws.take<unsigned long long>(static_cast<size_t>(rows) * slices * K);
+  return w;
+}
+
+bool beam_sizes_ok(int N, int W, int V, int K) {
+  return N >= 1 && W >= 1 && W <= kBmMaxW && V >= 1 && V <= (1 << 24) && K >= 1 && K <= kBmMaxK &&
+         static_cast<long long>(K) <= static_cast<long long>(W) * V &&
+         static_cast<long long>(N) * W <= 65535;
+}
+
+}  // namespace
+
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" {
+
+size_t msa_beam_select_workspace_size(int N, int W, int V, int K) {
+  if (!beam_sizes_ok(N, W, V, K)) return 0;
+  WsCursor ws(nullptr);
+  const long long rows = static_cast<long long>(N) * W;
+  carve_beam_workspace(ws, rows, beam_slices(rows, W, V, K), K);
+  return ws.used + 256;
+}
+
+msa_status_t msa_beam_select(const void* logits, int dtype, int64_t row_stride, const float* scores,
+                             const uint8_t* finished, int N, int W, int V, int K, int pad_token,
+                             float* scores_out, int32_t* parents, int32_t* tokens,
+                             void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  const size_t size = dtype == MSA_F32 ? 4 : 2;
+  if (dtype != MSA_F32 && dtype != MSA_BF16)
+    return fail(MSA_ERR_INVALID_ARG, "dtype %d is neither MSA_F32 nor MSA_BF16", dtype);
+  if (!logits || reinterpret_cast<uintptr_t>(logits) % size != 0)
+    return fail(MSA_ERR_INVALID_ARG, "logits is null or not aligned to its type");
+  MSA_REQUIRE_PTR(scores_out);
+  MSA_REQUIRE_PTR(parents);
+  MSA_REQUIRE_PTR(tokens);
+  MSA_REQUIRE_PTR(workspace);
+  if (!scores || reinterpret_cast<uintptr_t>(scores) % 4 != 0)
+    return fail(MSA_ERR_INVALID_ARG, "scores is null or not 4-byte aligned");
+  if (N < 1 || W < 1 || V < 1 || K < 1)
+    return fail(MSA_ERR_INVALID_ARG, "N, W, V and K must be >= 1 (got %d, %d, %d, %d)", N, W, V, K);
+  if (W > kBmMaxW || K > kBmMaxK || V > (1 << 24) || static_cast<long long>(N) * W > 65535)
+    return fail(MSA_ERR_UNSUPPORTED,
+                "at most %d beams, %d continuations, 2^24 tokens and 65535 rows (got %d, %d, %d, %lld)",
+                kBmMaxW, kBmMaxK, W, K, V, static_cast<long long>(N) * W);
+  if (static_cast<long long>(K) > static_cast<long long>(W) * V)
+    return fail(MSA_ERR_INVALID_ARG, "K = %d of only %lld continuations", K, static_cast<long long>(W) * V);
+  if (row_stride < V) return fail(MSA_ERR_INVALID_ARG, "row_stride is below V");
+  if (pad_token < 0 || pad_token >= V)
+    return fail(MSA_ERR_INVALID_ARG, "pad_token %d outside [0, %d)", pad_token, V);
+  if (workspace_bytes < msa_beam_select_workspace_size(N, W, V, K))
+    return fail(MSA_ERR_INVALID_ARG, "workspace too small");
+  const long long rows = static_cast<long long>(N) * W;
+  const int slices = beam_slices(rows, W, V, K);
+  WsCursor ws(workspace);
+  const BeamWorkspace w = carve_beam_workspace(ws, rows, slices, K);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  {
+    TraceScope trace_("beam_scan_kernel", st);
+    const dim3 grid(slices, static_cast<unsigned>(rows));
+    if (dtype == MSA_F32)
+      launch_pdl(beam_scan_kernel<float>, grid, kBmThreads, 0, st, static_cast<const float*>(logits),
+                 row_stride, V, K, finished, w.stats, w.keys);
+    else
+      launch_pdl(beam_scan_kernel<__nv_bfloat16>, grid, kBmThreads, 0, st,
+                 static_cast<const __nv_bfloat16*>(logits), row_stride, V, K, finished, w.stats, w.keys);
+  }
+  MSA_TRY(check_launch("beam_scan_kernel"));
+  MSA_TRY(ensure_smem(beam_merge_kernel, sizeof(MergeSmem), "beam_merge_kernel"));
+  {
+    TraceScope trace_("beam_merge_kernel", st);
+    launch_pdl(beam_merge_kernel, static_cast<unsigned>(N), kBmMergeThreads, sizeof(MergeSmem), st,
+               w.stats, w.keys, scores, finished, W, V, K, slices, pad_token, scores_out, parents, tokens);
+  }
+  return check_launch("beam_merge_kernel");
+}
+
+}  // extern "C"

@@ -474,6 +474,18 @@ PyObject* pages_compact(PyObject* const* a) {
   return pair(map, live);
 }
 
+// parents, block_table, cache_lens, ref_count, kept, workspace
+PyObject* pages_reorder(PyObject* const* a) {
+  const Call c(a[1], "block_table");
+  const Tables t(c, a[1], a[2], a[3]);
+  const auto* parents = static_cast<const int32_t*>(c.arg(a[0], "parents", at::kInt, {t.B}));
+  const Tensor kept = c.out(a[4], "kept", at::kInt, {t.B});
+  const Workspace ws(c, a[5], msa_pages_reorder_workspace_size(t.B, t.maxp));
+  check(msa_pages_reorder(parents, t.table, t.lens, t.ref, t.B, t.P, t.maxp,
+                          static_cast<int32_t*>(kept.data_ptr()), ws.ptr(), ws.bytes, c.stream()));
+  return wrap(kept);
+}
+
 // src, dst, caches
 PyObject* pages_copy(PyObject* const* a) {
   const Call c(a[0], "src");
@@ -498,6 +510,136 @@ PyObject* pages_copy(PyObject* const* a) {
   const Caches k(c, a[2], P);
   check(msa_pages_copy(src, dst, size32(n, "n"), size32(P, "num_pages"), k.ptr, k.bytes, k.n, c.stream()));
   Py_RETURN_NONE;
+}
+
+// ---------------------------------------------------------------- 16-bit cache
+
+struct Table16 {
+  int64_t P = 0, Hkv = 0, maxp = 0;
+  const int32_t* table = nullptr;
+  Table16(const Call& c, PyObject* first_o, const char* name, PyObject* table_o, int64_t rows) {
+    const Tensor& first = tensor(first_o, name);
+    if (first.dim() != 4) throw ValueErr(std::string(name) + " must have shape (num_pages, Hkv, 128, 128)");
+    P = first.size(0);
+    Hkv = first.size(1);
+    const Tensor& t = tensor(table_o, "block_table");
+    if (t.dim() != 2 || t.size(0) != rows)
+      throw ValueErr("block_table must have shape (" + std::to_string(rows) + ", max_pages)");
+    maxp = t.size(1);
+    table = static_cast<const int32_t*>(c.arg(t, "block_table", at::kInt, {rows, maxp}));
+  }
+  void* cache(const Call& c, PyObject* o, const char* name) const {
+    return c.arg(o, name, at::kBFloat16, {P, Hkv, 128, kD});
+  }
+  int pages() const { return size32(P, "num_pages"); }
+  int heads() const { return size32(Hkv, "Hkv"); }
+  int per_row() const { return size32(maxp, "max_pages"); }
+};
+
+// q, k, v, k_cache, v_cache, block_table, cu_seqlens, cache_lens, rope, w_q, w_k, q_idx, k_idx,
+// kidx_cache, w_qi, w_ki, q_out, q_idx_out, eps
+PyObject* cache_append(PyObject* const* a) {
+  const Call c(a[0], "q");
+  const Tensor& q = tensor(a[0], "q");
+  if (q.dim() != 3) throw ValueErr("q must have shape (T, Hq, 128)");
+  const int64_t T = q.size(0), Hq = q.size(1);
+  const auto [cu, S] = sequences(c, a[6]);
+  const Table16 t(c, a[3], "k_cache", a[5], S);
+  const void* qp = c.arg(q, "q", at::kBFloat16, {T, Hq, kD});
+  const void* kp = c.arg(a[1], "k", at::kBFloat16, {T, t.Hkv, kD});
+  const void* vp = c.arg(a[2], "v", at::kBFloat16, {T, t.Hkv, kD});
+  void *kc = t.cache(c, a[3], "k_cache"), *vc = t.cache(c, a[4], "v_cache");
+  const auto* lens = static_cast<const int32_t*>(c.arg(a[7], "cache_lens", at::kInt, {S}));
+  const void* wq = c.opt<void>(a[9], "w_q", at::kBFloat16, {kD});
+  const void* wk = c.opt<void>(a[10], "w_k", at::kBFloat16, {kD});
+  const bool index = !none(a[11]);
+  if (index != !none(a[12]) || index != !none(a[13]))
+    throw ValueErr("q_idx, k_idx and kidx_cache must be given together");
+  const void *qi = nullptr, *ki = nullptr, *wqi = nullptr, *wki = nullptr;
+  void* ic = nullptr;
+  const Tensor q_out = c.out(a[16], "q_out", at::kBFloat16, {T, Hq, kD});
+  Tensor qi_out;
+  if (index) {
+    qi = c.arg(a[11], "q_idx", at::kBFloat16, {T, t.Hkv, kD});
+    ki = c.arg(a[12], "k_idx", at::kBFloat16, {T, t.Hkv, kD});
+    ic = t.cache(c, a[13], "kidx_cache");
+    wqi = c.opt<void>(a[14], "w_qi", at::kBFloat16, {kD});
+    wki = c.opt<void>(a[15], "w_ki", at::kBFloat16, {kD});
+    qi_out = c.out(a[17], "q_idx_out", at::kBFloat16, {T, t.Hkv, kD});
+  } else if (!none(a[14]) || !none(a[15]) || !none(a[17])) {
+    throw ValueErr("w_qi, w_ki and q_idx_out need q_idx, k_idx and kidx_cache");
+  }
+  check(msa_cache_append(qp, kp, vp, qi, ki, wq, wk, wqi, wki, kc, vc, ic, t.table, cu, lens, S,
+                         size32(T, "T"), size32(Hq, "Hq"), t.heads(), t.pages(), t.per_row(), rope_at(a[8]),
+                         number(a[18]), q_out.data_ptr(), index ? qi_out.data_ptr() : nullptr, c.stream()));
+  if (index) return pair(q_out, qi_out);
+  PyObject* r = PyTuple_New(2);
+  if (!r) throw PyErrSet();
+  PyTuple_SET_ITEM(r, 0, wrap(q_out));
+  Py_INCREF(Py_None);
+  PyTuple_SET_ITEM(r, 1, Py_None);
+  return r;
+}
+
+// q, k_cache, v_cache, block_table, cache_lens, scale, out, lse, workspace
+PyObject* decode_shared(PyObject* const* a) {
+  const Call c(a[0], "q");
+  const auto [B, Hq] = rows_heads(a[0], "q");
+  const Table16 t(c, a[1], "k_cache", a[3], B);
+  const void* q = c.arg(a[0], "q", at::kBFloat16, {B, Hq, kD});
+  const void *kc = t.cache(c, a[1], "k_cache"), *vc = t.cache(c, a[2], "v_cache");
+  const auto* lens = static_cast<const int32_t*>(c.arg(a[4], "cache_lens", at::kInt, {B}));
+  const Tensor o = c.out(a[6], "out", at::kBFloat16, {B, Hq, kD});
+  const Tensor lse = c.out(a[7], "lse", at::kFloat, {B, Hq});
+  const int b = size32(B, "B"), hq = size32(Hq, "Hq");
+  const Workspace ws(c, a[8], msa_decode_shared_workspace_size(b, hq, t.heads(), t.per_row()));
+  check(msa_decode_shared(q, kc, vc, t.table, lens, b, hq, t.heads(), t.pages(), t.per_row(), number(a[5]),
+                          o.data_ptr(), static_cast<float*>(lse.data_ptr()), ws.ptr(), ws.bytes, c.stream()));
+  return pair(o, lse);
+}
+
+// ---------------------------------------------------------------- beams
+
+// logits, scores, beams, n_out, finished, pad_token, scores_out, parents, tokens, workspace
+PyObject* beam_select(PyObject* const* a) {
+  const Call c(a[0], "logits");
+  const Tensor& x = tensor(a[0], "logits");
+  if (x.dim() != 2) throw ValueErr("logits must have shape (N * beams, V)");
+  int dtype = MSA_F32;
+  if (x.scalar_type() == at::kBFloat16) {
+    dtype = MSA_BF16;
+  } else if (x.scalar_type() != at::kFloat) {
+    std::ostringstream s;
+    s << "logits must be Float or BFloat16, got " << x.scalar_type();
+    throw ValueErr(s.str());
+  }
+  const int64_t R = x.size(0), V = x.size(1), W = whole(a[2]), K = whole(a[3]);
+  if ((V > 1 && x.stride(1) != 1) || (R > 1 && x.stride(0) < V))
+    throw ValueErr("rows of logits must be contiguous and must not overlap");
+  if (W < 1 || R < 1 || R % W != 0) throw ValueErr("logits must have beams rows for every prompt");
+  const int64_t N = R / W;
+  const void* scores = c.arg(a[1], "scores", at::kFloat, {R});
+  const uint8_t* finished = nullptr;
+  if (!none(a[4])) {
+    const Tensor& f = tensor(a[4], "finished");
+    finished = static_cast<const uint8_t*>(
+        c.arg(f, "finished", f.scalar_type() == at::kBool ? at::kBool : at::kByte, {R}));
+  }
+  const int n = size32(N, "N"), w = size32(W, "beams"), v = size32(V, "V"), k = size32(K, "n_out");
+  if (k < 1) throw ValueErr("n_out must be >= 1");
+  const Tensor so = c.out(a[6], "scores_out", at::kFloat, {N, K});
+  const Tensor po = c.out(a[7], "parents", at::kInt, {N, K}), to = c.out(a[8], "tokens", at::kInt, {N, K});
+  const Workspace ws(c, a[9], msa_beam_select_workspace_size(n, w, v, k));
+  check(msa_beam_select(x.data_ptr(), dtype, R > 1 ? x.stride(0) : V, static_cast<const float*>(scores),
+                        finished, n, w, v, k, size32(whole(a[5]), "pad_token"),
+                        static_cast<float*>(so.data_ptr()), static_cast<int32_t*>(po.data_ptr()),
+                        static_cast<int32_t*>(to.data_ptr()), ws.ptr(), ws.bytes, c.stream()));
+  PyObject* r = PyTuple_New(3);
+  if (!r) throw PyErrSet();
+  PyTuple_SET_ITEM(r, 0, wrap(so));
+  PyTuple_SET_ITEM(r, 1, wrap(po));
+  PyTuple_SET_ITEM(r, 2, wrap(to));
+  return r;
 }
 
 // ---------------------------------------------------------------- module
@@ -532,7 +674,9 @@ PyMethodDef kMethods[] = {
     MSA_ENTRY(qk_norm_rope_ex, 7), MSA_ENTRY(qk_norm_rope_bwd_ex, 10), MSA_ENTRY(cache4_store, 12),
     MSA_ENTRY(cache4_load, 13),    MSA_ENTRY(decode4_append, 21),      MSA_ENTRY(decode4_step, 14),
     MSA_ENTRY(pages_fork, 7),      MSA_ENTRY(pages_free, 6),           MSA_ENTRY(pages_extend, 7),
-    MSA_ENTRY(pages_compact, 7),   MSA_ENTRY(pages_copy, 3),           {nullptr, nullptr, 0, nullptr}};
+    MSA_ENTRY(pages_compact, 7),   MSA_ENTRY(pages_copy, 3),
+    MSA_ENTRY(pages_reorder, 6),   MSA_ENTRY(cache_append, 19),       MSA_ENTRY(decode_shared, 9),
+    MSA_ENTRY(beam_select, 10),    {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_msa_torch", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -333,6 +333,103 @@ __global__ void __launch_bounds__(kPgThreads) pages_compact_kernel(
   }
 }
 
+// ---------------------------------------------------------------- reorder
+//
+// Rows take each other's places: every row is put aside in the workspace first, and the
+// references of the rows that change are taken back; then each row is written from its
+// parent's copy and its references are added.  A warp per row.  Few entries: one cluster
+// does both halves with a barrier between them (one launch less); many: two launches
+// over the whole GPU.
+constexpr int kRoThreads = 512;
+constexpr int kRoCluster = 8;
+constexpr long long kRoOneLaunch = 65536;    // entries of the table at most
+
+struct ReorderArgs {
+  const int32_t* parents;
+  int32_t *table, *lens, *ref, *kept;
+  int32_t *held, *held_lens;                // [B, max_pages], [B]: the rows as they were
+  int B, num_pages, max_pages;
+};
+
+// The row that row r becomes: -1 = none; r itself where parents or lengths are not usable.
+__device__ __forceinline__ int reorder_from(const ReorderArgs& a, const int32_t* lens, int r, bool* bad) {
+  const int p = a.parents[r];
+  *bad = p < -1 || p >= a.B;
+  if (*bad || p < 0) return *bad ? r : -1;
+  *bad = !row_ok(lens[p], a.max_pages);
+  return *bad ? r : p;
+}
+
+__device__ __forceinline__ void reorder_put_aside(const ReorderArgs& a, int warp, int warps, uint32_t* status) {
+  const int lane = threadIdx.x & 31;
+  for (int r = warp; r < a.B; r += warps) {
+    const int L = a.lens[r];
+    if (lane == 0) a.held_lens[r] = L;
+    if (!row_ok(L, a.max_pages)) {
+      if (lane == 0) atomicOr(status, kStatusBounds);
+      continue;
+    }
+    bool bad;
+    const bool changes = reorder_from(a, a.lens, r, &bad) != r;
+    const int32_t* row = a.table + static_cast<size_t>(r) * a.max_pages;
+    int32_t* to = a.held + static_cast<size_t>(r) * a.max_pages;
+    for (int j = lane; j < blocks_of(L); j += 32) {
+      const int pg = row[j];
+      to[j] = pg;
+      if (!changes) continue;
+      if (pg < 0 || pg >= a.num_pages) {
+        atomicOr(status, kStatusBounds);
+      } else if (atomicSub(&a.ref[pg], 1) <= 0) {      // held more often than counted
+        atomicAdd(&a.ref[pg], 1);
+        atomicOr(status, kStatusBounds);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void reorder_take(const ReorderArgs& a, int warp, int warps, uint32_t* status) {
+  const int lane = threadIdx.x & 31;
+  for (int r = warp; r < a.B; r += warps) {
+    bool bad;
+    const int p = reorder_from(a, a.held_lens, r, &bad);
+    const int old = a.held_lens[r];
+    if (bad && lane == 0) atomicOr(status, kStatusBounds);
+    if (p == r) {
+      if (lane == 0) a.kept[r] = bad ? -1 : old;
+      continue;
+    }
+    const int L = p < 0 ? 0 : a.held_lens[p];
+    int32_t* row = a.table + static_cast<size_t>(r) * a.max_pages;
+    const int32_t* from = a.held + static_cast<size_t>(max(p, 0)) * a.max_pages;
+    for (int j = lane; j < blocks_of(L); j += 32) {
+      const int pg = from[j];
+      row[j] = pg;
+      if (pg < 0 || pg >= a.num_pages) atomicOr(status, kStatusBounds);
+      else atomicAdd(&a.ref[pg], 1);
+    }
+    if (row_ok(old, a.max_pages))
+      for (int j = blocks_of(L) + lane; j < blocks_of(old); j += 32) row[j] = -1;
+    if (lane == 0) {
+      a.lens[r] = L;
+      a.kept[r] = L;
+    }
+  }
+}
+
+// kHalf 0: both halves, the grid is one cluster; 1: put aside; 2: take
+template <int kHalf>
+__global__ void __launch_bounds__(kRoThreads) pages_reorder_kernel(const ReorderArgs a, uint32_t* status) {
+  pdl_enter();
+  const int warp = blockIdx.x * (kRoThreads / 32) + (threadIdx.x >> 5);
+  const int warps = gridDim.x * (kRoThreads / 32);
+  if (kHalf != 2) reorder_put_aside(a, warp, warps, status);
+  if (kHalf == 0) {
+    // releases what every thread of the cluster wrote and has it seen by the others
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  if (kHalf != 1) reorder_take(a, warp, warps, status);
+}
+
 // ---------------------------------------------------------------- copies
 //
 // Items are (pair, chunk of a page's caches), cut into equal runs over a
@@ -515,6 +612,13 @@ CompactWorkspace carve_compact_workspace(WsCursor& ws, int num_pages) {
   return w;
 }
 
+ReorderArgs carve_reorder_workspace(WsCursor& ws, int B, int max_pages) {
+  ReorderArgs a{};
+  a.held = ws.take<int32_t>(static_cast<size_t>(B) * max_pages);
+  a.held_lens = ws.take<int32_t>(B);
+  return a;
+}
+
 msa_status_t launch_copy(const PageCaches& pc, const int32_t* src, const int32_t* dst, int n,
                          const int32_t* n_dev, long long most, int num_pages, int32_t* table,
                          const int32_t* lens, const int32_t* page_map, int B, int max_pages,
@@ -664,6 +768,69 @@ msa_status_t msa_pages_compact(int32_t* block_table, const int32_t* cache_lens,
   MSA_TRY(check_launch("pages_compact_kernel"));
   return launch_copy(pc, w.copy_src, w.copy_dst, 0, w.n_copies, num_pages, num_pages, block_table,
                      cache_lens, page_map, B, max_pages, sw, st);
+}
+
+size_t msa_pages_reorder_workspace_size(int B, int max_pages) {
+  if (B < 1 || max_pages < 1) return 0;
+  WsCursor ws(nullptr);
+  carve_reorder_workspace(ws, B, max_pages);
+  return ws.used + 256;
+}
+
+msa_status_t msa_pages_reorder(const int32_t* parents, int32_t* block_table, int32_t* cache_lens,
+                               int32_t* ref_count, int B, int num_pages, int max_pages,
+                               int32_t* kept, void* workspace, size_t workspace_bytes,
+                               msa_stream_t stream) {
+  MSA_REQUIRE_PTR(parents);
+  MSA_REQUIRE_PTR(kept);
+  MSA_REQUIRE_PTR(workspace);
+  MSA_TRY(check_tables(block_table, cache_lens, ref_count, B, num_pages, max_pages));
+  if (workspace_bytes < msa_pages_reorder_workspace_size(B, max_pages))
+    return fail(MSA_ERR_INVALID_ARG, "workspace too small");
+  WsCursor ws(workspace);
+  ReorderArgs a = carve_reorder_workspace(ws, B, max_pages);
+  a.parents = parents;
+  a.table = block_table;
+  a.lens = cache_lens;
+  a.ref = ref_count;
+  a.kept = kept;
+  a.B = B;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  uint32_t* sw = nullptr;
+  MSA_TRY(status_word(&sw));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int warps = kRoThreads / 32, ctas = (B + warps - 1) / warps;
+  if (static_cast<long long>(B) * max_pages <= kRoOneLaunch) {
+    TraceScope trace_("pages_reorder_kernel", st);
+    const unsigned n = ctas >= kRoCluster ? kRoCluster : ctas > 2 ? 4 : ctas;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = n;
+    cfg.blockDim = kRoThreads;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaLaunchKernelEx(&cfg, pages_reorder_kernel<0>, a, sw);
+    return check_launch("pages_reorder_kernel");
+  }
+  const int most = 4 * device_sm_count();
+  {
+    TraceScope trace_("pages_reorder_aside_kernel", st);
+    launch_pdl(pages_reorder_kernel<1>, ctas < most ? ctas : most, kRoThreads, 0, st, a, sw);
+  }
+  MSA_TRY(check_launch("pages_reorder_aside_kernel"));
+  {
+    TraceScope trace_("pages_reorder_take_kernel", st);
+    launch_pdl(pages_reorder_kernel<2>, ctas < most ? ctas : most, kRoThreads, 0, st, a, sw);
+  }
+  return check_launch("pages_reorder_take_kernel");
 }
 
 msa_status_t msa_pages_copy(const int32_t* src, const int32_t* dst, int n, int num_pages,

@@ -1,0 +1,1014 @@
+// Full attention of one new token per row over the 16-bit paged cache, with pages that
+// neighbouring rows share read once for all of them.
+//   o = softmax(scale q K^T) V,   lse = log sum exp(scale q K^T)
+//
+// Sharing.  With c_i the number of leading full pages that the rows i and i + 1 (of those
+// with tokens) have in common, the rows that share a page at column c are the maximal
+// runs with c_i > c: the runs form a tree, whose nodes are rectangles (rows i0 .. i0 + m - 1,
+// columns v0 .. v1 - 1).  A row's keys are those of the nodes on its path and of its own
+// leaf (one row, the columns behind).  Every node is cut into items (up to 256 query rows x a
+// range of columns x a KV head) of about equal work; an item leaves a partial result
+// (maximum, sum, unnormalised o in fp32) per query row, and the parts of a row are joined.
+//
+//   shared_plan_kernel     one CTA: c_i, tree, item length, items, each row's list of parts
+//   shared_attn_kernel     persistent CTAs (one per SM) that claim items
+//   shared_combine_kernel  joins the parts
+//
+// Attention of an item: tiles of 128 query rows (token rows x the G heads of a KV head),
+// two streams of tensor-core work per CTA:
+//   wide    two tiles over the same pages; stream s has tile s, S = Q_s K^T (128 x 128)
+//   narrow  one tile (a leaf's G rows, or up to 128 shared ones); stream s has the keys
+//           64 s .. 64 s + 63 of every page, S double-buffered; the halves' results are
+//           merged at the end
+// so that a page in shared memory serves up to 256 query rows and either stream's softmax
+// runs while the other's products do.  Roles: warp 0 claims items and streams K and V pages
+// through a ring of 32 KB stages by TMA; warps 1 and 2 issue a stream's MMAs (P, in bf16, is
+// read from TMEM as the A operand); warp 3 gathers q; warps 4-7 and 8-11 are the streams'
+// softmax (a thread per query row).  P is rounded to bf16 (2^-9 each, beside o's own
+// rounding); maxima, sums and o stay in fp32.
+#include <cmath>
+#include "kernels.cuh"
+
+namespace msa {
+
+namespace {
+
+constexpr int kSaMaxRows = 2048;           // rows of a call
+constexpr int kSaLevels = 6;               // levels of sharing above a leaf
+constexpr int kSaMaxSegs = kSaLevels + 1;
+constexpr int kSaThreads = 384;
+constexpr int kSaStages = 5;
+constexpr int kSaTile = 128 * 128 * 2;     // bytes of a 128 x 128 bf16 tile
+constexpr int kSaHalf = kSaTile / 2;       // one 64-channel half
+constexpr int kSaQWarp = 3;
+constexpr uint32_t kSaIdescWide = idesc_bf16(128, 128, false, false);    // S = Q K^T
+constexpr uint32_t kSaIdescNarrow = idesc_bf16(128, 64, false, false);   // 64 keys
+constexpr uint32_t kSaIdescPV = idesc_bf16(128, 128, false, true);       // O += P V
+constexpr float kSaLog2e = 1.4426950408889634f;
+constexpr float kSaRescale = 8.0f;         // log2 of the largest P before o is rescaled
+constexpr uint32_t kSaColO = 256;          // S of stream s at 128 s, O at 256 + 128 s
+
+// Work of a CTA: rows i0 .. i0 + nr - 1 (of the live ones), columns c0 .. c1 - 1, KV head
+// g.  Its parts are query rows ro * G .. of a block of m * G whose first is `base`.
+struct SaItem {
+  int i0, nr, c0, c1;
+  int g, m, ro, base;
+};
+
+// Parts of a row in one node: splits of (m G) query rows each, `ro` the row in the node
+struct SaSeg {
+  int base, m, ro, splits;
+};
+
+struct SaPlan {
+  int* live;          // [B] rows with tokens, in order
+  SaItem* items;
+  int* counts;        // [0] items, [1] next to claim
+  SaSeg* segs;        // [B][kSaMaxSegs]
+  int* n_segs;        // [B], 0 for rows without tokens
+  float4* part_o;     // [blocks][32][m G]
+  float2* part_ml;    // (maximum in log2, sum)
+  int max_items, max_parts;
+};
+
+__device__ __forceinline__ float sa_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void umma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- plan
+
+namespace {
+
+constexpr int kPlThreads = 1024;
+constexpr int kPlLengths = 32;
+// Candidate item lengths in pages
+__constant__ int kPlLength[kPlLengths] = {1,  2,  3,  4,  5,  6,  7,   8,   10,  12,  14,
+                                          16, 20, 24, 28, 32, 40, 48,  56,  64,  80,  96,
+                                          112, 128, 160, 192, 256, 320, 384, 512, 768, 1024};
+
+struct PlanSmem {
+  int warp_sums[32];
+  int n_live, items, parts;
+  float cost[kPlLengths];
+};
+
+// Exclusive scan over the CTA; *total = the sum
+__device__ __forceinline__ int pl_scan(int v, int* warp_sums, int* total) {
+  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) warp_sums[wp] = x;
+  __syncthreads();
+  if (wp == 0) {
+    int w = warp_sums[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, d);
+      if (lane >= d) w += y;
+    }
+    warp_sums[lane] = w;
+  }
+  __syncthreads();
+  const int before = wp > 0 ? warp_sums[wp - 1] : 0;
+  *total = warp_sums[31];
+  __syncthreads();
+  return before + x - v;
+}
+
+__device__ __forceinline__ int pl_splits(int pages, int L) { return (pages + L - 1) / L; }
+
+}  // namespace
+
+// Dynamic shared memory: 10 ints per row.  Nodes: boundary i (between live rows i and
+// i + 1) stands for the run in which it is the first boundary with its value; leaf i.
+__global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
+    const int32_t* __restrict__ table, const int32_t* __restrict__ lens, int B, int G, int Hkv,
+    int max_pages, int sms, SaPlan plan, uint32_t* status) {
+  pdl_enter();
+  extern __shared__ int smem_i[];
+  __shared__ PlanSmem sm;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int* row_of = smem_i;                    // [B] live rows
+  int* len_of = row_of + B;                // [B] their lengths
+  int* common = len_of + B;                // [B] c_i
+  int* parent = common + B;                // [B] boundary of the node above, -1: none
+  int* depth = parent + B;                 // [B] levels above; -1: no node here
+  int* first = depth + B;                  // [B] first live row of the node
+  int* rows = first + B;                   // [B] live rows of the node
+  int* base_n = rows + B;                  // [B] first part, nodes
+  int* base_l = base_n + B;                // [B] first part, leaves
+  int* leaf_up = base_l + B;               // [B] boundary of the node above a leaf, -1: none
+
+  // ---- rows with tokens
+  int n = 0;
+  for (int b0 = 0; b0 < B; b0 += kPlThreads) {
+    const int b = b0 + tid;
+    int L = 0;
+    if (b < B) {
+      L = lens[b];
+      if (L < 0 || L > max_pages * kBlock) {
+        atomicOr(status, kStatusBounds);
+        L = 0;
+      }
+      if (L == 0) plan.n_segs[b] = 0;
+    }
+    int total;
+    const int at = n + pl_scan(L > 0, sm.warp_sums, &total);
+    if (L > 0) {
+      row_of[at] = b;
+      len_of[at] = L;
+      plan.live[at] = b;
+    }
+    n += total;
+  }
+  __syncthreads();
+  // ---- full pages that neighbours have in common, a warp per pair
+  for (int i = warp; i < n; i += kPlThreads / 32) {
+    int c = 0;
+    if (i + 1 < n) {
+      const int most = min(len_of[i], len_of[i + 1]) / kBlock;
+      const int32_t* a = table + static_cast<size_t>(row_of[i]) * max_pages;
+      const int32_t* b = table + static_cast<size_t>(row_of[i + 1]) * max_pages;
+      c = most;
+      for (int j0 = 0; j0 < most; j0 += 128) {
+        int x[4], y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int j = j0 + 32 * k + lane;
+          x[k] = j < most ? __ldg(a + j) : 0;
+          y[k] = j < most ? __ldg(b + j) : 0;
+        }
+        int at = -1;
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+          const uint32_t differ = __ballot_sync(0xffffffffu, x[k] != y[k]);
+          if (differ) at = j0 + 32 * k + __ffs(differ) - 1;
+        }
+        if (at >= 0) {
+          c = at;
+          break;
+        }
+      }
+    }
+    if (lane == 0) common[i] = c;
+  }
+  __syncthreads();
+  // ---- runs.  Boundary i, value v: the nearest boundaries below v on both sides bound
+  // the run; the higher of their values is where the node above ends.
+  for (int i = tid; i < n; i += kPlThreads) {
+    const int v = i + 1 < n ? common[i] : 0;
+    int up = -1, rep = i, l = i - 1, r = i + 1;
+    if (v > 0) {
+      while (l >= 0 && common[l] >= v) {
+        if (common[l] == v) rep = l;
+        --l;
+      }
+      if (rep == i) {
+        while (r + 1 < n && common[r] >= v) ++r;
+        const int lv = l >= 0 ? common[l] : 0, rv = r + 1 < n ? common[r] : 0;
+        if (lv > 0 || rv > 0) up = lv >= rv ? l : r;
+      }
+    }
+    depth[i] = v > 0 && rep == i ? 0 : -1;
+    parent[i] = up;                         // a boundary of the run above, not yet its first
+    base_n[i] = rep;                        // first boundary of the run (kept here for now)
+    first[i] = l + 1;
+    rows[i] = r - l;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kPlThreads) {
+    if (depth[i] == 0 && parent[i] >= 0) parent[i] = base_n[parent[i]];
+    const int lv = i > 0 ? common[i - 1] : 0, rv = i + 1 < n ? common[i] : 0;
+    leaf_up[i] = lv > 0 || rv > 0 ? base_n[lv >= rv ? i - 1 : i] : -1;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kPlThreads)
+    if (depth[i] >= 0) {
+      int d = 0;
+      for (int p = parent[i]; p >= 0; p = parent[p]) ++d;
+      base_l[i] = d;
+    }
+  __syncthreads();
+  for (int i = tid; i < n; i += kPlThreads) {
+    if (depth[i] >= 0) depth[i] = base_l[i] < kSaLevels ? base_l[i] : -1;   // deeper runs: not shared
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kPlThreads) {
+    int p = leaf_up[i];
+    while (p >= 0 && depth[p] < 0) p = parent[p];
+    leaf_up[i] = p;
+  }
+  __syncthreads();
+  // Node k < n: boundary k; n <= k < 2n: leaf k - n.  v0 .. v1 - 1, m rows from i0.
+  const int tile_rows = 128 / G;            // token rows of a tile
+  auto node = [&](int k, int& v0, int& pages, int& i0, int& m) -> bool {
+    if (k < n) {
+      if (depth[k] < 0) return false;
+      v0 = parent[k] >= 0 ? common[parent[k]] : 0;
+      pages = common[k] - v0;
+      i0 = first[k];
+      m = rows[k];
+      return true;
+    }
+    k -= n;
+    v0 = leaf_up[k] >= 0 ? common[leaf_up[k]] : 0;
+    pages = (len_of[k] + kBlock - 1) / kBlock - v0;
+    i0 = k;
+    m = 1;
+    return pages > 0;
+  };
+  auto tiles_of = [&](int m) { return (m + 2 * tile_rows - 1) / (2 * tile_rows); };
+  // ---- item length: a warp weighs a candidate.  An item costs its pages, one for its
+  // start and end, and its parts' traffic; the CTAs' share of all that, or the rounds
+  // that the long items take, whichever is more.
+  for (int q = warp; q < kPlLengths; q += kPlThreads / 32) {
+    const int L = kPlLength[q];
+    float sum = 0.f, longest = 0.f;
+    int items = 0, big = 0;
+    long long parts = 0;
+    for (int k = lane; k < 2 * n; k += 32) {
+      int v0, pages, i0, m;
+      if (!node(k, v0, pages, i0, m)) continue;
+      const int ns = pl_splits(pages, L), tiles = tiles_of(m), each = tiles * ns * Hkv;
+      const float per = static_cast<float>(pages) / ns + 1.f +
+                        static_cast<float>(min(m, 2 * tile_rows) * G) * (1.f / 128.f);
+      sum += per * each;
+      longest = fmaxf(longest, per);
+      items += each;
+      parts += static_cast<long long>(m) * G * ns * Hkv;
+      if (2 * ((pages + ns - 1) / ns) > min(L, max_pages)) big += each;
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      longest = fmaxf(longest, __shfl_xor_sync(0xffffffffu, longest, d));
+      items += __shfl_xor_sync(0xffffffffu, items, d);
+      big += __shfl_xor_sync(0xffffffffu, big, d);
+      parts += __shfl_xor_sync(0xffffffffu, parts, d);
+    }
+    if (lane == 0) {
+      const bool fits = items <= plan.max_items && parts <= plan.max_parts;
+      const float rounds = static_cast<float>((max(big, 1) + sms - 1) / sms) * longest;
+      sm.cost[q] = fits ? fmaxf(sum / sms, rounds) : INFINITY;
+    }
+  }
+  __syncthreads();
+  int L = kPlLength[kPlLengths - 1];
+  {
+    float least = sm.cost[kPlLengths - 1];
+    for (int q = kPlLengths - 2; q >= 0; --q)
+      if (sm.cost[q] < least) {
+        least = sm.cost[q];
+        L = kPlLength[q];
+      }
+  }
+  // ---- first item and part of every node, shared nodes first
+  int at_item = 0, at_part = 0;
+  for (int k0 = 0; k0 < 2 * n; k0 += kPlThreads) {
+    const int k = k0 + tid;
+    int v0 = 0, pages = 0, i0 = 0, m = 0, items = 0, parts = 0;
+    const bool here = k < 2 * n && node(k, v0, pages, i0, m);
+    int ns = 0;
+    if (here) {
+      ns = pl_splits(pages, L);
+      items = tiles_of(m) * ns * Hkv;
+      parts = m * G * ns * Hkv;
+    }
+    int total_i, total_p;
+    const int it = at_item + pl_scan(items, sm.warp_sums, &total_i);
+    const int pt = at_part + pl_scan(parts, sm.warp_sums, &total_p);
+    at_item += total_i;
+    at_part += total_p;
+    if (k < n) base_n[k] = pt;
+    else if (k < 2 * n) base_l[k - n] = pt;
+    // this node's items, by its warp: nodes of the warp one after another
+    for (uint32_t todo = __ballot_sync(0xffffffffu, here); todo; todo &= todo - 1) {
+      const int src = __ffs(todo) - 1;
+      const int w_it = __shfl_sync(0xffffffffu, it, src), w_pt = __shfl_sync(0xffffffffu, pt, src);
+      const int w_v0 = __shfl_sync(0xffffffffu, v0, src), w_pages = __shfl_sync(0xffffffffu, pages, src);
+      const int w_i0 = __shfl_sync(0xffffffffu, i0, src), w_m = __shfl_sync(0xffffffffu, m, src);
+      const int w_ns = __shfl_sync(0xffffffffu, ns, src), count = __shfl_sync(0xffffffffu, items, src);
+      for (int e = lane; e < count; e += 32) {
+        const int tile = e % tiles_of(w_m), rest = e / tiles_of(w_m);
+        const int g = rest % Hkv, s = rest / Hkv;
+        SaItem item;
+        item.ro = tile * 2 * tile_rows;
+        item.i0 = w_i0 + item.ro;
+        item.nr = min(2 * tile_rows, w_m - item.ro);
+        item.c0 = w_v0 + static_cast<int>(static_cast<long long>(w_pages) * s / w_ns);
+        item.c1 = w_v0 + static_cast<int>(static_cast<long long>(w_pages) * (s + 1) / w_ns);
+        item.g = g;
+        item.m = w_m;
+        item.base = w_pt + (s * Hkv + g) * w_m * G;
+        if (w_it + e < plan.max_items) plan.items[w_it + e] = item;
+      }
+    }
+  }
+  if (tid == 0) {
+    plan.counts[0] = min(at_item, plan.max_items);
+    plan.counts[1] = 0;
+  }
+  __syncthreads();
+  // ---- every row's parts: its leaf, then the nodes above
+  for (int i = tid; i < n; i += kPlThreads) {
+    SaSeg* out = plan.segs + static_cast<size_t>(row_of[i]) * kSaMaxSegs;
+    int k = 0;
+    for (int p = n + i; p >= 0; p = p >= n ? leaf_up[i] : parent[p]) {
+      int v0, pages, i0, m;
+      if (!node(p, v0, pages, i0, m)) continue;
+      out[k++] = {p < n ? base_n[p] : base_l[p - n], m, i - i0, pl_splits(pages, L)};
+    }
+    plan.n_segs[row_of[i]] = k;
+  }
+}
+
+// ---------------------------------------------------------------- attention
+
+namespace {
+
+// What an item is for the warps other than the producer
+struct SaSlot {
+  int i0, nr, g, m;
+  int ro, base;
+  int pages;          // valid ones; -1: no items left
+  int tail;           // keys of the last of them
+  int wide;
+  uint32_t ring;      // stages used before the item
+  uint32_t qt;        // q tiles used before the item
+};
+
+struct SaSmem {
+  uint8_t q[2][kSaTile];
+  uint8_t ring[kSaStages][kSaTile];
+  float2 ml[2][128];                           // narrow: (max, sum) of each half's rows
+  SaSlot slot[2];
+  uint64_t slot_full[2], slot_empty[2];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t full[kSaStages], empty[kSaStages];
+  // per stream and S buffer: a waiter is never more than one phase behind
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];
+  uint64_t ml_full, o_free;
+  uint32_t tmem_base;
+};
+static_assert(sizeof(SaSmem) <= 232448, "above the 227 KB of a CTA");
+
+// 64 values of S as P: p = 2^(s sl2 - mu), packed; sums into acc
+__device__ __forceinline__ void sa_exp64(const uint32_t (&sv)[64], float sl2, float mu, uint32_t* pk,
+                                         float2 (&acc)[4]) {
+  const float2 f = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float2 y = ffma2(make_float2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), f, nmu);
+    const float2 p = make_float2(sa_ex2(y.x), sa_ex2(y.y));
+    acc[j & 3] = fadd2(acc[j & 3], p);
+    pk[j] = pack_bf16x2(p.x, p.y);
+  }
+}
+
+__device__ __forceinline__ float sa_max64(const uint32_t (&sv)[64]) {
+  float mx[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(sv[8 * i + j]);
+    mx[i] = fmaxf(max3f(max3f(max3f(x[0], x[1], x[2]), x[3], x[4]), x[5], x[6]), x[7]);
+  }
+  return max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+}
+
+__device__ __forceinline__ void sa_load64(uint32_t addr, uint32_t (&sv)[64]) {
+  tmem_ld32(addr, sv);
+  tmem_ld32(addr + 32, sv + 32);
+  tmem_ld_wait();
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ table,
+    const int32_t* __restrict__ lens, int G, int Hkv, int num_pages, int max_pages, float sl2,
+    const SaPlan plan, uint32_t* status) {
+  pdl_enter();
+  const int n_items = plan.counts[0];
+  if (static_cast<int>(blockIdx.x) >= n_items) return;    // as many items are claimed by the others
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023u) {                       // the tiles need 1024-byte alignment
+    if (threadIdx.x == 0) atomicOr(status, kStatusBounds);
+    return;
+  }
+  SaSmem& sm = *reinterpret_cast<SaSmem*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int Hq = G * Hkv, tile_rows = 128 / G;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.slot_full[i], 1);
+      mbar_init(&sm.slot_empty[i], 2 + 1 + 8);
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_empty[i], 2);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sm.s_full[i][b], 1);
+        mbar_init(&sm.p_full[i][b], 4);
+        mbar_init(&sm.pv_done[i][b], 1);
+      }
+    }
+    for (int i = 0; i < kSaStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 2);
+    }
+    mbar_init(&sm.ml_full, 8);
+    mbar_init(&sm.o_free, 8);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tmap(&tm_k);
+      prefetch_tmap(&tm_v);
+    }
+    uint32_t pos = 0, qt = 0, tc = 0;
+    bool alive = true;
+    while (alive) {
+      int id = 0;
+      if (lane == 0) id = atomicAdd(plan.counts + 1, 1);
+      id = __shfl_sync(0xffffffffu, id, 0);
+      const int tb = tc & 1;
+      if (lane == 0) alive = mbar_wait(&sm.slot_empty[tb], ((tc >> 1) & 1) ^ 1, status, 100);
+      alive = __shfl_sync(0xffffffffu, alive ? 1 : 0, 0) != 0;
+      if (!alive) break;
+      if (id >= n_items) {
+        if (lane == 0) {
+          sm.slot[tb].pages = -1;
+          mbar_arrive(&sm.slot_full[tb]);
+        }
+        break;
+      }
+      const SaItem it = plan.items[id];
+      const int row = plan.live[it.i0];
+      const int32_t* trow = table + static_cast<size_t>(row) * max_pages;
+      // pages that are none have no keys; the others are counted first
+      int valid = 0;
+      bool last_ok = true;
+      for (int c = it.c0; c < it.c1; c += 32) {
+        const int pg = c + lane < it.c1 ? __ldg(trow + c + lane) : 0;
+        const bool ok = c + lane < it.c1 && pg >= 0 && pg < num_pages;
+        const uint32_t oks = __ballot_sync(0xffffffffu, ok);
+        valid += __popc(oks);
+        if (it.c1 - c <= 32) last_ok = (oks >> (it.c1 - 1 - c)) & 1;
+      }
+      if (lane == 0) {
+        if (valid != it.c1 - it.c0) atomicOr(status, kStatusBounds);
+        SaSlot& s = sm.slot[tb];
+        s.i0 = it.i0;
+        s.nr = it.nr;
+        s.g = it.g;
+        s.m = it.m;
+        s.ro = it.ro;
+        s.base = it.base;
+        s.pages = valid;
+        s.tail = last_ok ? min(kBlock, lens[row] - (it.c1 - 1) * kBlock) : kBlock;
+        s.wide = it.nr > tile_rows;
+        s.ring = pos;
+        s.qt = qt;
+        mbar_arrive(&sm.slot_full[tb]);
+      }
+      qt += it.nr > tile_rows ? 2 : 1;
+      for (int c = it.c0; alive && c < it.c1; c += 32) {
+        const int mine = c + lane < it.c1 ? __ldg(trow + c + lane) : -1;
+        uint32_t oks = __ballot_sync(0xffffffffu, mine >= 0 && mine < num_pages);
+        for (; alive && oks; oks &= oks - 1) {
+          const int page = __shfl_sync(0xffffffffu, mine, __ffs(oks) - 1);
+          if (lane == 0) {
+            const int at = page * Hkv + it.g;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              const uint32_t st = pos % kSaStages;
+              alive = mbar_wait(&sm.empty[st], ((pos / kSaStages) & 1) ^ 1, status, 101 + kv);
+              if (!alive) break;
+              mbar_arrive_expect_tx(&sm.full[st], kSaTile);
+              const CUtensorMap* tm = kv ? &tm_v : &tm_k;
+              tma_load_3d(sm.ring[st], tm, &sm.full[st], 0, 0, at);
+              tma_load_3d(sm.ring[st] + kSaHalf, tm, &sm.full[st], 64, 0, at);
+              ++pos;
+            }
+          }
+          alive = __shfl_sync(0xffffffffu, alive ? 1 : 0, 0) != 0;
+        }
+      }
+      pos = __shfl_sync(0xffffffffu, pos, 0);
+      ++tc;
+    }
+    if (!alive && lane == 0) {
+      // a wait ran out: the copies in flight have to land before the CTA ends
+      const uint32_t from = pos > kSaStages ? pos - kSaStages : 0;
+      for (uint32_t p = from; p < pos; ++p)
+        (void)mbar_wait(&sm.full[p % kSaStages], (p / kSaStages) & 1, status, 103);
+    }
+  } else if (warp == 1 || warp == 2) {
+    // ------------------------------------------------------------ MMA of stream s
+    const int s = warp - 1;
+    if (elect_one()) {
+      uint32_t uses[2] = {0, 0};            // of the S buffers
+      uint32_t tc = 0, items_with_o = 0;
+      bool ok = true;
+      auto pv_wait = [&](int b) {           // the last PV that read buffer b is done
+        return uses[b] == 0 || mbar_wait(&sm.pv_done[s][b], (uses[b] - 1) & 1, status, 110);
+      };
+      while (ok) {
+        const int tb = tc & 1;
+        if (!(ok = mbar_wait(&sm.slot_full[tb], (tc >> 1) & 1, status, 111))) break;
+        const SaSlot t = sm.slot[tb];
+        if (t.pages < 0) break;
+        const uint32_t qi = t.qt + (t.wide ? s : 0);
+        const int qb = qi & 1;
+        if (!(ok = mbar_wait(&sm.q_full[qb], (qi >> 1) & 1, status, 112))) break;
+        if (!(ok = pv_wait(0) && pv_wait(1))) break;
+        tc_fence_after();
+        const uint32_t qa = smem_u32(sm.q[qb]);
+        const uint32_t d_s = tmem + 128 * s, d_o = tmem + kSaColO + 128 * s;
+        auto scores = [&](int i) -> bool {
+          const uint32_t p = t.ring + 2 * i, st = p % kSaStages;
+          const int b = t.wide ? 0 : (i & 1);
+          if (!mbar_wait(&sm.full[st], (p / kSaStages) & 1, status, 113) || !pv_wait(b)) return false;
+          tc_fence_after();
+          const uint32_t ka = smem_u32(sm.ring[st]) + (t.wide ? 0 : s * 64 * 128);
+          const uint32_t d = d_s + 64 * b, idesc = t.wide ? kSaIdescWide : kSaIdescNarrow;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * kSaHalf + (kk & 3) * 32;
+            umma_bf16(d, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), idesc, kk > 0);
+          }
+          umma_commit(&sm.s_full[s][b]);
+          umma_commit(&sm.empty[st]);
+          ++uses[b];
+          return true;
+        };
+        if (t.pages > 0) ok = scores(0);
+        for (int i = 0; ok && i < t.pages; ++i) {
+          if (!t.wide && i + 1 < t.pages && !(ok = scores(i + 1))) break;
+          const int b = t.wide ? 0 : (i & 1);
+          const uint32_t p = t.ring + 2 * i + 1, st = p % kSaStages;
+          // uses of b so far, without the score of page i + 2
+          if (!(ok = mbar_wait(&sm.p_full[s][b], (uses[b] - 1) & 1, status, 114))) break;
+          if (!(ok = mbar_wait(&sm.full[st], (p / kSaStages) & 1, status, 115))) break;
+          // the item's first PV overwrites O: the item before must have been read
+          if (i == 0 && items_with_o > 0 &&
+              !(ok = mbar_wait(&sm.o_free, (items_with_o - 1) & 1, status, 116)))
+            break;
+          tc_fence_after();
+          const uint32_t va = smem_u32(sm.ring[st]) + (t.wide ? 0 : s * 64 * 128);
+          const int steps = t.wide ? 8 : 4;
+          for (int kk = 0; kk < steps; ++kk)
+            umma_tmem_a(d_o, d_s + 64 * b + 8 * kk, sdesc_sw128(va + kk * 2048, kSaHalf, 1024), kSaIdescPV,
+                        i > 0 || kk > 0);
+          umma_commit(&sm.pv_done[s][b]);
+          umma_commit(&sm.empty[st]);
+          if (t.wide && i + 1 < t.pages && !(ok = scores(i + 1))) break;
+        }
+        if (!ok) break;
+        ++items_with_o;
+        mbar_arrive(&sm.slot_empty[tb]);
+        if (t.wide) mbar_arrive(&sm.q_empty[qb]);    // the other stream reads the other tile
+        umma_commit(&sm.q_empty[qb]);
+        ++tc;
+      }
+    }
+  } else if (warp == kSaQWarp) {
+    // ------------------------------------------------------------ q
+    uint32_t tc = 0;
+    bool ok = true;
+    while (ok) {
+      const int tb = tc & 1;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.slot_full[tb], (tc >> 1) & 1, status, 120)))) break;
+      const SaSlot t = sm.slot[tb];
+      if (t.pages < 0) break;
+      for (int w = 0; ok && w <= t.wide; ++w) {
+        const uint32_t qi = t.qt + w;
+        const int qb = qi & 1;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_empty[qb], ((qi >> 1) & 1) ^ 1, status, 121)))) break;
+        const int r0 = w * tile_rows, nr = min(tile_rows, t.nr - r0) * G;
+        const int c = lane & 15;
+        uint8_t* dst = sm.q[qb] + (c >> 3) * kSaHalf;
+        for (int r = lane >> 4; r < nr; r += 16) {
+          uint4 v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rr = r + 2 * k;
+            if (rr < nr) {
+              const int tok = rr / G, h = rr - tok * G;
+              const int b = plan.live[t.i0 + r0 + tok];
+              v[k] = *reinterpret_cast<const uint4*>(q + (static_cast<size_t>(b) * Hq + t.g * G + h) * kD + 8 * c);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rr = r + 2 * k;
+            if (rr < nr) *reinterpret_cast<uint4*>(dst + sw128_offset(rr, c & 7)) = v[k];
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_full[qb]);
+      }
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(&sm.slot_empty[tb]);
+      ++tc;
+    }
+  } else {
+    // ------------------------------------------------------------ softmax of stream s
+    const int s = (warp - 4) >> 2, subp = warp & 3;
+    const int r = subp * 32 + lane;                      // tile row = TMEM lane
+    const uint32_t trow = static_cast<uint32_t>(subp * 32) << 16;
+    const uint32_t d_s = tmem + 128 * s + trow, d_o = tmem + kSaColO + 128 * s + trow;
+    uint32_t uses[2] = {0, 0}, tc = 0, merges = 0;
+    bool ok = true;
+    while (ok) {
+      const int tb = tc & 1;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.slot_full[tb], (tc >> 1) & 1, status, 130)))) break;
+      const SaSlot t = sm.slot[tb];
+      if (t.pages < 0) break;
+      const int r0 = t.wide ? s * tile_rows : 0;         // first token row of the tile
+      const int nq = min(tile_rows, t.nr - r0) * G;      // its query rows
+      const bool work = subp * 32 < nq;                  // the warp has any
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; ok && i < t.pages; ++i) {
+        const int b = t.wide ? 0 : (i & 1);
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[s][b], uses[b] & 1, status, 131)))) break;
+        tc_fence_after();
+        const bool last = i + 1 == t.pages;
+        const int keys = last ? t.tail : kBlock;
+        // keys of this stream's half of the page (a wide item has full pages only)
+        const int lim = t.wide ? 64 : min(64, keys - 64 * s);
+        const uint32_t sbuf = d_s + 64 * b;
+        if (work) {
+          uint32_t sv[64], pk[64];
+          float mx = -INFINITY;
+          if (t.wide) {
+            sa_load64(sbuf, sv);
+            mx = sa_max64(sv);
+          }
+          // wide: the second 64 keys are exponentiated first, then the first 64 again
+          sa_load64(t.wide ? sbuf + 64 : sbuf, sv);
+          if (lim < 64) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) sv[j] = j < lim ? sv[j] : 0xFF800000u;
+          }
+          mx = fmaxf(mx, sa_max64(sv));
+          const bool any = lim > 0;
+          const float mnew = any ? fmaxf(m, mx * sl2) : m;
+          const bool resc = mnew > m + kSaRescale;
+          const float mu = resc ? mnew : m;
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                           make_float2(0.f, 0.f)};
+          if (any) {
+            sa_exp64(sv, sl2, mu, pk + 32, acc);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) pk[32 + j] = 0u;
+          }
+          if (t.wide) {
+            sa_load64(sbuf, sv);
+            sa_exp64(sv, sl2, mu, pk, acc);
+          }
+          const bool need = resc && m != -INFINITY;
+          if (__any_sync(0xffffffffu, need)) {
+            // O stands still once the PV of the page before is done
+            const int pb = t.wide ? 0 : ((i - 1) & 1);
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[s][pb], (uses[pb] - 1) & 1, status, 132)))) break;
+            tc_fence_after();
+            const float alpha = need ? sa_ex2(m - mu) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[32];
+              tmem_ld32(d_o + c * 32, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+              tmem_st16(d_o + c * 32, v);
+              tmem_st16(d_o + c * 32 + 16, v + 16);
+            }
+          }
+          if (any) {
+            const float2 a = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+            const float rs = a.x + a.y;
+            l = m == -INFINITY ? rs : (resc ? l * sa_ex2(m - mu) : l) + rs;
+            m = mu;
+          }
+          if (t.wide) {
+            tmem_st16(sbuf, pk);
+            tmem_st16(sbuf + 16, pk + 16);
+            tmem_st16(sbuf + 32, pk + 32);
+            tmem_st16(sbuf + 48, pk + 48);
+          } else {
+            tmem_st16(sbuf, pk + 32);
+            tmem_st16(sbuf + 16, pk + 48);
+          }
+          tmem_st_wait();
+        }
+        if (last && t.tail < kBlock) {
+          // what lies behind the row's end may be anything, and 0 times it has to be 0
+          const uint32_t p = t.ring + 2 * i + 1, st = p % kSaStages;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[st], (p / kSaStages) & 1, status, 133)))) break;
+          // (only a leaf has such a page: either stream clears the 64 keys that it multiplies)
+          const int key = 64 * s + (r >> 1);
+          if (key >= t.tail) {
+            uint4* v = reinterpret_cast<uint4*>(sm.ring[st] + (r & 1) * kSaHalf + key * 128);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[s][b]);
+        ++uses[b];
+      }
+      if (!ok) break;
+      // ---- the item's parts
+      const size_t rows = static_cast<size_t>(t.m) * G;
+      const size_t at = static_cast<size_t>(t.ro + r0) * G + r;
+      float4* po = plan.part_o + static_cast<size_t>(t.base) * 32 + at;
+      const bool mine = r < nq;
+      if (t.pages > 0) {
+        const int b = t.wide ? 0 : ((t.pages - 1) & 1);
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[s][b], (uses[b] - 1) & 1, status, 134)))) break;
+      }
+      float f0 = 1.f, f1 = 0.f;
+      float2 ml = make_float2(m, l);
+      if (!t.wide && t.pages > 0) {
+        // both halves' maxima; either stream then writes half of the channels
+        sm.ml[s][r] = ml;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.ml_full);
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.ml_full, merges & 1, status, 135)))) break;
+        ++merges;
+        const float2 a = sm.ml[0][r], c = sm.ml[1][r];
+        const float M = fmaxf(a.x, c.x);
+        f0 = a.x == -INFINITY ? 0.f : sa_ex2(a.x - M);
+        f1 = c.x == -INFINITY ? 0.f : sa_ex2(c.x - M);
+        ml = make_float2(M, a.y * f0 + c.y * f1);
+      }
+      tc_fence_after();
+      if (t.pages == 0) {
+        if (mine && (t.wide || s == 0)) {
+          for (int d = 0; d < 32; ++d) po[d * rows] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      } else if (work) {
+        const uint32_t o0 = tmem + kSaColO + trow;
+#pragma unroll 1
+        for (int c = 0; c < (t.wide ? 8 : 4); ++c) {
+          const int col = t.wide ? 16 * c : 64 * s + 16 * c;
+          uint32_t x[16], y[16];
+          if (t.wide) {
+            tmem_ld16(d_o + col, x);
+          } else {
+            tmem_ld16(o0 + col, x);
+            tmem_ld16(o0 + 128 + col, y);
+          }
+          tmem_ld_wait();
+          if (!t.wide) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float a = f0 > 0.f ? __uint_as_float(x[j]) * f0 : 0.f;
+              x[j] = __float_as_uint(f1 > 0.f ? fmaf(__uint_as_float(y[j]), f1, a) : a);
+            }
+          }
+          if (mine) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              po[(col / 4 + j) * rows] =
+                  make_float4(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1]),
+                              __uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3]));
+          }
+        }
+      }
+      if (mine && (t.wide || s == 0)) plan.part_ml[t.base + at] = ml;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.o_free);
+        mbar_arrive(&sm.slot_empty[tb]);
+      }
+      ++tc;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- combine
+
+// grid (rows, KV heads, shares of the G heads); thread (d4, head): heads run fastest, as the
+// parts lie in memory
+__global__ void __launch_bounds__(512) shared_combine_kernel(const SaPlan plan, int G, int Hkv,
+                                                             __nv_bfloat16* __restrict__ o,
+                                                             float* __restrict__ lse) {
+  pdl_enter();
+  const int b = blockIdx.x, g = blockIdx.y, Gc = blockDim.x / 32;
+  const int h = blockIdx.z * Gc + threadIdx.x % Gc, d4 = threadIdx.x / Gc;
+  if (h >= G) return;
+  const int ns = plan.n_segs[b];
+  float M = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < ns; ++k) {
+    const SaSeg sg = plan.segs[static_cast<size_t>(b) * kSaMaxSegs + k];
+    const size_t rows = static_cast<size_t>(sg.m) * G, at = static_cast<size_t>(sg.ro) * G + h;
+    for (int s = 0; s < sg.splits; ++s) {
+      const size_t base = sg.base + (static_cast<size_t>(s) * Hkv + g) * rows;
+      const float2 ml = plan.part_ml[base + at];
+      const float4 x = plan.part_o[base * 32 + d4 * rows + at];
+      if (ml.x == -INFINITY) continue;
+      const float top = fmaxf(M, ml.x), f = sa_ex2(M - top), e = sa_ex2(ml.x - top);
+      acc.x = fmaf(acc.x, f, x.x * e);
+      acc.y = fmaf(acc.y, f, x.y * e);
+      acc.z = fmaf(acc.z, f, x.z * e);
+      acc.w = fmaf(acc.w, f, x.w * e);
+      l = fmaf(l, f, ml.y * e);
+      M = top;
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const size_t at = (static_cast<size_t>(b) * Hkv + g) * G + h;
+  if (M == -INFINITY) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  *reinterpret_cast<uint2*>(o + at * kD + 4 * d4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lse && d4 == 0) lse[at] = M == -INFINITY ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
+}
+
+// ---------------------------------------------------------------- host
+
+namespace {
+
+SaPlan carve_shared_workspace(WsCursor& ws, int B, int Hq, int Hkv) {
+  const long long sms = device_sm_count();
+  SaPlan p{};
+  // With items of the longest length a node has one per tile and KV head: B tiles of leaves
+  // and at most 3/4 B (runs of 3 in tiles of 2 rows) at each of the levels; beyond that, room
+  // to cut for all SMs.
+  p.max_items = static_cast<int>(6LL * B * Hkv + 8 * sms);
+  const long long parts = static_cast<long long>(B) * Hq * kSaMaxSegs + 2 * sms * 256;
+  p.max_parts = static_cast<int>(parts);
+  p.live = ws.take<int>(B);
+  p.items = ws.take<SaItem>(p.max_items);
+  p.counts = ws.take<int>(2);
+  p.segs = ws.take<SaSeg>(static_cast<size_t>(B) * kSaMaxSegs);
+  p.n_segs = ws.take<int>(B);
+  p.part_ml = ws.take<float2>(p.max_parts);
+  p.part_o = ws.take<float4>(static_cast<size_t>(p.max_parts) * 32);
+  return p;
+}
+
+bool shared_sizes_ok(int B, int Hq, int Hkv) {
+  return B >= 1 && B <= kSaMaxRows && Hkv >= 1 && Hkv <= 256 && Hq >= 1 && Hq % Hkv == 0 &&
+         Hq / Hkv <= 128 && Hq <= 1024;
+}
+
+}  // namespace
+
+}  // namespace msa
+
+using namespace msa;
+
+extern "C" {
+
+size_t msa_decode_shared_workspace_size(int B, int Hq, int Hkv, int max_pages) {
+  (void)max_pages;
+  if (!shared_sizes_ok(B, Hq, Hkv)) return 0;
+  WsCursor ws(nullptr);
+  carve_shared_workspace(ws, B, Hq, Hkv);
+  return ws.used + 256;
+}
+
+msa_status_t msa_decode_shared(const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_table, const int32_t* cache_lens, int B,
+                               int Hq, int Hkv, int num_pages, int max_pages, float scale, void* o,
+                               float* lse, void* workspace, size_t workspace_bytes,
+                               msa_stream_t stream) {
+  MSA_REQUIRE_PTR(q);
+  MSA_REQUIRE_PTR(k_cache);
+  MSA_REQUIRE_PTR(v_cache);
+  MSA_REQUIRE_PTR(block_table);
+  MSA_REQUIRE_PTR(cache_lens);
+  MSA_REQUIRE_PTR(o);
+  MSA_REQUIRE_PTR(workspace);
+  if (lse && !aligned16(lse)) return fail(MSA_ERR_INVALID_ARG, "lse is not 16-byte aligned");
+  if (B < 1) return fail(MSA_ERR_INVALID_ARG, "B must be >= 1");
+  if (B > kSaMaxRows) return fail(MSA_ERR_UNSUPPORTED, "at most %d rows (got %d)", kSaMaxRows, B);
+  MSA_TRY(check_cache_sizes(Hkv, num_pages, max_pages));
+  if (Hq < 1 || Hq % Hkv != 0)
+    return fail(MSA_ERR_INVALID_ARG, "Hq (%d) must be a positive multiple of Hkv (%d)", Hq, Hkv);
+  if (!shared_sizes_ok(B, Hq, Hkv))
+    return fail(MSA_ERR_UNSUPPORTED, "at most 128 query heads per KV head and 1024 in all (got %d / %d)", Hq, Hkv);
+  if (static_cast<long long>(num_pages) * Hkv > INT32_MAX)
+    return fail(MSA_ERR_UNSUPPORTED, "num_pages * Hkv above 2^31");
+  if (!(scale >= 0x1p-64f && scale <= 0x1p64f))
+    return fail(MSA_ERR_INVALID_ARG, "scale must be from 2^-64 to 2^64");
+  if (workspace_bytes < msa_decode_shared_workspace_size(B, Hq, Hkv, max_pages))
+    return fail(MSA_ERR_INVALID_ARG, "workspace too small");
+  WsCursor ws(workspace);
+  const SaPlan plan = carve_shared_workspace(ws, B, Hq, Hkv);
+  const int G = Hq / Hkv, sms = device_sm_count();
+  CUtensorMap tk, tv;
+  const uint64_t dims[3] = {static_cast<uint64_t>(kD), static_cast<uint64_t>(kBlock),
+                            static_cast<uint64_t>(num_pages) * Hkv};
+  const uint32_t box[3] = {64, kBlock, 1};
+  if (!make_tmap_bf16(&tk, k_cache, 3, dims, box) || !make_tmap_bf16(&tv, v_cache, 3, dims, box))
+    return fail(MSA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the caches");
+  uint32_t* sw = nullptr;
+  MSA_TRY(status_word(&sw));
+  MSA_TRY(ensure_smem(shared_attn_kernel, sizeof(SaSmem), "shared_attn_kernel"));
+  const size_t plan_smem = static_cast<size_t>(B) * 10 * sizeof(int);
+  MSA_TRY(ensure_smem(shared_plan_kernel, static_cast<size_t>(kSaMaxRows) * 10 * sizeof(int), "shared_plan_kernel"));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  {
+    TraceScope trace_("shared_plan_kernel", st);
+    launch_pdl(shared_plan_kernel, 1, kPlThreads, plan_smem, st, block_table, cache_lens, B, G, Hkv,
+               max_pages, sms, plan, sw);
+  }
+  MSA_TRY(check_launch("shared_plan_kernel"));
+  {
+    TraceScope trace_("shared_attn_kernel", st);
+    launch_pdl(shared_attn_kernel, sms, kSaThreads, sizeof(SaSmem), st, tk, tv,
+               static_cast<const __nv_bfloat16*>(q), block_table, cache_lens, G, Hkv, num_pages, max_pages,
+               scale * kSaLog2e, plan, sw);
+  }
+  MSA_TRY(check_launch("shared_attn_kernel"));
+  {
+    TraceScope trace_("shared_combine_kernel", st);
+    const int Gc = G < 16 ? G : 16;
+    launch_pdl(shared_combine_kernel, dim3(B, Hkv, (G + Gc - 1) / Gc), 32 * Gc, 0, st, plan, G, Hkv,
+               static_cast<__nv_bfloat16*>(o), lse);
+  }
+  return check_launch("shared_combine_kernel");
+}
+
+}  // extern "C"
