@@ -471,7 +471,8 @@ MSA_API msa_status_t msa_decode_shared(const void* q, const void* k_cache, const
  * as 64-bit values over a log-sum-exp of fp32 exponentials; equal ones go to the lower
  * w V + v.  A beam with finished[r] != 0 (uint8 [N W], NULL: none) goes on by
  * pad_token alone, with its score unchanged; its logits are not read.  A NaN among
- * the logits counts as -infinity, +infinity as the largest finite value; a beam whose
+ * the logits counts as -infinity, what lies above 2^28 as 2^28 (and, where a beam has
+ * nothing else, what lies below -2^28 as -2^28); a beam whose
  * score is -infinity or NaN is dead.  Continuations of probability zero are never chosen:
  * where fewer than K are left, the last places get score -infinity, parent -1, token -1
  * (msa_pages_reorder empties such rows).  W, K <= 64, K <= W V, V <= 2^24, N W <= 65535.

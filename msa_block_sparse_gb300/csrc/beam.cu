@@ -26,12 +26,15 @@ namespace {
 constexpr int kBmThreads = 256;
 constexpr int kBmMaxK = 64;
 constexpr int kBmMaxW = 64;
-constexpr int kBmValues = 32;                          // of a thread and tile
+constexpr int kBmValues = 16;                          // of a thread and tile
 constexpr int kBmTile = kBmThreads * kBmValues;
 constexpr int kBmCap = kBmMaxK * kBmValues + kBmThreads;   // keys of the buffer
 constexpr int kBmCandidates = 16384;                   // of a prompt, at most
 constexpr int kBmMergeThreads = 512;
-constexpr float kBmLog2e = 1.4426950408889634f;
+constexpr float kBmLog2eHi = 1.4426950216293335f;      // log2 e, and what fp32 leaves of it
+constexpr float kBmLog2eLo = 1.925963033500e-8f;
+constexpr double kBmLn2 = 0.69314718055994530942;
+constexpr float kBmHuge = 0x1p28f;                     // beyond: |x log2 e - ref| could overflow 2^127
 
 // Order of floats as order of unsigned integers (0: below -infinity, used for "nothing")
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -51,9 +54,10 @@ __device__ __forceinline__ unsigned long long key_of(float x, uint32_t idx) {
   return (static_cast<unsigned long long>(ordered(x)) << 32) | (0xFFFFFFFFu - idx);
 }
 
+// Sum of e^x of a slice: sum * 2^ref, ref a whole number (-infinity: the sum is 0), so that
+// joining two sums rounds nothing but the addition
 struct BeamScan {
-  double top;    // maximum
-  double sum;    // of e^(x - top)
+  float ref, sum;
 };
 
 template <typename T>
@@ -111,6 +115,11 @@ __device__ __forceinline__ float bm_ex2(float x) {
   return y;
 }
 
+// 2^d of a whole number d <= 0
+__device__ __forceinline__ float bm_scale(float d) {
+  return d < -126.f ? 0.f : __int_as_float((static_cast<int>(d) + 127) << 23);
+}
+
 // NaN counts as -infinity, +infinity as the largest finite value
 __device__ __forceinline__ float plain(float x) {
   return x != x ? -INFINITY : fminf(x, FLT_MAX);
@@ -121,8 +130,7 @@ struct ScanSmem {
   unsigned long long best[kBmMaxK];
   alignas(16) float group[128];
   alignas(16) unsigned long long gkey[kBmThreads];
-  double sum[kBmThreads / 32];
-  float top[kBmThreads / 32];
+  float sum[kBmThreads / 32], ref[kBmThreads / 32];
   float bound;
   unsigned long long bound_key;
   int count;
@@ -173,13 +181,9 @@ __device__ __forceinline__ void bm_rank(ScanSmem& sm, int K) {
 
 }  // namespace
 
-// e^(x - top) as a power of two; the factor's rounding (1.3e-8 of the exponent) is far below
-// the exponential's own
-__device__ __forceinline__ float bm_exp(float x, float top) { return bm_ex2((x - top) * kBmLog2e); }
-
 // grid (slices, rows)
 template <typename T>
-__global__ void __launch_bounds__(kBmThreads) beam_scan_kernel(
+__global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
     const T* __restrict__ logits, long long ld, int V, int K, const uint8_t* __restrict__ finished,
     BeamScan* __restrict__ stats, unsigned long long* __restrict__ keys) {
   pdl_enter();
@@ -203,8 +207,8 @@ __global__ void __launch_bounds__(kBmThreads) beam_scan_kernel(
       return __ldcs(reinterpret_cast<const uint4*>(xa + lo));
     return L::part(xa + lo, skew - lo, skew + V - lo);
   };
-  float top = -INFINITY, bound = -INFINITY;
-  double sum = 0.0;
+  float ref = -INFINITY, sum = 0.f, bound = -INFINITY;   // this thread's sum is sum * 2^ref
+  int kept = 0;                                          // keys in the buffer, at most kBmThreads
   if (tid == 0) sm.count = 0;
   uint4 raw[kVecs];
 #pragma unroll
@@ -220,39 +224,41 @@ __global__ void __launch_bounds__(kBmThreads) beam_scan_kernel(
     auto place = [&](int i) -> uint32_t {
       return static_cast<uint32_t>((vt + (i / L::kN) * kBmThreads + tid) * L::kN + i % L::kN - skew);
     };
-    // ---- maximum and sum of exponentials of this thread's values
-    float best = -INFINITY, part = 0.f;
-    auto scan = [&]() {
+    // ---- maximum and sum of exponentials of this thread's values.  x log2 e - ref with ref
+    // whole is rounded relative to itself, however large x is.
+    float best = -INFINITY, part = 0.f, to = ref;
+    auto scan = [&](float most) {
       best = val[0];
 #pragma unroll
       for (int i = 1; i < kBmValues; ++i) best = fmaxf(best, val[i]);
-      const float ref = best > -INFINITY ? -best : 0.f;
-      float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                       make_float2(0.f, 0.f)};
+      to = fmaxf(ref, rintf(fminf(fmaxf(best, -most), most) * kBmLog2eHi));
+      const float2 hi = make_float2(kBmLog2eHi, kBmLog2eHi), lo = make_float2(kBmLog2eLo, kBmLog2eLo);
+      const float2 r = make_float2(-to, -to);
+      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int i = 0; i < kBmValues; i += 2) {
-        const float2 y = __fmul2_rn(__fadd2_rn(make_float2(val[i], val[i + 1]), make_float2(ref, ref)),
-                                    make_float2(kBmLog2e, kBmLog2e));
-        acc[(i >> 1) & 3] = __fadd2_rn(acc[(i >> 1) & 3], make_float2(bm_ex2(y.x), bm_ex2(y.y)));
+        float2 x = make_float2(val[i], val[i + 1]);
+        if (most < INFINITY) {                           // the ends, but for -infinity, count as +-2^28
+          x.x = x.x > -INFINITY ? fminf(fmaxf(x.x, -most), most) : x.x;
+          x.y = x.y > -INFINITY ? fminf(fmaxf(x.y, -most), most) : x.y;
+        }
+        const float2 y = __ffma2_rn(x, lo, __ffma2_rn(x, hi, r));
+        acc[(i >> 1) & 1] = __fadd2_rn(acc[(i >> 1) & 1], make_float2(bm_ex2(y.x), bm_ex2(y.y)));
       }
-      const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+      const float2 a = __fadd2_rn(acc[0], acc[1]);
       part = a.x + a.y;
     };
-    scan();
-    if (!(part < INFINITY)) {                            // a NaN or +infinity among them
+    scan(INFINITY);
+    if (best > -INFINITY && !(part < INFINITY && fabsf(best) < kBmHuge)) {   // NaN, +infinity, huge
 #pragma unroll
       for (int i = 0; i < kBmValues; ++i) val[i] = plain(val[i]);
-      scan();
+      scan(kBmHuge);
     }
-    if (best > top) {
-      sum = sum * bm_exp(top, best) + part;
-      top = best;
-    } else if (best > -INFINITY) {
-      sum += static_cast<double>(part) * bm_exp(best, top);
+    if (best > -INFINITY) {
+      sum = (ref > -INFINITY ? sum * bm_scale(ref - to) : 0.f) + part;
+      ref = to;
     }
     // ---- candidates: what reaches the bound goes into the buffer
-    int kept = 0;                                        // keys of earlier tiles
-    float least = bound;
     const bool first = vt == v0;
     if (first) {
       // bound: the K-th largest of the maxima of 64 or 128 groups of threads
@@ -277,11 +283,11 @@ __global__ void __launch_bounds__(kBmThreads) beam_scan_kernel(
       }
       if (above < K && level >= K) sm.bound = g;         // one value, whoever writes it
       __syncthreads();
-      bound = least = sm.bound;
-    } else {
-      kept = sm.count;                                   // at most kBmThreads
-      __syncthreads();
+      bound = sm.bound;
+    } else if (!__syncthreads_or(best > bound)) {
+      continue;
     }
+    const float least = bound;
     // later tiles lose ties: K values at least as large stand before them
     if (first ? best >= least : best > least) {
 #pragma unroll
@@ -317,35 +323,35 @@ __global__ void __launch_bounds__(kBmThreads) beam_scan_kernel(
       }
       __syncthreads();
     }
-    if (sm.count > kBmThreads) {
+    kept = sm.count;
+    if (kept > kBmThreads) {
       bm_rank(sm, K);
-      if (sm.count == K) bound = unordered(static_cast<uint32_t>(sm.key[K - 1] >> 32));
+      kept = sm.count;
+      if (kept == K) bound = unordered(static_cast<uint32_t>(sm.key[K - 1] >> 32));
     }
   }
   bm_rank(sm, K);
   unsigned long long* out = keys + (static_cast<size_t>(row) * slices + blockIdx.x) * K;
   if (tid < K) out[tid] = tid < sm.count ? sm.key[tid] : 0;
-  // ---- maximum and sum of the slice
+  // ---- the slice's sum
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) {
-    const float o = __shfl_xor_sync(0xffffffffu, top, m);
-    const double os = __shfl_xor_sync(0xffffffffu, sum, m);
-    const float t = fmaxf(top, o);
-    if (t > -INFINITY) sum = sum * bm_exp(top, t) + os * bm_exp(o, t);
-    top = t;
+    const float o = __shfl_xor_sync(0xffffffffu, ref, m), os = __shfl_xor_sync(0xffffffffu, sum, m);
+    const float t = fmaxf(ref, o);
+    if (t > -INFINITY) sum = sum * bm_scale(ref - t) + os * bm_scale(o - t);
+    ref = t;
   }
   if (lane == 0) {
-    sm.top[warp] = top;
+    sm.ref[warp] = ref;
     sm.sum[warp] = sum;
   }
   __syncthreads();
   if (tid == 0) {
-    for (int i = 1; i < kBmThreads / 32; ++i) {
-      const float o = sm.top[i], t = fmaxf(top, o);
-      if (t > -INFINITY) sum = sum * bm_exp(top, t) + sm.sum[i] * bm_exp(o, t);
-      top = t;
-    }
-    stats[static_cast<size_t>(row) * slices + blockIdx.x] = {top, sum};
+    for (int i = 1; i < kBmThreads / 32; ++i) ref = fmaxf(ref, sm.ref[i]);
+    double total = 0.0;
+    if (ref > -INFINITY)
+      for (int i = 0; i < kBmThreads / 32; ++i) total += sm.sum[i] * bm_scale(sm.ref[i] - ref);
+    stats[static_cast<size_t>(row) * slices + blockIdx.x] = {ref, static_cast<float>(total)};
   }
 }
 
@@ -373,6 +379,7 @@ struct MergeSmem {
   unsigned long long gs[kBmGroups];
   uint32_t gat[kBmGroups];
   double lse[kBmMaxW], score[kBmMaxW];
+  bool huge[kBmMaxW];                  // the sum counts values cut at +-2^28
   unsigned long long bound_s;
   uint32_t bound_at;
   int count;
@@ -428,25 +435,22 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
     const float s = scores[row];
     const bool live = s > -INFINITY;
     const bool ended = finished && finished[row];
-    double top = -INFINITY, sum = 0.0;
+    float ref = -INFINITY;
+    double sum = 0.0;
     if (live && !ended) {
-      for (int i = lane; i < slices; i += 32) {
-        const BeamScan b = stats[static_cast<size_t>(row) * slices + i];
-        const double t = fmax(top, b.top);
-        if (t > -INFINITY) sum = sum * exp(top - t) + b.sum * exp(b.top - t);
-        top = t;
-      }
+      const BeamScan* st = stats + static_cast<size_t>(row) * slices;
+      for (int i = lane; i < slices; i += 32) ref = fmaxf(ref, st[i].ref);
 #pragma unroll
-      for (int m = 16; m >= 1; m >>= 1) {
-        const double o = __shfl_xor_sync(0xffffffffu, top, m), os = __shfl_xor_sync(0xffffffffu, sum, m);
-        const double t = fmax(top, o);
-        if (t > -INFINITY) sum = sum * exp(top - t) + os * exp(o - t);
-        top = t;
-      }
+      for (int m = 16; m >= 1; m >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, m));
+      if (ref > -INFINITY)
+        for (int i = lane; i < slices; i += 32) sum += st[i].sum * bm_scale(st[i].ref - ref);
+#pragma unroll
+      for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
     }
     if (lane == 0) {
       sm.score[w] = live ? static_cast<double>(s) : -INFINITY;
-      sm.lse[w] = ended ? 0.0 : top + log(sum);        // all masked: -infinity + -infinity
+      sm.lse[w] = ended ? 0.0 : ref * kBmLn2 + log(sum);   // all masked: no candidates either
+      sm.huge[w] = fabsf(ref) >= kBmHuge;
     }
   }
   __syncthreads();
@@ -463,8 +467,9 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
     const unsigned long long key = keys[static_cast<size_t>(n) * total + i];
     if (key == 0) return {0, 0};
     const uint32_t v = 0xFFFFFFFFu - static_cast<uint32_t>(key);
-    const double x = unordered(static_cast<uint32_t>(key >> 32));
-    return {ordered(s + (x - sm.lse[w])), ~(static_cast<uint32_t>(w) * V + v)};
+    float x = unordered(static_cast<uint32_t>(key >> 32));
+    if (sm.huge[w]) x = fminf(fmaxf(x, -kBmHuge), kBmHuge);
+    return {ordered(s + (static_cast<double>(x) - sm.lse[w])), ~(static_cast<uint32_t>(w) * V + v)};
   };
   Cand top = {0, 0};
   for (int i = tid; i < total; i += kBmMergeThreads) {
@@ -546,7 +551,7 @@ struct BeamWorkspace {
 // Slices of a row: enough CTAs for the GPU, tiles of a row shared evenly; no slice under
 // 1024 values, and a prompt's candidates within what the merge takes.
 int beam_slices(long long rows, int W, int V, int K) {
-  const int fill = 8 * device_sm_count();
+  const int fill = 12 * device_sm_count();
   const int tiles = (V + kBmTile - 1) / kBmTile;
   long long want = (fill + rows - 1) / rows;
   if (want >= tiles) {

@@ -92,17 +92,17 @@ __device__ __forceinline__ void umma_tmem_a(uint32_t d, uint32_t a, uint64_t b, 
 namespace {
 
 constexpr int kPlThreads = 1024;
+constexpr int kPlWarps = kPlThreads / 32;
 constexpr int kPlLengths = 32;
+constexpr int kPlRowInts = 9, kPlNodeInts = 8;    // of the dynamic shared memory, per row and node
 // Candidate item lengths in pages
 __constant__ int kPlLength[kPlLengths] = {1,  2,  3,  4,  5,  6,  7,   8,   10,  12,  14,
                                           16, 20, 24, 28, 32, 40, 48,  56,  64,  80,  96,
                                           112, 128, 160, 192, 256, 320, 384, 512, 768, 1024};
-
-struct PlanSmem {
-  int warp_sums[32];
-  int n_live, items, parts;
-  float cost[kPlLengths];
-};
+// Costs in pages of a narrow item, which take what the memory takes for 64 KB
+constexpr float kPlWide = 1.3f;          // a page of a wide item
+constexpr float kPlStart = 1.5f;         // an item's start and end
+constexpr float kPlPart = 1.f / 128.f;   // a query row's part, written and read
 
 // Exclusive scan over the CTA; *total = the sum
 __device__ __forceinline__ int pl_scan(int v, int* warp_sums, int* total) {
@@ -115,45 +115,55 @@ __device__ __forceinline__ int pl_scan(int v, int* warp_sums, int* total) {
   }
   if (lane == 31) warp_sums[wp] = x;
   __syncthreads();
-  if (wp == 0) {
-    int w = warp_sums[lane];
+  int w = warp_sums[lane];                 // every warp sums the warps for itself
+  const int own = w;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, d);
-      if (lane >= d) w += y;
-    }
-    warp_sums[lane] = w;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, w, d);
+    if (lane >= d) w += y;
   }
-  __syncthreads();
-  const int before = wp > 0 ? warp_sums[wp - 1] : 0;
-  *total = warp_sums[31];
-  __syncthreads();
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w - own, wp);
+  __syncthreads();                         // warp_sums may be used again
   return before + x - v;
 }
 
-__device__ __forceinline__ int pl_splits(int pages, int L) { return (pages + L - 1) / L; }
+// ceil(pages / L) with 1 / L at hand: (x + 1/2) / L stays 1 / 2048 away from whole numbers,
+// the product's error (pages, L <= 1024) does not reach that far
+__device__ __forceinline__ int pl_splits(int pages, int L, float inv) {
+  return static_cast<int>((static_cast<float>(pages + L - 1) + 0.5f) * inv);
+}
 
 }  // namespace
 
-// Dynamic shared memory: 10 ints per row.  Nodes: boundary i (between live rows i and
-// i + 1) stands for the run in which it is the first boundary with its value; leaf i.
+// Runs of rows that share: boundary i, between the live rows i and i + 1, stands for the run
+// of which it is the first boundary with the run's least value c_i (the run's rows share the
+// columns below c_i, and only a part of the run's rows any behind).
 __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
     const int32_t* __restrict__ table, const int32_t* __restrict__ lens, int B, int G, int Hkv,
     int max_pages, int sms, SaPlan plan, uint32_t* status) {
   pdl_enter();
   extern __shared__ int smem_i[];
-  __shared__ PlanSmem sm;
+  __shared__ int warp_sums[kPlWarps];
+  __shared__ float cost[kPlLengths];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int* row_of = smem_i;                    // [B] live rows
-  int* len_of = row_of + B;                // [B] their lengths
-  int* common = len_of + B;                // [B] c_i
-  int* parent = common + B;                // [B] boundary of the node above, -1: none
-  int* depth = parent + B;                 // [B] levels above; -1: no node here
-  int* first = depth + B;                  // [B] first live row of the node
-  int* rows = first + B;                   // [B] live rows of the node
-  int* base_n = rows + B;                  // [B] first part, nodes
-  int* base_l = base_n + B;                // [B] first part, leaves
-  int* leaf_up = base_l + B;               // [B] boundary of the node above a leaf, -1: none
+  int* row_of = smem_i;                    // live rows
+  int* len_of = row_of + B;                // their lengths
+  int* common = len_of + B;                // c_i
+  int* rep = common + B;                   // first boundary of the run
+  int* parent = rep + B;                   // boundary of the run above, -1: none
+  int* first = parent + B;                 // first live row of the run
+  int* rows = first + B;                   // its live rows; 0: the boundary stands for no run
+  int* leaf_up = rows + B;                 // boundary of the run above a row alone, -1: none
+  int* depth = leaf_up + B;
+  int* nd_of = depth + B;                  // [2 B] node of boundary i, of live row i; -1: none
+  int* nd_v0 = nd_of + 2 * B;              // nodes: first column,
+  int* nd_pages = nd_v0 + 2 * B;           // columns,
+  int* nd_i0 = nd_pages + 2 * B;           // first live row,
+  int* nd_m = nd_i0 + 2 * B;               // rows,
+  int* nd_tiles = nd_m + 2 * B;            // tiles of up to 256 query rows,
+  int* nd_item = nd_tiles + 2 * B;         // first item
+  int* nd_part = nd_item + 2 * B;          // and first part
 
   // ---- rows with tokens
   int n = 0;
@@ -169,7 +179,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       if (L == 0) plan.n_segs[b] = 0;
     }
     int total;
-    const int at = n + pl_scan(L > 0, sm.warp_sums, &total);
+    const int at = n + pl_scan(L > 0, warp_sums, &total);
     if (L > 0) {
       row_of[at] = b;
       len_of[at] = L;
@@ -178,202 +188,228 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
     n += total;
   }
   __syncthreads();
-  // ---- full pages that neighbours have in common, a warp per pair
-  for (int i = warp; i < n; i += kPlThreads / 32) {
-    int c = 0;
-    if (i + 1 < n) {
+  for (int i = tid; i < n; i += kPlThreads)
+    common[i] = i + 1 < n ? min(len_of[i], len_of[i + 1]) / kBlock : 0;
+  __syncthreads();
+  // ---- full pages that neighbours have in common: a warp per pair and 256 columns, which
+  // lowers the value to the first column that differs
+  {
+    const int chunks = (max_pages + 255) / 256;
+    for (int u = warp; u < (n - 1) * chunks; u += kPlWarps) {
+      const int i = u / chunks, j0 = (u - i * chunks) * 256;
       const int most = min(len_of[i], len_of[i + 1]) / kBlock;
+      if (j0 >= most) continue;
       const int32_t* a = table + static_cast<size_t>(row_of[i]) * max_pages;
       const int32_t* b = table + static_cast<size_t>(row_of[i + 1]) * max_pages;
-      c = most;
-      for (int j0 = 0; j0 < most; j0 += 128) {
-        int x[4], y[4];
+      int x[8], y[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int j = j0 + 32 * k + lane;
-          x[k] = j < most ? __ldg(a + j) : 0;
-          y[k] = j < most ? __ldg(b + j) : 0;
-        }
-        int at = -1;
+      for (int k = 0; k < 8; ++k) {
+        const int j = j0 + 32 * k + lane;
+        x[k] = j < most ? __ldg(a + j) : 0;
+        y[k] = j < most ? __ldg(b + j) : 0;
+      }
+      int at = -1;
 #pragma unroll
-        for (int k = 3; k >= 0; --k) {
-          const uint32_t differ = __ballot_sync(0xffffffffu, x[k] != y[k]);
-          if (differ) at = j0 + 32 * k + __ffs(differ) - 1;
-        }
-        if (at >= 0) {
-          c = at;
+      for (int k = 7; k >= 0; --k) {
+        const uint32_t differ = __ballot_sync(0xffffffffu, x[k] != y[k]);
+        if (differ) at = j0 + 32 * k + __ffs(differ) - 1;
+      }
+      if (at >= 0 && lane == 0) atomicMin(&common[i], at);
+    }
+  }
+  __syncthreads();
+  // ---- runs, a warp per boundary: the nearest boundaries with less on both sides; the
+  // higher of the two values is where the run above ends
+  for (int i = warp; i < n; i += kPlWarps) {
+    const int v = common[i];               // the last row's is 0
+    int l = -1, r = n - 1, rp = i, up = -1;
+    if (v > 0) {
+      for (int j0 = i - 1; j0 >= 0; j0 -= 32) {
+        const int c = j0 - lane >= 0 ? common[j0 - lane] : -1;
+        const uint32_t less = __ballot_sync(0xffffffffu, c < v);
+        const uint32_t run = less ? (less & (0u - less)) - 1u : 0xffffffffu;   // lanes before the first
+        const uint32_t same = __ballot_sync(0xffffffffu, c == v) & run;
+        if (same) rp = j0 - (31 - __clz(same));
+        if (less) {
+          l = j0 - (__ffs(less) - 1);
           break;
         }
       }
-    }
-    if (lane == 0) common[i] = c;
-  }
-  __syncthreads();
-  // ---- runs.  Boundary i, value v: the nearest boundaries below v on both sides bound
-  // the run; the higher of their values is where the node above ends.
-  for (int i = tid; i < n; i += kPlThreads) {
-    const int v = i + 1 < n ? common[i] : 0;
-    int up = -1, rep = i, l = i - 1, r = i + 1;
-    if (v > 0) {
-      while (l >= 0 && common[l] >= v) {
-        if (common[l] == v) rep = l;
-        --l;
+      for (int j0 = i + 1; j0 < n - 1; j0 += 32) {
+        const int c = j0 + lane < n - 1 ? common[j0 + lane] : -1;
+        const uint32_t less = __ballot_sync(0xffffffffu, c < v);
+        if (less) {
+          r = min(j0 + __ffs(less) - 1, n - 1);
+          break;
+        }
       }
-      if (rep == i) {
-        while (r + 1 < n && common[r] >= v) ++r;
-        const int lv = l >= 0 ? common[l] : 0, rv = r + 1 < n ? common[r] : 0;
-        if (lv > 0 || rv > 0) up = lv >= rv ? l : r;
-      }
+      l = max(l, -1);
+      const int lv = l >= 0 ? common[l] : 0, rv = r < n - 1 ? common[r] : 0;
+      if (lv > 0 || rv > 0) up = lv >= rv ? l : r;
     }
-    depth[i] = v > 0 && rep == i ? 0 : -1;
-    parent[i] = up;                         // a boundary of the run above, not yet its first
-    base_n[i] = rep;                        // first boundary of the run (kept here for now)
-    first[i] = l + 1;
-    rows[i] = r - l;
+    if (lane == 0) {
+      rep[i] = rp;
+      parent[i] = up;
+      first[i] = l + 1;
+      rows[i] = v > 0 && rp == i ? r - l : 0;
+    }
   }
   __syncthreads();
   for (int i = tid; i < n; i += kPlThreads) {
-    if (depth[i] == 0 && parent[i] >= 0) parent[i] = base_n[parent[i]];
-    const int lv = i > 0 ? common[i - 1] : 0, rv = i + 1 < n ? common[i] : 0;
-    leaf_up[i] = lv > 0 || rv > 0 ? base_n[lv >= rv ? i - 1 : i] : -1;
+    const int lv = i > 0 ? common[i - 1] : 0, rv = common[i];
+    leaf_up[i] = lv > 0 || rv > 0 ? rep[lv >= rv ? i - 1 : i] : -1;
+    int p = parent[i];
+    if (p >= 0) p = rep[p];
+    parent[i] = p;
   }
   __syncthreads();
-  for (int i = tid; i < n; i += kPlThreads)
-    if (depth[i] >= 0) {
-      int d = 0;
+  for (int i = tid; i < n; i += kPlThreads) {
+    int d = 0;
+    if (rows[i] > 0)
       for (int p = parent[i]; p >= 0; p = parent[p]) ++d;
-      base_l[i] = d;
-    }
-  __syncthreads();
-  for (int i = tid; i < n; i += kPlThreads) {
-    if (depth[i] >= 0) depth[i] = base_l[i] < kSaLevels ? base_l[i] : -1;   // deeper runs: not shared
+    depth[i] = d;
   }
   __syncthreads();
-  for (int i = tid; i < n; i += kPlThreads) {
-    int p = leaf_up[i];
-    while (p >= 0 && depth[p] < 0) p = parent[p];
-    leaf_up[i] = p;
-  }
-  __syncthreads();
-  // Node k < n: boundary k; n <= k < 2n: leaf k - n.  v0 .. v1 - 1, m rows from i0.
-  const int tile_rows = 128 / G;            // token rows of a tile
-  auto node = [&](int k, int& v0, int& pages, int& i0, int& m) -> bool {
-    if (k < n) {
-      if (depth[k] < 0) return false;
-      v0 = parent[k] >= 0 ? common[parent[k]] : 0;
-      pages = common[k] - v0;
-      i0 = first[k];
-      m = rows[k];
-      return true;
+  // ---- nodes: the runs of the first levels (deeper ones are not shared), then the rows
+  // alone with the columns that are left
+  const int tile_rows = 128 / G;           // token rows of a tile
+  int nodes = 0;
+  for (int half = 0; half < 2; ++half)
+    for (int k0 = 0; k0 < n; k0 += kPlThreads) {
+      const int k = k0 + tid;
+      int v0 = 0, pages = 0, i0 = k, m = 1;
+      if (k < n) {
+        if (half == 0) {
+          if (rows[k] > 0 && depth[k] < kSaLevels) {
+            v0 = parent[k] >= 0 ? common[parent[k]] : 0;
+            pages = common[k] - v0;
+            i0 = first[k];
+            m = rows[k];
+          }
+        } else {
+          int p = leaf_up[k];
+          while (p >= 0 && depth[p] >= kSaLevels) p = parent[p];
+          leaf_up[k] = p;
+          v0 = p >= 0 ? common[p] : 0;
+          pages = (len_of[k] + kBlock - 1) / kBlock - v0;
+        }
+      }
+      int total;
+      const int at = nodes + pl_scan(pages > 0, warp_sums, &total);
+      if (k < n) nd_of[half * B + k] = pages > 0 ? at : -1;
+      if (pages > 0) {
+        nd_v0[at] = v0;
+        nd_pages[at] = pages;
+        nd_i0[at] = i0;
+        nd_m[at] = m;
+        nd_tiles[at] = (m + 2 * tile_rows - 1) / (2 * tile_rows);
+      }
+      nodes += total;
     }
-    k -= n;
-    v0 = leaf_up[k] >= 0 ? common[leaf_up[k]] : 0;
-    pages = (len_of[k] + kBlock - 1) / kBlock - v0;
-    i0 = k;
-    m = 1;
-    return pages > 0;
-  };
-  auto tiles_of = [&](int m) { return (m + 2 * tile_rows - 1) / (2 * tile_rows); };
-  // ---- item length: a warp weighs a candidate.  An item costs its pages, one for its
-  // start and end, and its parts' traffic; the CTAs' share of all that, or the rounds
-  // that the long items take, whichever is more.
-  for (int q = warp; q < kPlLengths; q += kPlThreads / 32) {
-    const int L = kPlLength[q];
+  __syncthreads();
+  // ---- item length: a warp weighs a candidate.  The CTAs' share of all items' costs, and
+  // half an item that others wait for at the end.
+  for (int c = warp; c < kPlLengths; c += kPlWarps) {
+    const int L = kPlLength[c];
+    const float inv = 1.f / static_cast<float>(L);
     float sum = 0.f, longest = 0.f;
-    int items = 0, big = 0;
+    int items = 0;
     long long parts = 0;
-    for (int k = lane; k < 2 * n; k += 32) {
-      int v0, pages, i0, m;
-      if (!node(k, v0, pages, i0, m)) continue;
-      const int ns = pl_splits(pages, L), tiles = tiles_of(m), each = tiles * ns * Hkv;
-      const float per = static_cast<float>(pages) / ns + 1.f +
-                        static_cast<float>(min(m, 2 * tile_rows) * G) * (1.f / 128.f);
-      sum += per * each;
-      longest = fmaxf(longest, per);
+    for (int k = lane; k < nodes; k += 32) {
+      const int pages = nd_pages[k], m = nd_m[k], ns = pl_splits(pages, L, inv);
+      const int each = nd_tiles[k] * ns * Hkv;
+      const int nr = min(m, 2 * tile_rows);
+      const float page = nr > tile_rows ? kPlWide : 1.f;
+      const float fix = kPlStart + static_cast<float>(nr * G) * kPlPart;
+      sum += static_cast<float>(nd_tiles[k] * Hkv) * (page * pages + fix * ns);
+      longest = fmaxf(longest, page * min(L, pages) + fix);
       items += each;
       parts += static_cast<long long>(m) * G * ns * Hkv;
-      if (2 * ((pages + ns - 1) / ns) > min(L, max_pages)) big += each;
     }
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) {
       sum += __shfl_xor_sync(0xffffffffu, sum, d);
       longest = fmaxf(longest, __shfl_xor_sync(0xffffffffu, longest, d));
       items += __shfl_xor_sync(0xffffffffu, items, d);
-      big += __shfl_xor_sync(0xffffffffu, big, d);
       parts += __shfl_xor_sync(0xffffffffu, parts, d);
     }
-    if (lane == 0) {
-      const bool fits = items <= plan.max_items && parts <= plan.max_parts;
-      const float rounds = static_cast<float>((max(big, 1) + sms - 1) / sms) * longest;
-      sm.cost[q] = fits ? fmaxf(sum / sms, rounds) : INFINITY;
-    }
+    // all in one round: the longest item is what counts
+    const float time = items <= sms ? longest : sum / sms + 0.5f * longest;
+    if (lane == 0)
+      cost[c] = items <= plan.max_items && parts <= plan.max_parts ? time : INFINITY;
   }
   __syncthreads();
-  int L = kPlLength[kPlLengths - 1];
+  int best = lane;
   {
-    float least = sm.cost[kPlLengths - 1];
-    for (int q = kPlLengths - 2; q >= 0; --q)
-      if (sm.cost[q] < least) {
-        least = sm.cost[q];
-        L = kPlLength[q];
+    float t = cost[lane];
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+      const float ot = __shfl_xor_sync(0xffffffffu, t, d);
+      const int ob = __shfl_xor_sync(0xffffffffu, best, d);
+      if (ot < t || (ot == t && ob > best)) {
+        t = ot;
+        best = ob;
       }
+    }
   }
-  // ---- first item and part of every node, shared nodes first
-  int at_item = 0, at_part = 0;
-  for (int k0 = 0; k0 < 2 * n; k0 += kPlThreads) {
+  const int L = kPlLength[best];
+  const float inv = 1.f / static_cast<float>(L);
+  // ---- first item and part of every node
+  int n_items = 0, n_parts = 0;
+  for (int k0 = 0; k0 < nodes; k0 += kPlThreads) {
     const int k = k0 + tid;
-    int v0 = 0, pages = 0, i0 = 0, m = 0, items = 0, parts = 0;
-    const bool here = k < 2 * n && node(k, v0, pages, i0, m);
-    int ns = 0;
-    if (here) {
-      ns = pl_splits(pages, L);
-      items = tiles_of(m) * ns * Hkv;
-      parts = m * G * ns * Hkv;
+    int items = 0, parts = 0;
+    if (k < nodes) {
+      const int ns = pl_splits(nd_pages[k], L, inv);
+      items = nd_tiles[k] * ns * Hkv;
+      parts = nd_m[k] * G * ns * Hkv;
     }
     int total_i, total_p;
-    const int it = at_item + pl_scan(items, sm.warp_sums, &total_i);
-    const int pt = at_part + pl_scan(parts, sm.warp_sums, &total_p);
-    at_item += total_i;
-    at_part += total_p;
-    if (k < n) base_n[k] = pt;
-    else if (k < 2 * n) base_l[k - n] = pt;
-    // this node's items, by its warp: nodes of the warp one after another
-    for (uint32_t todo = __ballot_sync(0xffffffffu, here); todo; todo &= todo - 1) {
-      const int src = __ffs(todo) - 1;
-      const int w_it = __shfl_sync(0xffffffffu, it, src), w_pt = __shfl_sync(0xffffffffu, pt, src);
-      const int w_v0 = __shfl_sync(0xffffffffu, v0, src), w_pages = __shfl_sync(0xffffffffu, pages, src);
-      const int w_i0 = __shfl_sync(0xffffffffu, i0, src), w_m = __shfl_sync(0xffffffffu, m, src);
-      const int w_ns = __shfl_sync(0xffffffffu, ns, src), count = __shfl_sync(0xffffffffu, items, src);
-      for (int e = lane; e < count; e += 32) {
-        const int tile = e % tiles_of(w_m), rest = e / tiles_of(w_m);
-        const int g = rest % Hkv, s = rest / Hkv;
-        SaItem item;
-        item.ro = tile * 2 * tile_rows;
-        item.i0 = w_i0 + item.ro;
-        item.nr = min(2 * tile_rows, w_m - item.ro);
-        item.c0 = w_v0 + static_cast<int>(static_cast<long long>(w_pages) * s / w_ns);
-        item.c1 = w_v0 + static_cast<int>(static_cast<long long>(w_pages) * (s + 1) / w_ns);
-        item.g = g;
-        item.m = w_m;
-        item.base = w_pt + (s * Hkv + g) * w_m * G;
-        if (w_it + e < plan.max_items) plan.items[w_it + e] = item;
-      }
+    const int it = n_items + pl_scan(items, warp_sums, &total_i);
+    const int pt = n_parts + pl_scan(parts, warp_sums, &total_p);
+    if (k < nodes) {
+      nd_item[k] = it;
+      nd_part[k] = pt;
     }
+    n_items += total_i;
+    n_parts += total_p;
   }
+  n_items = min(n_items, plan.max_items);
   if (tid == 0) {
-    plan.counts[0] = min(at_item, plan.max_items);
+    plan.counts[0] = n_items;
     plan.counts[1] = 0;
   }
   __syncthreads();
-  // ---- every row's parts: its leaf, then the nodes above
+  // ---- items, a thread each; those of a node's tiles over the same pages side by side
+  for (int e = tid; e < n_items; e += kPlThreads) {
+    int lo = 0, hi = nodes;
+    while (hi - lo > 1) {                  // last node whose first item is not behind e
+      const int mid = (lo + hi) >> 1;
+      if (nd_item[mid] <= e) lo = mid; else hi = mid;
+    }
+    const int pages = nd_pages[lo], m = nd_m[lo], tiles = nd_tiles[lo], ns = pl_splits(pages, L, inv);
+    const int rest = (e - nd_item[lo]) / tiles, tile = e - nd_item[lo] - rest * tiles;
+    const int s = rest / Hkv, g = rest - s * Hkv;
+    SaItem item;
+    item.ro = tile * 2 * tile_rows;
+    item.i0 = nd_i0[lo] + item.ro;
+    item.nr = min(2 * tile_rows, m - item.ro);
+    item.c0 = nd_v0[lo] + pages * s / ns;
+    item.c1 = nd_v0[lo] + pages * (s + 1) / ns;
+    item.g = g;
+    item.m = m;
+    item.base = nd_part[lo] + (s * Hkv + g) * m * G;
+    plan.items[e] = item;
+  }
+  // ---- every row's parts: its own node, then the runs above
   for (int i = tid; i < n; i += kPlThreads) {
     SaSeg* out = plan.segs + static_cast<size_t>(row_of[i]) * kSaMaxSegs;
     int k = 0;
-    for (int p = n + i; p >= 0; p = p >= n ? leaf_up[i] : parent[p]) {
-      int v0, pages, i0, m;
-      if (!node(p, v0, pages, i0, m)) continue;
-      out[k++] = {p < n ? base_n[p] : base_l[p - n], m, i - i0, pl_splits(pages, L)};
-    }
+    auto add = [&](int nd) {
+      out[k++] = {nd_part[nd], nd_m[nd], i - nd_i0[nd], pl_splits(nd_pages[nd], L, inv)};
+    };
+    if (nd_of[B + i] >= 0) add(nd_of[B + i]);
+    for (int p = leaf_up[i]; p >= 0; p = parent[p]) add(nd_of[p]);
     plan.n_segs[row_of[i]] = k;
   }
 }
@@ -882,18 +918,37 @@ __global__ void __launch_bounds__(512) shared_combine_kernel(const SaPlan plan, 
   for (int k = 0; k < ns; ++k) {
     const SaSeg sg = plan.segs[static_cast<size_t>(b) * kSaMaxSegs + k];
     const size_t rows = static_cast<size_t>(sg.m) * G, at = static_cast<size_t>(sg.ro) * G + h;
-    for (int s = 0; s < sg.splits; ++s) {
-      const size_t base = sg.base + (static_cast<size_t>(s) * Hkv + g) * rows;
-      const float2 ml = plan.part_ml[base + at];
-      const float4 x = plan.part_o[base * 32 + d4 * rows + at];
-      if (ml.x == -INFINITY) continue;
-      const float top = fmaxf(M, ml.x), f = sa_ex2(M - top), e = sa_ex2(ml.x - top);
-      acc.x = fmaf(acc.x, f, x.x * e);
-      acc.y = fmaf(acc.y, f, x.y * e);
-      acc.z = fmaf(acc.z, f, x.z * e);
-      acc.w = fmaf(acc.w, f, x.w * e);
-      l = fmaf(l, f, ml.y * e);
+    constexpr int kDeep = 8;               // parts whose loads are in flight together
+    for (int s0 = 0; s0 < sg.splits; s0 += kDeep) {
+      float2 ml[kDeep];
+      float4 x[kDeep];
+#pragma unroll
+      for (int s = 0; s < kDeep; ++s) {
+        ml[s] = make_float2(-INFINITY, 0.f);
+        if (s0 + s < sg.splits) {
+          const size_t base = sg.base + (static_cast<size_t>(s0 + s) * Hkv + g) * rows;
+          ml[s] = plan.part_ml[base + at];
+          x[s] = plan.part_o[base * 32 + d4 * rows + at];
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int s = 0; s < kDeep; ++s) top = fmaxf(top, ml[s].x);
+      if (top == -INFINITY) continue;
+      const float f = sa_ex2(M - top);
+      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+      l *= f;
       M = top;
+#pragma unroll
+      for (int s = 0; s < kDeep; ++s) {
+        if (ml[s].x == -INFINITY) continue;
+        const float e = sa_ex2(ml[s].x - top);
+        acc.x = fmaf(x[s].x, e, acc.x);
+        acc.y = fmaf(x[s].y, e, acc.y);
+        acc.z = fmaf(x[s].z, e, acc.z);
+        acc.w = fmaf(x[s].w, e, acc.w);
+        l = fmaf(ml[s].y, e, l);
+      }
     }
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -986,8 +1041,9 @@ msa_status_t msa_decode_shared(const void* q, const void* k_cache, const void* v
   uint32_t* sw = nullptr;
   MSA_TRY(status_word(&sw));
   MSA_TRY(ensure_smem(shared_attn_kernel, sizeof(SaSmem), "shared_attn_kernel"));
-  const size_t plan_smem = static_cast<size_t>(B) * 10 * sizeof(int);
-  MSA_TRY(ensure_smem(shared_plan_kernel, static_cast<size_t>(kSaMaxRows) * 10 * sizeof(int), "shared_plan_kernel"));
+  constexpr size_t kPlanRow = (kPlRowInts + 2 * kPlNodeInts) * sizeof(int);
+  const size_t plan_smem = B * kPlanRow;
+  MSA_TRY(ensure_smem(shared_plan_kernel, kSaMaxRows * kPlanRow, "shared_plan_kernel"));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   {
     TraceScope trace_("shared_plan_kernel", st);
