@@ -16,12 +16,12 @@
 //
 // Attention of an item: tiles of 128 query rows (token rows x the G heads of a KV head),
 // two streams of tensor-core work per CTA:
-//   wide    two tiles over the same pages; stream s has tile s, S = Q_s K^T (128 x 128)
+//   wide    two tiles over the same pages; stream s has tile s and all keys
 //   narrow  one tile (a leaf's G rows, or up to 128 shared ones); stream s has the keys
-//           64 s .. 64 s + 63 of every page, S double-buffered; the halves' results are
-//           merged at the end
+//           64 s .. 64 s + 63 of every page; the halves' results are merged at the end
 // so that a page in shared memory serves up to 256 query rows and either stream's softmax
-// runs while the other's products do.  Roles: warp 0 claims items and streams K and V pages
+// runs while the other's products do.  A stream takes 64 keys at a time, S (128 x 64) in two
+// buffers, so that the next block's products are there when a softmax ends.  Roles: warp 0 claims items and streams K and V pages
 // through a ring of 32 KB stages by TMA; warps 1 and 2 issue a stream's MMAs (P, in bf16, is
 // read from TMEM as the A operand); warp 3 gathers q; warps 4-7 and 8-11 are the streams'
 // softmax (a thread per query row).  P is rounded to bf16 (2^-9 each, beside o's own
@@ -41,8 +41,7 @@ constexpr int kSaStages = 5;
 constexpr int kSaTile = 128 * 128 * 2;     // bytes of a 128 x 128 bf16 tile
 constexpr int kSaHalf = kSaTile / 2;       // one 64-channel half
 constexpr int kSaQWarp = 3;
-constexpr uint32_t kSaIdescWide = idesc_bf16(128, 128, false, false);    // S = Q K^T
-constexpr uint32_t kSaIdescNarrow = idesc_bf16(128, 64, false, false);   // 64 keys
+constexpr uint32_t kSaIdescS = idesc_bf16(128, 64, false, false);        // S = Q K^T, 64 keys
 constexpr uint32_t kSaIdescPV = idesc_bf16(128, 128, false, true);       // O += P V
 constexpr float kSaLog2e = 1.4426950408889634f;
 constexpr float kSaRescale = 8.0f;         // log2 of the largest P before o is rescaled
@@ -53,6 +52,7 @@ constexpr uint32_t kSaColO = 256;          // S of stream s at 128 s, O at 256 +
 struct SaItem {
   int i0, nr, c0, c1;
   int g, m, ro, base;
+  int row, len, pad[2];   // the first of the rows, and its tokens
 };
 
 // Parts of a row in one node: splits of (m G) query rows each, `ro` the row in the node
@@ -63,7 +63,7 @@ struct SaSeg {
 struct SaPlan {
   int* live;          // [B] rows with tokens, in order
   SaItem* items;
-  int* counts;        // [0] items, [1] next to claim
+  int* counts;        // [0] items, [1] next to claim (behind the CTAs' first ones)
   SaSeg* segs;        // [B][kSaMaxSegs]
   int* n_segs;        // [B], 0 for rows without tokens
   float4* part_o;     // [blocks][32][m G]
@@ -76,6 +76,12 @@ __device__ __forceinline__ float sa_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// 16 bytes global -> shared, asynchronously
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void umma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   n_items = min(n_items, plan.max_items);
   if (tid == 0) {
     plan.counts[0] = n_items;
-    plan.counts[1] = 0;
+    plan.counts[1] = sms;                  // every CTA begins with the item of its own number
   }
   __syncthreads();
   // ---- items, a thread each; those of a node's tiles over the same pages side by side
@@ -399,6 +405,8 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
     item.g = g;
     item.m = m;
     item.base = nd_part[lo] + (s * Hkv + g) * m * G;
+    item.row = row_of[item.i0];
+    item.len = len_of[item.i0];
     plan.items[e] = item;
   }
   // ---- every row's parts: its own node, then the runs above
@@ -479,8 +487,7 @@ __device__ __forceinline__ void sa_load64(uint32_t addr, uint32_t (&sv)[64]) {
 
 __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-    const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ table,
-    const int32_t* __restrict__ lens, int G, int Hkv, int num_pages, int max_pages, float sl2,
+    const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ table, int G, int Hkv, int num_pages, int max_pages, float sl2,
     const SaPlan plan, uint32_t* status) {
   pdl_enter();
   const int n_items = plan.counts[0];
@@ -531,10 +538,12 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
     }
     uint32_t pos = 0, qt = 0, tc = 0;
     bool alive = true;
+    int id = blockIdx.x;
     while (alive) {
-      int id = 0;
-      if (lane == 0) id = atomicAdd(plan.counts + 1, 1);
-      id = __shfl_sync(0xffffffffu, id, 0);
+      if (tc > 0) {
+        if (lane == 0) id = atomicAdd(plan.counts + 1, 1);
+        id = __shfl_sync(0xffffffffu, id, 0);
+      }
       const int tb = tc & 1;
       if (lane == 0) alive = mbar_wait(&sm.slot_empty[tb], ((tc >> 1) & 1) ^ 1, status, 100);
       alive = __shfl_sync(0xffffffffu, alive ? 1 : 0, 0) != 0;
@@ -547,8 +556,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
         break;
       }
       const SaItem it = plan.items[id];
-      const int row = plan.live[it.i0];
-      const int32_t* trow = table + static_cast<size_t>(row) * max_pages;
+      const int32_t* trow = table + static_cast<size_t>(it.row) * max_pages;
       // pages that are none have no keys; the others are counted first
       int valid = 0;
       bool last_ok = true;
@@ -569,7 +577,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
         s.ro = it.ro;
         s.base = it.base;
         s.pages = valid;
-        s.tail = last_ok ? min(kBlock, lens[row] - (it.c1 - 1) * kBlock) : kBlock;
+        s.tail = last_ok ? min(kBlock, it.len - (it.c1 - 1) * kBlock) : kBlock;
         s.wide = it.nr > tile_rows;
         s.ring = pos;
         s.qt = qt;
@@ -625,48 +633,48 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
         const uint32_t qi = t.qt + (t.wide ? s : 0);
         const int qb = qi & 1;
         if (!(ok = mbar_wait(&sm.q_full[qb], (qi >> 1) & 1, status, 112))) break;
-        if (!(ok = pv_wait(0) && pv_wait(1))) break;
         tc_fence_after();
         const uint32_t qa = smem_u32(sm.q[qb]);
         const uint32_t d_s = tmem + 128 * s, d_o = tmem + kSaColO + 128 * s;
-        auto scores = [&](int i) -> bool {
-          const uint32_t p = t.ring + 2 * i, st = p % kSaStages;
-          const int b = t.wide ? 0 : (i & 1);
+        // block j: 64 keys of page j (narrow) or half of page j / 2 (wide), in S buffer j & 1
+        const int blocks = t.wide ? 2 * t.pages : t.pages;
+        auto scores = [&](int j) -> bool {
+          const uint32_t p = t.ring + 2 * (t.wide ? j >> 1 : j), st = p % kSaStages;
+          const int b = j & 1, half = t.wide ? b : s;
           if (!mbar_wait(&sm.full[st], (p / kSaStages) & 1, status, 113) || !pv_wait(b)) return false;
           tc_fence_after();
-          const uint32_t ka = smem_u32(sm.ring[st]) + (t.wide ? 0 : s * 64 * 128);
-          const uint32_t d = d_s + 64 * b, idesc = t.wide ? kSaIdescWide : kSaIdescNarrow;
+          const uint32_t ka = smem_u32(sm.ring[st]) + half * 64 * 128;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t off = (kk >> 2) * kSaHalf + (kk & 3) * 32;
-            umma_bf16(d, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), idesc, kk > 0);
+            umma_bf16(d_s + 64 * b, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024),
+                      kSaIdescS, kk > 0);
           }
           umma_commit(&sm.s_full[s][b]);
-          umma_commit(&sm.empty[st]);
+          if (!t.wide || b == 1) umma_commit(&sm.empty[st]);
           ++uses[b];
           return true;
         };
-        if (t.pages > 0) ok = scores(0);
-        for (int i = 0; ok && i < t.pages; ++i) {
-          if (!t.wide && i + 1 < t.pages && !(ok = scores(i + 1))) break;
-          const int b = t.wide ? 0 : (i & 1);
-          const uint32_t p = t.ring + 2 * i + 1, st = p % kSaStages;
-          // uses of b so far, without the score of page i + 2
+        if (blocks > 0) ok = scores(0);
+        for (int j = 0; ok && j < blocks; ++j) {
+          if (j + 1 < blocks && !(ok = scores(j + 1))) break;
+          const int b = j & 1, half = t.wide ? b : s;
+          const uint32_t p = t.ring + 2 * (t.wide ? j >> 1 : j) + 1, st = p % kSaStages;
+          // uses of b so far: block j's (block j + 2 has not been issued)
           if (!(ok = mbar_wait(&sm.p_full[s][b], (uses[b] - 1) & 1, status, 114))) break;
           if (!(ok = mbar_wait(&sm.full[st], (p / kSaStages) & 1, status, 115))) break;
           // the item's first PV overwrites O: the item before must have been read
-          if (i == 0 && items_with_o > 0 &&
+          if (j == 0 && items_with_o > 0 &&
               !(ok = mbar_wait(&sm.o_free, (items_with_o - 1) & 1, status, 116)))
             break;
           tc_fence_after();
-          const uint32_t va = smem_u32(sm.ring[st]) + (t.wide ? 0 : s * 64 * 128);
-          const int steps = t.wide ? 8 : 4;
-          for (int kk = 0; kk < steps; ++kk)
+          const uint32_t va = smem_u32(sm.ring[st]) + half * 64 * 128;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
             umma_tmem_a(d_o, d_s + 64 * b + 8 * kk, sdesc_sw128(va + kk * 2048, kSaHalf, 1024), kSaIdescPV,
-                        i > 0 || kk > 0);
+                        j > 0 || kk > 0);
           umma_commit(&sm.pv_done[s][b]);
-          umma_commit(&sm.empty[st]);
-          if (t.wide && i + 1 < t.pages && !(ok = scores(i + 1))) break;
+          if (!t.wide || b == 1) umma_commit(&sm.empty[st]);
         }
         if (!ok) break;
         ++items_with_o;
@@ -689,26 +697,29 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
         const uint32_t qi = t.qt + w;
         const int qb = qi & 1;
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_empty[qb], ((qi >> 1) & 1) ^ 1, status, 121)))) break;
+        // rows of the tile, 16 lanes each; all copies are in flight together, so that a tile takes
+        // two latencies (which rows, then q)
         const int r0 = w * tile_rows, nr = min(tile_rows, t.nr - r0) * G;
-        const int c = lane & 15;
+        uint32_t from[4];                                // this lane's rows 32 k + lane, as rows of q
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = 32 * k + lane, tok = r / G;
+          from[k] = r < nr ? plan.live[t.i0 + r0 + tok] * Hq + t.g * G + (r - tok * G) : 0;
+        }
+        const int c = lane & 15, up = lane >> 4;
         uint8_t* dst = sm.q[qb] + (c >> 3) * kSaHalf;
-        for (int r = lane >> 4; r < nr; r += 16) {
-          uint4 v[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int rr = r + 2 * k;
-            if (rr < nr) {
-              const int tok = rr / G, h = rr - tok * G;
-              const int b = plan.live[t.i0 + r0 + tok];
-              v[k] = *reinterpret_cast<const uint4*>(q + (static_cast<size_t>(b) * Hq + t.g * G + h) * kD + 8 * c);
-            }
-          }
+        for (int k = 0; k < 4; ++k) {
+          if (32 * k >= nr) break;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int rr = r + 2 * k;
-            if (rr < nr) *reinterpret_cast<uint4*>(dst + sw128_offset(rr, c & 7)) = v[k];
+          for (int j = 0; j < 16; ++j) {
+            const int r = 32 * k + 2 * j + up;
+            const uint32_t f = __shfl_sync(0xffffffffu, from[k], 2 * j + up);
+            if (r < nr)
+              cp_async16(dst + sw128_offset(r, c & 7), q + static_cast<size_t>(f) * kD + 8 * c);
           }
         }
+        cp_async_wait_all();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_full[qb]);
@@ -734,50 +745,38 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
       const int nq = min(tile_rows, t.nr - r0) * G;      // its query rows
       const bool work = subp * 32 < nq;                  // the warp has any
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; ok && i < t.pages; ++i) {
-        const int b = t.wide ? 0 : (i & 1);
+      const int blocks = t.wide ? 2 * t.pages : t.pages;
+      for (int j = 0; ok && j < blocks; ++j) {
+        const int b = j & 1;
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[s][b], uses[b] & 1, status, 131)))) break;
         tc_fence_after();
-        const bool last = i + 1 == t.pages;
-        const int keys = last ? t.tail : kBlock;
-        // keys of this stream's half of the page (a wide item has full pages only)
-        const int lim = t.wide ? 64 : min(64, keys - 64 * s);
+        // keys of the block: a page that is not full is a leaf's last (narrow)
+        const bool cut = j + 1 == blocks && t.tail < kBlock;
+        const int lim = cut ? min(64, t.tail - 64 * s) : 64;
         const uint32_t sbuf = d_s + 64 * b;
         if (work) {
-          uint32_t sv[64], pk[64];
-          float mx = -INFINITY;
-          if (t.wide) {
-            sa_load64(sbuf, sv);
-            mx = sa_max64(sv);
-          }
-          // wide: the second 64 keys are exponentiated first, then the first 64 again
-          sa_load64(t.wide ? sbuf + 64 : sbuf, sv);
+          uint32_t sv[64], pk[32];
+          sa_load64(sbuf, sv);
           if (lim < 64) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j) sv[j] = j < lim ? sv[j] : 0xFF800000u;
+            for (int k = 0; k < 64; ++k) sv[k] = k < lim ? sv[k] : 0xFF800000u;
           }
-          mx = fmaxf(mx, sa_max64(sv));
           const bool any = lim > 0;
-          const float mnew = any ? fmaxf(m, mx * sl2) : m;
+          const float mnew = any ? fmaxf(m, sa_max64(sv) * sl2) : m;
           const bool resc = mnew > m + kSaRescale;
           const float mu = resc ? mnew : m;
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                            make_float2(0.f, 0.f)};
           if (any) {
-            sa_exp64(sv, sl2, mu, pk + 32, acc);
+            sa_exp64(sv, sl2, mu, pk, acc);
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) pk[32 + j] = 0u;
-          }
-          if (t.wide) {
-            sa_load64(sbuf, sv);
-            sa_exp64(sv, sl2, mu, pk, acc);
+            for (int k = 0; k < 32; ++k) pk[k] = 0u;
           }
           const bool need = resc && m != -INFINITY;
           if (__any_sync(0xffffffffu, need)) {
-            // O stands still once the PV of the page before is done
-            const int pb = t.wide ? 0 : ((i - 1) & 1);
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[s][pb], (uses[pb] - 1) & 1, status, 132)))) break;
+            // O stands still once the PV of the block before is done
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[s][b ^ 1], (uses[b ^ 1] - 1) & 1, status, 132)))) break;
             tc_fence_after();
             const float alpha = need ? sa_ex2(m - mu) : 1.f;
 #pragma unroll 1
@@ -786,7 +785,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
               tmem_ld32(d_o + c * 32, v);
               tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
+              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
               tmem_st16(d_o + c * 32, v);
               tmem_st16(d_o + c * 32 + 16, v + 16);
             }
@@ -797,27 +796,20 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
             l = m == -INFINITY ? rs : (resc ? l * sa_ex2(m - mu) : l) + rs;
             m = mu;
           }
-          if (t.wide) {
-            tmem_st16(sbuf, pk);
-            tmem_st16(sbuf + 16, pk + 16);
-            tmem_st16(sbuf + 32, pk + 32);
-            tmem_st16(sbuf + 48, pk + 48);
-          } else {
-            tmem_st16(sbuf, pk + 32);
-            tmem_st16(sbuf + 16, pk + 48);
-          }
+          tmem_st16(sbuf, pk);
+          tmem_st16(sbuf + 16, pk + 16);
           tmem_st_wait();
         }
-        if (last && t.tail < kBlock) {
+        if (cut) {
           // what lies behind the row's end may be anything, and 0 times it has to be 0
-          const uint32_t p = t.ring + 2 * i + 1, st = p % kSaStages;
+          // (either stream clears what it multiplies)
+          const uint32_t p = t.ring + 2 * j + 1, st = p % kSaStages;
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[st], (p / kSaStages) & 1, status, 133)))) break;
-          // (only a leaf has such a page: either stream clears the 64 keys that it multiplies)
           const int key = 64 * s + (r >> 1);
           if (key >= t.tail) {
             uint4* v = reinterpret_cast<uint4*>(sm.ring[st] + (r & 1) * kSaHalf + key * 128);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = make_uint4(0u, 0u, 0u, 0u);
+            for (int k = 0; k < 8; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
         }
@@ -833,7 +825,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
       float4* po = plan.part_o + static_cast<size_t>(t.base) * 32 + at;
       const bool mine = r < nq;
       if (t.pages > 0) {
-        const int b = t.wide ? 0 : ((t.pages - 1) & 1);
+        const int b = (blocks - 1) & 1;
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[s][b], (uses[b] - 1) & 1, status, 134)))) break;
       }
       float f0 = 1.f, f1 = 0.f;
@@ -1054,7 +1046,7 @@ msa_status_t msa_decode_shared(const void* q, const void* k_cache, const void* v
   {
     TraceScope trace_("shared_attn_kernel", st);
     launch_pdl(shared_attn_kernel, sms, kSaThreads, sizeof(SaSmem), st, tk, tv,
-               static_cast<const __nv_bfloat16*>(q), block_table, cache_lens, G, Hkv, num_pages, max_pages,
+               static_cast<const __nv_bfloat16*>(q), block_table, G, Hkv, num_pages, max_pages,
                scale * kSaLog2e, plan, sw);
   }
   MSA_TRY(check_launch("shared_attn_kernel"));
