@@ -49,7 +49,7 @@ constexpr uint32_t kSaColO = 256;          // S of stream s at 128 s, O at 256 +
 
 // Work of a CTA: rows i0 .. i0 + nr - 1 (of the live ones), columns c0 .. c1 - 1, KV head
 // g.  Its parts are query rows ro * G .. of a block of m * G whose first is `base`.
-struct SaItem {
+struct alignas(16) SaItem {
   int i0, nr, c0, c1;
   int g, m, ro, base;
   int row, len, pad[2];   // the first of the rows, and its tokens
@@ -105,10 +105,17 @@ constexpr int kPlRowInts = 9, kPlNodeInts = 8;    // of the dynamic shared memor
 __constant__ int kPlLength[kPlLengths] = {1,  2,  3,  4,  5,  6,  7,   8,   10,  12,  14,
                                           16, 20, 24, 28, 32, 40, 48,  56,  64,  80,  96,
                                           112, 128, 160, 192, 256, 320, 384, 512, 768, 1024};
-// Costs in pages of a narrow item, which take what the memory takes for 64 KB
-constexpr float kPlWide = 1.3f;          // a page of a wide item
-constexpr float kPlStart = 1.5f;         // an item's start and end
-constexpr float kPlPart = 1.f / 128.f;   // a query row's part, written and read
+// Costs in pages of a narrow item (what the memory takes for 64 KB per SM, 1.47 us with all
+// SMs at it), from runs over item lengths: a page of a wide item 1.5 to 1.65 us; start and
+// end of an item, as far as no pages stream meanwhile; a query row's part, written and read
+constexpr float kPlWide = 1.1f;
+constexpr float kPlStart = 1.5f, kPlWideStart = 3.5f;
+constexpr float kPlPart = 1.f / 48.f;
+constexpr float kPlTail = 0.3f;          // of a row's longest item: what others wait for at the end
+// Runs come first and may be long (their parts are what costs); a row alone is cut shorter, so
+// that its items fill what the runs leave.  (Not with the last lengths, which always fit the
+// workspace: one item per node and tile.)
+__device__ __forceinline__ int pl_alone(int L) { return L < 512 ? min(L, 24) : L; }
 
 // Exclusive scan over the CTA; *total = the sum
 __device__ __forceinline__ int pl_scan(int v, int* warp_sums, int* total) {
@@ -200,27 +207,40 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   // ---- full pages that neighbours have in common: a warp per pair and 256 columns, which
   // lowers the value to the first column that differs
   {
-    const int chunks = (max_pages + 255) / 256;
-    for (int u = warp; u < (n - 1) * chunks; u += kPlWarps) {
-      const int i = u / chunks, j0 = (u - i * chunks) * 256;
-      const int most = min(len_of[i], len_of[i + 1]) / kBlock;
-      if (j0 >= most) continue;
-      const int32_t* a = table + static_cast<size_t>(row_of[i]) * max_pages;
-      const int32_t* b = table + static_cast<size_t>(row_of[i + 1]) * max_pages;
-      int x[8], y[8];
+    const int chunks = (max_pages + 255) / 256, units = (n - 1) * chunks;
+    struct Unit {
+      int i, j0, most, x[8], y[8];
+    };
+    auto load = [&](Unit& t, int u) {
+      t.i = chunks == 1 ? u : u / chunks;
+      t.j0 = (u - t.i * chunks) * 256;
+      t.most = u < units ? min(len_of[t.i], len_of[t.i + 1]) / kBlock : 0;
+      if (t.j0 >= t.most) return;
+      const int32_t* a = table + static_cast<size_t>(row_of[t.i]) * max_pages;
+      const int32_t* b = table + static_cast<size_t>(row_of[t.i + 1]) * max_pages;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int j = j0 + 32 * k + lane;
-        x[k] = j < most ? __ldg(a + j) : 0;
-        y[k] = j < most ? __ldg(b + j) : 0;
+        const int j = t.j0 + 32 * k + lane;
+        t.x[k] = j < t.most ? __ldg(a + j) : 0;
+        t.y[k] = j < t.most ? __ldg(b + j) : 0;
       }
+    };
+    auto look = [&](const Unit& t) {
+      if (t.j0 >= t.most) return;
       int at = -1;
 #pragma unroll
       for (int k = 7; k >= 0; --k) {
-        const uint32_t differ = __ballot_sync(0xffffffffu, x[k] != y[k]);
-        if (differ) at = j0 + 32 * k + __ffs(differ) - 1;
+        const uint32_t differ = __ballot_sync(0xffffffffu, t.x[k] != t.y[k]);
+        if (differ) at = t.j0 + 32 * k + __ffs(differ) - 1;
       }
-      if (at >= 0 && lane == 0) atomicMin(&common[i], at);
+      if (at >= 0 && lane == 0) atomicMin(&common[t.i], at);
+    };
+    for (int u = warp; u < units; u += 2 * kPlWarps) {   // two units' loads in flight
+      Unit p, q;
+      load(p, u);
+      load(q, u + kPlWarps);
+      look(p);
+      look(q);
     }
   }
   __syncthreads();
@@ -313,34 +333,63 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       nodes += total;
     }
   __syncthreads();
-  // ---- item length: a warp weighs a candidate.  The CTAs' share of all items' costs, and
-  // half an item that others wait for at the end.
+  // ---- item length: a warp weighs a candidate.  Either all items' costs shared by the CTAs
+  // and a part of a row's item at the end, or the rounds that the runs' long items take,
+  // whichever is more (in a round that is not full, items are 0.6 as long: the CTAs at work
+  // have more of the memory's bandwidth each).
   for (int c = warp; c < kPlLengths; c += kPlWarps) {
     const int L = kPlLength[c];
-    const float inv = 1.f / static_cast<float>(L);
-    float sum = 0.f, longest = 0.f;
-    int items = 0;
+    const int L1 = pl_alone(L);
+    const float inv = 1.f / static_cast<float>(L), inv1 = 1.f / static_cast<float>(L1);
+    float sum = 0.f, run = 0.f, alone = 0.f, long_sum = 0.f;
+    int items = 0, long_items = 0, most = 0;
     long long parts = 0;
+    for (int k = lane; k < nodes; k += 32)
+      if (nd_m[k] > 1) most = max(most, nd_pages[k]);
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+    most = min(most, L);
     for (int k = lane; k < nodes; k += 32) {
-      const int pages = nd_pages[k], m = nd_m[k], ns = pl_splits(pages, L, inv);
+      const int pages = nd_pages[k], m = nd_m[k];
+      const int ns = m > 1 ? pl_splits(pages, L, inv) : pl_splits(pages, L1, inv1);
       const int each = nd_tiles[k] * ns * Hkv;
       const int nr = min(m, 2 * tile_rows);
-      const float page = nr > tile_rows ? kPlWide : 1.f;
-      const float fix = kPlStart + static_cast<float>(nr * G) * kPlPart;
-      sum += static_cast<float>(nd_tiles[k] * Hkv) * (page * pages + fix * ns);
-      longest = fmaxf(longest, page * min(L, pages) + fix);
+      const bool wide = nr > tile_rows;
+      const float per = __fdividef((wide ? kPlWide : 1.f) * pages, static_cast<float>(ns)) +
+                        (wide ? kPlWideStart : kPlStart) + static_cast<float>(nr * G) * kPlPart;
+      sum += per * each;
       items += each;
       parts += static_cast<long long>(m) * G * ns * Hkv;
+      if (m == 1) {
+        alone = fmaxf(alone, per);
+      } else {
+        run = fmaxf(run, per);
+        if (2 * pages > most * ns) {
+          long_sum += per * each;
+          long_items += each;
+        }
+      }
     }
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) {
       sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      longest = fmaxf(longest, __shfl_xor_sync(0xffffffffu, longest, d));
+      run = fmaxf(run, __shfl_xor_sync(0xffffffffu, run, d));
+      alone = fmaxf(alone, __shfl_xor_sync(0xffffffffu, alone, d));
+      long_sum += __shfl_xor_sync(0xffffffffu, long_sum, d);
       items += __shfl_xor_sync(0xffffffffu, items, d);
+      long_items += __shfl_xor_sync(0xffffffffu, long_items, d);
       parts += __shfl_xor_sync(0xffffffffu, parts, d);
     }
-    // all in one round: the longest item is what counts
-    const float time = items <= sms ? longest : sum / sms + 0.5f * longest;
+    float time = fmaxf(run, alone);
+    if (items > sms) {
+      float rounds_time = run;
+      if (long_items > sms) {
+        const float x = static_cast<float>(long_items) / sms, full = floorf(x);
+        const float last = x > full ? fmaxf(x - full, 0.6f) : 0.f;
+        rounds_time = long_sum / long_items * (full + last);
+      }
+      time = fmaxf(sum / sms + kPlTail * alone, rounds_time);
+    }
     if (lane == 0)
       cost[c] = items <= plan.max_items && parts <= plan.max_parts ? time : INFINITY;
   }
@@ -358,15 +407,18 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       }
     }
   }
-  const int L = kPlLength[best];
-  const float inv = 1.f / static_cast<float>(L);
+  const int L = kPlLength[best], L1 = pl_alone(L);
+  const float inv = 1.f / static_cast<float>(L), inv1 = 1.f / static_cast<float>(L1);
+  auto splits = [&](int k) {
+    return nd_m[k] > 1 ? pl_splits(nd_pages[k], L, inv) : pl_splits(nd_pages[k], L1, inv1);
+  };
   // ---- first item and part of every node
   int n_items = 0, n_parts = 0;
   for (int k0 = 0; k0 < nodes; k0 += kPlThreads) {
     const int k = k0 + tid;
     int items = 0, parts = 0;
     if (k < nodes) {
-      const int ns = pl_splits(nd_pages[k], L, inv);
+      const int ns = splits(k);
       items = nd_tiles[k] * ns * Hkv;
       parts = nd_m[k] * G * ns * Hkv;
     }
@@ -393,28 +445,26 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       const int mid = (lo + hi) >> 1;
       if (nd_item[mid] <= e) lo = mid; else hi = mid;
     }
-    const int pages = nd_pages[lo], m = nd_m[lo], tiles = nd_tiles[lo], ns = pl_splits(pages, L, inv);
-    const int rest = (e - nd_item[lo]) / tiles, tile = e - nd_item[lo] - rest * tiles;
-    const int s = rest / Hkv, g = rest - s * Hkv;
-    SaItem item;
-    item.ro = tile * 2 * tile_rows;
-    item.i0 = nd_i0[lo] + item.ro;
-    item.nr = min(2 * tile_rows, m - item.ro);
-    item.c0 = nd_v0[lo] + pages * s / ns;
-    item.c1 = nd_v0[lo] + pages * (s + 1) / ns;
-    item.g = g;
-    item.m = m;
-    item.base = nd_part[lo] + (s * Hkv + g) * m * G;
-    item.row = row_of[item.i0];
-    item.len = len_of[item.i0];
-    plan.items[e] = item;
+    const int pages = nd_pages[lo], m = nd_m[lo], tiles = nd_tiles[lo], ns = splits(lo);
+    const uint32_t at = e - nd_item[lo];
+    const uint32_t rest = tiles == 1 ? at : at / static_cast<uint32_t>(tiles);
+    const int tile = at - rest * tiles;
+    const int s = rest / static_cast<uint32_t>(Hkv), g = rest - s * Hkv;
+    const float inv_ns = 1.f / static_cast<float>(ns);
+    // pages s / ns, rounded down (the products stay below 2^21: see pl_splits)
+    auto cut = [&](int k) { return static_cast<int>((static_cast<float>(pages * k) + 0.5f) * inv_ns); };
+    const int ro = tile * 2 * tile_rows, i0 = nd_i0[lo] + ro;
+    int4* item = reinterpret_cast<int4*>(plan.items + e);
+    item[0] = make_int4(i0, min(2 * tile_rows, m - ro), nd_v0[lo] + cut(s), nd_v0[lo] + cut(s + 1));
+    item[1] = make_int4(g, m, ro, nd_part[lo] + (s * Hkv + g) * m * G);
+    item[2] = make_int4(row_of[i0], len_of[i0], 0, 0);
   }
   // ---- every row's parts: its own node, then the runs above
   for (int i = tid; i < n; i += kPlThreads) {
     SaSeg* out = plan.segs + static_cast<size_t>(row_of[i]) * kSaMaxSegs;
     int k = 0;
     auto add = [&](int nd) {
-      out[k++] = {nd_part[nd], nd_m[nd], i - nd_i0[nd], pl_splits(nd_pages[nd], L, inv)};
+      out[k++] = {nd_part[nd], nd_m[nd], i - nd_i0[nd], splits(nd)};
     };
     if (nd_of[B + i] >= 0) add(nd_of[B + i]);
     for (int p = leaf_up[i]; p >= 0; p = parent[p]) add(nd_of[p]);
@@ -536,61 +586,91 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
       prefetch_tmap(&tm_k);
       prefetch_tmap(&tm_v);
     }
-    uint32_t pos = 0, qt = 0, tc = 0;
+    // The next item is claimed, read, checked and published in steps between the last pages
+    // of the current one, so that their latencies (an atomic, the item, its table entries) pass
+    // while pages are on the way, and q is there when the item's turn comes.  Not earlier:
+    // an item claimed by a CTA that is still busy waits (claims at the first page: system
+    // prompt 110 -> 125 us).
+    uint32_t pos = 0, qt = 0, tc = 0;      // stages and q tiles used, items published
     bool alive = true;
-    int id = blockIdx.x;
-    while (alive) {
-      if (tc > 0) {
+    SaItem it, nx;
+    int id = 0, page = -1, nx_page = -1, valid = 0, step = 1;
+    uint32_t ring_end = 0;                 // stages used when the published items are loaded
+    auto entry = [&](const SaItem& t, int c) {
+      return c < t.c1 ? __ldg(table + static_cast<size_t>(t.row) * max_pages + c) : -1;
+    };
+    auto prepare = [&]() {
+      if (step == 0) {
         if (lane == 0) id = atomicAdd(plan.counts + 1, 1);
-        id = __shfl_sync(0xffffffffu, id, 0);
-      }
-      const int tb = tc & 1;
-      if (lane == 0) alive = mbar_wait(&sm.slot_empty[tb], ((tc >> 1) & 1) ^ 1, status, 100);
-      alive = __shfl_sync(0xffffffffu, alive ? 1 : 0, 0) != 0;
-      if (!alive) break;
-      if (id >= n_items) {
-        if (lane == 0) {
-          sm.slot[tb].pages = -1;
-          mbar_arrive(&sm.slot_full[tb]);
+      } else if (step == 1) {
+        id = tc > 0 ? __shfl_sync(0xffffffffu, id, 0) : static_cast<int>(blockIdx.x);
+        if (id < n_items) nx = plan.items[id];
+      } else if (step == 2) {
+        if (id < n_items) nx_page = entry(nx, nx.c0 + lane);
+      } else if (step == 3) {
+        // pages that are none have no keys
+        const bool more = id < n_items;
+        bool last_ok = true;
+        valid = 0;
+        if (more) {
+          int pg = nx_page;
+          for (int c = nx.c0;;) {
+            const uint32_t oks = __ballot_sync(0xffffffffu, pg >= 0 && pg < num_pages);
+            valid += __popc(oks);
+            if (nx.c1 - c <= 32) {
+              last_ok = (oks >> (nx.c1 - 1 - c)) & 1;
+              break;
+            }
+            c += 32;
+            pg = entry(nx, c + lane);
+          }
         }
-        break;
+        const int tb = tc & 1;
+        if (lane == 0) {
+          alive = mbar_wait(&sm.slot_empty[tb], ((tc >> 1) & 1) ^ 1, status, 100);
+          if (alive) {
+            SaSlot& s = sm.slot[tb];
+            s.pages = -1;
+            if (more) {
+              if (valid != nx.c1 - nx.c0) atomicOr(status, kStatusBounds);
+              s.i0 = nx.i0;
+              s.nr = nx.nr;
+              s.g = nx.g;
+              s.m = nx.m;
+              s.ro = nx.ro;
+              s.base = nx.base;
+              s.pages = valid;
+              s.tail = last_ok ? min(kBlock, nx.len - (nx.c1 - 1) * kBlock) : kBlock;
+              s.wide = nx.nr > tile_rows;
+              s.ring = ring_end;
+              s.qt = qt;
+            }
+            mbar_arrive(&sm.slot_full[tb]);
+          }
+        }
+        alive = __shfl_sync(0xffffffffu, alive ? 1 : 0, 0) != 0;
+        if (more) {
+          ring_end += 2 * valid;
+          qt += nx.nr > tile_rows ? 2 : 1;
+        }
+        ++tc;
       }
-      const SaItem it = plan.items[id];
-      const int32_t* trow = table + static_cast<size_t>(it.row) * max_pages;
-      // pages that are none have no keys; the others are counted first
-      int valid = 0;
-      bool last_ok = true;
-      for (int c = it.c0; c < it.c1; c += 32) {
-        const int pg = c + lane < it.c1 ? __ldg(trow + c + lane) : 0;
-        const bool ok = c + lane < it.c1 && pg >= 0 && pg < num_pages;
-        const uint32_t oks = __ballot_sync(0xffffffffu, ok);
-        valid += __popc(oks);
-        if (it.c1 - c <= 32) last_ok = (oks >> (it.c1 - 1 - c)) & 1;
-      }
-      if (lane == 0) {
-        if (valid != it.c1 - it.c0) atomicOr(status, kStatusBounds);
-        SaSlot& s = sm.slot[tb];
-        s.i0 = it.i0;
-        s.nr = it.nr;
-        s.g = it.g;
-        s.m = it.m;
-        s.ro = it.ro;
-        s.base = it.base;
-        s.pages = valid;
-        s.tail = last_ok ? min(kBlock, it.len - (it.c1 - 1) * kBlock) : kBlock;
-        s.wide = it.nr > tile_rows;
-        s.ring = pos;
-        s.qt = qt;
-        mbar_arrive(&sm.slot_full[tb]);
-      }
-      qt += it.nr > tile_rows ? 2 : 1;
+      ++step;
+    };
+    while (true) {
+      while (alive && step < 4) prepare();
+      if (!alive || id >= n_items) break;
+      it = nx;
+      page = nx_page;
+      step = 0;
+      int left = valid;                    // pages of the item to come
       for (int c = it.c0; alive && c < it.c1; c += 32) {
-        const int mine = c + lane < it.c1 ? __ldg(trow + c + lane) : -1;
-        uint32_t oks = __ballot_sync(0xffffffffu, mine >= 0 && mine < num_pages);
+        if (c > it.c0) page = entry(it, c + lane);
+        uint32_t oks = __ballot_sync(0xffffffffu, page >= 0 && page < num_pages);
         for (; alive && oks; oks &= oks - 1) {
-          const int page = __shfl_sync(0xffffffffu, mine, __ffs(oks) - 1);
+          const int pg = __shfl_sync(0xffffffffu, page, __ffs(oks) - 1);
           if (lane == 0) {
-            const int at = page * Hkv + it.g;
+            const int at = pg * Hkv + it.g;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
               const uint32_t st = pos % kSaStages;
@@ -604,10 +684,9 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
             }
           }
           alive = __shfl_sync(0xffffffffu, alive ? 1 : 0, 0) != 0;
+          if (alive && --left < 4 && step < 4) prepare();
         }
       }
-      pos = __shfl_sync(0xffffffffu, pos, 0);
-      ++tc;
     }
     if (!alive && lane == 0) {
       // a wait ran out: the copies in flight have to land before the CTA ends
