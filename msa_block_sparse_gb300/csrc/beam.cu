@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
   };
   float ref = -INFINITY, sum = 0.f, bound = -INFINITY;   // this thread's sum is sum * 2^ref
   int kept = 0;                                          // keys in the buffer, at most kBmThreads
+  const int enough = K < 24 ? 48 : 2 * K;
   if (tid == 0) sm.count = 0;
   uint4 raw[kVecs];
 #pragma unroll
@@ -290,12 +291,18 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
     const float least = bound;
     // later tiles lose ties: K values at least as large stand before them
     if (first ? best >= least : best > least) {
+      uint32_t hits = 0;
 #pragma unroll
       for (int i = 0; i < kBmValues; ++i)
-        if ((first ? val[i] >= least : val[i] > least) && val[i] > -INFINITY) {
-          const int at = atomicAdd(&sm.count, 1);
-          if (at < kBmCap) sm.key[at] = key_of(val[i], place(i));
-        }
+        hits |= (first ? val[i] >= least : val[i] > least) ? 1u << i : 0u;
+      const bool one = (hits & (hits - 1)) == 0;         // as a rule, and then the largest
+      for (; hits; hits &= hits - 1) {
+        const uint32_t idx = place(__ffs(hits) - 1);
+        const float v = one ? best : plain(static_cast<float>(x[idx]));
+        if (v == -INFINITY) continue;
+        const int at = atomicAdd(&sm.count, 1);
+        if (at < kBmCap) sm.key[at] = key_of(v, idx);
+      }
     }
     __syncthreads();
     if (sm.count > kBmCap) {
@@ -324,7 +331,7 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
       __syncthreads();
     }
     kept = sm.count;
-    if (kept > kBmThreads) {
+    if (kept > enough) {                                 // a closer bound spares later tiles
       bm_rank(sm, K);
       kept = sm.count;
       if (kept == K) bound = unordered(static_cast<uint32_t>(sm.key[K - 1] >> 32));
@@ -548,20 +555,26 @@ struct BeamWorkspace {
   unsigned long long* keys;
 };
 
-// Slices of a row: enough CTAs for the GPU, tiles of a row shared evenly; no slice under
-// 1024 values, and a prompt's candidates within what the merge takes.
+// Slices of a row: the number that makes (rounds of CTAs over the GPU) x (a CTA's time) least.
+// A thread spends about 6.5 instructions on a value and 800 on the CTA's start, bound and
+// ranking (32 rows x 8 of 131,072 values: 8 slices 60 us, 2 slices TBD); a slice costs the
+// merge about as much as 4 values.  No slice under 1024 values, and a prompt's candidates
+// within what the merge takes.
 int beam_slices(long long rows, int W, int V, int K) {
-  const int fill = 12 * device_sm_count();
-  const int tiles = (V + kBmTile - 1) / kBmTile;
-  long long want = (fill + rows - 1) / rows;
-  if (want >= tiles) {
-    const int small = V / 1024 < 1 ? 1 : V / 1024;
-    want = want < small ? want : small;
-    if (want < tiles) want = tiles;
+  const long long cap = 4LL * device_sm_count();
+  long long most = V / 1024;
+  if (most > kBmCandidates / (W * K)) most = kBmCandidates / (W * K);
+  long long best = 1, least = 0;
+  for (long long s = 1; s <= most || s == 1; ++s) {
+    const long long rounds = (rows * s + cap - 1) / cap;
+    const long long tiles = (V + kBmTile * s - 1) / (kBmTile * s);
+    const long long time = rounds * (tiles * kBmValues * 13 / 2 + 800) + 26 * s;
+    if (s == 1 || time < least) {
+      least = time;
+      best = s;
+    }
   }
-  const int most = kBmCandidates / (W * K);
-  if (want > most) want = most;
-  return static_cast<int>(want < 1 ? 1 : want);
+  return static_cast<int>(best);
 }
 
 BeamWorkspace carve_beam_workspace(WsCursor& ws, long long rows, int slices, int K) {

@@ -7,10 +7,13 @@
 //
 // Bound by memory for a pack (each value read and written once), by latency for a step.
 //
-// Work: a CTA takes a run of tokens and either heads of q or heads of the smaller tensors
-// (k, v, index q, index k: taken as one tensor of all their heads, since each by itself is a few
-// rows per token).  It looks up the tokens' places and the angles once; a row of 128
-// channels then belongs to 16 threads (rope_ex.cuh), three rows' loads in flight.
+// Work, of two kinds of CTAs.  Those of q take a run of its [T Hq] rows, as in
+// rope_ex.cu: a row of 128 channels belongs to 16 threads, which keep the factors
+// (1 + w) cos and (1 + w) sin while the token stays the same.  k, v and the index heads are a
+// few rows per token each: a CTA takes 8 tokens, 16 threads each, through a share of all
+// these heads, tensor after tensor; the factors are formed once per tensor, and all threads
+// change tensors at the same row, so that the loads (three rows are in flight) run on across
+// the border.  A CTA looks its tokens' places and angles up once.
 #include <cmath>
 #include "rope_ex.cuh"
 
@@ -19,8 +22,9 @@ namespace msa {
 namespace {
 
 constexpr int kCaThreads = 128;
-constexpr int kCaMaxTokens = 16;                 // of a CTA
 constexpr int kCaSlots = kCaThreads / (kD / 8);  // rows side by side
+constexpr int kCaTokens = 16;                    // of a CTA at most
+constexpr int kCaDeep = 4;                       // rows of a thread loaded or at work
 
 struct CaJob {
   const __nv_bfloat16* x;       // [T, H, 128]
@@ -30,222 +34,223 @@ struct CaJob {
 };
 
 struct CaArgs {
-  CaJob q, small[4];            // small: k, v, index q, index k, each of Hkv heads
-  int Hq, Hkv, smalls;
+  CaJob q, small[4];            // small: k, v, index q, index k, each of H heads
+  int Hq, H, rows;              // rows: heads of all small tensors
+  int q_run, q_ctas;            // rows of q per CTA; CTAs of q, the others have small tensors,
+  int shares;                   // the rows of a group of tokens in so many shares
   const int32_t *table, *cu, *lens;
-  int S, T, num_pages, max_pages, R, run;
-  int q_shares;                 // blockIdx.y below: heads of q, the others: of the small ones
+  int S, T, num_pages, max_pages, R;
   float eps, gain;
   uint32_t inv_half;            // ceil(2^20 / (R / 2)), for k < 2048
+  uint32_t inv_hq;              // ceil(2^20 / Hq), for i < 4096
 };
 
 struct CaSmem {
-  alignas(16) float table[kCaMaxTokens * kD];
-  alignas(16) float w1[4][kD];  // 1 + w of the small tensors
+  alignas(16) float table[kCaTokens * kD];       // per token: cos, then sin, of its R / 2 pairs
   unsigned long long freq[kD / 2];
-  int pos[kCaMaxTokens];
-  int page[kCaMaxTokens];       // -1: the token is left alone
+  int2 place[kCaTokens];                         // position, page (-1: the token is left alone)
 };
 
-// Rows (token, head h0 .. h0 + nh - 1); heads run fastest.  kQ: heads of q, whose factors
-// (1 + w) cos and (1 + w) sin stay in registers while the token stays the same.  Otherwise
-// head h is head h % Hkv of small tensor h / Hkv.  kNorm: the tensor (one of them) has weights.
-template <bool kQ, bool kNorm, bool kHalf>
-__device__ __forceinline__ void ca_rows(const CaArgs& a, const CaSmem& sm, int t0, int ntok, int h0,
-                                        int nh) {
-  const int c = threadIdx.x & 15, slot = threadIdx.x >> 4;
-  const RxLane l = rx_lane<kHalf>(c, a.R);
-  const int n = ntok * nh;
-  float2 w1[4];
+// Places and angles of the tokens t0 .. t0 + ntok - 1
+__device__ __forceinline__ void ca_tokens(const CaArgs& a, const RxTurns& turns, CaSmem& sm, int t0,
+                                          int ntok, uint32_t* status) {
+  const int half = a.R >> 1;
+  for (int i = threadIdx.x; i < half; i += kCaThreads) sm.freq[i] = turns.f[i];
+  if (static_cast<int>(threadIdx.x) < kCaTokens) {
+    int pos = 0, page = -1;
+    const int t = t0 + threadIdx.x;
+    if (static_cast<int>(threadIdx.x) < ntok) {
+      // as many tokens in every row: a first guess that one load confirms
+      int s = static_cast<int>(static_cast<long long>(t) * a.S / a.T);
+      int first = __ldg(a.cu + s), end = __ldg(a.cu + s + 1), L = __ldg(a.lens + s);
+      if (t < first || t >= end) {
+        int lo = 0, hi = a.S;                    // largest s with cu[s] <= t
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid;
+        }
+        s = lo;
+        first = __ldg(a.cu + s);
+        end = __ldg(a.cu + s + 1);
+        L = __ldg(a.lens + s);
+      }
+      if (t >= first && t < end && L != 0) {     // length 0: padding
+        const long long p = static_cast<long long>(L) - end + t;
+        if (p >= 0 && p < static_cast<long long>(a.max_pages) * kBlock) {
+          pos = static_cast<int>(p);
+          page = __ldg(a.table + static_cast<size_t>(s) * a.max_pages + pos / kBlock);
+        }
+        if (page < 0 || page >= a.num_pages) {
+          page = -1;
+          atomicOr(status, kStatusBounds);
+        }
+      }
+    }
+    sm.place[threadIdx.x] = make_int2(pos, page);
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < ntok * half; k += kCaThreads) {
+    const int tok = static_cast<int>((static_cast<uint32_t>(k) * a.inv_half) >> 20);
+    const int i = k - tok * half;
+    const float2 cs = rx_cos_sin(sm.place[tok].x, sm.freq[i]);
+    sm.table[tok * a.R + i] = cs.x * a.gain;
+    sm.table[tok * a.R + half + i] = cs.y * a.gain;
+  }
+  __syncthreads();
+}
+
+template <bool kHalf>
+__device__ __forceinline__ void ca_weights(const __nv_bfloat16* w, const RxLane& l, float2 (&w1)[4]) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) w1[p] = make_float2(1.f, 1.f);
-  if (kQ && kNorm) {
-    float2 wv[4];
-    RxRow wr;
-    wr.a = *reinterpret_cast<const uint2*>(a.q.w + l.off0);
-    wr.b = *reinterpret_cast<const uint2*>(a.q.w + l.off1);
-    rx_unpack<kHalf>(wr, wv);
+  if (!w) return;
+  float2 wv[4];
+  RxRow wr;
+  wr.a = *reinterpret_cast<const uint2*>(w + l.off0);
+  wr.b = *reinterpret_cast<const uint2*>(w + l.off1);
+  rx_unpack<kHalf>(wr, wv);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) w1[p] = __fadd2_rn(wv[p], w1[p]);
+  for (int p = 0; p < 4; ++p) w1[p] = __fadd2_rn(wv[p], w1[p]);
+}
+
+// Norm (of the 16 lanes' row) and rotation of a row; what is not turned keeps its bits
+template <bool kNorm, bool kHalf>
+__device__ __forceinline__ RxRow ca_row(const RxRow& raw, const float2 (&cc)[4], const float2 (&ss)[4],
+                                        const RxLane& l, float eps) {
+  float2 v[4];
+  rx_unpack<kHalf>(raw, v);
+  float2 rr = make_float2(1.f, 1.f);
+  if (kNorm) {
+    float2 q = __fmul2_rn(v[0], v[0]);
+#pragma unroll
+    for (int p = 1; p < 4; ++p) q = __ffma2_rn(v[p], v[p], q);
+    float sum = q.x + q.y;
+#pragma unroll
+    for (int m = 8; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    rr.x = rr.y = rsqrtf(sum * (1.f / kD) + eps);
   }
-  constexpr int kDeep = 4;
-  RxRow raw[kDeep];
-  // row i = (token f_tok, head h0 + f_h); both counters go up by kCaSlots rows at a time
-  int f_tok = slot / nh, f_h = slot - f_tok * nh, c_tok = f_tok, c_h = f_h;
-  const int d_tok = kCaSlots / nh, d_h = kCaSlots - d_tok * nh;
-  auto step = [&](int& tok, int& h) {
-    tok += d_tok;
-    h += d_h;
-    if (h >= nh) {
-      h -= nh;
-      ++tok;
-    }
+  rx_turn(v, cc, ss, !kNorm || l.rot);
+  if (kNorm) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) v[p] = __fmul2_rn(v[p], rr);
+  }
+  return kNorm || l.rot ? rx_pack<kHalf>(v) : raw;
+}
+
+// n consecutive rows of q from row r0 on, the first of token t0 and head h0
+template <bool kNorm, bool kHalf>
+__device__ __forceinline__ void ca_q(const CaArgs& a, const RxTurns& turns, CaSmem& sm, uint32_t* status) {
+  const long long all = static_cast<long long>(a.T) * a.Hq, r0 = static_cast<long long>(blockIdx.x) * a.q_run;
+  const int n = static_cast<int>(all - r0 < a.q_run ? all - r0 : a.q_run);
+  const int t0 = static_cast<int>(r0 / a.Hq), h0 = static_cast<int>(r0 - static_cast<long long>(t0) * a.Hq);
+  const int c = threadIdx.x & 15, slot = threadIdx.x >> 4;
+  const RxLane l = rx_lane<kHalf>(c, a.R);
+  const __nv_bfloat16* xb = a.q.x + r0 * kD;
+  __nv_bfloat16* yb = a.q.y + r0 * kD;
+  RxRow raw[kCaDeep];
+  auto fetch = [&](int i, RxRow& r) {
+    r.a = r.b = make_uint2(0u, 0u);
+    if (i < n) r = rx_load<kHalf>(xb + static_cast<size_t>(i) * kD, l);
   };
+#pragma unroll
+  for (int k = 0; k < kCaDeep - 1; ++k) fetch(k * kCaSlots + slot, raw[k]);
+  float2 w1[4];
+  ca_weights<kHalf>(kNorm ? a.q.w : nullptr, l, w1);
+  ca_tokens(a, turns, sm, t0, (h0 + n + a.Hq - 1) / a.Hq, status);
+  int have = -1;
+  bool live = false;
+  float2 cc[4], ss[4];
+  for (int base = 0; base < n; base += kCaDeep * kCaSlots) {   // uniform: every lane reaches the shuffles
+#pragma unroll
+    for (int k = 0; k < kCaDeep; ++k) {
+      if (base + k * kCaSlots >= n) break;
+      const int i = base + k * kCaSlots + slot;
+      fetch(i + (kCaDeep - 1) * kCaSlots, raw[(k + kCaDeep - 1) % kCaDeep]);
+      const int tok = static_cast<int>((static_cast<uint32_t>(h0 + i) * a.inv_hq) >> 20);
+      if (tok != have && i < n) {
+        have = tok;
+        live = sm.place[tok].y >= 0;
+        rx_coefficients(sm.table + tok * a.R, a.R >> 1, l, w1, 1.f, cc, ss);
+      }
+      const RxRow out = ca_row<kNorm, kHalf>(raw[k], cc, ss, l, a.eps);
+      if (i < n && live) rx_store<kHalf>(yb + static_cast<size_t>(i) * kD, l, out);
+    }
+  }
+}
+
+// The small tensors' heads r0 .. r1 - 1 of 8 tokens
+template <bool kHalf>
+__device__ __forceinline__ void ca_small(const CaArgs& a, const RxTurns& turns, CaSmem& sm, uint32_t* status) {
+  const int cta = blockIdx.x - a.q_ctas, group = cta / a.shares, share = cta - group * a.shares;
+  const int t0 = group * kCaSlots, ntok = min(kCaSlots, a.T - t0);
+  const int r0 = a.rows * share / a.shares, r1 = a.rows * (share + 1) / a.shares;
+  const int c = threadIdx.x & 15, slot = threadIdx.x >> 4;
+  const RxLane l = rx_lane<kHalf>(c, a.R);
+  const size_t first = static_cast<size_t>(t0 + slot) * a.H;    // row of this token in any of them
+  // loads
+  int fr = r0, fj = r0 / a.H, fleft = a.H - (r0 - fj * a.H);
+  const __nv_bfloat16* fp = a.small[fj].x + (first + a.H - fleft) * kD;
+  RxRow raw[kCaDeep];
   auto fetch = [&](RxRow& r) {
     r.a = r.b = make_uint2(0u, 0u);
-    if (f_tok < ntok) {
-      const __nv_bfloat16* x = a.q.x;
-      int H = a.Hq, h = h0 + f_h;
-      if (!kQ) {
-        H = a.Hkv;
-        const int j = h / H;
-        h -= j * H;
-        x = a.small[j].x;
-      }
-      r = rx_load<kHalf>(x + (static_cast<size_t>(t0 + f_tok) * H + h) * kD, l);
+    if (fr >= r1) return;
+    if (slot < ntok) r = rx_load<kHalf>(fp, l);
+    fp += kD;
+    if (--fleft == 0 && fr + 1 < r1) {
+      fp = a.small[++fj].x + first * kD;
+      fleft = a.H;
     }
-    step(f_tok, f_h);
+    ++fr;
   };
 #pragma unroll
-  for (int k = 0; k < kDeep - 1; ++k) fetch(raw[k]);
-  int have = -1;
+  for (int k = 0; k < kCaDeep - 1; ++k) fetch(raw[k]);
+  ca_tokens(a, turns, sm, t0, ntok, status);
+  const int2 at = sm.place[slot];
+  int r = r0, j = r0 / a.H, left = 0, ystep = kD;
+  bool norm = false, turn = false;
+  __nv_bfloat16* yp = nullptr;
   float2 cc[4], ss[4];
-  for (int base = 0; base < n; base += kDeep * kCaSlots) {   // uniform: every lane reaches the shuffles
+  auto enter = [&](int h) {                    // tensor j, from its head h on
+    const CaJob& b = a.small[j];
+    left = a.H - h;
+    norm = b.w != nullptr;
+    turn = b.turn != 0;
+    ystep = b.paged ? kBlock * kD : kD;
+    yp = b.y + (b.paged ? (static_cast<size_t>(max(at.y, 0)) * a.H + h) * kBlock + (at.x & (kBlock - 1))
+                        : first + h) * kD;
+    float2 w1[4];
+    ca_weights<kHalf>(b.w, l, w1);
+    rx_coefficients(sm.table + slot * a.R, a.R >> 1, l, w1, 1.f, cc, ss);
+  };
+  enter(r0 - j * a.H);
+  while (r < r1) {                             // uniform over the CTA
 #pragma unroll
-    for (int k = 0; k < kDeep; ++k) {
-      if (base + k * kCaSlots >= n) break;
-      fetch(raw[(k + kDeep - 1) % kDeep]);
-      float2 v[4];
-      rx_unpack<kHalf>(raw[k], v);
-      float2 rr = make_float2(1.f, 1.f);
-      if (kNorm) {
-        float2 q = __fmul2_rn(v[0], v[0]);
-#pragma unroll
-        for (int p = 1; p < 4; ++p) q = __ffma2_rn(v[p], v[p], q);
-        float sum = q.x + q.y;
-#pragma unroll
-        for (int m = 8; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        rr.x = rr.y = rsqrtf(sum * (1.f / kD) + a.eps);
+    for (int k = 0; k < kCaDeep; ++k) {
+      if (r >= r1) break;
+      fetch(raw[(k + kCaDeep - 1) % kCaDeep]);
+      RxRow out = raw[k];
+      if (turn) out = norm ? ca_row<true, kHalf>(raw[k], cc, ss, l, a.eps) : ca_row<false, kHalf>(raw[k], cc, ss, l, a.eps);
+      if (at.y >= 0) rx_store<kHalf>(yp, l, out);
+      yp += ystep;
+      if (++r < r1 && --left == 0) {
+        ++j;
+        enter(0);
       }
-      const int tok = c_tok;
-      int h = h0 + c_h;
-      step(c_tok, c_h);
-      if (tok >= ntok || sm.page[tok] < 0) continue;
-      __nv_bfloat16* row;
-      RxRow out = raw[k];                                    // what is not turned keeps its bits
-      if (kQ) {
-        if (tok != have) {
-          have = tok;
-          rx_coefficients(sm.table + tok * a.R, a.R >> 1, l, w1, 1.f, cc, ss);
-        }
-        rx_turn(v, cc, ss, !kNorm || l.rot);
-        if (kNorm) {
-#pragma unroll
-          for (int p = 0; p < 4; ++p) v[p] = __fmul2_rn(v[p], rr);
-        }
-        if (kNorm || l.rot) out = rx_pack<kHalf>(v);
-        row = a.q.y + (static_cast<size_t>(t0 + tok) * a.Hq + h) * kD;
-      } else {
-        const int j = h / a.Hkv;
-        h -= j * a.Hkv;
-        const CaJob& job = a.small[j];
-        if (job.turn) {
-          const bool norm = kNorm && job.w;
-          if (norm) {
-            const float4 x = *reinterpret_cast<const float4*>(&sm.w1[j][l.off0]);
-            const float4 y = *reinterpret_cast<const float4*>(&sm.w1[j][l.off1]);
-            if (kHalf) {
-              w1[0] = make_float2(x.x, x.y);
-              w1[1] = make_float2(x.z, x.w);
-              w1[2] = make_float2(y.x, y.y);
-              w1[3] = make_float2(y.z, y.w);
-            } else {
-              w1[0] = make_float2(x.x, x.z);
-              w1[1] = make_float2(y.x, y.z);
-              w1[2] = make_float2(x.y, x.w);
-              w1[3] = make_float2(y.y, y.w);
-            }
-#pragma unroll
-            for (int p = 0; p < 4; ++p) w1[p] = __fmul2_rn(w1[p], rr);
-          } else {
-#pragma unroll
-            for (int p = 0; p < 4; ++p) w1[p] = make_float2(1.f, 1.f);
-          }
-          rx_coefficients(sm.table + tok * a.R, a.R >> 1, l, w1, 1.f, cc, ss);
-          rx_turn(v, cc, ss, !norm || l.rot);
-          if (norm || l.rot) out = rx_pack<kHalf>(v);
-        }
-        row = job.paged ? job.y + ((static_cast<size_t>(sm.page[tok]) * a.Hkv + h) * kBlock +
-                                   (sm.pos[tok] & (kBlock - 1))) * kD
-                        : job.y + (static_cast<size_t>(t0 + tok) * a.Hkv + h) * kD;
-      }
-      rx_store<kHalf>(row, l, out);
     }
   }
 }
 
 }  // namespace
 
-// grid (runs of tokens, shares of q's heads and of the small tensors' heads)
 template <bool kHalf>
-__global__ void __launch_bounds__(kCaThreads, 6) cache_append_kernel(const __grid_constant__ CaArgs a,
+__global__ void __launch_bounds__(kCaThreads, 8) cache_append_kernel(const __grid_constant__ CaArgs a,
                                                                      const __grid_constant__ RxTurns turns,
                                                                      uint32_t* status) {
   pdl_enter();
   __shared__ CaSmem sm;
-  const int t0 = blockIdx.x * a.run, ntok = min(a.run, a.T - t0);
-  const int half = a.R >> 1;
-  const bool of_q = static_cast<int>(blockIdx.y) < a.q_shares;
-  for (int i = threadIdx.x; i < half; i += kCaThreads) sm.freq[i] = turns.f[i];
-  if (static_cast<int>(threadIdx.x) < ntok) {
-    const int t = t0 + threadIdx.x;
-    // as many tokens in every row: a first guess that one load confirms
-    int s = static_cast<int>(static_cast<long long>(t) * a.S / a.T);
-    int first = __ldg(a.cu + s), end = __ldg(a.cu + s + 1), L = __ldg(a.lens + s);
-    if (t < first || t >= end) {
-      int lo = 0, hi = a.S;                // largest s with cu[s] <= t
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid;
-      }
-      s = lo;
-      first = __ldg(a.cu + s);
-      end = __ldg(a.cu + s + 1);
-      L = __ldg(a.lens + s);
-    }
-    int pos = 0, page = -1;
-    if (t >= first && t < end && L != 0) {     // length 0: padding
-      const long long p = static_cast<long long>(L) - end + t;
-      if (p >= 0 && p < static_cast<long long>(a.max_pages) * kBlock) {
-        pos = static_cast<int>(p);
-        page = __ldg(a.table + static_cast<size_t>(s) * a.max_pages + pos / kBlock);
-      }
-      if (page < 0 || page >= a.num_pages) {
-        page = -1;
-        atomicOr(status, kStatusBounds);
-      }
-    }
-    sm.pos[threadIdx.x] = pos;
-    sm.page[threadIdx.x] = page;
-  }
-  bool normed = false;                         // one of the small tensors is
-  if (!of_q) {
-    for (int j = 0; j < a.smalls; ++j) {
-      if (!a.small[j].w) continue;
-      normed = true;
-      sm.w1[j][threadIdx.x] = 1.f + __bfloat162float(a.small[j].w[threadIdx.x]);
-    }
-  }
-  __syncthreads();
-  for (int k = threadIdx.x; k < ntok * half; k += kCaThreads) {
-    const int tok = static_cast<int>((static_cast<uint32_t>(k) * a.inv_half) >> 20);
-    const int i = k - tok * half;
-    const float2 cs = rx_cos_sin(sm.pos[tok], sm.freq[i]);
-    sm.table[tok * a.R + i] = cs.x * a.gain;
-    sm.table[tok * a.R + half + i] = cs.y * a.gain;
-  }
-  __syncthreads();
-  const int heads = of_q ? a.Hq : a.smalls * a.Hkv;
-  const int y = of_q ? blockIdx.y : blockIdx.y - a.q_shares;
-  const int ny = of_q ? a.q_shares : gridDim.y - a.q_shares;
-  const int h0 = heads * y / ny, nh = heads * (y + 1) / ny - h0;
-  if (of_q) {
-    if (a.q.w) ca_rows<true, true, kHalf>(a, sm, t0, ntok, h0, nh);
-    else ca_rows<true, false, kHalf>(a, sm, t0, ntok, h0, nh);
-  } else {
-    if (normed) ca_rows<false, true, kHalf>(a, sm, t0, ntok, h0, nh);
-    else ca_rows<false, false, kHalf>(a, sm, t0, ntok, h0, nh);
-  }
+  if (static_cast<int>(blockIdx.x) >= a.q_ctas) ca_small<kHalf>(a, turns, sm, status);
+  else if (a.q.w) ca_q<true, kHalf>(a, turns, sm, status);
+  else ca_q<false, kHalf>(a, turns, sm, status);
 }
 
 }  // namespace msa
@@ -300,14 +305,14 @@ msa_status_t msa_cache_append(const void* q, const void* k, const void* v, const
   a.q = job(q, w_q, q_out, false, true);
   a.small[0] = job(k, w_k, k_cache, true, true);
   a.small[1] = job(v, nullptr, v_cache, true, false);
-  a.smalls = 2;
+  a.rows = 2 * Hkv;
   if (index) {
     a.small[2] = job(q_idx, w_qi, q_idx_out, false, true);
     a.small[3] = job(k_idx, w_ki, kidx_cache, true, true);
-    a.smalls = 4;
+    a.rows = 4 * Hkv;
   }
   a.Hq = Hq;
-  a.Hkv = Hkv;
+  a.H = Hkv;
   a.table = block_table;
   a.cu = cu_seqlens;
   a.lens = cache_lens;
@@ -319,20 +324,21 @@ msa_status_t msa_cache_append(const void* q, const void* k, const void* v, const
   a.eps = eps;
   a.gain = rope->gain;
   a.inv_half = ((1u << 20) + rope->dim / 2 - 1) / (rope->dim / 2);
-  // Tokens per CTA: about 256 rows of q (shorter runs repeat the places' and angles' work),
-  // but enough CTAs for the GPU; heads are split when there are few tokens.
-  const int small = a.smalls * Hkv, fill = 8 * device_sm_count();
-  int run = 256 / Hq;
-  if (run > T / fill) run = T / fill;
-  a.run = run < 1 ? 1 : (run > kCaMaxTokens ? kCaMaxTokens : run);
-  const int runs = (T + a.run - 1) / a.run;
-  auto shares = [&](int heads) {               // no CTA with less than a pass of rows
-    const int want = fill / runs, most = (heads * a.run + kCaSlots - 1) / kCaSlots;
-    const int n = want < most ? want : most;
-    return n < 1 ? 1 : n > heads ? heads : n;
-  };
-  a.q_shares = shares(Hq);
-  const int y_ctas = a.q_shares + shares(small);
+  a.inv_hq = ((1u << 20) + Hq - 1) / Hq;
+  // q: 64 rows per CTA, fewer (a pass of rows at least) when that would leave SMs without one;
+  // at most 16 tokens.  The others: shares of a token's heads while there are SMs for them.
+  const int sms = device_sm_count();
+  const long long q_rows = static_cast<long long>(T) * Hq;
+  long long run = q_rows / (2 * sms);
+  run = run < kCaSlots ? kCaSlots : (run > 64 ? 64 : run);
+  if (run > static_cast<long long>(kCaTokens - 1) * Hq) run = static_cast<long long>(kCaTokens - 1) * Hq;
+  a.q_run = static_cast<int>(run > Hq ? run / Hq * Hq : run);
+  const long long q_ctas = (q_rows + a.q_run - 1) / a.q_run;
+  const int groups = (T + kCaSlots - 1) / kCaSlots, fill = 4 * sms / groups;
+  a.shares = fill < 1 ? 1 : (fill < a.rows ? fill : a.rows);
+  const long long ctas = q_ctas + static_cast<long long>(groups) * a.shares;
+  if (ctas > INT32_MAX) return fail(MSA_ERR_UNSUPPORTED, "T = %d tokens of %d heads are too many", T, Hq);
+  a.q_ctas = static_cast<int>(q_ctas);
   const RxTurns turns = rx_turns(*rope);
   uint32_t* sw = nullptr;
   MSA_TRY(status_word(&sw));
@@ -340,7 +346,7 @@ msa_status_t msa_cache_append(const void* q, const void* k, const void* v, const
   {
     TraceScope trace_("cache_append_kernel", st);
     launch_pdl(rope->layout == MSA_ROPE_HALF ? cache_append_kernel<true> : cache_append_kernel<false>,
-               dim3(runs, y_ctas), kCaThreads, 0, st, a, turns, sw);
+               static_cast<unsigned>(ctas), kCaThreads, 0, st, a, turns, sw);
   }
   return check_launch("cache_append_kernel");
 }
