@@ -3,19 +3,21 @@
 //
 // Bound by memory: the logits are read once (the only large input).
 //
-//   beam_scan_kernel   CTA = a slice of one beam's vocabulary.  Every thread keeps the
-//                      running maximum and sum of exponentials of its values (sums joined
-//                      in 64 bits); the slice's K best values are kept beside
-//                      them.  Within a beam the order of the scores is that of the values,
-//                      so that nothing else of the slice can be chosen.
+//   beam_scan_kernel   CTA = a slice of one beam's vocabulary.  One pass: every thread sums
+//                      the exponentials of its values (2^(x log2 e - ref), ref a whole
+//                      number) and keeps the maximum of each 16 or so of them.  The maxima
+//                      give a bound that the slice's K best values reach; the few pieces that
+//                      hold any such value are read again (from L2) and ranked.  Within
+//                      a beam the order of the scores is that of the values, so that nothing
+//                      else of the slice can be chosen.
 //   beam_merge_kernel  CTA = a prompt.  Log-sum-exp of its beams from the slices, scores of
 //                      the slices' candidates in 64 bits, the best K in order.
 //
 // K best of n values without sorting: the values are dealt into groups, and the K-th
 // largest of the groups' maxima is a bound that at least K values reach; of values in no
-// particular order about 1.4 K do.  These few are ranked by counting.  Keys are unique
-// (value, then the lower index), so that at most the K best groups hold anything above
-// the bound, whatever the values are.
+// particular order about 1.4 K do.  These few are ranked by counting.  Where far more reach
+// it (equal values at the border), the slice is taken tile by tile with unique keys (value,
+// then the lower index): at most the K best threads hold anything above the bound then.
 #include <cfloat>
 #include "kernels.cuh"
 
@@ -29,6 +31,8 @@ constexpr int kBmMaxW = 64;
 constexpr int kBmValues = 16;                          // of a thread and tile
 constexpr int kBmTile = kBmThreads * kBmValues;
 constexpr int kBmCap = kBmMaxK * kBmValues + kBmThreads;   // keys of the buffer
+constexpr int kBmPieces = 32;                          // maxima that a thread keeps
+constexpr int kBmList = 1024;                          // pieces read again
 constexpr int kBmCandidates = 16384;                   // of a prompt, at most
 constexpr int kBmMergeThreads = 512;
 constexpr float kBmLog2eHi = 1.4426950216293335f;      // log2 e, and what fp32 leaves of it
@@ -129,11 +133,15 @@ struct ScanSmem {
   unsigned long long key[kBmCap];
   unsigned long long best[kBmMaxK];
   alignas(16) float group[128];
-  alignas(16) unsigned long long gkey[kBmThreads];
+  union {
+    float piece[kBmPieces][kBmThreads];                // maxima of the pass
+    unsigned long long gkey[kBmThreads];               // later: the threads' best keys
+  };
+  int list[kBmList];
   float sum[kBmThreads / 32], ref[kBmThreads / 32];
   float bound;
   unsigned long long bound_key;
-  int count;
+  int count, pieces;
 };
 
 // The K best of the sm.count keys in sm.key, in order, into sm.best; count <= kBmCap.
@@ -155,6 +163,7 @@ __device__ __forceinline__ void bm_rank(ScanSmem& sm, int K) {
     sm.gkey[tid] = top;
     __syncthreads();
     int above = 0;
+#pragma unroll 8
     for (int i = 0; i < kBmThreads; ++i) above += sm.gkey[i] > top;
     if (above == K - 1) sm.bound_key = top;      // n > 256 >= K: there is a K-th group
     if (tid == 0) sm.count = 0;
@@ -169,6 +178,7 @@ __device__ __forceinline__ void bm_rank(ScanSmem& sm, int K) {
   if (tid < n) {
     const unsigned long long mine = sm.key[tid];
     int above = 0;
+#pragma unroll 8
     for (int i = 0; i < n; ++i) above += sm.key[i] > mine;
     if (above < K) sm.best[above] = mine;
   }
@@ -207,24 +217,25 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
       return __ldcs(reinterpret_cast<const uint4*>(xa + lo));
     return L::part(xa + lo, skew - lo, skew + V - lo);
   };
-  float ref = -INFINITY, sum = 0.f, bound = -INFINITY;   // this thread's sum is sum * 2^ref
-  int kept = 0;                                          // keys in the buffer, at most kBmThreads
-  const int enough = K < 24 ? 48 : 2 * K;
-  if (tid == 0) sm.count = 0;
+  float ref = -INFINITY, sum = 0.f;                      // this thread's sum is sum * 2^ref
+  constexpr int kTile = kVecs * kBmThreads;              // vectors of a tile
+  const int tiles = (v1 - v0 + kTile - 1) / kTile, per = (tiles + kBmPieces - 1) / kBmPieces;
+  float top = -INFINITY, piece = -INFINITY;              // maxima: of all, of `per` tiles
+  if (tid == 0) sm.count = sm.pieces = 0;
   uint4 raw[kVecs];
+  auto load_tile = [&](int t) {
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u) raw[u] = load(v0 + u * kBmThreads + tid);
-  for (int vt = v0; vt < v1; vt += kVecs * kBmThreads) {
+    for (int u = 0; u < kVecs; ++u) raw[u] = load(v0 + t * kTile + u * kBmThreads + tid);
+  };
+  auto place = [&](int t, int i) -> uint32_t {           // value i of this thread and tile t
+    return static_cast<uint32_t>((v0 + t * kTile + (i / L::kN) * kBmThreads + tid) * L::kN + i % L::kN - skew);
+  };
+  load_tile(0);
+  for (int t = 0, left = per; t < tiles; ++t) {
     float val[kBmValues];
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) L::unpack(raw[u], val + u * L::kN);
-    if (vt + kVecs * kBmThreads < v1) {
-#pragma unroll
-      for (int u = 0; u < kVecs; ++u) raw[u] = load(vt + (kVecs + u) * kBmThreads + tid);
-    }
-    auto place = [&](int i) -> uint32_t {
-      return static_cast<uint32_t>((vt + (i / L::kN) * kBmThreads + tid) * L::kN + i % L::kN - skew);
-    };
+    if (t + 1 < tiles) load_tile(t + 1);
     // ---- maximum and sum of exponentials of this thread's values.  x log2 e - ref with ref
     // whole is rounded relative to itself, however large x is.
     float best = -INFINITY, part = 0.f, to = ref;
@@ -259,82 +270,105 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
       sum = (ref > -INFINITY ? sum * bm_scale(ref - to) : 0.f) + part;
       ref = to;
     }
-    // ---- candidates: what reaches the bound goes into the buffer
-    const bool first = vt == v0;
-    if (first) {
-      // bound: the K-th largest of the maxima of 64 or 128 groups of threads
-      const int groups = K <= 32 ? 64 : 128, per = kBmThreads / groups;
-      float g = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, 1));
-      if (per == 4) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-      if (tid % per == 0) sm.group[tid / per] = g;
-      __syncthreads();
-      // the threads of a group compare its maximum with a share of the others each
-      int above = 0, level = 0;
-      const int share = groups / per, from = tid % per * share;
-      for (int i = from; i < from + share; i += 4) {
-        const float4 o = *reinterpret_cast<const float4*>(&sm.group[i]);
-        above += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g);
-        level += (o.x >= g) + (o.y >= g) + (o.z >= g) + (o.w >= g);
-      }
-      above += __shfl_xor_sync(0xffffffffu, above, 1);
-      level += __shfl_xor_sync(0xffffffffu, level, 1);
-      if (per == 4) {
-        above += __shfl_xor_sync(0xffffffffu, above, 2);
-        level += __shfl_xor_sync(0xffffffffu, level, 2);
-      }
-      if (above < K && level >= K) sm.bound = g;         // one value, whoever writes it
-      __syncthreads();
-      bound = sm.bound;
-    } else if (!__syncthreads_or(best > bound)) {
-      continue;
+    piece = fmaxf(piece, best);
+    if (--left == 0 || t + 1 == tiles) {
+      sm.piece[t / per][tid] = piece;
+      top = fmaxf(top, piece);
+      piece = -INFINITY;
+      left = per;
     }
-    const float least = bound;
-    // later tiles lose ties: K values at least as large stand before them
-    if (first ? best >= least : best > least) {
-      uint32_t hits = 0;
-#pragma unroll
-      for (int i = 0; i < kBmValues; ++i)
-        hits |= (first ? val[i] >= least : val[i] > least) ? 1u << i : 0u;
-      const bool one = (hits & (hits - 1)) == 0;         // as a rule, and then the largest
-      for (; hits; hits &= hits - 1) {
-        const uint32_t idx = place(__ffs(hits) - 1);
-        const float v = one ? best : plain(static_cast<float>(x[idx]));
-        if (v == -INFINITY) continue;
+  }
+  // ---- bound: the K-th largest of the maxima of 64 or 128 groups of threads
+  float bound;
+  {
+    const int groups = K <= 32 ? 64 : 128, share_of = kBmThreads / groups;
+    float g = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    if (share_of == 4) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+    if (tid % share_of == 0) sm.group[tid / share_of] = g;
+    __syncthreads();
+    // the threads of a group compare its maximum with a share of the others each
+    int above = 0, level = 0;
+    const int share = groups / share_of, from = tid % share_of * share;
+    for (int i = from; i < from + share; i += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(&sm.group[i]);
+      above += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g);
+      level += (o.x >= g) + (o.y >= g) + (o.z >= g) + (o.w >= g);
+    }
+    above += __shfl_xor_sync(0xffffffffu, above, 1);
+    level += __shfl_xor_sync(0xffffffffu, level, 1);
+    if (share_of == 4) {
+      above += __shfl_xor_sync(0xffffffffu, above, 2);
+      level += __shfl_xor_sync(0xffffffffu, level, 2);
+    }
+    if (above < K && level >= K) sm.bound = g;           // one value, whoever writes it
+    __syncthreads();
+    bound = sm.bound;
+  }
+  // ---- the pieces that reach it, and their values
+  if (top >= bound && top > -INFINITY)
+    for (int p = 0; p * per < tiles; ++p) {
+      const float m = sm.piece[p][tid];
+      if (m >= bound && m > -INFINITY) {
+        const int at = atomicAdd(&sm.pieces, 1);
+        if (at < kBmList) sm.list[at] = p << 8 | tid;
+      }
+    }
+  __syncthreads();
+  const int pieces = sm.pieces;
+  if (pieces <= kBmList) {
+    const int each = per * kBmValues;
+    for (int e = tid; e < pieces * each; e += kBmThreads) {
+      const int k = e / each, i = e - k * each, u = i / L::kN;
+      const int v = v0 + ((sm.list[k] >> 8) * per * kVecs + u) * kBmThreads + (sm.list[k] & 255);
+      const int idx = v * L::kN + i % L::kN - skew;
+      if (v >= v1 || idx < 0 || idx >= V) continue;
+      const float z = plain(static_cast<float>(x[idx]));
+      if (z >= bound && z > -INFINITY) {
         const int at = atomicAdd(&sm.count, 1);
-        if (at < kBmCap) sm.key[at] = key_of(v, idx);
+        if (at < kBmCap) sm.key[at] = key_of(z, idx);
       }
     }
     __syncthreads();
-    if (sm.count > kBmCap) {
-      // far more than K (equal or ascending values): the threads are the groups, their best
-      // keys, no two alike, give the bound, and at most K threads hold anything above it
+  }
+  if (pieces > kBmList || sm.count > kBmCap) {
+    // equal values at the border, or the best ones close together: tile by tile, the threads
+    // are the groups, and at most K threads hold keys above the bound of their best keys
+    int kept = 0;                                        // keys of the tiles before
+    __syncthreads();
+    for (int t = 0; t < tiles; ++t) {
+      load_tile(t);
+      float val[kBmValues];
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) L::unpack(raw[u], val + u * L::kN);
       unsigned long long mine = 0;
 #pragma unroll
       for (int i = 0; i < kBmValues; ++i) {
-        const unsigned long long k = val[i] > -INFINITY ? key_of(val[i], place(i)) : 0;
+        val[i] = plain(val[i]);
+        const unsigned long long k = val[i] > -INFINITY ? key_of(val[i], place(t, i)) : 0;
         mine = k > mine ? k : mine;
       }
+      // K keys are kept: only better ones matter
+      const unsigned long long floor_key = kept == K ? sm.key[K - 1] : 0;
+      if (!__syncthreads_or(mine > floor_key)) continue;
       sm.gkey[tid] = mine;
-      if (tid == 0) sm.bound_key = 1;                    // fewer than K threads hold anything
-      __syncthreads();
-      int above = 0;
-      for (int i = 0; i < kBmThreads; ++i) above += sm.gkey[i] > mine;
-      if (above == K - 1 && mine > 0) sm.bound_key = mine;
-      if (tid == 0) sm.count = kept;
-      __syncthreads();
-      const unsigned long long bk = sm.bound_key;
-#pragma unroll
-      for (int i = 0; i < kBmValues; ++i) {
-        const unsigned long long k = val[i] > -INFINITY ? key_of(val[i], place(i)) : 0;
-        if (k >= bk) sm.key[atomicAdd(&sm.count, 1)] = k;
+      if (tid == 0) {
+        sm.bound_key = 1;                                // fewer than K threads hold anything
+        sm.count = kept;
       }
       __syncthreads();
-    }
-    kept = sm.count;
-    if (kept > enough) {                                 // a closer bound spares later tiles
+      int above = 0;
+#pragma unroll 8
+      for (int i = 0; i < kBmThreads; ++i) above += sm.gkey[i] > mine;
+      if (above == K - 1 && mine > 0) sm.bound_key = mine;
+      __syncthreads();
+      const unsigned long long bk = sm.bound_key > floor_key ? sm.bound_key : floor_key + 1;
+#pragma unroll
+      for (int i = 0; i < kBmValues; ++i) {
+        const unsigned long long k = val[i] > -INFINITY ? key_of(val[i], place(t, i)) : 0;
+        if (k >= bk) sm.key[atomicAdd(&sm.count, 1)] = k;
+      }
       bm_rank(sm, K);
       kept = sm.count;
-      if (kept == K) bound = unordered(static_cast<uint32_t>(sm.key[K - 1] >> 32));
     }
   }
   bm_rank(sm, K);
@@ -413,8 +447,10 @@ __device__ __forceinline__ void bm_bound(MergeSmem& sm, Cand top, int K) {
   }
   __syncthreads();
   int above = 0;
-  const int share = kBmGroups / kBmPer, from = tid % kBmPer * share;
-  for (int i = from; i < from + share; ++i) above += beats(sm.gs[i], sm.gat[i], top.s, top.at);
+  const int from = tid % kBmPer * (kBmGroups / kBmPer);
+#pragma unroll
+  for (int i = 0; i < kBmGroups / kBmPer; ++i)
+    above += beats(sm.gs[from + i], sm.gat[from + i], top.s, top.at);
 #pragma unroll
   for (int m = 1; m < kBmPer; m <<= 1) above += __shfl_xor_sync(0xffffffffu, above, m);
   if (above == K - 1 && top.s > 0 && tid % kBmPer == 0) {
@@ -436,21 +472,27 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
   extern __shared__ __align__(16) uint8_t smem_raw[];
   MergeSmem& sm = *reinterpret_cast<MergeSmem*>(smem_raw);
   const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // candidate i = (beam, slice, rank); the first key is asked for before it is needed
+  const int per_row = slices * K, total = W * per_row;
+  const unsigned long long key0 = tid < total ? keys[static_cast<size_t>(n) * total + tid] : 0;
   // ---- log-sum-exp of every beam, a warp each; NaN as score: the beam is dead
   for (int w = warp; w < W; w += kBmMergeThreads / 32) {
     const int row = n * W + w;
+    const BeamScan* st = stats + static_cast<size_t>(row) * slices;
+    const BeamScan mine = lane < slices ? st[lane] : BeamScan{-INFINITY, 0.f};
     const float s = scores[row];
     const bool live = s > -INFINITY;
     const bool ended = finished && finished[row];
-    float ref = -INFINITY;
+    float ref = mine.ref;
     double sum = 0.0;
     if (live && !ended) {
-      const BeamScan* st = stats + static_cast<size_t>(row) * slices;
-      for (int i = lane; i < slices; i += 32) ref = fmaxf(ref, st[i].ref);
+      for (int i = lane + 32; i < slices; i += 32) ref = fmaxf(ref, st[i].ref);
 #pragma unroll
       for (int m = 16; m >= 1; m >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, m));
-      if (ref > -INFINITY)
-        for (int i = lane; i < slices; i += 32) sum += st[i].sum * bm_scale(st[i].ref - ref);
+      if (ref > -INFINITY) {
+        sum = mine.sum * bm_scale(mine.ref - ref);
+        for (int i = lane + 32; i < slices; i += 32) sum += st[i].sum * bm_scale(st[i].ref - ref);
+      }
 #pragma unroll
       for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
     }
@@ -461,8 +503,6 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
     }
   }
   __syncthreads();
-  // ---- candidate i = (beam, slice, rank)
-  const int per_row = slices * K, total = W * per_row;
   auto get = [&](int i) -> Cand {
     const int w = i / per_row, row = n * W + w;
     const double s = sm.score[w];
@@ -471,7 +511,7 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
       if (i - w * per_row != 0) return {0, 0};
       return {ordered(s), ~(static_cast<uint32_t>(w) * V + pad_token)};
     }
-    const unsigned long long key = keys[static_cast<size_t>(n) * total + i];
+    const unsigned long long key = i < kBmMergeThreads ? key0 : keys[static_cast<size_t>(n) * total + i];
     if (key == 0) return {0, 0};
     const uint32_t v = 0xFFFFFFFFu - static_cast<uint32_t>(key);
     float x = unordered(static_cast<uint32_t>(key >> 32));
@@ -530,6 +570,7 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
     const unsigned long long s = sm.s[tid];
     const uint32_t at = sm.at[tid];
     int above = 0;
+#pragma unroll 8
     for (int i = 0; i < left; ++i) above += beats(sm.s[i], sm.at[i], s, at);
     if (above < K) {
       const uint32_t flat = ~at;
@@ -556,10 +597,9 @@ struct BeamWorkspace {
 };
 
 // Slices of a row: the number that makes (rounds of CTAs over the GPU) x (a CTA's time) least.
-// A thread spends about 6.5 instructions on a value and 800 on the CTA's start, bound and
-// ranking (32 rows x 8 of 131,072 values: 8 slices 60 us, 2 slices TBD); a slice costs the
-// merge about as much as 4 values.  No slice under 1024 values, and a prompt's candidates
-// within what the merge takes.
+// A thread spends about 7 instructions on a value and 700 on the CTA's start, bound and ranking;
+// a slice costs the merge about as much as 4 values.  No slice under 1024 values, and a prompt's
+// candidates within what the merge takes.
 int beam_slices(long long rows, int W, int V, int K) {
   const long long cap = 4LL * device_sm_count();
   long long most = V / 1024;
@@ -568,7 +608,7 @@ int beam_slices(long long rows, int W, int V, int K) {
   for (long long s = 1; s <= most || s == 1; ++s) {
     const long long rounds = (rows * s + cap - 1) / cap;
     const long long tiles = (V + kBmTile * s - 1) / (kBmTile * s);
-    const long long time = rounds * (tiles * kBmValues * 13 / 2 + 800) + 26 * s;
+    const long long time = rounds * (tiles * kBmValues * 7 + 700) + 26 * s;
     if (s == 1 || time < least) {
       least = time;
       best = s;

@@ -334,7 +334,7 @@ msa_status_t msa_cache_append(const void* q, const void* k, const void* v, const
   if (run > static_cast<long long>(kCaTokens - 1) * Hq) run = static_cast<long long>(kCaTokens - 1) * Hq;
   a.q_run = static_cast<int>(run > Hq ? run / Hq * Hq : run);
   const long long q_ctas = (q_rows + a.q_run - 1) / a.q_run;
-  const int groups = (T + kCaSlots - 1) / kCaSlots, fill = 4 * sms / groups;
+  const int groups = (T - 1) / kCaSlots + 1, fill = 4 * sms / groups;
   a.shares = fill < 1 ? 1 : (fill < a.rows ? fill : a.rows);
   const long long ctas = q_ctas + static_cast<long long>(groups) * a.shares;
   if (ctas > INT32_MAX) return fail(MSA_ERR_UNSUPPORTED, "T = %d tokens of %d heads are too many", T, Hq);

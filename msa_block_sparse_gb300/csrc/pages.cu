@@ -337,11 +337,13 @@ __global__ void __launch_bounds__(kPgThreads) pages_compact_kernel(
 //
 // Rows take each other's places: every row is put aside in the workspace first, and the
 // references of the rows that change are taken back; then each row is written from its
-// parent's copy and its references are added.  A warp per row.  Few entries: one cluster
-// does both halves with a barrier between them (one launch less); many: two launches
-// over the whole GPU.
-constexpr int kRoThreads = 512;
+// parent's copy and its references are added.  Bound by latency (lengths, parents, the
+// parent's length, entries, atomics, one after another).  Few entries: one cluster does both
+// halves, a warp per row, with a barrier between them (one launch less); many: two launches
+// over the whole GPU, a CTA per row.
+constexpr int kRoThreads = 512, kRoRowThreads = 128;
 constexpr int kRoCluster = 8;
+constexpr int kRoBatch = 8;                  // entries of a lane in flight: their atomics overlap
 constexpr long long kRoOneLaunch = 65536;    // entries of the table at most
 
 struct ReorderArgs {
@@ -360,9 +362,11 @@ __device__ __forceinline__ int reorder_from(const ReorderArgs& a, const int32_t*
   return *bad ? r : p;
 }
 
-__device__ __forceinline__ void reorder_put_aside(const ReorderArgs& a, int warp, int warps, uint32_t* status) {
-  const int lane = threadIdx.x & 31;
-  for (int r = warp; r < a.B; r += warps) {
+// kThreads threads per row: group `group` of `groups`, `lane` within it
+template <int kThreads>
+__device__ __forceinline__ void reorder_put_aside(const ReorderArgs& a, int group, int groups, int lane,
+                                                  uint32_t* status) {
+  for (int r = group; r < a.B; r += groups) {
     const int L = a.lens[r];
     if (lane == 0) a.held_lens[r] = L;
     if (!row_ok(L, a.max_pages)) {
@@ -373,23 +377,31 @@ __device__ __forceinline__ void reorder_put_aside(const ReorderArgs& a, int warp
     const bool changes = reorder_from(a, a.lens, r, &bad) != r;
     const int32_t* row = a.table + static_cast<size_t>(r) * a.max_pages;
     int32_t* to = a.held + static_cast<size_t>(r) * a.max_pages;
-    for (int j = lane; j < blocks_of(L); j += 32) {
-      const int pg = row[j];
-      to[j] = pg;
-      if (!changes) continue;
-      if (pg < 0 || pg >= a.num_pages) {
-        atomicOr(status, kStatusBounds);
-      } else if (atomicSub(&a.ref[pg], 1) <= 0) {      // held more often than counted
-        atomicAdd(&a.ref[pg], 1);
-        atomicOr(status, kStatusBounds);
+    for (int j0 = lane; j0 < blocks_of(L); j0 += kThreads * kRoBatch) {
+      int pg[kRoBatch], old[kRoBatch];
+#pragma unroll
+      for (int k = 0; k < kRoBatch; ++k) pg[k] = j0 + kThreads * k < blocks_of(L) ? row[j0 + kThreads * k] : -1;
+#pragma unroll
+      for (int k = 0; k < kRoBatch; ++k) {
+        const bool here = j0 + kThreads * k < blocks_of(L);
+        if (here) to[j0 + kThreads * k] = pg[k];
+        old[k] = 1;
+        if (here && changes) old[k] = pg[k] >= 0 && pg[k] < a.num_pages ? atomicSub(&a.ref[pg[k]], 1) : -1;
       }
+#pragma unroll
+      for (int k = 0; k < kRoBatch; ++k)
+        if (old[k] <= 0) {                             // no page, or held more often than counted
+          if (pg[k] >= 0 && pg[k] < a.num_pages) atomicAdd(&a.ref[pg[k]], 1);
+          atomicOr(status, kStatusBounds);
+        }
     }
   }
 }
 
-__device__ __forceinline__ void reorder_take(const ReorderArgs& a, int warp, int warps, uint32_t* status) {
-  const int lane = threadIdx.x & 31;
-  for (int r = warp; r < a.B; r += warps) {
+template <int kThreads>
+__device__ __forceinline__ void reorder_take(const ReorderArgs& a, int group, int groups, int lane,
+                                             uint32_t* status) {
+  for (int r = group; r < a.B; r += groups) {
     bool bad;
     const int p = reorder_from(a, a.held_lens, r, &bad);
     const int old = a.held_lens[r];
@@ -401,14 +413,20 @@ __device__ __forceinline__ void reorder_take(const ReorderArgs& a, int warp, int
     const int L = p < 0 ? 0 : a.held_lens[p];
     int32_t* row = a.table + static_cast<size_t>(r) * a.max_pages;
     const int32_t* from = a.held + static_cast<size_t>(max(p, 0)) * a.max_pages;
-    for (int j = lane; j < blocks_of(L); j += 32) {
-      const int pg = from[j];
-      row[j] = pg;
-      if (pg < 0 || pg >= a.num_pages) atomicOr(status, kStatusBounds);
-      else atomicAdd(&a.ref[pg], 1);
+    for (int j0 = lane; j0 < blocks_of(L); j0 += kThreads * kRoBatch) {
+      int pg[kRoBatch];
+#pragma unroll
+      for (int k = 0; k < kRoBatch; ++k) pg[k] = j0 + kThreads * k < blocks_of(L) ? from[j0 + kThreads * k] : -1;
+#pragma unroll
+      for (int k = 0; k < kRoBatch; ++k) {
+        if (j0 + kThreads * k >= blocks_of(L)) break;
+        row[j0 + kThreads * k] = pg[k];
+        if (pg[k] < 0 || pg[k] >= a.num_pages) atomicOr(status, kStatusBounds);
+        else atomicAdd(&a.ref[pg[k]], 1);
+      }
     }
     if (row_ok(old, a.max_pages))
-      for (int j = blocks_of(L) + lane; j < blocks_of(old); j += 32) row[j] = -1;
+      for (int j = blocks_of(L) + lane; j < blocks_of(old); j += kThreads) row[j] = -1;
     if (lane == 0) {
       a.lens[r] = L;
       a.kept[r] = L;
@@ -418,16 +436,21 @@ __device__ __forceinline__ void reorder_take(const ReorderArgs& a, int warp, int
 
 // kHalf 0: both halves, the grid is one cluster; 1: put aside; 2: take
 template <int kHalf>
-__global__ void __launch_bounds__(kRoThreads) pages_reorder_kernel(const ReorderArgs a, uint32_t* status) {
+__global__ void __launch_bounds__(kHalf == 0 ? kRoThreads : kRoRowThreads)
+    pages_reorder_kernel(const ReorderArgs a, uint32_t* status) {
   pdl_enter();
-  const int warp = blockIdx.x * (kRoThreads / 32) + (threadIdx.x >> 5);
-  const int warps = gridDim.x * (kRoThreads / 32);
-  if (kHalf != 2) reorder_put_aside(a, warp, warps, status);
   if (kHalf == 0) {
+    const int warp = blockIdx.x * (kRoThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int warps = gridDim.x * (kRoThreads / 32);
+    reorder_put_aside<32>(a, warp, warps, lane, status);
     // releases what every thread of the cluster wrote and has it seen by the others
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    reorder_take<32>(a, warp, warps, lane, status);
+  } else if (kHalf == 1) {
+    reorder_put_aside<kRoRowThreads>(a, blockIdx.x, gridDim.x, threadIdx.x, status);
+  } else {
+    reorder_take<kRoRowThreads>(a, blockIdx.x, gridDim.x, threadIdx.x, status);
   }
-  if (kHalf != 1) reorder_take(a, warp, warps, status);
 }
 
 // ---------------------------------------------------------------- copies
@@ -820,15 +843,15 @@ msa_status_t msa_pages_reorder(const int32_t* parents, int32_t* block_table, int
     cudaLaunchKernelEx(&cfg, pages_reorder_kernel<0>, a, sw);
     return check_launch("pages_reorder_kernel");
   }
-  const int most = 4 * device_sm_count();
+  const int most = 16 * device_sm_count();
   {
     TraceScope trace_("pages_reorder_aside_kernel", st);
-    launch_pdl(pages_reorder_kernel<1>, ctas < most ? ctas : most, kRoThreads, 0, st, a, sw);
+    launch_pdl(pages_reorder_kernel<1>, B < most ? B : most, kRoRowThreads, 0, st, a, sw);
   }
   MSA_TRY(check_launch("pages_reorder_aside_kernel"));
   {
     TraceScope trace_("pages_reorder_take_kernel", st);
-    launch_pdl(pages_reorder_kernel<2>, ctas < most ? ctas : most, kRoThreads, 0, st, a, sw);
+    launch_pdl(pages_reorder_kernel<2>, B < most ? B : most, kRoRowThreads, 0, st, a, sw);
   }
   return check_launch("pages_reorder_take_kernel");
 }

@@ -44,7 +44,7 @@ constexpr int kSaQWarp = 3;
 constexpr uint32_t kSaIdescS = idesc_bf16(128, 64, false, false);        // S = Q K^T, 64 keys
 constexpr uint32_t kSaIdescPV = idesc_bf16(128, 128, false, true);       // O += P V
 constexpr float kSaLog2e = 1.4426950408889634f;
-constexpr float kSaRescale = 8.0f;         // log2 of the largest P before o is rescaled
+constexpr float kSaRescale = 8.0f;         // log2 of the largest P before o is rescaled (P < 256 fits bf16)
 constexpr uint32_t kSaColO = 256;          // S of stream s at 128 s, O at 256 + 128 s
 
 // Work of a CTA: rows i0 .. i0 + nr - 1 (of the live ones), columns c0 .. c1 - 1, KV head
@@ -67,7 +67,7 @@ struct SaPlan {
   SaSeg* segs;        // [B][kSaMaxSegs]
   int* n_segs;        // [B], 0 for rows without tokens
   float4* part_o;     // [blocks][32][m G]
-  float2* part_ml;    // (maximum in log2, sum)
+  float2* part_ml;    // (reference for the exponentials among the products q k, sum)
   int max_items, max_parts;
 };
 
@@ -502,13 +502,14 @@ struct SaSmem {
 };
 static_assert(sizeof(SaSmem) <= 232448, "above the 227 KB of a CTA");
 
-// 64 values of S as P: p = 2^(s sl2 - mu), packed; sums into acc
+// 64 values of S as P: p = 2^((s - mu) sl2), packed; sums into acc.  The maximum is subtracted
+// before the factor: rounded as a product, a large one would be off by whole units.
 __device__ __forceinline__ void sa_exp64(const uint32_t (&sv)[64], float sl2, float mu, uint32_t* pk,
                                          float2 (&acc)[4]) {
   const float2 f = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
-    const float2 y = ffma2(make_float2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), f, nmu);
+    const float2 y = fmul2(fadd2(make_float2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), nmu), f);
     const float2 p = make_float2(sa_ex2(y.x), sa_ex2(y.y));
     acc[j & 3] = fadd2(acc[j & 3], p);
     pk[j] = pack_bf16x2(p.x, p.y);
@@ -538,7 +539,7 @@ __device__ __forceinline__ void sa_load64(uint32_t addr, uint32_t (&sv)[64]) {
 __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ table, int G, int Hkv, int num_pages, int max_pages, float sl2,
-    const SaPlan plan, uint32_t* status) {
+    float rescale, const SaPlan plan, uint32_t* status) {
   pdl_enter();
   const int n_items = plan.counts[0];
   if (static_cast<int>(blockIdx.x) >= n_items) return;    // as many items are claimed by the others
@@ -841,8 +842,8 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
             for (int k = 0; k < 64; ++k) sv[k] = k < lim ? sv[k] : 0xFF800000u;
           }
           const bool any = lim > 0;
-          const float mnew = any ? fmaxf(m, sa_max64(sv) * sl2) : m;
-          const bool resc = mnew > m + kSaRescale;
+          const float mnew = any ? fmaxf(m, sa_max64(sv)) : m;
+          const bool resc = mnew > m + rescale;
           const float mu = resc ? mnew : m;
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                            make_float2(0.f, 0.f)};
@@ -857,7 +858,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
             // O stands still once the PV of the block before is done
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[s][b ^ 1], (uses[b ^ 1] - 1) & 1, status, 132)))) break;
             tc_fence_after();
-            const float alpha = need ? sa_ex2(m - mu) : 1.f;
+            const float alpha = need ? sa_ex2((m - mu) * sl2) : 1.f;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               uint32_t v[32];
@@ -872,7 +873,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
           if (any) {
             const float2 a = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
             const float rs = a.x + a.y;
-            l = m == -INFINITY ? rs : (resc ? l * sa_ex2(m - mu) : l) + rs;
+            l = m == -INFINITY ? rs : (resc ? l * sa_ex2((m - mu) * sl2) : l) + rs;
             m = mu;
           }
           tmem_st16(sbuf, pk);
@@ -908,6 +909,9 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.pv_done[s][b], (uses[b] - 1) & 1, status, 134)))) break;
       }
       float f0 = 1.f, f1 = 0.f;
+      // keys, but no product that is a number: as the definition has it, NaN (a reference of
+      // -infinity would stand for no keys)
+      if (l != l && m == -INFINITY) m = 0.f;
       float2 ml = make_float2(m, l);
       if (!t.wide && t.pages > 0) {
         // both halves' maxima; either stream then writes half of the channels
@@ -918,8 +922,8 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
         ++merges;
         const float2 a = sm.ml[0][r], c = sm.ml[1][r];
         const float M = fmaxf(a.x, c.x);
-        f0 = a.x == -INFINITY ? 0.f : sa_ex2(a.x - M);
-        f1 = c.x == -INFINITY ? 0.f : sa_ex2(c.x - M);
+        f0 = a.x == -INFINITY ? 0.f : sa_ex2((a.x - M) * sl2);
+        f1 = c.x == -INFINITY ? 0.f : sa_ex2((c.x - M) * sl2);
         ml = make_float2(M, a.y * f0 + c.y * f1);
       }
       tc_fence_after();
@@ -976,7 +980,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
 
 // grid (rows, KV heads, shares of the G heads); thread (d4, head): heads run fastest, as the
 // parts lie in memory
-__global__ void __launch_bounds__(512) shared_combine_kernel(const SaPlan plan, int G, int Hkv,
+__global__ void __launch_bounds__(512) shared_combine_kernel(const SaPlan plan, int G, int Hkv, float sl2,
                                                              __nv_bfloat16* __restrict__ o,
                                                              float* __restrict__ lse) {
   pdl_enter();
@@ -1006,14 +1010,14 @@ __global__ void __launch_bounds__(512) shared_combine_kernel(const SaPlan plan, 
 #pragma unroll
       for (int s = 0; s < kDeep; ++s) top = fmaxf(top, ml[s].x);
       if (top == -INFINITY) continue;
-      const float f = sa_ex2(M - top);
+      const float f = M == -INFINITY ? 0.f : sa_ex2((M - top) * sl2);
       acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
       l *= f;
       M = top;
 #pragma unroll
       for (int s = 0; s < kDeep; ++s) {
         if (ml[s].x == -INFINITY) continue;
-        const float e = sa_ex2(ml[s].x - top);
+        const float e = sa_ex2((ml[s].x - top) * sl2);
         acc.x = fmaf(x[s].x, e, acc.x);
         acc.y = fmaf(x[s].y, e, acc.y);
         acc.z = fmaf(x[s].z, e, acc.z);
@@ -1022,12 +1026,12 @@ __global__ void __launch_bounds__(512) shared_combine_kernel(const SaPlan plan, 
       }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   const size_t at = (static_cast<size_t>(b) * Hkv + g) * G + h;
   if (M == -INFINITY) acc = make_float4(0.f, 0.f, 0.f, 0.f);
   *reinterpret_cast<uint2*>(o + at * kD + 4 * d4) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (lse && d4 == 0) lse[at] = M == -INFINITY ? -INFINITY : (M + __log2f(l)) * 0.6931471805599453f;
+  if (lse && d4 == 0) lse[at] = M == -INFINITY ? -INFINITY : fmaf(M, sl2, log2f(l)) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------- host
@@ -1126,13 +1130,13 @@ msa_status_t msa_decode_shared(const void* q, const void* k_cache, const void* v
     TraceScope trace_("shared_attn_kernel", st);
     launch_pdl(shared_attn_kernel, sms, kSaThreads, sizeof(SaSmem), st, tk, tv,
                static_cast<const __nv_bfloat16*>(q), block_table, G, Hkv, num_pages, max_pages,
-               scale * kSaLog2e, plan, sw);
+               scale * kSaLog2e, kSaRescale / (scale * kSaLog2e), plan, sw);
   }
   MSA_TRY(check_launch("shared_attn_kernel"));
   {
     TraceScope trace_("shared_combine_kernel", st);
     const int Gc = G < 16 ? G : 16;
-    launch_pdl(shared_combine_kernel, dim3(B, Hkv, (G + Gc - 1) / Gc), 32 * Gc, 0, st, plan, G, Hkv,
+    launch_pdl(shared_combine_kernel, dim3(B, Hkv, (G + Gc - 1) / Gc), 32 * Gc, 0, st, plan, G, Hkv, scale * kSaLog2e,
                static_cast<__nv_bfloat16*>(o), lse);
   }
   return check_launch("shared_combine_kernel");
