@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
     return static_cast<uint32_t>((v0 + t * kTile + (i / L::kN) * kBmThreads + tid) * L::kN + i % L::kN - skew);
   };
   load_tile(0);
+  float* mine = &sm.piece[0][tid];                       // where the next maximum goes
   for (int t = 0, left = per; t < tiles; ++t) {
     float val[kBmValues];
 #pragma unroll
@@ -240,9 +241,9 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
     // whole is rounded relative to itself, however large x is.
     float best = -INFINITY, part = 0.f, to = ref;
     auto scan = [&](float most) {
-      best = val[0];
+      best = fmaxf(val[0], val[1]);
 #pragma unroll
-      for (int i = 1; i < kBmValues; ++i) best = fmaxf(best, val[i]);
+      for (int i = 2; i < kBmValues; i += 2) best = max3f(best, val[i], val[i + 1]);
       to = fmaxf(ref, rintf(fminf(fmaxf(best, -most), most) * kBmLog2eHi));
       const float2 hi = make_float2(kBmLog2eHi, kBmLog2eHi), lo = make_float2(kBmLog2eLo, kBmLog2eLo);
       const float2 r = make_float2(-to, -to);
@@ -272,7 +273,8 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
     }
     piece = fmaxf(piece, best);
     if (--left == 0 || t + 1 == tiles) {
-      sm.piece[t / per][tid] = piece;
+      *mine = piece;
+      mine += kBmThreads;
       top = fmaxf(top, piece);
       piece = -INFINITY;
       left = per;
@@ -288,8 +290,8 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
     __syncthreads();
     // the threads of a group compare its maximum with a share of the others each
     int above = 0, level = 0;
-    const int share = groups / share_of, from = tid % share_of * share;
-    for (int i = from; i < from + share; i += 4) {
+#pragma unroll 4
+    for (int i = tid % share_of * 4; i < groups; i += 4 * share_of) {   // side by side: no bank twice
       const float4 o = *reinterpret_cast<const float4*>(&sm.group[i]);
       above += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g);
       level += (o.x >= g) + (o.y >= g) + (o.z >= g) + (o.w >= g);
@@ -306,6 +308,7 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
   }
   // ---- the pieces that reach it, and their values
   if (top >= bound && top > -INFINITY)
+#pragma unroll 4
     for (int p = 0; p * per < tiles; ++p) {
       const float m = sm.piece[p][tid];
       if (m >= bound && m > -INFINITY) {
@@ -374,25 +377,32 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
   bm_rank(sm, K);
   unsigned long long* out = keys + (static_cast<size_t>(row) * slices + blockIdx.x) * K;
   if (tid < K) out[tid] = tid < sm.count ? sm.key[tid] : 0;
-  // ---- the slice's sum
+  // ---- the slice's sum: references first, then the sums, the last of them in 64 bits
+  float most = ref;
 #pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) {
-    const float o = __shfl_xor_sync(0xffffffffu, ref, m), os = __shfl_xor_sync(0xffffffffu, sum, m);
-    const float t = fmaxf(ref, o);
-    if (t > -INFINITY) sum = sum * bm_scale(ref - t) + os * bm_scale(o - t);
-    ref = t;
-  }
+  for (int m = 16; m >= 1; m >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
+  sum = most > -INFINITY ? sum * bm_scale(ref - most) : 0.f;
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
   if (lane == 0) {
-    sm.ref[warp] = ref;
+    sm.ref[warp] = most;
     sm.sum[warp] = sum;
   }
   __syncthreads();
   if (tid == 0) {
-    for (int i = 1; i < kBmThreads / 32; ++i) ref = fmaxf(ref, sm.ref[i]);
+    float r[kBmThreads / 32], v[kBmThreads / 32];
+#pragma unroll
+    for (int i = 0; i < kBmThreads / 32; ++i) {
+      r[i] = sm.ref[i];
+      v[i] = sm.sum[i];
+      most = fmaxf(most, r[i]);
+    }
     double total = 0.0;
-    if (ref > -INFINITY)
-      for (int i = 0; i < kBmThreads / 32; ++i) total += sm.sum[i] * bm_scale(sm.ref[i] - ref);
-    stats[static_cast<size_t>(row) * slices + blockIdx.x] = {ref, static_cast<float>(total)};
+    if (most > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < kBmThreads / 32; ++i) total += v[i] * bm_scale(r[i] - most);
+    }
+    stats[static_cast<size_t>(row) * slices + blockIdx.x] = {most, static_cast<float>(total)};
   }
 }
 
@@ -426,6 +436,27 @@ struct MergeSmem {
   int count;
 };
 
+// ln(hi + lo) + n ln 2, hi >= 0 the larger part, to 1e-9 or so: with hi = 2^e m, m from
+// sqrt(1/2) to sqrt(2), and s = (m - 1) / (m + 1), ln m = 2 s + 2 s^3 / 3 + 2 s^5 / 5 + ...  s is kept as
+// a sum of two fp32, so that only the last steps need 64 bits (a log in 64 bits takes 1.5 us here).
+__device__ __forceinline__ double bm_log(float hi, float lo, float n) {
+  int e = static_cast<int>(__float_as_uint(hi) >> 23) - 127;
+  float m = __uint_as_float((__float_as_uint(hi) & 0x007FFFFFu) | 0x3F800000u);
+  if (m > 1.41421354f) {
+    m *= 0.5f;
+    ++e;
+  }
+  lo *= __int_as_float((127 - e) << 23);                // e from -1 to 60 or so here
+  const float f = m - 1.f, g = m + 1.f, g1 = (m - (g - 1.f)) + lo;   // f exact, m + 1 + lo = g + g1
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(g));
+  const float s = f * r;
+  const float s1 = (fmaf(-s, g, f) + lo - s * g1) * r;
+  const float q = s * s;
+  const float c = q * s * fmaf(q, fmaf(q, fmaf(q, fmaf(q, fmaf(q, 2.f / 13, 2.f / 11), 2.f / 9), 2.f / 7), 2.f / 5), 2.f / 3);
+  return (static_cast<double>(n) + e) * kBmLn2 + (static_cast<double>(2.f * s) + fmaf(2.f, s1, c));
+}
+
 // Bound that at least K candidates reach, from the best candidate of every thread.  At most
 // the K best groups (of 4 threads) hold anything at or above it.
 __device__ __forceinline__ void bm_bound(MergeSmem& sm, Cand top, int K) {
@@ -447,10 +478,9 @@ __device__ __forceinline__ void bm_bound(MergeSmem& sm, Cand top, int K) {
   }
   __syncthreads();
   int above = 0;
-  const int from = tid % kBmPer * (kBmGroups / kBmPer);
-#pragma unroll
-  for (int i = 0; i < kBmGroups / kBmPer; ++i)
-    above += beats(sm.gs[from + i], sm.gat[from + i], top.s, top.at);
+#pragma unroll 8
+  for (int i = tid % kBmPer; i < kBmGroups; i += kBmPer)      // side by side: no bank twice
+    above += beats(sm.gs[i], sm.gat[i], top.s, top.at);
 #pragma unroll
   for (int m = 1; m < kBmPer; m <<= 1) above += __shfl_xor_sync(0xffffffffu, above, m);
   if (above == K - 1 && top.s > 0 && tid % kBmPer == 0) {
@@ -483,22 +513,29 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
     const float s = scores[row];
     const bool live = s > -INFINITY;
     const bool ended = finished && finished[row];
-    float ref = mine.ref;
-    double sum = 0.0;
+    float ref = mine.ref, hi = 0.f, lo = 0.f;           // sum: hi + lo, times 2^ref
+    auto join = [&](float x, float x1) {
+      const float t = hi + x, d = t - hi;
+      lo += x1 + ((hi - (t - d)) + (x - d));
+      hi = t;
+    };
     if (live && !ended) {
       for (int i = lane + 32; i < slices; i += 32) ref = fmaxf(ref, st[i].ref);
 #pragma unroll
       for (int m = 16; m >= 1; m >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, m));
       if (ref > -INFINITY) {
-        sum = mine.sum * bm_scale(mine.ref - ref);
-        for (int i = lane + 32; i < slices; i += 32) sum += st[i].sum * bm_scale(st[i].ref - ref);
+        hi = mine.sum * bm_scale(mine.ref - ref);
+        for (int i = lane + 32; i < slices; i += 32) join(st[i].sum * bm_scale(st[i].ref - ref), 0.f);
       }
 #pragma unroll
-      for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+      for (int m = 16; m >= 1; m >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, hi, m);
+        join(x, __shfl_xor_sync(0xffffffffu, lo, m));
+      }
     }
     if (lane == 0) {
       sm.score[w] = live ? static_cast<double>(s) : -INFINITY;
-      sm.lse[w] = ended ? 0.0 : ref * kBmLn2 + log(sum);   // all masked: no candidates either
+      sm.lse[w] = ended || ref == -INFINITY ? 0.0 : bm_log(hi, lo, ref);   // no candidates: no matter
       sm.huge[w] = fabsf(ref) >= kBmHuge;
     }
   }
@@ -518,8 +555,9 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
     if (sm.huge[w]) x = fminf(fmaxf(x, -kBmHuge), kBmHuge);
     return {ordered(s + (static_cast<double>(x) - sm.lse[w])), ~(static_cast<uint32_t>(w) * V + v)};
   };
-  Cand top = {0, 0};
-  for (int i = tid; i < total; i += kBmMergeThreads) {
+  const Cand one = tid < total ? get(tid) : Cand{0, 0};
+  Cand top = one;
+  for (int i = tid + kBmMergeThreads; i < total; i += kBmMergeThreads) {
     const Cand c = get(i);
     if (beats(c.s, c.at, top.s, top.at)) top = c;
   }
@@ -529,7 +567,7 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
     const uint32_t ba = sm.bound_at;
     if (!beats(bs, ba, top.s, top.at))
       for (int i = tid; i < total; i += kBmMergeThreads) {
-        const Cand c = get(i);
+        const Cand c = i == tid ? one : get(i);
         if (!beats(bs, ba, c.s, c.at)) {
           const int at = atomicAdd(&sm.count, 1);
           sm.s[at] = c.s;

@@ -117,28 +117,29 @@ constexpr float kPlTail = 0.3f;          // of a row's longest item: what others
 // workspace: one item per node and tile.)
 __device__ __forceinline__ int pl_alone(int L) { return L < 512 ? min(L, 24) : L; }
 
-// Exclusive scan over the CTA; *total = the sum
-__device__ __forceinline__ int pl_scan(int v, int* warp_sums, int* total) {
+// Exclusive scans over the CTA of two values at a time; total = the sums
+__device__ __forceinline__ int2 pl_scan(int2 v, int2* warp_sums, int2* total) {
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-  int x = v;
+  auto warp_scan = [&](int2 x) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
-  }
+    for (int d = 1; d < 32; d <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, x.x, d), b = __shfl_up_sync(0xffffffffu, x.y, d);
+      if (lane >= d) {
+        x.x += a;
+        x.y += b;
+      }
+    }
+    return x;
+  };
+  const int2 x = warp_scan(v);
   if (lane == 31) warp_sums[wp] = x;
   __syncthreads();
-  int w = warp_sums[lane];                 // every warp sums the warps for itself
-  const int own = w;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, w, d);
-    if (lane >= d) w += y;
-  }
-  *total = __shfl_sync(0xffffffffu, w, 31);
-  const int before = __shfl_sync(0xffffffffu, w - own, wp);
+  const int2 own = warp_sums[lane];        // every warp sums the warps for itself
+  const int2 w = warp_scan(own);
+  *total = make_int2(__shfl_sync(0xffffffffu, w.x, 31), __shfl_sync(0xffffffffu, w.y, 31));
+  const int bx = __shfl_sync(0xffffffffu, w.x - own.x, wp), by = __shfl_sync(0xffffffffu, w.y - own.y, wp);
   __syncthreads();                         // warp_sums may be used again
-  return before + x - v;
+  return make_int2(bx + x.x - v.x, by + x.y - v.y);
 }
 
 // ceil(pages / L) with 1 / L at hand: (x + 1/2) / L stays 1 / 2048 away from whole numbers,
@@ -157,7 +158,8 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
     int max_pages, int sms, SaPlan plan, uint32_t* status) {
   pdl_enter();
   extern __shared__ int smem_i[];
-  __shared__ int warp_sums[kPlWarps];
+  __shared__ int2 warp_sums[kPlWarps];
+  __shared__ int longest_run, short_items;
   __shared__ float cost[kPlLengths];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int* row_of = smem_i;                    // live rows
@@ -191,15 +193,16 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       }
       if (L == 0) plan.n_segs[b] = 0;
     }
-    int total;
-    const int at = n + pl_scan(L > 0, warp_sums, &total);
+    int2 total;
+    const int at = n + pl_scan(make_int2(L > 0, 0), warp_sums, &total).x;
     if (L > 0) {
       row_of[at] = b;
       len_of[at] = L;
       plan.live[at] = b;
     }
-    n += total;
+    n += total.x;
   }
+  if (tid == 0) longest_run = short_items = 0;
   __syncthreads();
   for (int i = tid; i < n; i += kPlThreads)
     common[i] = i + 1 < n ? min(len_of[i], len_of[i + 1]) / kBlock : 0;
@@ -299,56 +302,71 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   // ---- nodes: the runs of the first levels (deeper ones are not shared), then the rows
   // alone with the columns that are left
   const int tile_rows = 128 / G;           // token rows of a tile
-  int nodes = 0;
-  for (int half = 0; half < 2; ++half)
+  int runs = 0, alone = 0;                 // nodes of either kind; first the runs
+  for (int k = tid; k < n; k += kPlThreads) {
+    int p = leaf_up[k];
+    while (p >= 0 && depth[p] >= kSaLevels) p = parent[p];
+    leaf_up[k] = p;
+  }
+  for (int pass = 0; pass < 2; ++pass) {   // count the runs, then place both kinds
+    if (pass == 0 && n <= kPlThreads) continue;          // one round: the scan tells it
+    int at_run = 0, at_alone = 0;
     for (int k0 = 0; k0 < n; k0 += kPlThreads) {
       const int k = k0 + tid;
-      int v0 = 0, pages = 0, i0 = k, m = 1;
+      int v0 = 0, pages = 0, v1 = 0, pages1 = 0;
       if (k < n) {
-        if (half == 0) {
-          if (rows[k] > 0 && depth[k] < kSaLevels) {
-            v0 = parent[k] >= 0 ? common[parent[k]] : 0;
-            pages = common[k] - v0;
-            i0 = first[k];
-            m = rows[k];
-          }
-        } else {
-          int p = leaf_up[k];
-          while (p >= 0 && depth[p] >= kSaLevels) p = parent[p];
-          leaf_up[k] = p;
-          v0 = p >= 0 ? common[p] : 0;
-          pages = (len_of[k] + kBlock - 1) / kBlock - v0;
+        if (rows[k] > 0 && depth[k] < kSaLevels) {
+          v0 = parent[k] >= 0 ? common[parent[k]] : 0;
+          pages = common[k] - v0;
+        }
+        v1 = leaf_up[k] >= 0 ? common[leaf_up[k]] : 0;
+        pages1 = (len_of[k] + kBlock - 1) / kBlock - v1;
+      }
+      int2 total;
+      const int2 sc = pl_scan(make_int2(pages > 0, pages1 > 0), warp_sums, &total);
+      if (n <= kPlThreads) runs = total.x;
+      if (pass == 1 && k < n) {
+        auto put = [&](int at, int first_col, int cols, int i0, int m) {
+          nd_v0[at] = first_col;
+          nd_pages[at] = cols;
+          nd_i0[at] = i0;
+          nd_m[at] = m;
+          nd_tiles[at] = (m + 2 * tile_rows - 1) / (2 * tile_rows);
+          atomicAdd(&short_items, cols * nd_tiles[at]);
+        };
+        nd_of[k] = nd_of[B + k] = -1;
+        if (pages > 0) {
+          nd_of[k] = at_run + sc.x;
+          put(nd_of[k], v0, pages, first[k], rows[k]);
+          atomicMax(&longest_run, pages);
+        }
+        if (pages1 > 0) {
+          nd_of[B + k] = runs + at_alone + sc.y;
+          put(nd_of[B + k], v1, pages1, k, 1);
         }
       }
-      int total;
-      const int at = nodes + pl_scan(pages > 0, warp_sums, &total);
-      if (k < n) nd_of[half * B + k] = pages > 0 ? at : -1;
-      if (pages > 0) {
-        nd_v0[at] = v0;
-        nd_pages[at] = pages;
-        nd_i0[at] = i0;
-        nd_m[at] = m;
-        nd_tiles[at] = (m + 2 * tile_rows - 1) / (2 * tile_rows);
-      }
-      nodes += total;
+      at_run += total.x;
+      at_alone += total.y;
     }
+    runs = at_run;
+    alone = at_alone;
+  }
+  const int nodes = runs + alone;
   __syncthreads();
   // ---- item length: a warp weighs a candidate.  Either all items' costs shared by the CTAs
   // and a part of a row's item at the end, or the rounds that the runs' long items take,
   // whichever is more (in a round that is not full, items are 0.6 as long: the CTAs at work
   // have more of the memory's bandwidth each).
-  for (int c = warp; c < kPlLengths; c += kPlWarps) {
+  // (Where items of one page fit a round, they are the shortest.)
+  const bool one_page = static_cast<long long>(short_items) * Hkv <= sms;
+  for (int c = warp; c < kPlLengths && !one_page; c += kPlWarps) {
     const int L = kPlLength[c];
     const int L1 = pl_alone(L);
     const float inv = 1.f / static_cast<float>(L), inv1 = 1.f / static_cast<float>(L1);
-    float sum = 0.f, run = 0.f, alone = 0.f, long_sum = 0.f;
-    int items = 0, long_items = 0, most = 0;
+    float sum = 0.f, run = 0.f, single = 0.f, long_sum = 0.f;
+    int items = 0, long_items = 0;
     long long parts = 0;
-    for (int k = lane; k < nodes; k += 32)
-      if (nd_m[k] > 1) most = max(most, nd_pages[k]);
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-    most = min(most, L);
+    const int most = min(longest_run, L);
     for (int k = lane; k < nodes; k += 32) {
       const int pages = nd_pages[k], m = nd_m[k];
       const int ns = m > 1 ? pl_splits(pages, L, inv) : pl_splits(pages, L1, inv1);
@@ -361,7 +379,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       items += each;
       parts += static_cast<long long>(m) * G * ns * Hkv;
       if (m == 1) {
-        alone = fmaxf(alone, per);
+        single = fmaxf(single, per);
       } else {
         run = fmaxf(run, per);
         if (2 * pages > most * ns) {
@@ -373,14 +391,16 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) {
       sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      run = fmaxf(run, __shfl_xor_sync(0xffffffffu, run, d));
-      alone = fmaxf(alone, __shfl_xor_sync(0xffffffffu, alone, d));
       long_sum += __shfl_xor_sync(0xffffffffu, long_sum, d);
-      items += __shfl_xor_sync(0xffffffffu, items, d);
-      long_items += __shfl_xor_sync(0xffffffffu, long_items, d);
-      parts += __shfl_xor_sync(0xffffffffu, parts, d);
     }
-    float time = fmaxf(run, alone);
+    // maxima of numbers that are not negative, as integers; parts capped so that the sum fits
+    run = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(run)));
+    single = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(single)));
+    items = __reduce_add_sync(0xffffffffu, items);
+    long_items = __reduce_add_sync(0xffffffffu, long_items);
+    const uint32_t all_parts =
+        __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(parts < (1 << 26) ? parts : (1 << 26)));
+    float time = fmaxf(run, single);
     if (items > sms) {
       float rounds_time = run;
       if (long_items > sms) {
@@ -388,14 +408,14 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
         const float last = x > full ? fmaxf(x - full, 0.6f) : 0.f;
         rounds_time = long_sum / long_items * (full + last);
       }
-      time = fmaxf(sum / sms + kPlTail * alone, rounds_time);
+      time = fmaxf(sum / sms + kPlTail * single, rounds_time);
     }
     if (lane == 0)
-      cost[c] = items <= plan.max_items && parts <= plan.max_parts ? time : INFINITY;
+      cost[c] = items <= plan.max_items && all_parts <= static_cast<uint32_t>(plan.max_parts) ? time : INFINITY;
   }
   __syncthreads();
-  int best = lane;
-  {
+  int best = one_page ? 0 : lane;
+  if (!one_page) {
     float t = cost[lane];
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) {
@@ -422,15 +442,14 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       items = nd_tiles[k] * ns * Hkv;
       parts = nd_m[k] * G * ns * Hkv;
     }
-    int total_i, total_p;
-    const int it = n_items + pl_scan(items, warp_sums, &total_i);
-    const int pt = n_parts + pl_scan(parts, warp_sums, &total_p);
+    int2 total;
+    const int2 at = pl_scan(make_int2(items, parts), warp_sums, &total);
     if (k < nodes) {
-      nd_item[k] = it;
-      nd_part[k] = pt;
+      nd_item[k] = n_items + at.x;
+      nd_part[k] = n_parts + at.y;
     }
-    n_items += total_i;
-    n_parts += total_p;
+    n_items += total.x;
+    n_parts += total.y;
   }
   n_items = min(n_items, plan.max_items);
   if (tid == 0) {
@@ -540,14 +559,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ table, int G, int Hkv, int num_pages, int max_pages, float sl2,
     float rescale, const SaPlan plan, uint32_t* status) {
-  pdl_enter();
-  const int n_items = plan.counts[0];
-  if (static_cast<int>(blockIdx.x) >= n_items) return;    // as many items are claimed by the others
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  if (smem_u32(smem_raw) & 1023u) {                       // the tiles need 1024-byte alignment
-    if (threadIdx.x == 0) atomicOr(status, kStatusBounds);
-    return;
-  }
   SaSmem& sm = *reinterpret_cast<SaSmem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hq = G * Hkv, tile_rows = 128 / G;
@@ -576,17 +588,25 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
     tmem_alloc(&sm.tmem_base, 512);
     tmem_relinquish();
   }
+  if (tid == 0) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  // All that needed nothing of the plan: the kernel that makes it runs meanwhile (it uses no
+  // TMEM, and what came before it has ended, so that no CTA waits for the columns taken here).
+  pdl_enter();
+  const bool aligned = (smem_u32(smem_raw) & 1023u) == 0;  // the tiles need it
+  if (!aligned && tid == 0) atomicOr(status, kStatusBounds);
+  const int n_items = aligned ? plan.counts[0] : 0;
+  // CTAs beyond the items have nothing to do: the others claim as many
 
-  if (warp == 0) {
+  if (static_cast<int>(blockIdx.x) >= n_items) {
+  } else if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      prefetch_tmap(&tm_k);
-      prefetch_tmap(&tm_v);
-    }
     // The next item is claimed, read, checked and published in steps between the last pages
     // of the current one, so that their latencies (an atomic, the item, its table entries) pass
     // while pages are on the way, and q is there when the item's turn comes.  Not earlier:
@@ -978,57 +998,88 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
 
 // ---------------------------------------------------------------- combine
 
-// grid (rows, KV heads, shares of the G heads); thread (d4, head): heads run fastest, as the
-// parts lie in memory
-__global__ void __launch_bounds__(512) shared_combine_kernel(const SaPlan plan, int G, int Hkv, float sl2,
-                                                             __nv_bfloat16* __restrict__ o,
-                                                             float* __restrict__ lse) {
+// grid (rows, KV heads, shares of Gc heads); thread (way, d4, head): heads run fastest, as the
+// parts lie in memory, and the ways take every so many-th part.  Bound by latency (the row's
+// list, then its parts, 8 per thread in flight), so the list is read at once, by whoever
+// is there first.
+constexpr int kCbThreads = 512, kCbDeep = 8;
+
+__global__ void __launch_bounds__(kCbThreads) shared_combine_kernel(const SaPlan plan, int G, int Hkv, int Gc,
+                                                                    int ways, float sl2,
+                                                                    __nv_bfloat16* __restrict__ o,
+                                                                    float* __restrict__ lse) {
   pdl_enter();
-  const int b = blockIdx.x, g = blockIdx.y, Gc = blockDim.x / 32;
-  const int h = blockIdx.z * Gc + threadIdx.x % Gc, d4 = threadIdx.x / Gc;
-  if (h >= G) return;
-  const int ns = plan.n_segs[b];
+  __shared__ SaSeg seg[kSaMaxSegs];
+  __shared__ int n_seg;
+  __shared__ float4 part[kCbThreads];
+  __shared__ float2 part_ml[kCbThreads];
+  const int b = blockIdx.x, g = blockIdx.y, tid = threadIdx.x;
+  if (tid < kSaMaxSegs) seg[tid] = plan.segs[static_cast<size_t>(b) * kSaMaxSegs + tid];
+  if (tid == kSaMaxSegs) n_seg = plan.n_segs[b];
+  const int h = blockIdx.z * Gc + tid % Gc, d4 = tid / Gc % 32, way = tid / (32 * Gc);
+  __syncthreads();
+  const int ns = n_seg;
+  int total = 0;
+  for (int k = 0; k < ns; ++k) total += seg[k].splits;
   float M = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = 0; k < ns; ++k) {
-    const SaSeg sg = plan.segs[static_cast<size_t>(b) * kSaMaxSegs + k];
-    const size_t rows = static_cast<size_t>(sg.m) * G, at = static_cast<size_t>(sg.ro) * G + h;
-    constexpr int kDeep = 8;               // parts whose loads are in flight together
-    for (int s0 = 0; s0 < sg.splits; s0 += kDeep) {
-      float2 ml[kDeep];
-      float4 x[kDeep];
+  if (h < G) {
+    int k = 0, s = way;                      // next part: split s of segment k
+    for (int p = way; p < total; p += ways * kCbDeep) {
+      float2 ml[kCbDeep];
+      float4 x[kCbDeep];
 #pragma unroll
-      for (int s = 0; s < kDeep; ++s) {
-        ml[s] = make_float2(-INFINITY, 0.f);
-        if (s0 + s < sg.splits) {
-          const size_t base = sg.base + (static_cast<size_t>(s0 + s) * Hkv + g) * rows;
-          ml[s] = plan.part_ml[base + at];
-          x[s] = plan.part_o[base * 32 + d4 * rows + at];
-        }
+      for (int i = 0; i < kCbDeep; ++i) {
+        ml[i] = make_float2(-INFINITY, 0.f);
+        if (p + i * ways >= total) continue;
+        while (s >= seg[k].splits) s -= seg[k++].splits;
+        const size_t rows = static_cast<size_t>(seg[k].m) * G, at = static_cast<size_t>(seg[k].ro) * G + h;
+        const size_t base = seg[k].base + (static_cast<size_t>(s) * Hkv + g) * rows;
+        ml[i] = plan.part_ml[base + at];
+        x[i] = plan.part_o[base * 32 + d4 * rows + at];
+        s += ways;
       }
       float top = M;
 #pragma unroll
-      for (int s = 0; s < kDeep; ++s) top = fmaxf(top, ml[s].x);
+      for (int i = 0; i < kCbDeep; ++i) top = fmaxf(top, ml[i].x);
       if (top == -INFINITY) continue;
       const float f = M == -INFINITY ? 0.f : sa_ex2((M - top) * sl2);
       acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
       l *= f;
       M = top;
 #pragma unroll
-      for (int s = 0; s < kDeep; ++s) {
-        if (ml[s].x == -INFINITY) continue;
-        const float e = sa_ex2((ml[s].x - top) * sl2);
-        acc.x = fmaf(x[s].x, e, acc.x);
-        acc.y = fmaf(x[s].y, e, acc.y);
-        acc.z = fmaf(x[s].z, e, acc.z);
-        acc.w = fmaf(x[s].w, e, acc.w);
-        l = fmaf(ml[s].y, e, l);
+      for (int i = 0; i < kCbDeep; ++i) {
+        if (ml[i].x == -INFINITY) continue;
+        const float e = sa_ex2((ml[i].x - top) * sl2);
+        acc.x = fmaf(x[i].x, e, acc.x);
+        acc.y = fmaf(x[i].y, e, acc.y);
+        acc.z = fmaf(x[i].z, e, acc.z);
+        acc.w = fmaf(x[i].w, e, acc.w);
+        l = fmaf(ml[i].y, e, l);
       }
     }
   }
+  if (ways > 1 && total > 1) {               // uniform
+    part[tid] = acc;
+    part_ml[tid] = make_float2(M, l);
+    __syncthreads();
+    if (way == 0) {
+      for (int w = 1; w < ways; ++w) {
+        const float2 ml = part_ml[tid + w * 32 * Gc];
+        const float4 x = part[tid + w * 32 * Gc];
+        if (ml.x == -INFINITY) continue;
+        const float top = fmaxf(M, ml.x), f = M == -INFINITY ? 0.f : sa_ex2((M - top) * sl2);
+        const float e = sa_ex2((ml.x - top) * sl2);
+        acc = make_float4(fmaf(x.x, e, acc.x * f), fmaf(x.y, e, acc.y * f), fmaf(x.z, e, acc.z * f),
+                          fmaf(x.w, e, acc.w * f));
+        l = fmaf(ml.y, e, l * f);
+        M = top;
+      }
+    }
+  }
+  if (way > 0 || h >= G) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const size_t at = (static_cast<size_t>(b) * Hkv + g) * G + h;
-  if (M == -INFINITY) acc = make_float4(0.f, 0.f, 0.f, 0.f);
   *reinterpret_cast<uint2*>(o + at * kD + 4 * d4) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   if (lse && d4 == 0) lse[at] = M == -INFINITY ? -INFINITY : fmaf(M, sl2, log2f(l)) * 0.6931471805599453f;
@@ -1135,9 +1186,13 @@ msa_status_t msa_decode_shared(const void* q, const void* k_cache, const void* v
   MSA_TRY(check_launch("shared_attn_kernel"));
   {
     TraceScope trace_("shared_combine_kernel", st);
-    const int Gc = G < 16 ? G : 16;
-    launch_pdl(shared_combine_kernel, dim3(B, Hkv, (G + Gc - 1) / Gc), 32 * Gc, 0, st, plan, G, Hkv, scale * kSaLog2e,
-               static_cast<__nv_bfloat16*>(o), lse);
+    // few rows: 8 heads per CTA and up to 4 ways, so that more parts are in flight; many: the
+    // ways only cost (64 rows x 64 heads: 9.5 us with one, 13 with two)
+    const bool few = static_cast<long long>(B) * Hq <= 16LL * sms;
+    const int most = few ? 8 : 16, Gc = G < most ? G : most, fit = kCbThreads / (32 * Gc);
+    const int ways = !few ? 1 : (fit < 4 ? fit : 4);
+    launch_pdl(shared_combine_kernel, dim3(B, Hkv, (G + Gc - 1) / Gc), 32 * Gc * ways, 0, st, plan, G, Hkv, Gc,
+               ways, scale * kSaLog2e, static_cast<__nv_bfloat16*>(o), lse);
   }
   return check_launch("shared_combine_kernel");
 }
