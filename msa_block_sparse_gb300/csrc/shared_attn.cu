@@ -101,21 +101,24 @@ constexpr int kPlThreads = 1024;
 constexpr int kPlWarps = kPlThreads / 32;
 constexpr int kPlLengths = 32;
 constexpr int kPlRowInts = 9, kPlNodeInts = 8;    // of the dynamic shared memory, per row and node
-// Candidate item lengths in pages
-__constant__ int kPlLength[kPlLengths] = {1,  2,  3,  4,  5,  6,  7,   8,   10,  12,  14,
-                                          16, 20, 24, 28, 32, 40, 48,  56,  64,  80,  96,
-                                          112, 128, 160, 192, 256, 320, 384, 512, 768, 1024};
-// Costs in pages of a narrow item (what the memory takes for 64 KB per SM, 1.47 us with all
-// SMs at it), from runs over item lengths: a page of a wide item 1.5 to 1.65 us; start and
-// end of an item, as far as no pages stream meanwhile; a query row's part, written and read
-constexpr float kPlWide = 1.1f;
-constexpr float kPlStart = 1.5f, kPlWideStart = 3.5f;
-constexpr float kPlPart = 1.f / 48.f;
-constexpr float kPlTail = 0.3f;          // of a row's longest item: what others wait for at the end
-// Runs come first and may be long (their parts are what costs); a row alone is cut shorter, so
-// that its items fill what the runs leave.  (Not with the last lengths, which always fit the
-// workspace: one item per node and tile.)
-__device__ __forceinline__ int pl_alone(int L) { return L < 512 ? min(L, 24) : L; }
+// Candidate item lengths in pages: of runs, and of rows alone, which are cut shorter (their
+// items fill what the runs leave, and their parts are small).  The last ones always fit the
+// workspace: one item per node and tile.
+constexpr int kPlCuts = kPlLengths / 2;
+__constant__ int kPlCut[kPlCuts] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128, 256, 1024};
+__device__ __forceinline__ int2 pl_length(int c) {
+  const int L = kPlCut[c >> 1];
+  return make_int2(L, L < 512 ? min(L, c & 1 ? 8 : 24) : L);
+}
+// Times in us, from traces and from runs over item lengths: a page in a narrow and a wide item,
+// an item's start and end as far as no page passes; of the whole GPU: a query row's part
+// (written, joined), 64 KB of K and V from memory
+constexpr float kPlNarrow = 1.07f, kPlWide = 1.7f;
+constexpr float kPlStart = 2.2f, kPlWideStart = 4.5f;
+constexpr float kPlPart = 0.00022f;
+constexpr float kPlMemory = 0.0099f;
+constexpr float kPlTail = 0.12f;         // of a row's longest item: what others wait for at the end
+constexpr int kPlLong = 8;               // rows alone with as many pages come before the others
 
 // Exclusive scans over the CTA of two values at a time; total = the sums
 __device__ __forceinline__ int2 pl_scan(int2 v, int2* warp_sums, int2* total) {
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   // ---- nodes: the runs of the first levels (deeper ones are not shared), then the rows
   // alone with the columns that are left
   const int tile_rows = 128 / G;           // token rows of a tile
-  int runs = 0, alone = 0;                 // nodes of either kind; first the runs
+  int runs = 0, longs = 0, alone = 0;      // nodes: the runs, then rows alone, long ones first
   for (int k = tid; k < n; k += kPlThreads) {
     int p = leaf_up[k];
     while (p >= 0 && depth[p] >= kSaLevels) p = parent[p];
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   }
   for (int pass = 0; pass < 2; ++pass) {   // count the runs, then place both kinds
     if (pass == 0 && n <= kPlThreads) continue;          // one round: the scan tells it
-    int at_run = 0, at_alone = 0;
+    int at_run = 0, at_long = 0, at_alone = 0;
     for (int k0 = 0; k0 < n; k0 += kPlThreads) {
       const int k = k0 + tid;
       int v0 = 0, pages = 0, v1 = 0, pages1 = 0;
@@ -323,8 +326,12 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
         pages1 = (len_of[k] + kBlock - 1) / kBlock - v1;
       }
       int2 total;
-      const int2 sc = pl_scan(make_int2(pages > 0, pages1 > 0), warp_sums, &total);
-      if (n <= kPlThreads) runs = total.x;
+      const bool is_long = pages1 >= kPlLong;
+      const int2 sc = pl_scan(make_int2((pages > 0) | (is_long << 16), pages1 > 0 && !is_long), warp_sums, &total);
+      if (n <= kPlThreads) {
+        runs = total.x & 0xFFFF;
+        longs = total.x >> 16;
+      }
       if (pass == 1 && k < n) {
         auto put = [&](int at, int first_col, int cols, int i0, int m) {
           nd_v0[at] = first_col;
@@ -336,46 +343,48 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
         };
         nd_of[k] = nd_of[B + k] = -1;
         if (pages > 0) {
-          nd_of[k] = at_run + sc.x;
+          nd_of[k] = at_run + (sc.x & 0xFFFF);
           put(nd_of[k], v0, pages, first[k], rows[k]);
           atomicMax(&longest_run, pages);
         }
         if (pages1 > 0) {
-          nd_of[B + k] = runs + at_alone + sc.y;
+          nd_of[B + k] = is_long ? runs + at_long + (sc.x >> 16) : runs + longs + at_alone + sc.y;
           put(nd_of[B + k], v1, pages1, k, 1);
         }
       }
-      at_run += total.x;
+      at_run += total.x & 0xFFFF;
+      at_long += total.x >> 16;
       at_alone += total.y;
     }
     runs = at_run;
+    longs = at_long;
     alone = at_alone;
   }
-  const int nodes = runs + alone;
+  const int nodes = runs + longs + alone;
   __syncthreads();
-  // ---- item length: a warp weighs a candidate.  Either all items' costs shared by the CTAs
-  // and a part of a row's item at the end, or the rounds that the runs' long items take,
-  // whichever is more (in a round that is not full, items are 0.6 as long: the CTAs at work
-  // have more of the memory's bandwidth each).
-  // (Where items of one page fit a round, they are the shortest.)
+  // ---- item lengths: a warp weighs a candidate.  The SMs' share of all items' times, or the
+  // memory's, and a part of a row's item at the end; or the rounds that the runs' long items
+  // take, whichever is more (in a round that is not full, items are 0.6 as long: the CTAs at
+  // work have more of the memory's bandwidth each).  Where items of one page fit a round,
+  // they are the shortest.
   const bool one_page = static_cast<long long>(short_items) * Hkv <= sms;
   for (int c = warp; c < kPlLengths && !one_page; c += kPlWarps) {
-    const int L = kPlLength[c];
-    const int L1 = pl_alone(L);
-    const float inv = 1.f / static_cast<float>(L), inv1 = 1.f / static_cast<float>(L1);
-    float sum = 0.f, run = 0.f, single = 0.f, long_sum = 0.f;
+    const int2 L = pl_length(c);
+    const float inv = 1.f / static_cast<float>(L.x), inv1 = 1.f / static_cast<float>(L.y);
+    float sum = 0.f, run = 0.f, single = 0.f, long_sum = 0.f, memory = 0.f;
     int items = 0, long_items = 0;
     long long parts = 0;
-    const int most = min(longest_run, L);
+    const int most = min(longest_run, L.x);
     for (int k = lane; k < nodes; k += 32) {
       const int pages = nd_pages[k], m = nd_m[k];
-      const int ns = m > 1 ? pl_splits(pages, L, inv) : pl_splits(pages, L1, inv1);
+      const int ns = m > 1 ? pl_splits(pages, L.x, inv) : pl_splits(pages, L.y, inv1);
       const int each = nd_tiles[k] * ns * Hkv;
       const int nr = min(m, 2 * tile_rows);
       const bool wide = nr > tile_rows;
-      const float per = __fdividef((wide ? kPlWide : 1.f) * pages, static_cast<float>(ns)) +
-                        (wide ? kPlWideStart : kPlStart) + static_cast<float>(nr * G) * kPlPart;
+      const float per = __fdividef((wide ? kPlWide : kPlNarrow) * pages, static_cast<float>(ns)) +
+                        (wide ? kPlWideStart : kPlStart);
       sum += per * each;
+      memory += static_cast<float>(pages * Hkv) * kPlMemory;
       items += each;
       parts += static_cast<long long>(m) * G * ns * Hkv;
       if (m == 1) {
@@ -392,6 +401,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
     for (int d = 16; d >= 1; d >>= 1) {
       sum += __shfl_xor_sync(0xffffffffu, sum, d);
       long_sum += __shfl_xor_sync(0xffffffffu, long_sum, d);
+      memory += __shfl_xor_sync(0xffffffffu, memory, d);
     }
     // maxima of numbers that are not negative, as integers; parts capped so that the sum fits
     run = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(run)));
@@ -400,15 +410,16 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
     long_items = __reduce_add_sync(0xffffffffu, long_items);
     const uint32_t all_parts =
         __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(parts < (1 << 26) ? parts : (1 << 26)));
-    float time = fmaxf(run, single);
+    float time = fmaxf(run, single) + all_parts * kPlPart;
     if (items > sms) {
+      const float share = sum / sms, slow = fmaxf(1.f, memory / share);
       float rounds_time = run;
       if (long_items > sms) {
         const float x = static_cast<float>(long_items) / sms, full = floorf(x);
         const float last = x > full ? fmaxf(x - full, 0.6f) : 0.f;
         rounds_time = long_sum / long_items * (full + last);
       }
-      time = fmaxf(sum / sms + kPlTail * single, rounds_time);
+      time = slow * fmaxf(share + kPlTail * single, rounds_time) + all_parts * kPlPart;
     }
     if (lane == 0)
       cost[c] = items <= plan.max_items && all_parts <= static_cast<uint32_t>(plan.max_parts) ? time : INFINITY;
@@ -427,7 +438,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       }
     }
   }
-  const int L = kPlLength[best], L1 = pl_alone(L);
+  const int L = pl_length(best).x, L1 = pl_length(best).y;
   const float inv = 1.f / static_cast<float>(L), inv1 = 1.f / static_cast<float>(L1);
   auto splits = [&](int k) {
     return nd_m[k] > 1 ? pl_splits(nd_pages[k], L, inv) : pl_splits(nd_pages[k], L1, inv1);
