@@ -35,9 +35,8 @@ constexpr int kBmPieces = 32;                          // maxima that a thread k
 constexpr int kBmList = 1024;                          // pieces read again
 constexpr int kBmCandidates = 16384;                   // of a prompt, at most
 constexpr int kBmMergeThreads = 512;
-constexpr float kBmLog2eHi = 1.4426950216293335f;      // log2 e, and what fp32 leaves of it
-constexpr float kBmLog2eLo = 1.925963033500e-8f;
-constexpr double kBmLn2 = 0.69314718055994530942;
+constexpr float kBmLog2e = 1.4426950216293335f;        // log2 e in fp32, 1.33e-8 of it too small
+constexpr double kBmLn2 = 0.69314718055994530942, kBmRef = kBmLn2 * (1.4426950408889634 / 1.4426950216293335);
 constexpr float kBmHuge = 0x1p28f;                     // beyond: |x log2 e - ref| could overflow 2^127
 
 // Order of floats as order of unsigned integers (0: below -infinity, used for "nothing")
@@ -59,7 +58,9 @@ __device__ __forceinline__ unsigned long long key_of(float x, uint32_t idx) {
 }
 
 // Sum of e^x of a slice: sum * 2^ref, ref a whole number (-infinity: the sum is 0), so that
-// joining two sums rounds nothing but the addition
+// joining two sums rounds nothing but the addition.  Exponents are x times fp32's log2 e, whose
+// 1.33e-8 is put right for x = ref ln 2, from which the terms that count are a few away:
+// ref ln 2 (1 + 1.33e-8) stands for ref.
 struct BeamScan {
   float ref, sum;
 };
@@ -223,9 +224,18 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
   float top = -INFINITY, piece = -INFINITY;              // maxima: of all, of `per` tiles
   if (tid == 0) sm.count = sm.pieces = 0;
   uint4 raw[kVecs];
+  // tiles that lie within the slice and the row, but for the vectors at the row's ends
+  const int whole_lo = skew > 0 ? 1 : 0, whole_hi = min(v1, (skew + V) / L::kN);
   auto load_tile = [&](int t) {
+    const int v = v0 + t * kTile;
+    if (v >= whole_lo && v + kTile <= whole_hi) {
+      const uint4* p = reinterpret_cast<const uint4*>(xa + static_cast<size_t>(v) * L::kN) + tid;
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) raw[u] = load(v0 + t * kTile + u * kBmThreads + tid);
+      for (int u = 0; u < kVecs; ++u) raw[u] = __ldcs(p + u * kBmThreads);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) raw[u] = load(v + u * kBmThreads + tid);
+    }
   };
   auto place = [&](int t, int i) -> uint32_t {           // value i of this thread and tile t
     return static_cast<uint32_t>((v0 + t * kTile + (i / L::kN) * kBmThreads + tid) * L::kN + i % L::kN - skew);
@@ -244,8 +254,8 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
       best = fmaxf(val[0], val[1]);
 #pragma unroll
       for (int i = 2; i < kBmValues; i += 2) best = max3f(best, val[i], val[i + 1]);
-      to = fmaxf(ref, rintf(fminf(fmaxf(best, -most), most) * kBmLog2eHi));
-      const float2 hi = make_float2(kBmLog2eHi, kBmLog2eHi), lo = make_float2(kBmLog2eLo, kBmLog2eLo);
+      to = fmaxf(ref, rintf(fminf(fmaxf(best, -most), most) * kBmLog2e));
+      const float2 hi = make_float2(kBmLog2e, kBmLog2e);
       const float2 r = make_float2(-to, -to);
       float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -255,7 +265,7 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
           x.x = x.x > -INFINITY ? fminf(fmaxf(x.x, -most), most) : x.x;
           x.y = x.y > -INFINITY ? fminf(fmaxf(x.y, -most), most) : x.y;
         }
-        const float2 y = __ffma2_rn(x, lo, __ffma2_rn(x, hi, r));
+        const float2 y = __ffma2_rn(x, hi, r);
         acc[(i >> 1) & 1] = __fadd2_rn(acc[(i >> 1) & 1], make_float2(bm_ex2(y.x), bm_ex2(y.y)));
       }
       const float2 a = __fadd2_rn(acc[0], acc[1]);
@@ -268,7 +278,8 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
       scan(kBmHuge);
     }
     if (best > -INFINITY) {
-      sum = (ref > -INFINITY ? sum * bm_scale(ref - to) : 0.f) + part;
+      if (to != ref) sum = ref > -INFINITY ? sum * bm_scale(ref - to) : 0.f;
+      sum += part;
       ref = to;
     }
     piece = fmaxf(piece, best);
@@ -436,7 +447,7 @@ struct MergeSmem {
   int count;
 };
 
-// ln(hi + lo) + n ln 2, hi >= 0 the larger part, to 1e-9 or so: with hi = 2^e m, m from
+// ln(hi + lo) + n ln 2 (see BeamScan), hi >= 0 the larger part, to 1e-9 or so: with hi = 2^e m, m from
 // sqrt(1/2) to sqrt(2), and s = (m - 1) / (m + 1), ln m = 2 s + 2 s^3 / 3 + 2 s^5 / 5 + ...  s is kept as
 // a sum of two fp32, so that only the last steps need 64 bits (a log in 64 bits takes 1.5 us here).
 __device__ __forceinline__ double bm_log(float hi, float lo, float n) {
@@ -454,7 +465,7 @@ __device__ __forceinline__ double bm_log(float hi, float lo, float n) {
   const float s1 = (fmaf(-s, g, f) + lo - s * g1) * r;
   const float q = s * s;
   const float c = q * s * fmaf(q, fmaf(q, fmaf(q, fmaf(q, fmaf(q, 2.f / 13, 2.f / 11), 2.f / 9), 2.f / 7), 2.f / 5), 2.f / 3);
-  return (static_cast<double>(n) + e) * kBmLn2 + (static_cast<double>(2.f * s) + fmaf(2.f, s1, c));
+  return n * kBmRef + e * kBmLn2 + (static_cast<double>(2.f * s) + fmaf(2.f, s1, c));
 }
 
 // Bound that at least K candidates reach, from the best candidate of every thread.  At most

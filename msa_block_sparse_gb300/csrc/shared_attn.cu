@@ -97,8 +97,7 @@ __device__ __forceinline__ void umma_tmem_a(uint32_t d, uint32_t a, uint64_t b, 
 
 namespace {
 
-constexpr int kPlThreads = 1024;
-constexpr int kPlWarps = kPlThreads / 32;
+constexpr int kPlThreads = 1024;           // fewer for few rows, whose barriers then cost less
 constexpr int kPlLengths = 32;
 constexpr int kPlRowInts = 9, kPlNodeInts = 8;    // of the dynamic shared memory, per row and node
 // Candidate item lengths in pages: of runs, and of rows alone, which are cut shorter (their
@@ -137,7 +136,7 @@ __device__ __forceinline__ int2 pl_scan(int2 v, int2* warp_sums, int2* total) {
   const int2 x = warp_scan(v);
   if (lane == 31) warp_sums[wp] = x;
   __syncthreads();
-  const int2 own = warp_sums[lane];        // every warp sums the warps for itself
+  const int2 own = lane < static_cast<int>(blockDim.x) / 32 ? warp_sums[lane] : make_int2(0, 0);   // in every warp
   const int2 w = warp_scan(own);
   *total = make_int2(__shfl_sync(0xffffffffu, w.x, 31), __shfl_sync(0xffffffffu, w.y, 31));
   const int bx = __shfl_sync(0xffffffffu, w.x - own.x, wp), by = __shfl_sync(0xffffffffu, w.y - own.y, wp);
@@ -161,10 +160,11 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
     int max_pages, int sms, SaPlan plan, uint32_t* status) {
   pdl_enter();
   extern __shared__ int smem_i[];
-  __shared__ int2 warp_sums[kPlWarps];
+  __shared__ int2 warp_sums[kPlThreads / 32];
   __shared__ int longest_run, short_items;
   __shared__ float cost[kPlLengths];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int threads = blockDim.x, warps = threads / 32;
   int* row_of = smem_i;                    // live rows
   int* len_of = row_of + B;                // their lengths
   int* common = len_of + B;                // c_i
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
 
   // ---- rows with tokens
   int n = 0;
-  for (int b0 = 0; b0 < B; b0 += kPlThreads) {
+  for (int b0 = 0; b0 < B; b0 += threads) {
     const int b = b0 + tid;
     int L = 0;
     if (b < B) {
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   }
   if (tid == 0) longest_run = short_items = 0;
   __syncthreads();
-  for (int i = tid; i < n; i += kPlThreads)
+  for (int i = tid; i < n; i += threads)
     common[i] = i + 1 < n ? min(len_of[i], len_of[i + 1]) / kBlock : 0;
   __syncthreads();
   // ---- full pages that neighbours have in common: a warp per pair and 256 columns, which
@@ -241,10 +241,10 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       }
       if (at >= 0 && lane == 0) atomicMin(&common[t.i], at);
     };
-    for (int u = warp; u < units; u += 2 * kPlWarps) {   // two units' loads in flight
+    for (int u = warp; u < units; u += 2 * warps) {   // two units' loads in flight
       Unit p, q;
       load(p, u);
-      load(q, u + kPlWarps);
+      load(q, u + warps);
       look(p);
       look(q);
     }
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   __syncthreads();
   // ---- runs, a warp per boundary: the nearest boundaries with less on both sides; the
   // higher of the two values is where the run above ends
-  for (int i = warp; i < n; i += kPlWarps) {
+  for (int i = warp; i < n; i += warps) {
     const int v = common[i];               // the last row's is 0
     int l = -1, r = n - 1, rp = i, up = -1;
     if (v > 0) {
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
     }
   }
   __syncthreads();
-  for (int i = tid; i < n; i += kPlThreads) {
+  for (int i = tid; i < n; i += threads) {
     const int lv = i > 0 ? common[i - 1] : 0, rv = common[i];
     leaf_up[i] = lv > 0 || rv > 0 ? rep[lv >= rv ? i - 1 : i] : -1;
     int p = parent[i];
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
     parent[i] = p;
   }
   __syncthreads();
-  for (int i = tid; i < n; i += kPlThreads) {
+  for (int i = tid; i < n; i += threads) {
     int d = 0;
     if (rows[i] > 0)
       for (int p = parent[i]; p >= 0; p = parent[p]) ++d;
@@ -306,15 +306,15 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   // alone with the columns that are left
   const int tile_rows = 128 / G;           // token rows of a tile
   int runs = 0, longs = 0, alone = 0;      // nodes: the runs, then rows alone, long ones first
-  for (int k = tid; k < n; k += kPlThreads) {
+  for (int k = tid; k < n; k += threads) {
     int p = leaf_up[k];
     while (p >= 0 && depth[p] >= kSaLevels) p = parent[p];
     leaf_up[k] = p;
   }
   for (int pass = 0; pass < 2; ++pass) {   // count the runs, then place both kinds
-    if (pass == 0 && n <= kPlThreads) continue;          // one round: the scan tells it
+    if (pass == 0 && n <= threads) continue;          // one round: the scan tells it
     int at_run = 0, at_long = 0, at_alone = 0;
-    for (int k0 = 0; k0 < n; k0 += kPlThreads) {
+    for (int k0 = 0; k0 < n; k0 += threads) {
       const int k = k0 + tid;
       int v0 = 0, pages = 0, v1 = 0, pages1 = 0;
       if (k < n) {
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       int2 total;
       const bool is_long = pages1 >= kPlLong;
       const int2 sc = pl_scan(make_int2((pages > 0) | (is_long << 16), pages1 > 0 && !is_long), warp_sums, &total);
-      if (n <= kPlThreads) {
+      if (n <= threads) {
         runs = total.x & 0xFFFF;
         longs = total.x >> 16;
       }
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   // work have more of the memory's bandwidth each).  Where items of one page fit a round,
   // they are the shortest.
   const bool one_page = static_cast<long long>(short_items) * Hkv <= sms;
-  for (int c = warp; c < kPlLengths && !one_page; c += kPlWarps) {
+  for (int c = warp; c < kPlLengths && !one_page; c += warps) {
     const int2 L = pl_length(c);
     const float inv = 1.f / static_cast<float>(L.x), inv1 = 1.f / static_cast<float>(L.y);
     float sum = 0.f, run = 0.f, single = 0.f, long_sum = 0.f, memory = 0.f;
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   };
   // ---- first item and part of every node
   int n_items = 0, n_parts = 0;
-  for (int k0 = 0; k0 < nodes; k0 += kPlThreads) {
+  for (int k0 = 0; k0 < nodes; k0 += threads) {
     const int k = k0 + tid;
     int items = 0, parts = 0;
     if (k < nodes) {
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   }
   __syncthreads();
   // ---- items, a thread each; those of a node's tiles over the same pages side by side
-  for (int e = tid; e < n_items; e += kPlThreads) {
+  for (int e = tid; e < n_items; e += threads) {
     int lo = 0, hi = nodes;
     while (hi - lo > 1) {                  // last node whose first item is not behind e
       const int mid = (lo + hi) >> 1;
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
     item[2] = make_int4(row_of[i0], len_of[i0], 0, 0);
   }
   // ---- every row's parts: its own node, then the runs above
-  for (int i = tid; i < n; i += kPlThreads) {
+  for (int i = tid; i < n; i += threads) {
     SaSeg* out = plan.segs + static_cast<size_t>(row_of[i]) * kSaMaxSegs;
     int k = 0;
     auto add = [&](int nd) {
@@ -1184,7 +1184,7 @@ msa_status_t msa_decode_shared(const void* q, const void* k_cache, const void* v
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   {
     TraceScope trace_("shared_plan_kernel", st);
-    launch_pdl(shared_plan_kernel, 1, kPlThreads, plan_smem, st, block_table, cache_lens, B, G, Hkv,
+    launch_pdl(shared_plan_kernel, 1, B <= 16 ? 256 : kPlThreads, plan_smem, st, block_table, cache_lens, B, G, Hkv,
                max_pages, sms, plan, sw);
   }
   MSA_TRY(check_launch("shared_plan_kernel"));
