@@ -443,6 +443,7 @@ __global__ void __launch_bounds__(kHalf == 0 ? kRoThreads : kRoRowThreads)
     const int warp = blockIdx.x * (kRoThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int warps = gridDim.x * (kRoThreads / 32);
     reorder_put_aside<32>(a, warp, warps, lane, status);
+    __syncwarp();                              // the barrier below is a whole warp's
     // releases what every thread of the cluster wrote and has it seen by the others
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
     reorder_take<32>(a, warp, warps, lane, status);

@@ -893,6 +893,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               uint32_t v[32];
+              __syncwarp();
               tmem_ld32(d_o + c * 32, v);
               tmem_ld_wait();
 #pragma unroll
@@ -907,6 +908,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
             l = m == -INFINITY ? rs : (resc ? l * sa_ex2((m - mu) * sl2) : l) + rs;
             m = mu;
           }
+          __syncwarp();                        // the stores are the whole warp's
           tmem_st16(sbuf, pk);
           tmem_st16(sbuf + 16, pk + 16);
           tmem_st_wait();
@@ -968,6 +970,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
         for (int c = 0; c < (t.wide ? 8 : 4); ++c) {
           const int col = t.wide ? 16 * c : 64 * s + 16 * c;
           uint32_t x[16], y[16];
+          __syncwarp();                          // the loads are the whole warp's
           if (t.wide) {
             tmem_ld16(d_o + col, x);
           } else {
@@ -1001,6 +1004,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
       ++tc;
     }
   }
+  __syncwarp();                              // the lanes of a role join
   tc_fence_before();
   __syncthreads();
   __syncwarp();
