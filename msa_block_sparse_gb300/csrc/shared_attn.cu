@@ -218,8 +218,9 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       int i, j0, most, x[8], y[8];
     };
     auto load = [&](Unit& t, int u) {
-      t.i = chunks == 1 ? u : u / chunks;
-      t.j0 = (u - t.i * chunks) * 256;
+      const int chunk = chunks == 1 ? 0 : u / (n - 1);   // the first columns of all pairs first
+      t.i = u - chunk * (n - 1);
+      t.j0 = chunk * 256;
       t.most = u < units ? min(len_of[t.i], len_of[t.i + 1]) / kBlock : 0;
       if (t.j0 >= t.most) return;
       const int32_t* a = table + static_cast<size_t>(row_of[t.i]) * max_pages;
@@ -612,6 +613,9 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
   pdl_enter();
   const bool aligned = (smem_u32(smem_raw) & 1023u) == 0;  // the tiles need it
   if (!aligned && tid == 0) atomicOr(status, kStatusBounds);
+  // the first item is asked for together with their number (there is room for it in any case)
+  SaItem it, nx;
+  if (warp == 0) nx = plan.items[blockIdx.x];
   const int n_items = aligned ? plan.counts[0] : 0;
   // CTAs beyond the items have nothing to do: the others claim as many
 
@@ -625,7 +629,6 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
     // prompt 110 -> 125 us).
     uint32_t pos = 0, qt = 0, tc = 0;      // stages and q tiles used, items published
     bool alive = true;
-    SaItem it, nx;
     int id = 0, page = -1, nx_page = -1, valid = 0, step = 1;
     uint32_t ring_end = 0;                 // stages used when the published items are loaded
     auto entry = [&](const SaItem& t, int c) {
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
         if (lane == 0) id = atomicAdd(plan.counts + 1, 1);
       } else if (step == 1) {
         id = tc > 0 ? __shfl_sync(0xffffffffu, id, 0) : static_cast<int>(blockIdx.x);
-        if (id < n_items) nx = plan.items[id];
+        if (tc > 0 && id < n_items) nx = plan.items[id];
       } else if (step == 2) {
         if (id < n_items) nx_page = entry(nx, nx.c0 + lane);
       } else if (step == 3) {
