@@ -1018,11 +1018,11 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
 
 // grid (rows, KV heads, shares of Gc heads); thread (way, d4, head): heads run fastest, as the
 // parts lie in memory, and the ways take every so many-th part.  Bound by latency (the row's
-// list, then its parts, 8 per thread in flight), so the list is read at once, by whoever
+// list, then its parts, 6 per thread in flight), so the list is read at once, by whoever
 // is there first.
-constexpr int kCbThreads = 512, kCbDeep = 8;
+constexpr int kCbThreads = 512, kCbDeep = 6;
 
-__global__ void __launch_bounds__(kCbThreads) shared_combine_kernel(const SaPlan plan, int G, int Hkv, int Gc,
+__global__ void __launch_bounds__(kCbThreads, 2) shared_combine_kernel(const SaPlan plan, int G, int Hkv, int Gc,
                                                                     int ways, float sl2,
                                                                     __nv_bfloat16* __restrict__ o,
                                                                     float* __restrict__ lse) {
@@ -1204,10 +1204,10 @@ msa_status_t msa_decode_shared(const void* q, const void* k_cache, const void* v
   MSA_TRY(check_launch("shared_attn_kernel"));
   {
     TraceScope trace_("shared_combine_kernel", st);
-    // few rows: 8 heads per CTA and up to 4 ways, so that more parts are in flight; many: the
+    // few rows: 4 heads per CTA and 4 ways, so that more parts are in flight; many: the
     // ways only cost (64 rows x 64 heads: 9.5 us with one, 13 with two)
     const bool few = static_cast<long long>(B) * Hq <= 16LL * sms;
-    const int most = few ? 8 : 16, Gc = G < most ? G : most, fit = kCbThreads / (32 * Gc);
+    const int most = few ? 4 : 16, Gc = G < most ? G : most, fit = kCbThreads / (32 * Gc);
     const int ways = !few ? 1 : (fit < 4 ? fit : 4);
     launch_pdl(shared_combine_kernel, dim3(B, Hkv, (G + Gc - 1) / Gc), 32 * Gc * ways, 0, st, plan, G, Hkv, Gc,
                ways, scale * kSaLog2e, static_cast<__nv_bfloat16*>(o), lse);
