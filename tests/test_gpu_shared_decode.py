@@ -530,6 +530,38 @@ def test_beam_select_values_alike_and_in_order(m, dt, V, W, K):
     assert (dead[0] == -math.inf).all() and (dead[1] == -1).all() and (dead[2] == -1).all()
 
 
+@pytest.mark.parametrize("dt,V,more", [(torch.bfloat16, 300007, 1), (torch.float32, 160001, 3)])
+def test_beam_select_many_rows_of_a_large_vocabulary(m, dt, V, more):
+    """More rows than CTAs at a time: a CTA keeps one maximum for several tiles."""
+    W, N = 4, 170
+    g = torch.Generator(device=DEV).manual_seed(V)
+    x = torch.empty(N * W, V + more, device=DEV, dtype=dt).normal_(0, 3, generator=g)[:, :V]
+    scores = -torch.rand(N * W, generator=g, device=DEV)
+    so, po, to = m.msa_beam_select(x, scores, W, 9)
+    m.msa_check_status()
+    for n in (0, 77, N - 1):
+        s = slice(n * W, (n + 1) * W)
+        ws, wp, wt = S.beam_select(f64(x[s]), f64(scores[s]), W, 9)
+        within(f64(so[n:n + 1]), ws, 2.0 ** -20 + 2.0 ** -23 * np.abs(ws), "score")
+        near = np.abs(np.diff(ws)).min() < 2.0 ** -18       # no choice between scores as near as their errors
+        assert near or (np.array_equal(po[n:n + 1].cpu().numpy() - n * W, wp) and np.array_equal(to[n:n + 1].cpu().numpy(), wt))
+
+
+def test_beam_select_best_values_side_by_side(m):
+    """The K best of a row in one thread's hands, in one tile or one of each tile, and in falling order."""
+    V, W, K = 262144, 2, 64
+    base = torch.full((W, V), -20.0, device=DEV)
+    vec, tile = 4, 256 * 16                                   # fp32: values of a load, values of a tile
+    for where in ([8 * tile + 5 * vec + j + 1024 * u for u in range(4) for j in range(vec)] * 4,
+                  [t * tile + 77 * vec + j for t in range(16) for j in range(vec)],
+                  list(range(100000, 100064)), [V - 1 - i for i in range(64)]):
+        for order in (1.0, -1.0, 0.0):
+            x = base.clone()
+            at = torch.tensor(sorted(set(where)), device=DEV)
+            x[:, at] = 5 + order * 0.125 * torch.arange(len(at), device=DEV)
+            beam_check(m, x, torch.tensor([-1.0, -1.0], device=DEV), W, K)
+
+
 def test_beam_select_beams_alike(m):
     """The first step: all beams equal, the lowest takes every place."""
     x = torch.randn(1, 5000, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).repeat(6, 1)
