@@ -1,7 +1,10 @@
 // Beam search's selection: of all W * V continuations of a prompt's W beams the K with the
 // best score s_w + log softmax(x_w)_v.
 //
-// Bound by memory: the logits are read once (the only large input).
+// Bound by memory in the limit: the logits are read once (the only large input).  Measured: 32
+// prompts x 8 beams x 131,072 bf16 logits 25.8 us, of which the scan takes about 17 (67 MB, 3.9
+// TB/s; an exponential per value and its end fill half of the issue slots) and the merge 5; 4
+// beams x 32,000 fp32 7.4 us, latency.
 //
 //   beam_scan_kernel   CTA = a slice of one beam's vocabulary.  One pass: every thread sums
 //                      the exponentials of its values (2^(x log2 e - ref), ref a whole
@@ -447,7 +450,7 @@ struct MergeSmem {
   int count;
 };
 
-// ln(hi + lo) + n ln 2 (see BeamScan), hi >= 0 the larger part, to 1e-9 or so: with hi = 2^e m, m from
+// ln(hi + lo) + n ln 2 (see BeamScan), hi >= 0 the larger part, to 5e-9: with hi = 2^e m, m from
 // sqrt(1/2) to sqrt(2), and s = (m - 1) / (m + 1), ln m = 2 s + 2 s^3 / 3 + 2 s^5 / 5 + ...  s is kept as
 // a sum of two fp32, so that only the last steps need 64 bits (a log in 64 bits takes 1.5 us here).
 __device__ __forceinline__ double bm_log(float hi, float lo, float n) {

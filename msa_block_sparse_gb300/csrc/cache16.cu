@@ -5,7 +5,8 @@
 // slot p % 128 of its page.  Several tokens per row: a prompt, a chunk of one, drafted
 // tokens, or the one new token of a decode step.
 //
-// Bound by memory for a pack (each value read and written once), by latency for a step.
+// Bound by memory for a pack (each value read and written once): 22.5k tokens of 64 + 4 + 4 heads and
+// index heads 166 us (922 MB, 5.5 TB/s); by latency for a step: 64 rows 3.5 us.
 //
 // Work, of two kinds of CTAs.  Those of q take a run of its [T Hq] rows, as in
 // rope_ex.cu: a row of 128 channels belongs to 16 threads, which keep the factors

@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(kPgThreads) pages_compact_kernel(
 // parent's copy and its references are added.  Bound by latency (lengths, parents, the
 // parent's length, entries, atomics, one after another).  Few entries: one cluster does both
 // halves, a warp per row, with a barrier between them (one launch less); many: two launches
-// over the whole GPU, a CTA per row.
+// over the whole GPU, a CTA per row.  Measured, with a copy that resets the tables before each:
+// 64 rows of up to 256 pages 8.8 us, 1,000 rows of up to 1,024 pages 14.8 (45 by one cluster).
 constexpr int kRoThreads = 512, kRoRowThreads = 128;
 constexpr int kRoCluster = 8;
 constexpr int kRoBatch = 8;                  // entries of a lane in flight: their atomics overlap

@@ -24,8 +24,13 @@
 // buffers, so that the next block's products are there when a softmax ends.  Roles: warp 0 claims items and streams K and V pages
 // through a ring of 32 KB stages by TMA; warps 1 and 2 issue a stream's MMAs (P, in bf16, is
 // read from TMEM as the A operand); warp 3 gathers q; warps 4-7 and 8-11 are the streams'
-// softmax (a thread per query row).  P is rounded to bf16 (2^-9 each, beside o's own
+// softmax (a thread per query row).  P is rounded to bf16 (at most 2^-8 each, beside o's own
 // rounding); maxima, sums and o stay in fp32.
+//
+// Bound by memory where little is shared: 64 rows of 8k to 32k tokens, 64 heads on 4, 382 us (2.5
+// GB, 6.6 TB/s).  Prefixes of 8k to 32k shared by 8 rows each: 95 us (443 MB).  One of 16k shared
+// by 64 rows with up to 4k of their own: 97 us (348 MB, 40 GFLOP), the plan about 10 of them.  4
+// rows of 1,500 tokens: 16.5 us, latency.
 #include <cmath>
 #include "kernels.cuh"
 
