@@ -448,9 +448,9 @@ MSA_API msa_status_t msa_cache_append(const void* q, const void* k, const void* 
  * full pages that they have in common are read once for all of them, at up to 6
  * levels (a system prompt, behind it a prompt of each user, behind that its samples); so
  * put rows that share next to each other.  This is found out on the device in each call.
- * A row with cache_lens[b] = 0 gets o = 0 and lse = -infinity; lengths outside
- * [0, 128 max_pages] set MSA_STATUS_BOUNDS and are treated so too.  A page outside
- * [0, num_pages) sets MSA_STATUS_BOUNDS and has no keys.  Slots of a row's last page behind
+ * A row with cache_lens[b] = 0 gets o = 0 and lse = -infinity, and so does a head whose
+ * products are all -infinity; lengths outside [0, 128 max_pages] set MSA_STATUS_BOUNDS and are
+ * treated so too.  A page outside [0, num_pages) sets MSA_STATUS_BOUNDS and has no keys.  o may be q.  Slots of a row's last page behind
  * its end may hold anything.  B <= 2048; scale from 2^-64 to 2^64.
  */
 MSA_API size_t msa_decode_shared_workspace_size(int B, int Hq, int Hkv, int max_pages);
@@ -475,7 +475,8 @@ MSA_API msa_status_t msa_decode_shared(const void* q, const void* k_cache, const
  * nothing else, what lies below -2^28 as -2^28); a beam whose
  * score is -infinity or NaN is dead.  Continuations of probability zero are never chosen:
  * where fewer than K are left, the last places get score -infinity, parent -1, token -1
- * (msa_pages_reorder empties such rows).  W, K <= 64, K <= W V, V <= 2^24, N W <= 65535.
+ * (msa_pages_reorder empties such rows).  scores_out may be scores where K = W, and must not
+ * overlap them otherwise.  W, K <= 64, K <= W V, V <= 2^24, N W <= 65535.
  */
 enum { MSA_F32 = 0, MSA_BF16 = 1 };
 
@@ -644,7 +645,7 @@ MSA_API msa_status_t msa_pages_compact(int32_t* block_table, const int32_t* cach
  * parent lose their pages, and entries that a row no longer needs become -1.  kept[r]
  * (int32 [B], output) is the row's length after the call, -1 where it is refused and left
  * as it was: a parent outside [-1, B), or one whose length is out of range (both set
- * MSA_STATUS_BOUNDS).
+ * MSA_STATUS_BOUNDS).  parents, kept and the tables must not overlap.
  */
 MSA_API size_t msa_pages_reorder_workspace_size(int B, int max_pages);
 

@@ -509,8 +509,8 @@ __device__ __forceinline__ void bm_bound(MergeSmem& sm, Cand top, int K) {
 // grid (prompts)
 __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
     const BeamScan* __restrict__ stats, const unsigned long long* __restrict__ keys,
-    const float* __restrict__ scores, const uint8_t* __restrict__ finished, int W, int V, int K,
-    int slices, int pad_token, float* __restrict__ scores_out, int32_t* __restrict__ parents,
+    const float* scores, const uint8_t* __restrict__ finished, int W, int V, int K,
+    int slices, int pad_token, float* scores_out, int32_t* __restrict__ parents,
     int32_t* __restrict__ tokens) {
   pdl_enter();
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -724,6 +724,9 @@ msa_status_t msa_beam_select(const void* logits, int dtype, int64_t row_stride, 
   if (row_stride < V) return fail(MSA_ERR_INVALID_ARG, "row_stride is below V");
   if (pad_token < 0 || pad_token >= V)
     return fail(MSA_ERR_INVALID_ARG, "pad_token %d outside [0, %d)", pad_token, V);
+  // a prompt's CTA reads its own W scores before it writes its K: in place where they are the same
+  if (overlap(scores_out, 4ull * N * K, scores, 4ull * N * W) && !(scores_out == scores && K == W))
+    return fail(MSA_ERR_INVALID_ARG, "scores_out overlaps scores (it may be scores where K = W)");
   if (workspace_bytes < msa_beam_select_workspace_size(N, W, V, K))
     return fail(MSA_ERR_INVALID_ARG, "workspace too small");
   const long long rows = static_cast<long long>(N) * W;

@@ -31,6 +31,7 @@
 // GB, 6.6 TB/s).  Prefixes of 8k to 32k shared by 8 rows each: 95 us (443 MB).  One of 16k shared
 // by 64 rows with up to 4k of their own: 97 us (348 MB, 40 GFLOP), the plan about 10 of them.  4
 // rows of 1,500 tokens: 16.5 us, latency.
+#include <cfloat>
 #include <cmath>
 #include "kernels.cuh"
 
@@ -883,7 +884,8 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
           const bool any = lim > 0;
           const float mnew = any ? fmaxf(m, sa_max64(sv)) : m;
           const bool resc = mnew > m + rescale;
-          const float mu = resc ? mnew : m;
+          // products of -infinity alone so far: they weigh nothing, and -infinity less itself would be NaN
+          const float mu = resc ? mnew : fmaxf(m, -FLT_MAX);
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                            make_float2(0.f, 0.f)};
           if (any) {
@@ -913,8 +915,8 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
           if (any) {
             const float2 a = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
             const float rs = a.x + a.y;
-            l = m == -INFINITY ? rs : (resc ? l * sa_ex2((m - mu) * sl2) : l) + rs;
-            m = mu;
+            l = (need ? l * sa_ex2((m - mu) * sl2) : l) + rs;   // without `need` and with resc: 0 or NaN
+            m = resc ? mnew : m;
           }
           __syncwarp();                        // the stores are the whole warp's
           tmem_st16(sbuf, pk);

@@ -421,6 +421,30 @@ def test_shared_attention_small_and_large_logits(m, scale, q_gain):
         within(f64(lse)[b], z[b].max(1) * scale, (e + 2.0 ** -22 * np.abs(z[b]).max()) * scale + 7, "lse")
 
 
+def test_shared_attention_products_of_minus_infinity(m):
+    """Keys whose products are -infinity weigh nothing, be it whole blocks, pages or parts of a row;
+    a head that has no others counts as one without keys."""
+    table, lens, P = tree_table(np.random.default_rng(13), [(5, [40] * 18), (3, [0, 300]), 700, 130], empties=())
+    rng = np.random.default_rng(14)
+    q = bf16(rng.standard_normal((len(lens), 16, 128)))
+    q[:, :, 5] = 1.0
+    kc, vc = (bf16(rng.standard_normal((P, 1, 128, 128))) for _ in range(2))
+    for b, off in ((0, range(0, 3)), (18, range(1, 4)), (19, (0, 4)), (20, (0, 1, 2)), (21, (0, 1))):
+        for c in off:
+            if c < S.blocks(lens[b]):
+                kc[table[b, c], 0, :, 5] = -math.inf
+    kc[table[20, 3], 0, :64, 5] = -math.inf
+    o, lse = m.msa_decode_shared(q, kc, vc, i32(table), i32(lens))
+    m.msa_check_status()
+    kn = np.where(np.isinf(f64(kc)), -1e30, f64(kc))
+    want, wlse = S.attend(f64(q), kn, f64(vc), table, lens, SCALE)
+    none = wlse < -1e20
+    assert none.any() and not none.all()
+    assert (f64(o)[none] == 0).all() and (f64(lse)[none] == -np.inf).all()
+    assert np.linalg.norm(f64(o)[~none] - want[~none]) <= 2.0 ** -8 * np.linalg.norm(want[~none])
+    within(f64(lse)[~none], wlse[~none], 2.0 ** -10, "lse")
+
+
 def test_shared_attention_rows_and_heads_do_not_mix(m):
     """A query row, or a row's own keys, that hold infinities or NaN change no other row."""
     table, lens, P = tree_table(np.random.default_rng(12), [(2, [40] * 12), 200])
@@ -571,6 +595,16 @@ def test_beam_select_beams_alike(m):
     first = torch.tensor([0.0, -math.inf, -math.inf] * 2, device=DEV)
     so, po, to = m.msa_beam_select(x, first, 3, 3)
     assert po.tolist() == [[0] * 3, [3] * 3] and torch.equal(to[0].long(), x[0].topk(3)[1])
+
+
+def test_beam_select_scores_in_place(m):
+    x = torch.randn(12, 3001, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    scores = -torch.arange(12.0, device=DEV) / 3
+    want = m.msa_beam_select(x, scores, 4)
+    got = m.msa_beam_select(x, scores, 4, scores_out=scores.view(3, 4))
+    assert torch.equal(scores.view(3, 4), want[0]) and all(torch.equal(a, b) for a, b in zip(got, want))
+    with pytest.raises(m.MSAError, match="overlaps"):
+        m.msa_beam_select(x, scores, 4, n_out=2, scores_out=scores[:6].view(3, 2))
 
 
 def test_beam_select_argument_checks(m):

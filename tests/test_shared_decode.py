@@ -173,6 +173,35 @@ def test_pages_reorder_refusals(lib):
         assert call(**{**dict(size=1 << 50), **kw}) == 2, kw
 
 
+def at(k):
+    return ctypes.c_void_p((1 << 20) + (k << 12))
+
+
+def test_beam_select_refuses_scores_that_overlap(lib):
+    """In place only where a prompt's new scores lie where its old ones were (that call is not made here:
+    the workspace is refused next)."""
+    def call(so, K):
+        rc = lib.msa_beam_select(at(0), 0, 50, at(1), None, 2, 3, 50, K, 0, so, at(2), at(3), at(4), 0, None)
+        assert rc == 1
+        return lib.msa_last_error().decode()
+    assert "overlaps" in call(at(1), 4) and "overlaps" in call(at(1), 2)
+    assert "overlaps" in call(ctypes.c_void_p(at(1).value + 16), 3)
+    assert "workspace" in call(at(1), 3) and "workspace" in call(ctypes.c_void_p(at(1).value + 32), 3)
+
+
+def test_pages_reorder_refuses_arguments_that_overlap(lib):
+    names = dict(parents=at(0), table=at(1), lens=at(2), ref=at(3), B=4, P=9, maxp=5, kept=at(4), ws=at(5), size=0,
+                 stream=None)
+
+    def call(**kw):
+        assert lib.msa_pages_reorder(*{**names, **kw}.values()) == 1
+        return lib.msa_last_error().decode()
+    assert "workspace" in call()
+    for kw in (dict(kept=at(0)), dict(kept=at(2)), dict(kept=ctypes.c_void_p(at(1).value + 64)), dict(kept=at(3)),
+               dict(parents=at(2)), dict(parents=at(1))):
+        assert "overlaps" in call(**kw), kw
+
+
 def test_binding_refuses_cpu_tensors():
     t = torch.zeros(2, 4, 128, dtype=torch.bfloat16)
     i = torch.zeros(2, dtype=torch.int32)
