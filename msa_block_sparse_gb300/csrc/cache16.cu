@@ -6,7 +6,7 @@
 // tokens, or the one new token of a decode step.
 //
 // Bound by memory for a pack (each value read and written once): 22.5k tokens of 64 + 4 + 4 heads and
-// index heads 166 us (922 MB, 5.5 TB/s); by latency for a step: 64 rows 3.5 us.
+// index heads 159 us (922 MB, 5.8 TB/s); by latency for a step: 64 rows 3.5 us.
 //
 // Work, of two kinds of CTAs.  Those of q take a run of its [T Hq] rows, as in
 // rope_ex.cu: a row of 128 channels belongs to 16 threads, which keep the factors
@@ -25,6 +25,7 @@ namespace {
 constexpr int kCaThreads = 128;
 constexpr int kCaSlots = kCaThreads / (kD / 8);  // rows side by side
 constexpr int kCaTokens = 16;                    // of a CTA at most
+constexpr int kCaPerSm = 8;                      // CTAs of an SM
 constexpr int kCaDeep = 4;                       // rows of a thread loaded or at work
 
 struct CaJob {
@@ -244,7 +245,7 @@ __device__ __forceinline__ void ca_small(const CaArgs& a, const RxTurns& turns, 
 }  // namespace
 
 template <bool kHalf>
-__global__ void __launch_bounds__(kCaThreads, 8) cache_append_kernel(const __grid_constant__ CaArgs a,
+__global__ void __launch_bounds__(kCaThreads, kCaPerSm) cache_append_kernel(const __grid_constant__ CaArgs a,
                                                                      const __grid_constant__ RxTurns turns,
                                                                      uint32_t* status) {
   pdl_enter();
@@ -326,12 +327,16 @@ msa_status_t msa_cache_append(const void* q, const void* k, const void* v, const
   a.gain = rope->gain;
   a.inv_half = ((1u << 20) + rope->dim / 2 - 1) / (rope->dim / 2);
   a.inv_hq = ((1u << 20) + Hq - 1) / Hq;
-  // q: 64 rows per CTA, fewer (a pass of rows at least) when that would leave SMs without one;
-  // at most 16 tokens.  The others: shares of a token's heads while there are SMs for them.
+  // q: 64 rows per CTA, fewer (a pass of rows at least) when that would leave SMs without one; more,
+  // up to 256, as long as that leaves 4 rounds of CTAs (places and angles are looked up once per CTA:
+  // 22.5k tokens of 64 heads 168 us with 64 rows, 163 with 128, 160 with 256 or 512); at most 16 tokens.
+  // The others: shares of a token's heads while there are SMs for them.
   const int sms = device_sm_count();
   const long long q_rows = static_cast<long long>(T) * Hq;
   long long run = q_rows / (2 * sms);
   run = run < kCaSlots ? kCaSlots : (run > 64 ? 64 : run);
+  const long long rounds = q_rows / (4 * kCaPerSm * sms);
+  if (rounds > run) run = rounds > 256 ? 256 : rounds;
   if (run > static_cast<long long>(kCaTokens - 1) * Hq) run = static_cast<long long>(kCaTokens - 1) * Hq;
   a.q_run = static_cast<int>(run > Hq ? run / Hq * Hq : run);
   const long long q_ctas = (q_rows + a.q_run - 1) / a.q_run;
