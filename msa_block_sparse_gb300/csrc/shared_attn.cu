@@ -110,11 +110,21 @@ constexpr int kPlRowInts = 9, kPlNodeInts = 8;    // of the dynamic shared memor
 // items fill what the runs leave, and their parts are small).  The last ones always fit the
 // workspace: one item per node and tile.
 constexpr int kPlCuts = kPlLengths / 2;
+constexpr int kPlAlones = 10;
 __constant__ int kPlCut[kPlCuts] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128, 256, 1024};
-__device__ __forceinline__ int2 pl_length(int c) {
-  const int L = kPlCut[c >> 1];
-  return make_int2(L, L < 512 ? min(L, c & 1 ? 8 : 24) : L);
+__constant__ int kPlAlone[kPlAlones] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 1024};
+// Candidate c: its runs' length is c / 2, its rows' is as long, but at most 8 or 24
+__device__ __forceinline__ int pl_alone(int c) {
+  return c >> 1 == kPlCuts - 1 ? kPlAlones - 1 : min(c >> 1, c & 1 ? 5 : 8);
 }
+__device__ __forceinline__ int2 pl_length(int c) { return make_int2(kPlCut[c >> 1], kPlAlone[pl_alone(c)]); }
+
+// What runs, or rows alone, come to in items of a length
+struct PlWeight {
+  float sum, slowest, long_sum, memory;    // times of all items, the longest, the runs' long ones; of the memory
+  int items, long_items;
+  uint32_t parts;
+};
 // Times in us, from traces and from runs over item lengths: a page in a narrow and a wide item,
 // an item's start and end as far as no page passes; of the whole GPU: a query row's part
 // (written, joined), 64 KB of K and V from memory
@@ -168,7 +178,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   extern __shared__ int smem_i[];
   __shared__ int2 warp_sums[kPlThreads / 32];
   __shared__ int longest_run, short_items;
-  __shared__ float cost[kPlLengths];
+  __shared__ PlWeight weight[kPlCuts + kPlAlones];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int threads = blockDim.x, warps = threads / 32;
   int* row_of = smem_i;                    // live rows
@@ -189,6 +199,32 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   int* nd_item = nd_tiles + 2 * B;         // first item
   int* nd_part = nd_item + 2 * B;          // and first part
 
+  // Two units of what is compared below, asked for before the lengths are known: as if every row
+  // had tokens
+  struct Unit {
+    int i, j0, most, x[8], y[8];
+  };
+  const int chunks = (max_pages + 255) / 256;
+  auto place = [&](Unit& t, int u, int pairs) {
+    const int chunk = chunks == 1 || pairs < 1 ? 0 : u / pairs;   // the first columns of all pairs first
+    t.i = u - chunk * pairs;
+    t.j0 = chunk * 256;
+  };
+  auto load = [&](Unit& t, int ra, int rb, int end) {
+    const int32_t* a = table + static_cast<size_t>(ra) * max_pages;
+    const int32_t* b = table + static_cast<size_t>(rb) * max_pages;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int j = t.j0 + 32 * k + lane;
+      t.x[k] = j < end ? __ldg(a + j) : 0;
+      t.y[k] = j < end ? __ldg(b + j) : 0;
+    }
+  };
+  Unit p, q;
+  place(p, warp, B - 1);
+  place(q, warp + warps, B - 1);
+  if (warp < (B - 1) * chunks) load(p, p.i, p.i + 1, max_pages);
+  if (warp + warps < (B - 1) * chunks) load(q, q.i, q.i + 1, max_pages);
   // ---- rows with tokens
   int n = 0;
   for (int b0 = 0; b0 < B; b0 += threads) {
@@ -219,39 +255,32 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   // ---- full pages that neighbours have in common: a warp per pair and 256 columns, which
   // lowers the value to the first column that differs
   {
-    const int chunks = (max_pages + 255) / 256, units = (n - 1) * chunks;
-    struct Unit {
-      int i, j0, most, x[8], y[8];
-    };
-    auto load = [&](Unit& t, int u) {
-      const int chunk = chunks == 1 ? 0 : u / (n - 1);   // the first columns of all pairs first
-      t.i = u - chunk * (n - 1);
-      t.j0 = chunk * 256;
+    const int units = (n - 1) * chunks;
+    auto need = [&](Unit& t, int u) {
       t.most = u < units ? min(len_of[t.i], len_of[t.i + 1]) / kBlock : 0;
-      if (t.j0 >= t.most) return;
-      const int32_t* a = table + static_cast<size_t>(row_of[t.i]) * max_pages;
-      const int32_t* b = table + static_cast<size_t>(row_of[t.i + 1]) * max_pages;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int j = t.j0 + 32 * k + lane;
-        t.x[k] = j < t.most ? __ldg(a + j) : 0;
-        t.y[k] = j < t.most ? __ldg(b + j) : 0;
-      }
+      return t.j0 < t.most;
     };
     auto look = [&](const Unit& t) {
       if (t.j0 >= t.most) return;
       int at = -1;
 #pragma unroll
       for (int k = 7; k >= 0; --k) {
-        const uint32_t differ = __ballot_sync(0xffffffffu, t.x[k] != t.y[k]);
+        const uint32_t differ =
+            __ballot_sync(0xffffffffu, t.x[k] != t.y[k] && t.j0 + 32 * k + lane < t.most);
         if (differ) at = t.j0 + 32 * k + __ffs(differ) - 1;
       }
       if (at >= 0 && lane == 0) atomicMin(&common[t.i], at);
     };
     for (int u = warp; u < units; u += 2 * warps) {   // two units' loads in flight
-      Unit p, q;
-      load(p, u);
-      load(q, u + warps);
+      if (u != warp || n != B) {
+        place(p, u, n - 1);
+        place(q, u + warps, n - 1);
+        if (need(p, u)) load(p, row_of[p.i], row_of[p.i + 1], p.most);
+        if (need(q, u + warps)) load(q, row_of[q.i], row_of[q.i + 1], q.most);
+      } else {
+        need(p, u);
+        need(q, u + warps);
+      }
       look(p);
       look(q);
     }
@@ -369,72 +398,70 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   }
   const int nodes = runs + longs + alone;
   __syncthreads();
-  // ---- item lengths: a warp weighs a candidate.  The SMs' share of all items' times, or the
+  // ---- item lengths: a warp weighs a length of the runs, or of the rows alone.  The SMs' share of all items' times, or the
   // memory's, and a part of a row's item at the end; or the rounds that the runs' long items
   // take, whichever is more (in a round that is not full, items are 0.6 as long: the CTAs at
   // work have more of the memory's bandwidth each).  Where items of one page fit a round,
   // they are the shortest.
   const bool one_page = static_cast<long long>(short_items) * Hkv <= sms;
-  for (int c = warp; c < kPlLengths && !one_page; c += warps) {
-    const int2 L = pl_length(c);
-    const float inv = 1.f / static_cast<float>(L.x), inv1 = 1.f / static_cast<float>(L.y);
-    float sum = 0.f, run = 0.f, single = 0.f, long_sum = 0.f, memory = 0.f;
+  for (int c = warp; c < kPlCuts + kPlAlones && !one_page; c += warps) {
+    const bool shared = c < kPlCuts;       // of the runs, else of the rows alone
+    const int L = shared ? kPlCut[c] : kPlAlone[c - kPlCuts], most = min(longest_run, L);
+    const float inv = 1.f / static_cast<float>(L);
+    float sum = 0.f, slowest = 0.f, long_sum = 0.f, memory = 0.f;
     int items = 0, long_items = 0;
     long long parts = 0;
-    const int most = min(longest_run, L.x);
-    for (int k = lane; k < nodes; k += 32) {
+    for (int k = (shared ? 0 : runs) + lane; k < (shared ? runs : nodes); k += 32) {
       const int pages = nd_pages[k], m = nd_m[k];
-      const int ns = m > 1 ? pl_splits(pages, L.x, inv) : pl_splits(pages, L.y, inv1);
+      const int ns = pl_splits(pages, L, inv);
       const int each = nd_tiles[k] * ns * Hkv;
-      const int nr = min(m, 2 * tile_rows);
-      const bool wide = nr > tile_rows;
+      const bool wide = min(m, 2 * tile_rows) > tile_rows;
       const float per = __fdividef((wide ? kPlWide : kPlNarrow) * pages, static_cast<float>(ns)) +
                         (wide ? kPlWideStart : kPlStart);
       sum += per * each;
       memory += static_cast<float>(pages * Hkv) * kPlMemory;
       items += each;
       parts += static_cast<long long>(m) * G * ns * Hkv;
-      if (m == 1) {
-        single = fmaxf(single, per);
-      } else {
-        run = fmaxf(run, per);
-        if (2 * pages > most * ns) {
-          long_sum += per * each;
-          long_items += each;
-        }
+      slowest = fmaxf(slowest, per);
+      if (shared && 2 * pages > most * ns) {
+        long_sum += per * each;
+        long_items += each;
       }
     }
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) {
       sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      long_sum += __shfl_xor_sync(0xffffffffu, long_sum, d);
       memory += __shfl_xor_sync(0xffffffffu, memory, d);
+      if (shared) long_sum += __shfl_xor_sync(0xffffffffu, long_sum, d);
     }
-    // maxima of numbers that are not negative, as integers; parts capped so that the sum fits
-    run = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(run)));
-    single = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(single)));
+    // a maximum of numbers that are not negative, as integers; parts capped so that sums fit
+    slowest = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(slowest)));
     items = __reduce_add_sync(0xffffffffu, items);
     long_items = __reduce_add_sync(0xffffffffu, long_items);
     const uint32_t all_parts =
-        __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(parts < (1 << 26) ? parts : (1 << 26)));
-    float time = fmaxf(run, single) + all_parts * kPlPart;
+        __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(parts < (1 << 25) ? parts : (1 << 25)));
+    if (lane == 0) weight[c] = {sum, slowest, long_sum, memory, items, long_items, all_parts};
+  }
+  __syncthreads();
+  int best = 0;
+  if (!one_page) {                         // every warp for itself, a lane per candidate
+    best = lane;
+    const PlWeight a = weight[lane >> 1], b = weight[kPlCuts + pl_alone(lane)];
+    const float run = a.slowest, single = b.slowest, sum = a.sum + b.sum, memory = a.memory + b.memory;
+    const int items = a.items + b.items;
+    const uint32_t all_parts = a.parts + b.parts;
+    float t = fmaxf(run, single) + all_parts * kPlPart;
     if (items > sms) {
       const float share = sum / sms, slow = fmaxf(1.f, memory / share);
       float rounds_time = run;
-      if (long_items > sms) {
-        const float x = static_cast<float>(long_items) / sms, full = floorf(x);
+      if (a.long_items > sms) {
+        const float x = static_cast<float>(a.long_items) / sms, full = floorf(x);
         const float last = x > full ? fmaxf(x - full, 0.6f) : 0.f;
-        rounds_time = long_sum / long_items * (full + last);
+        rounds_time = a.long_sum / a.long_items * (full + last);
       }
-      time = slow * fmaxf(share + kPlTail * single, rounds_time) + all_parts * kPlPart;
+      t = slow * fmaxf(share + kPlTail * single, rounds_time) + all_parts * kPlPart;
     }
-    if (lane == 0)
-      cost[c] = items <= plan.max_items && all_parts <= static_cast<uint32_t>(plan.max_parts) ? time : INFINITY;
-  }
-  __syncthreads();
-  int best = one_page ? 0 : lane;
-  if (!one_page) {
-    float t = cost[lane];
+    if (items > plan.max_items || all_parts > static_cast<uint32_t>(plan.max_parts)) t = INFINITY;
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) {
       const float ot = __shfl_xor_sync(0xffffffffu, t, d);
@@ -1033,19 +1060,23 @@ __global__ void __launch_bounds__(kCbThreads, 2) shared_combine_kernel(const SaP
                                                                     int ways, float sl2,
                                                                     __nv_bfloat16* __restrict__ o,
                                                                     float* __restrict__ lse) {
-  pdl_enter();
   __shared__ SaSeg seg[kSaMaxSegs];
   __shared__ int n_seg;
   __shared__ float4 part[kCbThreads];
   __shared__ float2 part_ml[kCbThreads];
   const int b = blockIdx.x, g = blockIdx.y, tid = threadIdx.x;
-  if (tid < kSaMaxSegs) seg[tid] = plan.segs[static_cast<size_t>(b) * kSaMaxSegs + tid];
-  if (tid == kSaMaxSegs) n_seg = plan.n_segs[b];
+  // the plan was complete before the kernel that is waited for let this one start
+  if (tid < kSaMaxSegs) {
+    const int4 e = __ldcg(reinterpret_cast<const int4*>(plan.segs + static_cast<size_t>(b) * kSaMaxSegs + tid));
+    seg[tid] = {e.x, e.y, e.z, e.w};
+  }
+  if (tid == kSaMaxSegs) n_seg = __ldcg(plan.n_segs + b);
   const int h = blockIdx.z * Gc + tid % Gc, d4 = tid / Gc % 32, way = tid / (32 * Gc);
   __syncthreads();
   const int ns = n_seg;
   int total = 0;
   for (int k = 0; k < ns; ++k) total += seg[k].splits;
+  pdl_enter();
   float M = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (h < G) {
