@@ -58,7 +58,8 @@ constexpr uint32_t kSaColO = 256;          // S of stream s at 128 s, O at 256 +
 struct alignas(16) SaItem {
   int i0, nr, c0, c1;
   int g, m, ro, base;
-  int row, len, pad[2];   // the first of the rows, and its tokens
+  int row, len;           // the first of the rows, and its tokens
+  int side, pad;          // the rows are row, row + 1, ...: none between them is empty
 };
 
 // Parts of a row in one node: splits of (m G) query rows each, `ro` the row in the node
@@ -517,11 +518,12 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
     const float inv_ns = 1.f / static_cast<float>(ns);
     // pages s / ns, rounded down (the products stay below 2^21: see pl_splits)
     auto cut = [&](int k) { return static_cast<int>((static_cast<float>(pages * k) + 0.5f) * inv_ns); };
-    const int ro = tile * 2 * tile_rows, i0 = nd_i0[lo] + ro;
+    const int ro = tile * 2 * tile_rows, i0 = nd_i0[lo] + ro, nr = min(2 * tile_rows, m - ro);
     int4* item = reinterpret_cast<int4*>(plan.items + e);
-    item[0] = make_int4(i0, min(2 * tile_rows, m - ro), nd_v0[lo] + cut(s), nd_v0[lo] + cut(s + 1));
+    item[0] = make_int4(i0, nr, nd_v0[lo] + cut(s), nd_v0[lo] + cut(s + 1));
     item[1] = make_int4(g, m, ro, nd_part[lo] + (s * Hkv + g) * m * G);
-    item[2] = make_int4(row_of[i0], len_of[i0], 0, 0);
+    const int last = row_of[i0 + nr - 1];
+    item[2] = make_int4(row_of[i0], len_of[i0], last - row_of[i0] == nr - 1, 0);
   }
   // ---- every row's parts: its own node, then the runs above
   for (int i = tid; i < n; i += threads) {
@@ -547,6 +549,7 @@ struct SaSlot {
   int pages;          // valid ones; -1: no items left
   int tail;           // keys of the last of them
   int wide;
+  int row;            // the first of the rows where they lie side by side, else -1
   uint32_t ring;      // stages used before the item
   uint32_t qt;        // q tiles used before the item
 };
@@ -710,6 +713,7 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
               s.pages = valid;
               s.tail = last_ok ? min(kBlock, nx.len - (nx.c1 - 1) * kBlock) : kBlock;
               s.wide = nx.nr > tile_rows;
+              s.row = nx.side ? nx.row : -1;
               s.ring = ring_end;
               s.qt = qt;
             }
@@ -845,13 +849,15 @@ __global__ void __launch_bounds__(kSaThreads, 1) shared_attn_kernel(
         const int qb = qi & 1;
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_empty[qb], ((qi >> 1) & 1) ^ 1, status, 121)))) break;
         // rows of the tile, 16 lanes each; all copies are in flight together, so that a tile takes
-        // two latencies (which rows, then q)
+        // one latency, or two (which rows, then q)
         const int r0 = w * tile_rows, nr = min(tile_rows, t.nr - r0) * G;
         uint32_t from[4];                                // this lane's rows 32 k + lane, as rows of q
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int r = 32 * k + lane, tok = r / G;
-          from[k] = r < nr ? plan.live[t.i0 + r0 + tok] * Hq + t.g * G + (r - tok * G) : 0;
+          int row = 0;
+          if (r < nr) row = t.row >= 0 ? t.row + r0 + tok : plan.live[t.i0 + r0 + tok];
+          from[k] = row * Hq + t.g * G + (r - tok * G);
         }
         const int c = lane & 15, up = lane >> 4;
         uint8_t* dst = sm.q[qb] + (c >> 3) * kSaHalf;

@@ -33,10 +33,11 @@ __device__ __forceinline__ uint64_t globaltimer() {
 // pdl_wait() returns once that kernel has completed and its writes are
 // visible (immediately for a grid launched without the attribute).  Every
 // kernel of this library calls it, in every CTA, before its first global
-// access, so completion stays ordered along the stream.  One exception:
-// decode4_attend_kernel reads q and the lengths before its wait when it follows
-// decode4_score_kernel in the same call.  That kernel lets it launch only after a wait of
-// its own (pdl_enter), by which time what wrote them has completed.  pdl_launch()
+// access, so completion stays ordered along the stream.  Two exceptions read before their wait
+// what a kernel before the previous one wrote: decode4_attend_kernel (q and the lengths) and
+// shared_combine_kernel (the plan).  The previous kernel is of the same call and lets them
+// launch only after a wait of its own (pdl_enter), by which time what wrote these has completed.
+// pdl_launch()
 // lets the next grid of the stream begin its launch.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() {
