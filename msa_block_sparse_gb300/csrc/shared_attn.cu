@@ -27,10 +27,10 @@
 // softmax (a thread per query row).  P is rounded to bf16 (at most 2^-8 each, beside o's own
 // rounding); maxima, sums and o stay in fp32.
 //
-// Bound by memory where little is shared: 64 rows of 8k to 32k tokens, 64 heads on 4, 382 us (2.5
-// GB, 6.6 TB/s).  Prefixes of 8k to 32k shared by 8 rows each: 95 us (443 MB).  One of 16k shared
-// by 64 rows with up to 4k of their own: 97 us (348 MB, 40 GFLOP), the plan about 10 of them.  4
-// rows of 1,500 tokens: 16.5 us, latency.
+// Bound by memory where little is shared: 64 rows of 8k to 32k tokens, 64 heads on 4, 380 us (2.5
+// GB, 6.6 TB/s).  Prefixes of 8k to 32k shared by 8 rows each: 94 us (443 MB).  One of 16k shared
+// by 64 rows with up to 4k of their own: 94 us (348 MB, 40 GFLOP), the plan about 9 of them.  4
+// rows of 1,500 tokens: 15.4 us, latency.
 #include <cfloat>
 #include <cmath>
 #include "kernels.cuh"
@@ -136,33 +136,43 @@ constexpr float kPlMemory = 0.0099f;
 constexpr float kPlTail = 0.12f;         // of a row's longest item: what others wait for at the end
 constexpr int kPlLong = 8;               // rows alone with as many pages come before the others
 
-// Exclusive scans over the CTA of two values at a time; total = the sums
-__device__ __forceinline__ int2 pl_scan(int2 v, int2* warp_sums, int2* total) {
-  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-  auto warp_scan = [&](int2 x) {
+// Exclusive scans over the CTA's first `count` threads (the others' values are 0) of two values at
+// a time; total = the sums.  Warps without a value only add up.  One barrier: a buffer is used
+// again two scans later.
+struct PlScan {
+  int2 (*warp_sums)[kPlThreads / 32];
+  int turn = 0;
+
+  __device__ __forceinline__ int2 operator()(int2 v, int count, int2* total) {
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    const bool busy = wp * 32 < count;
+    int2* sums = warp_sums[turn];
+    turn ^= 1;
+    int2 x = v;
+    if (busy) {
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, x.x, d), b = __shfl_up_sync(0xffffffffu, x.y, d);
-      if (lane >= d) {
-        x.x += a;
-        x.y += b;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, x.x, d), b = __shfl_up_sync(0xffffffffu, x.y, d);
+        if (lane >= d) {
+          x.x += a;
+          x.y += b;
+        }
       }
+      if (lane == 31) sums[wp] = x;
+    }
+    __syncthreads();
+    const int2 own = lane * 32 < count ? sums[lane] : make_int2(0, 0);
+    *total = make_int2(__reduce_add_sync(0xffffffffu, own.x), __reduce_add_sync(0xffffffffu, own.y));
+    if (busy) {
+      x.x += __reduce_add_sync(0xffffffffu, lane < wp ? own.x : 0) - v.x;
+      x.y += __reduce_add_sync(0xffffffffu, lane < wp ? own.y : 0) - v.y;
     }
     return x;
-  };
-  const int2 x = warp_scan(v);
-  if (lane == 31) warp_sums[wp] = x;
-  __syncthreads();
-  const int2 own = lane < static_cast<int>(blockDim.x) / 32 ? warp_sums[lane] : make_int2(0, 0);   // in every warp
-  const int2 w = warp_scan(own);
-  *total = make_int2(__shfl_sync(0xffffffffu, w.x, 31), __shfl_sync(0xffffffffu, w.y, 31));
-  const int bx = __shfl_sync(0xffffffffu, w.x - own.x, wp), by = __shfl_sync(0xffffffffu, w.y - own.y, wp);
-  __syncthreads();                         // warp_sums may be used again
-  return make_int2(bx + x.x - v.x, by + x.y - v.y);
-}
+  }
+};
 
-// ceil(pages / L) with 1 / L at hand: (x + 1/2) / L stays 1 / 2048 away from whole numbers,
-// the product's error (pages, L <= 1024) does not reach that far
+// ceil(pages / L) with 1 / L, good to 2 units, at hand: (x + 1/2) / L stays 1 / (2 L) away from whole
+// numbers, the product's error (x <= 2047: 2047 / L 2^-21) does not reach that far
 __device__ __forceinline__ int pl_splits(int pages, int L, float inv) {
   return static_cast<int>((static_cast<float>(pages + L - 1) + 0.5f) * inv);
 }
@@ -177,11 +187,12 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
     int max_pages, int sms, SaPlan plan, uint32_t* status) {
   pdl_enter();
   extern __shared__ int smem_i[];
-  __shared__ int2 warp_sums[kPlThreads / 32];
-  __shared__ int longest_run, short_items;
+  __shared__ int2 warp_sums[2][kPlThreads / 32];
+  __shared__ int longest_run, short_items, chosen;
   __shared__ PlWeight weight[kPlCuts + kPlAlones];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int threads = blockDim.x, warps = threads / 32;
+  PlScan scan{warp_sums};
   int* row_of = smem_i;                    // live rows
   int* len_of = row_of + B;                // their lengths
   int* common = len_of + B;                // c_i
@@ -240,7 +251,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       if (L == 0) plan.n_segs[b] = 0;
     }
     int2 total;
-    const int at = n + pl_scan(make_int2(L > 0, 0), warp_sums, &total).x;
+    const int at = n + scan(make_int2(L > 0, 0), min(B - b0, threads), &total).x;
     if (L > 0) {
       row_of[at] = b;
       len_of[at] = L;
@@ -364,7 +375,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       }
       int2 total;
       const bool is_long = pages1 >= kPlLong;
-      const int2 sc = pl_scan(make_int2((pages > 0) | (is_long << 16), pages1 > 0 && !is_long), warp_sums, &total);
+      const int2 sc = scan(make_int2((pages > 0) | (is_long << 16), pages1 > 0 && !is_long), min(n - k0, threads), &total);
       if (n <= threads) {
         runs = total.x & 0xFFFF;
         longs = total.x >> 16;
@@ -408,7 +419,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
   for (int c = warp; c < kPlCuts + kPlAlones && !one_page; c += warps) {
     const bool shared = c < kPlCuts;       // of the runs, else of the rows alone
     const int L = shared ? kPlCut[c] : kPlAlone[c - kPlCuts], most = min(longest_run, L);
-    const float inv = 1.f / static_cast<float>(L);
+    const float inv = __fdividef(1.f, static_cast<float>(L));
     float sum = 0.f, slowest = 0.f, long_sum = 0.f, memory = 0.f;
     int items = 0, long_items = 0;
     long long parts = 0;
@@ -443,25 +454,26 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
         __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(parts < (1 << 25) ? parts : (1 << 25)));
     if (lane == 0) weight[c] = {sum, slowest, long_sum, memory, items, long_items, all_parts};
   }
-  __syncthreads();
-  int best = 0;
-  if (!one_page) {                         // every warp for itself, a lane per candidate
-    best = lane;
+  if (!one_page) __syncthreads();
+  if (!one_page && warp == 0) {            // a lane per candidate
+    int best = lane;
     const PlWeight a = weight[lane >> 1], b = weight[kPlCuts + pl_alone(lane)];
-    const float run = a.slowest, single = b.slowest, sum = a.sum + b.sum, memory = a.memory + b.memory;
+    const float run = a.slowest, single = b.slowest, all = static_cast<float>(sms);
     const int items = a.items + b.items;
     const uint32_t all_parts = a.parts + b.parts;
-    float t = fmaxf(run, single) + all_parts * kPlPart;
+    float t = fmaxf(run, single);
     if (items > sms) {
-      const float share = sum / sms, slow = fmaxf(1.f, memory / share);
+      const float share = __fdividef(a.sum + b.sum, all);
+      const float slow = fmaxf(1.f, __fdividef(a.memory + b.memory, share));
       float rounds_time = run;
       if (a.long_items > sms) {
-        const float x = static_cast<float>(a.long_items) / sms, full = floorf(x);
+        const float x = __fdividef(static_cast<float>(a.long_items), all), full = floorf(x);
         const float last = x > full ? fmaxf(x - full, 0.6f) : 0.f;
-        rounds_time = a.long_sum / a.long_items * (full + last);
+        rounds_time = __fdividef(a.long_sum, static_cast<float>(a.long_items)) * (full + last);
       }
-      t = slow * fmaxf(share + kPlTail * single, rounds_time) + all_parts * kPlPart;
+      t = slow * fmaxf(share + kPlTail * single, rounds_time);
     }
+    t += all_parts * kPlPart;
     if (items > plan.max_items || all_parts > static_cast<uint32_t>(plan.max_parts)) t = INFINITY;
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) {
@@ -472,9 +484,12 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
         best = ob;
       }
     }
+    if (lane == 0) chosen = best;
   }
+  if (!one_page) __syncthreads();
+  const int best = one_page ? 0 : chosen;
   const int L = pl_length(best).x, L1 = pl_length(best).y;
-  const float inv = 1.f / static_cast<float>(L), inv1 = 1.f / static_cast<float>(L1);
+  const float inv = __fdividef(1.f, static_cast<float>(L)), inv1 = __fdividef(1.f, static_cast<float>(L1));
   auto splits = [&](int k) {
     return nd_m[k] > 1 ? pl_splits(nd_pages[k], L, inv) : pl_splits(nd_pages[k], L1, inv1);
   };
@@ -489,7 +504,7 @@ __global__ void __launch_bounds__(kPlThreads) shared_plan_kernel(
       parts = nd_m[k] * G * ns * Hkv;
     }
     int2 total;
-    const int2 at = pl_scan(make_int2(items, parts), warp_sums, &total);
+    const int2 at = scan(make_int2(items, parts), min(nodes - k0, threads), &total);
     if (k < nodes) {
       nd_item[k] = n_items + at.x;
       nd_part[k] = n_parts + at.y;
