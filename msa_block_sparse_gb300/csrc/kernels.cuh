@@ -159,6 +159,19 @@ msa_status_t launch_decode(const void* q, const void* q_idx, const void* k_cache
 msa_status_t check_gains(float k_gain, float v_gain, float kidx_gain);
 msa_status_t check_cache_sizes(int Hkv, int num_pages, int max_pages);
 
+// ---------------------------------------------------------------- full attention over few pages
+struct ShortAttn {
+  CUtensorMap tm_k, tm_v;        // boxes of 64 channels x a page of a head
+  const __nv_bfloat16* q;        // [B, G Hkv, 128]
+  const int32_t *table, *lens;
+  int B, G, Hkv, num_pages, max_pages;
+  float sl2;                     // scale log2(e)
+  __nv_bfloat16* o;
+  float* lse;                    // may be null
+};
+bool short_attn_fits(int B, int G, int Hkv, int max_pages);
+msa_status_t launch_short_attn(const ShortAttn& a, cudaStream_t stream);
+
 // ---------------------------------------------------------------- narrow blocks
 // 4-token key blocks, head dim 256, 12 query heads per KV head.
 constexpr int kQsaMaxSeqlen = 32768;

@@ -1241,6 +1241,10 @@ msa_status_t msa_decode_shared(const void* q, const void* k_cache, const void* v
   const uint32_t box[3] = {64, kBlock, 1};
   if (!make_tmap_bf16(&tk, k_cache, 3, dims, box) || !make_tmap_bf16(&tv, v_cache, 3, dims, box))
     return fail(MSA_ERR_CUDA, "cuTensorMapEncodeTiled failed for the caches");
+  if (short_attn_fits(B, G, Hkv, max_pages))
+    return launch_short_attn({tk, tv, static_cast<const __nv_bfloat16*>(q), block_table, cache_lens, B, G, Hkv,
+                              num_pages, max_pages, scale * kSaLog2e, static_cast<__nv_bfloat16*>(o), lse},
+                             static_cast<cudaStream_t>(stream));
   uint32_t* sw = nullptr;
   MSA_TRY(status_word(&sw));
   MSA_TRY(ensure_smem(shared_attn_kernel, sizeof(SaSmem), "shared_attn_kernel"));

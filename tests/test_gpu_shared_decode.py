@@ -232,7 +232,20 @@ def tree_table(rng, groups, maxp=None, empties=()):
     return table, np.array([n for _, n in rows]), max(1, at[0])
 
 
-def attend_check(m, G, Hkv, table, lens, P, seed=0, scale=SCALE, extra=0, q_gain=1.0, rows=None, garbage=True):
+def widen(table, wide=True):
+    """The table with columns behind it that no row uses: no longer one of the small calls, which
+    take one launch and look for nothing that is shared."""
+    return np.pad(table, ((0, 0), (0, 100)), constant_values=-1) if wide else table
+
+
+def attend_check(m, G, Hkv, table, lens, P, **kw):
+    """Against the definition, small calls in both forms."""
+    if table.shape[1] <= 64:
+        attend_check_one(m, G, Hkv, widen(table), lens, P, **kw)
+    return attend_check_one(m, G, Hkv, table, lens, P, **kw)
+
+
+def attend_check_one(m, G, Hkv, table, lens, P, seed=0, scale=SCALE, extra=0, q_gain=1.0, rows=None, garbage=True):
     rng = np.random.default_rng(seed)
     B, Hq = len(lens), G * Hkv
     q = bf16(q_gain * rng.standard_normal((B, Hq, 128)))
@@ -273,6 +286,9 @@ def attend_check(m, G, Hkv, table, lens, P, seed=0, scale=SCALE, extra=0, q_gain
     o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
     r = m.msa_decode_shared(q, kc, vc, tt, lt, scale=scale, out=o2, lse=lse2)
     assert r[0] is o2 and torch.equal(o2, o) and torch.equal(lse2, lse)
+    o2 = q.clone()
+    m.msa_decode_shared(o2, kc, vc, tt, lt, scale=scale, out=o2)
+    assert torch.equal(o2, o)
     return q, kc, vc, tt, lt, o, lse
 
 
@@ -287,6 +303,21 @@ ROWS = [
 def test_shared_attention_of_rows_apart(m, G, Hkv, lens):
     table, lens, P = tree_table(np.random.default_rng(G), [int(n) for n in lens])
     attend_check(m, G, Hkv, table, lens, P, seed=G + Hkv)
+
+
+SMALL = [                                     # heads per KV head, KV heads, lengths, columns
+    (16, 4, [4096, 1, 0, 2048], 32), (7, 1, [129], 2), (1, 8, [257, 256, 255], 3), (16, 1, [4096, 3969, 127], 32),
+    (9, 2, [33, 31, 32, 65, 97, 128, 1, 64, 96, 127], 1), (8, 3, [512, 511, 385, 384], 4), (15, 1, [0, 0], 5),
+    (3, 2, [640, 513, 1, 0], 5), (16, 19, [1024] * 4, 8), (16, 2, [1025, 1152, 2000, 900], 31), (10, 5, [1, 130], 9),
+    (16, 4, [8192, 8065, 4096, 100], 64), (16, 2, [7000] * 19, 64), (5, 1, [3000] * 70, 32), (16, 64, [300], 3), (1, 1, [1], 1), (16, 1, [128] * 608, 1), (2, 1, [200] * 300, 2),
+]
+
+
+@pytest.mark.parametrize("G,Hkv,lens,cols", SMALL, ids=lambda v: str(v) if not isinstance(v, list) else f"{len(v)}rows{v[0]}")
+def test_shared_attention_of_few_pages(m, G, Hkv, lens, cols):
+    table, lens, P = tree_table(np.random.default_rng(cols), [int(n) for n in lens if n], maxp=cols,
+                                empties=[i for i, n in enumerate(lens) if n == 0])
+    attend_check(m, G, Hkv, table, lens, P, seed=G + cols, rows=list(range(min(len(lens), 12))))
 
 
 TREES = [
@@ -375,7 +406,8 @@ def test_shared_attention_beyond_4_gb(m):
     within(f64(lse), wlse, 2.0 ** -10, "lse")
 
 
-def test_shared_attention_bad_pages_and_lengths(m):
+@pytest.mark.parametrize("wide", [False, True])
+def test_shared_attention_bad_pages_and_lengths(m, wide):
     rng = np.random.default_rng(9)
     P, G, Hkv = 6, 4, 2
     q = bf16(rng.standard_normal((6, G * Hkv, 128)))
@@ -384,7 +416,7 @@ def test_shared_attention_bad_pages_and_lengths(m):
     for table, lens in ((good, [-1, 513, 2 ** 31 - 1, 512, 0, 77]),
                         (np.array([[0, 9, 2, 3], [0, 9, 2, -4], [-1, 1, 2, 6], [6, 6, 6, 6], [0, 1, 2, 3], [5, -2 ** 31, 0, 0]]),
                          [512, 500, 400, 300, 512, 129])):
-        lens = np.array(lens)
+        lens, table = np.array(lens), widen(table, wide)
         o, lse = m.msa_decode_shared(q, kc, vc, i32(table), i32(lens))
         with pytest.raises(m.MSAError, match="BOUNDS"):
             m.msa_check_status()
@@ -396,9 +428,11 @@ def test_shared_attention_bad_pages_and_lengths(m):
 
 
 @pytest.mark.parametrize("scale,q_gain", [(2.0 ** -64, 1.0), (2.0 ** -30, 1.0), (1.0, 30.0), (2.0 ** 20, 1.0), (2.0 ** 64, 1.0)])
-def test_shared_attention_small_and_large_logits(m, scale, q_gain):
+@pytest.mark.parametrize("wide", [False, True])
+def test_shared_attention_small_and_large_logits(m, scale, q_gain, wide):
     """Nothing but rounding where logits are all alike; one key where they are far apart."""
     table, lens, P = tree_table(np.random.default_rng(10), [(3, [100, 5] + [3] * 8), 129])
+    table = widen(table, wide)
     if scale < 1:
         attend_check(m, 16, 1, table, lens, P, scale=scale)
         return
@@ -421,10 +455,12 @@ def test_shared_attention_small_and_large_logits(m, scale, q_gain):
         within(f64(lse)[b], z[b].max(1) * scale, (e + 2.0 ** -22 * np.abs(z[b]).max()) * scale + 7, "lse")
 
 
-def test_shared_attention_products_of_minus_infinity(m):
+@pytest.mark.parametrize("wide", [False, True])
+def test_shared_attention_products_of_minus_infinity(m, wide):
     """Keys whose products are -infinity weigh nothing, be it whole blocks, pages or parts of a row;
     a head that has no others counts as one without keys."""
     table, lens, P = tree_table(np.random.default_rng(13), [(5, [40] * 18), (3, [0, 300]), 700, 130], empties=())
+    table = widen(table, wide)
     rng = np.random.default_rng(14)
     q = bf16(rng.standard_normal((len(lens), 16, 128)))
     q[:, :, 5] = 1.0
@@ -445,9 +481,11 @@ def test_shared_attention_products_of_minus_infinity(m):
     within(f64(lse)[~none], wlse[~none], 2.0 ** -10, "lse")
 
 
-def test_shared_attention_rows_and_heads_do_not_mix(m):
+@pytest.mark.parametrize("wide", [False, True])
+def test_shared_attention_rows_and_heads_do_not_mix(m, wide):
     """A query row, or a row's own keys, that hold infinities or NaN change no other row."""
     table, lens, P = tree_table(np.random.default_rng(12), [(2, [40] * 12), 200])
+    table = widen(table, wide)
     q, kc, vc, tt, lt, o, lse = attend_check(m, 16, 2, table, lens, P)
     bad = q.clone()
     bad[3, 5], bad[7, 20] = float("nan"), float("inf")
@@ -744,12 +782,13 @@ def loop_state(m, N, W, Hkv, G, prompt, maxp=6, V=97, seed=0):
     return st
 
 
-def test_beam_search_loop(m):
+@pytest.mark.parametrize("maxp", [6, 100])
+def test_beam_search_loop(m, maxp):
     """Prompts stored, forked to their beams and searched: every call against its definition, and
     at the end each row's pages hold the tokens that led to it."""
     N, W, Hkv, G, steps = 3, 4, 2, 3, 9
     prompt = [250, 129, 120]
-    st = loop_state(m, N, W, Hkv, G, prompt)
+    st = loop_state(m, N, W, Hkv, G, prompt, maxp=maxp)
     B, Hq, V = N * W, Hkv * G, st["V"]
     split = lambda e: (e[:, :Hq].contiguous(), e[:, Hq:Hq + Hkv].contiguous(), e[:, Hq + Hkv:].contiguous())   # noqa: E731
     toks = [st["rng"].integers(0, V, n) for n in prompt]
@@ -797,11 +836,12 @@ def test_beam_search_loop(m):
         assert torch.equal(rows, emb[torch.tensor(history[b])])
 
 
-def test_captured_loop_follows_the_tables(m):
+@pytest.mark.parametrize("maxp", [5, 100])
+def test_captured_loop_follows_the_tables(m, maxp):
     """A step captured once and replayed while rows change places: what is shared is found out
     at each replay.  Beside it a second captured step on another stream with its own workspace."""
     N, W, Hkv, G = 2, 3, 1, 16
-    table, lens, P = tree_table(np.random.default_rng(20), [(2, [100, 30, 64]), (1, [200, 128, 5])], maxp=5)
+    table, lens, P = tree_table(np.random.default_rng(20), [(2, [100, 30, 64]), (1, [200, 128, 5])], maxp=maxp)
     B = len(lens)
     rng = np.random.default_rng(21)
     kc, vc = (bf16(rng.standard_normal((P + 30, Hkv, 128, 128))) for _ in range(2))
@@ -853,7 +893,7 @@ d = 'cuda'; bf = dict(dtype=torch.bfloat16, device=d); i32 = dict(dtype=torch.in
 B = 5
 q, k = torch.randn(B, 32, 128, **bf), torch.randn(B, 2, 128, **bf)
 kc, vc = torch.randn(9, 2, 128, 128, **bf), torch.randn(9, 2, 128, 128, **bf)
-table = torch.tensor([[0, 1, 2 + b] for b in range(B)], **i32)
+table = torch.tensor([[0, 1, 2 + b] + [-1] * {more} for b in range(B)], **i32)
 lens, ref = torch.full((B,), 300, **i32), torch.tensor([5, 5, 1, 1, 1, 1, 1, 0, 0], **i32)
 cu, x, s = torch.arange(B + 1, **i32), torch.randn(B, 999, device=d), torch.zeros(B, device=d)
 rope, m_ = m.msa_rope(64), m
@@ -873,7 +913,8 @@ print('first ok')
 """
 
 
-def test_first_calls_of_a_process_are_captured(m):
+@pytest.mark.parametrize("more", [0, 100])
+def test_first_calls_of_a_process_are_captured(m, more):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root)], capture_output=True, text=True, timeout=300)
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root, more=more)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "first ok" in r.stdout, r.stdout + r.stderr
