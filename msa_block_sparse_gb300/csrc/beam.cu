@@ -651,11 +651,12 @@ struct BeamWorkspace {
 // Slices of a row: the number that makes (rounds of CTAs over the GPU) x (a CTA's time) least.
 // A thread spends about 7 instructions on a value and 700 on the CTA's start, bound and ranking;
 // a slice costs the merge about as much as 4 values.  No slice under 1024 values, and a prompt's
-// candidates within what the merge takes.
+// candidates within what the merge takes.  16 rounds even out the last one.
 int beam_slices(long long rows, int W, int V, int K) {
   const long long cap = 4LL * device_sm_count();
   long long most = V / 1024;
   if (most > kBmCandidates / (W * K)) most = kBmCandidates / (W * K);
+  if (most > 16 * cap / rows) most = 16 * cap / rows;
   long long best = 1, least = 0;
   for (long long s = 1; s <= most || s == 1; ++s) {
     const long long rounds = (rows * s + cap - 1) / cap;
@@ -676,6 +677,12 @@ BeamWorkspace carve_beam_workspace(WsCursor& ws, long long rows, int slices, int
   return w;
 }
 
+size_t beam_bytes(long long rows, int slices, int K) {
+  WsCursor ws(nullptr);
+  carve_beam_workspace(ws, rows, slices, K);
+  return ws.used + 256;
+}
+
 bool beam_sizes_ok(int N, int W, int V, int K) {
   return N >= 1 && W >= 1 && W <= kBmMaxW && V >= 1 && V <= (1 << 24) && K >= 1 && K <= kBmMaxK &&
          static_cast<long long>(K) <= static_cast<long long>(W) * V &&
@@ -692,10 +699,8 @@ extern "C" {
 
 size_t msa_beam_select_workspace_size(int N, int W, int V, int K) {
   if (!beam_sizes_ok(N, W, V, K)) return 0;
-  WsCursor ws(nullptr);
   const long long rows = static_cast<long long>(N) * W;
-  carve_beam_workspace(ws, rows, beam_slices(rows, W, V, K), K);
-  return ws.used + 256;
+  return beam_bytes(rows, beam_slices(rows, W, V, K), K);
 }
 
 msa_status_t msa_beam_select(const void* logits, int dtype, int64_t row_stride, const float* scores,
@@ -727,10 +732,9 @@ msa_status_t msa_beam_select(const void* logits, int dtype, int64_t row_stride, 
   // a prompt's CTA reads its own W scores before it writes its K: in place where they are the same
   if (overlap(scores_out, 4ull * N * K, scores, 4ull * N * W) && !(scores_out == scores && K == W))
     return fail(MSA_ERR_INVALID_ARG, "scores_out overlaps scores (it may be scores where K = W)");
-  if (workspace_bytes < msa_beam_select_workspace_size(N, W, V, K))
-    return fail(MSA_ERR_INVALID_ARG, "workspace too small");
   const long long rows = static_cast<long long>(N) * W;
   const int slices = beam_slices(rows, W, V, K);
+  if (workspace_bytes < beam_bytes(rows, slices, K)) return fail(MSA_ERR_INVALID_ARG, "workspace too small");
   WsCursor ws(workspace);
   const BeamWorkspace w = carve_beam_workspace(ws, rows, slices, K);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
