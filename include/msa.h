@@ -448,7 +448,7 @@ MSA_API msa_status_t msa_cache_append(const void* q, const void* k, const void* 
  * full pages that they have in common are read once for all of them, at up to 6
  * levels (a system prompt, behind it a prompt of each user, behind that its samples); so
  * put rows that share next to each other.  This is found out on the device in each call; calls
- * with G <= 16 whose tables are small (max_pages <= 64, few pages in all) read every row by itself,
+ * with G <= 16 whose tables are small (max_pages <= 128, few pages in all) read every row by itself,
  * which then takes less time.
  * A row with cache_lens[b] = 0 gets o = 0 and lse = -infinity, and so does a head whose
  * products are all -infinity; lengths outside [0, 128 max_pages] set MSA_STATUS_BOUNDS and are

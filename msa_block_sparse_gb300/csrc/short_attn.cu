@@ -376,16 +376,16 @@ static int short_ctas(int rows, int max_pages) {
 }
 
 // Few pages in all, and few of a row, so that reading every row by itself, mostly from L2 where
-// rows share, costs less than finding out what they share.  On tables of that size, this
-// kernel against the three of shared_attn.cu: 4 heads, 1 row x 4 pages 3.7 us against 13.0; 4 x 13,
-// 11 of them shared, 6.0 against 15.7; 8 x 64 all different 23 against 38, all shared 14 against 22;
-// 24 x 24 26 against 47 and 20 against 30.  The border is where all shared would lose: 16 x 64 24
-// against 26, 35 x 71 (2 heads) 38 against 31; and where few CTAs walk a long row: 1 x 64 11 against 20,
-// 1 x 128 20 against 22.
+// rows share, costs less than finding out what they share.  This kernel against the three of
+// shared_attn.cu on the same tables (16 heads per KV head): 1 row x 4 pages x 4 KV heads 3.7 us against
+// 13.0; 4 x 13 x 4, 11 of them shared, 6.0 against 15.7; 8 x 64 x 4 all different 23 against 38, all shared 14
+// against 22; 16 x 64 x 4 32 against 47 half full, 24 against 26 all shared.  The borders are where all
+// shared or a CTA's many pages would lose: 256 x 32 55 against 65 half full, but 51 against 49 with
+// half of them shared; 70 rows x 71 pages 38 against 31; 4 rows x 128 pages 20 against 22.
 bool short_attn_fits(int B, int G, int Hkv, int max_pages) {
   const long long rows = static_cast<long long>(B) * Hkv;
-  return G <= 16 && max_pages <= 64 && rows * max_pages <= 16LL * device_sm_count() &&
-         max_pages <= 32 * short_ctas(static_cast<int>(rows), max_pages);    // a lane per page of a CTA
+  return G <= 16 && max_pages <= 128 && rows * max_pages <= 32LL * device_sm_count() &&
+         max_pages <= 20 * short_ctas(static_cast<int>(rows), max_pages);    // a lane per page of a CTA
 }
 
 msa_status_t launch_short_attn(const ShortAttn& a, cudaStream_t stream) {

@@ -235,12 +235,12 @@ def tree_table(rng, groups, maxp=None, empties=()):
 def widen(table, wide=True):
     """The table with columns behind it that no row uses: no longer one of the small calls, which
     take one launch and look for nothing that is shared."""
-    return np.pad(table, ((0, 0), (0, 100)), constant_values=-1) if wide else table
+    return np.pad(table, ((0, 0), (0, 200)), constant_values=-1) if wide else table
 
 
 def attend_check(m, G, Hkv, table, lens, P, **kw):
     """Against the definition, small calls in both forms."""
-    if table.shape[1] <= 64:
+    if table.shape[1] <= 128:
         attend_check_one(m, G, Hkv, widen(table), lens, P, **kw)
     return attend_check_one(m, G, Hkv, table, lens, P, **kw)
 
@@ -309,7 +309,7 @@ SMALL = [                                     # heads per KV head, KV heads, len
     (16, 4, [4096, 1, 0, 2048], 32), (7, 1, [129], 2), (1, 8, [257, 256, 255], 3), (16, 1, [4096, 3969, 127], 32),
     (9, 2, [33, 31, 32, 65, 97, 128, 1, 64, 96, 127], 1), (8, 3, [512, 511, 385, 384], 4), (15, 1, [0, 0], 5),
     (3, 2, [640, 513, 1, 0], 5), (16, 19, [1024] * 4, 8), (16, 2, [1025, 1152, 2000, 900], 31), (10, 5, [1, 130], 9),
-    (16, 4, [8192, 8065, 4096, 100], 64), (16, 2, [7000] * 19, 64), (5, 1, [3000] * 70, 32), (16, 64, [300], 3), (1, 1, [1], 1), (16, 1, [128] * 608, 1), (2, 1, [200] * 300, 2),
+    (16, 4, [8192, 8065, 4096, 100], 64), (16, 2, [7000] * 19, 64), (16, 2, [16384, 129, 16000], 128), (4, 4, [2500] * 60, 20), (8, 2, [4700] * 60, 40), (5, 1, [3000] * 70, 32), (16, 64, [300], 3), (1, 1, [1], 1), (16, 1, [128] * 608, 1), (2, 1, [200] * 300, 2),
 ]
 
 
@@ -782,7 +782,7 @@ def loop_state(m, N, W, Hkv, G, prompt, maxp=6, V=97, seed=0):
     return st
 
 
-@pytest.mark.parametrize("maxp", [6, 100])
+@pytest.mark.parametrize("maxp", [6, 200])
 def test_beam_search_loop(m, maxp):
     """Prompts stored, forked to their beams and searched: every call against its definition, and
     at the end each row's pages hold the tokens that led to it."""
@@ -836,7 +836,7 @@ def test_beam_search_loop(m, maxp):
         assert torch.equal(rows, emb[torch.tensor(history[b])])
 
 
-@pytest.mark.parametrize("maxp", [5, 100])
+@pytest.mark.parametrize("maxp", [5, 200])
 def test_captured_loop_follows_the_tables(m, maxp):
     """A step captured once and replayed while rows change places: what is shared is found out
     at each replay.  Beside it a second captured step on another stream with its own workspace."""
@@ -913,7 +913,7 @@ print('first ok')
 """
 
 
-@pytest.mark.parametrize("more", [0, 100])
+@pytest.mark.parametrize("more", [0, 200])
 def test_first_calls_of_a_process_are_captured(m, more):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST.format(root=root, more=more)], capture_output=True, text=True, timeout=300)
