@@ -10,7 +10,7 @@
 // asynchronous stores into the one that finishes a row.
 //
 // Bound by latency in the smallest calls (launch, lengths and table entries, K and V, the joining: 4
-// rows of 1,500 tokens, 64 heads on 4, 6.0 us), by memory in the largest (8 rows of 8k tokens, 134 MB, 23
+// rows of 1,500 tokens, 64 heads on 4, 5.6 us), by memory in the largest (8 rows of 8k tokens, 134 MB, 23
 // us, 5.8 TB/s).  K and V each have one buffer, which refills while the other is in use: two of each
 // leave room for one CTA per SM, and half of the clusters wait (4 rows x 13 pages 6.4 -> 10.1 us).
 #include <cfloat>
