@@ -2,7 +2,7 @@
 // best score s_w + log softmax(x_w)_v.
 //
 // Bound by memory in the limit: the logits are read once (the only large input).  Measured: 32
-// prompts x 8 beams x 131,072 bf16 logits 25.8 us, of which the scan takes about 17 (67 MB, 3.9
+// prompts x 8 beams x 131,072 bf16 logits 25 us, of which the scan takes about 17 (67 MB, 3.9
 // TB/s; an exponential per value and its end fill half of the issue slots) and the merge 5; 4
 // beams x 32,000 fp32 7.4 us, latency.
 //
@@ -648,20 +648,25 @@ struct BeamWorkspace {
   unsigned long long* keys;
 };
 
-// Slices of a row: the number that makes (rounds of CTAs over the GPU) x (a CTA's time) least.
-// A thread spends about 7 instructions on a value and 700 on the CTA's start, bound and ranking;
-// a slice costs the merge about as much as 4 values.  No slice under 1024 values, and a prompt's
-// candidates within what the merge takes.  16 rounds even out the last one.
+// Slices of a row: the number that makes the time least.  A thread spends about 7 instructions on
+// a value and 700 on the CTA's start, bound and ranking; with c CTAs on an SM the pass over the
+// values, which waits for memory, takes 0.3 c times as long and the rest 0.8 c (not less than once).  A slice
+// costs the merge about as much as 4 values, and a candidate beyond one per thread half an
+// instruction of each (its score in 64 bits).  Measured against counting rounds of 4 CTAs per SM alone, candidates
+// for free: 16 prompts x 4 x 50,000 10.3 us and 11.7, 19 x 5 x 50,001 11.8 and 13.1, 4 x 16 x 50,000 (K = 16) 13.1 and
+// 21.4, 1 x 32 x 100,000 (K = 32) 25 and 65, but 64 x 4 x 32,000 14.4 and 13.5.  No slice under 1024 values, and a
+// prompt's candidates within what the merge takes.
 int beam_slices(long long rows, int W, int V, int K) {
-  const long long cap = 4LL * device_sm_count();
+  const long long sms = device_sm_count();
   long long most = V / 1024;
   if (most > kBmCandidates / (W * K)) most = kBmCandidates / (W * K);
-  if (most > 16 * cap / rows) most = 16 * cap / rows;
+  if (most > 64 * sms / rows) most = 64 * sms / rows;        // more even nothing out
   long long best = 1, least = 0;
   for (long long s = 1; s <= most || s == 1; ++s) {
-    const long long rounds = (rows * s + cap - 1) / cap;
+    const long long c = (rows * s + sms - 1) / sms, scan = c > 3 ? 3 * c : 10, rest = c > 1 ? 8 * c : 10;
     const long long tiles = (V + kBmTile * s - 1) / (kBmTile * s);
-    const long long time = rounds * (tiles * kBmValues * 7 + 700) + 26 * s;
+    const long long more = W * K * s - kBmMergeThreads;
+    const long long time = (scan * tiles * kBmValues * 7 + rest * 700) / 10 + 26 * s + (more > 0 ? more / 2 : 0);
     if (s == 1 || time < least) {
       least = time;
       best = s;
