@@ -547,6 +547,7 @@ BEAMS = [
     (1, 1, 1, 1, "f", 0, 0, 0), (1, 1, 64, 64, "b", 0, 0, 0), (1, 4, 32000, 4, "f", 0, 0, 0), (3, 5, 1009, 10, "f", 1, 0, 0.3),
     (2, 8, 4097, 16, "b", 3, 0.5, 0), (5, 2, 8193, 33, "b", 7, 0, 0.5), (1, 64, 700, 64, "f", 5, 0.9, 0), (2, 3, 100000, 64, "b", 0, 0, 0),
     (40, 4, 333, 5, "f", 11, 0.99, 0.2), (300, 2, 50, 3, "b", 0, 0, 0), (2, 2, 1 << 20, 8, "b", 1, 0, 0), (7, 3, 4, 12, "f", 0, 0.5, 0.5),
+    (1, 64, 32000, 64, "b", 0, 0, 0.1), (4, 16, 50000, 16, "f", 1, 0, 0), (1, 32, 100000, 32, "b", 3, 0.5, 0),
 ]
 
 
