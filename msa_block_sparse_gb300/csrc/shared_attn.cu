@@ -30,7 +30,7 @@
 // Bound by memory where little is shared: 64 rows of 8k to 32k tokens, 64 heads on 4, 380 us (2.5
 // GB, 6.6 TB/s).  Prefixes of 8k to 32k shared by 8 rows each: 94 us (443 MB).  One of 16k shared
 // by 64 rows with up to 4k of their own: 94 us (348 MB, 40 GFLOP), the plan about 9 of them.  4
-// rows of 1,500 tokens: 15.4 us, latency (short_attn.cu takes such calls where the tables are small: 5.6).
+// rows of 1,500 tokens: 15.4 us, latency (short_attn.cu takes such calls where the tables are small: 5.8).
 #include <cfloat>
 #include <cmath>
 #include "kernels.cuh"

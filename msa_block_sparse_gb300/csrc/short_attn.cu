@@ -10,7 +10,7 @@
 // asynchronous stores into the one that finishes a row.
 //
 // Bound by latency in the smallest calls (launch, lengths and table entries, K and V, the joining: 4
-// rows of 1,500 tokens, 64 heads on 4, 5.6 us), by memory in the largest (8 rows of 8k tokens, 134 MB, 23
+// rows of 1,500 tokens, 64 heads on 4, 5.8 us), by memory in the largest (8 rows of 8k tokens, 134 MB, 23
 // us, 5.8 TB/s).  K and V each have one buffer, which refills while the other is in use: two of each
 // leave room for one CTA per SM, and half of the clusters wait (4 rows x 13 pages 6.4 -> 10.1 us).
 #include <cfloat>
@@ -67,7 +67,7 @@ __device__ __forceinline__ int sh_at(int r, int chunk) { return r * kD + 4 * (ch
 // (g >> 1) + 4 (g & 1), so that 16-byte loads of K meet no bank twice; the channels of
 // two k-steps are a thread's 8 consecutive ones, for q and K alike.
 template <int NS>
-__global__ void __launch_bounds__(kShThreads) short_attn_kernel(
+__global__ void __launch_bounds__(kShThreads, 3) short_attn_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __nv_bfloat16* q, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
     int G, int Hkv, int num_pages, int max_pages, float sl2, __nv_bfloat16* o,
@@ -338,12 +338,32 @@ __global__ void __launch_bounds__(kShThreads) short_attn_kernel(
   }
 }
 
+// CTAs per (row, KV head), and how many of them an SM takes: two where all of them then run side by
+// side (three would crowd some SMs: 16 x 4 rows of 8 pages 6.2 us and 7.7), else three.  Clusters leave
+// gaps: of 304 places those of 4 CTAs fill about 285, those of 8 266.  More CTAs than run at two per SM
+// pay where each keeps 4 pages or more (24 x 4 rows of 16 pages 11.3 us with 4 CTAs, 14.8 with 2; 76 rows of
+// 8 7.8 and 7.5).
+struct ShortPlan {
+  int ctas, per_sm;
+};
+static ShortPlan short_plan(int rows, int max_pages) {
+  const int sms = device_sm_count();
+  auto places = [&](int n) { return n == 8 ? 7 * sms / 4 : n == 4 ? 15 * sms / 8 : 2 * sms; };
+  for (int n = 8; n > 1; n /= 2) {
+    if (max_pages <= n / 2) continue;
+    if (n * rows <= places(n)) return {n, 2};
+    if (2 * n * rows <= 3 * places(n) && max_pages >= 4 * n) return {n, 3};
+  }
+  return {1, rows <= places(1) ? 2 : 3};
+}
+
 namespace {
 
 template <int NS>
-msa_status_t launch_short(const ShortAttn& a, cudaStream_t st, uint32_t* sw) {
-  constexpr size_t kSmem = 2 * kShTile + 1024;
-  MSA_TRY(ensure_smem(short_attn_kernel<NS>, kSmem, "short_attn_kernel"));
+msa_status_t launch_short(const ShortAttn& a, int per_sm, cudaStream_t st, uint32_t* sw) {
+  // a third of an SM's shared memory; so much more that only two fit
+  constexpr size_t kSmem = 2 * kShTile + 1024, kMore = 16384;
+  MSA_TRY(ensure_smem(short_attn_kernel<NS>, kSmem + kMore, "short_attn_kernel"));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -354,7 +374,7 @@ msa_status_t launch_short(const ShortAttn& a, cudaStream_t st, uint32_t* sw) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(NS, static_cast<unsigned>(a.B * a.Hkv));
   cfg.blockDim = kShThreads;
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = kSmem + (per_sm == 2 ? kMore : 0);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -365,38 +385,29 @@ msa_status_t launch_short(const ShortAttn& a, cudaStream_t st, uint32_t* sw) {
 
 }  // namespace
 
-// CTAs per (row, KV head): as many as its pages can keep busy and run side by side, up to 7 on 4
-// SMs (clusters leave gaps; 76 rows of 8 pages 10.2 us in clusters of 4, 7.6 of 2; 64 rows 6.2 in
-// clusters of 4, 7.5 of 2)
-static int short_ctas(int rows, int max_pages) {
-  const int most = device_sm_count() * 7 / 4;
-  for (int n = 8; n > 1; n /= 2)
-    if (max_pages > n / 2 && n * rows <= most) return n;
-  return 1;
-}
-
 // Few pages in all, and few of a row, so that reading every row by itself, mostly from L2 where
 // rows share, costs less than finding out what they share.  This kernel against the three of
-// shared_attn.cu on the same tables (16 heads per KV head): 1 row x 4 pages x 4 KV heads 3.7 us against
-// 13.0; 4 x 13 x 4, 11 of them shared, 6.0 against 15.7; 8 x 64 x 4 all different 23 against 38, all shared 14
-// against 22; 16 x 64 x 4 32 against 47 half full, 24 against 26 all shared.  The borders are where all
-// shared or a CTA's many pages would lose: 256 x 32 55 against 65 half full, but 51 against 49 with
-// half of them shared; 70 rows x 71 pages 38 against 31; 4 rows x 128 pages 20 against 22.
+// shared_attn.cu on the same tables (16 heads per KV head, 4 KV heads): 1 row x 4 pages 3.7 us against 13.0; 4 x 13,
+// 11 of them shared, 6.0 against 15.9; 8 x 64 all different 23 against 38, all shared 14.9 against 22.5; 24 x 60
+// up to 60 pages each 34 against 53, all 60 shared 29 against 35 (26.6 with 2 heads).  The borders are where rows that
+// are full and share everything take as long in either form: 20 x 70 33.7 and 34.5, 16 x 80 30.9 and 29.9, 10 x 125
+// 30.4 and 30.7; and where a CTA walks many pages alone: 1 x 128 20.6 and 22.0.
 bool short_attn_fits(int B, int G, int Hkv, int max_pages) {
   const long long rows = static_cast<long long>(B) * Hkv;
-  return G <= 16 && max_pages <= 128 && rows * max_pages <= 32LL * device_sm_count() &&
-         max_pages <= 20 * short_ctas(static_cast<int>(rows), max_pages);    // a lane per page of a CTA
+  return G <= 16 && max_pages <= 128 && rows * max_pages <= 40LL * device_sm_count() &&
+         max_pages <= 20 * short_plan(static_cast<int>(rows), max_pages).ctas;    // a lane per page of a CTA
 }
 
 msa_status_t launch_short_attn(const ShortAttn& a, cudaStream_t stream) {
   uint32_t* sw = nullptr;
   MSA_TRY(status_word(&sw));
   TraceScope trace_("short_attn_kernel", stream);
-  switch (short_ctas(a.B * a.Hkv, a.max_pages)) {
-    case 8: return launch_short<8>(a, stream, sw);
-    case 4: return launch_short<4>(a, stream, sw);
-    case 2: return launch_short<2>(a, stream, sw);
-    default: return launch_short<1>(a, stream, sw);
+  const ShortPlan plan = short_plan(a.B * a.Hkv, a.max_pages);
+  switch (plan.ctas) {
+    case 8: return launch_short<8>(a, plan.per_sm, stream, sw);
+    case 4: return launch_short<4>(a, plan.per_sm, stream, sw);
+    case 2: return launch_short<2>(a, plan.per_sm, stream, sw);
+    default: return launch_short<1>(a, plan.per_sm, stream, sw);
   }
 }
 
