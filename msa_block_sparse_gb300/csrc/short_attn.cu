@@ -70,9 +70,8 @@ template <int NS>
 __global__ void __launch_bounds__(kShThreads, 3) short_attn_kernel(
     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
     const __nv_bfloat16* q, const int32_t* __restrict__ table, const int32_t* __restrict__ lens,
-    int G, int Hkv, int num_pages, int max_pages, float sl2, __nv_bfloat16* o,
-   
-    float* __restrict__ lse, uint32_t* status) {
+    int G, int Hkv, int num_pages, int max_pages, float sl2, __nv_bfloat16* o, float* __restrict__ lse,
+    uint32_t* status) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ ShortSmem<NS> sm;
   // K, then V of a page; later the warps' sums
