@@ -128,9 +128,9 @@ __device__ __forceinline__ float bm_scale(float d) {
   return d < -126.f ? 0.f : __int_as_float((static_cast<int>(d) + 127) << 23);
 }
 
-// NaN counts as -infinity, +infinity as the largest finite value
+// NaN counts as -infinity, +infinity as the largest finite value, -0 as 0: keys go by the bits
 __device__ __forceinline__ float plain(float x) {
-  return x != x ? -INFINITY : fminf(x, FLT_MAX);
+  return x != x ? -INFINITY : x == 0.f ? 0.f : fminf(x, FLT_MAX);
 }
 
 struct ScanSmem {
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
       }
     }
     if (lane == 0) {
-      sm.score[w] = live ? static_cast<double>(s) : -INFINITY;
+      sm.score[w] = live ? (s == 0.f ? 0.0 : static_cast<double>(s)) : -INFINITY;   // -0 is 0
       sm.lse[w] = ended || ref == -INFINITY ? 0.0 : bm_log(hi, lo, ref);   // no candidates: no matter
       sm.huge[w] = fabsf(ref) >= kBmHuge;
     }

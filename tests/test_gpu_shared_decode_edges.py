@@ -1,0 +1,56 @@
+"""Append, shared attention and beam selection on the GPU where values that count as equal, long
+sums or overlapping storage could go wrong.  Helpers and definitions are those of
+test_gpu_shared_decode.py, and so are the tolerances, in the form derived there: scores within
+2^-20 + 2^-24 |score|."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import shared_oracle as S
+from tests import test_gpu_shared_decode as base
+
+pytestmark = pytest.mark.gpu
+m = base.m
+DEV, f64, within = base.DEV, base.f64, base.within
+
+
+# ------------------------------------------------------------------ values that count as equal
+
+def choice(m, x, scores, W, K, **kw):
+    """The very choice of the definition: for rows whose different scores are far apart."""
+    so, po, to = m.msa_beam_select(x, scores, W, K, **kw)
+    m.msa_check_status()
+    fin = kw.get("finished")
+    ws, wp, wt = S.beam_select(f64(x), f64(scores), W, K, None if fin is None else fin.cpu().numpy(), kw.get("pad_token", 0))
+    assert np.array_equal(to.cpu().numpy(), wt), (to.cpu().numpy(), wt)
+    assert np.array_equal(po.cpu().numpy(), wp)
+    live = ws > -np.inf
+    assert (f64(so)[~live] == -np.inf).all()
+    within(f64(so)[live], ws[live], 2.0 ** -20 + 2.0 ** -24 * np.abs(ws[live]), "score")
+
+
+def generator(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,K", [(4, 1), (50, 3), (5000, 16), (5000, 64), (70001, 20)])
+def test_zeros_of_either_sign_are_equal(m, dt, V, K):
+    g = generator(V + K)
+    x = torch.full((2, V), -1.0, device=DEV)
+    many = torch.rand(2, V, generator=g, device=DEV) < 0.6                  # some of these K or more
+    x[many] = 0.0
+    x[many & (torch.rand(2, V, generator=g, device=DEV) < 0.5)] = -0.0
+    x[:, 0], x[:, 1] = -0.0, 0.0
+    choice(m, x.to(dt), torch.tensor([-1.0, -1.5], device=DEV), 1, K)
+    x[:, 2:] = -1.0                                                         # a few
+    choice(m, x.to(dt), torch.tensor([-1.0, -1.5], device=DEV), 1, 1)
+
+
+def test_scores_of_zeros_of_either_sign_are_equal(m):
+    x, s = torch.zeros(6, 10, device=DEV), torch.tensor([-0.0, 0.0, -0.0, 0.0, -0.0, 0.0], device=DEV)
+    fin = torch.ones(6, dtype=torch.bool, device=DEV)
+    for W, K in ((2, 1), (3, 2), (6, 4), (6, 6)):
+        choice(m, x, s, W, K, finished=fin, pad_token=7)
