@@ -21,7 +21,6 @@
 // particular order about 1.4 K do.  These few are ranked by counting.  Where far more reach
 // it (equal values at the border), the slice is taken tile by tile with unique keys (value,
 // then the lower index): at most the K best threads hold anything above the bound then.
-#include <cfloat>
 #include "kernels.cuh"
 
 namespace msa {
@@ -128,9 +127,9 @@ __device__ __forceinline__ float bm_scale(float d) {
   return d < -126.f ? 0.f : __int_as_float((static_cast<int>(d) + 127) << 23);
 }
 
-// NaN counts as -infinity, +infinity as the largest finite value, -0 as 0: keys go by the bits
+// NaN counts as -infinity, what lies above 2^28 as 2^28, -0 as 0: keys go by the bits
 __device__ __forceinline__ float plain(float x) {
-  return x != x ? -INFINITY : x == 0.f ? 0.f : fminf(x, FLT_MAX);
+  return x != x ? -INFINITY : x == 0.f ? 0.f : fminf(x, kBmHuge);
 }
 
 struct ScanSmem {

@@ -54,3 +54,21 @@ def test_scores_of_zeros_of_either_sign_are_equal(m):
     fin = torch.ones(6, dtype=torch.bool, device=DEV)
     for W, K in ((2, 1), (3, 2), (6, 4), (6, 6)):
         choice(m, x, s, W, K, finished=fin, pad_token=7)
+
+
+HUGE = [50, 5000, 70001, 300000]
+
+
+@pytest.mark.parametrize("V", HUGE)
+def test_values_above_the_limit_are_equal(m, V):
+    """What lies above 2^28 counts as 2^28: the lowest places are chosen, not the largest values."""
+    g = generator(V)
+    x = torch.randn(3, V, generator=g, device=DEV)
+    up = torch.rand(3, V, generator=g, device=DEV) < 0.5
+    x = torch.where(up, 2.0 ** (29 + 90 * torch.rand(3, V, generator=g, device=DEV)), x)
+    x[1, V // 2:] = math.inf
+    x[2, :V // 3] = -1.0
+    for dt in (torch.float32, torch.bfloat16):
+        for W, K in ((1, 1), (1, 5), (3, 16)):
+            choice(m, x.to(dt), torch.tensor([-1.0, -2.0, -30.0], device=DEV), W, K)
+    choice(m, torch.tensor([[3e8, 4e8, 0.0, 0.0]], device=DEV), torch.zeros(1, device=DEV), 1, 1)
