@@ -40,6 +40,7 @@ constexpr int kBmMergeThreads = 512;
 constexpr float kBmLog2e = 1.4426950216293335f;        // log2 e in fp32, 1.33e-8 of it too small
 constexpr double kBmLn2 = 0.69314718055994530942, kBmRef = kBmLn2 * (1.4426950408889634 / 1.4426950216293335);
 constexpr float kBmHuge = 0x1p28f;                     // beyond: |x log2 e - ref| could overflow 2^127
+constexpr float kBmLow = -0x1p29f;                     // reference of values below -2^28 alone: below any other
 
 // Order of floats as order of unsigned integers (0: below -infinity, used for "nothing")
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -62,7 +63,7 @@ __device__ __forceinline__ unsigned long long key_of(float x, uint32_t idx) {
 // Sum of e^x of a slice: sum * 2^ref, ref a whole number (-infinity: the sum is 0), so that
 // joining two sums rounds nothing but the addition.  Exponents are x times fp32's log2 e, whose
 // 1.33e-8 is put right for x = ref ln 2, from which the terms that count are a few away:
-// ref ln 2 (1 + 1.33e-8) stands for ref.
+// ref ln 2 (1 + 1.33e-8) stands for ref.  ref = kBmLow: nothing above -2^28, sum is a count.
 struct BeamScan {
   float ref, sum;
 };
@@ -252,32 +253,33 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
     // ---- maximum and sum of exponentials of this thread's values.  x log2 e - ref with ref
     // whole is rounded relative to itself, however large x is.
     float best = -INFINITY, part = 0.f, to = ref;
-    auto scan = [&](float most) {
+    auto scan = [&]() {
       best = fmaxf(val[0], val[1]);
 #pragma unroll
       for (int i = 2; i < kBmValues; i += 2) best = max3f(best, val[i], val[i + 1]);
-      to = fmaxf(ref, rintf(fminf(fmaxf(best, -most), most) * kBmLog2e));
+      to = fmaxf(ref, rintf(best * kBmLog2e));
       const float2 hi = make_float2(kBmLog2e, kBmLog2e);
       const float2 r = make_float2(-to, -to);
       float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int i = 0; i < kBmValues; i += 2) {
-        float2 x = make_float2(val[i], val[i + 1]);
-        if (most < INFINITY) {                           // the ends, but for -infinity, count as +-2^28
-          x.x = x.x > -INFINITY ? fminf(fmaxf(x.x, -most), most) : x.x;
-          x.y = x.y > -INFINITY ? fminf(fmaxf(x.y, -most), most) : x.y;
-        }
-        const float2 y = __ffma2_rn(x, hi, r);
+        const float2 y = __ffma2_rn(make_float2(val[i], val[i + 1]), hi, r);
         acc[(i >> 1) & 1] = __fadd2_rn(acc[(i >> 1) & 1], make_float2(bm_ex2(y.x), bm_ex2(y.y)));
       }
       const float2 a = __fadd2_rn(acc[0], acc[1]);
       part = a.x + a.y;
     };
-    scan(INFINITY);
+    scan();
     if (best > -INFINITY && !(part < INFINITY && fabsf(best) < kBmHuge)) {   // NaN, +infinity, huge
 #pragma unroll
       for (int i = 0; i < kBmValues; ++i) val[i] = plain(val[i]);
-      scan(kBmHuge);
+      scan();
+      if (best < -kBmHuge) {                             // they count where the beam has nothing else, and alike
+        to = fmaxf(ref, kBmLow);
+        part = 0.f;
+#pragma unroll
+        for (int i = 0; i < kBmValues; ++i) part += val[i] > -INFINITY && to == kBmLow ? 1.f : 0.f;
+      }
     }
     if (best > -INFINITY) {
       if (to != ref) sum = ref > -INFINITY ? sum * bm_scale(ref - to) : 0.f;
@@ -443,7 +445,7 @@ struct MergeSmem {
   unsigned long long gs[kBmGroups];
   uint32_t gat[kBmGroups];
   double lse[kBmMaxW], score[kBmMaxW];
-  bool huge[kBmMaxW];                  // the sum counts values cut at +-2^28
+  bool low[kBmMaxW];                   // nothing above -2^28: all that is there counts as -2^28
   unsigned long long bound_s;
   uint32_t bound_at;
   int count;
@@ -548,8 +550,9 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
     }
     if (lane == 0) {
       sm.score[w] = live ? (s == 0.f ? 0.0 : static_cast<double>(s)) : -INFINITY;   // -0 is 0
-      sm.lse[w] = ended || ref == -INFINITY ? 0.0 : bm_log(hi, lo, ref);   // no candidates: no matter
-      sm.huge[w] = fabsf(ref) >= kBmHuge;
+      const bool low = ref == kBmLow;
+      sm.lse[w] = ended || ref == -INFINITY ? 0.0 : bm_log(hi, lo, low ? 0.f : ref) - (low ? kBmHuge : 0.f);   // no candidates: no matter
+      sm.low[w] = low;
     }
   }
   __syncthreads();
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
     if (key == 0) return {0, 0};
     const uint32_t v = 0xFFFFFFFFu - static_cast<uint32_t>(key);
     float x = unordered(static_cast<uint32_t>(key >> 32));
-    if (sm.huge[w]) x = fminf(fmaxf(x, -kBmHuge), kBmHuge);
+    if (sm.low[w]) x = -kBmHuge;
     return {ordered(s + (static_cast<double>(x) - sm.lse[w])), ~(static_cast<uint32_t>(w) * V + v)};
   };
   const Cand one = tid < total ? get(tid) : Cand{0, 0};

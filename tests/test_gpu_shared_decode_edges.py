@@ -72,3 +72,16 @@ def test_values_above_the_limit_are_equal(m, V):
         for W, K in ((1, 1), (1, 5), (3, 16)):
             choice(m, x.to(dt), torch.tensor([-1.0, -2.0, -30.0], device=DEV), W, K)
     choice(m, torch.tensor([[3e8, 4e8, 0.0, 0.0]], device=DEV), torch.zeros(1, device=DEV), 1, 1)
+
+
+@pytest.mark.parametrize("V", HUGE)
+def test_low_values_beside_others_keep_their_size(m, V):
+    """Only where a beam has nothing else do values below -2^28 count as -2^28."""
+    lows = -(2.0 ** torch.linspace(30, 120, 40, device=DEV))
+    for top in (math.inf, 1e30, 2.0 ** 28, 2.0e8, 5.0, -2.0e8, -2.0 ** 28):
+        x = torch.full((2, V), -math.inf, device=DEV)
+        at = torch.randperm(V, generator=generator(V), device=DEV)
+        x[:, at[:40]] = lows
+        x[0, at[41]] = x[1, at[41]] = top
+        choice(m, x, torch.tensor([-1.0, -2.0], device=DEV), 1, 9)
+        choice(m, x, torch.tensor([-1.0, -2.0], device=DEV), 2, 9)
