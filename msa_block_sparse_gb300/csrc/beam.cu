@@ -445,7 +445,8 @@ struct MergeSmem {
   unsigned long long gs[kBmGroups];
   uint32_t gat[kBmGroups];
   double lse[kBmMaxW], score[kBmMaxW];
-  bool low[kBmMaxW];                   // nothing above -2^28: all that is there counts as -2^28
+  int low[kBmMaxW];                    // nothing above -2^28: so many values, which count as -2^28
+  int found[8][kBmMergeThreads / 32];  // among them: of a warp's pieces
   unsigned long long bound_s;
   uint32_t bound_at;
   int count;
@@ -505,12 +506,50 @@ __device__ __forceinline__ void bm_bound(MergeSmem& sm, Cand top, int K) {
   __syncthreads();
 }
 
+// Candidates of a beam that has nothing above -2^28 (rare): its values count alike, so that the
+// K best are those at the lowest places, which the slices, who rank by size, need not have kept.
+// `left` values are there; out: the beam's keys in place of its slices'.
+template <typename T>
+__device__ __forceinline__ void bm_lowest(MergeSmem& sm, const T* x, int V, int K, int left, unsigned long long* out,
+                                       int room) {
+  constexpr int kDeep = 8;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int want = left < K ? left : K;
+  int have = 0;
+  for (int v0 = 0; v0 < V && have < want; v0 += kDeep * kBmMergeThreads) {
+    uint32_t there[kDeep];
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int v = v0 + u * kBmMergeThreads + tid;
+      there[u] = v < V && static_cast<float>(x[v]) > -INFINITY;
+    }
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      there[u] = __ballot_sync(0xffffffffu, there[u] != 0);
+      if (lane == 0) sm.found[u][warp] = __popc(there[u]);
+    }
+    __syncthreads();
+    for (int u = 0; u < kDeep && have < want; ++u) {
+      int before = have;
+      for (int w = 0; w < kBmMergeThreads / 32; ++w) {
+        have += sm.found[u][w];
+        before += w < warp ? sm.found[u][w] : 0;
+      }
+      before += __popc(there[u] & ((1u << lane) - 1u));
+      if ((there[u] >> lane & 1) && before < want)
+        out[before] = key_of(-kBmHuge, v0 + u * kBmMergeThreads + tid);
+    }
+    __syncthreads();                                   // read before the next pieces are counted
+  }
+  for (int i = want + tid; i < room; i += kBmMergeThreads) out[i] = 0;
+}
+
 }  // namespace
 
 // grid (prompts)
-__global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
-    const BeamScan* __restrict__ stats, const unsigned long long* __restrict__ keys,
-    const float* scores, const uint8_t* __restrict__ finished, int W, int V, int K,
+__global__ void __launch_bounds__(kBmMergeThreads, 2) beam_merge_kernel(
+    const BeamScan* __restrict__ stats, unsigned long long* keys, const void* __restrict__ logits, int dtype,
+    long long ld, const float* scores, const uint8_t* __restrict__ finished, int W, int V, int K,
     int slices, int pad_token, float* scores_out, int32_t* __restrict__ parents,
     int32_t* __restrict__ tokens) {
   pdl_enter();
@@ -519,7 +558,9 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
   const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // candidate i = (beam, slice, rank); the first key is asked for before it is needed
   const int per_row = slices * K, total = W * per_row;
-  const unsigned long long key0 = tid < total ? keys[static_cast<size_t>(n) * total + tid] : 0;
+  keys += static_cast<size_t>(n) * total;
+  unsigned long long key0 = tid < total ? keys[tid] : 0;
+  int any_low = 0;
   // ---- log-sum-exp of every beam, a warp each; NaN as score: the beam is dead
   for (int w = warp; w < W; w += kBmMergeThreads / 32) {
     const int row = n * W + w;
@@ -549,13 +590,29 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
       }
     }
     if (lane == 0) {
-      sm.score[w] = live ? (s == 0.f ? 0.0 : static_cast<double>(s)) : -INFINITY;   // -0 is 0
-      const bool low = ref == kBmLow;
-      sm.lse[w] = ended || ref == -INFINITY ? 0.0 : bm_log(hi, lo, low ? 0.f : ref) - (low ? kBmHuge : 0.f);   // no candidates: no matter
-      sm.low[w] = low;
+      sm.score[w] = live ? static_cast<double>(s == 0.f ? 0.f : s) : -INFINITY;   // -0 is 0
+      sm.lse[w] = ended || ref == -INFINITY ? 0.0 : bm_log(hi, lo, ref);   // no candidates: no matter
+      sm.low[w] = 0;
+      if (live && !ended && ref == kBmLow) {
+        sm.lse[w] = bm_log(hi, lo, 0.f) - kBmHuge;
+        sm.low[w] = static_cast<int>(hi + lo);             // at most 2^24: exact
+        any_low = 1;
+      }
     }
   }
-  __syncthreads();
+  if (__syncthreads_or(any_low)) {
+    for (int w = 0; w < W; ++w) {
+      const int left = sm.low[w];
+      if (left == 0) continue;
+      const long long at = (static_cast<long long>(n) * W + w) * ld;
+      if (dtype == MSA_F32)
+        bm_lowest(sm, static_cast<const float*>(logits) + at, V, K, left, keys + w * per_row, per_row);
+      else
+        bm_lowest(sm, static_cast<const __nv_bfloat16*>(logits) + at, V, K, left, keys + w * per_row, per_row);
+    }
+    __syncthreads();
+    if (tid < total) key0 = keys[tid];
+  }
   auto get = [&](int i) -> Cand {
     const int w = i / per_row, row = n * W + w;
     const double s = sm.score[w];
@@ -564,7 +621,7 @@ __global__ void __launch_bounds__(kBmMergeThreads) beam_merge_kernel(
       if (i - w * per_row != 0) return {0, 0};
       return {ordered(s), ~(static_cast<uint32_t>(w) * V + pad_token)};
     }
-    const unsigned long long key = i < kBmMergeThreads ? key0 : keys[static_cast<size_t>(n) * total + i];
+    const unsigned long long key = i < kBmMergeThreads ? key0 : keys[i];
     if (key == 0) return {0, 0};
     const uint32_t v = 0xFFFFFFFFu - static_cast<uint32_t>(key);
     float x = unordered(static_cast<uint32_t>(key >> 32));
@@ -760,7 +817,8 @@ msa_status_t msa_beam_select(const void* logits, int dtype, int64_t row_stride, 
   {
     TraceScope trace_("beam_merge_kernel", st);
     launch_pdl(beam_merge_kernel, static_cast<unsigned>(N), kBmMergeThreads, sizeof(MergeSmem), st,
-               w.stats, w.keys, scores, finished, W, V, K, slices, pad_token, scores_out, parents, tokens);
+               w.stats, w.keys, logits, dtype, static_cast<long long>(row_stride), scores, finished, W, V, K, slices,
+               pad_token, scores_out, parents, tokens);
   }
   return check_launch("beam_merge_kernel");
 }

@@ -85,3 +85,29 @@ def test_low_values_beside_others_keep_their_size(m, V):
         x[0, at[41]] = x[1, at[41]] = top
         choice(m, x, torch.tensor([-1.0, -2.0], device=DEV), 1, 9)
         choice(m, x, torch.tensor([-1.0, -2.0], device=DEV), 2, 9)
+
+
+@pytest.mark.parametrize("V", HUGE)
+def test_values_below_the_limit_are_equal_where_there_is_nothing_else(m, V):
+    g = generator(V)
+    x = -(2.0 ** (29 + 90 * torch.rand(4, V, generator=g, device=DEV)))
+    x[1, torch.rand(V, generator=g, device=DEV) < 0.9] = -math.inf
+    x[2] = -math.inf
+    x[2, torch.randperm(V, generator=g, device=DEV)[:7]] = torch.tensor([-1e9, -3e8, -1e30, -1e9, -2e38, -2e9, -1e10], device=DEV)
+    x[3, :V // 2] = math.nan
+    for dt in (torch.float32, torch.bfloat16):
+        for W, K in ((1, 1), (1, 20), (4, 30)):
+            choice(m, x.to(dt), torch.tensor([-1.0, -2.0, -30.0, -31.0], device=DEV), W, K)
+    fin = torch.tensor([False, True, False, True], device=DEV)
+    choice(m, x, torch.tensor([-1.0, -2.0, -3.0, -math.inf], device=DEV), 4, 12, finished=fin, pad_token=V - 1)
+
+
+@pytest.mark.parametrize("V", HUGE)
+def test_rows_of_low_values_beside_other_rows(m, V):
+    for top in (math.inf, 2.0e8, 5.0, -2.0 ** 28):
+        x = torch.full((2, V), -math.inf, device=DEV)
+        at = torch.randperm(V, generator=generator(V), device=DEV)
+        x[:, at[:40]] = -(2.0 ** torch.linspace(30, 120, 40, device=DEV))
+        x[0, at[41]] = top
+        choice(m, x, torch.tensor([-1.0, -2.0], device=DEV), 1, 9)
+        choice(m, x, torch.tensor([-1.0, -2.0], device=DEV), 2, 9)
