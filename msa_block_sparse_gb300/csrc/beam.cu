@@ -221,7 +221,9 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
       return __ldcs(reinterpret_cast<const uint4*>(xa + lo));
     return L::part(xa + lo, skew - lo, skew + V - lo);
   };
-  float ref = -INFINITY, sum = 0.f;                      // this thread's sum is sum * 2^ref
+  // this thread's sum is (sum - less) * 2^ref: `less` is what rounding added, as a slice of the largest
+  // vocabulary has 4,096 tiles, whose errors can all go one way (equal logits)
+  float ref = -INFINITY, sum = 0.f, less = 0.f;
   constexpr int kTile = kVecs * kBmThreads;              // vectors of a tile
   const int tiles = (v1 - v0 + kTile - 1) / kTile, per = (tiles + kBmPieces - 1) / kBmPieces;
   float top = -INFINITY, piece = -INFINITY;              // maxima: of all, of `per` tiles
@@ -282,8 +284,14 @@ __global__ void __launch_bounds__(kBmThreads, 4) beam_scan_kernel(
       }
     }
     if (best > -INFINITY) {
-      if (to != ref) sum = ref > -INFINITY ? sum * bm_scale(ref - to) : 0.f;
-      sum += part;
+      if (to != ref) {
+        const float f = ref > -INFINITY ? bm_scale(ref - to) : 0.f;
+        sum *= f;
+        less *= f;
+      }
+      const float y = part - less, all = sum + y;
+      less = (all - sum) - y;
+      sum = all;
       ref = to;
     }
     piece = fmaxf(piece, best);

@@ -111,3 +111,25 @@ def test_rows_of_low_values_beside_other_rows(m, V):
         x[0, at[41]] = top
         choice(m, x, torch.tensor([-1.0, -2.0], device=DEV), 1, 9)
         choice(m, x, torch.tensor([-1.0, -2.0], device=DEV), 2, 9)
+
+
+# ------------------------------------------------------------------ sums
+
+@pytest.mark.parametrize("dt,V,W,K", [(torch.bfloat16, 1 << 24, 64, 64), (torch.float32, 1 << 24, 3, 5), (torch.float32, (1 << 24) - 5, 16, 64),
+                                      (torch.bfloat16, 3000001, 64, 64)])
+def test_sums_over_the_largest_vocabularies(m, dt, V, W, K):
+    """Equal logits: every partial sum is rounded in the same direction, and a row's scores are s - log V."""
+    x = torch.empty(W, V, dtype=dt, device=DEV)
+    x.copy_((torch.arange(W, device=DEV) * (0.69 / 64) - 0.35)[:, None])
+    scores = -torch.arange(W, device=DEV) / 4.0
+    so, po, to = m.msa_beam_select(x, scores, W, K)
+    m.msa_check_status()
+    want = -math.log(V)
+    within(f64(so)[0], np.full(K, want), 2.0 ** -20 + 2.0 ** -24 * abs(want), "score")
+    assert (po == 0).all() and to.tolist() == [list(range(K))]
+    # each row by itself
+    so, po, to = m.msa_beam_select(x, scores, 1, 1)
+    m.msa_check_status()
+    want = f64(scores) - math.log(V)
+    within(f64(so)[:, 0], want, 2.0 ** -20 + 2.0 ** -24 * np.abs(want), "score")
+    assert (to == 0).all()
