@@ -477,8 +477,8 @@ MSA_API msa_status_t msa_decode_shared(const void* q, const void* k_cache, const
  * nothing else, what lies below -2^28 as -2^28); a beam whose
  * score is -infinity or NaN is dead.  Continuations of probability zero are never chosen:
  * where fewer than K are left, the last places get score -infinity, parent -1, token -1
- * (msa_pages_reorder empties such rows).  scores_out may be scores where K = W, and must not
- * overlap them otherwise.  W, K <= 64, K <= W V, V <= 2^24, N W <= 65535.
+ * (msa_pages_reorder empties such rows).  scores_out may be scores where K = W; the outputs
+ * must not overlap scores or finished otherwise, nor each other.  W, K <= 64, K <= W V, V <= 2^24, N W <= 65535.
  */
 enum { MSA_F32 = 0, MSA_BF16 = 1 };
 

@@ -801,9 +801,22 @@ msa_status_t msa_beam_select(const void* logits, int dtype, int64_t row_stride, 
   if (row_stride < V) return fail(MSA_ERR_INVALID_ARG, "row_stride is below V");
   if (pad_token < 0 || pad_token >= V)
     return fail(MSA_ERR_INVALID_ARG, "pad_token %d outside [0, %d)", pad_token, V);
-  // a prompt's CTA reads its own W scores before it writes its K: in place where they are the same
-  if (overlap(scores_out, 4ull * N * K, scores, 4ull * N * W) && !(scores_out == scores && K == W))
-    return fail(MSA_ERR_INVALID_ARG, "scores_out overlaps scores (it may be scores where K = W)");
+  // a prompt's CTA writes its K places while others' scores and flags are still to be read; its own W scores
+  // it has read before: in place where they are the same
+  const struct {
+    const void* at;
+    const char* name;
+  } out[3] = {{scores_out, "scores_out"}, {parents, "parents"}, {tokens, "tokens"}};
+  const size_t places = 4ull * N * K, rows_in = static_cast<size_t>(N) * W;
+  for (int i = 0; i < 3; ++i) {
+    if (overlap(out[i].at, places, scores, 4 * rows_in) && !(i == 0 && scores_out == scores && K == W))
+      return fail(MSA_ERR_INVALID_ARG, "%s overlaps scores (scores_out may be scores where K = W)", out[i].name);
+    if (finished && overlap(out[i].at, places, finished, rows_in))
+      return fail(MSA_ERR_INVALID_ARG, "%s overlaps finished", out[i].name);
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].at, places, out[j].at, places))
+        return fail(MSA_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, out[j].name);
+  }
   const long long rows = static_cast<long long>(N) * W;
   const int slices = beam_slices(rows, W, V, K);
   if (workspace_bytes < beam_bytes(rows, slices, K)) return fail(MSA_ERR_INVALID_ARG, "workspace too small");

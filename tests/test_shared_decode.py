@@ -213,3 +213,20 @@ def test_binding_refuses_cpu_tensors():
             call()
     with pytest.raises(ValueError):
         m.msa_cache_append(t, t, t, t, t, i, i, i, "rope")
+
+
+def test_beam_select_refuses_outputs_that_overlap(lib):
+    """parents and tokens over what other prompts' CTAs still read, outputs over each other."""
+    good = dict(x=at(0), dtype=0, ld=50, scores=at(1), fin=at(2), N=2, W=3, V=50, K=3, pad=0, so=at(3), po=at(4), to=at(5),
+                ws=at(6), size=0, stream=None)
+
+    def call(**kw):
+        assert lib.msa_beam_select(*{**good, **kw}.values()) == 1
+        return lib.msa_last_error().decode()
+    assert "workspace" in call()
+    for kw in (dict(po=at(1)), dict(to=at(1)), dict(so=at(2)), dict(po=at(2)), dict(to=at(2)), dict(po=at(3)), dict(to=at(3)),
+               dict(to=at(4)), dict(po=ctypes.c_void_p(at(3).value + 16)), dict(to=ctypes.c_void_p(at(4).value + 16)),
+               dict(so=at(1), po=at(1)), dict(fin=ctypes.c_void_p(at(4).value + 23))):
+        assert "overlap" in call(**kw), kw
+    for kw in (dict(so=at(1)), dict(fin=None), dict(po=ctypes.c_void_p(at(3).value + 32)), dict(fin=ctypes.c_void_p(at(4).value + 24))):
+        assert "workspace" in call(**kw), kw
