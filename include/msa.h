@@ -647,7 +647,7 @@ MSA_API msa_status_t msa_pages_compact(int32_t* block_table, const int32_t* cach
  * parent lose their pages, and entries that a row no longer needs become -1.  kept[r]
  * (int32 [B], output) is the row's length after the call, -1 where it is refused and left
  * as it was: a parent outside [-1, B), or one whose length is out of range (both set
- * MSA_STATUS_BOUNDS).  parents, kept and the tables must not overlap.
+ * MSA_STATUS_BOUNDS).  parents, kept, the tables and ref_count must not overlap.
  */
 MSA_API size_t msa_pages_reorder_workspace_size(int B, int max_pages);
 

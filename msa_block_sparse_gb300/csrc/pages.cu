@@ -810,14 +810,14 @@ msa_status_t msa_pages_reorder(const int32_t* parents, int32_t* block_table, int
   MSA_REQUIRE_PTR(kept);
   MSA_REQUIRE_PTR(workspace);
   MSA_TRY(check_tables(block_table, cache_lens, ref_count, B, num_pages, max_pages));
-  // rows read what other threads write: kept has to be a buffer of its own
-  const size_t rows = static_cast<size_t>(B) * sizeof(int32_t);
+  // rows read what other threads write: kept has to be a buffer of its own, and so have the parents
+  const size_t rows = static_cast<size_t>(B) * sizeof(int32_t), counts = static_cast<size_t>(num_pages) * sizeof(int32_t);
   if (overlap(kept, rows, parents, rows) || overlap(kept, rows, cache_lens, rows) ||
-      overlap(kept, rows, block_table, rows * max_pages) ||
-      overlap(kept, rows, ref_count, static_cast<size_t>(num_pages) * sizeof(int32_t)))
+      overlap(kept, rows, block_table, rows * max_pages) || overlap(kept, rows, ref_count, counts))
     return fail(MSA_ERR_INVALID_ARG, "kept overlaps another argument");
-  if (overlap(parents, rows, cache_lens, rows) || overlap(parents, rows, block_table, rows * max_pages))
-    return fail(MSA_ERR_INVALID_ARG, "parents overlaps the rows");
+  if (overlap(parents, rows, cache_lens, rows) || overlap(parents, rows, block_table, rows * max_pages) ||
+      overlap(parents, rows, ref_count, counts))
+    return fail(MSA_ERR_INVALID_ARG, "parents overlaps the rows or the counts");
   if (workspace_bytes < msa_pages_reorder_workspace_size(B, max_pages))
     return fail(MSA_ERR_INVALID_ARG, "workspace too small");
   WsCursor ws(workspace);

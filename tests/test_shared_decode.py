@@ -230,3 +230,12 @@ def test_beam_select_refuses_outputs_that_overlap(lib):
         assert "overlap" in call(**kw), kw
     for kw in (dict(so=at(1)), dict(fin=None), dict(po=ctypes.c_void_p(at(3).value + 32)), dict(fin=ctypes.c_void_p(at(4).value + 24))):
         assert "workspace" in call(**kw), kw
+
+
+def test_pages_reorder_refuses_parents_over_the_counts(lib):
+    def call(ref):
+        assert lib.msa_pages_reorder(at(0), at(1), at(2), ref, 4, 9, 5, at(4), at(5), 0, None) == 1
+        return lib.msa_last_error().decode()
+    assert "workspace" in call(at(3))
+    assert "overlaps" in call(at(0))
+    assert "overlaps" in call(ctypes.c_void_p(at(0).value - 32))
