@@ -67,15 +67,6 @@ struct Call {
   Tensor fresh(at::ScalarType type, at::IntArrayRef shape) const {
     return Tensor(at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, dev), std::nullopt));
   }
-  // Contiguous part of `of` from an element on: small outputs of one call share an allocation
-  // (a microsecond of host time each)
-  static Tensor part(const Tensor& of, int64_t first, at::ScalarType type, at::IntArrayRef shape) {
-    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(of.storage()), of.key_set(),
-                                                        c10::scalarTypeToTypeMeta(type));
-    t.unsafeGetTensorImpl()->set_storage_offset(first);
-    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-    return t;
-  }
   // Address of a contiguous tensor of this type, shape and device
   void* arg(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape) const {
     if (t.scalar_type() != type) {
@@ -636,18 +627,9 @@ PyObject* beam_select(PyObject* const* a) {
   }
   const int n = size32(N, "N"), w = size32(W, "beams"), v = size32(V, "V"), k = size32(K, "n_out");
   if (k < 1) throw ValueErr("n_out must be >= 1");
-  Tensor so, po, to;
-  if (none(a[6]) && none(a[7]) && none(a[8])) {
-    const int64_t n4 = (N * K + 3) / 4 * 4;          // each 16-byte aligned
-    const Tensor all = c.fresh(at::kInt, {3 * n4});
-    so = Call::part(all, 0, at::kFloat, {N, K});
-    po = Call::part(all, n4, at::kInt, {N, K});
-    to = Call::part(all, 2 * n4, at::kInt, {N, K});
-  } else {
-    so = c.out(a[6], "scores_out", at::kFloat, {N, K});
-    po = c.out(a[7], "parents", at::kInt, {N, K});
-    to = c.out(a[8], "tokens", at::kInt, {N, K});
-  }
+  const Tensor so = c.out(a[6], "scores_out", at::kFloat, {N, K});
+  const Tensor po = c.out(a[7], "parents", at::kInt, {N, K});
+  const Tensor to = c.out(a[8], "tokens", at::kInt, {N, K});
   const Workspace ws(c, a[9], msa_beam_select_workspace_size(n, w, v, k));
   check(msa_beam_select(x.data_ptr(), dtype, R > 1 ? x.stride(0) : V, static_cast<const float*>(scores),
                         finished, n, w, v, k, size32(whole(a[5]), "pad_token"),

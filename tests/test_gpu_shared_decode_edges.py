@@ -2,6 +2,7 @@
 sums or overlapping storage could go wrong.  Helpers and definitions are those of
 test_gpu_shared_decode.py, and so are the tolerances, in the form derived there: scores within
 2^-20 + 2^-24 |score|."""
+import io
 import math
 
 import numpy as np
@@ -133,3 +134,20 @@ def test_sums_over_the_largest_vocabularies(m, dt, V, W, K):
     want = f64(scores) - math.log(V)
     within(f64(so)[:, 0], want, 2.0 ** -20 + 2.0 ** -24 * np.abs(want), "score")
     assert (to == 0).all()
+
+
+# ------------------------------------------------------------------ outputs
+
+def test_selected_outputs_are_tensors_of_their_own(m):
+    """Saved together, grown or kept by themselves."""
+    x = torch.randn(8, 1000, generator=generator(5), device=DEV)
+    out = m.msa_beam_select(x, torch.zeros(8, device=DEV), 4)
+    want = [t.clone() for t in out]
+    buf = io.BytesIO()
+    torch.save(dict(zip("spt", out)), buf)
+    buf.seek(0)
+    back = torch.load(buf)
+    assert all(torch.equal(back[k], t) for k, t in zip("spt", want))
+    assert len({t.untyped_storage().data_ptr() for t in out}) == 3
+    out[0].resize_(30).fill_(5.0)
+    assert torch.equal(out[1], want[1]) and torch.equal(out[2], want[2])
