@@ -1199,8 +1199,8 @@ using namespace msa;
 extern "C" {
 
 size_t msa_decode_shared_workspace_size(int B, int Hq, int Hkv, int max_pages) {
-  (void)max_pages;
   if (!shared_sizes_ok(B, Hq, Hkv)) return 0;
+  if (max_pages >= 1 && short_attn_fits(B, Hq / Hkv, Hkv, max_pages)) return 256;   // nothing is kept there
   WsCursor ws(nullptr);
   carve_shared_workspace(ws, B, Hq, Hkv);
   return ws.used + 256;
@@ -1232,8 +1232,6 @@ msa_status_t msa_decode_shared(const void* q, const void* k_cache, const void* v
     return fail(MSA_ERR_INVALID_ARG, "scale must be from 2^-64 to 2^64");
   if (workspace_bytes < msa_decode_shared_workspace_size(B, Hq, Hkv, max_pages))
     return fail(MSA_ERR_INVALID_ARG, "workspace too small");
-  WsCursor ws(workspace);
-  const SaPlan plan = carve_shared_workspace(ws, B, Hq, Hkv);
   const int G = Hq / Hkv, sms = device_sm_count();
   CUtensorMap tk, tv;
   const uint64_t dims[3] = {static_cast<uint64_t>(kD), static_cast<uint64_t>(kBlock),
@@ -1245,6 +1243,8 @@ msa_status_t msa_decode_shared(const void* q, const void* k_cache, const void* v
     return launch_short_attn({tk, tv, static_cast<const __nv_bfloat16*>(q), block_table, cache_lens, B, G, Hkv,
                               num_pages, max_pages, scale * kSaLog2e, static_cast<__nv_bfloat16*>(o), lse},
                              static_cast<cudaStream_t>(stream));
+  WsCursor ws(workspace);
+  const SaPlan plan = carve_shared_workspace(ws, B, Hq, Hkv);
   uint32_t* sw = nullptr;
   MSA_TRY(status_word(&sw));
   MSA_TRY(ensure_smem(shared_attn_kernel, sizeof(SaSmem), "shared_attn_kernel"));

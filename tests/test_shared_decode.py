@@ -239,3 +239,14 @@ def test_pages_reorder_refuses_parents_over_the_counts(lib):
     assert "workspace" in call(at(3))
     assert "overlaps" in call(at(0))
     assert "overlaps" in call(ctypes.c_void_p(at(0).value - 32))
+
+
+def test_decode_shared_workspace_follows_the_form(lib):
+    """Calls that one launch serves need none; a smaller call never needs more than a larger one."""
+    size = lib.msa_decode_shared_workspace_size
+    assert size(4, 64, 4, 12) <= 4096 and size(1, 16, 1, 1) <= 4096
+    assert size(4, 64, 4, 200) > 1 << 20 and size(64, 64, 4, 256) > 1 << 20 and size(4, 68, 4, 12) > 1 << 20
+    Bs, cols = (1, 2, 3, 9, 24, 33, 50, 70, 115, 229, 300, 610, 2048), (1, 4, 8, 9, 16, 20, 21, 31, 32, 40, 41, 64, 80, 128, 129, 1024)
+    for Hq, Hkv in ((16, 1), (64, 4), (8, 8)):
+        got = np.array([[size(B, Hq, Hkv, c) for c in cols] for B in Bs])
+        assert (got > 0).all() and (np.diff(got, axis=0) >= 0).all() and (np.diff(got, axis=1) >= 0).all()
