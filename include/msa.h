@@ -420,11 +420,12 @@ MSA_API msa_status_t msa_decode_append(const void* q, const void* q_idx, const v
  *   k_cache[page, h, p % 128]    = prologue(k, w_k)[h]
  *   kidx_cache[page, h, p % 128] = prologue(k_idx, w_ki)[h]
  *   v_cache[page, h, p % 128]    = v[h]             with page = block_table[s, p / 128]
- * Caches as in msa_decode_step; Hq is any multiple of Hkv up to 256.  Tokens outside
- * [cu_seqlens[0], cu_seqlens[S]) and those of rows with cache_lens[s] = 0 (padding) are
- * left alone.  Positions outside [0, 128 max_pages) and pages outside [0, num_pages) set
- * MSA_STATUS_BOUNDS and leave the token's outputs untouched.  A page that rows share has
- * to be made the row's own first (msa_pages_extend).
+ * q_out and q_idx_out must not overlap the inputs otherwise.  Caches as in msa_decode_step; Hq
+ * is any multiple of Hkv up to 256.  Tokens outside [cu_seqlens[0], cu_seqlens[S]) and those
+ * of rows with cache_lens[s] = 0 (padding) are left alone.  Positions outside [0, 128
+ * max_pages) and pages outside [0, num_pages) set MSA_STATUS_BOUNDS and leave the token's
+ * outputs untouched.  A page that rows share has to be made the row's own first
+ * (msa_pages_extend).
  */
 MSA_API msa_status_t msa_cache_append(const void* q, const void* k, const void* v,
                                       const void* q_idx, const void* k_idx, const void* w_q,
@@ -452,8 +453,9 @@ MSA_API msa_status_t msa_cache_append(const void* q, const void* k, const void* 
  * which then takes less time.
  * A row with cache_lens[b] = 0 gets o = 0 and lse = -infinity, and so does a head whose
  * products are all -infinity; lengths outside [0, 128 max_pages] set MSA_STATUS_BOUNDS and are
- * treated so too.  A page outside [0, num_pages) sets MSA_STATUS_BOUNDS and has no keys.  o may be q.  Slots of a row's last page behind
- * its end may hold anything.  B <= 2048; scale from 2^-64 to 2^64.
+ * treated so too.  A page outside [0, num_pages) sets MSA_STATUS_BOUNDS and has no keys.  o
+ * may be q; o and lse must not overlap the inputs otherwise.  Slots of a row's last page
+ * behind its end may hold anything.  B <= 2048; scale from 2^-64 to 2^64.
  */
 MSA_API size_t msa_decode_shared_workspace_size(int B, int Hq, int Hkv, int max_pages);
 

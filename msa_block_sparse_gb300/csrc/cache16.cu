@@ -345,6 +345,20 @@ msa_status_t msa_cache_append(const void* q, const void* k, const void* v, const
   const long long ctas = q_ctas + static_cast<long long>(groups) * a.shares;
   if (ctas > INT32_MAX) return fail(MSA_ERR_UNSUPPORTED, "T = %d tokens of %d heads are too many", T, Hq);
   a.q_ctas = static_cast<int>(q_ctas);
+  // a row is read and written by the same threads, in place where the rows are the same; elsewhere other
+  // CTAs have yet to read
+  const size_t qb = static_cast<size_t>(T) * Hq * kD * sizeof(bf), kb = static_cast<size_t>(T) * Hkv * kD * sizeof(bf);
+  const struct {
+    const void* at;
+    size_t bytes;
+    const char* name;
+  } out[2] = {{q_out, qb, "q_out"}, {q_idx_out, kb, "q_idx_out"}},
+    in[5] = {{q, qb, "q"}, {k, kb, "k"}, {v, kb, "v"}, {q_idx, kb, "q_idx"}, {k_idx, kb, "k_idx"}};
+  for (int i = 0; i < (index ? 2 : 1); ++i)
+    for (int j = 0; j < (index ? 5 : 3); ++j)
+      if (overlap(out[i].at, out[i].bytes, in[j].at, in[j].bytes) && !(j == 3 * i && out[i].at == in[j].at))
+        return fail(MSA_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, in[j].name);
+  if (index && overlap(q_out, qb, q_idx_out, kb)) return fail(MSA_ERR_INVALID_ARG, "q_out overlaps q_idx_out");
   const RxTurns turns = rx_turns(*rope);
   uint32_t* sw = nullptr;
   MSA_TRY(status_word(&sw));

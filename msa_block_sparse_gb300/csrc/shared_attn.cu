@@ -1230,6 +1230,21 @@ msa_status_t msa_decode_shared(const void* q, const void* k_cache, const void* v
     return fail(MSA_ERR_UNSUPPORTED, "num_pages * Hkv above 2^31");
   if (!(scale >= 0x1p-64f && scale <= 0x1p64f))
     return fail(MSA_ERR_INVALID_ARG, "scale must be from 2^-64 to 2^64");
+  // o may be q: a head is read before it is written; other CTAs have yet to read the rest
+  const size_t heads = static_cast<size_t>(B) * Hq, ob = heads * kD * sizeof(__nv_bfloat16);
+  const size_t rows = static_cast<size_t>(B) * sizeof(int32_t);
+  if (o != q && overlap(o, ob, q, ob)) return fail(MSA_ERR_INVALID_ARG, "o overlaps q (it may be q)");
+  const struct {
+    const void* at;
+    size_t bytes;
+    const char* name;
+  } out[2] = {{o, ob, "o"}, {lse, heads * sizeof(float), "lse"}};
+  for (int i = 0; i < (lse ? 2 : 1); ++i)
+    if (overlap(out[i].at, out[i].bytes, cache_lens, rows) ||
+        overlap(out[i].at, out[i].bytes, block_table, rows * max_pages))
+      return fail(MSA_ERR_INVALID_ARG, "%s overlaps the rows", out[i].name);
+  if (lse && (overlap(lse, out[1].bytes, q, ob) || overlap(lse, out[1].bytes, o, ob)))
+    return fail(MSA_ERR_INVALID_ARG, "lse overlaps q or o");
   if (workspace_bytes < msa_decode_shared_workspace_size(B, Hq, Hkv, max_pages))
     return fail(MSA_ERR_INVALID_ARG, "workspace too small");
   const int G = Hq / Hkv, sms = device_sm_count();

@@ -250,3 +250,32 @@ def test_decode_shared_workspace_follows_the_form(lib):
     for Hq, Hkv in ((16, 1), (64, 4), (8, 8)):
         got = np.array([[size(B, Hq, Hkv, c) for c in cols] for B in Bs])
         assert (got > 0).all() and (np.diff(got, axis=0) >= 0).all() and (np.diff(got, axis=1) >= 0).all()
+
+
+def test_append_and_attention_refuse_outputs_that_overlap(lib):
+    """q_out may be q, q_idx_out q_idx and o q; nothing else that other CTAs still read."""
+    rc = rope()
+    names = ("q", "k", "v", "q_idx", "k_idx")
+    x = {n: at(64 * i) for i, n in enumerate(names)}              # 9 tokens of up to 4 heads: 9,216 bytes
+
+    def append(q_out, q_idx_out):
+        r = lib.msa_cache_append(x["q"], x["k"], x["v"], x["q_idx"], x["k_idx"], None, None, None, None, at(500), at(600),
+                                 at(700), at(800), at(801), at(802), 2, 9, 4, 2, 5, 3, ctypes.byref(rc), 1e-6, q_out, q_idx_out, None)
+        assert r == 1
+        return lib.msa_last_error().decode()
+    for n in ("k", "v", "q_idx", "k_idx"):
+        assert "overlaps" in append(x[n], at(900)), n
+    for n in ("q", "k", "v", "k_idx"):
+        assert "overlaps" in append(at(900), x[n]), n
+    assert "overlaps" in append(ctypes.c_void_p(x["q"].value + 256), at(900))
+    assert "overlaps" in append(at(900), ctypes.c_void_p(x["q_idx"].value + 256))
+    assert "overlaps" in append(at(900), at(900))
+
+    def attend(o, lse):
+        r = lib.msa_decode_shared(at(0), at(100), at(200), at(300), at(301), 3, 8, 2, 5, 3, 0.1, o, lse, at(400), 0, None)
+        assert r == 1
+        return lib.msa_last_error().decode()
+    assert "workspace" in attend(at(0), None) and "workspace" in attend(at(10), at(20))
+    assert "overlaps" in attend(ctypes.c_void_p(at(0).value + 256), None)
+    assert "overlaps" in attend(at(10), at(0)) and "overlaps" in attend(at(10), at(10))
+    assert "overlaps" in attend(at(10), at(301))
