@@ -1,7 +1,7 @@
 """Append, shared attention and beam selection on the GPU where values that count as equal, long
 sums or overlapping storage could go wrong.  Helpers and definitions are those of
 test_gpu_shared_decode.py, and so are the tolerances, in the form derived there: scores within
-2^-20 + 2^-24 |score|."""
+2^-20 + 2^-24 |score|, lse within e + 2^-22 |lse|."""
 import io
 import math
 
@@ -14,7 +14,7 @@ from tests import test_gpu_shared_decode as base
 
 pytestmark = pytest.mark.gpu
 m = base.m
-DEV, f64, within = base.DEV, base.f64, base.within
+DEV, f64, i32, bf16, within = base.DEV, base.f64, base.i32, base.bf16, base.within
 
 
 # ------------------------------------------------------------------ values that count as equal
@@ -136,7 +136,99 @@ def test_sums_over_the_largest_vocabularies(m, dt, V, W, K):
     assert (to == 0).all()
 
 
+@pytest.mark.parametrize("case", base.BEAMS, ids=lambda c: "-".join(map(str, c)))
+def test_scores_to_half_a_step(m, case):
+    N, W, V, K, dt, more, masked, ended = case
+    g = generator(2 * V + K)
+    x = 3 * torch.randn(N * W, V + more, generator=g, device=DEV)
+    x[torch.rand(x.shape, generator=g, device=DEV) < masked] = -math.inf
+    x = x.to(torch.float32 if dt == "f" else torch.bfloat16)[:, :V]
+    scores = -5 * torch.rand(N * W, generator=g, device=DEV)
+    fin = torch.rand(N * W, generator=g, device=DEV) < ended if ended else None
+    so, po, to = m.msa_beam_select(x, scores, W, K, finished=fin, pad_token=V - 1)
+    m.msa_check_status()
+    every = S.beam_scores(f64(x), f64(scores), None if fin is None else fin.cpu().numpy(), V - 1)
+    got, p, t = f64(so), po.cpu().numpy(), to.cpu().numpy()
+    live = p >= 0
+    want = every[p[live], t[live]]
+    within(got[live], want, 2.0 ** -20 + 2.0 ** -24 * np.abs(want), "score")
+    best = np.sort(every.reshape(N, -1), 1)[:, ::-1][:, :K]
+    assert np.array_equal(live, best > -np.inf)
+    within(got[live], best[live], 2.0 ** -20 + 2.0 ** -24 * np.abs(best[live]), "place")
+
+
+@pytest.mark.parametrize("scale,q_gain", [(2.0 ** -64, 1.0), (2.0 ** -30, 1.0), (1.0, 1.0), (1.0, 30.0), (2.0 ** 20, 1.0), (2.0 ** 64, 1.0)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_lse_of_small_and_large_logits(m, scale, q_gain, wide):
+    table, lens, P = base.tree_table(np.random.default_rng(10), [(2, [40, 90, 128]), 300, 1, (1, [30] * 9)])
+    table = base.widen(table, wide)
+    rng = np.random.default_rng(11)
+    q = bf16(q_gain * rng.standard_normal((len(lens), 16, 128)))
+    kc, vc = (bf16(rng.standard_normal((P, 1, 128, 128))) for _ in range(2))
+    o, lse = m.msa_decode_shared(q, kc, vc, i32(table), i32(lens), scale=scale)
+    m.msa_check_status()
+    for b, n in enumerate(lens):
+        K = S.row_tokens(f64(kc), table, b, 0, n)
+        z = f64(q)[b] @ K.T * scale
+        want = z.max(1) + np.log(np.exp(z - z.max(1, keepdims=True)).sum(1))
+        e = 2.0 ** -16 * scale * (np.abs(f64(q)[b]) @ np.abs(K).T).max() + 2.0 ** -18
+        within(f64(lse)[b], want, e + 2.0 ** -22 * np.abs(want), f"lse {b}")
+
+
+# ------------------------------------------------------------------ both forms of the attention
+
+def test_shared_attention_by_items_beyond_4_gb(m):
+    """Pages whose byte offsets pass 32 bits, by the kernels that read shared pages once."""
+    P, Hkv = 40000, 4
+    kc, vc = (torch.zeros(P, Hkv, 128, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    g = generator(8)
+    pages = [39999, 33000, 12, 39000]
+    for c in (kc, vc):
+        c[pages] = torch.randn(4, Hkv, 128, 128, generator=g, device=DEV).to(torch.bfloat16)
+    q = torch.randn(2, 16, 128, generator=g, device=DEV).to(torch.bfloat16)
+    table, lens = np.array([[39999, 33000, 12], [39999, 33000, 39000]]), np.array([300, 384])
+    o, lse = m.msa_decode_shared(q, kc, vc, i32(base.widen(table)), i32(lens))
+    m.msa_check_status()
+    t2 = np.vectorize({p: i for i, p in enumerate(pages)}.get)(table)
+    want, wlse = S.attend(f64(q), f64(kc[pages]), f64(vc[pages]), t2, lens, base.SCALE)
+    assert np.linalg.norm(f64(o) - want) <= 2.0 ** -8 * np.linalg.norm(want)
+    within(f64(lse), wlse, 2.0 ** -10, "lse")
+
+
+def test_shared_attention_by_items_equals_the_sparse_step_up_to_its_blocks(m):
+    rng = np.random.default_rng(13)
+    lens = [2048, 1, 700, 1999]
+    table, lens, P = base.tree_table(rng, [int(n) for n in lens], maxp=16)
+    q, qi = bf16(rng.standard_normal((4, 32, 128))), bf16(rng.standard_normal((4, 2, 128)))
+    kc, vc, ic = (bf16(rng.standard_normal((P, 2, 128, 128))) for _ in range(3))
+    a, _ = m.msa_decode_step(q, qi, kc, vc, ic, i32(table), i32(lens))
+    b, _ = m.msa_decode_shared(q, kc, vc, i32(base.widen(table)), i32(lens))
+    assert np.linalg.norm(f64(a) - f64(b)) <= 2.0 ** -7 * np.linalg.norm(f64(b))
+    m.msa_check_status()
+
+
 # ------------------------------------------------------------------ outputs
+
+@pytest.mark.parametrize("case", [c for c in base.APPEND if c[8]], ids=lambda c: f"{len(c[0])}x{c[2]}x{c[3]}")
+def test_append_in_place_with_index_heads(m, case):
+    n, before, G, Hkv, R, layout, scaling, norms, _ = case
+    x, w, (kc, vc, ic), table, cu, end, pos, row = base.append_case(n, before, G, Hkv, True, seed=len(n) + R)
+    factor = 1.0 if scaling == "none" else 4.0
+    rope = m.msa_rope(R, 1e7, layout=layout, scaling=scaling, factor=factor, orig_len=4096.0)
+    wt = {k: w[k] if k in norms else None for k in "qkij"}
+
+    def call(q, qi, caches, **out):
+        return m.msa_cache_append(q, x["k"], x["v"], *caches[:2], i32(table), i32(cu), i32(end), rope, w_q=wt["q"], w_k=wt["k"],
+                                  q_idx=qi, k_idx=x["k_idx"], kidx_cache=caches[2], w_qi=wt["i"], w_ki=wt["j"], **out)
+    first = (kc, vc, ic)
+    again = [torch.full_like(c, 7.0) for c in first]
+    q, qi = call(x["q"], x["q_idx"], first)
+    q2, qi2 = x["q"].clone(), x["q_idx"].clone()
+    a, b = call(q2, qi2, again, q_out=q2, q_idx_out=qi2)
+    m.msa_check_status()
+    assert a is q2 and b is qi2 and torch.equal(q2, q) and torch.equal(qi2, qi)
+    assert all(torch.equal(s, t) for s, t in zip(again, first))
+
 
 def test_selected_outputs_are_tensors_of_their_own(m):
     """Saved together, grown or kept by themselves."""
