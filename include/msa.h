@@ -471,16 +471,16 @@ MSA_API msa_status_t msa_decode_shared(const void* q, const void* k_cache, const
  * scores fp32 [N W] the beams' log probabilities.  Of the continuations
  *   score(w, v) = scores[w] + logits[w, v] - log sum_u exp(logits[w, u])
  * of a prompt the K best, best first: scores_out fp32 [N, K], parents int32 [N, K] (the row
- * n W + w), tokens int32 [N, K].  Scores are compared before they are rounded to fp32,
- * as 64-bit values over a log-sum-exp of fp32 exponentials; equal ones go to the lower
- * w V + v.  A beam with finished[r] != 0 (uint8 [N W], NULL: none) goes on by
- * pad_token alone, with its score unchanged; its logits are not read.  A NaN among
- * the logits counts as -infinity, what lies above 2^28 as 2^28 (and, where a beam has
- * nothing else, what lies below -2^28 as -2^28); a beam whose
- * score is -infinity or NaN is dead.  Continuations of probability zero are never chosen:
- * where fewer than K are left, the last places get score -infinity, parent -1, token -1
- * (msa_pages_reorder empties such rows).  scores_out may be scores where K = W; the outputs
- * must not overlap scores or finished otherwise, nor each other.  W, K <= 64, K <= W V, V <= 2^24, N W <= 65535.
+ * n W + w), tokens int32 [N, K].  Scores are compared before they are rounded to fp32, as
+ * 64-bit values over a log-sum-exp of fp32 exponentials; equal ones go to the lower w, then to
+ * the larger logit, then to the lower v.  A beam with finished[r] != 0 (uint8 [N W], NULL:
+ * none) goes on by pad_token alone, with its score unchanged; its logits are not read.  A NaN
+ * among the logits counts as -infinity, what lies above 2^28 as 2^28 (and, where a beam has
+ * nothing else, what lies below -2^28 as -2^28); a beam whose score is -infinity or NaN is
+ * dead.  Continuations of probability zero are never chosen: where fewer than K are left, the
+ * last places get score -infinity, parent -1, token -1 (msa_pages_reorder empties such rows).
+ * scores_out may be scores where K = W; the outputs must not overlap scores or finished
+ * otherwise, nor each other.  W, K <= 64, K <= W V, V <= 2^24, N W <= 65535.
  */
 enum { MSA_F32 = 0, MSA_BF16 = 1 };
 

@@ -616,7 +616,8 @@ def msa_beam_select(logits, scores, beams: int, n_out: Optional[int] = None,
     """The n_out (default: beams) best continuations of each prompt by scores[r] +
     log softmax(logits[r]): logits fp32 or bf16 [N * beams, V] (rows of any stride), scores
     fp32 [N * beams].  Returns (scores fp32, parents int32, tokens int32), each [N, n_out],
-    best first, equal scores by the lower beam and token; parents are rows of logits.
+    best first, equal scores by the lower beam, the larger logit, the lower token; parents are
+    rows of logits.
     finished (bool or uint8 [N * beams]): such a beam goes on by pad_token alone, its score
     unchanged.  Where fewer continuations are possible: -inf, -1, -1."""
     return _native().beam_select(logits, scores, beams, beams if n_out is None else n_out, finished,

@@ -438,27 +438,35 @@ constexpr int kBmPer = kBmMergeThreads / kBmGroups;
 constexpr int kBmMine = kBmCandidates / kBmMergeThreads;            // candidates of a thread
 constexpr int kBmSurvivors = kBmMaxK * kBmPer * kBmMine;            // at most after the first cut
 
-// A candidate: score (ordered; 0: none) and ~(place among the prompt's W * V): larger wins
+// A candidate: score (ordered; 0: none) and what decides where scores are equal: the lower beam, then
+// the larger logit, then the lower token.  Larger wins.  (Scores of a beam are ordered as its
+// logits, by which its slices chose; rounded to 64 bits, near ones or those of a beam far below 0 are equal.)
 struct Cand {
-  unsigned long long s;
-  uint32_t at;
+  unsigned long long s, tie;
 };
-__device__ __forceinline__ bool beats(unsigned long long s, uint32_t at, unsigned long long t, uint32_t bt) {
-  return s > t || (s == t && at > bt);
+__device__ __forceinline__ bool beats(const Cand& a, const Cand& b) {
+  return a.s > b.s || (a.s == b.s && a.tie > b.tie);
+}
+__device__ __forceinline__ unsigned long long tie_of(int w, uint32_t logit, uint32_t token) {
+  return static_cast<unsigned long long>(kBmMaxW - 1 - w) << 56 | static_cast<unsigned long long>(logit) << 24 |
+         (0xFFFFFFu - token);                          // V <= 2^24
 }
 
 struct MergeSmem {
-  unsigned long long s[kBmSurvivors];
-  uint32_t at[kBmSurvivors];
-  unsigned long long gs[kBmGroups];
-  uint32_t gat[kBmGroups];
+  union {
+    Cand group[kBmGroups];
+    unsigned long long group_s[kBmGroups];
+  };
   double lse[kBmMaxW], score[kBmMaxW];
   int low[kBmMaxW];                    // nothing above -2^28: so many values, which count as -2^28
   int found[8][kBmMergeThreads / 32];  // among them: of a warp's pieces
-  unsigned long long bound_s;
-  uint32_t bound_at;
+  Cand bound;
   int count;
+  unsigned long long left[2];          // scores of as many candidates as merge_room says, then their ties
 };
+
+// Candidates left after the first cut: K groups of kBmPer threads at most, each with its share of `total`
+constexpr int merge_room(int total, int K) { return K * kBmPer * ((total + kBmMergeThreads - 1) / kBmMergeThreads); }
 
 // ln(hi + lo) + n ln 2 (see BeamScan), hi >= 0 the larger part, to 5e-9: with hi = 2^e m, m from
 // sqrt(1/2) to sqrt(2), and s = (m - 1) / (m + 1), ln m = 2 s + 2 s^3 / 3 + 2 s^5 / 5 + ...  s is kept as
@@ -487,30 +495,49 @@ __device__ __forceinline__ void bm_bound(MergeSmem& sm, Cand top, int K) {
   const int tid = threadIdx.x;
 #pragma unroll
   for (int m = 1; m < kBmPer; m <<= 1) {
-    const unsigned long long s = __shfl_xor_sync(0xffffffffu, top.s, m);
-    const uint32_t at = __shfl_xor_sync(0xffffffffu, top.at, m);
-    if (beats(s, at, top.s, top.at)) top = {s, at};
+    const Cand o = {__shfl_xor_sync(0xffffffffu, top.s, m), __shfl_xor_sync(0xffffffffu, top.tie, m)};
+    if (beats(o, top)) top = o;
   }
-  if (tid % kBmPer == 0) {
-    sm.gs[tid / kBmPer] = top.s;
-    sm.gat[tid / kBmPer] = top.at;
-  }
+  if (tid % kBmPer == 0) sm.group[tid / kBmPer] = top;
   if (tid == 0) {
-    sm.bound_s = 1;                     // fewer than K groups hold anything
-    sm.bound_at = 0;
+    sm.bound = {1, 0};                  // fewer than K groups hold anything
     sm.count = 0;
   }
   __syncthreads();
   int above = 0;
 #pragma unroll 8
   for (int i = tid % kBmPer; i < kBmGroups; i += kBmPer)      // side by side: no bank twice
-    above += beats(sm.gs[i], sm.gat[i], top.s, top.at);
+    above += beats(sm.group[i], top);
 #pragma unroll
   for (int m = 1; m < kBmPer; m <<= 1) above += __shfl_xor_sync(0xffffffffu, above, m);
-  if (above == K - 1 && top.s > 0 && tid % kBmPer == 0) {
-    sm.bound_s = top.s;
-    sm.bound_at = top.at;
+  if (above == K - 1 && top.s > 0 && tid % kBmPer == 0) sm.bound = top;
+  __syncthreads();
+}
+
+// The same by scores alone: at least K candidates reach sm.bound.s, and with equal scores at the
+// border any number.
+__device__ __forceinline__ void bm_bound_score(MergeSmem& sm, unsigned long long top, int K) {
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int m = 1; m < kBmPer; m <<= 1) {
+    const unsigned long long o = __shfl_xor_sync(0xffffffffu, top, m);
+    top = o > top ? o : top;
   }
+  if (tid % kBmPer == 0) sm.group_s[tid / kBmPer] = top;
+  if (tid == 0) sm.count = 0;
+  __syncthreads();
+  int above = 0, level = 0;
+#pragma unroll 8
+  for (int i = tid % kBmPer; i < kBmGroups; i += kBmPer) {
+    above += sm.group_s[i] > top;
+    level += sm.group_s[i] >= top;
+  }
+#pragma unroll
+  for (int m = 1; m < kBmPer; m <<= 1) {
+    above += __shfl_xor_sync(0xffffffffu, above, m);
+    level += __shfl_xor_sync(0xffffffffu, level, m);
+  }
+  if (above < K && level >= K) sm.bound.s = top > 0 ? top : 1;   // one value, whoever writes it
   __syncthreads();
 }
 
@@ -621,63 +648,77 @@ __global__ void __launch_bounds__(kBmMergeThreads, 2) beam_merge_kernel(
     __syncthreads();
     if (tid < total) key0 = keys[tid];
   }
-  auto get = [&](int i) -> Cand {
+  auto score = [&](int i) -> unsigned long long {        // ordered; 0: none
     const int w = i / per_row, row = n * W + w;
     const double s = sm.score[w];
-    if (!(s > -INFINITY)) return {0, 0};
-    if (finished && finished[row]) {
-      if (i - w * per_row != 0) return {0, 0};
-      return {ordered(s), ~(static_cast<uint32_t>(w) * V + pad_token)};
-    }
+    if (!(s > -INFINITY)) return 0;
+    if (finished && finished[row]) return i - w * per_row == 0 ? ordered(s) : 0;
     const unsigned long long key = i < kBmMergeThreads ? key0 : keys[i];
-    if (key == 0) return {0, 0};
-    const uint32_t v = 0xFFFFFFFFu - static_cast<uint32_t>(key);
-    float x = unordered(static_cast<uint32_t>(key >> 32));
-    if (sm.low[w]) x = -kBmHuge;
-    return {ordered(s + (static_cast<double>(x) - sm.lse[w])), ~(static_cast<uint32_t>(w) * V + v)};
+    if (key == 0) return 0;
+    const float x = sm.low[w] ? -kBmHuge : unordered(static_cast<uint32_t>(key >> 32));
+    return ordered(s + (static_cast<double>(x) - sm.lse[w]));
   };
-  const Cand one = tid < total ? get(tid) : Cand{0, 0};
-  Cand top = one;
-  for (int i = tid + kBmMergeThreads; i < total; i += kBmMergeThreads) {
-    const Cand c = get(i);
-    if (beats(c.s, c.at, top.s, top.at)) top = c;
-  }
-  bm_bound(sm, top, K);
+  auto tie = [&](int i) -> unsigned long long {
+    const int w = i / per_row;
+    if (finished && finished[n * W + w]) return tie_of(w, 0u, pad_token);
+    const unsigned long long key = i < kBmMergeThreads ? key0 : keys[i];
+    return tie_of(w, static_cast<uint32_t>(key >> 32), 0xFFFFFFFFu - static_cast<uint32_t>(key));
+  };
+  const int room = merge_room(total, K);
+  unsigned long long *left_s = sm.left, *left_tie = sm.left + room;
+  auto keep = [&](int at, const Cand& c) {
+    left_s[at] = c.s;
+    left_tie[at] = c.tie;
+  };
+  const unsigned long long one = tid < total ? score(tid) : 0;
   {
-    const unsigned long long bs = sm.bound_s;
-    const uint32_t ba = sm.bound_at;
-    if (!beats(bs, ba, top.s, top.at))
+    unsigned long long top = one;
+    for (int i = tid + kBmMergeThreads; i < total; i += kBmMergeThreads) {
+      const unsigned long long s = score(i);
+      top = s > top ? s : top;
+    }
+    bm_bound_score(sm, top, K);
+    const unsigned long long bound = sm.bound.s;
+    if (top >= bound)
       for (int i = tid; i < total; i += kBmMergeThreads) {
-        const Cand c = i == tid ? one : get(i);
-        if (!beats(bs, ba, c.s, c.at)) {
-          const int at = atomicAdd(&sm.count, 1);
-          sm.s[at] = c.s;
-          sm.at[at] = c.at;
-        }
+        const unsigned long long s = i == tid ? one : score(i);
+        if (s < bound) continue;
+        const int at = atomicAdd(&sm.count, 1);
+        if (at < room) keep(at, {s, tie(i)});
       }
   }
   __syncthreads();
   int left = sm.count;
   __syncthreads();
-  while (left > kBmMergeThreads) {                     // rare: the best ones lie in few threads
-    Cand mine[kBmSurvivors / kBmMergeThreads];
-    top = {0, 0};
-#pragma unroll
-    for (int k = 0; k < kBmSurvivors / kBmMergeThreads; ++k) {
-      const int i = tid + k * kBmMergeThreads;
-      mine[k] = i < left ? Cand{sm.s[i], sm.at[i]} : Cand{0, 0};
-      if (beats(mine[k].s, mine[k].at, top.s, top.at)) top = mine[k];
+  if (left > room) {                                   // rare: equal scores at the border
+    Cand top = {0, 0};
+    for (int i = tid; i < total; i += kBmMergeThreads) {
+      const Cand c = {score(i), tie(i)};
+      if (beats(c, top)) top = c;
     }
-    bm_bound(sm, top, K);                              // its first barrier: all have read theirs
-    const unsigned long long bs = sm.bound_s;
-    const uint32_t ba = sm.bound_at;
-#pragma unroll
-    for (int k = 0; k < kBmSurvivors / kBmMergeThreads; ++k)
-      if (!beats(bs, ba, mine[k].s, mine[k].at)) {
-        const int at = atomicAdd(&sm.count, 1);
-        sm.s[at] = mine[k].s;
-        sm.at[at] = mine[k].at;
-      }
+    bm_bound(sm, top, K);
+    const Cand bound = sm.bound;
+    for (int i = tid; i < total; i += kBmMergeThreads) {
+      const Cand c = {score(i), tie(i)};
+      if (!beats(bound, c)) keep(atomicAdd(&sm.count, 1), c);
+    }
+    __syncthreads();
+    left = sm.count;
+    __syncthreads();
+  }
+  while (left > kBmMergeThreads) {                     // rare: the best ones lie in few threads
+    Cand top = {0, 0};
+    for (int i = tid; i < left; i += kBmMergeThreads) {
+      const Cand c = {left_s[i], left_tie[i]};
+      if (beats(c, top)) top = c;
+    }
+    bm_bound(sm, top, K);
+    const Cand bound = sm.bound;
+    for (int i0 = 0; i0 < left; i0 += kBmMergeThreads) {   // what is kept moves down, among what has been read
+      const Cand c = i0 + tid < left ? Cand{left_s[i0 + tid], left_tie[i0 + tid]} : Cand{0, 0};
+      __syncthreads();
+      if (!beats(bound, c)) keep(atomicAdd(&sm.count, 1), c);
+    }
     __syncthreads();
     left = sm.count;
     __syncthreads();                                   // read before the next round clears it
@@ -686,17 +727,18 @@ __global__ void __launch_bounds__(kBmMergeThreads, 2) beam_merge_kernel(
   float* so = scores_out + static_cast<size_t>(n) * K;
   int32_t *po = parents + static_cast<size_t>(n) * K, *to = tokens + static_cast<size_t>(n) * K;
   if (tid < left) {
-    const unsigned long long s = sm.s[tid];
-    const uint32_t at = sm.at[tid];
+    const Cand mine = {left_s[tid], left_tie[tid]};
     int above = 0;
 #pragma unroll 8
-    for (int i = 0; i < left; ++i) above += beats(sm.s[i], sm.at[i], s, at);
+    for (int i = 0; i < left; ++i) above += left_s[i] > mine.s;
+    if (above < K)                                     // few: equal scores
+#pragma unroll 8
+      for (int i = 0; i < left; ++i) above += left_s[i] == mine.s && left_tie[i] > mine.tie;
     if (above < K) {
-      const uint32_t flat = ~at;
-      const unsigned long long u = s >> 63 ? s & ~(1ull << 63) : ~s;
+      const unsigned long long u = mine.s >> 63 ? mine.s & ~(1ull << 63) : ~mine.s;
       so[above] = static_cast<float>(__longlong_as_double(static_cast<long long>(u)));
-      po[above] = n * W + static_cast<int>(flat / V);
-      to[above] = static_cast<int>(flat % V);
+      po[above] = n * W + kBmMaxW - 1 - static_cast<int>(mine.tie >> 56);
+      to[above] = static_cast<int>(0xFFFFFFu - static_cast<uint32_t>(mine.tie & 0xFFFFFFu));
     }
   }
   if (tid >= left && tid < K) {                        // fewer continuations than places
@@ -834,10 +876,11 @@ msa_status_t msa_beam_select(const void* logits, int dtype, int64_t row_stride, 
                  static_cast<const __nv_bfloat16*>(logits), row_stride, V, K, finished, w.stats, w.keys);
   }
   MSA_TRY(check_launch("beam_scan_kernel"));
-  MSA_TRY(ensure_smem(beam_merge_kernel, sizeof(MergeSmem), "beam_merge_kernel"));
+  MSA_TRY(ensure_smem(beam_merge_kernel, sizeof(MergeSmem) + kBmSurvivors * sizeof(Cand), "beam_merge_kernel"));
   {
     TraceScope trace_("beam_merge_kernel", st);
-    launch_pdl(beam_merge_kernel, static_cast<unsigned>(N), kBmMergeThreads, sizeof(MergeSmem), st,
+    const size_t smem = sizeof(MergeSmem) + merge_room(W * slices * K, K) * sizeof(Cand);
+    launch_pdl(beam_merge_kernel, static_cast<unsigned>(N), kBmMergeThreads, smem, st,
                w.stats, w.keys, logits, dtype, static_cast<long long>(row_stride), scores, finished, W, V, K, slices,
                pad_token, scores_out, parents, tokens);
   }

@@ -80,6 +80,24 @@ def beam_select(logits, scores, W, K, finished=None, pad=0):
     return so, po, to
 
 
+def beam_order(logits, scores, W, K, finished=None, pad=0):
+    """(parents, tokens) by score, equal ones by the lower beam, then the larger logit, then the lower token:
+    beam_select wherever different logits of a beam have different 64-bit scores."""
+    all_scores = beam_scores(logits, scores, finished, pad)
+    R, V = all_scores.shape
+    x = np.minimum(np.where(np.isnan(logits), -np.inf, logits), 2.0 ** 28)
+    x[x.max(-1) < -2.0 ** 28] = 0.0
+    po, to = np.full((R // W, K), -1), np.full((R // W, K), -1)
+    for n in range(R // W):
+        rows = slice(n * W, (n + 1) * W)
+        w, v = np.divmod(np.arange(W * V), V)
+        flat = all_scores[rows].ravel()
+        order = np.lexsort((v, -x[rows].ravel(), w, -flat))[:K]
+        order = order[flat[order] > -np.inf]
+        po[n, :len(order)], to[n, :len(order)] = n * W + w[order], v[order]
+    return po, to
+
+
 def reorder(parents, table, lens, ref):
     """(table, lens, ref, kept) after the call, from copies."""
     t, n, r = table.copy(), lens.copy(), ref.copy()

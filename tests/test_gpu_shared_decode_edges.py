@@ -114,6 +114,29 @@ def test_rows_of_low_values_beside_other_rows(m, V):
         choice(m, x, torch.tensor([-1.0, -2.0], device=DEV), 2, 9)
 
 
+@pytest.mark.parametrize("V", [40, 5000, 70001, 300000])
+@pytest.mark.parametrize("score", [0.0, -1e9, -1e16, -1e30, -3.4028234663852886e38])
+def test_logits_of_a_beam_order_it_where_its_scores_are_equal(m, V, score):
+    """Scores in 64 bits of a beam far below 0, or of logits next to each other, are equal: the larger logit
+    is the better one, however many slices or rows a call has."""
+    g = generator(V)
+    x = 1e-3 * torch.randn(2, V, generator=g, device=DEV)
+    x[:, ::3] = -1.0
+    x[1] *= 1e-22                                       # logits nearer to each other than the scores' steps
+    s = torch.tensor([score, 2 * score if score > -1e38 else -1e38], device=DEV)
+    for dt in (torch.float32, torch.bfloat16):
+        y = x.to(dt)
+        for W, K in ((1, 1), (1, 2), (1, 20), (2, 30)):
+            if W == 2 and score == 0.0:
+                continue                                # beams near each other
+            po, to = S.beam_order(f64(y), f64(s), W, K)
+            got = m.msa_beam_select(y, s, W, K)
+            assert np.array_equal(got[2].cpu().numpy(), to) and np.array_equal(got[1].cpu().numpy(), po)
+            many = m.msa_beam_select(y.repeat(100, 1), s.repeat(100), W, K)
+            assert torch.equal(many[2].view(100, -1)[37], got[2].view(-1))
+    m.msa_check_status()
+
+
 # ------------------------------------------------------------------ sums
 
 @pytest.mark.parametrize("dt,V,W,K", [(torch.bfloat16, 1 << 24, 64, 64), (torch.float32, 1 << 24, 3, 5), (torch.float32, (1 << 24) - 5, 16, 64),
