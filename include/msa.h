@@ -455,7 +455,8 @@ MSA_API msa_status_t msa_cache_append(const void* q, const void* k, const void* 
  * products are all -infinity; lengths outside [0, 128 max_pages] set MSA_STATUS_BOUNDS and are
  * treated so too.  A page outside [0, num_pages) sets MSA_STATUS_BOUNDS and has no keys.  o
  * may be q; o and lse must not overlap the inputs otherwise.  Slots of a row's last page
- * behind its end may hold anything.  B <= 2048; scale from 2^-64 to 2^64.
+ * behind its end may hold anything.  B <= 2048, Hq <= 1024, Hkv <= 256, max_pages <= 1024; scale
+ * from 2^-64 to 2^64.  Small calls as above need no workspace to speak of (256 bytes).
  */
 MSA_API size_t msa_decode_shared_workspace_size(int B, int Hq, int Hkv, int max_pages);
 

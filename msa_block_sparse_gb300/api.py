@@ -599,8 +599,9 @@ def msa_decode_shared(q, k_cache, v_cache, block_table, cache_lens, scale: Optio
                       workspace: Optional[torch.Tensor] = None):
     """Full attention of one new token per row (q bf16 [B, Hq, 128]) over all cached
     tokens of the row: (o bf16 [B, Hq, 128], lse fp32 [B, Hq]).  Full pages with which
-    neighbouring rows begin alike are read once for all of them.  Rows of length 0 get o = 0,
-    lse = -inf."""
+    neighbouring rows begin alike are read once for all of them; small calls (at most 16 heads per
+    KV head and 128 columns, few pages in all) read every row by itself, which then takes less
+    time.  Rows of length 0 get o = 0, lse = -inf.  out may be q."""
     return _native().decode_shared(q, k_cache, v_cache, block_table, cache_lens,
                                    _SCALE if scale is None else scale, out, lse, workspace)
 

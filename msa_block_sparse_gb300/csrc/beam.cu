@@ -2,9 +2,9 @@
 // best score s_w + log softmax(x_w)_v.
 //
 // Bound by memory in the limit: the logits are read once (the only large input).  Measured: 32
-// prompts x 8 beams x 131,072 bf16 logits 25 us, of which the scan takes about 17 (67 MB, 3.9
-// TB/s; an exponential per value and its end fill half of the issue slots) and the merge 5; 4
-// beams x 32,000 fp32 7.4 us, latency.
+// prompts x 8 beams x 131,072 bf16 logits (67 MB) 24 us; alone and with cold caches the scan takes
+// 22 (3.1 TB/s; an exponential per value and its end fill half of the issue slots) and the merge
+// 9, of which about 7 are launch and latency.  4 beams x 32,000 fp32 7.5 us, latency.
 //
 //   beam_scan_kernel   CTA = a slice of one beam's vocabulary.  One pass: every thread sums
 //                      the exponentials of its values (2^(x log2 e - ref), ref a whole
@@ -14,7 +14,8 @@
 //                      a beam the order of the scores is that of the values, so that nothing
 //                      else of the slice can be chosen.
 //   beam_merge_kernel  CTA = a prompt.  Log-sum-exp of its beams from the slices, scores of
-//                      the slices' candidates in 64 bits, the best K in order.
+//                      the slices' candidates in 64 bits, the best K in order; equal scores
+//                      by the beam, then by the values, as the slices had them.
 //
 // K best of n values without sorting: the values are dealt into groups, and the K-th
 // largest of the groups' maxima is a bound that at least K values reach; of values in no
@@ -762,9 +763,10 @@ struct BeamWorkspace {
 // values, which waits for memory, takes 0.3 c times as long and the rest 0.8 c (not less than once).  A slice
 // costs the merge about as much as 4 values, and a candidate beyond one per thread half an
 // instruction of each (its score in 64 bits).  Measured against counting rounds of 4 CTAs per SM alone, candidates
-// for free: 16 prompts x 4 x 50,000 10.3 us and 11.7, 19 x 5 x 50,001 11.8 and 13.1, 4 x 16 x 50,000 (K = 16) 13.1 and
-// 21.4, 1 x 32 x 100,000 (K = 32) 25 and 65, but 64 x 4 x 32,000 14.4 and 13.5.  No slice under 1024 values, and a
-// prompt's candidates within what the merge takes.
+// for free, on the same logits again and again: 16 prompts x 4 x 50,000 10.5 us and 10.7, 19 x 5 x 50,001 10.9 and
+// 11.9, 4 x 16 x 50,000 (K = 16) 13.3 and 17.2, 1 x 32 x 100,000 (K = 32) 28 and 57, 64 x 4 x 32,000 13.6 and 13.4.
+// On several sets of logits in turn: 12.5 and 10.9, 12.7 and 12.5, 15.3 and 17.4, 30 and 57, 15.5 and 14.9.  No slice
+// under 1024 values, and a prompt's candidates within what the merge takes.
 int beam_slices(long long rows, int W, int V, int K) {
   const long long sms = device_sm_count();
   long long most = V / 1024;
